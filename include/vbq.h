@@ -291,6 +291,144 @@ vbq_status vbq_residual_error(const vbq_matrix* m, const float* E_in, float* E_o
  * bound: device, B x N float32, 4-byte aligned, fully overwritten. */
 vbq_status cell_drift_bound(const vbq_matrix* m, const uint16_t* x, int32_t B, float* bound, hipStream_t stream);
 
+/* ---- 4-bit key/value cache ------------------------------------------------------
+ *
+ * Keys and values of decoder attention, held in 4 bits in this library's
+ * group format (VBQ abstract for groups of 64 and packed low-bit storage, SLQ
+ * abstract for scale + offset): 64 consecutive channels of one token of one
+ * key/value head are a group with 4-bit codes, an fp16 scale and an fp16
+ * offset, 36 bytes per 64 values.
+ *
+ * Quantiser, in binary32 without contraction:
+ *   w' = w is NaN ? 0 : clamp(w, -61440, 61440); lo = min, hi = max of the group;
+ *   scale16 = fp16(f32(hi - lo) / 15); offset16 = fp16(lo); s, o = those values;
+ *   q = s == 0 ? 0 : clamp(rint(f32(w' - o) / s), 0, 15)       (ties to even)
+ * and the value held is f32(s*q) + o. With the clamp s <= 8192, so every value
+ * held is a finite number that fp16 can round to: a cache written by kv4_append
+ * holds no infinity and no NaN, and a token that a mask hides cannot reach an
+ * output. A NaN that was stored as 0 is reported in the flag word.
+ *
+ * Pages. The cache is n_pages pages of page_tokens tokens (a power of two,
+ * 32 .. 65536). Position p of a sequence is token p % page_tokens of the page
+ * that entry p / page_tokens of the sequence's row of the block table names.
+ * A page holds, for each key/value head in turn, page_tokens / 32 blocks of 32
+ * tokens; a block takes 2304 bytes per 64 channels (G = head_dim / 64 groups):
+ *   1024 G bytes of key codes, 1024 G bytes of value codes (group by group),
+ *   128 G bytes of key scales and offsets, 128 G bytes of value scales and
+ *   offsets (per group 32 fp16 scales, then 32 fp16 offsets).
+ * With t < 32 the token in its block and c < 64 the channel in its group:
+ *   key codes:   u32 word 4*(16*(c%32/8) + 4*(t/8) + t%4) + 2*(t%8/4) + c/32 of
+ *                the group, bits 4*(c%8) .. 4*(c%8)+3;
+ *   value codes: u32 word 64*(t/8) + c of the group, bits 4*(t%8) .. 4*(t%8)+3;
+ *   key scale and offset:   entry t;
+ *   value scale and offset: entry 8*(t/8) + 2*(t%4) + t%8/4.
+ * The words are the operands of the matrix instructions that read them, so a
+ * wavefront's loads are contiguous and no code moves between lanes.
+ *
+ * Ownership and streams as everywhere in this header. Several sequences may
+ * read a page; a page that is written belongs to one sequence. Calls that
+ * write tokens another call reads must be ordered by the caller.
+ *
+ * Device-side errors. Lengths, starts and block tables live on the device, so
+ * the kernels check them: a page outside 0 .. n_pages-1 is never touched, a
+ * sequence whose numbers do not fit is left out. What was found is OR-ed into
+ * the flag word. */
+#define VBQ_KV4_BLOCK_TOKENS 32
+#define VBQ_KV4_MAX_GROUPS 4      /* head_dim = 64, 128, 192 or 256 */
+#define VBQ_KV4_FLAG_PAGE 1u      /* a block-table entry outside the cache */
+#define VBQ_KV4_FLAG_LENGTH 2u    /* lengths or starts that are negative, beyond the table or the stated maxima */
+#define VBQ_KV4_FLAG_NAN 4u       /* kv4_append stored a NaN as 0 */
+
+typedef enum vbq_dtype { VBQ_F16 = 0, VBQ_BF16 = 1, VBQ_F32 = 2 } vbq_dtype;
+
+/* Descriptor of a cache (caller-owned device buffers). */
+typedef struct vbq_kv4 {
+  int64_t n_pages;        /* >= 1, at most 2^31 - 1 */
+  int32_t page_tokens;    /* power of two, 32 .. 65536 */
+  int32_t n_kv_heads;     /* 1 .. 4096 */
+  int32_t head_dim;       /* 64, 128, 192 or 256 */
+  int32_t reserved;       /* 0 */
+  uint8_t* data;          /* device, n_pages * kv4_page_bytes(...), 16-byte aligned */
+  uint32_t* flags;        /* device, one word, or NULL */
+} vbq_kv4;
+
+/* A range of tokens of every sequence of a batch: sequence b's tokens
+ * start[b] .. start[b] + cu[b+1] - cu[b] - 1 are rows cu[b] .. cu[b+1] - 1 of
+ * the tensors that hold them. */
+typedef struct vbq_kv4_range {
+  int32_t batch;          /* 1 .. 65535 */
+  int32_t table_width;    /* entries per row of the block table, >= 1 */
+  int32_t total_tokens;   /* rows of the tensors, >= 0 */
+  int32_t max_tokens;     /* no sequence has more rows than this; >= 0 */
+  const int32_t* table;   /* device, [batch][table_width] */
+  const int32_t* start;   /* device, [batch], first position */
+  const int32_t* cu;      /* device, [batch + 1], cumulative row counts from 0 */
+} vbq_kv4_range;
+
+/* Bytes of one page, 0 if the sizes are not supported. Host only. */
+int64_t kv4_page_bytes(int32_t page_tokens, int32_t n_kv_heads, int32_t head_dim);
+
+/* Quantises keys and values as they are written. k, v: device, rows [token]
+ * [head][channel] of type `dtype` (a vbq_dtype) with the given strides in
+ * elements between tokens and heads (channels are contiguous); base pointers
+ * and strides are multiples of 16 bytes. A token's place is overwritten; the
+ * other tokens of its block keep theirs. */
+vbq_status kv4_append(const vbq_kv4* cache, const vbq_kv4_range* r, const void* k, const void* v, int32_t dtype,
+                      int64_t k_token_stride, int64_t k_head_stride, int64_t v_token_stride, int64_t v_head_stride,
+                      hipStream_t stream);
+
+/* Reads tokens back: f32(s*q) + o rounded once to `dtype`. k, v: device,
+ * [total_tokens][n_kv_heads][head_dim], contiguous, 16-byte aligned; either
+ * may be NULL. Rows of tokens whose page is not in the cache are zeroed. */
+vbq_status kv4_read(const vbq_kv4* cache, const vbq_kv4_range* r, void* k, void* v, int32_t dtype,
+                    hipStream_t stream);
+
+/* Attention of new query tokens over a cache:
+ *   out[t][h] = sum_j softmax_j(scale * q[t][h] . K_j) V_j
+ * over the positions j that the row sees, with K, V the values held for head
+ * h / (n_heads / n_kv_heads). Sequence b holds kv_lens[b] tokens; its queries
+ * are rows cu_q[b] .. cu_q[b+1] - 1 and stand at its last positions, so query
+ * i of n is at p = kv_lens[b] - n + i. It sees j < kv_lens[b] with
+ *   causal:  j <= p
+ *   window:  j > p - window or j < sinks     (window > 0, causal only)
+ * A row that sees nothing gives zeros (and lse = -infinity).
+ * Scores are sums of products of q (fp16, or bf16) with the exact codes in
+ * fp32, scaled and offset in fp32; the softmax is held in fp32; probabilities
+ * and the values held are rounded to fp16 for the product with fp32 sums.
+ * Results repeat bit for bit for the same sizes. */
+typedef struct vbq_kv4_attn {
+  int32_t batch;          /* 1 .. 65535 */
+  int32_t table_width;
+  int32_t total_q;        /* rows of q, >= 0 */
+  int32_t max_q;          /* no sequence has more queries than this */
+  int32_t max_kv;         /* no sequence holds more tokens than this */
+  int32_t n_heads;        /* a multiple of the cache's n_kv_heads */
+  int32_t dtype;          /* VBQ_F16 or VBQ_BF16: q and out */
+  int32_t causal;         /* 0 or 1 */
+  int32_t window;         /* 0: none */
+  int32_t sinks;          /* first tokens that a window leaves visible */
+  float scale;            /* > 0 */
+  int32_t reserved;       /* 0 */
+  const int32_t* table;   /* device, [batch][table_width] */
+  const int32_t* kv_lens; /* device, [batch] */
+  const int32_t* cu_q;    /* device, [batch + 1] */
+  const void* q;          /* device, [total_q][n_heads][head_dim] with the strides below, 16-byte aligned */
+  int64_t q_token_stride; /* in elements, multiples of 8 */
+  int64_t q_head_stride;
+  void* out;              /* device, [total_q][n_heads][head_dim], contiguous, 16-byte aligned */
+  float* lse;             /* device, [total_q][n_heads], natural log of the sum of exponentials, or NULL */
+  void* workspace;        /* device, kv4_attention_workspace() bytes, 16-byte aligned; its first
+                             VBQ_KV4_COUNTER_BYTES bytes zero before the first call that uses it (every call
+                             leaves them zero). Calls that overlap in time need workspaces of their own. */
+  int64_t workspace_bytes;
+} vbq_kv4_attn;
+#define VBQ_KV4_COUNTER_BYTES 65536
+
+/* Bytes of workspace that kv4_attention needs for these sizes (pointers are
+ * not looked at), or -1 if the sizes are refused. Host only. */
+int64_t kv4_attention_workspace(const vbq_kv4* cache, const vbq_kv4_attn* a);
+vbq_status kv4_attention(const vbq_kv4* cache, const vbq_kv4_attn* a, hipStream_t stream);
+
 #ifdef __cplusplus
 }
 #endif

@@ -12,7 +12,8 @@ tensors are checked here, before anything is launched (a wrong tensor raises
 Function names follow the C ABI: ``vbq_pack``, ``vbq_gemv``,
 ``vbq_gemv_batched``, ``vbq_gemv_batched_static``, ``vbq_gemv_levels``,
 ``vbq_gemv_cell8``, ``vbq_gemm``, ``cell_requant_verify``, ``cell_drift_bound``,
-``cell8_encode``, ``cell8_decode``, ``vbq_residual_error``.
+``cell8_encode``, ``cell8_decode``, ``vbq_residual_error``, and for the 4-bit
+key/value cache (``Kv4Cache``) ``kv4_append``, ``kv4_read``, ``kv4_attention``.
 """
 from __future__ import annotations
 
@@ -53,7 +54,26 @@ class vbq_layout_sizes(C.Structure):
 EXPORTS = ("vbq_abi_version", "vbq_status_string", "vbq_pack_query", "vbq_pack", "vbq_matrix_check",
            "vbq_gemv", "vbq_gemv_batched", "vbq_gemv_batched_static", "vbq_gemv_levels", "vbq_gemm",
            "cell_requant_verify", "cell_drift_bound", "vbq_residual_error", "vbq_gemv_cell8", "cell8_encode",
-           "cell8_decode")
+           "cell8_decode", "kv4_page_bytes", "kv4_append", "kv4_read", "kv4_attention_workspace", "kv4_attention")
+
+
+class vbq_kv4(C.Structure):
+    _fields_ = [("n_pages", C.c_int64), ("page_tokens", C.c_int32), ("n_kv_heads", C.c_int32),
+                ("head_dim", C.c_int32), ("reserved", C.c_int32), ("data", C.c_void_p), ("flags", C.c_void_p)]
+
+
+class vbq_kv4_range(C.Structure):
+    _fields_ = [("batch", C.c_int32), ("table_width", C.c_int32), ("total_tokens", C.c_int32),
+                ("max_tokens", C.c_int32), ("table", C.c_void_p), ("start", C.c_void_p), ("cu", C.c_void_p)]
+
+
+class vbq_kv4_attn(C.Structure):
+    _fields_ = [(n, C.c_int32) for n in ("batch", "table_width", "total_q", "max_q", "max_kv", "n_heads", "dtype",
+                                         "causal", "window", "sinks")] + \
+               [("scale", C.c_float), ("reserved", C.c_int32)] + \
+               [(n, C.c_void_p) for n in ("table", "kv_lens", "cu_q", "q")] + \
+               [("q_token_stride", C.c_int64), ("q_head_stride", C.c_int64)] + \
+               [(n, C.c_void_p) for n in ("out", "lse", "workspace")] + [("workspace_bytes", C.c_int64)]
 
 
 def _load():
@@ -95,6 +115,17 @@ def _load():
     lib.cell8_encode.argtypes = [C.POINTER(vbq_matrix), P, P, P]
     lib.cell8_decode.restype = C.c_int
     lib.cell8_decode.argtypes = [C.POINTER(vbq_matrix), P, P, P]
+    I64 = C.c_int64
+    lib.kv4_page_bytes.restype = I64
+    lib.kv4_page_bytes.argtypes = [I32, I32, I32]
+    lib.kv4_append.restype = C.c_int
+    lib.kv4_append.argtypes = [C.POINTER(vbq_kv4), C.POINTER(vbq_kv4_range), P, P, I32, I64, I64, I64, I64, P]
+    lib.kv4_read.restype = C.c_int
+    lib.kv4_read.argtypes = [C.POINTER(vbq_kv4), C.POINTER(vbq_kv4_range), P, P, I32, P]
+    lib.kv4_attention_workspace.restype = I64
+    lib.kv4_attention_workspace.argtypes = [C.POINTER(vbq_kv4), C.POINTER(vbq_kv4_attn)]
+    lib.kv4_attention.restype = C.c_int
+    lib.kv4_attention.argtypes = [C.POINTER(vbq_kv4), C.POINTER(vbq_kv4_attn), P]
     return lib
 
 
@@ -444,4 +475,195 @@ def vbq_gemv_levels(pms, x, out=None, stream=None):
         out = torch.empty(B, pms[0].N, dtype=torch.float32, device=x.device)
     _need(out, "out", torch.float32, (B, pms[0].N), pms[0].device)
     _check(lib.vbq_gemv_levels(n, descs, _ptr(x2), B, _ptr(out), _stream(stream)), "vbq_gemv_levels")
+    return out
+
+
+# ---- 4-bit key/value cache ---------------------------------------------------------
+KV4_FLAG_PAGE, KV4_FLAG_LENGTH, KV4_FLAG_NAN = 1, 2, 4
+KV4_COUNTER_BYTES = 65536
+
+
+def _kv4_dtype(dtype, what: str, names=("float16", "bfloat16", "float32")) -> int:
+    import torch
+    for i, n in enumerate(names):
+        if dtype == getattr(torch, n):
+            return i
+    raise ValueError(f"{what}: dtype {dtype}, expected one of {', '.join(names)}")
+
+
+def _kv4_rows(t, what: str, heads: int, dim: int, device):
+    """Raises ValueError unless t is [tokens][heads][dim] on `device` with
+    contiguous channels and 16-byte aligned rows; returns its strides."""
+    import torch
+    if not isinstance(t, torch.Tensor):
+        raise ValueError(f"{what}: expected a torch tensor, got {type(t).__name__}")
+    if t.dim() != 3 or t.shape[1] != heads or t.shape[2] != dim:
+        raise ValueError(f"{what}: shape {tuple(t.shape)}, expected (tokens, {heads}, {dim})")
+    if t.device != device:
+        raise ValueError(f"{what}: on {t.device}, expected {device}")
+    ts, hs, cs = t.stride()
+    per16 = 16 // t.element_size()
+    if cs != 1:
+        raise ValueError(f"{what}: channels are not contiguous")
+    if t.shape[0] < 2:
+        ts = 0
+    if heads < 2:
+        hs = 0
+    if ts % per16 or hs % per16 or t.data_ptr() % 16:
+        raise ValueError(f"{what}: token and head rows are not 16-byte aligned (strides {t.stride()})")
+    return ts, hs
+
+
+class Kv4Cache:
+    """Device buffers of a 4-bit key/value cache (layout in include/vbq.h):
+    n_pages pages of page_tokens tokens, n_kv_heads heads of head_dim
+    channels. data: an existing uint8 buffer of nbytes, or None for a new one
+    (zeroed)."""
+
+    def __init__(self, n_pages: int, page_tokens: int, n_kv_heads: int, head_dim: int, device="cuda", data=None):
+        import torch
+        self.page_bytes = lib.kv4_page_bytes(page_tokens, n_kv_heads, head_dim)
+        if self.page_bytes == 0 or not 1 <= n_pages < 2 ** 31:
+            raise ValueError(f"Kv4Cache: {n_pages} pages of {page_tokens} tokens, {n_kv_heads} heads of {head_dim}: "
+                             "pages take a power of two of tokens (32..65536), heads 64, 128, 192 or 256 channels")
+        self.n_pages, self.page_tokens = int(n_pages), int(page_tokens)
+        self.n_kv_heads, self.head_dim = int(n_kv_heads), int(head_dim)
+        if data is None:
+            data = torch.zeros(self.nbytes, dtype=torch.uint8, device=device)
+        else:
+            _need(data, "data", torch.uint8, (self.nbytes,))
+        self.data = data
+        self.flags = torch.zeros(1, dtype=torch.int32, device=data.device)
+        self.desc = vbq_kv4(self.n_pages, self.page_tokens, self.n_kv_heads, self.head_dim, 0, data.data_ptr(),
+                            self.flags.data_ptr())
+        self._ref = C.byref(self.desc)
+
+    @property
+    def device(self):
+        return self.data.device
+
+    @property
+    def nbytes(self) -> int:
+        return self.n_pages * self.page_bytes
+
+    def check(self):
+        """Waits for the device and raises VbqError if a call so far met a page
+        outside the cache or lengths that do not fit; returns True if a NaN was
+        stored as 0, else False. The flags are cleared."""
+        f = int(self.flags.item())
+        self.flags.zero_()
+        if f & (KV4_FLAG_PAGE | KV4_FLAG_LENGTH):
+            raise VbqError(6, "Kv4Cache: " + " and ".join(
+                n for b, n in ((KV4_FLAG_PAGE, "a block-table entry outside the cache"),
+                               (KV4_FLAG_LENGTH, "lengths outside the table or the stated maxima")) if f & b))
+        return bool(f & KV4_FLAG_NAN)
+
+
+def _kv4_index(cache: Kv4Cache, block_table, vec, cu):
+    import torch
+    if not isinstance(block_table, torch.Tensor) or block_table.dim() != 2:
+        raise ValueError("block_table: expected a 2-D torch tensor")
+    B, W = block_table.shape
+    _need(block_table, "block_table", torch.int32, (B, W), cache.device)
+    _need(vec, "lengths", torch.int32, (B,), cache.device)
+    _need(cu, "cumulative lengths", torch.int32, (B + 1,), cache.device)
+    if B < 1 or W < 1:
+        raise ValueError(f"block_table: shape {(B, W)}")
+    return B, W
+
+
+def kv4_append(cache: Kv4Cache, k, v, block_table, start, cu_tokens, max_tokens=None, stream=None):
+    """Quantises k and v [tokens][n_kv_heads][head_dim] (fp16, bf16 or fp32;
+    token and head rows may be strided) into the cache: sequence b's rows
+    cu_tokens[b] .. cu_tokens[b+1] become its tokens start[b], start[b] + 1, ...
+    block_table int32 [B][W], start int32 [B], cu_tokens int32 [B+1], all on
+    the GPU. max_tokens: no sequence has more rows (default: all of them)."""
+    B, W = _kv4_index(cache, block_table, start, cu_tokens)
+    dt = _kv4_dtype(getattr(k, "dtype", None), "k")
+    kts, khs = _kv4_rows(k, "k", cache.n_kv_heads, cache.head_dim, cache.device)
+    vts, vhs = _kv4_rows(v, "v", cache.n_kv_heads, cache.head_dim, cache.device)
+    T = k.shape[0]
+    if v.dtype != k.dtype or v.shape[0] != T:
+        raise ValueError(f"v: {v.dtype} {tuple(v.shape)}, expected k's {k.dtype} {tuple(k.shape)}")
+    r = vbq_kv4_range(B, W, T, T if max_tokens is None else max_tokens, block_table.data_ptr(), start.data_ptr(),
+                      cu_tokens.data_ptr())
+    _check(lib.kv4_append(cache._ref, C.byref(r), k.data_ptr(), v.data_ptr(), dt, kts, khs, vts, vhs,
+                          _stream(stream)), "kv4_append")
+
+
+def kv4_read(cache: Kv4Cache, block_table, start, cu_tokens, total_tokens, dtype, max_tokens=None, out=None,
+             stream=None):
+    """Reads tokens back as k, v [total_tokens][n_kv_heads][head_dim] of
+    `dtype` (fp16, bf16 or fp32), rows as in kv4_append. out: (k, v) tensors
+    to fill."""
+    import torch
+    B, W = _kv4_index(cache, block_table, start, cu_tokens)
+    dt = _kv4_dtype(dtype, "dtype")
+    shape = (total_tokens, cache.n_kv_heads, cache.head_dim)
+    if out is None:
+        with torch.cuda.stream(stream):   # the buffers belong to the stream that fills them
+            out = (torch.empty(shape, dtype=dtype, device=cache.device),
+                   torch.empty(shape, dtype=dtype, device=cache.device))
+    k, v = out
+    _need(k, "out k", dtype, shape, cache.device)
+    _need(v, "out v", dtype, shape, cache.device)
+    r = vbq_kv4_range(B, W, total_tokens, total_tokens if max_tokens is None else max_tokens,
+                      block_table.data_ptr(), start.data_ptr(), cu_tokens.data_ptr())
+    _check(lib.kv4_read(cache._ref, C.byref(r), k.data_ptr(), v.data_ptr(), dt, _stream(stream)), "kv4_read")
+    return k, v
+
+
+def kv4_attention_workspace(cache: Kv4Cache, batch: int, total_q: int, n_heads: int, max_q: int, max_kv: int,
+                            window: int = 0, sinks: int = 0):
+    """A zeroed workspace for kv4_attention calls of these sizes (or any that
+    need no more) that do not overlap in time."""
+    import torch
+    a = vbq_kv4_attn(batch=batch, table_width=1, total_q=total_q, max_q=max_q, max_kv=max_kv, n_heads=n_heads,
+                     dtype=0, causal=1, window=window, sinks=sinks, scale=1.0)
+    n = lib.kv4_attention_workspace(cache._ref, C.byref(a))
+    if n < 0:
+        raise ValueError(f"kv4_attention: sizes refused (batch {batch}, {total_q} queries, {n_heads} heads over "
+                         f"{cache.n_kv_heads}, max_q {max_q}, max_kv {max_kv}, window {window}, sinks {sinks})")
+    return torch.zeros(n, dtype=torch.uint8, device=cache.device)
+
+
+def kv4_attention(cache: Kv4Cache, q, block_table, kv_lens, cu_q, max_q: int, max_kv: int, scale=None,
+                  causal: bool = True, window: int = 0, sinks: int = 0, out=None, lse=None, workspace=None,
+                  stream=None):
+    """Attention of q [queries][n_heads][head_dim] (fp16 or bf16, rows may be
+    strided) over the cache. Sequence b holds kv_lens[b] tokens, and its
+    queries, rows cu_q[b] .. cu_q[b+1] of q, are its last ones. A query sees the
+    tokens up to its own (causal=False: all), with window > 0 only the last
+    `window` of them and the first `sinks` of the sequence. n_heads is a
+    multiple of the cache's heads. max_q, max_kv: no sequence has more queries
+    or tokens. scale: 1/sqrt(head_dim) by default. Returns out, of q's type;
+    lse: float32 [queries][n_heads] to fill, or None. workspace: from
+    kv4_attention_workspace, for calls that allocate nothing."""
+    import torch
+    B, W = _kv4_index(cache, block_table, kv_lens, cu_q)
+    D = cache.head_dim
+    dt = _kv4_dtype(getattr(q, "dtype", None), "q", ("float16", "bfloat16"))
+    if q.dim() != 3 or q.shape[1] < 1 or q.shape[1] % cache.n_kv_heads:
+        raise ValueError(f"q: shape {tuple(q.shape)}, expected (queries, a multiple of {cache.n_kv_heads}, {D})")
+    T, H = q.shape[0], q.shape[1]
+    ts, hs = _kv4_rows(q, "q", H, D, cache.device)
+    if window and not causal:
+        raise ValueError("window: needs causal=True")
+    if out is None:
+        with torch.cuda.stream(stream):   # the buffer belongs to the stream that fills it
+            out = torch.empty(T, H, D, dtype=q.dtype, device=q.device)
+    else:
+        _need(out, "out", q.dtype, (T, H, D), cache.device)
+    if lse is not None:
+        _need(lse, "lse", torch.float32, (T, H), cache.device)
+    if workspace is None:
+        with torch.cuda.stream(stream):
+            workspace = kv4_attention_workspace(cache, B, T, H, max_q, max_kv, window, sinks)
+    elif workspace.dtype != torch.uint8 or workspace.device != cache.device or not workspace.is_contiguous():
+        raise ValueError("workspace: expected a contiguous uint8 tensor on the cache's device")
+    a = vbq_kv4_attn(B, W, T, max_q, max_kv, H, dt, 1 if causal else 0, window, sinks,
+                     D ** -0.5 if scale is None else scale, 0, block_table.data_ptr(), kv_lens.data_ptr(),
+                     cu_q.data_ptr(), q.data_ptr(), ts, hs, out.data_ptr(),
+                     None if lse is None else lse.data_ptr(), workspace.data_ptr(), workspace.numel())
+    _check(lib.kv4_attention(cache._ref, C.byref(a), _stream(stream)), "kv4_attention")
     return out

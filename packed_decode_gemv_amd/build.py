@@ -31,8 +31,8 @@ COMMON = [
     "-Wall", "-Wno-unused-function",
 ]
 # Sources whose arithmetic decides integers are built without FMA contraction.
-EXACT = {"pack.hip", "verify.hip"}
-SOURCES = ["api.cpp", "pack.hip", "gemv.hip", "verify.hip", "gemm.hip"]
+EXACT = {"pack.hip", "verify.hip", "kv4.hip"}
+SOURCES = ["api.cpp", "pack.hip", "gemv.hip", "verify.hip", "gemm.hip", "kv4.hip", "kvattn.hip"]
 
 
 def _compile(src: str) -> str:

@@ -7,7 +7,7 @@
 #include <algorithm>
 #include <vector>
 
-#include "vbq_common.h"
+#include "kv4.h"
 
 using namespace vbq;
 
@@ -72,9 +72,154 @@ uint64_t host_tile_bytes(const uint8_t* widths, int N, int G, int rt, int kt, bo
   return bytes;
 }
 
+// ---- 4-bit key/value cache ----
+bool kv4_sizes_ok(int32_t page_tokens, int32_t heads, int32_t dim) {
+  return page_tokens >= kKvBlock && page_tokens <= 65536 && (page_tokens & (page_tokens - 1)) == 0 && heads >= 1 &&
+         heads <= 4096 && dim >= kGroup && dim % kGroup == 0 && dim / kGroup <= VBQ_KV4_MAX_GROUPS;
+}
+
+vbq_status check_cache(const vbq_kv4* c, bool pointers, KvCache* out) {
+  if (!c) return VBQ_ERR_INVALID_ARG;
+  if (!kv4_sizes_ok(c->page_tokens, c->n_kv_heads, c->head_dim)) return VBQ_ERR_SHAPE;
+  if (c->reserved != 0) return VBQ_ERR_INVALID_ARG;
+  if (c->n_pages < 1) return VBQ_ERR_SHAPE;
+  if (c->n_pages > INT32_MAX) return VBQ_ERR_UNSUPPORTED;
+  if (pointers) {
+    if (!c->data) return VBQ_ERR_INVALID_ARG;
+    if (!aligned(c->data, 16) || !aligned(c->flags, 4)) return VBQ_ERR_ALIGNMENT;
+  }
+  out->data = c->data;
+  out->flags = c->flags;
+  out->n_pages = (int32_t)c->n_pages;
+  out->heads = c->n_kv_heads;
+  out->block_shift = 0;
+  while ((kKvBlock << out->block_shift) < c->page_tokens) out->block_shift++;
+  out->groups = c->head_dim / kGroup;
+  return VBQ_OK;
+}
+
+vbq_status check_range(const vbq_kv4_range* r, KvRange* out) {
+  if (!r) return VBQ_ERR_INVALID_ARG;
+  if (r->batch < 1 || r->table_width < 1 || r->total_tokens < 0 || r->max_tokens < 0) return VBQ_ERR_SHAPE;
+  if (r->batch > 65535) return VBQ_ERR_UNSUPPORTED;
+  if (!r->table || !r->start || !r->cu) return VBQ_ERR_INVALID_ARG;
+  if (!aligned(r->table, 4) || !aligned(r->start, 4) || !aligned(r->cu, 4)) return VBQ_ERR_ALIGNMENT;
+  *out = KvRange{r->batch, r->table_width, r->total_tokens, r->max_tokens, r->table, r->start, r->cu};
+  return VBQ_OK;
+}
+
+vbq_status check_attn(const vbq_kv4* cache, const vbq_kv4_attn* a, bool pointers, KvCache* c, KvAttnPlan* p,
+                      int64_t* bytes) {
+  vbq_status st = check_cache(cache, pointers, c);
+  if (st != VBQ_OK) return st;
+  if (!a || a->reserved != 0) return VBQ_ERR_INVALID_ARG;
+  if (a->batch < 1 || a->table_width < 1 || a->total_q < 0 || a->max_q < 0 || a->max_kv < 0 || a->n_heads < 1 ||
+      a->n_heads % cache->n_kv_heads != 0)
+    return VBQ_ERR_SHAPE;
+  if (a->dtype != VBQ_F16 && a->dtype != VBQ_BF16) return VBQ_ERR_INVALID_ARG;
+  if ((a->causal != 0 && a->causal != 1) || a->window < 0 || a->sinks < 0) return VBQ_ERR_INVALID_ARG;
+  if (a->window > 0 && !a->causal) return VBQ_ERR_INVALID_ARG;
+  if (!(a->scale > 0.f && a->scale <= 3.0e38f)) return VBQ_ERR_INVALID_ARG;
+  if (a->batch > 65535 || a->n_heads > 65536) return VBQ_ERR_UNSUPPORTED;
+  const int ratio = a->n_heads / cache->n_kv_heads;
+  if ((int64_t)a->max_q * ratio > INT32_MAX - 64) return VBQ_ERR_UNSUPPORTED;
+  if (a->max_kv > INT32_MAX - 64) return VBQ_ERR_UNSUPPORTED;
+  *p = kv4_attn_plan(a->batch, cache->n_kv_heads, ratio, c->groups, a->max_q, a->max_kv, a->window, a->sinks);
+  *bytes = VBQ_KV4_COUNTER_BYTES;
+  if (p->splits > 1) *bytes += p->tiles * p->splits * p->rows * (int64_t)(cache->head_dim + 2) * 4;
+  return VBQ_OK;
+}
+
 }  // namespace
 
 extern "C" {
+
+int64_t kv4_page_bytes(int32_t page_tokens, int32_t n_kv_heads, int32_t head_dim) {
+  if (!kv4_sizes_ok(page_tokens, n_kv_heads, head_dim)) return 0;
+  return (int64_t)(page_tokens / kKvBlock) * n_kv_heads * (head_dim / kGroup) * kKvGroupBytes;
+}
+
+vbq_status kv4_append(const vbq_kv4* cache, const vbq_kv4_range* r, const void* k, const void* v, int32_t dtype,
+                      int64_t k_ts, int64_t k_hs, int64_t v_ts, int64_t v_hs, hipStream_t stream) {
+  KvCache c;
+  KvRange rg;
+  vbq_status st = check_cache(cache, true, &c);
+  if (st == VBQ_OK) st = check_range(r, &rg);
+  if (st != VBQ_OK) return st;
+  if (dtype != VBQ_F16 && dtype != VBQ_BF16 && dtype != VBQ_F32) return VBQ_ERR_INVALID_ARG;
+  if (rg.total == 0) return VBQ_OK;
+  if (!k || !v) return VBQ_ERR_INVALID_ARG;
+  const int64_t per16 = dtype == VBQ_F32 ? 4 : 8;
+  if (!aligned(k, 16) || !aligned(v, 16) || k_ts % per16 || k_hs % per16 || v_ts % per16 || v_hs % per16)
+    return VBQ_ERR_ALIGNMENT;
+  hipError_t e = launch_kv4_append(c, rg, k, v, dtype, k_ts, k_hs, v_ts, v_hs, stream);
+  return e == hipErrorNotSupported ? VBQ_ERR_UNSUPPORTED : from_hip(e);
+}
+
+vbq_status kv4_read(const vbq_kv4* cache, const vbq_kv4_range* r, void* k, void* v, int32_t dtype,
+                    hipStream_t stream) {
+  KvCache c;
+  KvRange rg;
+  vbq_status st = check_cache(cache, true, &c);
+  if (st == VBQ_OK) st = check_range(r, &rg);
+  if (st != VBQ_OK) return st;
+  if (dtype != VBQ_F16 && dtype != VBQ_BF16 && dtype != VBQ_F32) return VBQ_ERR_INVALID_ARG;
+  if (!aligned(k, 16) || !aligned(v, 16)) return VBQ_ERR_ALIGNMENT;
+  if (rg.total == 0 || (!k && !v)) return VBQ_OK;
+  hipError_t e = launch_kv4_read(c, rg, k, v, dtype, stream);
+  return e == hipErrorNotSupported ? VBQ_ERR_UNSUPPORTED : from_hip(e);
+}
+
+int64_t kv4_attention_workspace(const vbq_kv4* cache, const vbq_kv4_attn* a) {
+  KvCache c;
+  KvAttnPlan p;
+  int64_t bytes = 0;
+  return check_attn(cache, a, false, &c, &p, &bytes) == VBQ_OK ? bytes : -1;
+}
+
+vbq_status kv4_attention(const vbq_kv4* cache, const vbq_kv4_attn* a, hipStream_t stream) {
+  KvAttn k;
+  KvAttnPlan p;
+  int64_t bytes = 0;
+  vbq_status st = check_attn(cache, a, true, &k.cache, &p, &bytes);
+  if (st != VBQ_OK) return st;
+  if (!a->table || !a->kv_lens || !a->cu_q || !a->workspace) return VBQ_ERR_INVALID_ARG;
+  if (!aligned(a->table, 4) || !aligned(a->kv_lens, 4) || !aligned(a->cu_q, 4) || !aligned(a->workspace, 16) ||
+      !aligned(a->lse, 4) || !aligned(a->q, 16) || !aligned(a->out, 16) || a->q_token_stride % 8 ||
+      a->q_head_stride % 8)
+    return VBQ_ERR_ALIGNMENT;
+  if (a->workspace_bytes < bytes) return VBQ_ERR_CAPACITY;
+  if (a->total_q == 0 || a->max_q == 0) return VBQ_OK;
+  if (!a->q || !a->out) return VBQ_ERR_INVALID_ARG;
+  k.table = a->table;
+  k.lens = a->kv_lens;
+  k.cu = a->cu_q;
+  k.q = static_cast<const uint16_t*>(a->q);
+  k.q_ts = a->q_token_stride;
+  k.q_hs = a->q_head_stride;
+  k.out = static_cast<uint16_t*>(a->out);
+  k.lse = a->lse;
+  uint8_t* const ws = static_cast<uint8_t*>(a->workspace);
+  k.counters = reinterpret_cast<uint32_t*>(ws);
+  k.acc = reinterpret_cast<float*>(ws + VBQ_KV4_COUNTER_BYTES);
+  k.ml = k.acc + (p.splits > 1 ? p.tiles * p.splits * p.rows * (int64_t)cache->head_dim : 0);
+  k.width = a->table_width;
+  k.total_q = a->total_q;
+  k.max_q = a->max_q;
+  k.max_kv = a->max_kv;
+  k.n_heads = a->n_heads;
+  k.ratio = a->n_heads / cache->n_kv_heads;
+  k.bf16 = a->dtype == VBQ_BF16;
+  k.causal = a->causal;
+  k.window = a->window;
+  k.sinks = a->window ? a->sinks : 0;
+  k.row_tiles = p.row_tiles;
+  k.splits = p.splits;
+  k.chunk = p.chunk;
+  k.scale_log2 = a->scale * 1.44269504088896341f;
+  hipError_t e = launch_kv4_attention(k, p, a->batch, stream);
+  return e == hipErrorNotSupported ? VBQ_ERR_UNSUPPORTED : from_hip(e);
+}
 
 int vbq_abi_version(void) { return VBQ_ABI_VERSION; }
 

@@ -1,0 +1,565 @@
+"""The 4-bit key/value cache on the GPU: kv4_append and kv4_read bit for bit
+against a plain numpy writer and reader of the layout that include/vbq.h
+states, kv4_attention against softmax attention in 64 bits."""
+import math
+
+import numpy as np
+import pytest
+
+pytestmark = pytest.mark.gpu
+
+BLOCK = 32
+CLAMP = np.float32(61440.0)
+
+
+@pytest.fixture(scope="module")
+def vbq():
+    import torch
+    if not torch.cuda.is_available():
+        pytest.skip("needs a GPU")
+    import packed_decode_gemv_amd as vbq
+    return vbq
+
+
+# ---- plain quantiser and layout -----------------------------------------------------
+def quantise(x):
+    """Codes, scale and offset (float16) of groups on the last axis (64 long), in binary32."""
+    x = np.asarray(x, np.float32)
+    x = np.where(np.isnan(x), np.float32(0), np.clip(x, -CLAMP, CLAMP)).astype(np.float32)
+    lo, hi = x.min(-1), x.max(-1)
+    s = ((hi - lo).astype(np.float32) / np.float32(15)).astype(np.float16)
+    o = lo.astype(np.float16)
+    sf, of = s.astype(np.float32)[..., None], o.astype(np.float32)[..., None]
+    with np.errstate(divide="ignore", invalid="ignore"):
+        q = np.where(sf == 0, np.float32(0), np.clip(np.rint((x - of) / sf), 0, 15))
+    return q.astype(np.uint32), s, o
+
+
+def value_of(q, s, o):
+    return (s.astype(np.float32)[..., None] * q.astype(np.float32) + o.astype(np.float32)[..., None]).astype(np.float32)
+
+
+class Layout:
+    """Addresses of one cache's codes, scales and offsets, from the header's text."""
+
+    def __init__(self, page, heads, dim):
+        self.page, self.heads, self.dim, self.G = page, heads, dim, dim // 64
+
+    def block(self, page, head, tok_in_page):
+        return ((page * self.heads + head) * (self.page // BLOCK) + tok_in_page // BLOCK) * 2304 * self.G
+
+    def key_word(self, t, c):       # byte offset of the word in the group's codes, and the code's first bit
+        return 4 * (4 * (16 * (c % 32 // 8) + 4 * (t // 8) + t % 4) + 2 * (t % 8 // 4) + c // 32), 4 * (c % 8)
+
+    def value_word(self, t, c):
+        return 4 * (64 * (t // 8) + c), 4 * (t % 8)
+
+    def places(self, base, t, kv):
+        """Byte offsets of the scale and the offset per group."""
+        first = base + 2048 * self.G + (128 * self.G if kv else 0)
+        e = 8 * (t // 8) + 2 * (t % 4) + t % 8 // 4 if kv else t
+        return [(first + 128 * g + 2 * e, first + 128 * g + 64 + 2 * e) for g in range(self.G)]
+
+    def write(self, data, base, t, kv, q, s, o):
+        """data: uint8; q [G][64], s, o [G]: one token of one head."""
+        for g in range(self.G):
+            for c in range(64):
+                off, bit = (self.value_word if kv else self.key_word)(t, c)
+                w = data[base + 1024 * (self.G * kv + g) + off:][:4].view(np.uint32)
+                w[0] = (int(w[0]) & ~(15 << bit) & 0xFFFFFFFF) | (int(q[g, c]) << bit)
+        for g, (a, b) in enumerate(self.places(base, t, kv)):
+            data[a:a + 2].view(np.float16)[0] = s[g]
+            data[b:b + 2].view(np.float16)[0] = o[g]
+
+    def read(self, data, base, t, kv):
+        """float32 [dim] of one token of one head."""
+        out = np.empty((self.G, 64), np.float32)
+        c = np.arange(64)
+        off, bit = (self.value_word if kv else self.key_word)(t, c)
+        for g, (a, b) in enumerate(self.places(base, t, kv)):
+            w = data.view(np.uint32)[(base + 1024 * (self.G * kv + g) + off) // 4]
+            s, o = data[a:a + 2].view(np.float16), data[b:b + 2].view(np.float16)
+            out[g] = value_of((w >> np.asarray(bit).astype(np.uint32)) & 15, s, o)[0]
+        return out.reshape(-1)
+
+
+def random_cache(rng, n_pages, page, heads, dim):
+    """Bytes of a cache whose every place holds finite values: codes at random, scales and offsets of
+    ordinary size, as uint8."""
+    G = dim // 64
+    blocks = n_pages * heads * (page // BLOCK)
+    data = rng.integers(0, 256, (blocks, 2304 * G), dtype=np.uint8)
+    so = np.empty((blocks, 2, G, 2, 32), np.float16)
+    so[:, :, :, 0] = rng.uniform(0.02, 0.4, so[:, :, :, 0].shape)
+    so[:, :, :, 1] = rng.normal(-1.5, 0.7, so[:, :, :, 1].shape)
+    data[:, 2048 * G:] = so.reshape(blocks, -1).view(np.uint8)
+    return data.reshape(-1)
+
+
+def table_for(rng, lens, page, spare=1):
+    """A block table of distinct pages in random order, -1 where a sequence has none."""
+    need = [-(-n // page) for n in lens]
+    width = max(1, max(need))
+    perm = rng.permutation(sum(need) + spare).astype(np.int32)
+    table = np.full((len(lens), width), -1, np.int32)
+    at = 0
+    for b, n in enumerate(need):
+        table[b, :n] = perm[at:at + n]
+        at += n
+    return table, len(perm)
+
+
+def gpu(a):
+    import torch
+    return torch.from_numpy(np.ascontiguousarray(a)).cuda()
+
+
+def cum(n):
+    return np.concatenate([[0], np.cumsum(n)]).astype(np.int32)
+
+
+# ---- append and read ---------------------------------------------------------------
+APPEND = [
+    # dtype, heads, dim, page, [(start, new)]
+    ("float16", 3, 64, 32, [(0, 1)]),
+    ("float16", 2, 128, 64, [(0, 8), (5, 3), (31, 2), (63, 1)]),
+    ("bfloat16", 1, 128, 32, [(7, 1), (8, 1), (30, 70), (0, 0), (3, 33)]),
+    ("float32", 2, 192, 64, [(60, 9), (1, 7), (0, 65)]),
+    ("float32", 1, 256, 128, [(100, 60), (0, 17)]),
+    ("bfloat16", 5, 64, 256, [(250, 9), (13, 3)]),
+]
+
+
+@pytest.mark.parametrize("case", range(len(APPEND)))
+@pytest.mark.parametrize("strided", [False, True])
+def test_append_writes_the_stated_bytes_and_no_others(vbq, case, strided):
+    import torch
+    dtype, heads, dim, page, seqs = APPEND[case]
+    rng = np.random.default_rng(case)
+    lens = [s + n for s, n in seqs]
+    table, n_pages = table_for(rng, lens, page)
+    data = random_cache(rng, n_pages, page, heads, dim)
+    T = sum(n for _, n in seqs)
+    x = rng.normal(0, 1, (2, T, heads, dim)).astype(np.float32)
+    x[:, :, :, ::13] *= 6
+    x[0, T // 2] = 0.25                      # a constant group: scale 0
+    x[1, T - 1, :, 5] = 3e38                 # clamped
+    x[0, 0, 0, 9] = -np.inf
+    xt = torch.from_numpy(x).to(getattr(torch, dtype))
+    if dtype == "float16":
+        xt = torch.nan_to_num(xt, posinf=float("inf"), neginf=float("-inf"))
+    if strided:   # keys and values are slices of one projection, heads interleaved with others
+        both = torch.zeros(T, 2, heads + 2, dim, dtype=xt.dtype)
+        both[:, 0, 1:heads + 1], both[:, 1, 1:heads + 1] = xt[0], xt[1]
+        both = both.cuda()
+        k, v = both[:, 0, 1:heads + 1], both[:, 1, 1:heads + 1]
+    else:
+        k, v = xt[0].contiguous().cuda(), xt[1].contiguous().cuda()
+    cache = vbq.Kv4Cache(n_pages, page, heads, dim, data=gpu(data.copy()))
+    start = np.array([s for s, _ in seqs], np.int32)
+    cu = cum([n for _, n in seqs])
+    vbq.kv4_append(cache, k, v, gpu(table), gpu(start), gpu(cu), max_tokens=max(n for _, n in seqs))
+    assert cache.check() is False
+    lay = Layout(page, heads, dim)
+    xf = xt.float().numpy()
+    want = data.copy()
+    for b, (s, n) in enumerate(seqs):
+        for i in range(n):
+            p = s + i
+            for h in range(heads):
+                base = lay.block(int(table[b, p // page]), h, p % page)
+                for kv in range(2):
+                    lay.write(want, base, p % 32, kv, *quantise(xf[kv, cu[b] + i, h].reshape(-1, 64)))
+    got = cache.data.cpu().numpy()
+    assert np.array_equal(got, want), np.flatnonzero(got != want)[:8]
+
+
+@pytest.mark.parametrize("dtype", ["float16", "bfloat16", "float32"])
+@pytest.mark.parametrize("heads,dim,page,seqs", [
+    (1, 64, 32, [(0, 1)]),
+    (2, 128, 64, [(3, 70), (0, 0), (62, 5), (0, 64)]),
+    (3, 192, 32, [(31, 2), (8, 40)]),
+    (1, 256, 256, [(255, 9)]),
+])
+def test_read_returns_the_values_held(vbq, dtype, heads, dim, page, seqs):
+    import torch
+    rng = np.random.default_rng(dim + len(seqs))
+    lens = [s + n for s, n in seqs]
+    table, n_pages = table_for(rng, lens, page)
+    data = random_cache(rng, n_pages, page, heads, dim)
+    cache = vbq.Kv4Cache(n_pages, page, heads, dim, data=gpu(data))
+    start, cu = np.array([s for s, _ in seqs], np.int32), cum([n for _, n in seqs])
+    dt = getattr(torch, dtype)
+    k, v = vbq.kv4_read(cache, gpu(table), gpu(start), gpu(cu), int(cu[-1]), dt, max_tokens=max(n for _, n in seqs))
+    lay = Layout(page, heads, dim)
+    want = np.empty((2, int(cu[-1]), heads, dim), np.float32)
+    for b, (s, n) in enumerate(seqs):
+        for i in range(n):
+            p = s + i
+            for h in range(heads):
+                base = lay.block(int(table[b, p // page]), h, p % page)
+                for kv in range(2):
+                    want[kv, cu[b] + i, h] = lay.read(data, base, p % 32, kv)
+    w = torch.from_numpy(want).to(dt)
+    assert torch.equal(k.cpu(), w[0]) and torch.equal(v.cpu(), w[1])
+    assert cache.check() is False
+
+
+def test_tokens_one_at_a_time_equal_all_at_once(vbq):
+    import torch
+    gen = torch.Generator(device="cuda").manual_seed(3)
+    heads, dim, page, n = 4, 128, 64, 77
+    k = torch.randn(n, heads, dim, generator=gen, device="cuda").half()
+    v = torch.randn(n, heads, dim, generator=gen, device="cuda").half()
+    table = torch.tensor([[2, 0]], dtype=torch.int32, device="cuda")
+    one, all_ = (vbq.Kv4Cache(3, page, heads, dim) for _ in range(2))
+    i32 = dict(dtype=torch.int32, device="cuda")
+    vbq.kv4_append(all_, k, v, table, torch.zeros(1, **i32), torch.tensor([0, n], **i32))
+    cu = torch.tensor([0, 1], **i32)
+    for i in range(n):
+        vbq.kv4_append(one, k[i:i + 1], v[i:i + 1], table, torch.tensor([i], **i32), cu)
+    assert torch.equal(one.data, all_.data)
+
+
+def test_nan_is_stored_as_zero_and_reported(vbq):
+    import torch
+    i32 = dict(dtype=torch.int32, device="cuda")
+    k = torch.ones(2, 1, 64, device="cuda")
+    v = torch.full((2, 1, 64), 2.0, device="cuda")
+    k[1, 0, 7] = float("nan")
+    v[0, 0, 1] = float("inf")
+    v[0, 0, 2] = -float("inf")
+    cache = vbq.Kv4Cache(1, 32, 1, 64)
+    args = (torch.zeros(1, 1, **i32), torch.zeros(1, **i32), torch.tensor([0, 2], **i32))
+    vbq.kv4_append(cache, k, v, *args)
+    assert cache.check() is True and cache.check() is False
+    rk, rv = vbq.kv4_read(cache, *args, 2, torch.float32)
+    assert rk[1, 0, 7] == 0 and torch.isfinite(rk).all()
+    assert rv[0, 0, 1] == 61440 and rv[0, 0, 2] == -61440
+    assert torch.isfinite(vbq.kv4_read(cache, *args, 2, torch.float16)[1]).all()
+
+
+# ---- attention ---------------------------------------------------------------------
+def reference(lay, data, table, lens, news, q, scale, causal, window, sinks):
+    """Outputs, lse, sum of p |v| and a bound of the scores' magnitudes per row, in 64 bits.
+    q: float64 [T][H][D]."""
+    T, H, D = q.shape
+    R = H // lay.heads
+    out, mass = np.zeros((T, H, D)), np.zeros((T, H, D))
+    lse, size = np.full((T, H), -np.inf), np.zeros((T, H))
+    at = 0
+    for b, (L, n) in enumerate(zip(lens, news)):
+        for h in range(lay.heads):
+            K, V = np.zeros((L, D)), np.zeros((L, D))
+            for t in range(L):
+                base = lay.block(int(table[b, t // lay.page]), h, t % lay.page)
+                K[t], V[t] = lay.read(data, base, t % 32, 0), lay.read(data, base, t % 32, 1)
+            # the score is formed from codes and offsets apart: their magnitudes bound its rounding
+            Kabs = np.abs(K) + 2 * np.abs(K).max() if L else K
+            for i in range(n):
+                p = L - n + i
+                j = np.arange(L)
+                see = j <= p if causal else j < L
+                if window:
+                    see &= (j > p - window) | (j < sinks)
+                if not see.any():
+                    continue
+                for r in range(h * R, h * R + R):
+                    s = scale * (K[see] @ q[at + i, r])
+                    e = np.exp(s - s.max())
+                    w = e / e.sum()
+                    out[at + i, r] = w @ V[see]
+                    mass[at + i, r] = w @ np.abs(V[see])
+                    lse[at + i, r] = s.max() + math.log(e.sum())
+                    size[at + i, r] = scale * (Kabs[see] @ np.abs(q[at + i, r])).max()
+        at += n
+    return out, lse, mass, size
+
+
+def check(got, want, mass, size, dtype, D):
+    """Rounding bound of one output, u = 2^-24 and h = 2^-11 the half ulps of fp32 and fp16.
+    A score of magnitude at most S takes at most D + 16 roundings in fp32 (products are exact) and its
+    exponential's argument and value two more each: its probability is off by (D + 24) u S + 8 u at most,
+    numerator and denominator alike. Probabilities and values are rounded to fp16 once each (h; absolute
+    2^-25 below fp16's normal range, where probabilities carry 2^15), sums of up to 2^17 terms in blocks of 32
+    lose under 2^13 u. The output is rounded once."""
+    u, h = 2.0 ** -24, 2.0 ** -11
+    out_h = h if dtype == "float16" else 2.0 ** -8
+    rel = 2 * ((D + 24) * u * size + 8 * u) + 2.1 * h + 2 ** 13 * u
+    bound = rel[..., None] * mass + out_h * np.abs(want) + 2.0 ** -24
+    err = np.abs(got - want)
+    assert np.isfinite(got).all()
+    assert (err <= bound).all(), (float((err / bound).max()), np.argwhere(err > bound)[:4])
+
+
+def attend(vbq, rng, heads, ratio, dim, page, lens, news, dtype="float16", causal=True, window=0, sinks=0,
+           scale=None, spoil=True, max_kv=None, gain=1.0):
+    """Runs kv4_attention on a random cache and returns everything a check needs."""
+    import torch
+    table, n_pages = table_for(rng, lens, page)
+    data = random_cache(rng, n_pages, page, heads, dim)
+    lay = Layout(page, heads, dim)
+    if spoil:   # places past a sequence's end hold NaN and infinity scales
+        for b, L in enumerate(lens):
+            for t in range(L, -(-L // page) * page):
+                for h in range(heads):
+                    base = lay.block(int(table[b, t // page]), h, t % page)
+                    for kv in range(2):
+                        for a, o in lay.places(base, t % 32, kv):
+                            data[a:a + 2].view(np.uint16)[0] = 0x7E00 if t % 2 else 0x7C00
+                            data[o:o + 2].view(np.uint16)[0] = 0xFC00
+    cache = vbq.Kv4Cache(n_pages, page, heads, dim, data=gpu(data))
+    T = sum(news)
+    q = torch.from_numpy(rng.normal(0, gain, (T, heads * ratio, dim)).astype(np.float32)).to(getattr(torch, dtype))
+    qd = q.cuda()
+    lse = torch.full((T, heads * ratio), float("nan"), device="cuda")
+    kw = dict(scale=scale, causal=causal, window=window, sinks=sinks)
+    args = (cache, qd, gpu(table), gpu(np.array(lens, np.int32)), gpu(cum(news)), max(news),
+            max(lens) if max_kv is None else max_kv)
+    out = vbq.kv4_attention(*args, lse=lse, **kw)
+    assert cache.check() is False
+    sc = dim ** -0.5 if scale is None else scale
+    want = reference(lay, data, table, lens, news, q.double().numpy(), sc, causal, window, sinks)
+    check(out.double().cpu().numpy(), want[0], want[2], want[3], dtype, dim)
+    gl, wl = lse.cpu().numpy().astype(np.float64), want[1]
+    seen = np.isfinite(wl)
+    assert np.array_equal(np.isneginf(gl), ~seen)
+    tol = (dim + 40) * 2.0 ** -24 * (want[3] + np.abs(np.where(seen, wl, 0)) + 30)
+    assert (np.abs(gl[seen] - wl[seen]) <= tol[seen]).all()
+    return args, kw, out
+
+
+@pytest.mark.parametrize("dtype", ["float16", "bfloat16"])
+@pytest.mark.parametrize("heads,ratio,dim,page", [
+    (2, 4, 128, 64), (3, 1, 64, 32), (1, 7, 128, 32), (1, 16, 64, 64), (2, 2, 192, 32), (1, 4, 256, 128),
+    (1, 20, 128, 32),
+])
+def test_attention_of_single_tokens(vbq, dtype, heads, ratio, dim, page):
+    rng = np.random.default_rng(dim + ratio)
+    lens = [1, 31, 32, 33, 150, 0, 257, 64]
+    attend(vbq, rng, heads, ratio, dim, page, lens, [1] * len(lens), dtype)
+
+
+@pytest.mark.parametrize("dtype", ["float16", "bfloat16"])
+@pytest.mark.parametrize("heads,ratio,dim,page,lens,news", [
+    (2, 4, 128, 32, [40, 33, 5, 300], [5, 1, 5, 3]),
+    (1, 1, 64, 64, [100, 70], [100, 33]),
+    (1, 5, 128, 32, [64, 31, 97], [64, 0, 50]),
+    (1, 3, 256, 64, [90], [41]),
+    (2, 2, 192, 32, [65, 50], [20, 50]),
+    (1, 4, 64, 32, [3, 20], [7, 20]),       # more queries than tokens: the first rows see nothing
+])
+def test_attention_of_several_tokens(vbq, dtype, heads, ratio, dim, page, lens, news):
+    rng = np.random.default_rng(sum(lens) + dim)
+    attend(vbq, rng, heads, ratio, dim, page, lens, news, dtype)
+    attend(vbq, rng, heads, ratio, dim, page, lens, news, dtype, causal=False, scale=0.3)
+
+
+@pytest.mark.parametrize("window,sinks", [(1, 0), (7, 1), (32, 4), (50, 33), (64, 200), (1000, 4), (33, 64)])
+@pytest.mark.parametrize("lens,news", [([200, 1, 37, 99], [1, 1, 1, 1]), ([210, 70], [9, 70]), ([33, 160], [20, 64])])
+def test_attention_under_a_window(vbq, window, sinks, lens, news):
+    rng = np.random.default_rng(window + sinks + lens[0])
+    attend(vbq, rng, 2, 2, 64, 32, lens, news, window=window, sinks=sinks)
+    attend(vbq, rng, 1, 5, 128, 64, lens, news, "bfloat16", window=window, sinks=sinks)
+
+
+def test_attention_in_pieces_and_whole(vbq):
+    """A long sequence is split over workgroups, beside short ones that are not."""
+    rng = np.random.default_rng(5)
+    attend(vbq, rng, 1, 4, 128, 64, [4200, 3, 600, 0], [1, 1, 1, 1], max_kv=6000)
+    attend(vbq, rng, 1, 8, 64, 128, [3000, 700], [4, 2], "bfloat16")
+    attend(vbq, rng, 1, 4, 256, 64, [1500], [9], window=900, sinks=5)
+
+
+def test_attention_of_peaked_and_flat_scores(vbq):
+    rng = np.random.default_rng(6)
+    attend(vbq, rng, 1, 4, 128, 64, [700], [1], gain=12.0)
+    attend(vbq, rng, 1, 4, 128, 64, [700], [1], gain=1e-4)
+    attend(vbq, rng, 1, 4, 128, 64, [300], [20], gain=12.0)
+
+
+def test_attention_repeats_and_strided_queries_agree(vbq):
+    import torch
+    rng = np.random.default_rng(7)
+    args, kw, out = attend(vbq, rng, 2, 4, 128, 64, [900, 2000], [3, 1])
+    ws = vbq.kv4_attention_workspace(args[0], 2, 4, 8, 3, 2000)
+    for _ in range(4):
+        again = vbq.kv4_attention(*args, workspace=ws, **kw)
+        assert torch.equal(again, out)
+    assert int(ws[:vbq.KV4_COUNTER_BYTES].max()) == 0
+    q = args[1]
+    wide = torch.randn(q.shape[0], 3, 12, 128, device="cuda").half()
+    wide[:, 1, 2:10] = q
+    assert torch.equal(vbq.kv4_attention(args[0], wide[:, 1, 2:10], *args[2:], **kw), out)
+    turned = q.transpose(0, 1).contiguous().transpose(0, 1)     # heads first in memory
+    assert torch.equal(vbq.kv4_attention(args[0], turned, *args[2:], **kw), out)
+
+
+def test_a_hidden_token_cannot_reach_an_output(vbq):
+    """Appending infinities and NaN after a query's position leaves its output as it was."""
+    import torch
+    i32 = dict(dtype=torch.int32, device="cuda")
+    gen = torch.Generator(device="cuda").manual_seed(1)
+    k = torch.randn(40, 1, 64, generator=gen, device="cuda")
+    v = torch.randn(40, 1, 64, generator=gen, device="cuda")
+    q = torch.randn(40, 4, 64, generator=gen, device="cuda").half()
+    outs = []
+    for bad in (False, True):
+        if bad:
+            k[20:, :, 3], v[20:, :, 5], v[25] = float("nan"), float("-inf"), float("inf")
+        cache = vbq.Kv4Cache(2, 32, 1, 64)
+        table, z, cu = torch.tensor([[1, 0]], **i32), torch.zeros(1, **i32), torch.tensor([0, 40], **i32)
+        vbq.kv4_append(cache, k, v, table, z, cu)
+        outs.append(vbq.kv4_attention(cache, q, table, torch.tensor([40], **i32), cu, 40, 40))
+    assert torch.equal(outs[0][:20], outs[1][:20])
+    assert torch.isfinite(outs[1]).all()
+
+
+def test_a_nan_query_spoils_its_own_rows_only(vbq):
+    import torch
+    rng = np.random.default_rng(8)
+    args, kw, out = attend(vbq, rng, 2, 4, 64, 32, [90, 50], [6, 1])
+    q = args[1].clone()
+    q[2, 5, 11] = float("nan")
+    got = vbq.kv4_attention(args[0], q, *args[2:], **kw)
+    assert torch.isnan(got[2, 5]).all()
+    got[2, 5] = out[2, 5]
+    assert torch.equal(got, out)
+
+
+def test_cache_calls_on_another_stream_and_in_a_graph(vbq):
+    import torch
+    i32 = dict(dtype=torch.int32, device="cuda")
+    gen = torch.Generator(device="cuda").manual_seed(2)
+    heads, dim, B, n = 2, 128, 3, 200
+    cache = vbq.Kv4Cache(B * 4, 64, heads, dim)
+    table = torch.randperm(B * 4, generator=gen, device="cuda").int().view(B, 4)
+    kv = torch.randn(2, B * n, heads, dim, generator=gen, device="cuda").half()
+    vbq.kv4_append(cache, kv[0], kv[1], table, torch.zeros(B, **i32), torch.arange(0, B * n + 1, n, **i32))
+    k1, v1 = torch.randn(2, B, heads, dim, generator=gen, device="cuda").half()
+    q = torch.randn(B, 8, dim, generator=gen, device="cuda").half()
+    start, lens = torch.full((B,), n, **i32), torch.full((B,), n + 1, **i32)
+    cu = torch.arange(B + 1, **i32)
+    ws = vbq.kv4_attention_workspace(cache, B, B, 8, 1, 256)
+    out = torch.empty_like(q)
+
+    def step():
+        vbq.kv4_append(cache, k1, v1, table, start, cu, max_tokens=1)
+        vbq.kv4_attention(cache, q, table, lens, cu, 1, 256, out=out, workspace=ws)
+
+    step()
+    eager = out.clone()
+    side = torch.cuda.Stream()
+    side.wait_stream(torch.cuda.current_stream())
+    got = vbq.kv4_attention(cache, q, table, lens, cu, 1, 256, stream=side)
+    side.synchronize()
+    assert torch.equal(got, eager)
+    graph = torch.cuda.CUDAGraph()
+    torch.cuda.synchronize()
+    with torch.cuda.graph(graph):
+        step()
+    for i in range(4):
+        k1.copy_(torch.randn(k1.shape, generator=gen, device="cuda"))
+        q.copy_(torch.randn(q.shape, generator=gen, device="cuda"))
+        graph.replay()
+        torch.cuda.synchronize()
+        replayed = out.clone()
+        step()
+        assert torch.equal(out, replayed)
+
+
+def test_far_pages_of_a_large_cache(vbq):
+    """Byte offsets past 4 GiB."""
+    import torch
+    i32 = dict(dtype=torch.int32, device="cuda")
+    heads, dim, page = 8, 128, 1024
+    n_pages = 4 * 2 ** 30 // vbq.lib.kv4_page_bytes(page, heads, dim) + 20
+    cache = vbq.Kv4Cache(n_pages, page, heads, dim)
+    small = vbq.Kv4Cache(2, page, heads, dim)
+    gen = torch.Generator(device="cuda").manual_seed(4)
+    kv = torch.randn(2, 1100, heads, dim, generator=gen, device="cuda").bfloat16()
+    q = torch.randn(3, 32, dim, generator=gen, device="cuda").bfloat16()
+    outs = []
+    for c, table in ((cache, [[n_pages - 1, n_pages - 2]]), (small, [[0, 1]])):
+        t = torch.tensor(table, **i32)
+        cu = torch.tensor([0, 1100], **i32)
+        vbq.kv4_append(c, kv[0], kv[1], t, torch.zeros(1, **i32), cu)
+        outs.append((vbq.kv4_attention(c, q, t, torch.tensor([1100], **i32), torch.tensor([0, 3], **i32), 3, 1100),
+                     *vbq.kv4_read(c, t, torch.zeros(1, **i32), cu, 1100, torch.float16)))
+        assert c.check() is False
+    for x, y in zip(*outs):
+        assert torch.equal(x, y)
+
+
+# ---- what does not fit ---------------------------------------------------------------
+def test_wrong_tables_and_lengths_are_reported_and_touch_nothing(vbq):
+    import torch
+    i32 = dict(dtype=torch.int32, device="cuda")
+    cache = vbq.Kv4Cache(3, 32, 1, 64)
+    k = torch.randn(4, 1, 64, device="cuda")
+    cu = torch.tensor([0, 1, 4], **i32)
+    good = torch.tensor([[0, 1], [2, 1]], **i32)
+    cases = [
+        (torch.tensor([[3, 1], [-1, 1]], **i32), torch.zeros(2, **i32), cu, 3, "block-table"),
+        (good, torch.tensor([-1, 64], **i32), cu, 3, "lengths"),
+        (good, torch.zeros(2, **i32), torch.tensor([0, 3, 1], **i32), 2, "lengths"),
+        (good, torch.zeros(2, **i32), torch.tensor([0, 0, 5], **i32), 9, "lengths"),
+    ]
+    for table, start, c, most, what in cases:
+        before = cache.data.clone()
+        vbq.kv4_append(cache, k, k, table, start, c, max_tokens=most)
+        with pytest.raises(vbq.VbqError, match=what):
+            cache.check()
+        assert torch.equal(cache.data, before)
+        assert cache.check() is False
+    q = torch.randn(2, 2, 64, device="cuda").half()
+    cu2 = torch.tensor([0, 1, 2], **i32)
+    for table, lens, c, max_q, max_kv, what in [
+        (torch.tensor([[0, 7], [2, 1]], **i32), [40, 40], cu2, 1, 64, "block-table"),
+        (good, [65, 3], cu2, 1, 100, "lengths"),
+        (good, [33, 3], cu2, 1, 32, "lengths"),
+        (good, [-1, 3], cu2, 1, 64, "lengths"),
+        (good, [3, 3], torch.tensor([0, 1, 9], **i32), 1, 64, "lengths"),
+    ]:
+        vbq.kv4_attention(cache, q, table, torch.tensor(lens, **i32), c, max_q, max_kv)
+        with pytest.raises(vbq.VbqError, match=what):
+            cache.check()
+    # a page that is not there counts as no tokens; reading it gives zeros
+    table = torch.tensor([[5, 1]], **i32)
+    rk, rv = vbq.kv4_read(cache, table, torch.zeros(1, **i32), torch.tensor([0, 4], **i32), 4, torch.float32)
+    assert not rk.any() and not rv.any()
+    with pytest.raises(vbq.VbqError):
+        cache.check()
+
+
+def test_the_binding_refuses_what_does_not_fit(vbq):
+    import torch
+    i32 = dict(dtype=torch.int32, device="cuda")
+    cache = vbq.Kv4Cache(2, 32, 2, 64)
+    table, lens, cu = torch.zeros(1, 2, **i32), torch.tensor([3], **i32), torch.tensor([0, 1], **i32)
+    q = torch.zeros(1, 4, 64, device="cuda").half()
+    k = torch.zeros(1, 2, 64, device="cuda").half()
+    with pytest.raises(ValueError, match="dtype"):
+        vbq.kv4_attention(cache, q.float(), table, lens, cu, 1, 3)
+    with pytest.raises(ValueError, match="shape"):
+        vbq.kv4_attention(cache, q[:, :3], table, lens, cu, 1, 3)
+    with pytest.raises(ValueError, match="lengths: dtype"):
+        vbq.kv4_attention(cache, q, table, lens.long(), cu, 1, 3)
+    with pytest.raises(ValueError, match="window"):
+        vbq.kv4_attention(cache, q, table, lens, cu, 1, 3, causal=False, window=4)
+    with pytest.raises(ValueError, match="aligned"):
+        vbq.kv4_attention(cache, torch.zeros(1 * 4 * 64 + 1, device="cuda").half()[1:].view(1, 4, 64), table, lens, cu, 1, 3)
+    with pytest.raises(ValueError, match="channels"):
+        vbq.kv4_append(cache, k.transpose(1, 2).contiguous().transpose(1, 2), k, table, lens, cu)
+    with pytest.raises(ValueError, match="v:"):
+        vbq.kv4_append(cache, k, k.bfloat16(), table, lens, cu)
+    with pytest.raises(ValueError, match="on cpu"):
+        vbq.kv4_append(cache, k.cpu(), k, table, lens, cu)
+    with pytest.raises(ValueError, match="out k"):
+        vbq.kv4_read(cache, table, lens, cu, 1, torch.float16, out=(k.float(), k.float()))
+    with pytest.raises(vbq.VbqError, match="layout does not match"):
+        vbq.kv4_attention(cache, q, table, lens, cu, 1, 3, workspace=torch.zeros(16, dtype=torch.uint8, device="cuda"))
+    with pytest.raises(vbq.VbqError, match="invalid argument"):
+        vbq.kv4_attention(cache, q, table, lens, cu, 1, 3, scale=-1.0)
+    with pytest.raises(ValueError, match="refused"):
+        vbq.kv4_attention(cache, q, table, lens, cu, 1, -3)
