@@ -157,7 +157,7 @@ __device__ inline f32x2 get2(const float* p) {
 }
 
 template <int G, int NT>
-__global__ __launch_bounds__(256) void k_kv4_attn(KvAttn a) {
+__global__ __launch_bounds__(256, (G <= 2 && NT == 1) ? 4 : (G * NT <= 4) ? 2 : 1) void k_kv4_attn(KvAttn a) {
   constexpr int D = 64 * G, ROWS = 16 * NT, PITCH = D + 4;
   __shared__ __attribute__((aligned(16))) float buf[kWaves * 16 * PITCH];
   __shared__ float wml[kWaves][ROWS][2];
