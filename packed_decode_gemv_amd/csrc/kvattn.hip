@@ -60,17 +60,29 @@ __device__ inline half8_t key_codes(uint32_t w) {
   return __builtin_bit_cast(half8_t, r);
 }
 
+// Constants of the value decode, opaque to the compiler: with the masks in
+// scalar and the exponents in vector registers (w & mask) | exponent is one
+// instruction; known constants become two with a literal each.
+struct Decode {
+  uint32_t m0, m4, ex;
+  __device__ Decode() : m0(0x000F000Fu), m4(0x00F000F0u), ex(0x64006400u) {
+    asm("" : "+s"(m0));
+    asm("" : "+s"(m4));
+    asm("" : "+v"(ex));
+  }
+};
+
 // Eight values s c + o of a value word, pairs (n, n + 4); s and o hold the
 // pairs' scales and offsets.
-__device__ inline half8_t values(uint32_t w, const u32x4& s, const u32x4& o) {
+__device__ inline half8_t values(const Decode& dc, uint32_t w, const u32x4& s, const u32x4& o) {
   const half2_t one = {(_Float16)1024.f, (_Float16)1024.f}, sx = {(_Float16)0.0625f, (_Float16)0.0625f},
                 sb = {(_Float16)-64.f, (_Float16)-64.f};
   const uint32_t h = w >> 8;
   half2_t c[4];
-  c[0] = __builtin_bit_cast(half2_t, (w & 0x000F000Fu) | 0x64006400u) - one;
-  c[1] = __builtin_elementwise_fma(__builtin_bit_cast(half2_t, (w & 0x00F000F0u) | 0x64006400u), sx, sb);
-  c[2] = __builtin_bit_cast(half2_t, (h & 0x000F000Fu) | 0x64006400u) - one;
-  c[3] = __builtin_elementwise_fma(__builtin_bit_cast(half2_t, (h & 0x00F000F0u) | 0x64006400u), sx, sb);
+  c[0] = __builtin_bit_cast(half2_t, (w & dc.m0) | dc.ex) - one;
+  c[1] = __builtin_elementwise_fma(__builtin_bit_cast(half2_t, (w & dc.m4) | dc.ex), sx, sb);
+  c[2] = __builtin_bit_cast(half2_t, (h & dc.m0) | dc.ex) - one;
+  c[3] = __builtin_elementwise_fma(__builtin_bit_cast(half2_t, (h & dc.m4) | dc.ex), sx, sb);
   u32x4 r;
 #pragma unroll
   for (int i = 0; i < 4; ++i) {
@@ -85,27 +97,17 @@ __device__ inline float half_at(const u32x4& w, int i) {
   return (float)__builtin_bit_cast(_Float16, (uint16_t)(w[i >> 1] >> (16 * (i & 1))));
 }
 
+// A block's copy to LDS, 16 bytes a lane and copy (no registers, so the next
+// block is on its way while this one is worked on).
 template <int G>
-struct Block {
-  u32x4 kc[G], vc[G], ks[G], ko[G], vs[G], vo[G];
-};
-
-template <int G>
-__device__ inline void load_block(Block<G>& b, const uint8_t* p, uint32_t lane) {
-  const uint32_t q = lane >> 4;
+__device__ inline void copy_block(uint32_t lds, const uint8_t* p, uint32_t lane) {
+  constexpr int BYTES = kKvGroupBytes * G;
+  const u32x4 rsrc = make_rsrc(p, BYTES);
 #pragma unroll
-  for (int g = 0; g < G; ++g) {
-    b.kc[g] = *reinterpret_cast<const u32x4*>(p + 1024 * g + 16 * lane);
-    b.ks[g] = *reinterpret_cast<const u32x4*>(p + kv_key_so(G) + 128 * g + 16 * q);
-    b.ko[g] = *reinterpret_cast<const u32x4*>(p + kv_key_so(G) + 128 * g + 64 + 16 * q);
-  }
-#pragma unroll
-  for (int g = 0; g < G; ++g) {
-    b.vc[g] = *reinterpret_cast<const u32x4*>(p + kv_value_codes(G) + 1024 * g + 16 * lane);
-    b.vs[g] = *reinterpret_cast<const u32x4*>(p + kv_value_so(G) + 128 * g + 16 * q);
-    b.vo[g] = *reinterpret_cast<const u32x4*>(p + kv_value_so(G) + 128 * g + 64 + 16 * q);
-  }
+  for (int i = 0; i < BYTES / 1024; ++i) dma16(rsrc, lds + 1024 * i, 1024 * i + 16 * lane);
+  if (lane < (BYTES % 1024) / 16) dma16(rsrc, lds + BYTES / 1024 * 1024, BYTES / 1024 * 1024 + 16 * lane);
 }
+__device__ inline u32x4 lds16(const uint8_t* p) { return *reinterpret_cast<const u32x4*>(p); }
 
 // The blocks that a row tile looks at: sink blocks 0 .. ns-1, then w0 .. w0+nw-1.
 struct Reach {
@@ -158,11 +160,15 @@ __device__ inline f32x2 get2(const float* p) {
 
 template <int G, int NT>
 __global__ __launch_bounds__(256, (G <= 2 && NT == 1) ? 4 : (G * NT <= 4) ? 2 : 1) void k_kv4_attn(KvAttn a) {
-  constexpr int D = 64 * G, ROWS = 16 * NT, PITCH = D + 4;
-  __shared__ __attribute__((aligned(16))) float buf[kWaves * 16 * PITCH];
+  constexpr int D = 64 * G, ROWS = 16 * NT, PITCH = D + 4, BYTES = kKvGroupBytes * G;
+  // two blocks a wavefront; afterwards the wavefronts' sums, the pieces' factors and partial sums
+  constexpr int SUMS = kWaves * 16 * PITCH * 4, JOIN = 16 * kMaxSplits * 4 + 256 * 16;
+  constexpr int AFTER = SUMS > JOIN ? SUMS : JOIN;
+  __shared__ __attribute__((aligned(16))) uint8_t ring[kWaves * 2 * BYTES > AFTER ? kWaves * 2 * BYTES : AFTER];
   __shared__ float wml[kWaves][ROWS][2];
-  __shared__ f32x4 share[256];
   __shared__ uint32_t last;
+  float* const buf = reinterpret_cast<float*>(ring);
+  f32x4* const share = reinterpret_cast<f32x4*>(ring + 16 * kMaxSplits * 4);
   const uint32_t tid = threadIdx.x, lane = tid & 63u, col = lane & 15u, quarter = lane >> 4;
   const int wave = __builtin_amdgcn_readfirstlane(tid >> 6);
 
@@ -190,6 +196,33 @@ __global__ __launch_bounds__(256, (G <= 2 && NT == 1) ? 4 : (G * NT <= 4) ? 2 : 
   const int splits = min(a.splits, max(1, (blocks + a.chunk - 1) / a.chunk));   // that have work
   if ((int)split >= splits) return;
   const int i0 = (int)split * a.chunk, i1 = (int)split == splits - 1 ? blocks : i0 + a.chunk;
+
+  // This wavefront's blocks, and the first one's copy.
+  const uint32_t in_page = (1u << a.cache.block_shift) - 1u;
+  uint8_t* const mine = ring + wave * 2 * BYTES;
+  const uint32_t mine_lds = lds_addr(mine);
+  int pages = -1;   // lane i: the page of the wavefront's block i (of 64 at a time)
+  auto block_of = [&](int idx) { return idx < re.ns ? idx : idx - re.ns + re.w0; };
+  // starts the copy of block `it` (number idx of the tile's) and returns whether there is one
+  auto start_copy = [&](int it, int idx) {
+    if ((it & 63) == 0) {
+      const int next = idx + kWaves * (int)lane;
+      pages = -1;
+      if (next < i1) {
+        pages = a.table[(int64_t)b * a.width + (block_of(next) >> a.cache.block_shift)];
+        if ((uint32_t)pages >= (uint32_t)a.cache.n_pages) {
+          pages = -1;
+          kv_flag(a.cache, VBQ_KV4_FLAG_PAGE);
+        }
+      }
+    }
+    const int page = __builtin_amdgcn_readlane(pages, it & 63);
+    if (page < 0) return false;
+    copy_block<G>(mine_lds + (it & 1) * BYTES,
+                  kv_block(a.cache, G, (uint32_t)page, head, (uint32_t)block_of(idx) & in_page), lane);
+    return true;
+  };
+  bool have = i0 + wave < i1 && start_copy(0, i0 + wave);
 
   // Queries: B operands per group and 32-channel step, their sums per group,
   // and what each lane's column sees.
@@ -245,6 +278,7 @@ __global__ __launch_bounds__(256, (G <= 2 && NT == 1) ? 4 : (G * NT <= 4) ? 2 : 
     lo[nt] = a.window ? p - a.window + 1 : INT32_MIN;
   }
 
+  const Decode dc;
   float m[NT], l[NT];
   f32x4 acc[NT][G][4];
 #pragma unroll
@@ -257,36 +291,27 @@ __global__ __launch_bounds__(256, (G <= 2 && NT == 1) ? 4 : (G * NT <= 4) ? 2 : 
       for (int w = 0; w < 4; ++w) acc[nt][g][w] = f32x4{0.f, 0.f, 0.f, 0.f};
   }
 
-  const uint32_t in_page = (1u << a.cache.block_shift) - 1u;
-  int pages = 0;   // lane i: the page of this wavefront's i-th block (of the current 64)
   for (int it = 0, idx = i0 + wave; idx < i1; ++it, idx += kWaves) {
-    if ((it & 63) == 0) {
-      const int mine = idx + kWaves * (int)lane;
-      pages = -1;
-      if (mine < i1) {
-        const int blk = mine < re.ns ? mine : mine - re.ns + re.w0;
-        pages = a.table[(int64_t)b * a.width + (blk >> a.cache.block_shift)];
-        if ((uint32_t)pages >= (uint32_t)a.cache.n_pages) {
-          pages = -1;
-          kv_flag(a.cache, VBQ_KV4_FLAG_PAGE);
-        }
-      }
-    }
-    const int page = __builtin_amdgcn_readlane(pages, it & 63);
-    if (page < 0) continue;
-    const int blk = idx < re.ns ? idx : idx - re.ns + re.w0;
-    Block<G> k;
-    load_block<G>(k, kv_block(a.cache, G, (uint32_t)page, head, (uint32_t)blk & in_page), lane);
+    const bool here = have;
+    // This block's copy has landed, and the last block's reads of the other buffer are done.
+    asm volatile("s_waitcnt vmcnt(0) lgkmcnt(0)" ::: "memory");
+    have = idx + kWaves < i1 && start_copy(it + 1, idx + kWaves);
+    if (!here) continue;
+    const int blk = block_of(idx);
+    const uint8_t* const k = mine + (it & 1) * BYTES;
 
     // scores of the lane's column: token 8 quarter + 4 half + i
     f32x4 sc[NT][2];
 #pragma unroll
     for (int nt = 0; nt < NT; ++nt) sc[nt][0] = sc[nt][1] = f32x4{0.f, 0.f, 0.f, 0.f};
 #pragma unroll
-    for (int g = 0; g < G; ++g)
+    for (int g = 0; g < G; ++g) {
+      const u32x4 kc = lds16(k + 1024 * g + 16 * lane);
+      const u32x4 ks = lds16(k + kv_key_so(G) + 128 * g + 16 * quarter);
+      const u32x4 ko = lds16(k + kv_key_so(G) + 128 * g + 64 + 16 * quarter);
 #pragma unroll
       for (int hf = 0; hf < 2; ++hf) {
-        const half8_t a0 = key_codes(k.kc[g][2 * hf]), a1 = key_codes(k.kc[g][2 * hf + 1]);
+        const half8_t a0 = key_codes(kc[2 * hf]), a1 = key_codes(kc[2 * hf + 1]);
 #pragma unroll
         for (int nt = 0; nt < NT; ++nt) {
           f32x4 d = f32x4{0.f, 0.f, 0.f, 0.f};
@@ -294,10 +319,11 @@ __global__ __launch_bounds__(256, (G <= 2 && NT == 1) ? 4 : (G * NT <= 4) ? 2 : 
           d = __builtin_amdgcn_mfma_f32_16x16x32_f16(a1, qf[nt][g][1], d, 0, 0, 0);
 #pragma unroll
           for (int i = 0; i < 4; ++i)
-            sc[nt][hf][i] = __builtin_fmaf(half_at(k.ks[g], 4 * hf + i), d[i],
-                                           __builtin_fmaf(half_at(k.ko[g], 4 * hf + i), qsum[nt][g], sc[nt][hf][i]));
+            sc[nt][hf][i] = __builtin_fmaf(half_at(ks, 4 * hf + i), d[i],
+                                           __builtin_fmaf(half_at(ko, 4 * hf + i), qsum[nt][g], sc[nt][hf][i]));
         }
       }
+    }
     const int t0 = blk * kKvBlock;
     const bool edge = t0 + kKvBlock - 1 > min(p_min, len - 1) ||
                       (a.window && t0 <= p_max - a.window && t0 + kKvBlock > a.sinks);
@@ -312,19 +338,10 @@ __global__ __launch_bounds__(256, (G <= 2 && NT == 1) ? 4 : (G * NT <= 4) ? 2 : 
             const bool see = t <= hi[nt] && (t >= lo[nt] || t < a.sinks);
             sc[nt][hf][i] = see ? sc[nt][hf][i] : -__builtin_inff();
           }
-          // places past the sequence's end may hold anything
-          if (t >= len) {
-            const uint32_t keep = hf ? 0x0000FFFFu : 0xFFFF0000u;
-#pragma unroll
-            for (int g = 0; g < G; ++g) {
-              k.vs[g][i] &= keep;
-              k.vo[g][i] &= keep;
-            }
-          }
         }
     }
     // running maximum and sum
-    half8_t pf[NT];
+    half8_t pf[NT], pl[NT];   // probabilities, and what their rounding to fp16 leaves
     bool grow = false;
     float mt[NT];
 #pragma unroll
@@ -359,17 +376,34 @@ __global__ __launch_bounds__(256, (G <= 2 && NT == 1) ? 4 : (G * NT <= 4) ? 2 : 
         l[nt] += p0 + p1;
         pf[nt][2 * i] = (_Float16)p0;
         pf[nt][2 * i + 1] = (_Float16)p1;
+        pl[nt][2 * i] = (_Float16)(p0 - (float)pf[nt][2 * i]);
+        pl[nt][2 * i + 1] = (_Float16)(p1 - (float)pf[nt][2 * i + 1]);
       }
     }
 #pragma unroll
-    for (int g = 0; g < G; ++g)
+    for (int g = 0; g < G; ++g) {
+      const u32x4 vc = lds16(k + kv_value_codes(G) + 1024 * g + 16 * lane);
+      u32x4 vs = lds16(k + kv_value_so(G) + 128 * g + 16 * quarter);
+      u32x4 vo = lds16(k + kv_value_so(G) + 128 * g + 64 + 16 * quarter);
+      if (t0 + kKvBlock > len) {   // places past the sequence's end may hold anything
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+          const int t = t0 + 8 * (int)quarter + i;
+          const uint32_t keep = t + 4 < len ? 0xFFFFFFFFu : t < len ? 0x0000FFFFu : 0u;
+          vs[i] &= keep;
+          vo[i] &= keep;
+        }
+      }
 #pragma unroll
       for (int w = 0; w < 4; ++w) {
-        const half8_t v = values(k.vc[g][w], k.vs[g], k.vo[g]);
+        const half8_t v = values(dc, vc[w], vs, vo);
 #pragma unroll
-        for (int nt = 0; nt < NT; ++nt)
+        for (int nt = 0; nt < NT; ++nt) {
           acc[nt][g][w] = __builtin_amdgcn_mfma_f32_16x16x32_f16(v, pf[nt], acc[nt][g][w], 0, 0, 0);
+          acc[nt][g][w] = __builtin_amdgcn_mfma_f32_16x16x32_f16(v, pl[nt], acc[nt][g][w], 0, 0, 0);
+        }
       }
+    }
   }
 
   // Join the four wavefronts: every one scales its sums to the common maximum.
