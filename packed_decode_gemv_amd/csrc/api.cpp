@@ -125,8 +125,7 @@ vbq_status check_attn(const vbq_kv4* cache, const vbq_kv4_attn* a, bool pointers
   if ((int64_t)a->max_q * ratio > INT32_MAX - 64) return VBQ_ERR_UNSUPPORTED;
   if (a->max_kv > INT32_MAX - 64) return VBQ_ERR_UNSUPPORTED;
   *p = kv4_attn_plan(a->batch, cache->n_kv_heads, ratio, c->groups, a->max_q, a->max_kv, a->window, a->sinks);
-  *bytes = VBQ_KV4_COUNTER_BYTES;
-  if (p->splits > 1) *bytes += p->tiles * p->splits * p->rows * (int64_t)(cache->head_dim + 2) * 4;
+  *bytes = (int64_t)2 * p->pieces * p->rows * (cache->head_dim + 2) * 4;
   return VBQ_OK;
 }
 
@@ -183,7 +182,7 @@ vbq_status kv4_attention(const vbq_kv4* cache, const vbq_kv4_attn* a, hipStream_
   int64_t bytes = 0;
   vbq_status st = check_attn(cache, a, true, &k.cache, &p, &bytes);
   if (st != VBQ_OK) return st;
-  if (!a->table || !a->kv_lens || !a->cu_q || !a->workspace) return VBQ_ERR_INVALID_ARG;
+  if (!a->table || !a->kv_lens || !a->cu_q || (bytes > 0 && !a->workspace)) return VBQ_ERR_INVALID_ARG;
   if (!aligned(a->table, 4) || !aligned(a->kv_lens, 4) || !aligned(a->cu_q, 4) || !aligned(a->workspace, 16) ||
       !aligned(a->lse, 4) || !aligned(a->q, 16) || !aligned(a->out, 16) || a->q_token_stride % 8 ||
       a->q_head_stride % 8)
@@ -199,10 +198,8 @@ vbq_status kv4_attention(const vbq_kv4* cache, const vbq_kv4_attn* a, hipStream_
   k.q_hs = a->q_head_stride;
   k.out = static_cast<uint16_t*>(a->out);
   k.lse = a->lse;
-  uint8_t* const ws = static_cast<uint8_t*>(a->workspace);
-  k.counters = reinterpret_cast<uint32_t*>(ws);
-  k.acc = reinterpret_cast<float*>(ws + VBQ_KV4_COUNTER_BYTES);
-  k.ml = k.acc + (p.splits > 1 ? p.tiles * p.splits * p.rows * (int64_t)cache->head_dim : 0);
+  k.acc = static_cast<float*>(a->workspace);
+  k.ml = k.acc + (int64_t)2 * p.pieces * p.rows * cache->head_dim;
   k.width = a->table_width;
   k.total_q = a->total_q;
   k.max_q = a->max_q;
@@ -214,8 +211,9 @@ vbq_status kv4_attention(const vbq_kv4* cache, const vbq_kv4_attn* a, hipStream_
   k.window = a->window;
   k.sinks = a->window ? a->sinks : 0;
   k.row_tiles = p.row_tiles;
-  k.splits = p.splits;
-  k.chunk = p.chunk;
+  k.batch = a->batch;
+  k.pieces = p.pieces;
+  k.min_chunk = 8;
   k.scale_log2 = a->scale * 1.44269504088896341f;
   hipError_t e = launch_kv4_attention(k, p, a->batch, stream);
   return e == hipErrorNotSupported ? VBQ_ERR_UNSUPPORTED : from_hip(e);

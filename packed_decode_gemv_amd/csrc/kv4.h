@@ -50,24 +50,24 @@ struct KvAttn {
   int64_t q_ts, q_hs;
   uint16_t* out;
   float* lse;
-  uint32_t* counters;   // one per row tile, zero between calls
-  float* ml;            // [tile][split][rows][2]: maximum (in powers of two) and sum
-  float* acc;           // [tile][split][rows][head_dim]
+  float* acc;           // partial sums, two slots a piece: [rows][head_dim]
+  float* ml;            // their maxima (powers of two) and sums: [rows][2]
   int32_t width, total_q, max_q, max_kv;
   int32_t n_heads, ratio;      // query heads, and how many share a key/value head
   int32_t bf16, causal, window, sinks;
   int32_t row_tiles;           // row tiles of a (sequence, head)
-  int32_t splits, chunk;       // pieces of the token axis, and blocks in each
+  int32_t batch;
+  int32_t pieces, min_chunk;   // pieces of the line (0: a workgroup a tile), and blocks each takes at least
   float scale_log2;            // scale * log2(e)
 };
 
 hipError_t launch_kv4_append(const KvCache& c, const KvRange& r, const void* k, const void* v, int dtype,
                              int64_t k_ts, int64_t k_hs, int64_t v_ts, int64_t v_hs, hipStream_t s);
 hipError_t launch_kv4_read(const KvCache& c, const KvRange& r, void* k, void* v, int dtype, hipStream_t s);
-// Sizes of an attention launch: rows a workgroup takes, row tiles, splits and
-// blocks per split, from the call's sizes alone.
+// Sizes of an attention launch, from the call's sizes alone: rows of a tile,
+// row tiles of a (sequence, head), pieces (0: a workgroup a tile), tiles.
 struct KvAttnPlan {
-  int32_t rows, row_tiles, splits, chunk;
+  int32_t rows, row_tiles, pieces;
   int64_t tiles;
 };
 KvAttnPlan kv4_attn_plan(int batch, int heads, int ratio, int groups, int max_q, int max_kv, int window, int sinks);

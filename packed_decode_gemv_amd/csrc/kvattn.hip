@@ -37,15 +37,39 @@ typedef float f32x2 __attribute__((ext_vector_type(2)));
 constexpr int kWaves = 4;
 constexpr float kNoMax = -1e30f;     // running maximum before any token
 constexpr float kProbShift = 15.f;   // probabilities are held times 2^15
-constexpr int kMaxSplits = 256;
+constexpr int kMaxPieces = 512;
 
-__device__ inline float rows_max(float v) {   // over the four lane quarters of a column
-  v = fmaxf(v, __shfl_xor(v, 16, 64));
-  return fmaxf(v, __shfl_xor(v, 32, 64));
+// Exchanges with the lanes 16 and 32 apart (the lane quarters of a column).
+typedef uint32_t pair_t __attribute__((ext_vector_type(2)));
+__device__ inline float rows_max(float v) {
+  uint32_t u = __builtin_bit_cast(uint32_t, v);
+  pair_t p = __builtin_amdgcn_permlane16_swap(u, u, false, false);
+  uint32_t x = p.x, y = p.y;
+  v = fmaxf(__builtin_bit_cast(float, x), __builtin_bit_cast(float, y));
+  u = __builtin_bit_cast(uint32_t, v);
+  p = __builtin_amdgcn_permlane32_swap(u, u, false, false);
+  x = p.x, y = p.y;
+  return fmaxf(__builtin_bit_cast(float, x), __builtin_bit_cast(float, y));
 }
 __device__ inline float rows_sum(float v) {
-  v += __shfl_xor(v, 16, 64);
-  return v + __shfl_xor(v, 32, 64);
+  uint32_t u = __builtin_bit_cast(uint32_t, v);
+  pair_t p = __builtin_amdgcn_permlane16_swap(u, u, false, false);
+  uint32_t x = p.x, y = p.y;
+  v = __builtin_bit_cast(float, x) + __builtin_bit_cast(float, y);
+  u = __builtin_bit_cast(uint32_t, v);
+  p = __builtin_amdgcn_permlane32_swap(u, u, false, false);
+  x = p.x, y = p.y;
+  return __builtin_bit_cast(float, x) + __builtin_bit_cast(float, y);
+}
+// Inclusive sum over the lanes of a wavefront.
+__device__ inline int wave_scan(int v) {
+  v += __builtin_amdgcn_update_dpp(0, v, 0x111, 0xF, 0xF, true);   // row_shr:1
+  v += __builtin_amdgcn_update_dpp(0, v, 0x112, 0xF, 0xF, true);   // row_shr:2
+  v += __builtin_amdgcn_update_dpp(0, v, 0x114, 0xF, 0xF, true);   // row_shr:4
+  v += __builtin_amdgcn_update_dpp(0, v, 0x118, 0xF, 0xF, true);   // row_shr:8
+  v += __builtin_amdgcn_update_dpp(0, v, 0x142, 0xA, 0xF, false);  // row_bcast:15 into rows 1 and 3
+  v += __builtin_amdgcn_update_dpp(0, v, 0x143, 0xC, 0xF, false);  // row_bcast:31 into rows 2 and 3
+  return v;
 }
 
 // Eight codes of a key word as fp16 subnormals: pairs (n, n + 4), the odd
@@ -97,8 +121,10 @@ __device__ inline float half_at(const u32x4& w, int i) {
   return (float)__builtin_bit_cast(_Float16, (uint16_t)(w[i >> 1] >> (16 * (i & 1))));
 }
 
-// A block's copy to LDS, 16 bytes a lane and copy (no registers, so the next
-// block is on its way while this one is worked on).
+// A block's copy to LDS: 16 bytes a lane and instruction, no registers, so
+// later blocks are on their way while one is worked on.
+template <int G>
+constexpr int kCopies = (kKvGroupBytes * G + 1023) / 1024;
 template <int G>
 __device__ inline void copy_block(uint32_t lds, const uint8_t* p, uint32_t lane) {
   constexpr int BYTES = kKvGroupBytes * G;
@@ -148,81 +174,204 @@ __device__ inline void store4(const KvAttn& a, int64_t elem, const f32x4& v) {
   *reinterpret_cast<u32x2*>(a.out + elem) = u32x2{w[0] | (w[1] << 16), w[2] | (w[3] << 16)};
 }
 
-__device__ inline void put2(float* p, float x, float y) {   // device-scope, written through
-  const f32x2 v = {x, y};
-  __hip_atomic_store(reinterpret_cast<uint64_t*>(p), __builtin_bit_cast(uint64_t, v), __ATOMIC_RELAXED,
-                     __HIP_MEMORY_SCOPE_AGENT);
-}
-__device__ inline f32x2 get2(const float* p) {
-  return __builtin_bit_cast(f32x2, __hip_atomic_load(reinterpret_cast<const uint64_t*>(p), __ATOMIC_RELAXED,
-                                                     __HIP_MEMORY_SCOPE_AGENT));
+// A sequence of the call as the kernels see it.
+struct Seq {
+  int32_t c0, nq, len, first;   // first row of q, queries, tokens held, position of query 0
+  Reach re;
+  int32_t blocks, tiles;        // blocks of every tile, and tiles: heads * row tiles
+};
+// False (and nothing to do) for numbers that do not fit.
+__device__ inline bool seq_from(const KvAttn& a, int rows_per_tile, int c0, int c1, int len, Seq& s) {
+  const int64_t nq = (int64_t)c1 - c0;
+  s.blocks = s.tiles = 0;
+  if (c0 < 0 || nq < 0 || c1 > a.total_q || nq > a.max_q || len < 0 || len > a.max_kv ||
+      (int64_t)len > ((int64_t)a.width << (a.cache.block_shift + 5)))
+    return false;
+  s.c0 = c0;
+  s.nq = (int32_t)nq;
+  s.len = len;
+  s.first = len - s.nq;
+  if (nq == 0) return true;
+  s.re = reach(len, a.causal ? s.first : len - 1, len - 1, a.window, a.sinks);
+  s.blocks = s.re.ns + s.re.nw;
+  s.tiles = a.cache.heads * ((s.nq * a.ratio + rows_per_tile - 1) / rows_per_tile);
+  return true;
 }
 
+// The token axes of all tiles laid end to end: sequence by sequence, tile by
+// tile, block by block. It is cut into equal pieces of `chunk` blocks, one a
+// workgroup, so the work is even whatever the lengths are; a tile that a cut
+// crosses leaves partial sums.
+struct Line {
+  int32_t total, chunk;
+  // lane l: sequence base + l of the batch, and the line's units up to its end
+  int32_t base, c0, c1, len, incl;
+};
+__device__ inline void line_load(const KvAttn& a, int rows_per_tile, uint32_t lane, int base, int before, bool report,
+                                 Line& l) {
+  const int b = base + (int)lane;
+  l.base = base;
+  l.c0 = l.c1 = l.len = 0;
+  int units = 0;
+  if (b < a.batch) {
+    l.c0 = a.cu[b];
+    l.c1 = a.cu[b + 1];
+    l.len = a.lens[b];
+    Seq s;
+    if (seq_from(a, rows_per_tile, l.c0, l.c1, l.len, s)) units = s.blocks * s.tiles;
+    else if (report) kv_flag(a.cache, VBQ_KV4_FLAG_LENGTH);
+  }
+  l.incl = before + wave_scan(units);
+}
+__device__ inline void line_of(const KvAttn& a, int rows_per_tile, uint32_t lane, bool report, Line& l) {
+  l.total = 0;
+  for (int base = 0; base < a.batch; base += 64) {
+    line_load(a, rows_per_tile, lane, base, l.total, report, l);
+    l.total = __builtin_amdgcn_readlane(l.incl, 63);
+  }
+  const uint32_t c = ((uint32_t)l.total + (uint32_t)a.pieces - 1u) / (uint32_t)a.pieces;
+  l.chunk = max((int)c, a.min_chunk);
+}
+// The sequence that unit `pos` (less than the total) belongs to.
+__device__ inline int line_find(const KvAttn& a, int rows_per_tile, uint32_t lane, int pos, Line& l) {
+  if (a.batch > 64) {
+    int before = 0;
+    for (int base = 0;; base += 64) {
+      line_load(a, rows_per_tile, lane, base, before, false, l);
+      before = __builtin_amdgcn_readlane(l.incl, 63);
+      if (before > pos || base + 64 >= a.batch) break;
+    }
+  }
+  const uint64_t past = __ballot(l.incl > pos);
+  return l.base + (past ? __builtin_ctzll(past) : 63);
+}
+__device__ inline int line_before(const Line& l, int lane_of_seq, int first) {   // units before a sequence
+  return lane_of_seq ? __builtin_amdgcn_readlane(l.incl, lane_of_seq - 1) : first;
+}
+
+// Where a piece's partial sums of a tile lie: the tile that a piece starts in
+// the middle of is its slot 0, one that it starts and does not end its slot 1.
 template <int G, int NT>
-__global__ __launch_bounds__(256, (G <= 2 && NT == 1) ? 4 : (G * NT <= 4) ? 2 : 1) void k_kv4_attn(KvAttn a) {
+struct Slot {
+  float *acc, *ml;
+  __device__ Slot(const KvAttn& a, int piece, bool starts) {
+    const int64_t n = 2 * piece + (starts ? 1 : 0);
+    acc = a.acc + n * (16 * NT) * (64 * G);
+    ml = a.ml + n * (16 * NT) * 2;
+  }
+};
+
+// STAGES blocks a wavefront in LDS, STAGES - 1 of them on their way.
+template <int G, int NT, int STAGES>
+__global__ __launch_bounds__(64 * kWaves, G * NT > 4 ? 1 : 2) void k_kv4_attn(KvAttn a) {
   constexpr int D = 64 * G, ROWS = 16 * NT, PITCH = D + 4, BYTES = kKvGroupBytes * G;
-  // two blocks a wavefront; afterwards the wavefronts' sums, the pieces' factors and partial sums
-  constexpr int SUMS = kWaves * 16 * PITCH * 4, JOIN = 16 * kMaxSplits * 4 + 256 * 16;
-  constexpr int AFTER = SUMS > JOIN ? SUMS : JOIN;
-  __shared__ __attribute__((aligned(16))) uint8_t ring[kWaves * 2 * BYTES > AFTER ? kWaves * 2 * BYTES : AFTER];
+  constexpr int RING = kWaves * STAGES * BYTES, SUMS = kWaves * 16 * PITCH * 4;
+  __shared__ __attribute__((aligned(16))) uint8_t ring[RING > SUMS ? RING : SUMS];
   __shared__ float wml[kWaves][ROWS][2];
-  __shared__ uint32_t last;
-  float* const buf = reinterpret_cast<float*>(ring);
-  f32x4* const share = reinterpret_cast<f32x4*>(ring + 16 * kMaxSplits * 4);
+  float* const buf = reinterpret_cast<float*>(ring);   // the wavefronts' sums, after a tile
   const uint32_t tid = threadIdx.x, lane = tid & 63u, col = lane & 15u, quarter = lane >> 4;
   const int wave = __builtin_amdgcn_readfirstlane(tid >> 6);
+  uint8_t* const own_ring = ring + wave * STAGES * BYTES;
+  const uint32_t ring_lds = lds_addr(own_ring);
+  const Decode dc;
 
-  const uint32_t split = blockIdx.x % (uint32_t)a.splits;
-  const uint32_t tile = blockIdx.x / (uint32_t)a.splits;
-  const int rt = (int)(tile % (uint32_t)a.row_tiles);
-  const uint32_t bh = tile / (uint32_t)a.row_tiles;
-  const int head = (int)(bh % (uint32_t)a.cache.heads), b = (int)(bh / (uint32_t)a.cache.heads);
-
-  const int c0 = a.cu[b], c1 = a.cu[b + 1], len = a.lens[b];
-  const int64_t nq = (int64_t)c1 - c0;
-  if (c0 < 0 || nq < 0 || c1 > a.total_q || nq > a.max_q || len < 0 || len > a.max_kv ||
-      (int64_t)len > ((int64_t)a.width << (a.cache.block_shift + 5))) {
-    if (tid == 0) kv_flag(a.cache, VBQ_KV4_FLAG_LENGTH);
-    return;
+  // This workgroup's piece of the line, or its tile.
+  int pos = 0, end = 1, b;
+  Line line;
+  if (a.pieces) {
+    line_of(a, ROWS, lane, blockIdx.x == 0 && wave == 0, line);
+    pos = (int)min((int64_t)blockIdx.x * line.chunk, (int64_t)line.total);
+    end = (int)min((int64_t)pos + line.chunk, (int64_t)line.total);
+    if (pos >= end) return;
+    b = line_find(a, ROWS, lane, pos, line);
+  } else {
+    b = (int)(blockIdx.x / (uint32_t)(a.cache.heads * a.row_tiles));
   }
-  const int rows = (int)nq * a.ratio, r0 = rt * ROWS;
-  if (r0 >= rows) return;
-  const int r1 = min(rows, r0 + ROWS);
-  const int first = len - (int)nq;   // position of query 0
+  for (bool fresh = true; pos < end; fresh = false) {
+  Seq sq;
+  int tile, i0, i1;
+  if (a.pieces) {
+    const int at = b - line.base;   // below 64: every sequence but the last ends inside the lanes' ones
+    const int past = __builtin_amdgcn_readlane(line.incl, at);
+    if (past <= pos) {   // on to the next sequence
+      if (++b >= a.batch) return;
+      if (at == 63) line_load(a, ROWS, lane, b, past, false, line);
+      continue;
+    }
+    seq_from(a, ROWS, __builtin_amdgcn_readlane(line.c0, at), __builtin_amdgcn_readlane(line.c1, at),
+             __builtin_amdgcn_readlane(line.len, at), sq);
+    const uint32_t rel = (uint32_t)(pos - (past - sq.blocks * sq.tiles));
+    tile = (int)(rel / (uint32_t)sq.blocks);
+    i0 = (int)rel - tile * sq.blocks;
+    i1 = min(sq.blocks, i0 + (end - pos));
+    pos += i1 - i0;
+  } else {
+    if (!seq_from(a, ROWS, a.cu[b], a.cu[b + 1], a.lens[b], sq)) {
+      if (tid == 0) kv_flag(a.cache, VBQ_KV4_FLAG_LENGTH);
+      return;
+    }
+    tile = (int)(blockIdx.x % (uint32_t)(a.cache.heads * a.row_tiles));
+    if (tile >= sq.tiles) return;
+    i0 = 0;
+    i1 = sq.blocks;
+    pos = end;
+  }
+  const Reach re = sq.re;
+  const int c0 = sq.c0, len = sq.len, first = sq.first, rows = sq.nq * a.ratio;
+  const int rts = (rows + ROWS - 1) / ROWS;
+  const int head = tile / rts, r0 = (tile - head * rts) * ROWS, r1 = min(rows, r0 + ROWS);
   const int p_min = a.causal ? first + r0 / a.ratio : len - 1;
   const int p_max = a.causal ? first + (r1 - 1) / a.ratio : len - 1;
-  const Reach re = reach(len, p_min, p_max, a.window, a.sinks);
-  const int blocks = re.ns + re.nw;
-  const int splits = min(a.splits, max(1, (blocks + a.chunk - 1) / a.chunk));   // that have work
-  if ((int)split >= splits) return;
-  const int i0 = (int)split * a.chunk, i1 = (int)split == splits - 1 ? blocks : i0 + a.chunk;
+  if (!fresh) __syncthreads();   // the ring held the last tile's sums
 
-  // This wavefront's blocks, and the first one's copy.
+  // Queries, on their way while the first pages are looked up.
+  u32x4 qraw[NT][G][2];
+#pragma unroll
+  for (int nt = 0; nt < NT; ++nt) {
+    const int r = r0 + 16 * nt + (int)col;
+    const int qi = r / a.ratio, hh = r - qi * a.ratio;
+#pragma unroll
+    for (int g = 0; g < G; ++g)
+#pragma unroll
+      for (int st = 0; st < 2; ++st) {
+        qraw[nt][g][st] = u32x4{0, 0, 0, 0};
+        if (r < rows)
+          qraw[nt][g][st] = *reinterpret_cast<const u32x4*>(a.q + (int64_t)(c0 + qi) * a.q_ts +
+                                                            (int64_t)(head * a.ratio + hh) * a.q_hs + 64 * g +
+                                                            32 * st + 8 * quarter);
+      }
+  }
+
+  // The wavefront's blocks: copies run STAGES - 1 ahead.
   const uint32_t in_page = (1u << a.cache.block_shift) - 1u;
-  uint8_t* const mine = ring + wave * 2 * BYTES;
-  const uint32_t mine_lds = lds_addr(mine);
   int pages = -1;   // lane i: the page of the wavefront's block i (of 64 at a time)
+  uint64_t gone = 0, gone_before = 0;   // those that are not in the cache, and of the 64 before
   auto block_of = [&](int idx) { return idx < re.ns ? idx : idx - re.ns + re.w0; };
-  // starts the copy of block `it` (number idx of the tile's) and returns whether there is one
-  auto start_copy = [&](int it, int idx) {
+  auto start_copy = [&](int it) {
+    const int idx = i0 + wave + kWaves * it;
     if ((it & 63) == 0) {
       const int next = idx + kWaves * (int)lane;
-      pages = -1;
+      pages = 0;
+      bool bad = false;
       if (next < i1) {
         pages = a.table[(int64_t)b * a.width + (block_of(next) >> a.cache.block_shift)];
-        if ((uint32_t)pages >= (uint32_t)a.cache.n_pages) {
-          pages = -1;
-          kv_flag(a.cache, VBQ_KV4_FLAG_PAGE);
-        }
+        bad = (uint32_t)pages >= (uint32_t)a.cache.n_pages;
       }
+      if (bad) {
+        pages = 0;   // copied, and left out of the sums
+        kv_flag(a.cache, VBQ_KV4_FLAG_PAGE);
+      }
+      gone_before = gone;
+      gone = __ballot(bad);
     }
     const int page = __builtin_amdgcn_readlane(pages, it & 63);
-    if (page < 0) return false;
-    copy_block<G>(mine_lds + (it & 1) * BYTES,
+    copy_block<G>(ring_lds + (uint32_t)(it % STAGES) * BYTES,
                   kv_block(a.cache, G, (uint32_t)page, head, (uint32_t)block_of(idx) & in_page), lane);
-    return true;
   };
-  bool have = i0 + wave < i1 && start_copy(0, i0 + wave);
+  const int count = i0 + wave < i1 ? (i1 - i0 - wave + kWaves - 1) / kWaves : 0;
+#pragma unroll
+  for (int it = 0; it < STAGES - 1; ++it)
+    if (it < count) start_copy(it);
 
   // Queries: B operands per group and 32-channel step, their sums per group,
   // and what each lane's column sees.
@@ -233,18 +382,14 @@ __global__ __launch_bounds__(256, (G <= 2 && NT == 1) ? 4 : (G * NT <= 4) ? 2 : 
   for (int nt = 0; nt < NT; ++nt) {
     const int r = r0 + 16 * nt + (int)col;
     const bool in = r < rows;
-    const int qi = r / a.ratio, hh = r - qi * a.ratio;
+    const int qi = r / a.ratio;
     float x[G][2][8];
     float top = 0.f;
 #pragma unroll
     for (int g = 0; g < G; ++g)
 #pragma unroll
       for (int st = 0; st < 2; ++st) {
-        u32x4 w = {0, 0, 0, 0};
-        if (in)
-          w = *reinterpret_cast<const u32x4*>(a.q + (int64_t)(c0 + qi) * a.q_ts +
-                                              (int64_t)(head * a.ratio + hh) * a.q_hs + 64 * g + 32 * st +
-                                              8 * quarter);
+        const u32x4 w = qraw[nt][g][st];
 #pragma unroll
         for (int i = 0; i < 8; ++i) {
           const uint32_t u = (w[i >> 1] >> (16 * (i & 1))) & 0xFFFFu;
@@ -278,7 +423,6 @@ __global__ __launch_bounds__(256, (G <= 2 && NT == 1) ? 4 : (G * NT <= 4) ? 2 : 
     lo[nt] = a.window ? p - a.window + 1 : INT32_MIN;
   }
 
-  const Decode dc;
   float m[NT], l[NT];
   f32x4 acc[NT][G][4];
 #pragma unroll
@@ -291,14 +435,19 @@ __global__ __launch_bounds__(256, (G <= 2 && NT == 1) ? 4 : (G * NT <= 4) ? 2 : 
       for (int w = 0; w < 4; ++w) acc[nt][g][w] = f32x4{0.f, 0.f, 0.f, 0.f};
   }
 
-  for (int it = 0, idx = i0 + wave; idx < i1; ++it, idx += kWaves) {
-    const bool here = have;
-    // This block's copy has landed, and the last block's reads of the other buffer are done.
-    asm volatile("s_waitcnt vmcnt(0) lgkmcnt(0)" ::: "memory");
-    have = idx + kWaves < i1 && start_copy(it + 1, idx + kWaves);
-    if (!here) continue;
-    const int blk = block_of(idx);
-    const uint8_t* const k = mine + (it & 1) * BYTES;
+  for (int it = 0; it < count; ++it) {
+    // This block's copy has landed (later ones may be on their way), and the
+    // reads of the buffer that the next copy takes are done.
+    if (it + STAGES - 1 <= count)
+      asm volatile("s_waitcnt vmcnt(%0) lgkmcnt(0)" ::"n"(kCopies<G> * (STAGES - 2)) : "memory");
+    else
+      asm volatile("s_waitcnt vmcnt(0) lgkmcnt(0)" ::: "memory");
+    const int ahead = it + STAGES - 1;
+    if (ahead < count) start_copy(ahead);
+    // (the pages of the 64 blocks after may have been looked up already)
+    if ((((it ^ min(ahead, count - 1)) >> 6 ? gone_before : gone) >> (it & 63)) & 1u) continue;
+    const int blk = block_of(i0 + wave + kWaves * it);
+    const uint8_t* const k = own_ring + (it % STAGES) * BYTES;
 
     // scores of the lane's column: token 8 quarter + 4 half + i
     f32x4 sc[NT][2];
@@ -416,9 +565,8 @@ __global__ __launch_bounds__(256, (G <= 2 && NT == 1) ? 4 : (G * NT <= 4) ? 2 : 
     }
   }
   __syncthreads();
-  const bool whole = splits == 1;
-  float* const pacc = a.acc + ((size_t)tile * a.splits + split) * ROWS * D;
-  float* const pml = a.ml + ((size_t)tile * a.splits + split) * ROWS * 2;
+  const bool whole = i0 == 0 && i1 == sq.blocks;
+  const Slot<G, NT> slot(a, blockIdx.x, i0 == 0);
 #pragma unroll
   for (int nt = 0; nt < NT; ++nt) {
     if (r0 + 16 * nt >= rows) break;
@@ -459,83 +607,89 @@ __global__ __launch_bounds__(256, (G <= 2 && NT == 1) ? 4 : (G * NT <= 4) ? 2 : 
         store4(a, o * D + 4 * c, v * inv);
         if (a.lse && c == 0) a.lse[o] = (top + __builtin_amdgcn_logf(sum) - kProbShift) * kLn2;
       } else {
-        float* const d = pacc + (size_t)rr * D + 4 * c;
-        put2(d, v[0], v[1]);
-        put2(d + 2, v[2], v[3]);
-        if (c == 0) put2(pml + 2 * rr, top, sum);
+        *reinterpret_cast<f32x4*>(slot.acc + rr * D + 4 * c) = v;
+        if (c == 0) *reinterpret_cast<f32x2*>(slot.ml + 2 * rr) = f32x2{top, sum};
       }
     }
   }
-  if (whole) return;
+  }
+}
 
-  // Join the pieces. The sums above are device-scope stores, which write
-  // through the caches; each wavefront waits for its own before the barrier,
-  // so when the counter counts this piece its sums can be read by every
-  // workgroup's device-scope loads. The last piece adds all of them in order.
-  __builtin_amdgcn_s_waitcnt(VBQ_VMCNT_IMM(0));
-  __syncthreads();
-  if (tid == 0)
-    last = __hip_atomic_fetch_add(&a.counters[tile], 1u, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT) ==
-           (uint32_t)(splits - 1);
-  __syncthreads();
-  if (!last) return;
-  if (tid == 0) __hip_atomic_store(&a.counters[tile], 0u, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
-  const float* const tacc = a.acc + (size_t)tile * a.splits * ROWS * D;
-  const float* const tml = a.ml + (size_t)tile * a.splits * ROWS * 2;
+// Joins the partial sums of tiles that the line's cuts cross, piece by piece in
+// order, and answers tiles that see no block at all. One workgroup a tile.
+constexpr int kJoinThreads = 512;
+template <int G, int NT>
+__global__ __launch_bounds__(kJoinThreads) void k_kv4_join(KvAttn a) {
+  constexpr int D = 64 * G, ROWS = 16 * NT, ROW_LANES = kJoinThreads / 16;
+  __shared__ float factor[16][kMaxPieces];
+  __shared__ f32x4 share[kJoinThreads];
+  __shared__ float total[16][2];
+  const uint32_t tid = threadIdx.x, lane = tid & 63u;
+  const uint32_t per = (uint32_t)(a.cache.heads * a.row_tiles);
+  const int b = (int)(blockIdx.x / per), tile = (int)(blockIdx.x % per);
+  Seq sq;
+  if (!seq_from(a, ROWS, a.cu[b], a.cu[b + 1], a.lens[b], sq) || tile >= sq.tiles) return;
+  const int rows = sq.nq * a.ratio, rts = (rows + ROWS - 1) / ROWS;
+  const int head = tile / rts, r0 = (tile - head * rts) * ROWS;
+  int p0 = 0, pieces = 0;
+  if (sq.blocks > 0) {
+    Line line;
+    line_of(a, ROWS, lane, false, line);
+    int before = 0;
+    if (a.batch > 64)
+      for (int base = 0;; base += 64) {   // the lanes' sequences are to hold b
+        line_load(a, ROWS, lane, base, before, false, line);
+        if (b < base + 64) break;
+        before = __builtin_amdgcn_readlane(line.incl, 63);
+      }
+    const uint32_t u = (uint32_t)(line_before(line, b - line.base, before) + tile * sq.blocks);
+    p0 = (int)(u / (uint32_t)line.chunk);
+    pieces = (int)((u + (uint32_t)sq.blocks - 1u) / (uint32_t)line.chunk) - p0 + 1;
+    if (pieces == 1) return;   // whole: its workgroup has answered
+  }
 #pragma unroll 1
   for (int nt = 0; nt < NT; ++nt) {
     const int nrow = min(16, rows - r0 - 16 * nt);
     if (nrow <= 0) break;
     __syncthreads();
-    {   // sixteen lanes a row: the common maximum, the total, each piece's factor
-      const int row = (int)(tid >> 4), j = (int)(tid & 15u);
-      float pm[kMaxSplits / 16], pl[kMaxSplits / 16];
-      float top = kNoMax;
-#pragma unroll
-      for (int i = 0; i < kMaxSplits / 16; ++i) {
-        const int sp = 16 * i + j;
-        pm[i] = kNoMax;
-        pl[i] = 0.f;
-        if (row < nrow && sp < splits) {
-          const f32x2 v = get2(tml + ((size_t)sp * ROWS + 16 * nt + row) * 2);
-          pm[i] = v.x;
-          pl[i] = v.y;
+    {   // 32 lanes a row: the common maximum, each piece's factor, the sum
+      const int row = (int)tid / ROW_LANES, j = (int)tid % ROW_LANES;
+      float top = kNoMax, sum = 0.f;
+      if (row < nrow) {
+        for (int p = j; p < pieces; p += ROW_LANES) {
+          const float m = Slot<G, NT>(a, p0 + p, p == 0).ml[2 * (16 * nt + row)];
+          factor[row][p] = m;
+          top = fmaxf(top, m);
         }
-        top = fmaxf(top, pm[i]);
       }
 #pragma unroll
-      for (int d = 1; d < 16; d <<= 1) top = fmaxf(top, __shfl_xor(top, d, 16));
-      float sum = 0.f;
-#pragma unroll
-      for (int i = 0; i < kMaxSplits / 16; ++i) {
-        const int sp = 16 * i + j;
-        const float f = __builtin_amdgcn_exp2f(pm[i] - top);
-        sum += pl[i] * f;
-        if (sp < splits) buf[row * kMaxSplits + sp] = f;
+      for (int d = 1; d < ROW_LANES; d <<= 1) top = fmaxf(top, __shfl_xor(top, d, 64));
+      if (row < nrow) {
+        for (int p = j; p < pieces; p += ROW_LANES) {
+          const float f = __builtin_amdgcn_exp2f(factor[row][p] - top);
+          factor[row][p] = f;
+          sum += f * Slot<G, NT>(a, p0 + p, p == 0).ml[2 * (16 * nt + row) + 1];
+        }
       }
 #pragma unroll
-      for (int d = 1; d < 16; d <<= 1) sum += __shfl_xor(sum, d, 16);
+      for (int d = 1; d < ROW_LANES; d <<= 1) sum += __shfl_xor(sum, d, 64);
       if (j == 0) {
-        wml[0][row][0] = top;
-        wml[0][row][1] = sum;
+        total[row][0] = top;
+        total[row][1] = sum;
       }
     }
     __syncthreads();
     // Threads beyond the rows' outputs share the pieces.
-    const int ne = nrow * (D / 4), parts = ne <= 128 ? 256 / ne : 1;
-    for (int e0 = 0; e0 < ne; e0 += 256) {
+    const int ne = nrow * (D / 4), parts = ne <= kJoinThreads / 2 ? kJoinThreads / ne : 1;
+    for (int e0 = 0; e0 < ne; e0 += kJoinThreads) {
       const int e = parts > 1 ? (int)tid % ne : e0 + (int)tid, part = parts > 1 ? (int)tid / ne : 0;
-      f32x4 v = {0.f, 0.f, 0.f, 0.f};
       const int row = e / (D / 4), c = e % (D / 4);
+      f32x4 v = {0.f, 0.f, 0.f, 0.f};
       if (e < ne && part < parts) {
-        const float* p = tacc + (size_t)(16 * nt + row) * D + 4 * c;
-        const float* w = buf + row * kMaxSplits;
-#pragma unroll 8
-        for (int sp = part; sp < splits; sp += parts) {
-          const float* u = p + (size_t)sp * ROWS * D;
-          const f32x2 x = get2(u), y = get2(u + 2);
-          v += f32x4{x.x, x.y, y.x, y.y} * w[sp];
-        }
+#pragma unroll 4
+        for (int p = part; p < pieces; p += parts)
+          v += *reinterpret_cast<const f32x4*>(Slot<G, NT>(a, p0 + p, p == 0).acc + (16 * nt + row) * D + 4 * c) *
+               factor[row][p];
       }
       if (parts > 1) {
         share[tid] = v;
@@ -545,8 +699,8 @@ __global__ __launch_bounds__(256, (G <= 2 && NT == 1) ? 4 : (G * NT <= 4) ? 2 : 
       }
       if (e < ne && part == 0) {
         const int r = r0 + 16 * nt + row, qi = r / a.ratio, hh = r - qi * a.ratio;
-        const int64_t o = (int64_t)(c0 + qi) * a.n_heads + head * a.ratio + hh;
-        const float top = wml[0][row][0], sum = wml[0][row][1];
+        const int64_t o = (int64_t)(sq.c0 + qi) * a.n_heads + head * a.ratio + hh;
+        const float top = total[row][0], sum = total[row][1];
         const float inv = sum > 0.f ? 1.f / sum : sum == 0.f ? 0.f : sum;
         store4(a, o * D + 4 * c, v * inv);
         if (a.lse && c == 0) a.lse[o] = (top + __builtin_amdgcn_logf(sum) - kProbShift) * kLn2;
@@ -557,6 +711,9 @@ __global__ __launch_bounds__(256, (G <= 2 && NT == 1) ? 4 : (G * NT <= 4) ? 2 : 
 
 }  // namespace
 
+// Rows a tile takes: one column tile of the MFMA, or two. Pieces of the line:
+// two workgroups a CU. A tile is not cut (a workgroup each, no join) when there
+// are enough of them to fill the chip or the tiles are short.
 KvAttnPlan kv4_attn_plan(int batch, int heads, int ratio, int groups, int max_q, int max_kv, int window, int sinks) {
   KvAttnPlan p;
   const int64_t rows = (int64_t)max_q * ratio;
@@ -564,38 +721,32 @@ KvAttnPlan kv4_attn_plan(int batch, int heads, int ratio, int groups, int max_q,
   p.row_tiles = rows > 0 ? (int32_t)((rows + p.rows - 1) / p.rows) : 1;
   p.tiles = (int64_t)batch * heads * p.row_tiles;
   int64_t blocks = ((int64_t)max_kv + kKvBlock - 1) / kKvBlock;
-  if (window) {   // a row tile sees its sinks, its queries' windows and the blocks these end in
-    const int64_t reach = ((int64_t)sinks + kKvBlock - 1) / kKvBlock +
-                          ((int64_t)window + (p.rows + ratio - 1) / ratio) / kKvBlock + 2;
-    blocks = blocks < reach ? blocks : reach;
+  if (window) {
+    const int64_t most = ((int64_t)sinks + window + max_q) / kKvBlock + 3;
+    blocks = blocks < most ? blocks : most;
   }
-  // Pieces: enough workgroups for four on every CU, none under two blocks a wavefront.
-  int64_t splits = (1024 + p.tiles - 1) / p.tiles;
-  const int64_t most = (blocks + 2 * kWaves - 1) / (2 * kWaves);
-  splits = splits < most ? splits : most;
-  splits = splits < kMaxSplits ? splits : kMaxSplits;
-  if (p.tiles > VBQ_KV4_COUNTER_BYTES / 4 || splits < 1) splits = 1;
-  int64_t chunk = (blocks + splits - 1) / splits;
-  chunk = (chunk + kWaves - 1) / kWaves * kWaves;
-  p.chunk = (int32_t)(chunk < 1 ? kWaves : chunk);
-  p.splits = (int32_t)((blocks + p.chunk - 1) / p.chunk);
-  if (p.splits < 1) p.splits = 1;
+  p.pieces = p.tiles < 2048 && blocks > 4 * kWaves && p.tiles * blocks < INT32_MAX - 65536 ? kMaxPieces : 0;
   return p;
 }
 
 hipError_t launch_kv4_attention(const KvAttn& a, const KvAttnPlan& p, int batch, hipStream_t s) {
-  const int64_t wgs = p.tiles * p.splits;
-  if (wgs > INT32_MAX) return hipErrorNotSupported;
-  const dim3 grid((uint32_t)wgs);
-#define VBQ_CALL(G)                                          \
-  if (p.rows == 16) k_kv4_attn<G, 1><<<grid, 256, 0, s>>>(a); \
-  else k_kv4_attn<G, 2><<<grid, 256, 0, s>>>(a)
+  if (p.tiles > INT32_MAX) return hipErrorNotSupported;
+  const dim3 grid(p.pieces ? (uint32_t)p.pieces : (uint32_t)p.tiles);
+#define VBQ_CALL(G, NT, ST)                                                           \
+  do {                                                                                \
+    k_kv4_attn<G, NT, ST><<<grid, 64 * kWaves, 0, s>>>(a);                            \
+    if (p.pieces) k_kv4_join<G, NT><<<(uint32_t)p.tiles, kJoinThreads, 0, s>>>(a);    \
+  } while (0)
+#define VBQ_CALL2(G, ST)                      \
+  if (p.rows == 16) VBQ_CALL(G, 1, ST);       \
+  else VBQ_CALL(G, 2, ST)
   switch (a.cache.groups) {
-    case 1: VBQ_CALL(1); break;
-    case 2: VBQ_CALL(2); break;
-    case 3: VBQ_CALL(3); break;
-    default: VBQ_CALL(4); break;
+    case 1: VBQ_CALL2(1, 4); break;
+    case 2: VBQ_CALL2(2, 4); break;
+    case 3: VBQ_CALL2(3, 2); break;
+    default: VBQ_CALL2(4, 2); break;
   }
+#undef VBQ_CALL2
 #undef VBQ_CALL
   return hipGetLastError();
 }

@@ -20,7 +20,7 @@ def _range(vbq, **kw):
 
 
 def _attn(vbq, **kw):
-    d = dict(batch=2, table_width=2, total_q=2, max_q=1, max_kv=128, n_heads=8, dtype=0, causal=1, window=0, sinks=0,
+    d = dict(batch=2, table_width=2, total_q=2, max_q=1, max_kv=4096, n_heads=8, dtype=0, causal=1, window=0, sinks=0,
              scale=0.1, reserved=0, table=BASE, kv_lens=BASE, cu_q=BASE, q=BASE, q_token_stride=1024,
              q_head_stride=128, out=BASE, lse=None, workspace=BASE, workspace_bytes=1 << 40)
     d.update(kw)
@@ -104,4 +104,4 @@ def test_workspace_is_bounded_and_grows_with_no_size_beyond_it(batch, heads, max
     c = _cache(vbq)
     n = vbq.lib.kv4_attention_workspace(C.byref(c), C.byref(_attn(vbq, batch=batch, n_heads=heads, max_q=max_q,
                                                                    max_kv=max_kv, window=window, sinks=sinks)))
-    assert vbq.KV4_COUNTER_BYTES <= n < vbq.KV4_COUNTER_BYTES + (1 << 30)
+    assert 0 <= n < 1 << 30
