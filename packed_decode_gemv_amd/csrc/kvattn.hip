@@ -17,14 +17,20 @@
 // of two, undone in the score), so fp16 holds bf16 queries exactly down to
 // 2^-28 of the row's largest.
 //
-// Output. O^T = V^T P^T by the same MFMA: A is 16 channels by 32 tokens of
-// values s c + o in fp16 (codes made exact by an exponent that is subtracted
-// again, then one packed multiply-add), B the probabilities as they come out
-// of the score MFMA: its result holds tokens 4 q + i of a column (row of the
+// Output. O^T = V^T P^T by the same MFMA: A is the value codes, 16 channels by
+// 32 tokens, again as fp16 subnormals; B the probabilities as they come out of
+// the score MFMA: its result holds tokens 4 q + i of a column (row of the
 // problem) in lane quarter q, and the cache orders a block's tokens so that
-// those of both 16-token halves are the octet 8 q .. 8 q + 7, which is a value
-// word. Probabilities carry a factor 2^15 so that fp16 keeps them normal down
-// to 2^-29 of the largest.
+// those of both 16-token halves are the octet 8 q .. 8 q + 7, a value word. B
+// carries p s (the token's scale in its group) as the sum of two fp16 numbers,
+// so nothing is lost to fp16 but what lies 2^-37 below the largest; offsets
+// enter as fp32 sums of p o per row and group. A wavefront holds p s times
+// 2^S, S from the largest scale it has met.
+//
+// Few rows. With up to 8 (4) rows the MFMA's other columns hold copies of the
+// queries, so every lane has every score of its row: lane part 0 .. 1 (0 .. 3)
+// takes the scores of a half (quarter) of its octet's tokens, and scale,
+// softmax and split are done once per score, not two (four) times.
 #include "kv4.h"
 
 namespace vbq {
@@ -36,7 +42,6 @@ typedef float f32x2 __attribute__((ext_vector_type(2)));
 
 constexpr int kWaves = 4;
 constexpr float kNoMax = -1e30f;     // running maximum before any token
-constexpr float kProbShift = 15.f;   // probabilities are held times 2^15
 constexpr int kMaxPieces = 512;
 
 // Exchanges with the lanes 16 and 32 apart (the lane quarters of a column).
@@ -61,6 +66,30 @@ __device__ inline float rows_sum(float v) {
   x = p.x, y = p.y;
   return __builtin_bit_cast(float, x) + __builtin_bit_cast(float, y);
 }
+// Lane l of a row of 16 gets lane l + N's value (any value past the row's end);
+// rotated by N.
+template <int N>
+__device__ inline uint32_t row_down(uint32_t v) {
+  return (uint32_t)__builtin_amdgcn_update_dpp(0, (int)v, 0x100 + N, 0xF, 0xF, true);
+}
+template <int N>
+__device__ inline float row_turn(float v) {
+  return __builtin_bit_cast(float, __builtin_amdgcn_update_dpp(0, __builtin_bit_cast(int, v), 0x120 + N, 0xF, 0xF, true));
+}
+// Over the lanes that share a row of the problem: PARTS of a column's copies,
+// then the lane quarters.
+template <int PARTS>
+__device__ inline float lanes_max(float v) {
+  if constexpr (PARTS >= 2) v = fmaxf(v, row_turn<8>(v));
+  if constexpr (PARTS == 4) v = fmaxf(v, row_turn<4>(v));
+  return rows_max(v);
+}
+template <int PARTS>
+__device__ inline float lanes_sum(float v) {
+  if constexpr (PARTS >= 2) v += row_turn<8>(v);
+  if constexpr (PARTS == 4) v += row_turn<4>(v);
+  return rows_sum(v);
+}
 // Inclusive sum over the lanes of a wavefront.
 __device__ inline int wave_scan(int v) {
   v += __builtin_amdgcn_update_dpp(0, v, 0x111, 0xF, 0xF, true);   // row_shr:1
@@ -72,9 +101,9 @@ __device__ inline int wave_scan(int v) {
   return v;
 }
 
-// Eight codes of a key word as fp16 subnormals: pairs (n, n + 4), the odd
-// pairs times 16.
-__device__ inline half8_t key_codes(uint32_t w) {
+// Eight codes of a word as fp16 subnormals: pairs (n, n + 4), the odd pairs
+// times 16.
+__device__ inline half8_t codes_of(uint32_t w) {
   u32x4 r;
   r.x = w & 0x000F000Fu;
   r.y = w & 0x00F000F0u;
@@ -84,42 +113,27 @@ __device__ inline half8_t key_codes(uint32_t w) {
   return __builtin_bit_cast(half8_t, r);
 }
 
-// Constants of the value decode, opaque to the compiler: with the masks in
-// scalar and the exponents in vector registers (w & mask) | exponent is one
-// instruction; known constants become two with a literal each.
-struct Decode {
-  uint32_t m0, m4, ex;
-  __device__ Decode() : m0(0x000F000Fu), m4(0x00F000F0u), ex(0x64006400u) {
-    asm("" : "+s"(m0));
-    asm("" : "+s"(m4));
-    asm("" : "+v"(ex));
+__device__ inline half2_t pair_of(uint32_t w) { return __builtin_bit_cast(half2_t, w); }
+
+// N fp16 numbers from LDS.
+template <int N>
+struct Halves {
+  uint32_t w[N > 1 ? N / 2 : 1];
+  __device__ explicit Halves(const uint8_t* p) {
+    if constexpr (N == 1) w[0] = *reinterpret_cast<const uint16_t*>(p);
+    else if constexpr (N == 2) w[0] = *reinterpret_cast<const uint32_t*>(p);
+    else if constexpr (N == 4) {
+      const u32x2 v = *reinterpret_cast<const u32x2*>(p);
+      w[0] = v.x, w[1] = v.y;
+    } else {
+      const u32x4 v = *reinterpret_cast<const u32x4*>(p);
+      w[0] = v.x, w[1] = v.y, w[2] = v.z, w[3] = v.w;
+    }
+  }
+  __device__ float operator[](int i) const {
+    return (float)(i & 1 ? pair_of(w[i >> 1]).y : pair_of(w[i >> 1]).x);
   }
 };
-
-// Eight values s c + o of a value word, pairs (n, n + 4); s and o hold the
-// pairs' scales and offsets.
-__device__ inline half8_t values(const Decode& dc, uint32_t w, const u32x4& s, const u32x4& o) {
-  const half2_t one = {(_Float16)1024.f, (_Float16)1024.f}, sx = {(_Float16)0.0625f, (_Float16)0.0625f},
-                sb = {(_Float16)-64.f, (_Float16)-64.f};
-  const uint32_t h = w >> 8;
-  half2_t c[4];
-  c[0] = __builtin_bit_cast(half2_t, (w & dc.m0) | dc.ex) - one;
-  c[1] = __builtin_elementwise_fma(__builtin_bit_cast(half2_t, (w & dc.m4) | dc.ex), sx, sb);
-  c[2] = __builtin_bit_cast(half2_t, (h & dc.m0) | dc.ex) - one;
-  c[3] = __builtin_elementwise_fma(__builtin_bit_cast(half2_t, (h & dc.m4) | dc.ex), sx, sb);
-  u32x4 r;
-#pragma unroll
-  for (int i = 0; i < 4; ++i) {
-    const uint32_t si = s[i], oi = o[i];   // (bit casts take no vector elements)
-    r[i] = __builtin_bit_cast(
-        uint32_t, __builtin_elementwise_fma(c[i], __builtin_bit_cast(half2_t, si), __builtin_bit_cast(half2_t, oi)));
-  }
-  return __builtin_bit_cast(half8_t, r);
-}
-
-__device__ inline float half_at(const u32x4& w, int i) {
-  return (float)__builtin_bit_cast(_Float16, (uint16_t)(w[i >> 1] >> (16 * (i & 1))));
-}
 
 // A block's copy to LDS: 16 bytes a lane and instruction, no registers, so
 // later blocks are on their way while one is worked on.
@@ -198,6 +212,18 @@ __device__ inline bool seq_from(const KvAttn& a, int rows_per_tile, int c0, int 
   return true;
 }
 
+// Four channels of row r (sums v and of p, held times 2^base) and, once a row,
+// the log of the sum of exponentials.
+template <int D>
+__device__ inline void answer4(const KvAttn& a, const Seq& s, int head, int r, int c, const f32x4& v, float sum,
+                               float base) {
+  const int qi = r / a.ratio, hh = r - qi * a.ratio;
+  const int64_t o = (int64_t)(s.c0 + qi) * a.n_heads + head * a.ratio + hh;
+  const float inv = sum > 0.f ? 1.f / sum : sum == 0.f ? 0.f : sum;   // 0: nothing seen; NaN stays
+  store4(a, o * D + 4 * c, v * inv);
+  if (a.lse && c == 0) a.lse[o] = (__builtin_amdgcn_logf(sum) - base) * kLn2;
+}
+
 // The token axes of all tiles laid end to end: sequence by sequence, tile by
 // tile, block by block. It is cut into equal pieces of `chunk` blocks, one a
 // workgroup, so the work is even whatever the lengths are; a tile that a cut
@@ -251,29 +277,34 @@ __device__ inline int line_before(const Line& l, int lane_of_seq, int first) {  
 
 // Where a piece's partial sums of a tile lie: the tile that a piece starts in
 // the middle of is its slot 0, one that it starts and does not end its slot 1.
-template <int G, int NT>
+template <int G, int ROWS>
 struct Slot {
   float *acc, *ml;
   __device__ Slot(const KvAttn& a, int piece, bool starts) {
     const int64_t n = 2 * piece + (starts ? 1 : 0);
-    acc = a.acc + n * (16 * NT) * (64 * G);
-    ml = a.ml + n * (16 * NT) * 2;
+    acc = a.acc + n * ROWS * (64 * G);
+    ml = a.ml + n * ROWS * 2;
   }
 };
 
 // STAGES blocks a wavefront in LDS, STAGES - 1 of them on their way.
-template <int G, int NT, int STAGES>
-__global__ __launch_bounds__(64 * kWaves, G * NT > 4 ? 1 : 2) void k_kv4_attn(KvAttn a) {
-  constexpr int D = 64 * G, ROWS = 16 * NT, PITCH = D + 4, BYTES = kKvGroupBytes * G;
-  constexpr int RING = kWaves * STAGES * BYTES, SUMS = kWaves * 16 * PITCH * 4;
+typedef uint16_t ushort2_t __attribute__((ext_vector_type(2)));
+
+template <int G, int ROWS, int STAGES>
+__global__ __launch_bounds__(64 * kWaves, G * ROWS > 64 ? 1 : 2) void k_kv4_attn(KvAttn a) {
+  constexpr int D = 64 * G, PITCH = D + 4, BYTES = kKvGroupBytes * G;
+  constexpr int NT = ROWS > 16 ? 2 : 1, COLS = ROWS > 16 ? 16 : ROWS;   // column tiles, and columns used of each
+  constexpr int PARTS = 16 / COLS, PAIRS = 4 / PARTS;   // lanes that share a row's octet, token pairs of each
+  constexpr int ODD = PARTS == 4 ? 1 : 2;   // sums kept apart for pairs whose codes come times 16
+  constexpr int RING = kWaves * STAGES * BYTES, SUMS = kWaves * COLS * PITCH * 4;
   __shared__ __attribute__((aligned(16))) uint8_t ring[RING > SUMS ? RING : SUMS];
   __shared__ float wml[kWaves][ROWS][2];
   float* const buf = reinterpret_cast<float*>(ring);   // the wavefronts' sums, after a tile
   const uint32_t tid = threadIdx.x, lane = tid & 63u, col = lane & 15u, quarter = lane >> 4;
+  const uint32_t qcol = col % COLS, part = col / COLS;
   const int wave = __builtin_amdgcn_readfirstlane(tid >> 6);
   uint8_t* const own_ring = ring + wave * STAGES * BYTES;
   const uint32_t ring_lds = lds_addr(own_ring);
-  const Decode dc;
 
   // This workgroup's piece of the line, or its tile.
   int pos = 0, end = 1, b;
@@ -328,7 +359,7 @@ __global__ __launch_bounds__(64 * kWaves, G * NT > 4 ? 1 : 2) void k_kv4_attn(Kv
   u32x4 qraw[NT][G][2];
 #pragma unroll
   for (int nt = 0; nt < NT; ++nt) {
-    const int r = r0 + 16 * nt + (int)col;
+    const int r = r0 + 16 * nt + (int)qcol;
     const int qi = r / a.ratio, hh = r - qi * a.ratio;
 #pragma unroll
     for (int g = 0; g < G; ++g)
@@ -380,7 +411,7 @@ __global__ __launch_bounds__(64 * kWaves, G * NT > 4 ? 1 : 2) void k_kv4_attn(Kv
   int hi[NT], lo[NT];
 #pragma unroll
   for (int nt = 0; nt < NT; ++nt) {
-    const int r = r0 + 16 * nt + (int)col;
+    const int r = r0 + 16 * nt + (int)qcol;
     const bool in = r < rows;
     const int qi = r / a.ratio;
     float x[G][2][8];
@@ -423,17 +454,29 @@ __global__ __launch_bounds__(64 * kWaves, G * NT > 4 ? 1 : 2) void k_kv4_attn(Kv
     lo[nt] = a.window ? p - a.window + 1 : INT32_MIN;
   }
 
-  float m[NT], l[NT];
+  // Running maximum m, and sums held times 2^base, base = S - m: of p, of p o,
+  // and (times 2^-24) of p s code.
+  float m[NT], base[NT], l[NT][ODD], po[NT][G][ODD];
   f32x4 acc[NT][G][4];
+  float shift[NT];   // S of the lane's row
+  int limit[NT];     // largest scale that S is fit for (bits of an fp16)
 #pragma unroll
   for (int nt = 0; nt < NT; ++nt) {
+    shift[nt] = 0.f;
+    limit[nt] = -1;
     m[nt] = kNoMax;
-    l[nt] = 0.f;
+    base[nt] = -kNoMax;
 #pragma unroll
-    for (int g = 0; g < G; ++g)
+    for (int d = 0; d < ODD; ++d) l[nt][d] = 0.f;
+#pragma unroll
+    for (int g = 0; g < G; ++g) {
+#pragma unroll
+      for (int d = 0; d < ODD; ++d) po[nt][g][d] = 0.f;
 #pragma unroll
       for (int w = 0; w < 4; ++w) acc[nt][g][w] = f32x4{0.f, 0.f, 0.f, 0.f};
+    }
   }
+  const float lane_odd = PARTS == 4 && (part & 1u) ? -4.f : 0.f;
 
   for (int it = 0; it < count; ++it) {
     // This block's copy has landed (later ones may be on their way), and the
@@ -449,166 +492,252 @@ __global__ __launch_bounds__(64 * kWaves, G * NT > 4 ? 1 : 2) void k_kv4_attn(Kv
     const int blk = block_of(i0 + wave + kWaves * it);
     const uint8_t* const k = own_ring + (it % STAGES) * BYTES;
 
-    // scores of the lane's column: token 8 quarter + 4 half + i
-    f32x4 sc[NT][2];
-#pragma unroll
-    for (int nt = 0; nt < NT; ++nt) sc[nt][0] = sc[nt][1] = f32x4{0.f, 0.f, 0.f, 0.f};
+    // Scores of the lane's tokens 8 quarter + PAIRS part + j (+ 4).
+    const int t0 = blk * kKvBlock, mine = t0 + 8 * (int)quarter + PAIRS * (int)part;
+    float sc[NT][PAIRS][2];
 #pragma unroll
     for (int g = 0; g < G; ++g) {
       const u32x4 kc = lds16(k + 1024 * g + 16 * lane);
-      const u32x4 ks = lds16(k + kv_key_so(G) + 128 * g + 16 * quarter);
-      const u32x4 ko = lds16(k + kv_key_so(G) + 128 * g + 64 + 16 * quarter);
+      const uint8_t* const so = k + kv_key_so(G) + 128 * g + 16 * quarter + 2 * PAIRS * part;
 #pragma unroll
-      for (int hf = 0; hf < 2; ++hf) {
-        const half8_t a0 = key_codes(kc[2 * hf]), a1 = key_codes(kc[2 * hf + 1]);
+      for (int h = 0; h < 2; ++h) {
+        const half8_t a0 = codes_of(kc[2 * h]), a1 = codes_of(kc[2 * h + 1]);
+        const Halves<PAIRS> s(so + 8 * h), o(so + 64 + 8 * h);
 #pragma unroll
         for (int nt = 0; nt < NT; ++nt) {
           f32x4 d = f32x4{0.f, 0.f, 0.f, 0.f};
           d = __builtin_amdgcn_mfma_f32_16x16x32_f16(a0, qf[nt][g][0], d, 0, 0, 0);
           d = __builtin_amdgcn_mfma_f32_16x16x32_f16(a1, qf[nt][g][1], d, 0, 0, 0);
 #pragma unroll
-          for (int i = 0; i < 4; ++i)
-            sc[nt][hf][i] = __builtin_fmaf(half_at(ks, 4 * hf + i), d[i],
-                                           __builtin_fmaf(half_at(ko, 4 * hf + i), qsum[nt][g], sc[nt][hf][i]));
+          for (int j = 0; j < PAIRS; ++j) {
+            float x = d[j];
+            if constexpr (PARTS == 2) x = part ? d[2 + j] : d[j];
+            if constexpr (PARTS == 4) {
+              const float x0 = part & 1u ? d[1] : d[0], x1 = part & 1u ? d[3] : d[2];
+              x = part & 2u ? x1 : x0;
+            }
+            x = __builtin_fmaf(s[j], x, o[j] * qsum[nt][g]);
+            sc[nt][j][h] = g ? sc[nt][j][h] + x : x;
+          }
         }
       }
     }
-    const int t0 = blk * kKvBlock;
+    // Values' scales and offsets, pairs (j, j + 4).
+    uint32_t vs[G][PAIRS], vo[G][PAIRS];
+#pragma unroll
+    for (int g = 0; g < G; ++g) {
+      const uint8_t* const so = k + kv_value_so(G) + 128 * g + 16 * quarter + 4 * PAIRS * part;
+      const Halves<2 * PAIRS> s(so), o(so + 64);
+#pragma unroll
+      for (int j = 0; j < PAIRS; ++j) {
+        vs[g][j] = s.w[j];
+        vo[g][j] = o.w[j];
+      }
+    }
+    if (t0 + kKvBlock > len) {   // places past the sequence's end may hold anything
+#pragma unroll
+      for (int j = 0; j < PAIRS; ++j) {
+        const uint32_t keep = mine + j + 4 < len ? 0xFFFFFFFFu : mine + j < len ? 0x0000FFFFu : 0u;
+#pragma unroll
+        for (int g = 0; g < G; ++g) {
+          vs[g][j] &= keep;
+          vo[g][j] &= keep;
+        }
+      }
+    }
+    // The largest scale among the tokens that the lane's row sees.
+    int s_max[NT];
     const bool edge = t0 + kKvBlock - 1 > min(p_min, len - 1) ||
                       (a.window && t0 <= p_max - a.window && t0 + kKvBlock > a.sinks);
-    if (edge) {
+    if (edge) {   // not every row sees all of the block
 #pragma unroll
-      for (int hf = 0; hf < 2; ++hf)
+      for (int nt = 0; nt < NT; ++nt) {
+        ushort2_t top = {0, 0};
 #pragma unroll
-        for (int i = 0; i < 4; ++i) {
-          const int t = t0 + 8 * (int)quarter + 4 * hf + i;
+        for (int j = 0; j < PAIRS; ++j) {
+          uint32_t keep = 0;
 #pragma unroll
-          for (int nt = 0; nt < NT; ++nt) {
+          for (int h = 0; h < 2; ++h) {
+            const int t = mine + j + 4 * h;
             const bool see = t <= hi[nt] && (t >= lo[nt] || t < a.sinks);
-            sc[nt][hf][i] = see ? sc[nt][hf][i] : -__builtin_inff();
+            sc[nt][j][h] = see ? sc[nt][j][h] : -__builtin_inff();
+            keep |= see ? 0xFFFFu << (16 * h) : 0u;
+          }
+#pragma unroll
+          for (int g = 0; g < G; ++g) {
+            const uint32_t u = vs[g][j] & keep;
+            top = __builtin_elementwise_max(top, __builtin_bit_cast(ushort2_t, u));
           }
         }
+        s_max[nt] = max((int)top.x, (int)top.y);
+      }
+    } else {
+      ushort2_t top = {0, 0};
+#pragma unroll
+      for (int g = 0; g < G; ++g)
+#pragma unroll
+        for (int j = 0; j < PAIRS; ++j) {
+          const uint32_t u = vs[g][j];
+          top = __builtin_elementwise_max(top, __builtin_bit_cast(ushort2_t, u));
+        }
+#pragma unroll
+      for (int nt = 0; nt < NT; ++nt) s_max[nt] = max((int)top.x, (int)top.y);
     }
-    // running maximum and sum
-    half8_t pf[NT], pl[NT];   // probabilities, and what their rounding to fp16 leaves
+
+    // Running maximum; sums follow it and S.
     bool grow = false;
     float mt[NT];
 #pragma unroll
     for (int nt = 0; nt < NT; ++nt) {
-      float t = -__builtin_inff();
+      float t = sc[nt][0][0];
 #pragma unroll
-      for (int hf = 0; hf < 2; ++hf)
+      for (int j = 0; j < PAIRS; ++j)
 #pragma unroll
-        for (int i = 0; i < 4; ++i) t = fmaxf(t, sc[nt][hf][i]);
-      mt[nt] = fmaxf(m[nt], rows_max(t) * to_log2[nt]);
-      grow |= mt[nt] > m[nt];
+        for (int h = 0; h < 2; ++h) t = fmaxf(t, sc[nt][j][h]);
+      mt[nt] = fmaxf(m[nt], lanes_max<PARTS>(t) * to_log2[nt]);
+      grow |= mt[nt] > m[nt] || s_max[nt] > limit[nt];
     }
     if (__any(grow)) {
 #pragma unroll
       for (int nt = 0; nt < NT; ++nt) {
-        const float f = __builtin_amdgcn_exp2f(m[nt] - mt[nt]);
+        // S brings the row's largest scale s below 2^12, and stays fit up to 8 s.
+        const float top = lanes_max<PARTS>((float)__builtin_bit_cast(_Float16, (uint16_t)s_max[nt]));
+        if ((int)__builtin_bit_cast(uint16_t, (_Float16)top) > limit[nt]) {
+          const int ex = (int)(__builtin_bit_cast(uint32_t, top) >> 23) - 126;   // top < 2^ex
+          shift[nt] = top > 0.f ? (float)(12 - ex) : 0.f;
+          const _Float16 most = (_Float16)fminf(ldexpf(1.f, ex + 3), 65504.f);
+          limit[nt] = top > 0.f ? (int)__builtin_bit_cast(uint16_t, most) : 0;
+        }
         m[nt] = mt[nt];
-        l[nt] *= f;
+        const float now = shift[nt] - mt[nt], f = __builtin_amdgcn_exp2f(now - base[nt]);
+        base[nt] = now;
 #pragma unroll
-        for (int g = 0; g < G; ++g)
+        for (int d = 0; d < ODD; ++d) l[nt][d] *= f;
+#pragma unroll
+        for (int g = 0; g < G; ++g) {
+#pragma unroll
+          for (int d = 0; d < ODD; ++d) po[nt][g][d] *= f;
 #pragma unroll
           for (int w = 0; w < 4; ++w) acc[nt][g][w] *= f;
-      }
-    }
-#pragma unroll
-    for (int nt = 0; nt < NT; ++nt) {
-      const float base = kProbShift - m[nt];
-#pragma unroll
-      for (int i = 0; i < 4; ++i) {
-        const float p0 = __builtin_amdgcn_exp2f(__builtin_fmaf(sc[nt][0][i], to_log2[nt], base));
-        const float p1 = __builtin_amdgcn_exp2f(__builtin_fmaf(sc[nt][1][i], to_log2[nt], base));
-        l[nt] += p0 + p1;
-        pf[nt][2 * i] = (_Float16)p0;
-        pf[nt][2 * i + 1] = (_Float16)p1;
-        pl[nt][2 * i] = (_Float16)(p0 - (float)pf[nt][2 * i]);
-        pl[nt][2 * i + 1] = (_Float16)(p1 - (float)pf[nt][2 * i + 1]);
-      }
-    }
-#pragma unroll
-    for (int g = 0; g < G; ++g) {
-      const u32x4 vc = lds16(k + kv_value_codes(G) + 1024 * g + 16 * lane);
-      u32x4 vs = lds16(k + kv_value_so(G) + 128 * g + 16 * quarter);
-      u32x4 vo = lds16(k + kv_value_so(G) + 128 * g + 64 + 16 * quarter);
-      if (t0 + kKvBlock > len) {   // places past the sequence's end may hold anything
-#pragma unroll
-        for (int i = 0; i < 4; ++i) {
-          const int t = t0 + 8 * (int)quarter + i;
-          const uint32_t keep = t + 4 < len ? 0xFFFFFFFFu : t < len ? 0x0000FFFFu : 0u;
-          vs[i] &= keep;
-          vo[i] &= keep;
         }
       }
+    }
+    // Probabilities times 2^S, those of odd pairs divided by 16.
+    float p[NT][PAIRS][2];
+#pragma unroll
+    for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+      for (int j = 0; j < PAIRS; ++j) {
+        const float bs = base[nt] + (PARTS == 4 ? lane_odd : j & 1 ? -4.f : 0.f);
+#pragma unroll
+        for (int h = 0; h < 2; ++h) p[nt][j][h] = __builtin_amdgcn_exp2f(__builtin_fmaf(sc[nt][j][h], to_log2[nt], bs));
+        l[nt][j % ODD] += p[nt][j][0] + p[nt][j][1];
+      }
+#pragma unroll
+    for (int g = 0; g < G; ++g) {
+      half8_t big[NT], small[NT];
+#pragma unroll
+      for (int nt = 0; nt < NT; ++nt) {
+        uint32_t x[PAIRS], y[PAIRS];
+#pragma unroll
+        for (int j = 0; j < PAIRS; ++j) {
+          const half2_t s = pair_of(vs[g][j]), o = pair_of(vo[g][j]);
+          const float u0 = p[nt][j][0] * (float)s.x, u1 = p[nt][j][1] * (float)s.y;
+          const half2_t b = {(_Float16)u0, (_Float16)u1};
+          const half2_t r = {(_Float16)(u0 - (float)b.x), (_Float16)(u1 - (float)b.y)};
+          x[j] = __builtin_bit_cast(uint32_t, b);
+          y[j] = __builtin_bit_cast(uint32_t, r);
+          po[nt][g][j % ODD] =
+              __builtin_fmaf(p[nt][j][0], (float)o.x, __builtin_fmaf(p[nt][j][1], (float)o.y, po[nt][g][j % ODD]));
+        }
+        // The octet's four pairs, from the lanes that hold them, in column `qcol`.
+        u32x4 bx, by;
+        if constexpr (PARTS == 1) {
+          bx = u32x4{x[0], x[1], x[2], x[3]};
+          by = u32x4{y[0], y[1], y[2], y[3]};
+        } else if constexpr (PARTS == 2) {
+          bx = u32x4{x[0], x[1], row_down<8>(x[0]), row_down<8>(x[1])};
+          by = u32x4{y[0], y[1], row_down<8>(y[0]), row_down<8>(y[1])};
+        } else {
+          bx = u32x4{x[0], row_down<4>(x[0]), row_down<8>(x[0]), row_down<12>(x[0])};
+          by = u32x4{y[0], row_down<4>(y[0]), row_down<8>(y[0]), row_down<12>(y[0])};
+        }
+        big[nt] = __builtin_bit_cast(half8_t, bx);
+        small[nt] = __builtin_bit_cast(half8_t, by);
+      }
+      const u32x4 vc = lds16(k + kv_value_codes(G) + 1024 * g + 16 * lane);
 #pragma unroll
       for (int w = 0; w < 4; ++w) {
-        const half8_t v = values(dc, vc[w], vs, vo);
+        const half8_t v = codes_of(vc[w]);
 #pragma unroll
         for (int nt = 0; nt < NT; ++nt) {
-          acc[nt][g][w] = __builtin_amdgcn_mfma_f32_16x16x32_f16(v, pf[nt], acc[nt][g][w], 0, 0, 0);
-          acc[nt][g][w] = __builtin_amdgcn_mfma_f32_16x16x32_f16(v, pl[nt], acc[nt][g][w], 0, 0, 0);
+          acc[nt][g][w] = __builtin_amdgcn_mfma_f32_16x16x32_f16(v, big[nt], acc[nt][g][w], 0, 0, 0);
+          acc[nt][g][w] = __builtin_amdgcn_mfma_f32_16x16x32_f16(v, small[nt], acc[nt][g][w], 0, 0, 0);
         }
       }
     }
   }
 
-  // Join the four wavefronts: every one scales its sums to the common maximum.
+  // Join the wavefronts: every one scales its sums to the smallest base.
+  float sum_l[NT];
 #pragma unroll
   for (int nt = 0; nt < NT; ++nt) {
-    l[nt] = rows_sum(l[nt]);
-    if (quarter == 0) {
-      wml[wave][16 * nt + col][0] = m[nt];
-      wml[wave][16 * nt + col][1] = l[nt];
+    const float times = PARTS == 4 && (part & 1u) ? 16.f : 1.f;
+    auto whole_row = [&](const float(&v)[ODD]) {
+      return lanes_sum<PARTS>(ODD == 2 ? v[0] + 16.f * v[ODD - 1] : times * v[0]);
+    };
+    sum_l[nt] = whole_row(l[nt]);
+#pragma unroll
+    for (int g = 0; g < G; ++g) po[nt][g][0] = whole_row(po[nt][g]);
+    if (quarter == 0 && part == 0) {
+      wml[wave][16 * nt + qcol][0] = base[nt];
+      wml[wave][16 * nt + qcol][1] = sum_l[nt];
     }
   }
   __syncthreads();
   const bool whole = i0 == 0 && i1 == sq.blocks;
-  const Slot<G, NT> slot(a, blockIdx.x, i0 == 0);
+  const Slot<G, ROWS> slot(a, blockIdx.x, i0 == 0);
 #pragma unroll
   for (int nt = 0; nt < NT; ++nt) {
     if (r0 + 16 * nt >= rows) break;
     if (nt) __syncthreads();   // the buffer is taken again
-    {
-      const int rr = 16 * nt + (int)col;
-      float top = wml[0][rr][0];
+    if (part == 0) {
+      const int rr = 16 * nt + (int)qcol;
+      float low = wml[0][rr][0];
 #pragma unroll
-      for (int w = 1; w < kWaves; ++w) top = fmaxf(top, wml[w][rr][0]);
-      const float f = __builtin_amdgcn_exp2f(m[nt] - top);
-      float* const mine = buf + (wave * 16 + col) * PITCH + 16 * quarter;
+      for (int w = 1; w < kWaves; ++w) low = fminf(low, wml[w][rr][0]);
+      const float f = __builtin_amdgcn_exp2f(low - base[nt]), f24 = f * 0x1p24f;
+      float* const to = buf + (wave * COLS + qcol) * PITCH + 16 * quarter;
 #pragma unroll
-      for (int g = 0; g < G; ++g)
+      for (int g = 0; g < G; ++g) {
+        const float z = po[nt][g][0] * f;
 #pragma unroll
         for (int i = 0; i < 4; ++i) {
-          const f32x4 v = {acc[nt][g][0][i] * f, acc[nt][g][1][i] * f, acc[nt][g][2][i] * f, acc[nt][g][3][i] * f};
-          *reinterpret_cast<f32x4*>(mine + 64 * g + 4 * i) = v;
+          const f32x4 v = {__builtin_fmaf(acc[nt][g][0][i], f24, z), __builtin_fmaf(acc[nt][g][1][i], f24, z),
+                           __builtin_fmaf(acc[nt][g][2][i], f24, z), __builtin_fmaf(acc[nt][g][3][i], f24, z)};
+          *reinterpret_cast<f32x4*>(to + 64 * g + 4 * i) = v;
         }
+      }
     }
     __syncthreads();
-    for (int e = (int)tid; e < 16 * (D / 4); e += 256) {
+    for (int e = (int)tid; e < COLS * (D / 4); e += 64 * kWaves) {
       const int row = e / (D / 4), c = e % (D / 4), rr = 16 * nt + row;
       if (r0 + rr >= rows) break;
-      float top = wml[0][rr][0];
+      float low = wml[0][rr][0];
 #pragma unroll
-      for (int w = 1; w < kWaves; ++w) top = fmaxf(top, wml[w][rr][0]);
+      for (int w = 1; w < kWaves; ++w) low = fminf(low, wml[w][rr][0]);
       float sum = 0.f;
       f32x4 v = {0.f, 0.f, 0.f, 0.f};
 #pragma unroll
       for (int w = 0; w < kWaves; ++w) {
-        sum += wml[w][rr][1] * __builtin_amdgcn_exp2f(wml[w][rr][0] - top);
-        v += *reinterpret_cast<const f32x4*>(buf + (w * 16 + row) * PITCH + 4 * c);
+        sum += wml[w][rr][1] * __builtin_amdgcn_exp2f(low - wml[w][rr][0]);
+        v += *reinterpret_cast<const f32x4*>(buf + (w * COLS + row) * PITCH + 4 * c);
       }
       if (whole) {
-        const int r = r0 + rr, qi = r / a.ratio, hh = r - qi * a.ratio;
-        const int64_t o = (int64_t)(c0 + qi) * a.n_heads + head * a.ratio + hh;
-        const float inv = sum > 0.f ? 1.f / sum : sum == 0.f ? 0.f : sum;
-        store4(a, o * D + 4 * c, v * inv);
-        if (a.lse && c == 0) a.lse[o] = (top + __builtin_amdgcn_logf(sum) - kProbShift) * kLn2;
+        answer4<D>(a, sq, head, r0 + rr, c, v, sum, low);
       } else {
         *reinterpret_cast<f32x4*>(slot.acc + rr * D + 4 * c) = v;
-        if (c == 0) *reinterpret_cast<f32x2*>(slot.ml + 2 * rr) = f32x2{top, sum};
+        if (c == 0) *reinterpret_cast<f32x2*>(slot.ml + 2 * rr) = f32x2{low, sum};
       }
     }
   }
@@ -618,9 +747,9 @@ __global__ __launch_bounds__(64 * kWaves, G * NT > 4 ? 1 : 2) void k_kv4_attn(Kv
 // Joins the partial sums of tiles that the line's cuts cross, piece by piece in
 // order, and answers tiles that see no block at all. One workgroup a tile.
 constexpr int kJoinThreads = 512;
-template <int G, int NT>
+template <int G, int ROWS>
 __global__ __launch_bounds__(kJoinThreads) void k_kv4_join(KvAttn a) {
-  constexpr int D = 64 * G, ROWS = 16 * NT, ROW_LANES = kJoinThreads / 16;
+  constexpr int D = 64 * G, NT = (ROWS + 15) / 16, ROW_LANES = kJoinThreads / 16;
   __shared__ float factor[16][kMaxPieces];
   __shared__ f32x4 share[kJoinThreads];
   __shared__ float total[16][2];
@@ -652,29 +781,29 @@ __global__ __launch_bounds__(kJoinThreads) void k_kv4_join(KvAttn a) {
     const int nrow = min(16, rows - r0 - 16 * nt);
     if (nrow <= 0) break;
     __syncthreads();
-    {   // 32 lanes a row: the common maximum, each piece's factor, the sum
+    {   // 32 lanes a row: the smallest base, each piece's factor, the sum
       const int row = (int)tid / ROW_LANES, j = (int)tid % ROW_LANES;
-      float top = kNoMax, sum = 0.f;
+      float low = -kNoMax, sum = 0.f;
       if (row < nrow) {
         for (int p = j; p < pieces; p += ROW_LANES) {
-          const float m = Slot<G, NT>(a, p0 + p, p == 0).ml[2 * (16 * nt + row)];
-          factor[row][p] = m;
-          top = fmaxf(top, m);
+          const float base = Slot<G, ROWS>(a, p0 + p, p == 0).ml[2 * (16 * nt + row)];
+          factor[row][p] = base;
+          low = fminf(low, base);
         }
       }
 #pragma unroll
-      for (int d = 1; d < ROW_LANES; d <<= 1) top = fmaxf(top, __shfl_xor(top, d, 64));
+      for (int d = 1; d < ROW_LANES; d <<= 1) low = fminf(low, __shfl_xor(low, d, 64));
       if (row < nrow) {
         for (int p = j; p < pieces; p += ROW_LANES) {
-          const float f = __builtin_amdgcn_exp2f(factor[row][p] - top);
+          const float f = __builtin_amdgcn_exp2f(low - factor[row][p]);
           factor[row][p] = f;
-          sum += f * Slot<G, NT>(a, p0 + p, p == 0).ml[2 * (16 * nt + row) + 1];
+          sum += f * Slot<G, ROWS>(a, p0 + p, p == 0).ml[2 * (16 * nt + row) + 1];
         }
       }
 #pragma unroll
       for (int d = 1; d < ROW_LANES; d <<= 1) sum += __shfl_xor(sum, d, 64);
       if (j == 0) {
-        total[row][0] = top;
+        total[row][0] = low;
         total[row][1] = sum;
       }
     }
@@ -688,7 +817,7 @@ __global__ __launch_bounds__(kJoinThreads) void k_kv4_join(KvAttn a) {
       if (e < ne && part < parts) {
 #pragma unroll 4
         for (int p = part; p < pieces; p += parts)
-          v += *reinterpret_cast<const f32x4*>(Slot<G, NT>(a, p0 + p, p == 0).acc + (16 * nt + row) * D + 4 * c) *
+          v += *reinterpret_cast<const f32x4*>(Slot<G, ROWS>(a, p0 + p, p == 0).acc + (16 * nt + row) * D + 4 * c) *
                factor[row][p];
       }
       if (parts > 1) {
@@ -698,12 +827,7 @@ __global__ __launch_bounds__(kJoinThreads) void k_kv4_join(KvAttn a) {
           for (int i = 1; i < parts; ++i) v += share[e + i * ne];
       }
       if (e < ne && part == 0) {
-        const int r = r0 + 16 * nt + row, qi = r / a.ratio, hh = r - qi * a.ratio;
-        const int64_t o = (int64_t)(sq.c0 + qi) * a.n_heads + head * a.ratio + hh;
-        const float top = total[row][0], sum = total[row][1];
-        const float inv = sum > 0.f ? 1.f / sum : sum == 0.f ? 0.f : sum;
-        store4(a, o * D + 4 * c, v * inv);
-        if (a.lse && c == 0) a.lse[o] = (top + __builtin_amdgcn_logf(sum) - kProbShift) * kLn2;
+        answer4<D>(a, sq, head, r0 + 16 * nt + row, c, v, total[row][1], total[row][0]);
       }
     }
   }
@@ -711,13 +835,13 @@ __global__ __launch_bounds__(kJoinThreads) void k_kv4_join(KvAttn a) {
 
 }  // namespace
 
-// Rows a tile takes: one column tile of the MFMA, or two. Pieces of the line:
+// Rows a tile takes: columns of one MFMA tile, or two tiles. Pieces of the line:
 // two workgroups a CU. A tile is not cut (a workgroup each, no join) when there
 // are enough of them to fill the chip or the tiles are short.
 KvAttnPlan kv4_attn_plan(int batch, int heads, int ratio, int groups, int max_q, int max_kv, int window, int sinks) {
   KvAttnPlan p;
   const int64_t rows = (int64_t)max_q * ratio;
-  p.rows = rows <= 16 ? 16 : 32;
+  p.rows = rows <= 4 ? 4 : rows <= 8 ? 8 : rows <= 16 ? 16 : 32;
   p.row_tiles = rows > 0 ? (int32_t)((rows + p.rows - 1) / p.rows) : 1;
   p.tiles = (int64_t)batch * heads * p.row_tiles;
   int64_t blocks = ((int64_t)max_kv + kKvBlock - 1) / kKvBlock;
@@ -732,14 +856,16 @@ KvAttnPlan kv4_attn_plan(int batch, int heads, int ratio, int groups, int max_q,
 hipError_t launch_kv4_attention(const KvAttn& a, const KvAttnPlan& p, int batch, hipStream_t s) {
   if (p.tiles > INT32_MAX) return hipErrorNotSupported;
   const dim3 grid(p.pieces ? (uint32_t)p.pieces : (uint32_t)p.tiles);
-#define VBQ_CALL(G, NT, ST)                                                           \
-  do {                                                                                \
-    k_kv4_attn<G, NT, ST><<<grid, 64 * kWaves, 0, s>>>(a);                            \
-    if (p.pieces) k_kv4_join<G, NT><<<(uint32_t)p.tiles, kJoinThreads, 0, s>>>(a);    \
+#define VBQ_CALL(G, ROWS, ST)                                                           \
+  do {                                                                                  \
+    k_kv4_attn<G, ROWS, ST><<<grid, 64 * kWaves, 0, s>>>(a);                            \
+    if (p.pieces) k_kv4_join<G, ROWS><<<(uint32_t)p.tiles, kJoinThreads, 0, s>>>(a);    \
   } while (0)
-#define VBQ_CALL2(G, ST)                      \
-  if (p.rows == 16) VBQ_CALL(G, 1, ST);       \
-  else VBQ_CALL(G, 2, ST)
+#define VBQ_CALL2(G, ST)                                                                \
+  if (p.rows == 4) VBQ_CALL(G, 4, ST);                                                  \
+  else if (p.rows == 8) VBQ_CALL(G, 8, ST);                                             \
+  else if (p.rows == 16) VBQ_CALL(G, 16, ST);                                           \
+  else VBQ_CALL(G, 32, ST)
   switch (a.cache.groups) {
     case 1: VBQ_CALL2(1, 4); break;
     case 2: VBQ_CALL2(2, 4); break;
