@@ -833,6 +833,347 @@ __global__ __launch_bounds__(kJoinThreads) void k_kv4_join(KvAttn a) {
   }
 }
 
+// ---- many rows ---------------------------------------------------------------------
+// WAVES wavefronts take 32 rows each of one head and walk the blocks together.
+// A block is copied raw to LDS (two ahead), spread there into operands (one
+// ahead, a part by each wavefront), and multiplied by every wavefront with
+// 32x32x16 MFMAs: S^T = K Q^T, O^T = V^T P^T. Key operands are the exact codes
+// (fp16 subnormals), scores take scale in fp32 as above and offsets by one more
+// MFMA: A holds a token's offsets o_g, B the rows' sums of q over group g.
+// Rounding keys to fp16 instead would save the scaling, but a score's error is
+// multiplied into its probability: it doubled the output's error in fp16.
+// Values are s c + o rounded to fp16, as are probabilities.
+// In LDS keys and values lie as the operands are read, 16 bytes a lane:
+//   keys:   chunk (channel / 8, row R), the 8 channels as pairs (n, n + 4);
+//           token 8 (2 A + h) + 4 u + b is row 8 (2 A + u) + 4 h + b, so the
+//           score MFMA leaves octet 2 A + h whole in lane half h;
+//   values: chunk (octet / 2, channel tile T, octet % 2, row), the octet's
+//           tokens as pairs; channel 64 g + 4 m + w is row 16 (w % 2) + m of
+//           tile 2 g + w / 2, so a result holds 16 neighbouring channels a lane.
+typedef float f32x16 __attribute__((ext_vector_type(16)));
+
+constexpr float kTileShift = 7.f;   // probabilities are held times 2^7 ...
+constexpr float kTileSlack = 8.f;   // ... and the maximum may be passed by 2^8 before sums are scaled
+
+// Constants of the decode, opaque to the compiler: with the masks in scalar and
+// the exponent in a vector register (w & mask) | exponent is one instruction;
+// known constants become two with a literal each.
+struct Decode {
+  uint32_t m0, m4, ex;
+  __device__ Decode() : m0(0x000F000Fu), m4(0x00F000F0u), ex(0x64006400u) {
+    asm("" : "+s"(m0));
+    asm("" : "+s"(m4));
+    asm("" : "+v"(ex));
+  }
+};
+// Eight values s c + o of a word as pairs (n, n + 4), one rounding each: the
+// codes are made exact by an exponent that is subtracted again.
+__device__ inline u32x4 values_of(const Decode& dc, uint32_t w, const half2_t (&s)[4], const half2_t (&o)[4]) {
+  const half2_t one = {(_Float16)1024.f, (_Float16)1024.f}, sx = {(_Float16)0.0625f, (_Float16)0.0625f},
+                sb = {(_Float16)-64.f, (_Float16)-64.f};
+  const uint32_t h = w >> 8;
+  const half2_t c[4] = {pair_of((w & dc.m0) | dc.ex) - one,
+                        __builtin_elementwise_fma(pair_of((w & dc.m4) | dc.ex), sx, sb),
+                        pair_of((h & dc.m0) | dc.ex) - one,
+                        __builtin_elementwise_fma(pair_of((h & dc.m4) | dc.ex), sx, sb)};
+  u32x4 r;
+#pragma unroll
+  for (int i = 0; i < 4; ++i) r[i] = __builtin_bit_cast(uint32_t, __builtin_elementwise_fma(c[i], s[i], o[i]));
+  return r;
+}
+
+__device__ inline float half_max(float v) {   // with the lane 32 apart
+  const uint32_t u = __builtin_bit_cast(uint32_t, v);
+  const pair_t p = __builtin_amdgcn_permlane32_swap(u, u, false, false);
+  const uint32_t x = p.x, y = p.y;
+  return fmaxf(__builtin_bit_cast(float, x), __builtin_bit_cast(float, y));
+}
+__device__ inline float half_sum(float v) {
+  const uint32_t u = __builtin_bit_cast(uint32_t, v);
+  const pair_t p = __builtin_amdgcn_permlane32_swap(u, u, false, false);
+  const uint32_t x = p.x, y = p.y;
+  return __builtin_bit_cast(float, x) + __builtin_bit_cast(float, y);
+}
+
+template <int G, int WAVES>
+__global__ __launch_bounds__(64 * WAVES, 2) void k_kv4_attn_tile(KvAttn a) {
+  constexpr int D = 64 * G, BYTES = kKvGroupBytes * G, RAW = 4, TILES = D / 32;
+  constexpr int SHARE = BYTES / WAVES;   // a wavefront's part of a block's copy
+  constexpr int COPIES = (SHARE + 1023) / 1024;
+  constexpr int KEYS = 32 * D * 2, HELD = 2 * KEYS;
+  static_assert(SHARE % 16 == 0, "copies are 16 bytes a lane");
+  __shared__ __attribute__((aligned(16))) uint8_t raw[RAW * BYTES];
+  __shared__ __attribute__((aligned(16))) uint8_t held[2 * HELD];
+  const uint32_t tid = threadIdx.x, lane = tid & 63u, col = lane & 31u, half = lane >> 5;
+  const int wave = __builtin_amdgcn_readfirstlane(tid >> 6);
+  const uint32_t raw_lds = lds_addr(raw);
+  const Decode dc;
+
+  // The tiles of a (sequence, head) lie a multiple of the heads apart (one L2
+  // where that is a multiple of 8); the last rows, which see most, go first.
+  const uint32_t bh_n = (uint32_t)(a.batch * a.cache.heads);
+  const uint32_t bh = blockIdx.x % bh_n;
+  const int b = (int)(bh / (uint32_t)a.cache.heads), head = (int)(bh % (uint32_t)a.cache.heads);
+  Seq sq;
+  if (!seq_from(a, 32 * WAVES, a.cu[b], a.cu[b + 1], a.lens[b], sq)) {
+    if (tid == 0) kv_flag(a.cache, VBQ_KV4_FLAG_LENGTH);
+    return;
+  }
+  const int rows = sq.nq * a.ratio, rts = (rows + 32 * WAVES - 1) / (32 * WAVES);
+  const int rt = rts - 1 - (int)(blockIdx.x / bh_n);
+  if (rt < 0) return;
+  const int len = sq.len, first = sq.first;
+  const int r0 = rt * 32 * WAVES, r1 = min(rows, r0 + 32 * WAVES);
+  const Reach re = reach(len, a.causal ? first + r0 / a.ratio : len - 1,
+                         a.causal ? first + (r1 - 1) / a.ratio : len - 1, a.window, a.sinks);
+  const int blocks = re.ns + re.nw;
+  auto block_of = [&](int i) { return i < re.ns ? i : i - re.ns + re.w0; };
+
+  // Copies: lane i keeps the page of block i of 64.
+  const uint32_t in_page = (1u << a.cache.block_shift) - 1u;
+  int pages = -1;
+  uint64_t gone = 0, gone_before = 0;   // blocks of the 64 (and of those before) whose page is not in the cache
+  auto start_copy = [&](int i) {
+    if ((i & 63) == 0) {
+      const int next = i + (int)lane;
+      pages = 0;
+      bool bad = false;
+      if (next < blocks) {
+        pages = a.table[(int64_t)b * a.width + (block_of(next) >> a.cache.block_shift)];
+        bad = (uint32_t)pages >= (uint32_t)a.cache.n_pages;
+      }
+      if (bad) {
+        pages = 0;   // copied, and hidden
+        if (wave == 0) kv_flag(a.cache, VBQ_KV4_FLAG_PAGE);
+      }
+      gone_before = gone;
+      gone = __ballot(bad);
+    }
+    const int page = __builtin_amdgcn_readlane(pages, i & 63);
+    const uint8_t* const p =
+        kv_block(a.cache, G, (uint32_t)page, head, (uint32_t)block_of(i) & in_page) + wave * SHARE;
+    const u32x4 rsrc = make_rsrc(p, SHARE);
+    const uint32_t to = raw_lds + (uint32_t)(i % RAW) * BYTES + (uint32_t)wave * SHARE;
+#pragma unroll
+    for (int c = 0; c < SHARE / 1024; ++c) dma16(rsrc, to + 1024 * c, 1024 * c + 16 * lane);
+    if (lane < (SHARE % 1024) / 16) dma16(rsrc, to + SHARE / 1024 * 1024, SHARE / 1024 * 1024 + 16 * lane);
+  };
+  auto is_gone = [&](int i, int newest) {   // newest: the last block whose copy was started
+    return (((i ^ newest) >> 6 ? gone_before : gone) >> (i & 63)) & 1u;
+  };
+
+  // Queries: B operands, channels of a chunk as pairs; what the lane's row sees.
+  half8_t qf[D / 16], qsum;
+  float to_log2;
+  const int r = r0 + 32 * wave + (int)col;
+  const int qi = r / a.ratio, hh = r - qi * a.ratio;
+  {
+    u32x4 x[D / 16];
+#pragma unroll
+    for (int c = 0; c < D / 16; ++c) {
+      x[c] = u32x4{0, 0, 0, 0};
+      if (r < rows)
+        x[c] = *reinterpret_cast<const u32x4*>(a.q + (int64_t)(sq.c0 + qi) * a.q_ts +
+                                               (int64_t)(head * a.ratio + hh) * a.q_hs + 16 * c + 8 * half);
+    }
+    for (int i = 0; i < 2; ++i)
+      if (i < blocks) start_copy(i);
+    auto at = [&](int c, int i) {
+      const uint32_t u = (x[c][i >> 1] >> (16 * (i & 1))) & 0xFFFFu;
+      return a.bf16 ? __builtin_bit_cast(float, u << 16) : (float)__builtin_bit_cast(_Float16, (uint16_t)u);
+    };
+    float top = 0.f;
+#pragma unroll
+    for (int c = 0; c < D / 16; ++c)
+#pragma unroll
+      for (int i = 0; i < 8; ++i) top = fmaxf(top, fabsf(at(c, i)));
+    top = half_max(top);
+    int ex = (int)(__builtin_bit_cast(uint32_t, top) >> 23) - 127;
+    ex = top > 0.f ? max(ex, -100) : 13;
+    const float up = ldexpf(1.f, 13 - ex);
+    to_log2 = a.scale_log2 * ldexpf(1.f, ex - 13 + 24);
+#pragma unroll
+    for (int j = 0; j < 8; ++j) qsum[j] = (_Float16)0.f;
+#pragma unroll
+    for (int g = 0; g < G; ++g) {
+      float sum = 0.f;
+#pragma unroll
+      for (int c = 4 * g; c < 4 * g + 4; ++c)
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+          const _Float16 v0 = (_Float16)(at(c, i) * up), v1 = (_Float16)(at(c, i + 4) * up);
+          sum += (float)v0 + (float)v1;
+          const _Float16 f = (i & 1) ? (_Float16)0.0625f : (_Float16)1.f;
+          qf[c][2 * i] = v0 * f;
+          qf[c][2 * i + 1] = v1 * f;
+        }
+      // the sum as two fp16 numbers, the second times 2^11 (and its offsets by 2^-11)
+      sum = half_sum(sum) * 0x1p-24f;
+      const _Float16 big = (_Float16)sum;
+      qsum[2 * g] = big;
+      qsum[2 * g + 1] = (_Float16)((sum - (float)big) * 0x1p11f);
+    }
+  }
+  const int p = a.causal ? first + qi : len - 1;
+  const int hi = r < rows ? min(p, len - 1) : -1, lo = a.window ? p - a.window + 1 : INT32_MIN;
+  // this wavefront's first and last positions
+  const int w_r0 = r0 + 32 * wave, w_r1 = min(rows, w_r0 + 32);
+  const int w_min = min(a.causal ? first + w_r0 / a.ratio : len - 1, len - 1);
+  const int w_max = w_r0 >= rows ? -1 : a.causal ? first + (w_r1 - 1) / a.ratio : len - 1;
+
+  // fp16 keys and values of block i (of buffer i % 2); a wavefront a task.
+  auto decode = [&](int i, bool hidden) {
+    const uint8_t* const from = raw + (i % RAW) * BYTES;
+    uint8_t* const to = held + (i & 1) * HELD;
+    const int end = hidden ? 0 : len - block_of(i) * kKvBlock;   // tokens of the block below it are the sequence's
+#pragma unroll
+    for (int t = wave; t < 2 * G; t += WAVES) {
+      const uint32_t m = lane & 15u, kq = lane >> 4;
+      if (t < G) {
+        const int g = t;
+        const u32x4 w = lds16(from + 1024 * g + 16 * lane);
+        const uint32_t A = m >> 3, h = (m >> 2) & 1u, bb = m & 3u;
+#pragma unroll
+        for (int u = 0; u < 2; ++u)
+#pragma unroll
+          for (int st = 0; st < 2; ++st)
+            *reinterpret_cast<half8_t*>(to + ((8 * g + 4 * st + kq) * 32 + 8 * (2 * A + u) + 4 * h + bb) * 16) =
+                codes_of(w[2 * u + st]);
+      } else {
+        const int g = t - G;
+        const u32x4 w = lds16(from + kv_value_codes(G) + 1024 * g + 16 * lane);
+        const uint8_t* const so = from + kv_value_so(G) + 128 * g + 16 * kq;
+        const Halves<8> s(so), o(so + 64);
+        half2_t s2[4], o2[4];
+#pragma unroll
+        for (int j = 0; j < 4; ++j) {
+          // places past the sequence's end may hold anything
+          const int t0 = 8 * (int)kq + j;
+          const uint32_t keep = t0 + 4 < end ? 0xFFFFFFFFu : t0 < end ? 0x0000FFFFu : 0u;
+          s2[j] = pair_of(s.w[j] & keep);
+          o2[j] = pair_of(o.w[j] & keep);
+        }
+#pragma unroll
+        for (int v = 0; v < 4; ++v) {
+          const uint32_t chunk = (((kq >> 1) * TILES + 2 * g + (v >> 1)) * 2 + (kq & 1u)) * 32 + 16 * (v & 1) + m;
+          *reinterpret_cast<u32x4*>(to + KEYS + chunk * 16) = values_of(dc, w[v], s2, o2);
+        }
+      }
+    }
+  };
+
+  float m = kNoMax, l = 0.f;
+  f32x16 acc[TILES];
+#pragma unroll
+  for (int t = 0; t < TILES; ++t)
+#pragma unroll
+    for (int i = 0; i < 16; ++i) acc[t][i] = 0.f;
+
+  // Block i is multiplied while block i + 1 is decoded and block i + 2 copied.
+  for (int i = -1; i < blocks; ++i) {
+    // copies of block i + 1 have landed: at most those of block i + 2 are on their way
+    if (i + 2 < blocks)
+      asm volatile("s_waitcnt vmcnt(%0) lgkmcnt(0)" ::"n"(COPIES) : "memory");
+    else
+      asm volatile("s_waitcnt vmcnt(0) lgkmcnt(0)" ::: "memory");
+    __syncthreads();
+    const int newest = min(i + 2, blocks - 1);
+    const bool gone_next = i + 1 < blocks && is_gone(i + 1, newest), gone_here = i >= 0 && is_gone(i, newest);
+    if (i + 3 < blocks) start_copy(i + 3);
+    if (i + 1 < blocks) decode(i + 1, gone_next);
+    const int t0 = i < 0 ? 0 : block_of(i) * kKvBlock;
+    if (i < 0 || t0 > w_max || gone_here) continue;
+    const uint8_t* const k = held + (i & 1) * HELD;
+    const uint8_t* const so = raw + (i % RAW) * BYTES + kv_key_so(G);
+    f32x16 sc, none;
+#pragma unroll
+    for (int j = 0; j < 16; ++j) none[j] = 0.f;
+    {
+      half8_t off;
+#pragma unroll
+      for (int j = 0; j < 8; ++j) off[j] = (_Float16)0.f;
+      const uint32_t tok = 16 * (col >> 4) + 8 * ((col >> 2) & 1u) + 4 * ((col >> 3) & 1u) + (col & 3u);
+#pragma unroll
+      for (int g = 0; g < G; ++g) {
+        const _Float16 o = *reinterpret_cast<const _Float16*>(so + 128 * g + 64 + 2 * tok);
+        off[2 * g] = half ? (_Float16)0.f : o;
+        off[2 * g + 1] = half ? (_Float16)0.f : o * (_Float16)0x1p-11f;
+      }
+      sc = __builtin_amdgcn_mfma_f32_32x32x16_f16(off, qsum, none, 0, 0, 0);
+    }
+#pragma unroll
+    for (int g = 0; g < G; ++g) {
+      f32x16 d = none;
+#pragma unroll
+      for (int c = 4 * g; c < 4 * g + 4; ++c)
+        d = __builtin_amdgcn_mfma_f32_32x32x16_f16(__builtin_bit_cast(half8_t, lds16(k + 1024 * c + 16 * lane)), qf[c],
+                                                   d, 0, 0, 0);
+#pragma unroll
+      for (int A = 0; A < 2; ++A) {
+        const Halves<8> s(so + 128 * g + 16 * (2 * A + half));
+#pragma unroll
+        for (int j = 0; j < 8; ++j) sc[8 * A + j] = __builtin_fmaf(s[j], d[8 * A + j], sc[8 * A + j]);
+      }
+    }
+    // register 8 A + 4 u + b: token 8 (2 A + half) + 4 u + b
+    if (t0 + kKvBlock - 1 > w_min || (a.window && t0 <= w_max - a.window && t0 + kKvBlock > a.sinks)) {
+#pragma unroll
+      for (int j = 0; j < 16; ++j) {
+        const int t = t0 + 8 * (2 * (j >> 3) + (int)half) + (j & 7);
+        const bool see = t <= hi && (t >= lo || t < a.sinks);
+        sc[j] = see ? sc[j] : -__builtin_inff();
+      }
+    }
+    float mx = sc[0];
+#pragma unroll
+    for (int j = 1; j < 16; ++j) mx = fmaxf(mx, sc[j]);
+    mx = half_max(mx) * to_log2;
+    if (__any(mx > m + kTileSlack)) {
+      const float mt = fmaxf(m, mx), f = __builtin_amdgcn_exp2f(m - mt);
+      m = mt;
+      l *= f;
+#pragma unroll
+      for (int t = 0; t < TILES; ++t) acc[t] *= f;
+    }
+    const float base = kTileShift - m;
+    half8_t pf[2];
+    const half2_t ones = {(_Float16)1.f, (_Float16)1.f};
+#pragma unroll
+    for (int A = 0; A < 2; ++A)
+#pragma unroll
+      for (int j = 0; j < 4; ++j) {
+        const half2_t pr = {
+            (_Float16)__builtin_amdgcn_exp2f(__builtin_fmaf(sc[8 * A + j], to_log2, base)),
+            (_Float16)__builtin_amdgcn_exp2f(__builtin_fmaf(sc[8 * A + 4 + j], to_log2, base))};
+        pf[A][2 * j] = pr.x;
+        pf[A][2 * j + 1] = pr.y;
+        l = __builtin_amdgcn_fdot2(pr, ones, l, false);   // the sum of what is multiplied
+      }
+#pragma unroll
+    for (int A = 0; A < 2; ++A)
+#pragma unroll
+      for (int t = 0; t < TILES; ++t)
+        acc[t] = __builtin_amdgcn_mfma_f32_32x32x16_f16(
+            __builtin_bit_cast(half8_t, lds16(k + KEYS + ((A * TILES + t) * 64 + lane) * 16)), pf[A], acc[t], 0, 0, 0);
+  }
+
+  l = half_sum(l);
+  if (r >= rows) return;
+  const float inv = l > 0.f ? 1.f / l : l == 0.f ? 0.f : l;   // 0: nothing seen; NaN stays
+  const int64_t o = (int64_t)(sq.c0 + qi) * a.n_heads + head * a.ratio + hh;
+#pragma unroll
+  for (int g = 0; g < G; ++g)
+#pragma unroll
+    for (int u = 0; u < 2; ++u)
+#pragma unroll
+      for (int bb = 0; bb < 4; ++bb) {
+        const f32x4 v = {acc[2 * g][4 * u + bb], acc[2 * g][8 + 4 * u + bb], acc[2 * g + 1][4 * u + bb],
+                         acc[2 * g + 1][8 + 4 * u + bb]};
+        store4(a, o * D + 64 * g + 4 * (8 * u + 4 * (int)half + bb), v * inv);
+      }
+  if (a.lse && half == 0) a.lse[o] = (__builtin_amdgcn_logf(l) + m - kTileShift) * kLn2;
+}
+
 }  // namespace
 
 // Rows a tile takes: columns of one MFMA tile, or two tiles. Pieces of the line:
@@ -841,6 +1182,13 @@ __global__ __launch_bounds__(kJoinThreads) void k_kv4_join(KvAttn a) {
 KvAttnPlan kv4_attn_plan(int batch, int heads, int ratio, int groups, int max_q, int max_kv, int window, int sinks) {
   KvAttnPlan p;
   const int64_t rows = (int64_t)max_q * ratio;
+  if (rows > 32) {   // many rows: the tile kernel
+    p.rows = groups <= 3 ? 128 : 256;
+    p.row_tiles = (int32_t)((rows + p.rows - 1) / p.rows);
+    p.tiles = (int64_t)batch * heads * p.row_tiles;
+    p.pieces = 0;
+    return p;
+  }
   p.rows = rows <= 4 ? 4 : rows <= 8 ? 8 : rows <= 16 ? 16 : 32;
   p.row_tiles = rows > 0 ? (int32_t)((rows + p.rows - 1) / p.rows) : 1;
   p.tiles = (int64_t)batch * heads * p.row_tiles;
@@ -866,6 +1214,15 @@ hipError_t launch_kv4_attention(const KvAttn& a, const KvAttnPlan& p, int batch,
   else if (p.rows == 8) VBQ_CALL(G, 8, ST);                                             \
   else if (p.rows == 16) VBQ_CALL(G, 16, ST);                                           \
   else VBQ_CALL(G, 32, ST)
+  if (p.rows > 32) {
+    switch (a.cache.groups) {
+      case 1: k_kv4_attn_tile<1, 4><<<grid, 256, 0, s>>>(a); break;
+      case 2: k_kv4_attn_tile<2, 4><<<grid, 256, 0, s>>>(a); break;
+      case 3: k_kv4_attn_tile<3, 4><<<grid, 256, 0, s>>>(a); break;
+      default: k_kv4_attn_tile<4, 8><<<grid, 512, 0, s>>>(a); break;
+    }
+    return hipGetLastError();
+  }
   switch (a.cache.groups) {
     case 1: VBQ_CALL2(1, 4); break;
     case 2: VBQ_CALL2(2, 4); break;
