@@ -834,10 +834,12 @@ __global__ __launch_bounds__(kJoinThreads) void k_kv4_join(KvAttn a) {
 }
 
 // ---- many rows ---------------------------------------------------------------------
-// WAVES wavefronts take 32 rows each of one head and walk the blocks together.
-// A block is copied raw to LDS (two ahead), spread there into operands (one
-// ahead, a part by each wavefront), and multiplied by every wavefront with
-// 32x32x16 MFMAs: S^T = K Q^T, O^T = V^T P^T. Key operands are the exact codes
+// Four wavefronts take 32 rows each of one head and walk the blocks together. A
+// block is copied raw to LDS, spread there into operands (a quarter by each
+// wavefront), and multiplied by every wavefront with 32x32x16 MFMAs: S^T = K
+// Q^T, O^T = V^T P^T. One turn of the loop spreads block i + 2, forms the
+// scores of block i + 1 and the probabilities and output of block i, in one
+// straight piece of code, so that matrix and vector instructions overlap. Key operands are the exact codes
 // (fp16 subnormals), scores take scale in fp32 as above and offsets by one more
 // MFMA: A holds a token's offsets o_g, B the rows' sums of q over group g.
 // Rounding keys to fp16 instead would save the scaling, but a score's error is
@@ -895,15 +897,15 @@ __device__ inline float half_sum(float v) {
   return __builtin_bit_cast(float, x) + __builtin_bit_cast(float, y);
 }
 
-template <int G, int WAVES>
-__global__ __launch_bounds__(64 * WAVES, 2) void k_kv4_attn_tile(KvAttn a) {
-  constexpr int D = 64 * G, BYTES = kKvGroupBytes * G, RAW = 4, TILES = D / 32;
+template <int G>
+__global__ __launch_bounds__(256, G >= 3 ? 1 : 2) void k_kv4_attn_tile(KvAttn a) {
+  constexpr int WAVES = 4, D = 64 * G, BYTES = kKvGroupBytes * G, RAW = 4, TILES = D / 32;
   constexpr int SHARE = BYTES / WAVES;   // a wavefront's part of a block's copy
   constexpr int COPIES = (SHARE + 1023) / 1024;
-  constexpr int KEYS = 32 * D * 2, HELD = 2 * KEYS;
+  constexpr int HELD = 32 * D * 2;   // a block's keys, or values
   static_assert(SHARE % 16 == 0, "copies are 16 bytes a lane");
   __shared__ __attribute__((aligned(16))) uint8_t raw[RAW * BYTES];
-  __shared__ __attribute__((aligned(16))) uint8_t held[2 * HELD];
+  __shared__ __attribute__((aligned(16))) uint8_t keys[2 * HELD], vals[3 * HELD];
   const uint32_t tid = threadIdx.x, lane = tid & 63u, col = lane & 31u, half = lane >> 5;
   const int wave = __builtin_amdgcn_readfirstlane(tid >> 6);
   const uint32_t raw_lds = lds_addr(raw);
@@ -1021,86 +1023,54 @@ __global__ __launch_bounds__(64 * WAVES, 2) void k_kv4_attn_tile(KvAttn a) {
   const int w_min = min(a.causal ? first + w_r0 / a.ratio : len - 1, len - 1);
   const int w_max = w_r0 >= rows ? -1 : a.causal ? first + (w_r1 - 1) / a.ratio : len - 1;
 
-  // fp16 keys and values of block i (of buffer i % 2); a wavefront a task.
-  auto decode = [&](int i, bool hidden) {
+  // Operands of block i: a wavefront takes word `wave` of every lane's four.
+  const uint32_t m16 = lane & 15u, kq = lane >> 4;
+  auto spread = [&](int i) {
     const uint8_t* const from = raw + (i % RAW) * BYTES;
-    uint8_t* const to = held + (i & 1) * HELD;
-    const int end = hidden ? 0 : len - block_of(i) * kKvBlock;   // tokens of the block below it are the sequence's
+    uint8_t* const tk = keys + (i & 1) * HELD + ((4 * (wave & 1) + kq) * 32 + 16 * (m16 >> 3) + 8 * (wave >> 1) +
+                                                 (m16 & 7u)) * 16;
+    uint8_t* const tv =
+        vals + (i % 3) * HELD + (((kq >> 1) * TILES + (wave >> 1)) * 64 + 32 * (kq & 1u) + 16 * (wave & 1) + m16) * 16;
 #pragma unroll
-    for (int t = wave; t < 2 * G; t += WAVES) {
-      const uint32_t m = lane & 15u, kq = lane >> 4;
-      if (t < G) {
-        const int g = t;
-        const u32x4 w = lds16(from + 1024 * g + 16 * lane);
-        const uint32_t A = m >> 3, h = (m >> 2) & 1u, bb = m & 3u;
-#pragma unroll
-        for (int u = 0; u < 2; ++u)
-#pragma unroll
-          for (int st = 0; st < 2; ++st)
-            *reinterpret_cast<half8_t*>(to + ((8 * g + 4 * st + kq) * 32 + 8 * (2 * A + u) + 4 * h + bb) * 16) =
-                codes_of(w[2 * u + st]);
-      } else {
-        const int g = t - G;
-        const u32x4 w = lds16(from + kv_value_codes(G) + 1024 * g + 16 * lane);
-        const uint8_t* const so = from + kv_value_so(G) + 128 * g + 16 * kq;
-        const Halves<8> s(so), o(so + 64);
-        half2_t s2[4], o2[4];
-#pragma unroll
-        for (int j = 0; j < 4; ++j) {
-          // places past the sequence's end may hold anything
-          const int t0 = 8 * (int)kq + j;
-          const uint32_t keep = t0 + 4 < end ? 0xFFFFFFFFu : t0 < end ? 0x0000FFFFu : 0u;
-          s2[j] = pair_of(s.w[j] & keep);
-          o2[j] = pair_of(o.w[j] & keep);
-        }
-#pragma unroll
-        for (int v = 0; v < 4; ++v) {
-          const uint32_t chunk = (((kq >> 1) * TILES + 2 * g + (v >> 1)) * 2 + (kq & 1u)) * 32 + 16 * (v & 1) + m;
-          *reinterpret_cast<u32x4*>(to + KEYS + chunk * 16) = values_of(dc, w[v], s2, o2);
-        }
-      }
+    for (int g = 0; g < G; ++g) {
+      *reinterpret_cast<half8_t*>(tk + 8 * 32 * 16 * g) =
+          codes_of(*reinterpret_cast<const uint32_t*>(from + 1024 * g + 16 * lane + 4 * wave));
+      const uint32_t w = *reinterpret_cast<const uint32_t*>(from + kv_value_codes(G) + 1024 * g + 16 * lane + 4 * wave);
+      const Halves<8> s(from + kv_value_so(G) + 128 * g + 16 * kq), o(from + kv_value_so(G) + 128 * g + 64 + 16 * kq);
+      const half2_t s2[4] = {pair_of(s.w[0]), pair_of(s.w[1]), pair_of(s.w[2]), pair_of(s.w[3])};
+      const half2_t o2[4] = {pair_of(o.w[0]), pair_of(o.w[1]), pair_of(o.w[2]), pair_of(o.w[3])};
+      *reinterpret_cast<u32x4*>(tv + 2 * 64 * 16 * g) = values_of(dc, w, s2, o2);
     }
   };
-
-  float m = kNoMax, l = 0.f;
-  f32x16 acc[TILES];
-#pragma unroll
-  for (int t = 0; t < TILES; ++t)
-#pragma unroll
-    for (int i = 0; i < 16; ++i) acc[t][i] = 0.f;
-
-  // Block i is multiplied while block i + 1 is decoded and block i + 2 copied.
-  for (int i = -1; i < blocks; ++i) {
-    // copies of block i + 1 have landed: at most those of block i + 2 are on their way
-    if (i + 2 < blocks)
-      asm volatile("s_waitcnt vmcnt(%0) lgkmcnt(0)" ::"n"(COPIES) : "memory");
-    else
-      asm volatile("s_waitcnt vmcnt(0) lgkmcnt(0)" ::: "memory");
-    __syncthreads();
-    const int newest = min(i + 2, blocks - 1);
-    const bool gone_next = i + 1 < blocks && is_gone(i + 1, newest), gone_here = i >= 0 && is_gone(i, newest);
-    if (i + 3 < blocks) start_copy(i + 3);
-    if (i + 1 < blocks) decode(i + 1, gone_next);
-    const int t0 = i < 0 ? 0 : block_of(i) * kKvBlock;
-    if (i < 0 || t0 > w_max || gone_here) continue;
-    const uint8_t* const k = held + (i & 1) * HELD;
-    const uint8_t* const so = raw + (i % RAW) * BYTES + kv_key_so(G);
-    f32x16 sc, none;
-#pragma unroll
-    for (int j = 0; j < 16; ++j) none[j] = 0.f;
-    {
-      half8_t off;
-#pragma unroll
-      for (int j = 0; j < 8; ++j) off[j] = (_Float16)0.f;
-      const uint32_t tok = 16 * (col >> 4) + 8 * ((col >> 2) & 1u) + 4 * ((col >> 3) & 1u) + (col & 3u);
-#pragma unroll
-      for (int g = 0; g < G; ++g) {
-        const _Float16 o = *reinterpret_cast<const _Float16*>(so + 128 * g + 64 + 2 * tok);
-        off[2 * g] = half ? (_Float16)0.f : o;
-        off[2 * g + 1] = half ? (_Float16)0.f : o * (_Float16)0x1p-11f;
-      }
-      sc = __builtin_amdgcn_mfma_f32_32x32x16_f16(off, qsum, none, 0, 0, 0);
+  // Places of block i past the sequence's end (all of them if its page is not
+  // in the cache) may hold anything: their values' scales and offsets become 0.
+  auto blank = [&](int i, int end) {
+    if (tid < 32 * G) {
+      const int t = (int)(tid & 31u);
+      const uint32_t place = 8 * ((uint32_t)t >> 3) + 2 * (t & 3) + ((t & 7) >> 2);
+      _Float16* const so = reinterpret_cast<_Float16*>(raw + (i % RAW) * BYTES + kv_value_so(G) + 128 * (tid >> 5));
+      if (t >= end) so[place] = so[32 + place] = (_Float16)0.f;
     }
+  };
+  // Scores of block i, unscaled by to_log2 and unmasked: register 8 A + 4 u + b
+  // is token 8 (2 A + half) + 4 u + b.
+  const uint32_t tok = 16 * (col >> 4) + 8 * ((col >> 2) & 1u) + 4 * ((col >> 3) & 1u) + (col & 3u);   // of row `col`
+  f32x16 none;
+#pragma unroll
+  for (int j = 0; j < 16; ++j) none[j] = 0.f;
+  auto scores = [&](int i) {
+    const uint8_t* const k = keys + (i & 1) * HELD;
+    const uint8_t* const so = raw + (i % RAW) * BYTES + kv_key_so(G);
+    half8_t off;
+#pragma unroll
+    for (int j = 0; j < 8; ++j) off[j] = (_Float16)0.f;
+#pragma unroll
+    for (int g = 0; g < G; ++g) {
+      const _Float16 o = *reinterpret_cast<const _Float16*>(so + 128 * g + 64 + 2 * tok);
+      off[2 * g] = half ? (_Float16)0.f : o;
+      off[2 * g + 1] = half ? (_Float16)0.f : o * (_Float16)0x1p-11f;
+    }
+    f32x16 x = __builtin_amdgcn_mfma_f32_32x32x16_f16(off, qsum, none, 0, 0, 0);
 #pragma unroll
     for (int g = 0; g < G; ++g) {
       f32x16 d = none;
@@ -1112,15 +1082,24 @@ __global__ __launch_bounds__(64 * WAVES, 2) void k_kv4_attn_tile(KvAttn a) {
       for (int A = 0; A < 2; ++A) {
         const Halves<8> s(so + 128 * g + 16 * (2 * A + half));
 #pragma unroll
-        for (int j = 0; j < 8; ++j) sc[8 * A + j] = __builtin_fmaf(s[j], d[8 * A + j], sc[8 * A + j]);
+        for (int j = 0; j < 8; ++j) x[8 * A + j] = __builtin_fmaf(s[j], d[8 * A + j], x[8 * A + j]);
       }
     }
-    // register 8 A + 4 u + b: token 8 (2 A + half) + 4 u + b
-    if (t0 + kKvBlock - 1 > w_min || (a.window && t0 <= w_max - a.window && t0 + kKvBlock > a.sinks)) {
+    return x;
+  };
+
+  float m = kNoMax, l = 0.f;
+  f32x16 acc[TILES];
+#pragma unroll
+  for (int t = 0; t < TILES; ++t) acc[t] = none;
+  // Masks scores of block i and lets the running maximum follow them.
+  auto settle = [&](int i, bool hidden, f32x16& sc) {
+    const int t0 = block_of(i) * kKvBlock;
+    if (hidden || t0 + kKvBlock - 1 > w_min || (a.window && t0 <= w_max - a.window && t0 + kKvBlock > a.sinks)) {
 #pragma unroll
       for (int j = 0; j < 16; ++j) {
         const int t = t0 + 8 * (2 * (j >> 3) + (int)half) + (j & 7);
-        const bool see = t <= hi && (t >= lo || t < a.sinks);
+        const bool see = !hidden && t <= hi && (t >= lo || t < a.sinks);
         sc[j] = see ? sc[j] : -__builtin_inff();
       }
     }
@@ -1135,26 +1114,63 @@ __global__ __launch_bounds__(64 * WAVES, 2) void k_kv4_attn_tile(KvAttn a) {
 #pragma unroll
       for (int t = 0; t < TILES; ++t) acc[t] *= f;
     }
-    const float base = kTileShift - m;
-    half8_t pf[2];
-    const half2_t ones = {(_Float16)1.f, (_Float16)1.f};
-#pragma unroll
-    for (int A = 0; A < 2; ++A)
-#pragma unroll
-      for (int j = 0; j < 4; ++j) {
-        const half2_t pr = {
-            (_Float16)__builtin_amdgcn_exp2f(__builtin_fmaf(sc[8 * A + j], to_log2, base)),
-            (_Float16)__builtin_amdgcn_exp2f(__builtin_fmaf(sc[8 * A + 4 + j], to_log2, base))};
-        pf[A][2 * j] = pr.x;
-        pf[A][2 * j + 1] = pr.y;
-        l = __builtin_amdgcn_fdot2(pr, ones, l, false);   // the sum of what is multiplied
+  };
+  // Waits for the copy of block i (of which at most block i + 1's follow), for
+  // every wavefront, and starts block i + 2's.
+  auto arrive = [&](int i) {
+    if (i + 1 < blocks)
+      asm volatile("s_waitcnt vmcnt(%0) lgkmcnt(0)" ::"n"(COPIES) : "memory");
+    else
+      asm volatile("s_waitcnt vmcnt(0) lgkmcnt(0)" ::: "memory");
+    __syncthreads();
+    if (i < blocks) {
+      const int end = is_gone(i, min(i + 1, blocks - 1)) ? 0 : len - block_of(i) * kKvBlock;
+      if (end < kKvBlock) {
+        blank(i, end);
+        __syncthreads();
       }
+      if (i + 2 < blocks) start_copy(i + 2);
+    }
+  };
+
+  if (blocks > 0) {
+    arrive(0);
+    spread(0);
+    arrive(1);
+    bool hide = is_gone(0, min(2, blocks - 1));
+    if (blocks > 1) spread(1);
+    f32x16 sc = scores(0);
+    settle(0, hide, sc);
+    for (int i = 0; i < blocks; ++i) {
+      arrive(i + 2);
+      hide = i + 1 < blocks && is_gone(i + 1, min(i + 4, blocks - 1));
+      // (the last turns spread and score what an older block left: unused)
+      const f32x16 next = scores(i + 1);
+      const float base = kTileShift - m;
+      half8_t pf[2];
+      const half2_t ones = {(_Float16)1.f, (_Float16)1.f};
 #pragma unroll
-    for (int A = 0; A < 2; ++A)
+      for (int A = 0; A < 2; ++A)
 #pragma unroll
-      for (int t = 0; t < TILES; ++t)
-        acc[t] = __builtin_amdgcn_mfma_f32_32x32x16_f16(
-            __builtin_bit_cast(half8_t, lds16(k + KEYS + ((A * TILES + t) * 64 + lane) * 16)), pf[A], acc[t], 0, 0, 0);
+        for (int j = 0; j < 4; ++j) {
+          const half2_t pr = {
+              (_Float16)__builtin_amdgcn_exp2f(__builtin_fmaf(sc[8 * A + j], to_log2, base)),
+              (_Float16)__builtin_amdgcn_exp2f(__builtin_fmaf(sc[8 * A + 4 + j], to_log2, base))};
+          pf[A][2 * j] = pr.x;
+          pf[A][2 * j + 1] = pr.y;
+          l = __builtin_amdgcn_fdot2(pr, ones, l, false);   // the sum of what is multiplied
+        }
+      const uint8_t* const v = vals + (i % 3) * HELD;
+#pragma unroll
+      for (int A = 0; A < 2; ++A)
+#pragma unroll
+        for (int t = 0; t < TILES; ++t)
+          acc[t] = __builtin_amdgcn_mfma_f32_32x32x16_f16(
+              __builtin_bit_cast(half8_t, lds16(v + ((A * TILES + t) * 64 + lane) * 16)), pf[A], acc[t], 0, 0, 0);
+      spread(i + 2);
+      sc = next;
+      if (i + 1 < blocks) settle(i + 1, hide, sc);
+    }
   }
 
   l = half_sum(l);
@@ -1183,7 +1199,7 @@ KvAttnPlan kv4_attn_plan(int batch, int heads, int ratio, int groups, int max_q,
   KvAttnPlan p;
   const int64_t rows = (int64_t)max_q * ratio;
   if (rows > 32) {   // many rows: the tile kernel
-    p.rows = groups <= 3 ? 128 : 256;
+    p.rows = 128;
     p.row_tiles = (int32_t)((rows + p.rows - 1) / p.rows);
     p.tiles = (int64_t)batch * heads * p.row_tiles;
     p.pieces = 0;
@@ -1216,10 +1232,10 @@ hipError_t launch_kv4_attention(const KvAttn& a, const KvAttnPlan& p, int batch,
   else VBQ_CALL(G, 32, ST)
   if (p.rows > 32) {
     switch (a.cache.groups) {
-      case 1: k_kv4_attn_tile<1, 4><<<grid, 256, 0, s>>>(a); break;
-      case 2: k_kv4_attn_tile<2, 4><<<grid, 256, 0, s>>>(a); break;
-      case 3: k_kv4_attn_tile<3, 4><<<grid, 256, 0, s>>>(a); break;
-      default: k_kv4_attn_tile<4, 8><<<grid, 512, 0, s>>>(a); break;
+      case 1: k_kv4_attn_tile<1><<<grid, 256, 0, s>>>(a); break;
+      case 2: k_kv4_attn_tile<2><<<grid, 256, 0, s>>>(a); break;
+      case 3: k_kv4_attn_tile<3><<<grid, 256, 0, s>>>(a); break;
+      default: k_kv4_attn_tile<4><<<grid, 256, 0, s>>>(a); break;
     }
     return hipGetLastError();
   }
