@@ -980,10 +980,27 @@ __global__ __launch_bounds__(256, G >= 3 ? 1 : 2) void k_kv4_attn_tile(KvAttn a)
     }
     for (int i = 0; i < 2; ++i)
       if (i < blocks) start_copy(i);
-    auto at = [&](int c, int i) {
-      const uint32_t u = (x[c][i >> 1] >> (16 * (i & 1))) & 0xFFFFu;
-      return a.bf16 ? __builtin_bit_cast(float, u << 16) : (float)__builtin_bit_cast(_Float16, (uint16_t)u);
-    };
+    // (one branch on the type, not one a number)
+    float y[D / 16][8];
+    if (a.bf16) {
+#pragma unroll
+      for (int c = 0; c < D / 16; ++c)
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+          y[c][2 * i] = __builtin_bit_cast(float, x[c][i] << 16);
+          y[c][2 * i + 1] = __builtin_bit_cast(float, x[c][i] & 0xFFFF0000u);
+        }
+    } else {
+#pragma unroll
+      for (int c = 0; c < D / 16; ++c)
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+          const uint32_t u = x[c][i];
+          y[c][2 * i] = (float)pair_of(u).x;
+          y[c][2 * i + 1] = (float)pair_of(u).y;
+        }
+    }
+    auto at = [&](int c, int i) { return y[c][i]; };
     float top = 0.f;
 #pragma unroll
     for (int c = 0; c < D / 16; ++c)
@@ -1092,7 +1109,7 @@ __global__ __launch_bounds__(256, G >= 3 ? 1 : 2) void k_kv4_attn_tile(KvAttn a)
   f32x16 acc[TILES];
 #pragma unroll
   for (int t = 0; t < TILES; ++t) acc[t] = none;
-  // Masks scores of block i and lets the running maximum follow them.
+  // Masks scores of block i and returns their row's maximum.
   auto settle = [&](int i, bool hidden, f32x16& sc) {
     const int t0 = block_of(i) * kKvBlock;
     if (hidden || t0 + kKvBlock - 1 > w_min || (a.window && t0 <= w_max - a.window && t0 + kKvBlock > a.sinks)) {
@@ -1106,14 +1123,7 @@ __global__ __launch_bounds__(256, G >= 3 ? 1 : 2) void k_kv4_attn_tile(KvAttn a)
     float mx = sc[0];
 #pragma unroll
     for (int j = 1; j < 16; ++j) mx = fmaxf(mx, sc[j]);
-    mx = half_max(mx) * to_log2;
-    if (__any(mx > m + kTileSlack)) {
-      const float mt = fmaxf(m, mx), f = __builtin_amdgcn_exp2f(m - mt);
-      m = mt;
-      l *= f;
-#pragma unroll
-      for (int t = 0; t < TILES; ++t) acc[t] *= f;
-    }
+    return half_max(mx) * to_log2;
   };
   // Waits for the copy of block i (of which at most block i + 1's follow), for
   // every wavefront, and starts block i + 2's.
@@ -1140,8 +1150,17 @@ __global__ __launch_bounds__(256, G >= 3 ? 1 : 2) void k_kv4_attn_tile(KvAttn a)
     bool hide = is_gone(0, min(2, blocks - 1));
     if (blocks > 1) spread(1);
     f32x16 sc = scores(0);
-    settle(0, hide, sc);
-    for (int i = 0; i < blocks; ++i) {
+    float mx = settle(0, hide, sc);
+    // The inner loop runs while no row's scores pass its running maximum by
+    // more than the slack: it has no vector arithmetic on the sums, so they
+    // stay in accumulation registers.
+    for (int i = 0; i < blocks;) {
+     const float mt = fmaxf(m, mx), f = __builtin_amdgcn_exp2f(m - mt);
+     m = mt;
+     l *= f;
+#pragma unroll
+     for (int t = 0; t < TILES; ++t) acc[t] *= f;
+     do {
       arrive(i + 2);
       hide = i + 1 < blocks && is_gone(i + 1, min(i + 4, blocks - 1));
       // (the last turns spread and score what an older block left: unused)
@@ -1169,7 +1188,9 @@ __global__ __launch_bounds__(256, G >= 3 ? 1 : 2) void k_kv4_attn_tile(KvAttn a)
               __builtin_bit_cast(half8_t, lds16(v + ((A * TILES + t) * 64 + lane) * 16)), pf[A], acc[t], 0, 0, 0);
       spread(i + 2);
       sc = next;
-      if (i + 1 < blocks) settle(i + 1, hide, sc);
+      ++i;
+      if (i < blocks) mx = settle(i, hide, sc);
+     } while (i < blocks && !__any(mx > m + kTileSlack));
     }
   }
 
