@@ -19,6 +19,7 @@ from __future__ import annotations
 
 import ctypes as C
 import os
+import struct
 
 import numpy as np
 
@@ -119,13 +120,13 @@ def _load():
     lib.kv4_page_bytes.restype = I64
     lib.kv4_page_bytes.argtypes = [I32, I32, I32]
     lib.kv4_append.restype = C.c_int
-    lib.kv4_append.argtypes = [C.POINTER(vbq_kv4), C.POINTER(vbq_kv4_range), P, P, I32, I64, I64, I64, I64, P]
+    lib.kv4_append.argtypes = [C.POINTER(vbq_kv4), P, P, P, I32, I64, I64, I64, I64, P]
     lib.kv4_read.restype = C.c_int
-    lib.kv4_read.argtypes = [C.POINTER(vbq_kv4), C.POINTER(vbq_kv4_range), P, P, I32, P]
+    lib.kv4_read.argtypes = [C.POINTER(vbq_kv4), P, P, P, I32, P]
     lib.kv4_attention_workspace.restype = I64
     lib.kv4_attention_workspace.argtypes = [C.POINTER(vbq_kv4), C.POINTER(vbq_kv4_attn)]
     lib.kv4_attention.restype = C.c_int
-    lib.kv4_attention.argtypes = [C.POINTER(vbq_kv4), C.POINTER(vbq_kv4_attn), P]
+    lib.kv4_attention.argtypes = [C.POINTER(vbq_kv4), P, P]
     return lib
 
 
@@ -482,35 +483,57 @@ def vbq_gemv_levels(pms, x, out=None, stream=None):
 KV4_FLAG_PAGE, KV4_FLAG_LENGTH, KV4_FLAG_NAN = 1, 2, 4
 
 
-def _kv4_dtype(dtype, what: str, names=("float16", "bfloat16", "float32")) -> int:
-    import torch
-    for i, n in enumerate(names):
-        if dtype == getattr(torch, n):
-            return i
-    raise ValueError(f"{what}: dtype {dtype}, expected one of {', '.join(names)}")
+_KV4_DTYPES = {}       # torch dtype -> vbq_dtype
+_KV4_RANGE = struct.Struct("@4i3P")                     # vbq_kv4_range
+_KV4_ATTN = struct.Struct("@10ifi4P2q3Pq")              # vbq_kv4_attn
+assert _KV4_RANGE.size == C.sizeof(vbq_kv4_range) and _KV4_ATTN.size == C.sizeof(vbq_kv4_attn)
 
 
-def _kv4_rows(t, what: str, heads: int, dim: int, device):
-    """Raises ValueError unless t is [tokens][heads][dim] on `device` with
-    contiguous channels and 16-byte aligned rows; returns its strides."""
-    import torch
-    if not isinstance(t, torch.Tensor):
-        raise ValueError(f"{what}: expected a torch tensor, got {type(t).__name__}")
-    if t.dim() != 3 or t.shape[1] != heads or t.shape[2] != dim:
-        raise ValueError(f"{what}: shape {tuple(t.shape)}, expected (tokens, {heads}, {dim})")
-    if t.device != device:
-        raise ValueError(f"{what}: on {t.device}, expected {device}")
+def _kv4_dtype(dtype, what: str, most: int = 2) -> int:
+    if not _KV4_DTYPES:
+        import torch
+        _KV4_DTYPES.update({torch.float16: 0, torch.bfloat16: 1, torch.float32: 2})
+    dt = _KV4_DTYPES.get(dtype, 3)
+    if dt > most:
+        raise ValueError(f"{what}: dtype {dtype}, expected one of {', '.join(('float16', 'bfloat16', 'float32')[:most + 1])}")
+    return dt
+
+
+def _kv4_rows(t, what: str, heads: int, cache):
+    """Raises ValueError unless t is [tokens][heads][head_dim] on the cache's
+    device with contiguous channels and 16-byte aligned rows; returns its
+    number of tokens, their stride and the heads'."""
+    if getattr(t, "ndim", 0) != 3:
+        raise ValueError(f"{what}: expected a torch tensor [tokens][{heads}][{cache.head_dim}]")
+    T, H, D = t.shape
+    if H != heads or D != cache.head_dim:
+        raise ValueError(f"{what}: shape {tuple(t.shape)}, expected (tokens, {heads}, {cache.head_dim})")
+    if t.get_device() != cache.index:
+        raise ValueError(f"{what}: on {t.device}, expected {cache.device}")
     ts, hs, cs = t.stride()
-    per16 = 16 // t.element_size()
     if cs != 1:
         raise ValueError(f"{what}: channels are not contiguous")
-    if t.shape[0] < 2:
+    if T < 2:
         ts = 0
-    if heads < 2:
+    if H < 2:
         hs = 0
+    per16 = 16 // t.itemsize
     if ts % per16 or hs % per16 or t.data_ptr() % 16:
         raise ValueError(f"{what}: token and head rows are not 16-byte aligned (strides {t.stride()})")
-    return ts, hs
+    return T, ts, hs
+
+
+def _kv4_stream(cache, stream) -> int:
+    return cache._raw_stream(cache.index) if stream is None else stream.cuda_stream
+
+
+def _kv4_new(cache, shape, dtype, stream):
+    """A tensor that belongs to the stream that will fill it."""
+    if stream is None:
+        return cache.data.new_empty(shape, dtype=dtype)
+    import torch
+    with torch.cuda.stream(stream):
+        return cache.data.new_empty(shape, dtype=dtype)
 
 
 class Kv4Cache:
@@ -536,6 +559,9 @@ class Kv4Cache:
         self.desc = vbq_kv4(self.n_pages, self.page_tokens, self.n_kv_heads, self.head_dim, 0, data.data_ptr(),
                             self.flags.data_ptr())
         self._ref = C.byref(self.desc)
+        self.index = data.get_device()
+        self._i32 = torch.int32
+        self._raw_stream = torch._C._cuda_getCurrentRawStream
 
     @property
     def device(self):
@@ -559,13 +585,17 @@ class Kv4Cache:
 
 
 def _kv4_index(cache: Kv4Cache, block_table, vec, cu):
-    import torch
-    if not isinstance(block_table, torch.Tensor) or block_table.dim() != 2:
+    """Batch and width of the block table, checked with the vectors beside it."""
+    if getattr(block_table, "ndim", 0) != 2:
         raise ValueError("block_table: expected a 2-D torch tensor")
     B, W = block_table.shape
-    _need(block_table, "block_table", torch.int32, (B, W), cache.device)
-    _need(vec, "lengths", torch.int32, (B,), cache.device)
-    _need(cu, "cumulative lengths", torch.int32, (B + 1,), cache.device)
+    i32, dev = cache._i32, cache.index
+    if not (block_table.dtype is i32 and vec.dtype is i32 and cu.dtype is i32 and block_table.get_device() == dev and
+            vec.get_device() == dev and cu.get_device() == dev and block_table.is_contiguous() and
+            vec.is_contiguous() and cu.is_contiguous() and vec.shape == (B,) and cu.shape == (B + 1,)):
+        _need(block_table, "block_table", i32, (B, W), cache.device)
+        _need(vec, "lengths", i32, (B,), cache.device)
+        _need(cu, "cumulative lengths", i32, (B + 1,), cache.device)
     if B < 1 or W < 1:
         raise ValueError(f"block_table: shape {(B, W)}")
     return B, W
@@ -578,16 +608,16 @@ def kv4_append(cache: Kv4Cache, k, v, block_table, start, cu_tokens, max_tokens=
     block_table int32 [B][W], start int32 [B], cu_tokens int32 [B+1], all on
     the GPU. max_tokens: no sequence has more rows (default: all of them)."""
     B, W = _kv4_index(cache, block_table, start, cu_tokens)
-    dt = _kv4_dtype(getattr(k, "dtype", None), "k")
-    kts, khs = _kv4_rows(k, "k", cache.n_kv_heads, cache.head_dim, cache.device)
-    vts, vhs = _kv4_rows(v, "v", cache.n_kv_heads, cache.head_dim, cache.device)
-    T = k.shape[0]
-    if v.dtype != k.dtype or v.shape[0] != T:
+    T, kts, khs = _kv4_rows(k, "k", cache.n_kv_heads, cache)
+    Tv, vts, vhs = _kv4_rows(v, "v", cache.n_kv_heads, cache)
+    dt = _kv4_dtype(k.dtype, "k")
+    if v.dtype is not k.dtype or Tv != T:
         raise ValueError(f"v: {v.dtype} {tuple(v.shape)}, expected k's {k.dtype} {tuple(k.shape)}")
-    r = vbq_kv4_range(B, W, T, T if max_tokens is None else max_tokens, block_table.data_ptr(), start.data_ptr(),
-                      cu_tokens.data_ptr())
-    _check(lib.kv4_append(cache._ref, C.byref(r), k.data_ptr(), v.data_ptr(), dt, kts, khs, vts, vhs,
-                          _stream(stream)), "kv4_append")
+    r = _KV4_RANGE.pack(B, W, T, T if max_tokens is None else max_tokens, block_table.data_ptr(), start.data_ptr(),
+                        cu_tokens.data_ptr())
+    st = lib.kv4_append(cache._ref, r, k.data_ptr(), v.data_ptr(), dt, kts, khs, vts, vhs, _kv4_stream(cache, stream))
+    if st:
+        _check(st, "kv4_append")
 
 
 def kv4_read(cache: Kv4Cache, block_table, start, cu_tokens, total_tokens, dtype, max_tokens=None, out=None,
@@ -595,35 +625,35 @@ def kv4_read(cache: Kv4Cache, block_table, start, cu_tokens, total_tokens, dtype
     """Reads tokens back as k, v [total_tokens][n_kv_heads][head_dim] of
     `dtype` (fp16, bf16 or fp32), rows as in kv4_append. out: (k, v) tensors
     to fill."""
-    import torch
     B, W = _kv4_index(cache, block_table, start, cu_tokens)
     dt = _kv4_dtype(dtype, "dtype")
     shape = (total_tokens, cache.n_kv_heads, cache.head_dim)
     if out is None:
-        with torch.cuda.stream(stream):   # the buffers belong to the stream that fills them
-            out = (torch.empty(shape, dtype=dtype, device=cache.device),
-                   torch.empty(shape, dtype=dtype, device=cache.device))
-    k, v = out
-    _need(k, "out k", dtype, shape, cache.device)
-    _need(v, "out v", dtype, shape, cache.device)
-    r = vbq_kv4_range(B, W, total_tokens, total_tokens if max_tokens is None else max_tokens,
-                      block_table.data_ptr(), start.data_ptr(), cu_tokens.data_ptr())
-    _check(lib.kv4_read(cache._ref, C.byref(r), k.data_ptr(), v.data_ptr(), dt, _stream(stream)), "kv4_read")
+        k = _kv4_new(cache, shape, dtype, stream)
+        v = _kv4_new(cache, shape, dtype, stream)
+    else:
+        k, v = out
+        _need(k, "out k", dtype, shape, cache.device)
+        _need(v, "out v", dtype, shape, cache.device)
+    r = _KV4_RANGE.pack(B, W, total_tokens, total_tokens if max_tokens is None else max_tokens,
+                        block_table.data_ptr(), start.data_ptr(), cu_tokens.data_ptr())
+    st = lib.kv4_read(cache._ref, r, k.data_ptr(), v.data_ptr(), dt, _kv4_stream(cache, stream))
+    if st:
+        _check(st, "kv4_read")
     return k, v
 
 
 def kv4_attention_workspace(cache: Kv4Cache, batch: int, total_q: int, n_heads: int, max_q: int, max_kv: int,
-                            window: int = 0, sinks: int = 0):
+                            window: int = 0, sinks: int = 0, stream=None):
     """A workspace for kv4_attention calls of these sizes (or any that
     need no more) that do not overlap in time."""
-    import torch
     a = vbq_kv4_attn(batch=batch, table_width=1, total_q=total_q, max_q=max_q, max_kv=max_kv, n_heads=n_heads,
                      dtype=0, causal=1, window=window, sinks=sinks, scale=1.0)
     n = lib.kv4_attention_workspace(cache._ref, C.byref(a))
     if n < 0:
         raise ValueError(f"kv4_attention: sizes refused (batch {batch}, {total_q} queries, {n_heads} heads over "
                          f"{cache.n_kv_heads}, max_q {max_q}, max_kv {max_kv}, window {window}, sinks {sinks})")
-    return torch.empty(n, dtype=torch.uint8, device=cache.device)
+    return _kv4_new(cache, (n,), cache.data.dtype, stream)
 
 
 def kv4_attention(cache: Kv4Cache, q, block_table, kv_lens, cu_q, max_q: int, max_kv: int, scale=None,
@@ -638,31 +668,33 @@ def kv4_attention(cache: Kv4Cache, q, block_table, kv_lens, cu_q, max_q: int, ma
     or tokens. scale: 1/sqrt(head_dim) by default. Returns out, of q's type;
     lse: float32 [queries][n_heads] to fill, or None. workspace: from
     kv4_attention_workspace, for calls that allocate nothing."""
-    import torch
     B, W = _kv4_index(cache, block_table, kv_lens, cu_q)
-    D = cache.head_dim
-    dt = _kv4_dtype(getattr(q, "dtype", None), "q", ("float16", "bfloat16"))
-    if q.dim() != 3 or q.shape[1] < 1 or q.shape[1] % cache.n_kv_heads:
-        raise ValueError(f"q: shape {tuple(q.shape)}, expected (queries, a multiple of {cache.n_kv_heads}, {D})")
-    T, H = q.shape[0], q.shape[1]
-    ts, hs = _kv4_rows(q, "q", H, D, cache.device)
+    H = q.shape[1] if getattr(q, "ndim", 0) == 3 else 0
+    if H < 1 or H % cache.n_kv_heads:
+        raise ValueError(f"q: shape {tuple(getattr(q, 'shape', ()))}, expected (queries, a multiple of "
+                         f"{cache.n_kv_heads}, {cache.head_dim})")
+    T, ts, hs = _kv4_rows(q, "q", H, cache)
+    D, dtype = cache.head_dim, q.dtype
+    dt = _kv4_dtype(dtype, "q", 1)
     if window and not causal:
         raise ValueError("window: needs causal=True")
     if out is None:
-        with torch.cuda.stream(stream):   # the buffer belongs to the stream that fills it
-            out = torch.empty(T, H, D, dtype=q.dtype, device=q.device)
+        out = _kv4_new(cache, (T, H, D), dtype, stream)
     else:
-        _need(out, "out", q.dtype, (T, H, D), cache.device)
+        _need(out, "out", dtype, (T, H, D), cache.device)
     if lse is not None:
+        import torch
         _need(lse, "lse", torch.float32, (T, H), cache.device)
     if workspace is None:
-        with torch.cuda.stream(stream):
-            workspace = kv4_attention_workspace(cache, B, T, H, max_q, max_kv, window, sinks)
-    elif workspace.dtype != torch.uint8 or workspace.device != cache.device or not workspace.is_contiguous():
+        workspace = kv4_attention_workspace(cache, B, T, H, max_q, max_kv, window, sinks, stream)
+    elif workspace.dtype is not cache.data.dtype or workspace.get_device() != cache.index or \
+            not workspace.is_contiguous():
         raise ValueError("workspace: expected a contiguous uint8 tensor on the cache's device")
-    a = vbq_kv4_attn(B, W, T, max_q, max_kv, H, dt, 1 if causal else 0, window, sinks,
-                     D ** -0.5 if scale is None else scale, 0, block_table.data_ptr(), kv_lens.data_ptr(),
-                     cu_q.data_ptr(), q.data_ptr(), ts, hs, out.data_ptr(),
-                     None if lse is None else lse.data_ptr(), workspace.data_ptr(), workspace.numel())
-    _check(lib.kv4_attention(cache._ref, C.byref(a), _stream(stream)), "kv4_attention")
+    a = _KV4_ATTN.pack(B, W, T, max_q, max_kv, H, dt, 1 if causal else 0, window, sinks,
+                       D ** -0.5 if scale is None else scale, 0, block_table.data_ptr(), kv_lens.data_ptr(),
+                       cu_q.data_ptr(), q.data_ptr(), ts, hs, out.data_ptr(), 0 if lse is None else lse.data_ptr(),
+                       workspace.data_ptr(), workspace.numel())
+    st = lib.kv4_attention(cache._ref, a, _kv4_stream(cache, stream))
+    if st:
+        _check(st, "kv4_attention")
     return out

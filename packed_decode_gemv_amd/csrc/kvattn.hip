@@ -897,9 +897,9 @@ __device__ inline float half_sum(float v) {
   return __builtin_bit_cast(float, x) + __builtin_bit_cast(float, y);
 }
 
-template <int G>
-__global__ __launch_bounds__(256, G >= 3 ? 1 : 2) void k_kv4_attn_tile(KvAttn a) {
-  constexpr int WAVES = 4, D = 64 * G, BYTES = kKvGroupBytes * G, RAW = 4, TILES = D / 32;
+template <int G, int NT>
+__global__ __launch_bounds__(256, G >= 3 || NT == 2 ? 1 : 2) void k_kv4_attn_tile(KvAttn a) {
+  constexpr int WAVES = 4, ROWS = 32 * NT * WAVES, D = 64 * G, BYTES = kKvGroupBytes * G, RAW = 4, TILES = D / 32;
   constexpr int SHARE = BYTES / WAVES;   // a wavefront's part of a block's copy
   constexpr int COPIES = (SHARE + 1023) / 1024;
   constexpr int HELD = 32 * D * 2;   // a block's keys, or values
@@ -917,15 +917,15 @@ __global__ __launch_bounds__(256, G >= 3 ? 1 : 2) void k_kv4_attn_tile(KvAttn a)
   const uint32_t bh = blockIdx.x % bh_n;
   const int b = (int)(bh / (uint32_t)a.cache.heads), head = (int)(bh % (uint32_t)a.cache.heads);
   Seq sq;
-  if (!seq_from(a, 32 * WAVES, a.cu[b], a.cu[b + 1], a.lens[b], sq)) {
+  if (!seq_from(a, ROWS, a.cu[b], a.cu[b + 1], a.lens[b], sq)) {
     if (tid == 0) kv_flag(a.cache, VBQ_KV4_FLAG_LENGTH);
     return;
   }
-  const int rows = sq.nq * a.ratio, rts = (rows + 32 * WAVES - 1) / (32 * WAVES);
+  const int rows = sq.nq * a.ratio, rts = (rows + ROWS - 1) / ROWS;
   const int rt = rts - 1 - (int)(blockIdx.x / bh_n);
   if (rt < 0) return;
   const int len = sq.len, first = sq.first;
-  const int r0 = rt * 32 * WAVES, r1 = min(rows, r0 + 32 * WAVES);
+  const int r0 = rt * ROWS, r1 = min(rows, r0 + ROWS);
   const Reach re = reach(len, a.causal ? first + r0 / a.ratio : len - 1,
                          a.causal ? first + (r1 - 1) / a.ratio : len - 1, a.window, a.sinks);
   const int blocks = re.ns + re.nw;
@@ -965,11 +965,15 @@ __global__ __launch_bounds__(256, G >= 3 ? 1 : 2) void k_kv4_attn_tile(KvAttn a)
   };
 
   // Queries: B operands, channels of a chunk as pairs; what the lane's row sees.
-  half8_t qf[D / 16], qsum;
-  float to_log2;
-  const int r = r0 + 32 * wave + (int)col;
-  const int qi = r / a.ratio, hh = r - qi * a.ratio;
-  {
+  for (int i = 0; i < 2; ++i)
+    if (i < blocks) start_copy(i);
+  half8_t qf[NT][D / 16], qsum[NT];
+  float to_log2[NT];
+  int hi[NT], lo[NT];
+  const int w_r0 = r0 + 32 * NT * wave;   // the wavefront's first row
+#pragma unroll
+  for (int nt = 0; nt < NT; ++nt) {
+    const int r = w_r0 + 32 * nt + (int)col, qi = r / a.ratio, hh = r - qi * a.ratio;
     u32x4 x[D / 16];
 #pragma unroll
     for (int c = 0; c < D / 16; ++c) {
@@ -978,8 +982,6 @@ __global__ __launch_bounds__(256, G >= 3 ? 1 : 2) void k_kv4_attn_tile(KvAttn a)
         x[c] = *reinterpret_cast<const u32x4*>(a.q + (int64_t)(sq.c0 + qi) * a.q_ts +
                                                (int64_t)(head * a.ratio + hh) * a.q_hs + 16 * c + 8 * half);
     }
-    for (int i = 0; i < 2; ++i)
-      if (i < blocks) start_copy(i);
     // (one branch on the type, not one a number)
     float y[D / 16][8];
     if (a.bf16) {
@@ -1000,19 +1002,18 @@ __global__ __launch_bounds__(256, G >= 3 ? 1 : 2) void k_kv4_attn_tile(KvAttn a)
           y[c][2 * i + 1] = (float)pair_of(u).y;
         }
     }
-    auto at = [&](int c, int i) { return y[c][i]; };
     float top = 0.f;
 #pragma unroll
     for (int c = 0; c < D / 16; ++c)
 #pragma unroll
-      for (int i = 0; i < 8; ++i) top = fmaxf(top, fabsf(at(c, i)));
+      for (int i = 0; i < 8; ++i) top = fmaxf(top, fabsf(y[c][i]));
     top = half_max(top);
     int ex = (int)(__builtin_bit_cast(uint32_t, top) >> 23) - 127;
     ex = top > 0.f ? max(ex, -100) : 13;
     const float up = ldexpf(1.f, 13 - ex);
-    to_log2 = a.scale_log2 * ldexpf(1.f, ex - 13 + 24);
+    to_log2[nt] = a.scale_log2 * ldexpf(1.f, ex - 13 + 24);
 #pragma unroll
-    for (int j = 0; j < 8; ++j) qsum[j] = (_Float16)0.f;
+    for (int j = 0; j < 8; ++j) qsum[nt][j] = (_Float16)0.f;
 #pragma unroll
     for (int g = 0; g < G; ++g) {
       float sum = 0.f;
@@ -1020,23 +1021,24 @@ __global__ __launch_bounds__(256, G >= 3 ? 1 : 2) void k_kv4_attn_tile(KvAttn a)
       for (int c = 4 * g; c < 4 * g + 4; ++c)
 #pragma unroll
         for (int i = 0; i < 4; ++i) {
-          const _Float16 v0 = (_Float16)(at(c, i) * up), v1 = (_Float16)(at(c, i + 4) * up);
+          const _Float16 v0 = (_Float16)(y[c][i] * up), v1 = (_Float16)(y[c][i + 4] * up);
           sum += (float)v0 + (float)v1;
           const _Float16 f = (i & 1) ? (_Float16)0.0625f : (_Float16)1.f;
-          qf[c][2 * i] = v0 * f;
-          qf[c][2 * i + 1] = v1 * f;
+          qf[nt][c][2 * i] = v0 * f;
+          qf[nt][c][2 * i + 1] = v1 * f;
         }
       // the sum as two fp16 numbers, the second times 2^11 (and its offsets by 2^-11)
       sum = half_sum(sum) * 0x1p-24f;
       const _Float16 big = (_Float16)sum;
-      qsum[2 * g] = big;
-      qsum[2 * g + 1] = (_Float16)((sum - (float)big) * 0x1p11f);
+      qsum[nt][2 * g] = big;
+      qsum[nt][2 * g + 1] = (_Float16)((sum - (float)big) * 0x1p11f);
     }
+    const int p = a.causal ? first + qi : len - 1;
+    hi[nt] = r < rows ? min(p, len - 1) : -1;
+    lo[nt] = a.window ? p - a.window + 1 : INT32_MIN;
   }
-  const int p = a.causal ? first + qi : len - 1;
-  const int hi = r < rows ? min(p, len - 1) : -1, lo = a.window ? p - a.window + 1 : INT32_MIN;
   // this wavefront's first and last positions
-  const int w_r0 = r0 + 32 * wave, w_r1 = min(rows, w_r0 + 32);
+  const int w_r1 = min(rows, w_r0 + 32 * NT);
   const int w_min = min(a.causal ? first + w_r0 / a.ratio : len - 1, len - 1);
   const int w_max = w_r0 >= rows ? -1 : a.causal ? first + (w_r1 - 1) / a.ratio : len - 1;
 
@@ -1075,7 +1077,7 @@ __global__ __launch_bounds__(256, G >= 3 ? 1 : 2) void k_kv4_attn_tile(KvAttn a)
   f32x16 none;
 #pragma unroll
   for (int j = 0; j < 16; ++j) none[j] = 0.f;
-  auto scores = [&](int i) {
+  auto scores = [&](int i, f32x16(&x)[NT]) {
     const uint8_t* const k = keys + (i & 1) * HELD;
     const uint8_t* const so = raw + (i % RAW) * BYTES + kv_key_so(G);
     half8_t off;
@@ -1087,43 +1089,62 @@ __global__ __launch_bounds__(256, G >= 3 ? 1 : 2) void k_kv4_attn_tile(KvAttn a)
       off[2 * g] = half ? (_Float16)0.f : o;
       off[2 * g + 1] = half ? (_Float16)0.f : o * (_Float16)0x1p-11f;
     }
-    f32x16 x = __builtin_amdgcn_mfma_f32_32x32x16_f16(off, qsum, none, 0, 0, 0);
+#pragma unroll
+    for (int nt = 0; nt < NT; ++nt) x[nt] = __builtin_amdgcn_mfma_f32_32x32x16_f16(off, qsum[nt], none, 0, 0, 0);
 #pragma unroll
     for (int g = 0; g < G; ++g) {
-      f32x16 d = none;
+      f32x16 d[NT];
 #pragma unroll
-      for (int c = 4 * g; c < 4 * g + 4; ++c)
-        d = __builtin_amdgcn_mfma_f32_32x32x16_f16(__builtin_bit_cast(half8_t, lds16(k + 1024 * c + 16 * lane)), qf[c],
-                                                   d, 0, 0, 0);
+      for (int c = 0; c < 4; ++c) {
+        const half8_t kc = __builtin_bit_cast(half8_t, lds16(k + 1024 * (4 * g + c) + 16 * lane));
+#pragma unroll
+        for (int nt = 0; nt < NT; ++nt)
+          d[nt] = __builtin_amdgcn_mfma_f32_32x32x16_f16(kc, qf[nt][4 * g + c], c ? d[nt] : none, 0, 0, 0);
+      }
 #pragma unroll
       for (int A = 0; A < 2; ++A) {
         const Halves<8> s(so + 128 * g + 16 * (2 * A + half));
 #pragma unroll
-        for (int j = 0; j < 8; ++j) x[8 * A + j] = __builtin_fmaf(s[j], d[8 * A + j], x[8 * A + j]);
+        for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+          for (int j = 0; j < 8; ++j) x[nt][8 * A + j] = __builtin_fmaf(s[j], d[nt][8 * A + j], x[nt][8 * A + j]);
       }
     }
-    return x;
   };
 
-  float m = kNoMax, l = 0.f;
-  f32x16 acc[TILES];
+  float m[NT], l[NT], mx[NT];
+  f32x16 acc[NT][TILES];
 #pragma unroll
-  for (int t = 0; t < TILES; ++t) acc[t] = none;
-  // Masks scores of block i and returns their row's maximum.
-  auto settle = [&](int i, bool hidden, f32x16& sc) {
+  for (int nt = 0; nt < NT; ++nt) {
+    m[nt] = kNoMax;
+    l[nt] = 0.f;
+#pragma unroll
+    for (int t = 0; t < TILES; ++t) acc[nt][t] = none;
+  }
+  // Masks scores of block i; their rows' maxima, and whether one passes its
+  // running maximum by more than the slack.
+  auto settle = [&](int i, bool hidden, f32x16(&sc)[NT]) {
     const int t0 = block_of(i) * kKvBlock;
     if (hidden || t0 + kKvBlock - 1 > w_min || (a.window && t0 <= w_max - a.window && t0 + kKvBlock > a.sinks)) {
 #pragma unroll
-      for (int j = 0; j < 16; ++j) {
-        const int t = t0 + 8 * (2 * (j >> 3) + (int)half) + (j & 7);
-        const bool see = !hidden && t <= hi && (t >= lo || t < a.sinks);
-        sc[j] = see ? sc[j] : -__builtin_inff();
-      }
-    }
-    float mx = sc[0];
+      for (int nt = 0; nt < NT; ++nt)
 #pragma unroll
-    for (int j = 1; j < 16; ++j) mx = fmaxf(mx, sc[j]);
-    return half_max(mx) * to_log2;
+        for (int j = 0; j < 16; ++j) {
+          const int t = t0 + 8 * (2 * (j >> 3) + (int)half) + (j & 7);
+          const bool see = !hidden && t <= hi[nt] && (t >= lo[nt] || t < a.sinks);
+          sc[nt][j] = see ? sc[nt][j] : -__builtin_inff();
+        }
+    }
+    bool pass = false;
+#pragma unroll
+    for (int nt = 0; nt < NT; ++nt) {
+      float top = sc[nt][0];
+#pragma unroll
+      for (int j = 1; j < 16; ++j) top = fmaxf(top, sc[nt][j]);
+      mx[nt] = half_max(top) * to_log2[nt];
+      pass |= mx[nt] > m[nt] + kTileSlack;
+    }
+    return (bool)__any(pass);
   };
   // Waits for the copy of block i (of which at most block i + 1's follow), for
   // every wavefront, and starts block i + 2's.
@@ -1149,66 +1170,83 @@ __global__ __launch_bounds__(256, G >= 3 ? 1 : 2) void k_kv4_attn_tile(KvAttn a)
     arrive(1);
     bool hide = is_gone(0, min(2, blocks - 1));
     if (blocks > 1) spread(1);
-    f32x16 sc = scores(0);
-    float mx = settle(0, hide, sc);
+    f32x16 sc[NT];
+    scores(0, sc);
+    settle(0, hide, sc);
     // The inner loop runs while no row's scores pass its running maximum by
     // more than the slack: it has no vector arithmetic on the sums, so they
     // stay in accumulation registers.
     for (int i = 0; i < blocks;) {
-     const float mt = fmaxf(m, mx), f = __builtin_amdgcn_exp2f(m - mt);
-     m = mt;
-     l *= f;
 #pragma unroll
-     for (int t = 0; t < TILES; ++t) acc[t] *= f;
-     do {
-      arrive(i + 2);
-      hide = i + 1 < blocks && is_gone(i + 1, min(i + 4, blocks - 1));
-      // (the last turns spread and score what an older block left: unused)
-      const f32x16 next = scores(i + 1);
-      const float base = kTileShift - m;
-      half8_t pf[2];
-      const half2_t ones = {(_Float16)1.f, (_Float16)1.f};
+      for (int nt = 0; nt < NT; ++nt) {
+        const float mt = fmaxf(m[nt], mx[nt]), f = __builtin_amdgcn_exp2f(m[nt] - mt);
+        m[nt] = mt;
+        l[nt] *= f;
 #pragma unroll
-      for (int A = 0; A < 2; ++A)
+        for (int t = 0; t < TILES; ++t) acc[nt][t] *= f;
+      }
+      bool pass = false;
+      do {
+        arrive(i + 2);
+        hide = i + 1 < blocks && is_gone(i + 1, min(i + 4, blocks - 1));
+        // (the last turns spread and score what an older block left: unused)
+        f32x16 next[NT];
+        scores(i + 1, next);
+        half8_t pf[NT][2];
+        const half2_t ones = {(_Float16)1.f, (_Float16)1.f};
 #pragma unroll
-        for (int j = 0; j < 4; ++j) {
-          const half2_t pr = {
-              (_Float16)__builtin_amdgcn_exp2f(__builtin_fmaf(sc[8 * A + j], to_log2, base)),
-              (_Float16)__builtin_amdgcn_exp2f(__builtin_fmaf(sc[8 * A + 4 + j], to_log2, base))};
-          pf[A][2 * j] = pr.x;
-          pf[A][2 * j + 1] = pr.y;
-          l = __builtin_amdgcn_fdot2(pr, ones, l, false);   // the sum of what is multiplied
+        for (int nt = 0; nt < NT; ++nt) {
+          const float base = kTileShift - m[nt];
+#pragma unroll
+          for (int A = 0; A < 2; ++A)
+#pragma unroll
+            for (int j = 0; j < 4; ++j) {
+              const half2_t pr = {
+                  (_Float16)__builtin_amdgcn_exp2f(__builtin_fmaf(sc[nt][8 * A + j], to_log2[nt], base)),
+                  (_Float16)__builtin_amdgcn_exp2f(__builtin_fmaf(sc[nt][8 * A + 4 + j], to_log2[nt], base))};
+              pf[nt][A][2 * j] = pr.x;
+              pf[nt][A][2 * j + 1] = pr.y;
+              l[nt] = __builtin_amdgcn_fdot2(pr, ones, l[nt], false);   // the sum of what is multiplied
+            }
         }
-      const uint8_t* const v = vals + (i % 3) * HELD;
+        const uint8_t* const v = vals + (i % 3) * HELD;
 #pragma unroll
-      for (int A = 0; A < 2; ++A)
+        for (int A = 0; A < 2; ++A)
 #pragma unroll
-        for (int t = 0; t < TILES; ++t)
-          acc[t] = __builtin_amdgcn_mfma_f32_32x32x16_f16(
-              __builtin_bit_cast(half8_t, lds16(v + ((A * TILES + t) * 64 + lane) * 16)), pf[A], acc[t], 0, 0, 0);
-      spread(i + 2);
-      sc = next;
-      ++i;
-      if (i < blocks) mx = settle(i, hide, sc);
-     } while (i < blocks && !__any(mx > m + kTileSlack));
+          for (int t = 0; t < TILES; ++t) {
+            const half8_t vc = __builtin_bit_cast(half8_t, lds16(v + ((A * TILES + t) * 64 + lane) * 16));
+#pragma unroll
+            for (int nt = 0; nt < NT; ++nt)
+              acc[nt][t] = __builtin_amdgcn_mfma_f32_32x32x16_f16(vc, pf[nt][A], acc[nt][t], 0, 0, 0);
+          }
+        spread(i + 2);
+#pragma unroll
+        for (int nt = 0; nt < NT; ++nt) sc[nt] = next[nt];
+        ++i;
+        if (i < blocks) pass = settle(i, hide, sc);
+      } while (i < blocks && !pass);
     }
   }
 
-  l = half_sum(l);
-  if (r >= rows) return;
-  const float inv = l > 0.f ? 1.f / l : l == 0.f ? 0.f : l;   // 0: nothing seen; NaN stays
-  const int64_t o = (int64_t)(sq.c0 + qi) * a.n_heads + head * a.ratio + hh;
 #pragma unroll
-  for (int g = 0; g < G; ++g)
+  for (int nt = 0; nt < NT; ++nt) {
+    const float sum = half_sum(l[nt]);
+    const int r = w_r0 + 32 * nt + (int)col, qi = r / a.ratio, hh = r - qi * a.ratio;
+    if (r >= rows) continue;
+    const float inv = sum > 0.f ? 1.f / sum : sum == 0.f ? 0.f : sum;   // 0: nothing seen; NaN stays
+    const int64_t o = (int64_t)(sq.c0 + qi) * a.n_heads + head * a.ratio + hh;
 #pragma unroll
-    for (int u = 0; u < 2; ++u)
+    for (int g = 0; g < G; ++g)
 #pragma unroll
-      for (int bb = 0; bb < 4; ++bb) {
-        const f32x4 v = {acc[2 * g][4 * u + bb], acc[2 * g][8 + 4 * u + bb], acc[2 * g + 1][4 * u + bb],
-                         acc[2 * g + 1][8 + 4 * u + bb]};
-        store4(a, o * D + 64 * g + 4 * (8 * u + 4 * (int)half + bb), v * inv);
-      }
-  if (a.lse && half == 0) a.lse[o] = (__builtin_amdgcn_logf(l) + m - kTileShift) * kLn2;
+      for (int u = 0; u < 2; ++u)
+#pragma unroll
+        for (int bb = 0; bb < 4; ++bb) {
+          const f32x4 v = {acc[nt][2 * g][4 * u + bb], acc[nt][2 * g][8 + 4 * u + bb], acc[nt][2 * g + 1][4 * u + bb],
+                           acc[nt][2 * g + 1][8 + 4 * u + bb]};
+          store4(a, o * D + 64 * g + 4 * (8 * u + 4 * (int)half + bb), v * inv);
+        }
+    if (a.lse && half == 0) a.lse[o] = (__builtin_amdgcn_logf(sum) + m[nt] - kTileShift) * kLn2;
+  }
 }
 
 }  // namespace
@@ -1251,12 +1289,15 @@ hipError_t launch_kv4_attention(const KvAttn& a, const KvAttnPlan& p, int batch,
   else if (p.rows == 8) VBQ_CALL(G, 8, ST);                                             \
   else if (p.rows == 16) VBQ_CALL(G, 16, ST);                                           \
   else VBQ_CALL(G, 32, ST)
+#define VBQ_TILE(G, NT2)                                              \
+  if (p.rows > 128) k_kv4_attn_tile<G, NT2><<<grid, 256, 0, s>>>(a);  \
+  else k_kv4_attn_tile<G, 1><<<grid, 256, 0, s>>>(a)
   if (p.rows > 32) {
     switch (a.cache.groups) {
-      case 1: k_kv4_attn_tile<1><<<grid, 256, 0, s>>>(a); break;
-      case 2: k_kv4_attn_tile<2><<<grid, 256, 0, s>>>(a); break;
-      case 3: k_kv4_attn_tile<3><<<grid, 256, 0, s>>>(a); break;
-      default: k_kv4_attn_tile<4><<<grid, 256, 0, s>>>(a); break;
+      case 1: VBQ_TILE(1, 2); break;
+      case 2: VBQ_TILE(2, 2); break;
+      case 3: VBQ_TILE(3, 1); break;
+      default: VBQ_TILE(4, 1); break;
     }
     return hipGetLastError();
   }
