@@ -417,10 +417,13 @@ typedef struct vbq_kv4_attn {
   int64_t q_head_stride;
   void* out;              /* device, [total_q][n_heads][head_dim], contiguous, 16-byte aligned */
   float* lse;             /* device, [total_q][n_heads], natural log of the sum of exponentials, or NULL */
-  void* workspace;        /* device, kv4_attention_workspace() bytes, 16-byte aligned (NULL if 0); calls that
-                             overlap in time need workspaces of their own */
+  void* workspace;        /* device, kv4_attention_workspace() bytes, 16-byte aligned (NULL if 0). Its first
+                             4 * VBQ_KV4_COUNTERS bytes are zero before the first call that uses it; every
+                             call leaves them zero. Calls that overlap in time need workspaces of their own. */
   int64_t workspace_bytes;
 } vbq_kv4_attn;
+
+#define VBQ_KV4_COUNTERS 2048
 
 /* Bytes of workspace that kv4_attention needs for these sizes (pointers are
  * not looked at), or -1 if the sizes are refused. Host only. */

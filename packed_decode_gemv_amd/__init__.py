@@ -481,6 +481,7 @@ def vbq_gemv_levels(pms, x, out=None, stream=None):
 
 # ---- 4-bit key/value cache ---------------------------------------------------------
 KV4_FLAG_PAGE, KV4_FLAG_LENGTH, KV4_FLAG_NAN = 1, 2, 4
+KV4_COUNTERS = 2048
 
 
 _KV4_DTYPES = {}       # torch dtype -> vbq_dtype
@@ -645,15 +646,20 @@ def kv4_read(cache: Kv4Cache, block_table, start, cu_tokens, total_tokens, dtype
 
 def kv4_attention_workspace(cache: Kv4Cache, batch: int, total_q: int, n_heads: int, max_q: int, max_kv: int,
                             window: int = 0, sinks: int = 0, stream=None):
-    """A workspace for kv4_attention calls of these sizes (or any that
-    need no more) that do not overlap in time."""
+    """A workspace for kv4_attention calls of these sizes (or any that need no
+    more) that do not overlap in time."""
+    import torch
     a = vbq_kv4_attn(batch=batch, table_width=1, total_q=total_q, max_q=max_q, max_kv=max_kv, n_heads=n_heads,
                      dtype=0, causal=1, window=window, sinks=sinks, scale=1.0)
     n = lib.kv4_attention_workspace(cache._ref, C.byref(a))
     if n < 0:
         raise ValueError(f"kv4_attention: sizes refused (batch {batch}, {total_q} queries, {n_heads} heads over "
                          f"{cache.n_kv_heads}, max_q {max_q}, max_kv {max_kv}, window {window}, sinks {sinks})")
-    return _kv4_new(cache, (n,), cache.data.dtype, stream)
+    w = _kv4_new(cache, (n,), cache.data.dtype, stream)
+    if n:
+        with torch.cuda.stream(stream):
+            w[:4 * KV4_COUNTERS].zero_()
+    return w
 
 
 def kv4_attention(cache: Kv4Cache, q, block_table, kv_lens, cu_q, max_q: int, max_kv: int, scale=None,

@@ -125,7 +125,7 @@ vbq_status check_attn(const vbq_kv4* cache, const vbq_kv4_attn* a, bool pointers
   if ((int64_t)a->max_q * ratio > INT32_MAX - 64) return VBQ_ERR_UNSUPPORTED;
   if (a->max_kv > INT32_MAX - 64) return VBQ_ERR_UNSUPPORTED;
   *p = kv4_attn_plan(a->batch, cache->n_kv_heads, ratio, c->groups, a->max_q, a->max_kv, a->window, a->sinks);
-  *bytes = (int64_t)2 * p->pieces * p->rows * (cache->head_dim + 2) * 4;
+  *bytes = p->pieces ? VBQ_KV4_COUNTERS * 4 + (int64_t)2 * p->pieces * p->rows * (cache->head_dim + 2) * 4 : 0;
   return VBQ_OK;
 }
 
@@ -198,7 +198,8 @@ vbq_status kv4_attention(const vbq_kv4* cache, const vbq_kv4_attn* a, hipStream_
   k.q_hs = a->q_head_stride;
   k.out = static_cast<uint16_t*>(a->out);
   k.lse = a->lse;
-  k.acc = static_cast<float*>(a->workspace);
+  k.counters = static_cast<uint32_t*>(a->workspace);
+  k.acc = static_cast<float*>(a->workspace) + VBQ_KV4_COUNTERS;
   k.ml = k.acc + (int64_t)2 * p.pieces * p.rows * cache->head_dim;
   k.width = a->table_width;
   k.total_q = a->total_q;
@@ -210,7 +211,7 @@ vbq_status kv4_attention(const vbq_kv4* cache, const vbq_kv4_attn* a, hipStream_
   k.causal = a->causal;
   k.window = a->window;
   k.sinks = a->window ? a->sinks : 0;
-  k.row_tiles = p.row_tiles;
+  k.ratio_inv = (65536 + k.ratio - 1) / k.ratio;
   k.batch = a->batch;
   k.pieces = p.pieces;
   k.min_chunk = 8;

@@ -50,12 +50,13 @@ struct KvAttn {
   int64_t q_ts, q_hs;
   uint16_t* out;
   float* lse;
+  uint32_t* counters;   // per (sequence, head): pieces done; zero between calls
   float* acc;           // partial sums, two slots a piece: [rows][head_dim]
-  float* ml;            // their maxima (powers of two) and sums: [rows][2]
+  float* ml;            // their bases (powers of two) and sums of p: [rows][2]
   int32_t width, total_q, max_q, max_kv;
   int32_t n_heads, ratio;      // query heads, and how many share a key/value head
   int32_t bf16, causal, window, sinks;
-  int32_t row_tiles;           // row tiles of a (sequence, head)
+  int32_t ratio_inv;           // ceil(65536 / ratio)
   int32_t batch;
   int32_t pieces, min_chunk;   // pieces of the line (0: a workgroup a tile), and blocks each takes at least
   float scale_log2;            // scale * log2(e)

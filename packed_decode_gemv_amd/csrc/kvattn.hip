@@ -188,16 +188,29 @@ __device__ inline void store4(const KvAttn& a, int64_t elem, const f32x4& v) {
   *reinterpret_cast<u32x2*>(a.out + elem) = u32x2{w[0] | (w[1] << 16), w[2] | (w[3] << 16)};
 }
 
+// Two numbers to and from other workgroups: device-scope, past the caches that
+// are not coherent.
+__device__ inline void put2(float* p, float x, float y) {
+  const f32x2 v = {x, y};
+  __hip_atomic_store(reinterpret_cast<uint64_t*>(p), __builtin_bit_cast(uint64_t, v), __ATOMIC_RELAXED,
+                     __HIP_MEMORY_SCOPE_AGENT);
+}
+__device__ inline f32x2 get2(const float* p) {
+  return __builtin_bit_cast(f32x2, __hip_atomic_load(reinterpret_cast<const uint64_t*>(p), __ATOMIC_RELAXED,
+                                                     __HIP_MEMORY_SCOPE_AGENT));
+}
+
 // A sequence of the call as the kernels see it.
 struct Seq {
   int32_t c0, nq, len, first;   // first row of q, queries, tokens held, position of query 0
   Reach re;
-  int32_t blocks, tiles;        // blocks of every tile, and tiles: heads * row tiles
+  int32_t blocks;               // that any of its rows sees
 };
 // False (and nothing to do) for numbers that do not fit.
-__device__ inline bool seq_from(const KvAttn& a, int rows_per_tile, int c0, int c1, int len, Seq& s) {
+__device__ inline bool seq_from(const KvAttn& a, int c0, int c1, int len, Seq& s) {
   const int64_t nq = (int64_t)c1 - c0;
-  s.blocks = s.tiles = 0;
+  s.blocks = 0;
+  s.re = Reach{0, 0, 0};
   if (c0 < 0 || nq < 0 || c1 > a.total_q || nq > a.max_q || len < 0 || len > a.max_kv ||
       (int64_t)len > ((int64_t)a.width << (a.cache.block_shift + 5)))
     return false;
@@ -208,75 +221,54 @@ __device__ inline bool seq_from(const KvAttn& a, int rows_per_tile, int c0, int 
   if (nq == 0) return true;
   s.re = reach(len, a.causal ? s.first : len - 1, len - 1, a.window, a.sinks);
   s.blocks = s.re.ns + s.re.nw;
-  s.tiles = a.cache.heads * ((s.nq * a.ratio + rows_per_tile - 1) / rows_per_tile);
   return true;
 }
+
+// Query of row r < 32 (up to 32 heads share a key/value head in the few-row kernel).
+__device__ inline int query_of(const KvAttn& a, int r) { return (r * a.ratio_inv) >> 16; }
 
 // Four channels of row r (sums v and of p, held times 2^base) and, once a row,
 // the log of the sum of exponentials.
 template <int D>
-__device__ inline void answer4(const KvAttn& a, const Seq& s, int head, int r, int c, const f32x4& v, float sum,
-                               float base) {
-  const int qi = r / a.ratio, hh = r - qi * a.ratio;
-  const int64_t o = (int64_t)(s.c0 + qi) * a.n_heads + head * a.ratio + hh;
+__device__ inline void answer4(const KvAttn& a, int c0, int head, int r, int c, const f32x4& v, float sum, float base) {
+  const int qi = query_of(a, r), hh = r - qi * a.ratio;
+  const int64_t o = (int64_t)(c0 + qi) * a.n_heads + head * a.ratio + hh;
   const float inv = sum > 0.f ? 1.f / sum : sum == 0.f ? 0.f : sum;   // 0: nothing seen; NaN stays
   store4(a, o * D + 4 * c, v * inv);
   if (a.lse && c == 0) a.lse[o] = (__builtin_amdgcn_logf(sum) - base) * kLn2;
 }
 
-// The token axes of all tiles laid end to end: sequence by sequence, tile by
-// tile, block by block. It is cut into equal pieces of `chunk` blocks, one a
-// workgroup, so the work is even whatever the lengths are; a tile that a cut
-// crosses leaves partial sums.
+// The token axes of all (sequence, head) tiles laid end to end: sequence by
+// sequence, head by head, block by block. The line is cut into kMaxPieces equal
+// pieces of `chunk` blocks, one a workgroup, so the work is even whatever the
+// lengths are; a tile that a cut crosses leaves partial sums.
 struct Line {
   int32_t total, chunk;
-  // lane l: sequence base + l of the batch, and the line's units up to its end
-  int32_t base, c0, c1, len, incl;
+  // lane l: sequence base + l of the batch, its blocks, and the line's units up to its end
+  int32_t base, c0, nq, len, ns, w0, blocks, incl;
 };
-__device__ inline void line_load(const KvAttn& a, int rows_per_tile, uint32_t lane, int base, int before, bool report,
-                                 Line& l) {
+__device__ inline void line_load(const KvAttn& a, uint32_t lane, int base, int before, bool report, Line& l) {
   const int b = base + (int)lane;
+  Seq s;
+  s.c0 = s.nq = s.len = s.blocks = 0;
+  s.re = Reach{0, 0, 0};
+  if (b < a.batch && !seq_from(a, a.cu[b], a.cu[b + 1], a.lens[b], s)) {
+    s.nq = 0;
+    if (report) kv_flag(a.cache, VBQ_KV4_FLAG_LENGTH);
+  }
   l.base = base;
-  l.c0 = l.c1 = l.len = 0;
-  int units = 0;
-  if (b < a.batch) {
-    l.c0 = a.cu[b];
-    l.c1 = a.cu[b + 1];
-    l.len = a.lens[b];
-    Seq s;
-    if (seq_from(a, rows_per_tile, l.c0, l.c1, l.len, s)) units = s.blocks * s.tiles;
-    else if (report) kv_flag(a.cache, VBQ_KV4_FLAG_LENGTH);
-  }
-  l.incl = before + wave_scan(units);
-}
-__device__ inline void line_of(const KvAttn& a, int rows_per_tile, uint32_t lane, bool report, Line& l) {
-  l.total = 0;
-  for (int base = 0; base < a.batch; base += 64) {
-    line_load(a, rows_per_tile, lane, base, l.total, report, l);
-    l.total = __builtin_amdgcn_readlane(l.incl, 63);
-  }
-  const uint32_t c = ((uint32_t)l.total + (uint32_t)a.pieces - 1u) / (uint32_t)a.pieces;
-  l.chunk = max((int)c, a.min_chunk);
-}
-// The sequence that unit `pos` (less than the total) belongs to.
-__device__ inline int line_find(const KvAttn& a, int rows_per_tile, uint32_t lane, int pos, Line& l) {
-  if (a.batch > 64) {
-    int before = 0;
-    for (int base = 0;; base += 64) {
-      line_load(a, rows_per_tile, lane, base, before, false, l);
-      before = __builtin_amdgcn_readlane(l.incl, 63);
-      if (before > pos || base + 64 >= a.batch) break;
-    }
-  }
-  const uint64_t past = __ballot(l.incl > pos);
-  return l.base + (past ? __builtin_ctzll(past) : 63);
-}
-__device__ inline int line_before(const Line& l, int lane_of_seq, int first) {   // units before a sequence
-  return lane_of_seq ? __builtin_amdgcn_readlane(l.incl, lane_of_seq - 1) : first;
+  l.c0 = s.c0;
+  l.nq = s.nq;
+  l.len = s.len;
+  l.ns = s.re.ns;
+  l.w0 = s.re.w0;
+  l.blocks = s.blocks;
+  l.incl = before + wave_scan(s.blocks * a.cache.heads);
 }
 
 // Where a piece's partial sums of a tile lie: the tile that a piece starts in
 // the middle of is its slot 0, one that it starts and does not end its slot 1.
+// They are written and read with device-scope accesses.
 template <int G, int ROWS>
 struct Slot {
   float *acc, *ml;
@@ -297,8 +289,11 @@ __global__ __launch_bounds__(64 * kWaves, G * ROWS > 64 ? 1 : 2) void k_kv4_attn
   constexpr int PARTS = 16 / COLS, PAIRS = 4 / PARTS;   // lanes that share a row's octet, token pairs of each
   constexpr int ODD = PARTS == 4 ? 1 : 2;   // sums kept apart for pairs whose codes come times 16
   constexpr int RING = kWaves * STAGES * BYTES, SUMS = kWaves * COLS * PITCH * 4;
-  __shared__ __attribute__((aligned(16))) uint8_t ring[RING > SUMS ? RING : SUMS];
+  constexpr int JOIN = 16 * kMaxPieces * 4 + 64 * kWaves * 16, AFTER = SUMS > JOIN ? SUMS : JOIN;
+  // blocks; afterwards the wavefronts' sums, or the pieces' factors and shares
+  __shared__ __attribute__((aligned(16))) uint8_t ring[RING > AFTER ? RING : AFTER];
   __shared__ float wml[kWaves][ROWS][2];
+  __shared__ uint32_t last;
   float* const buf = reinterpret_cast<float*>(ring);   // the wavefronts' sums, after a tile
   const uint32_t tid = threadIdx.x, lane = tid & 63u, col = lane & 15u, quarter = lane >> 4;
   const uint32_t qcol = col % COLS, part = col / COLS;
@@ -307,60 +302,85 @@ __global__ __launch_bounds__(64 * kWaves, G * ROWS > 64 ? 1 : 2) void k_kv4_attn
   const uint32_t ring_lds = lds_addr(own_ring);
 
   // This workgroup's piece of the line, or its tile.
-  int pos = 0, end = 1, b;
+  int pos = 0, end = 1;
   Line line;
   if (a.pieces) {
-    line_of(a, ROWS, lane, blockIdx.x == 0 && wave == 0, line);
-    pos = (int)min((int64_t)blockIdx.x * line.chunk, (int64_t)line.total);
-    end = (int)min((int64_t)pos + line.chunk, (int64_t)line.total);
-    if (pos >= end) return;
-    b = line_find(a, ROWS, lane, pos, line);
-  } else {
-    b = (int)(blockIdx.x / (uint32_t)(a.cache.heads * a.row_tiles));
+    line.total = 0;
+    for (int base = 0; base < a.batch; base += 64) {
+      line_load(a, lane, base, line.total, blockIdx.x == 0 && wave == 0, line);
+      line.total = __builtin_amdgcn_readlane(line.incl, 63);
+      // sequences that see nothing have no blocks: their rows are answered here
+      for (uint64_t none = __ballot(line.nq > 0 && line.blocks == 0); none; none &= none - 1) {
+        const int at = __builtin_ctzll(none);
+        if ((uint32_t)(base + at) % kMaxPieces != blockIdx.x) continue;
+        const int n = __builtin_amdgcn_readlane(line.nq, at) * a.n_heads;
+        const int64_t first = (int64_t)__builtin_amdgcn_readlane(line.c0, at) * a.n_heads;
+        for (int e = (int)tid; e < n * (D / 4); e += 64 * kWaves) store4(a, first * D + 4 * e, f32x4{0.f, 0.f, 0.f, 0.f});
+        if (a.lse)
+          for (int e = (int)tid; e < n; e += 64 * kWaves) a.lse[first + e] = -__builtin_inff();
+      }
+    }
+    line.chunk = max((line.total + kMaxPieces - 1) / kMaxPieces, a.min_chunk);
+    const int64_t from = (int64_t)blockIdx.x * line.chunk;
+    if (from >= line.total) return;
+    pos = (int)from;
+    end = min(pos + line.chunk, line.total);
+    if (a.batch > 64) {   // back to the lanes' sequences that hold `pos`
+      int before = 0;
+      for (int base = 0;; base += 64) {
+        line_load(a, lane, base, before, false, line);
+        before = __builtin_amdgcn_readlane(line.incl, 63);
+        if (before > pos) break;
+      }
+    }
   }
   for (bool fresh = true; pos < end; fresh = false) {
-  Seq sq;
-  int tile, i0, i1;
+  int b, head, i0, i1, blocks, c0, nq, len;
+  Reach re;
   if (a.pieces) {
-    const int at = b - line.base;   // below 64: every sequence but the last ends inside the lanes' ones
-    const int past = __builtin_amdgcn_readlane(line.incl, at);
-    if (past <= pos) {   // on to the next sequence
-      if (++b >= a.batch) return;
-      if (at == 63) line_load(a, ROWS, lane, b, past, false, line);
-      continue;
+    uint64_t past = __ballot(line.incl > pos);
+    if (!past) {   // on to the next 64 sequences
+      line_load(a, lane, line.base + 64, __builtin_amdgcn_readlane(line.incl, 63), false, line);
+      past = __ballot(line.incl > pos);
+      if (!past) continue;
     }
-    seq_from(a, ROWS, __builtin_amdgcn_readlane(line.c0, at), __builtin_amdgcn_readlane(line.c1, at),
-             __builtin_amdgcn_readlane(line.len, at), sq);
-    const uint32_t rel = (uint32_t)(pos - (past - sq.blocks * sq.tiles));
-    tile = (int)(rel / (uint32_t)sq.blocks);
-    i0 = (int)rel - tile * sq.blocks;
-    i1 = min(sq.blocks, i0 + (end - pos));
+    const int at = __builtin_ctzll(past);
+    b = line.base + at;
+    blocks = __builtin_amdgcn_readlane(line.blocks, at);
+    c0 = __builtin_amdgcn_readlane(line.c0, at);
+    nq = __builtin_amdgcn_readlane(line.nq, at);
+    len = __builtin_amdgcn_readlane(line.len, at);
+    re.ns = __builtin_amdgcn_readlane(line.ns, at);
+    re.w0 = __builtin_amdgcn_readlane(line.w0, at);
+    const uint32_t rel = (uint32_t)(pos - (__builtin_amdgcn_readlane(line.incl, at) - blocks * a.cache.heads));
+    head = (int)(rel / (uint32_t)blocks);
+    i0 = (int)rel - head * blocks;
+    i1 = min(blocks, i0 + (end - pos));
     pos += i1 - i0;
   } else {
-    if (!seq_from(a, ROWS, a.cu[b], a.cu[b + 1], a.lens[b], sq)) {
+    b = (int)(blockIdx.x / (uint32_t)a.cache.heads);
+    head = (int)(blockIdx.x % (uint32_t)a.cache.heads);
+    Seq sq;
+    if (!seq_from(a, a.cu[b], a.cu[b + 1], a.lens[b], sq)) {
       if (tid == 0) kv_flag(a.cache, VBQ_KV4_FLAG_LENGTH);
       return;
     }
-    tile = (int)(blockIdx.x % (uint32_t)(a.cache.heads * a.row_tiles));
-    if (tile >= sq.tiles) return;
+    c0 = sq.c0, nq = sq.nq, len = sq.len, re = sq.re, blocks = sq.blocks;
+    if (nq == 0) return;
     i0 = 0;
-    i1 = sq.blocks;
+    i1 = blocks;
     pos = end;
   }
-  const Reach re = sq.re;
-  const int c0 = sq.c0, len = sq.len, first = sq.first, rows = sq.nq * a.ratio;
-  const int rts = (rows + ROWS - 1) / ROWS;
-  const int head = tile / rts, r0 = (tile - head * rts) * ROWS, r1 = min(rows, r0 + ROWS);
-  const int p_min = a.causal ? first + r0 / a.ratio : len - 1;
-  const int p_max = a.causal ? first + (r1 - 1) / a.ratio : len - 1;
+  const int rows = nq * a.ratio, first = len - nq;
+  const int p_min = a.causal ? first : len - 1, p_max = len - 1;   // positions of the rows
   if (!fresh) __syncthreads();   // the ring held the last tile's sums
 
   // Queries, on their way while the first pages are looked up.
   u32x4 qraw[NT][G][2];
 #pragma unroll
   for (int nt = 0; nt < NT; ++nt) {
-    const int r = r0 + 16 * nt + (int)qcol;
-    const int qi = r / a.ratio, hh = r - qi * a.ratio;
+    const int r = 16 * nt + (int)qcol;
+    const int qi = query_of(a, r), hh = r - qi * a.ratio;
 #pragma unroll
     for (int g = 0; g < G; ++g)
 #pragma unroll
@@ -411,9 +431,9 @@ __global__ __launch_bounds__(64 * kWaves, G * ROWS > 64 ? 1 : 2) void k_kv4_attn
   int hi[NT], lo[NT];
 #pragma unroll
   for (int nt = 0; nt < NT; ++nt) {
-    const int r = r0 + 16 * nt + (int)qcol;
+    const int r = 16 * nt + (int)qcol;
     const bool in = r < rows;
-    const int qi = r / a.ratio;
+    const int qi = query_of(a, r);
     float x[G][2][8];
     float top = 0.f;
 #pragma unroll
@@ -695,11 +715,11 @@ __global__ __launch_bounds__(64 * kWaves, G * ROWS > 64 ? 1 : 2) void k_kv4_attn
     }
   }
   __syncthreads();
-  const bool whole = i0 == 0 && i1 == sq.blocks;
-  const Slot<G, ROWS> slot(a, blockIdx.x, i0 == 0);
+  const bool whole = i0 == 0 && i1 == blocks;
+  const Slot<G, ROWS> slot(a, (int)blockIdx.x, i0 == 0);
 #pragma unroll
   for (int nt = 0; nt < NT; ++nt) {
-    if (r0 + 16 * nt >= rows) break;
+    if (16 * nt >= rows) break;
     if (nt) __syncthreads();   // the buffer is taken again
     if (part == 0) {
       const int rr = 16 * nt + (int)qcol;
@@ -722,7 +742,7 @@ __global__ __launch_bounds__(64 * kWaves, G * ROWS > 64 ? 1 : 2) void k_kv4_attn
     __syncthreads();
     for (int e = (int)tid; e < COLS * (D / 4); e += 64 * kWaves) {
       const int row = e / (D / 4), c = e % (D / 4), rr = 16 * nt + row;
-      if (r0 + rr >= rows) break;
+      if (rr >= rows) break;
       float low = wml[0][rr][0];
 #pragma unroll
       for (int w = 1; w < kWaves; ++w) low = fminf(low, wml[w][rr][0]);
@@ -734,102 +754,91 @@ __global__ __launch_bounds__(64 * kWaves, G * ROWS > 64 ? 1 : 2) void k_kv4_attn
         v += *reinterpret_cast<const f32x4*>(buf + (w * COLS + row) * PITCH + 4 * c);
       }
       if (whole) {
-        answer4<D>(a, sq, head, r0 + rr, c, v, sum, low);
+        answer4<D>(a, c0, head, rr, c, v, sum, low);
       } else {
-        *reinterpret_cast<f32x4*>(slot.acc + rr * D + 4 * c) = v;
-        if (c == 0) *reinterpret_cast<f32x2*>(slot.ml + 2 * rr) = f32x2{low, sum};
+        put2(slot.acc + rr * D + 4 * c, v[0], v[1]);
+        put2(slot.acc + rr * D + 4 * c + 2, v[2], v[3]);
+        if (c == 0) put2(slot.ml + 2 * rr, low, sum);
       }
     }
   }
-  }
-}
+  if (whole) continue;
 
-// Joins the partial sums of tiles that the line's cuts cross, piece by piece in
-// order, and answers tiles that see no block at all. One workgroup a tile.
-constexpr int kJoinThreads = 512;
-template <int G, int ROWS>
-__global__ __launch_bounds__(kJoinThreads) void k_kv4_join(KvAttn a) {
-  constexpr int D = 64 * G, NT = (ROWS + 15) / 16, ROW_LANES = kJoinThreads / 16;
-  __shared__ float factor[16][kMaxPieces];
-  __shared__ f32x4 share[kJoinThreads];
-  __shared__ float total[16][2];
-  const uint32_t tid = threadIdx.x, lane = tid & 63u;
-  const uint32_t per = (uint32_t)(a.cache.heads * a.row_tiles);
-  const int b = (int)(blockIdx.x / per), tile = (int)(blockIdx.x % per);
-  Seq sq;
-  if (!seq_from(a, ROWS, a.cu[b], a.cu[b + 1], a.lens[b], sq) || tile >= sq.tiles) return;
-  const int rows = sq.nq * a.ratio, rts = (rows + ROWS - 1) / ROWS;
-  const int head = tile / rts, r0 = (tile - head * rts) * ROWS;
-  int p0 = 0, pieces = 0;
-  if (sq.blocks > 0) {
-    Line line;
-    line_of(a, ROWS, lane, false, line);
-    int before = 0;
-    if (a.batch > 64)
-      for (int base = 0;; base += 64) {   // the lanes' sequences are to hold b
-        line_load(a, ROWS, lane, base, before, false, line);
-        if (b < base + 64) break;
-        before = __builtin_amdgcn_readlane(line.incl, 63);
-      }
-    const uint32_t u = (uint32_t)(line_before(line, b - line.base, before) + tile * sq.blocks);
-    p0 = (int)(u / (uint32_t)line.chunk);
-    pieces = (int)((u + (uint32_t)sq.blocks - 1u) / (uint32_t)line.chunk) - p0 + 1;
-    if (pieces == 1) return;   // whole: its workgroup has answered
+  // Join the tile's pieces. The sums above are device-scope stores, which write
+  // through the caches; each wavefront waits for its own before the barrier, so
+  // once the tile's counter counts this piece every workgroup's device-scope
+  // loads see them. The piece that is counted last joins all of them, in order,
+  // and sets the counter back.
+  const int u0 = pos - (i1 - i0) - i0, p0 = u0 / line.chunk, pieces = (u0 + blocks - 1) / line.chunk - p0 + 1;
+  uint32_t* const counter = a.counters + (b * a.cache.heads + head);
+  __builtin_amdgcn_s_waitcnt(VBQ_VMCNT_IMM(0));
+  __syncthreads();
+  if (tid == 0) {
+    last = __hip_atomic_fetch_add(counter, 1u, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT) == (uint32_t)(pieces - 1);
+    if (last) __hip_atomic_store(counter, 0u, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
   }
+  __syncthreads();
+  if (!last) continue;
+  float* const factor = buf;                                                    // [16][kMaxPieces]
+  f32x4* const share = reinterpret_cast<f32x4*>(ring + 16 * kMaxPieces * 4);   // [threads]
+  constexpr int THREADS = 64 * kWaves, ROW_LANES = THREADS / 16;
 #pragma unroll 1
   for (int nt = 0; nt < NT; ++nt) {
-    const int nrow = min(16, rows - r0 - 16 * nt);
+    const int nrow = min(16, rows - 16 * nt);
     if (nrow <= 0) break;
     __syncthreads();
-    {   // 32 lanes a row: the smallest base, each piece's factor, the sum
+    {   // sixteen lanes a row: the smallest base, each piece's factor, the sum
       const int row = (int)tid / ROW_LANES, j = (int)tid % ROW_LANES;
       float low = -kNoMax, sum = 0.f;
       if (row < nrow) {
+#pragma unroll 4
         for (int p = j; p < pieces; p += ROW_LANES) {
-          const float base = Slot<G, ROWS>(a, p0 + p, p == 0).ml[2 * (16 * nt + row)];
-          factor[row][p] = base;
-          low = fminf(low, base);
+          const f32x2 v = get2(Slot<G, ROWS>(a, p0 + p, p == 0).ml + 2 * (16 * nt + row));
+          factor[row * kMaxPieces + p] = v.x;
+          low = fminf(low, v.x);
         }
       }
 #pragma unroll
       for (int d = 1; d < ROW_LANES; d <<= 1) low = fminf(low, __shfl_xor(low, d, 64));
       if (row < nrow) {
+#pragma unroll 4
         for (int p = j; p < pieces; p += ROW_LANES) {
-          const float f = __builtin_amdgcn_exp2f(low - factor[row][p]);
-          factor[row][p] = f;
-          sum += f * Slot<G, ROWS>(a, p0 + p, p == 0).ml[2 * (16 * nt + row) + 1];
+          const float f = __builtin_amdgcn_exp2f(low - factor[row * kMaxPieces + p]);
+          factor[row * kMaxPieces + p] = f;
+          sum += f * get2(Slot<G, ROWS>(a, p0 + p, p == 0).ml + 2 * (16 * nt + row)).y;
         }
       }
 #pragma unroll
       for (int d = 1; d < ROW_LANES; d <<= 1) sum += __shfl_xor(sum, d, 64);
       if (j == 0) {
-        total[row][0] = low;
-        total[row][1] = sum;
+        wml[0][row][0] = low;
+        wml[0][row][1] = sum;
       }
     }
     __syncthreads();
     // Threads beyond the rows' outputs share the pieces.
-    const int ne = nrow * (D / 4), parts = ne <= kJoinThreads / 2 ? kJoinThreads / ne : 1;
-    for (int e0 = 0; e0 < ne; e0 += kJoinThreads) {
-      const int e = parts > 1 ? (int)tid % ne : e0 + (int)tid, part = parts > 1 ? (int)tid / ne : 0;
+    const int ne = nrow * (D / 4), parts = ne <= THREADS / 2 ? THREADS / ne : 1;
+    for (int e0 = 0; e0 < ne; e0 += THREADS) {
+      const int e = parts > 1 ? (int)tid % ne : e0 + (int)tid, share_no = parts > 1 ? (int)tid / ne : 0;
       const int row = e / (D / 4), c = e % (D / 4);
       f32x4 v = {0.f, 0.f, 0.f, 0.f};
-      if (e < ne && part < parts) {
-#pragma unroll 4
-        for (int p = part; p < pieces; p += parts)
-          v += *reinterpret_cast<const f32x4*>(Slot<G, ROWS>(a, p0 + p, p == 0).acc + (16 * nt + row) * D + 4 * c) *
-               factor[row][p];
+      if (e < ne && share_no < parts) {
+#pragma unroll 8
+        for (int p = share_no; p < pieces; p += parts) {
+          const float* const q = Slot<G, ROWS>(a, p0 + p, p == 0).acc + (16 * nt + row) * D + 4 * c;
+          const f32x2 x = get2(q), y = get2(q + 2);
+          v += f32x4{x.x, x.y, y.x, y.y} * factor[row * kMaxPieces + p];
+        }
       }
       if (parts > 1) {
         share[tid] = v;
         __syncthreads();
-        if (part == 0)
+        if (share_no == 0)
           for (int i = 1; i < parts; ++i) v += share[e + i * ne];
       }
-      if (e < ne && part == 0) {
-        answer4<D>(a, sq, head, r0 + 16 * nt + row, c, v, total[row][1], total[row][0]);
-      }
+      if (e < ne && share_no == 0) answer4<D>(a, c0, head, 16 * nt + row, c, v, wml[0][row][1], wml[0][row][0]);
     }
+  }
   }
 }
 
@@ -917,7 +926,7 @@ __global__ __launch_bounds__(256, G >= 3 || NT == 2 ? 1 : 2) void k_kv4_attn_til
   const uint32_t bh = blockIdx.x % bh_n;
   const int b = (int)(bh / (uint32_t)a.cache.heads), head = (int)(bh % (uint32_t)a.cache.heads);
   Seq sq;
-  if (!seq_from(a, ROWS, a.cu[b], a.cu[b + 1], a.lens[b], sq)) {
+  if (!seq_from(a, a.cu[b], a.cu[b + 1], a.lens[b], sq)) {
     if (tid == 0) kv_flag(a.cache, VBQ_KV4_FLAG_LENGTH);
     return;
   }
@@ -1265,25 +1274,21 @@ KvAttnPlan kv4_attn_plan(int batch, int heads, int ratio, int groups, int max_q,
     return p;
   }
   p.rows = rows <= 4 ? 4 : rows <= 8 ? 8 : rows <= 16 ? 16 : 32;
-  p.row_tiles = rows > 0 ? (int32_t)((rows + p.rows - 1) / p.rows) : 1;
-  p.tiles = (int64_t)batch * heads * p.row_tiles;
+  p.row_tiles = 1;
+  p.tiles = (int64_t)batch * heads;
   int64_t blocks = ((int64_t)max_kv + kKvBlock - 1) / kKvBlock;
   if (window) {
     const int64_t most = ((int64_t)sinks + window + max_q) / kKvBlock + 3;
     blocks = blocks < most ? blocks : most;
   }
-  p.pieces = p.tiles < 2048 && blocks > 4 * kWaves && p.tiles * blocks < INT32_MAX - 65536 ? kMaxPieces : 0;
+  p.pieces = p.tiles <= VBQ_KV4_COUNTERS && blocks > 4 * kWaves && p.tiles * blocks < INT32_MAX - 65536 ? kMaxPieces : 0;
   return p;
 }
 
 hipError_t launch_kv4_attention(const KvAttn& a, const KvAttnPlan& p, int batch, hipStream_t s) {
   if (p.tiles > INT32_MAX) return hipErrorNotSupported;
   const dim3 grid(p.pieces ? (uint32_t)p.pieces : (uint32_t)p.tiles);
-#define VBQ_CALL(G, ROWS, ST)                                                           \
-  do {                                                                                  \
-    k_kv4_attn<G, ROWS, ST><<<grid, 64 * kWaves, 0, s>>>(a);                            \
-    if (p.pieces) k_kv4_join<G, ROWS><<<(uint32_t)p.tiles, kJoinThreads, 0, s>>>(a);    \
-  } while (0)
+#define VBQ_CALL(G, ROWS, ST) k_kv4_attn<G, ROWS, ST><<<grid, 64 * kWaves, 0, s>>>(a)
 #define VBQ_CALL2(G, ST)                                                                \
   if (p.rows == 4) VBQ_CALL(G, 4, ST);                                                  \
   else if (p.rows == 8) VBQ_CALL(G, 8, ST);                                             \
