@@ -188,13 +188,14 @@ __device__ inline void store4(const KvAttn& a, int64_t elem, const f32x4& v) {
   *reinterpret_cast<u32x2*>(a.out + elem) = u32x2{w[0] | (w[1] << 16), w[2] | (w[3] << 16)};
 }
 
-// Two numbers to and from other workgroups: device-scope, past the caches that
-// are not coherent.
+// Two numbers to and from other workgroups: device-scope accesses, past the
+// caches that are not coherent.
 __device__ inline void put2(float* p, float x, float y) {
   const f32x2 v = {x, y};
   __hip_atomic_store(reinterpret_cast<uint64_t*>(p), __builtin_bit_cast(uint64_t, v), __ATOMIC_RELAXED,
                      __HIP_MEMORY_SCOPE_AGENT);
 }
+
 __device__ inline f32x2 get2(const float* p) {
   return __builtin_bit_cast(f32x2, __hip_atomic_load(reinterpret_cast<const uint64_t*>(p), __ATOMIC_RELAXED,
                                                      __HIP_MEMORY_SCOPE_AGENT));
@@ -268,7 +269,6 @@ __device__ inline void line_load(const KvAttn& a, uint32_t lane, int base, int b
 
 // Where a piece's partial sums of a tile lie: the tile that a piece starts in
 // the middle of is its slot 0, one that it starts and does not end its slot 1.
-// They are written and read with device-scope accesses.
 template <int G, int ROWS>
 struct Slot {
   float *acc, *ml;
@@ -289,7 +289,7 @@ __global__ __launch_bounds__(64 * kWaves, G * ROWS > 64 ? 1 : 2) void k_kv4_attn
   constexpr int PARTS = 16 / COLS, PAIRS = 4 / PARTS;   // lanes that share a row's octet, token pairs of each
   constexpr int ODD = PARTS == 4 ? 1 : 2;   // sums kept apart for pairs whose codes come times 16
   constexpr int RING = kWaves * STAGES * BYTES, SUMS = kWaves * COLS * PITCH * 4;
-  constexpr int JOIN = 16 * kMaxPieces * 4 + 64 * kWaves * 16, AFTER = SUMS > JOIN ? SUMS : JOIN;
+  constexpr int FACTORS = kMaxPieces, JOIN = ROWS * FACTORS * 4 + 64 * kWaves * 16, AFTER = SUMS > JOIN ? SUMS : JOIN;
   // blocks; afterwards the wavefronts' sums, or the pieces' factors and shares
   __shared__ __attribute__((aligned(16))) uint8_t ring[RING > AFTER ? RING : AFTER];
   __shared__ float wml[kWaves][ROWS][2];
@@ -768,7 +768,8 @@ __global__ __launch_bounds__(64 * kWaves, G * ROWS > 64 ? 1 : 2) void k_kv4_attn
   // through the caches; each wavefront waits for its own before the barrier, so
   // once the tile's counter counts this piece every workgroup's device-scope
   // loads see them. The piece that is counted last joins all of them, in order,
-  // and sets the counter back.
+  // and sets the counter back. (An acquire fence and ordinary loads instead: 33
+  // against 22 us for 256 tiles of 34 blocks, since every fence empties an L2.)
   const int u0 = pos - (i1 - i0) - i0, p0 = u0 / line.chunk, pieces = (u0 + blocks - 1) / line.chunk - p0 + 1;
   uint32_t* const counter = a.counters + (b * a.cache.heads + head);
   __builtin_amdgcn_s_waitcnt(VBQ_VMCNT_IMM(0));
@@ -779,65 +780,58 @@ __global__ __launch_bounds__(64 * kWaves, G * ROWS > 64 ? 1 : 2) void k_kv4_attn
   }
   __syncthreads();
   if (!last) continue;
-  float* const factor = buf;                                                    // [16][kMaxPieces]
-  f32x4* const share = reinterpret_cast<f32x4*>(ring + 16 * kMaxPieces * 4);   // [threads]
-  constexpr int THREADS = 64 * kWaves, ROW_LANES = THREADS / 16;
-#pragma unroll 1
-  for (int nt = 0; nt < NT; ++nt) {
-    const int nrow = min(16, rows - 16 * nt);
-    if (nrow <= 0) break;
-    __syncthreads();
-    {   // sixteen lanes a row: the smallest base, each piece's factor, the sum
-      const int row = (int)tid / ROW_LANES, j = (int)tid % ROW_LANES;
-      float low = -kNoMax, sum = 0.f;
-      if (row < nrow) {
-#pragma unroll 4
-        for (int p = j; p < pieces; p += ROW_LANES) {
-          const f32x2 v = get2(Slot<G, ROWS>(a, p0 + p, p == 0).ml + 2 * (16 * nt + row));
-          factor[row * kMaxPieces + p] = v.x;
-          low = fminf(low, v.x);
-        }
-      }
-#pragma unroll
-      for (int d = 1; d < ROW_LANES; d <<= 1) low = fminf(low, __shfl_xor(low, d, 64));
-      if (row < nrow) {
-#pragma unroll 4
-        for (int p = j; p < pieces; p += ROW_LANES) {
-          const float f = __builtin_amdgcn_exp2f(low - factor[row * kMaxPieces + p]);
-          factor[row * kMaxPieces + p] = f;
-          sum += f * get2(Slot<G, ROWS>(a, p0 + p, p == 0).ml + 2 * (16 * nt + row)).y;
-        }
-      }
-#pragma unroll
-      for (int d = 1; d < ROW_LANES; d <<= 1) sum += __shfl_xor(sum, d, 64);
-      if (j == 0) {
-        wml[0][row][0] = low;
-        wml[0][row][1] = sum;
-      }
-    }
-    __syncthreads();
-    // Threads beyond the rows' outputs share the pieces.
-    const int ne = nrow * (D / 4), parts = ne <= THREADS / 2 ? THREADS / ne : 1;
-    for (int e0 = 0; e0 < ne; e0 += THREADS) {
-      const int e = parts > 1 ? (int)tid % ne : e0 + (int)tid, share_no = parts > 1 ? (int)tid / ne : 0;
-      const int row = e / (D / 4), c = e % (D / 4);
-      f32x4 v = {0.f, 0.f, 0.f, 0.f};
-      if (e < ne && share_no < parts) {
+  float* const factor = buf;                                                      // [rows][FACTORS]
+  f32x4* const share = reinterpret_cast<f32x4*>(ring + ROWS * FACTORS * 4);   // [threads]
+  constexpr int THREADS = 64 * kWaves, ROW_LANES = ROWS < 16 ? 16 : THREADS / ROWS;
+  {   // some lanes a row: the smallest base, each piece's factor, the sum
+    const int row = (int)tid / ROW_LANES, j = (int)tid % ROW_LANES;
+    float low = -kNoMax, sum = 0.f;   // sum is held times 2^low
+    if (row < rows) {
 #pragma unroll 8
-        for (int p = share_no; p < pieces; p += parts) {
-          const float* const q = Slot<G, ROWS>(a, p0 + p, p == 0).acc + (16 * nt + row) * D + 4 * c;
-          const f32x2 x = get2(q), y = get2(q + 2);
-          v += f32x4{x.x, x.y, y.x, y.y} * factor[row * kMaxPieces + p];
-        }
+      for (int p = j; p < pieces; p += ROW_LANES) {
+        const f32x2 v = get2(Slot<G, ROWS>(a, p0 + p, p == 0).ml + 2 * row);
+        factor[row * FACTORS + p] = v.x;
+        const float to = fminf(low, v.x);
+        sum = __builtin_fmaf(sum, __builtin_amdgcn_exp2f(to - low), v.y * __builtin_amdgcn_exp2f(to - v.x));
+        low = to;
       }
-      if (parts > 1) {
-        share[tid] = v;
-        __syncthreads();
-        if (share_no == 0)
-          for (int i = 1; i < parts; ++i) v += share[e + i * ne];
-      }
-      if (e < ne && share_no == 0) answer4<D>(a, c0, head, 16 * nt + row, c, v, wml[0][row][1], wml[0][row][0]);
     }
+    const float own = low;
+#pragma unroll
+    for (int d = 1; d < ROW_LANES; d <<= 1) low = fminf(low, __shfl_xor(low, d, 64));
+    sum *= __builtin_amdgcn_exp2f(low - own);
+    if (row < rows)
+      for (int p = j; p < pieces; p += ROW_LANES)
+        factor[row * FACTORS + p] = __builtin_amdgcn_exp2f(low - factor[row * FACTORS + p]);
+#pragma unroll
+    for (int d = 1; d < ROW_LANES; d <<= 1) sum += __shfl_xor(sum, d, 64);
+    if (j == 0 && row < rows) {
+      wml[0][row][0] = low;
+      wml[0][row][1] = sum;
+    }
+  }
+  __syncthreads();
+  // Threads beyond the rows' outputs share the pieces.
+  const int ne = rows * (D / 4), parts = ne <= THREADS / 2 ? THREADS / ne : 1;
+  for (int e0 = 0; e0 < ne; e0 += THREADS) {
+    const int e = parts > 1 ? (int)tid % ne : e0 + (int)tid, share_no = parts > 1 ? (int)tid / ne : 0;
+    const int row = e / (D / 4), c = e % (D / 4);
+    f32x4 v = {0.f, 0.f, 0.f, 0.f};
+    if (e < ne && share_no < parts) {
+#pragma unroll 16
+      for (int p = share_no; p < pieces; p += parts) {
+        const float* const q = Slot<G, ROWS>(a, p0 + p, p == 0).acc + row * D + 4 * c;
+        const f32x2 x = get2(q), y = get2(q + 2);
+        v += f32x4{x.x, x.y, y.x, y.y} * factor[row * FACTORS + p];
+      }
+    }
+    if (parts > 1) {
+      share[tid] = v;
+      __syncthreads();
+      if (share_no == 0)
+        for (int i = 1; i < parts; ++i) v += share[e + i * ne];
+    }
+    if (e < ne && share_no == 0) answer4<D>(a, c0, head, row, c, v, wml[0][row][1], wml[0][row][0]);
   }
   }
 }
