@@ -50,15 +50,15 @@ struct KvAttn {
   int64_t q_ts, q_hs;
   uint16_t* out;
   float* lse;
-  uint32_t* counters;   // per (sequence, head): pieces done; zero between calls
-  float* acc;           // partial sums, two slots a piece: [rows][head_dim]
+  uint32_t* counters;   // per (sequence, head): parts done; zero between calls
+  float* acc;           // sums of parts, by workgroup: [rows][head_dim]
   float* ml;            // their bases (powers of two) and sums of p: [rows][2]
   int32_t width, total_q, max_q, max_kv;
   int32_t n_heads, ratio;      // query heads, and how many share a key/value head
   int32_t bf16, causal, window, sinks;
   int32_t ratio_inv;           // ceil(65536 / ratio)
   int32_t batch;
-  int32_t pieces, min_chunk;   // pieces of the line (0: a workgroup a tile), and blocks each takes at least
+  int32_t parts;               // that long tiles are cut into in all, about (0: no cuts, a workgroup a tile)
   float scale_log2;            // scale * log2(e)
 };
 
@@ -66,10 +66,10 @@ hipError_t launch_kv4_append(const KvCache& c, const KvRange& r, const void* k, 
                              int64_t k_ts, int64_t k_hs, int64_t v_ts, int64_t v_hs, hipStream_t s);
 hipError_t launch_kv4_read(const KvCache& c, const KvRange& r, void* k, void* v, int dtype, hipStream_t s);
 // Sizes of an attention launch, from the call's sizes alone: rows of a tile,
-// row tiles of a (sequence, head), pieces (0: a workgroup a tile), tiles.
+// parts (as above), tiles and workgroups.
 struct KvAttnPlan {
-  int32_t rows, row_tiles, pieces;
-  int64_t tiles;
+  int32_t rows, row_tiles, parts;
+  int64_t tiles, grid;
 };
 KvAttnPlan kv4_attn_plan(int batch, int heads, int ratio, int groups, int max_q, int max_kv, int window, int sinks);
 hipError_t launch_kv4_attention(const KvAttn& a, const KvAttnPlan& p, int batch, hipStream_t s);

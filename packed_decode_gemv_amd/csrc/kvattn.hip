@@ -42,7 +42,8 @@ typedef float f32x2 __attribute__((ext_vector_type(2)));
 
 constexpr int kWaves = 4;
 constexpr float kNoMax = -1e30f;     // running maximum before any token
-constexpr int kMaxPieces = 512;
+constexpr int kParts = 512;          // workgroups that a launch aims at: two a CU
+constexpr int kLeastPart = 8;        // blocks of a part: two a wavefront
 
 // Exchanges with the lanes 16 and 32 apart (the lane quarters of a column).
 typedef uint32_t pair_t __attribute__((ext_vector_type(2)));
@@ -239,16 +240,14 @@ __device__ inline void answer4(const KvAttn& a, int c0, int head, int r, int c, 
   if (a.lse && c == 0) a.lse[o] = (__builtin_amdgcn_logf(sum) - base) * kLn2;
 }
 
-// The token axes of all (sequence, head) tiles laid end to end: sequence by
-// sequence, head by head, block by block. The line is cut into kMaxPieces equal
-// pieces of `chunk` blocks, one a workgroup, so the work is even whatever the
-// lengths are; a tile that a cut crosses leaves partial sums.
-struct Line {
-  int32_t total, chunk;
-  // lane l: sequence base + l of the batch, its blocks, and the line's units up to its end
-  int32_t base, c0, nq, len, ns, w0, blocks, incl;
+// Work is a tile (sequence, head) or a part of one: tiles longer than `chunk`
+// blocks are cut into equal parts, so that about kParts workgroups get work of
+// like size whatever the lengths are. The parts of all tiles, sequence by
+// sequence and head by head, are numbered by workgroup.
+struct Lanes {   // lane l: sequence base + l
+  int32_t base, c0, nq, len, ns, w0, blocks;
 };
-__device__ inline void line_load(const KvAttn& a, uint32_t lane, int base, int before, bool report, Line& l) {
+__device__ inline void lanes_load(const KvAttn& a, uint32_t lane, int base, bool report, Lanes& l) {
   const int b = base + (int)lane;
   Seq s;
   s.c0 = s.nq = s.len = s.blocks = 0;
@@ -264,20 +263,7 @@ __device__ inline void line_load(const KvAttn& a, uint32_t lane, int base, int b
   l.ns = s.re.ns;
   l.w0 = s.re.w0;
   l.blocks = s.blocks;
-  l.incl = before + wave_scan(s.blocks * a.cache.heads);
 }
-
-// Where a piece's partial sums of a tile lie: the tile that a piece starts in
-// the middle of is its slot 0, one that it starts and does not end its slot 1.
-template <int G, int ROWS>
-struct Slot {
-  float *acc, *ml;
-  __device__ Slot(const KvAttn& a, int piece, bool starts) {
-    const int64_t n = 2 * piece + (starts ? 1 : 0);
-    acc = a.acc + n * ROWS * (64 * G);
-    ml = a.ml + n * ROWS * 2;
-  }
-};
 
 // STAGES blocks a wavefront in LDS, STAGES - 1 of them on their way.
 typedef uint16_t ushort2_t __attribute__((ext_vector_type(2)));
@@ -289,8 +275,8 @@ __global__ __launch_bounds__(64 * kWaves, G * ROWS > 64 ? 1 : 2) void k_kv4_attn
   constexpr int PARTS = 16 / COLS, PAIRS = 4 / PARTS;   // lanes that share a row's octet, token pairs of each
   constexpr int ODD = PARTS == 4 ? 1 : 2;   // sums kept apart for pairs whose codes come times 16
   constexpr int RING = kWaves * STAGES * BYTES, SUMS = kWaves * COLS * PITCH * 4;
-  constexpr int FACTORS = kMaxPieces, JOIN = ROWS * FACTORS * 4 + 64 * kWaves * 16, AFTER = SUMS > JOIN ? SUMS : JOIN;
-  // blocks; afterwards the wavefronts' sums, or the pieces' factors and shares
+  constexpr int JOIN = ROWS * kParts * 4 + 64 * kWaves * 16, AFTER = SUMS > JOIN ? SUMS : JOIN;
+  // blocks; afterwards the wavefronts' sums, or the parts' factors and shares
   __shared__ __attribute__((aligned(16))) uint8_t ring[RING > AFTER ? RING : AFTER];
   __shared__ float wml[kWaves][ROWS][2];
   __shared__ uint32_t last;
@@ -301,62 +287,55 @@ __global__ __launch_bounds__(64 * kWaves, G * ROWS > 64 ? 1 : 2) void k_kv4_attn
   uint8_t* const own_ring = ring + wave * STAGES * BYTES;
   const uint32_t ring_lds = lds_addr(own_ring);
 
-  // This workgroup's piece of the line, or its tile.
-  int pos = 0, end = 1;
-  Line line;
-  if (a.pieces) {
-    line.total = 0;
-    for (int base = 0; base < a.batch; base += 64) {
-      line_load(a, lane, base, line.total, blockIdx.x == 0 && wave == 0, line);
-      line.total = __builtin_amdgcn_readlane(line.incl, 63);
-      // sequences that see nothing have no blocks: their rows are answered here
-      for (uint64_t none = __ballot(line.nq > 0 && line.blocks == 0); none; none &= none - 1) {
-        const int at = __builtin_ctzll(none);
-        if ((uint32_t)(base + at) % kMaxPieces != blockIdx.x) continue;
-        const int n = __builtin_amdgcn_readlane(line.nq, at) * a.n_heads;
-        const int64_t first = (int64_t)__builtin_amdgcn_readlane(line.c0, at) * a.n_heads;
-        for (int e = (int)tid; e < n * (D / 4); e += 64 * kWaves) store4(a, first * D + 4 * e, f32x4{0.f, 0.f, 0.f, 0.f});
-        if (a.lse)
-          for (int e = (int)tid; e < n; e += 64 * kWaves) a.lse[first + e] = -__builtin_inff();
-      }
-    }
-    line.chunk = max((line.total + kMaxPieces - 1) / kMaxPieces, a.min_chunk);
-    const int64_t from = (int64_t)blockIdx.x * line.chunk;
-    if (from >= line.total) return;
-    pos = (int)from;
-    end = min(pos + line.chunk, line.total);
-    if (a.batch > 64) {   // back to the lanes' sequences that hold `pos`
-      int before = 0;
-      for (int base = 0;; base += 64) {
-        line_load(a, lane, base, before, false, line);
-        before = __builtin_amdgcn_readlane(line.incl, 63);
-        if (before > pos) break;
-      }
-    }
-  }
-  for (bool fresh = true; pos < end; fresh = false) {
-  int b, head, i0, i1, blocks, c0, nq, len;
+  // This workgroup's part: blocks i0 .. i1 - 1 of a tile.
+  int b, head, i0 = 0, i1, blocks, c0, nq, len, part_no = 0, parts = 1;
   Reach re;
-  if (a.pieces) {
-    uint64_t past = __ballot(line.incl > pos);
-    if (!past) {   // on to the next 64 sequences
-      line_load(a, lane, line.base + 64, __builtin_amdgcn_readlane(line.incl, 63), false, line);
-      past = __ballot(line.incl > pos);
-      if (!past) continue;
+  if (a.parts) {
+    Lanes ln;
+    int total = 0;
+    for (int base = 0; base < a.batch; base += 64) {
+      lanes_load(a, lane, base, blockIdx.x == 0 && wave == 0, ln);
+      total += __builtin_amdgcn_readlane(wave_scan(ln.blocks), 63);
+      // sequences that see nothing have no parts: their rows are answered here
+      for (uint64_t none = __ballot(ln.nq > 0 && ln.blocks == 0); none; none &= none - 1) {
+        const int at = __builtin_ctzll(none);
+        if ((uint32_t)(base + at) % gridDim.x != blockIdx.x) continue;
+        const int n = __builtin_amdgcn_readlane(ln.nq, at) * a.n_heads;
+        const int64_t from = (int64_t)__builtin_amdgcn_readlane(ln.c0, at) * a.n_heads;
+        for (int e = (int)tid; e < n * (D / 4); e += 64 * kWaves) store4(a, from * D + 4 * e, f32x4{0.f, 0.f, 0.f, 0.f});
+        if (a.lse)
+          for (int e = (int)tid; e < n; e += 64 * kWaves) a.lse[from + e] = -__builtin_inff();
+      }
+    }
+    const int chunk = max((int)(((uint32_t)total * (uint32_t)a.cache.heads + (uint32_t)a.parts - 1u) / (uint32_t)a.parts),
+                          kLeastPart);
+    int before = 0, incl, n, size;   // of each lane's sequence: parts up to its end, parts of a tile, blocks of a part
+    uint64_t past;
+    for (int base = 0;; base += 64) {
+      if (a.batch > 64) lanes_load(a, lane, base, false, ln);
+      n = (int)((uint32_t)(ln.blocks + chunk - 1) / (uint32_t)chunk);
+      size = (int)((uint32_t)(ln.blocks + n - 1) / (uint32_t)max(n, 1));
+      n = (int)((uint32_t)(ln.blocks + size - 1) / (uint32_t)max(size, 1));
+      incl = before + wave_scan(n * a.cache.heads);
+      past = __ballot(incl > (int)blockIdx.x);
+      if (past) break;
+      if (base + 64 >= a.batch) return;
+      before = __builtin_amdgcn_readlane(incl, 63);
     }
     const int at = __builtin_ctzll(past);
-    b = line.base + at;
-    blocks = __builtin_amdgcn_readlane(line.blocks, at);
-    c0 = __builtin_amdgcn_readlane(line.c0, at);
-    nq = __builtin_amdgcn_readlane(line.nq, at);
-    len = __builtin_amdgcn_readlane(line.len, at);
-    re.ns = __builtin_amdgcn_readlane(line.ns, at);
-    re.w0 = __builtin_amdgcn_readlane(line.w0, at);
-    const uint32_t rel = (uint32_t)(pos - (__builtin_amdgcn_readlane(line.incl, at) - blocks * a.cache.heads));
-    head = (int)(rel / (uint32_t)blocks);
-    i0 = (int)rel - head * blocks;
-    i1 = min(blocks, i0 + (end - pos));
-    pos += i1 - i0;
+    b = ln.base + at;
+    blocks = __builtin_amdgcn_readlane(ln.blocks, at);
+    c0 = __builtin_amdgcn_readlane(ln.c0, at);
+    nq = __builtin_amdgcn_readlane(ln.nq, at);
+    len = __builtin_amdgcn_readlane(ln.len, at);
+    re.ns = __builtin_amdgcn_readlane(ln.ns, at);
+    re.w0 = __builtin_amdgcn_readlane(ln.w0, at);
+    parts = __builtin_amdgcn_readlane(n, at);
+    const int rel = (int)blockIdx.x - (__builtin_amdgcn_readlane(incl, at) - parts * a.cache.heads);
+    head = (int)((uint32_t)rel / (uint32_t)parts);
+    part_no = rel - head * parts;
+    i0 = part_no * __builtin_amdgcn_readlane(size, at);
+    i1 = min(blocks, i0 + __builtin_amdgcn_readlane(size, at));
   } else {
     b = (int)(blockIdx.x / (uint32_t)a.cache.heads);
     head = (int)(blockIdx.x % (uint32_t)a.cache.heads);
@@ -367,13 +346,10 @@ __global__ __launch_bounds__(64 * kWaves, G * ROWS > 64 ? 1 : 2) void k_kv4_attn
     }
     c0 = sq.c0, nq = sq.nq, len = sq.len, re = sq.re, blocks = sq.blocks;
     if (nq == 0) return;
-    i0 = 0;
     i1 = blocks;
-    pos = end;
   }
   const int rows = nq * a.ratio, first = len - nq;
   const int p_min = a.causal ? first : len - 1, p_max = len - 1;   // positions of the rows
-  if (!fresh) __syncthreads();   // the ring held the last tile's sums
 
   // Queries, on their way while the first pages are looked up.
   u32x4 qraw[NT][G][2];
@@ -715,8 +691,8 @@ __global__ __launch_bounds__(64 * kWaves, G * ROWS > 64 ? 1 : 2) void k_kv4_attn
     }
   }
   __syncthreads();
-  const bool whole = i0 == 0 && i1 == blocks;
-  const Slot<G, ROWS> slot(a, (int)blockIdx.x, i0 == 0);
+  float* const slot = a.acc + (int64_t)blockIdx.x * ROWS * D;   // a part's sums, and their bases and sums of p
+  float* const slot_ml = a.ml + (int64_t)blockIdx.x * ROWS * 2;
 #pragma unroll
   for (int nt = 0; nt < NT; ++nt) {
     if (16 * nt >= rows) break;
@@ -753,44 +729,45 @@ __global__ __launch_bounds__(64 * kWaves, G * ROWS > 64 ? 1 : 2) void k_kv4_attn
         sum += wml[w][rr][1] * __builtin_amdgcn_exp2f(low - wml[w][rr][0]);
         v += *reinterpret_cast<const f32x4*>(buf + (w * COLS + row) * PITCH + 4 * c);
       }
-      if (whole) {
+      if (parts == 1) {
         answer4<D>(a, c0, head, rr, c, v, sum, low);
       } else {
-        put2(slot.acc + rr * D + 4 * c, v[0], v[1]);
-        put2(slot.acc + rr * D + 4 * c + 2, v[2], v[3]);
-        if (c == 0) put2(slot.ml + 2 * rr, low, sum);
+        put2(slot + rr * D + 4 * c, v[0], v[1]);
+        put2(slot + rr * D + 4 * c + 2, v[2], v[3]);
+        if (c == 0) put2(slot_ml + 2 * rr, low, sum);
       }
     }
   }
-  if (whole) continue;
+  if (parts == 1) return;
 
-  // Join the tile's pieces. The sums above are device-scope stores, which write
+  // Join the tile's parts. The sums above are device-scope stores, which write
   // through the caches; each wavefront waits for its own before the barrier, so
-  // once the tile's counter counts this piece every workgroup's device-scope
-  // loads see them. The piece that is counted last joins all of them, in order,
+  // once the tile's counter counts this part every workgroup's device-scope
+  // loads see them. The part that is counted last joins all of them, in order,
   // and sets the counter back. (An acquire fence and ordinary loads instead: 33
   // against 22 us for 256 tiles of 34 blocks, since every fence empties an L2.)
-  const int u0 = pos - (i1 - i0) - i0, p0 = u0 / line.chunk, pieces = (u0 + blocks - 1) / line.chunk - p0 + 1;
   uint32_t* const counter = a.counters + (b * a.cache.heads + head);
   __builtin_amdgcn_s_waitcnt(VBQ_VMCNT_IMM(0));
   __syncthreads();
   if (tid == 0) {
-    last = __hip_atomic_fetch_add(counter, 1u, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT) == (uint32_t)(pieces - 1);
+    last = __hip_atomic_fetch_add(counter, 1u, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT) == (uint32_t)(parts - 1);
     if (last) __hip_atomic_store(counter, 0u, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
   }
   __syncthreads();
-  if (!last) continue;
-  float* const factor = buf;                                                      // [rows][FACTORS]
-  f32x4* const share = reinterpret_cast<f32x4*>(ring + ROWS * FACTORS * 4);   // [threads]
+  if (!last) return;
+  const float* const acc0 = slot - (int64_t)part_no * ROWS * D;
+  const float* const ml0 = slot_ml - (int64_t)part_no * ROWS * 2;
+  float* const factor = buf;                                                 // [rows][kParts]
+  f32x4* const share = reinterpret_cast<f32x4*>(ring + ROWS * kParts * 4);   // [threads]
   constexpr int THREADS = 64 * kWaves, ROW_LANES = ROWS < 16 ? 16 : THREADS / ROWS;
-  {   // some lanes a row: the smallest base, each piece's factor, the sum
+  {   // some lanes a row: the smallest base, each part's factor, the sum
     const int row = (int)tid / ROW_LANES, j = (int)tid % ROW_LANES;
     float low = -kNoMax, sum = 0.f;   // sum is held times 2^low
     if (row < rows) {
 #pragma unroll 8
-      for (int p = j; p < pieces; p += ROW_LANES) {
-        const f32x2 v = get2(Slot<G, ROWS>(a, p0 + p, p == 0).ml + 2 * row);
-        factor[row * FACTORS + p] = v.x;
+      for (int p = j; p < parts; p += ROW_LANES) {
+        const f32x2 v = get2(ml0 + (p * ROWS + row) * 2);
+        factor[row * kParts + p] = v.x;
         const float to = fminf(low, v.x);
         sum = __builtin_fmaf(sum, __builtin_amdgcn_exp2f(to - low), v.y * __builtin_amdgcn_exp2f(to - v.x));
         low = to;
@@ -801,8 +778,8 @@ __global__ __launch_bounds__(64 * kWaves, G * ROWS > 64 ? 1 : 2) void k_kv4_attn
     for (int d = 1; d < ROW_LANES; d <<= 1) low = fminf(low, __shfl_xor(low, d, 64));
     sum *= __builtin_amdgcn_exp2f(low - own);
     if (row < rows)
-      for (int p = j; p < pieces; p += ROW_LANES)
-        factor[row * FACTORS + p] = __builtin_amdgcn_exp2f(low - factor[row * FACTORS + p]);
+      for (int p = j; p < parts; p += ROW_LANES)
+        factor[row * kParts + p] = __builtin_amdgcn_exp2f(low - factor[row * kParts + p]);
 #pragma unroll
     for (int d = 1; d < ROW_LANES; d <<= 1) sum += __shfl_xor(sum, d, 64);
     if (j == 0 && row < rows) {
@@ -811,28 +788,27 @@ __global__ __launch_bounds__(64 * kWaves, G * ROWS > 64 ? 1 : 2) void k_kv4_attn
     }
   }
   __syncthreads();
-  // Threads beyond the rows' outputs share the pieces.
-  const int ne = rows * (D / 4), parts = ne <= THREADS / 2 ? THREADS / ne : 1;
+  // Threads beyond the rows' outputs share the parts.
+  const int ne = rows * (D / 4), shares = ne <= THREADS / 2 ? THREADS / ne : 1;
   for (int e0 = 0; e0 < ne; e0 += THREADS) {
-    const int e = parts > 1 ? (int)tid % ne : e0 + (int)tid, share_no = parts > 1 ? (int)tid / ne : 0;
+    const int e = shares > 1 ? (int)tid % ne : e0 + (int)tid, share_no = shares > 1 ? (int)tid / ne : 0;
     const int row = e / (D / 4), c = e % (D / 4);
     f32x4 v = {0.f, 0.f, 0.f, 0.f};
-    if (e < ne && share_no < parts) {
+    if (e < ne && share_no < shares) {
 #pragma unroll 16
-      for (int p = share_no; p < pieces; p += parts) {
-        const float* const q = Slot<G, ROWS>(a, p0 + p, p == 0).acc + row * D + 4 * c;
+      for (int p = share_no; p < parts; p += shares) {
+        const float* const q = acc0 + (p * ROWS + row) * D + 4 * c;
         const f32x2 x = get2(q), y = get2(q + 2);
-        v += f32x4{x.x, x.y, y.x, y.y} * factor[row * FACTORS + p];
+        v += f32x4{x.x, x.y, y.x, y.y} * factor[row * kParts + p];
       }
     }
-    if (parts > 1) {
+    if (shares > 1) {
       share[tid] = v;
       __syncthreads();
       if (share_no == 0)
-        for (int i = 1; i < parts; ++i) v += share[e + i * ne];
+        for (int i = 1; i < shares; ++i) v += share[e + i * ne];
     }
     if (e < ne && share_no == 0) answer4<D>(a, c0, head, row, c, v, wml[0][row][1], wml[0][row][0]);
-  }
   }
 }
 
@@ -1254,9 +1230,9 @@ __global__ __launch_bounds__(256, G >= 3 || NT == 2 ? 1 : 2) void k_kv4_attn_til
 
 }  // namespace
 
-// Rows a tile takes: columns of one MFMA tile, or two tiles. Pieces of the line:
-// two workgroups a CU. A tile is not cut (a workgroup each, no join) when there
-// are enough of them to fill the chip or the tiles are short.
+// Rows a tile takes: columns of one MFMA tile, or two tiles; above 32 the tile
+// kernel. Short tiles (up to four blocks a wavefront) are not cut: a workgroup
+// each, and no line to work out first.
 KvAttnPlan kv4_attn_plan(int batch, int heads, int ratio, int groups, int max_q, int max_kv, int window, int sinks) {
   KvAttnPlan p;
   const int64_t rows = (int64_t)max_q * ratio;
@@ -1264,7 +1240,8 @@ KvAttnPlan kv4_attn_plan(int batch, int heads, int ratio, int groups, int max_q,
     p.rows = 128;
     p.row_tiles = (int32_t)((rows + p.rows - 1) / p.rows);
     p.tiles = (int64_t)batch * heads * p.row_tiles;
-    p.pieces = 0;
+    p.parts = 0;
+    p.grid = p.tiles;
     return p;
   }
   p.rows = rows <= 4 ? 4 : rows <= 8 ? 8 : rows <= 16 ? 16 : 32;
@@ -1275,13 +1252,18 @@ KvAttnPlan kv4_attn_plan(int batch, int heads, int ratio, int groups, int max_q,
     const int64_t most = ((int64_t)sinks + window + max_q) / kKvBlock + 3;
     blocks = blocks < most ? blocks : most;
   }
-  p.pieces = p.tiles <= VBQ_KV4_COUNTERS && blocks > 4 * kWaves && p.tiles * blocks < INT32_MAX - 65536 ? kMaxPieces : 0;
+  // Parts are counted in 31 bits; a tile longer than total / parts is cut, so
+  // there are at most `parts` cuts beyond one part a tile. Aiming a little lower
+  // leaves room for the tiles' last parts, so that most launches run at once.
+  const bool cut = p.tiles <= VBQ_KV4_COUNTERS && blocks > 4 * kWaves && p.tiles * blocks < INT32_MAX - 65536;
+  p.parts = cut ? (int32_t)(kParts - (p.tiles < kParts ? p.tiles : kParts) / 2) : 0;
+  p.grid = cut ? p.parts + p.tiles : p.tiles;
   return p;
 }
 
 hipError_t launch_kv4_attention(const KvAttn& a, const KvAttnPlan& p, int batch, hipStream_t s) {
-  if (p.tiles > INT32_MAX) return hipErrorNotSupported;
-  const dim3 grid(p.pieces ? (uint32_t)p.pieces : (uint32_t)p.tiles);
+  if (p.grid > INT32_MAX) return hipErrorNotSupported;
+  const dim3 grid((uint32_t)p.grid);
 #define VBQ_CALL(G, ROWS, ST) k_kv4_attn<G, ROWS, ST><<<grid, 64 * kWaves, 0, s>>>(a)
 #define VBQ_CALL2(G, ST)                                                                \
   if (p.rows == 4) VBQ_CALL(G, 4, ST);                                                  \
