@@ -42,7 +42,7 @@ typedef float f32x2 __attribute__((ext_vector_type(2)));
 
 constexpr int kWaves = 4;
 constexpr float kNoMax = -1e30f;     // running maximum before any token
-constexpr int kParts = 512;          // workgroups that a launch aims at: two a CU
+constexpr int kParts = 512;          // workgroups that a launch aims at, at most
 constexpr int kLeastPart = 8;        // blocks of a part: two a wavefront
 
 // Exchanges with the lanes 16 and 32 apart (the lane quarters of a column).
@@ -265,11 +265,17 @@ __device__ inline void lanes_load(const KvAttn& a, uint32_t lane, int base, bool
   l.blocks = s.blocks;
 }
 
-// STAGES blocks a wavefront in LDS, STAGES - 1 of them on their way.
+// STAGES blocks a wavefront in LDS, STAGES - 1 of them on their way. Where
+// registers allow four workgroups a CU (up to 8 rows, heads of up to 128), two
+// stages: with heads of 128 the same bytes are on their way as with two
+// workgroups of four stages, and the wavefronts hide each other's arithmetic
+// (32 sequences of up to 8192 tokens, 4 rows a tile: 50 against 60 us).
+template <int G, int ROWS>
+constexpr bool kRoomy = G <= 2 && ROWS <= 8;
 typedef uint16_t ushort2_t __attribute__((ext_vector_type(2)));
 
 template <int G, int ROWS, int STAGES>
-__global__ __launch_bounds__(64 * kWaves, G * ROWS > 64 ? 1 : 2) void k_kv4_attn(KvAttn a) {
+__global__ __launch_bounds__(64 * kWaves, (kRoomy<G, ROWS>) ? 4 : G * ROWS > 64 ? 1 : 2) void k_kv4_attn(KvAttn a) {
   constexpr int D = 64 * G, PITCH = D + 4, BYTES = kKvGroupBytes * G;
   constexpr int NT = ROWS > 16 ? 2 : 1, COLS = ROWS > 16 ? 16 : ROWS;   // column tiles, and columns used of each
   constexpr int PARTS = 16 / COLS, PAIRS = 4 / PARTS;   // lanes that share a row's octet, token pairs of each
@@ -1231,8 +1237,11 @@ __global__ __launch_bounds__(256, G >= 3 || NT == 2 ? 1 : 2) void k_kv4_attn_til
 }  // namespace
 
 // Rows a tile takes: columns of one MFMA tile, or two tiles; above 32 the tile
-// kernel. Short tiles (up to four blocks a wavefront) are not cut: a workgroup
-// each, and no line to work out first.
+// kernel. Short tiles are not cut (a workgroup each, and no parts to work out
+// and join): up to five blocks a wavefront, or twelve where the tiles alone fill
+// the chip. Uncut and cut, heads of 128, 4 rows: 8 tiles of 19 blocks 9.4 and
+// 10.0 us, of 29 blocks 12.0 and 10.1; 256 tiles of 38 blocks 16.4 and 18.0,
+// of 63 blocks 21.8 and 22.2.
 KvAttnPlan kv4_attn_plan(int batch, int heads, int ratio, int groups, int max_q, int max_kv, int window, int sinks) {
   KvAttnPlan p;
   const int64_t rows = (int64_t)max_q * ratio;
@@ -1252,11 +1261,13 @@ KvAttnPlan kv4_attn_plan(int batch, int heads, int ratio, int groups, int max_q,
     const int64_t most = ((int64_t)sinks + window + max_q) / kKvBlock + 3;
     blocks = blocks < most ? blocks : most;
   }
-  // Parts are counted in 31 bits; a tile longer than total / parts is cut, so
-  // there are at most `parts` cuts beyond one part a tile. Aiming a little lower
-  // leaves room for the tiles' last parts, so that most launches run at once.
-  const bool cut = p.tiles <= VBQ_KV4_COUNTERS && blocks > 4 * kWaves && p.tiles * blocks < INT32_MAX - 65536;
-  p.parts = cut ? (int32_t)(kParts - (p.tiles < kParts ? p.tiles : kParts) / 2) : 0;
+  // Tiles longer than total / parts are cut, so there are at most `parts` parts
+  // beyond one a tile, and on average half a part a tile: the aim leaves room
+  // for those where two workgroups fit a CU, so that all run at once.
+  const bool cut = p.tiles <= VBQ_KV4_COUNTERS && blocks > (p.tiles < 256 ? 5 : 12) * kWaves &&
+                   p.tiles * blocks < INT32_MAX - 65536;
+  const int spare = groups <= 2 && p.rows <= 8 ? 0 : (int)(p.tiles < kParts ? p.tiles : kParts) / 2;
+  p.parts = cut ? kParts - spare : 0;
   p.grid = cut ? p.parts + p.tiles : p.tiles;
   return p;
 }
@@ -1265,9 +1276,9 @@ hipError_t launch_kv4_attention(const KvAttn& a, const KvAttnPlan& p, int batch,
   if (p.grid > INT32_MAX) return hipErrorNotSupported;
   const dim3 grid((uint32_t)p.grid);
 #define VBQ_CALL(G, ROWS, ST) k_kv4_attn<G, ROWS, ST><<<grid, 64 * kWaves, 0, s>>>(a)
-#define VBQ_CALL2(G, ST)                                                                \
-  if (p.rows == 4) VBQ_CALL(G, 4, ST);                                                  \
-  else if (p.rows == 8) VBQ_CALL(G, 8, ST);                                             \
+#define VBQ_CALL2(G, FEW, ST)                                                           \
+  if (p.rows == 4) VBQ_CALL(G, 4, FEW);                                                 \
+  else if (p.rows == 8) VBQ_CALL(G, 8, FEW);                                            \
   else if (p.rows == 16) VBQ_CALL(G, 16, ST);                                           \
   else VBQ_CALL(G, 32, ST)
 #define VBQ_TILE(G, NT2)                                              \
@@ -1283,10 +1294,10 @@ hipError_t launch_kv4_attention(const KvAttn& a, const KvAttnPlan& p, int batch,
     return hipGetLastError();
   }
   switch (a.cache.groups) {
-    case 1: VBQ_CALL2(1, 4); break;
-    case 2: VBQ_CALL2(2, 4); break;
-    case 3: VBQ_CALL2(3, 2); break;
-    default: VBQ_CALL2(4, 2); break;
+    case 1: VBQ_CALL2(1, 4, 4); break;
+    case 2: VBQ_CALL2(2, 2, 4); break;
+    case 3: VBQ_CALL2(3, 2, 2); break;
+    default: VBQ_CALL2(4, 2, 2); break;
   }
 #undef VBQ_CALL2
 #undef VBQ_CALL
