@@ -1,16 +1,27 @@
 // The 4-bit key/value cache: quantising tokens as they are written, and
 // reading them back. The layout and the quantiser are stated in vbq.h.
 //
-// One wavefront takes eight consecutive tokens (an octet: the tokens whose
-// value codes share words) of one head. Lane l = token + 8 * e holds channels
-// 8e .. 8e+7 of each group of one token: 16 bytes of fp16 per load, a group's
-// minimum and maximum over three exchanges (lanes 8, 16, 32 apart), and one
-// word of eight codes. For keys that word is a word of the cache; for values
+// Writing. One wavefront takes eight consecutive tokens (an octet: the tokens
+// whose value codes share words) of one head. Lane l = token + 8 * e holds
+// channels 8e .. 8e+7 of each group of one token: 16 bytes of fp16 per load, a
+// group's minimum and maximum over three exchanges (lanes 8, 16, 32 apart), and
+// one word of eight codes. For keys that word is a word of the cache; for values
 // the eight lanes of a channel octet transpose their 8x8 nibbles in three
 // exchanges (lanes 1, 2, 4 apart) and each then holds eight tokens of one
 // channel, a word of the cache. Words of an octet that is not written whole
 // keep the other tokens' nibbles (one wavefront owns an octet, so the read and
 // the write do not race).
+//   The arithmetic bounds it (HBM would take 26 us for 25000 tokens of 8 heads
+// of 128, both ways): a correctly rounded quotient a value made it 56 us. Codes
+// are decided by t = (w - o) * rcp(s): rcp is within 2^-23 and the product
+// within 2^-24, so t is within 16 * 2^-22 = 2^-18 of the correctly rounded
+// quotient where a code hangs on it (t < 16), and only a t within 2^-16 of a
+// tie takes the division (one wavefront's group in 60).
+//
+// Reading. One wavefront takes a block of 32 tokens of one head, 16 bytes a lane
+// as they lie, so the look-ups are paid once for 32 tokens and nothing moves
+// between lanes: a key word is eight channels of a token, the four value words
+// of a lane four channels of eight tokens.
 #include "kv4.h"
 
 namespace vbq {
@@ -47,52 +58,60 @@ __device__ inline uint32_t bf16_bits(float v) {   // round to nearest even; v is
   return (u + 0x7FFFu + ((u >> 16) & 1u)) >> 16;
 }
 
-template <int DT>
-__device__ inline void store8(void* base, int64_t elem, const float (&x)[8]) {
-  if constexpr (DT == VBQ_F32) {
-    float4* p = reinterpret_cast<float4*>(static_cast<float*>(base) + elem);
-    p[0] = make_float4(x[0], x[1], x[2], x[3]);
-    p[1] = make_float4(x[4], x[5], x[6], x[7]);
-  } else {
-    u32x4 w;
-#pragma unroll
-    for (int i = 0; i < 4; ++i) {
-      if constexpr (DT == VBQ_F16) {
-        const half2_t h = {(_Float16)x[2 * i], (_Float16)x[2 * i + 1]};
-        w[i] = __builtin_bit_cast(uint32_t, h);
-      } else {
-        w[i] = bf16_bits(x[2 * i]) | (bf16_bits(x[2 * i + 1]) << 16);
-      }
-    }
-    *reinterpret_cast<u32x4*>(static_cast<uint16_t*>(base) + elem) = w;
-  }
+template <int CTRL>
+__device__ inline uint32_t dpp(uint32_t v) {
+  return (uint32_t)__builtin_amdgcn_update_dpp(0, (int)v, CTRL, 0xF, 0xF, true);
 }
+constexpr int kXor1 = 0xB1, kXor2 = 0x4E, kXor3 = 0x1B, kXor7 = 0x141, kXor8 = 0x128;
 
 // Transposes the 8x8 nibbles that eight lanes (tok = 0..7) hold: nibble n of
 // lane t becomes nibble t of lane n.
 __device__ inline uint32_t transpose8(uint32_t w, uint32_t tok) {
-  const uint32_t p1 = (uint32_t)__shfl_xor((int)w, 1, 64);
+  const uint32_t p1 = dpp<kXor1>(w);
   w = (tok & 1u) ? ((w & 0xF0F0F0F0u) | ((p1 >> 4) & 0x0F0F0F0Fu)) : ((w & 0x0F0F0F0Fu) | ((p1 << 4) & 0xF0F0F0F0u));
-  const uint32_t p2 = (uint32_t)__shfl_xor((int)w, 2, 64);
+  const uint32_t p2 = dpp<kXor2>(w);
   w = (tok & 2u) ? ((w & 0xFF00FF00u) | ((p2 >> 8) & 0x00FF00FFu)) : ((w & 0x00FF00FFu) | ((p2 << 8) & 0xFF00FF00u));
-  const uint32_t p4 = (uint32_t)__shfl_xor((int)w, 4, 64);
+  const uint32_t p4 = dpp<kXor3>(dpp<kXor7>(w));
   return (tok & 4u) ? ((w & 0xFFFF0000u) | (p4 >> 16)) : ((w & 0x0000FFFFu) | (p4 << 16));
+}
+
+// Minimum and maximum over the lanes 8, 16 and 32 apart.
+__device__ inline float as_float(uint32_t u) { return __builtin_bit_cast(float, u); }
+__device__ inline uint32_t as_bits(float v) { return __builtin_bit_cast(uint32_t, v); }
+__device__ inline void spread_min_max(float& lo, float& hi) {
+  typedef uint32_t pair_t __attribute__((ext_vector_type(2)));
+  lo = fminf(lo, as_float(dpp<kXor8>(as_bits(lo))));
+  hi = fmaxf(hi, as_float(dpp<kXor8>(as_bits(hi))));
+  pair_t p = __builtin_amdgcn_permlane16_swap(as_bits(lo), as_bits(lo), false, false);
+  pair_t q = __builtin_amdgcn_permlane16_swap(as_bits(hi), as_bits(hi), false, false);
+  uint32_t p0 = p.x, p1 = p.y, q0 = q.x, q1 = q.y;
+  lo = fminf(as_float(p0), as_float(p1));
+  hi = fmaxf(as_float(q0), as_float(q1));
+  p = __builtin_amdgcn_permlane32_swap(as_bits(lo), as_bits(lo), false, false);
+  q = __builtin_amdgcn_permlane32_swap(as_bits(hi), as_bits(hi), false, false);
+  p0 = p.x, p1 = p.y, q0 = q.x, q1 = q.y;
+  lo = fminf(as_float(p0), as_float(p1));
+  hi = fmaxf(as_float(q0), as_float(q1));
 }
 
 // One octet of one head of one sequence.
 struct Octet {
   int32_t row0;      // tensor row of the octet's token 0 (may lie before the range)
-  uint32_t valid;    // bit t: token t is in the range and its place exists
-  uint32_t wanted;   // bit t: token t is in the range
-  uint8_t* block;    // null: no page
+  uint32_t valid;    // bit t: token t is in the range
+  uint8_t* block;
   uint32_t oct;      // octet in the block, 0..3
 };
+
+// Numbers of a sequence that fit the call.
+__device__ inline bool range_fits(const KvRange& r, int32_t c0, int64_t n, int32_t c1, int32_t s0) {
+  return c0 >= 0 && n >= 0 && c1 <= r.total && n <= r.max_tokens && s0 >= 0 && s0 <= INT32_MAX - 64 - n;
+}
 
 __device__ inline bool find_octet(const KvCache& c, const KvRange& r, int G, int b, int64_t o, int head, bool report,
                                   Octet& t) {
   const int32_t c0 = r.cu[b], c1 = r.cu[b + 1], s0 = r.start[b];
   const int64_t n = (int64_t)c1 - c0;
-  if (c0 < 0 || n < 0 || c1 > r.total || n > r.max_tokens || s0 < 0 || s0 > INT32_MAX - n) {
+  if (!range_fits(r, c0, n, c1, s0)) {
     if (report) kv_flag(c, VBQ_KV4_FLAG_LENGTH);
     return false;
   }
@@ -101,22 +120,18 @@ __device__ inline bool find_octet(const KvCache& c, const KvRange& r, int G, int
   const int lo = first < s0 ? (int)(s0 - first) : 0;
   const int64_t left = (int64_t)s0 + n - first;
   const int hi = left < 8 ? (int)left : 8;
-  t.wanted = (uint32_t)((1u << hi) - (1u << lo)) & 0xFFu;
-  t.valid = t.wanted;
+  t.valid = (uint32_t)((1u << hi) - (1u << lo)) & 0xFFu;
   t.row0 = (int32_t)(c0 + (first - s0));
   t.oct = (uint32_t)(first >> 3) & 3u;
-  t.block = nullptr;
   const int64_t blk = first >> 5, entry = blk >> c.block_shift;
   if (entry >= r.width) {
     if (report) kv_flag(c, VBQ_KV4_FLAG_LENGTH);
-    t.valid = 0;
-    return true;
+    return false;
   }
   const int32_t page = r.table[(int64_t)b * r.width + entry];
   if ((uint32_t)page >= (uint32_t)c.n_pages) {
     if (report) kv_flag(c, VBQ_KV4_FLAG_PAGE);
-    t.valid = 0;
-    return true;
+    return false;
   }
   t.block = kv_block(c, G, (uint32_t)page, head, (uint32_t)blk & ((1u << c.block_shift) - 1u));
   return true;
@@ -131,7 +146,7 @@ __global__ __launch_bounds__(256) void k_kv4_append(KvCache c, KvRange r, const 
   const int head = (int)(task - o * c.heads);
   if (o >= octets) return;
   Octet t;
-  if (!find_octet(c, r, G, blockIdx.y, o, head, lane == 0, t) || !t.valid) return;
+  if (!find_octet(c, r, G, blockIdx.y, o, head, lane == 0, t)) return;
   const bool mine = (t.valid >> tok) & 1u;
   float x[2][G][8];
 #pragma unroll
@@ -158,32 +173,50 @@ __global__ __launch_bounds__(256) void k_kv4_append(KvCache c, KvRange r, const 
 #pragma unroll
     for (int g = 0; g < G; ++g) {
       float(&w)[8] = x[kv][g];
+      float lo = fminf(fminf(w[0], w[1]), w[2]), hi = fmaxf(fmaxf(w[0], w[1]), w[2]);
+      lo = fminf(fminf(lo, w[3]), w[4]);
+      hi = fmaxf(fmaxf(hi, w[3]), w[4]);
+      lo = fminf(fminf(lo, w[5]), w[6]);
+      hi = fmaxf(fmaxf(hi, w[5]), w[6]);
+      lo = fminf(lo, w[7]);
+      hi = fmaxf(hi, w[7]);
+      // NaN, or beyond the clamp: rare, so put right afterwards
+      const bool odd = __builtin_isunordered(w[0], w[1]) | __builtin_isunordered(w[2], w[3]) |
+                       __builtin_isunordered(w[4], w[5]) | __builtin_isunordered(w[6], w[7]) | (lo < -kClamp) |
+                       (hi > kClamp);
+      if (__any(odd)) {
+        lo = kClamp;
+        hi = -kClamp;
 #pragma unroll
-      for (int i = 0; i < 8; ++i) {
-        const bool bad = w[i] != w[i];
-        nan |= bad;
-        w[i] = bad ? 0.f : fminf(fmaxf(w[i], -kClamp), kClamp);
+        for (int i = 0; i < 8; ++i) {
+          const bool bad = w[i] != w[i];
+          nan |= bad;
+          w[i] = bad ? 0.f : fminf(fmaxf(w[i], -kClamp), kClamp);
+          lo = fminf(lo, w[i]);
+          hi = fmaxf(hi, w[i]);
+        }
       }
-      float lo = w[0], hi = w[0];
-#pragma unroll
-      for (int i = 1; i < 8; ++i) {
-        lo = fminf(lo, w[i]);
-        hi = fmaxf(hi, w[i]);
-      }
-#pragma unroll
-      for (int d = 8; d < 64; d <<= 1) {
-        lo = fminf(lo, __shfl_xor(lo, d, 64));
-        hi = fmaxf(hi, __shfl_xor(hi, d, 64));
-      }
+      spread_min_max(lo, hi);
       const _Float16 s16 = (_Float16)__fdiv_rn(__fsub_rn(hi, lo), 15.f);
       const _Float16 o16 = (_Float16)lo;
       const float s = (float)s16, of = (float)o16;
-      uint32_t word = 0;
+      const float r = s != 0.f ? __builtin_amdgcn_rcpf(s) : 0.f;
+      float q[8], off = 0.f;
 #pragma unroll
       for (int i = 0; i < 8; ++i) {
-        const float q = s != 0.f ? fminf(fmaxf(rintf(__fdiv_rn(__fsub_rn(w[i], of), s)), 0.f), 15.f) : 0.f;
-        word |= (uint32_t)q << (4 * i);
+        const float u = __builtin_amdgcn_fmed3f(__fmul_rn(__fsub_rn(w[i], of), r), 0.f, 15.f);
+        q[i] = rintf(u);
+        off = fmaxf(off, fabsf(__fsub_rn(u, q[i])));
       }
+      if (__any(off > 0.5f - 0x1p-16f)) {
+#pragma unroll
+        for (int i = 0; i < 8; ++i)
+          q[i] = s != 0.f ? __builtin_amdgcn_fmed3f(rintf(__fdiv_rn(__fsub_rn(w[i], of), s)), 0.f, 15.f) : 0.f;
+      }
+      // four codes a half, exact as a float
+      const float h0 = __builtin_fmaf(q[3], 4096.f, __builtin_fmaf(q[2], 256.f, __builtin_fmaf(q[1], 16.f, q[0])));
+      const float h1 = __builtin_fmaf(q[7], 4096.f, __builtin_fmaf(q[6], 256.f, __builtin_fmaf(q[5], 16.f, q[4])));
+      const uint32_t word = (uint32_t)h0 | ((uint32_t)h1 << 16);
       _Float16* so = reinterpret_cast<_Float16*>(t.block + (kv ? kv_value_so(G) : kv_key_so(G)) + 128 * g);
       const uint32_t place = 8 * t.oct + (kv ? 2 * (tok & 3u) + (tok >> 2) : tok);
       if (mine && e == 0) {
@@ -200,58 +233,123 @@ __global__ __launch_bounds__(256) void k_kv4_append(KvCache c, KvRange r, const 
   if (__ballot(nan && mine) && lane == 0) kv_flag(c, VBQ_KV4_FLAG_NAN);
 }
 
-template <int G, int DT>
-__global__ __launch_bounds__(256) void k_kv4_read(KvCache c, KvRange r, void* k, void* v, int64_t octets) {
-  const uint32_t lane = threadIdx.x & 63u, tok = lane & 7u, e = lane >> 3;
-  const int64_t task = (int64_t)blockIdx.x * 4 + __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
-  const int64_t o = task / c.heads;
-  const int head = (int)(task - o * c.heads);
-  if (o >= octets) return;
-  Octet t;
-  if (!find_octet(c, r, G, blockIdx.y, o, head, lane == 0, t)) return;
-  const bool mine = (t.wanted >> tok) & 1u;
-  const bool held = t.valid != 0;
-  uint32_t word[2][G];
-  _Float16 s16[2][G], o16[2][G];
+// N neighbouring channels of a row, rounded once.
+template <int DT, int N>
+__device__ inline void store_row(void* base, int64_t elem, const float (&x)[N]) {
+  if constexpr (DT == VBQ_F32) {
+    float4* p = reinterpret_cast<float4*>(static_cast<float*>(base) + elem);
 #pragma unroll
-  for (int kv = 0; kv < 2; ++kv)
+    for (int i = 0; i < N / 4; ++i) p[i] = make_float4(x[4 * i], x[4 * i + 1], x[4 * i + 2], x[4 * i + 3]);
+  } else {
+    uint32_t w[N / 2];
 #pragma unroll
-    for (int g = 0; g < G; ++g) {
-      word[kv][g] = 0;
-      s16[kv][g] = o16[kv][g] = (_Float16)0.f;
-      if (!held || !(kv ? v : k)) continue;
-      const uint32_t* w = reinterpret_cast<const uint32_t*>(t.block + (kv ? kv_value_codes(G) : 0)) + 256 * g;
-      word[kv][g] = kv ? w[64 * t.oct + 8 * e + tok]
-                       : w[4 * (16 * (e & 3u) + 4 * t.oct + (tok & 3u)) + 2 * (tok >> 2) + (e >> 2)];
-      const _Float16* so =
-          reinterpret_cast<const _Float16*>(t.block + (kv ? kv_value_so(G) : kv_key_so(G)) + 128 * g);
-      const uint32_t place = 8 * t.oct + (kv ? 2 * (tok & 3u) + (tok >> 2) : tok);
-      s16[kv][g] = so[place];
-      o16[kv][g] = so[place + 32];
+    for (int i = 0; i < N / 2; ++i) {
+      if constexpr (DT == VBQ_F16) {
+        const half2_t h = {(_Float16)x[2 * i], (_Float16)x[2 * i + 1]};
+        w[i] = __builtin_bit_cast(uint32_t, h);
+      } else {
+        w[i] = bf16_bits(x[2 * i]) | (bf16_bits(x[2 * i + 1]) << 16);
+      }
     }
-#pragma unroll
-  for (int kv = 0; kv < 2; ++kv) {
-    void* const out = kv ? v : k;
-    if (!out) continue;
-#pragma unroll
-    for (int g = 0; g < G; ++g) {
-      const uint32_t w = kv ? transpose8(word[kv][g], tok) : word[kv][g];
-      const float s = (float)s16[kv][g], of = (float)o16[kv][g];
-      float x[8];
-#pragma unroll
-      for (int i = 0; i < 8; ++i) x[i] = __fadd_rn(__fmul_rn(s, (float)((w >> (4 * i)) & 15u)), of);
-      if (mine) store8<DT>(out, ((int64_t)(t.row0 + (int)tok) * c.heads + head) * (64 * G) + 64 * g + 8 * e, x);
-    }
+    uint16_t* const p = static_cast<uint16_t*>(base) + elem;
+    if constexpr (N == 8) *reinterpret_cast<u32x4*>(p) = u32x4{w[0], w[1], w[2], w[3]};
+    else *reinterpret_cast<u32x2*>(p) = u32x2{w[0], w[1]};
   }
 }
 
-// Octets that a sequence of max_tokens tokens can touch, and the grid over
-// (octet, head) and sequences; no launch when there is nothing to do.
-bool octet_grid(const KvCache& c, const KvRange& r, int64_t* octets, dim3* grid, hipError_t* err) {
+template <int G, int DT>
+__global__ __launch_bounds__(256) void k_kv4_read(KvCache c, KvRange r, void* k, void* v, int64_t blocks) {
+  const uint32_t lane = threadIdx.x & 63u, m = lane & 15u, kq = lane >> 4;
+  const int64_t task = (int64_t)blockIdx.x * 4 + __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+  const int64_t o = task / c.heads;
+  const int head = (int)(task - o * c.heads);
+  if (o >= blocks) return;
+  const int b = (int)blockIdx.y;
+  const int32_t c0 = r.cu[b], c1 = r.cu[b + 1], s0 = r.start[b];
+  const int64_t n = (int64_t)c1 - c0;
+  if (!range_fits(r, c0, n, c1, s0)) {
+    if (lane == 0) kv_flag(c, VBQ_KV4_FLAG_LENGTH);
+    return;
+  }
+  const int64_t blk = (s0 >> 5) + o, first = blk * 32;   // the block's first position
+  if (n == 0 || first >= (int64_t)s0 + n) return;
+  // tokens t of the block with from <= t < to are wanted; token t is row row0 + t
+  const int from = first < s0 ? (int)(s0 - first) : 0;
+  const int to = (int)((int64_t)s0 + n - first < 32 ? (int64_t)s0 + n - first : 32);
+  const int64_t row0 = c0 + (first - s0);
+  const int64_t entry = blk >> c.block_shift;
+  int32_t page = -1;
+  if (entry >= r.width) {
+    if (lane == 0) kv_flag(c, VBQ_KV4_FLAG_LENGTH);
+  } else {
+    page = r.table[(int64_t)b * r.width + entry];
+    if ((uint32_t)page >= (uint32_t)c.n_pages) {
+      if (lane == 0) kv_flag(c, VBQ_KV4_FLAG_PAGE);
+      page = -1;
+    }
+  }
+  const uint8_t* const p =
+      kv_block(c, G, page < 0 ? 0u : (uint32_t)page, head, (uint32_t)blk & ((1u << c.block_shift) - 1u));
+  u32x4 kw[G], vw[G], vs[G], vo[G];
+  _Float16 ks[G][2], ko[G][2];
+  const uint32_t tok = 8 * (m >> 2) + (m & 3u);   // of the key words' first half; + 4 for the second
+#pragma unroll
+  for (int g = 0; g < G; ++g) {
+    kw[g] = *reinterpret_cast<const u32x4*>(p + 1024 * g + 16 * lane);
+    vw[g] = *reinterpret_cast<const u32x4*>(p + kv_value_codes(G) + 1024 * g + 16 * lane);
+    const _Float16* const so = reinterpret_cast<const _Float16*>(p + kv_key_so(G) + 128 * g);
+#pragma unroll
+    for (int u = 0; u < 2; ++u) {
+      ks[g][u] = so[tok + 4 * u];
+      ko[g][u] = so[32 + tok + 4 * u];
+    }
+    vs[g] = *reinterpret_cast<const u32x4*>(p + kv_value_so(G) + 128 * g + 16 * kq);
+    vo[g] = *reinterpret_cast<const u32x4*>(p + kv_value_so(G) + 128 * g + 64 + 16 * kq);
+  }
+  const int64_t row_elems = (int64_t)c.heads * (64 * G);
+  if (k) {
+#pragma unroll
+    for (int g = 0; g < G; ++g)
+#pragma unroll
+      for (int u = 0; u < 2; ++u) {
+        const int t = (int)tok + 4 * u;
+        if (t < from || t >= to) continue;
+#pragma unroll
+        for (int st = 0; st < 2; ++st) {
+          const uint32_t w = kw[g][2 * u + st];
+          const float s = (float)ks[g][u], of = (float)ko[g][u];
+          float x[8];
+#pragma unroll
+          for (int i = 0; i < 8; ++i) x[i] = page < 0 ? 0.f : __builtin_fmaf(s, (float)((w >> (4 * i)) & 15u), of);
+          store_row<DT, 8>(k, (row0 + t) * row_elems + head * (64 * G) + 64 * g + 32 * st + 8 * kq, x);
+        }
+      }
+  }
+  if (v) {
+#pragma unroll
+    for (int g = 0; g < G; ++g)
+#pragma unroll
+      for (int n8 = 0; n8 < 8; ++n8) {   // token 8 kq + n8: scale at half n8 / 4 of pair n8 % 4
+        const int t = 8 * (int)kq + n8;
+        if (t < from || t >= to) continue;
+        const uint32_t sw = vs[g][n8 & 3], ow = vo[g][n8 & 3];
+        const half2_t sp = __builtin_bit_cast(half2_t, sw), op = __builtin_bit_cast(half2_t, ow);
+        const float s = (float)(n8 < 4 ? sp.x : sp.y), of = (float)(n8 < 4 ? op.x : op.y);
+        float x[4];
+#pragma unroll
+        for (int i = 0; i < 4; ++i) x[i] = page < 0 ? 0.f : __builtin_fmaf(s, (float)((vw[g][i] >> (4 * n8)) & 15u), of);
+        store_row<DT, 4>(v, (row0 + t) * row_elems + head * (64 * G) + 64 * g + 4 * m, x);
+      }
+  }
+}
+
+// Units of `size` tokens that a sequence of max_tokens tokens can touch, and the
+// grid over (unit, head) and sequences; no launch when there is nothing to do.
+bool token_grid(const KvCache& c, const KvRange& r, int size, int64_t* units, dim3* grid, hipError_t* err) {
   *err = hipSuccess;
   if (r.max_tokens == 0 || r.total == 0) return false;
-  *octets = ((int64_t)r.max_tokens + 14) / 8;
-  const int64_t wgs = (*octets * c.heads + 3) / 4;
+  *units = ((int64_t)r.max_tokens + 2 * size - 2) / size;
+  const int64_t wgs = (*units * c.heads + 3) / 4;
   if (wgs > INT32_MAX) {
     *err = hipErrorNotSupported;
     return false;
@@ -276,22 +374,22 @@ bool octet_grid(const KvCache& c, const KvRange& r, int64_t* octets, dim3* grid,
 
 hipError_t launch_kv4_append(const KvCache& c, const KvRange& r, const void* k, const void* v, int dtype,
                              int64_t k_ts, int64_t k_hs, int64_t v_ts, int64_t v_hs, hipStream_t s) {
-  int64_t octets;
+  int64_t units;
   dim3 grid;
   hipError_t err;
-  if (!octet_grid(c, r, &octets, &grid, &err)) return err;
-#define VBQ_CALL(G, DT) k_kv4_append<G, DT><<<grid, 256, 0, s>>>(c, r, k, v, k_ts, k_hs, v_ts, v_hs, octets)
+  if (!token_grid(c, r, 8, &units, &grid, &err)) return err;
+#define VBQ_CALL(G, DT) k_kv4_append<G, DT><<<grid, 256, 0, s>>>(c, r, k, v, k_ts, k_hs, v_ts, v_hs, units)
   VBQ_KV4_BY_TYPE(VBQ_CALL)
 #undef VBQ_CALL
   return hipGetLastError();
 }
 
 hipError_t launch_kv4_read(const KvCache& c, const KvRange& r, void* k, void* v, int dtype, hipStream_t s) {
-  int64_t octets;
+  int64_t units;
   dim3 grid;
   hipError_t err;
-  if (!octet_grid(c, r, &octets, &grid, &err)) return err;
-#define VBQ_CALL(G, DT) k_kv4_read<G, DT><<<grid, 256, 0, s>>>(c, r, k, v, octets)
+  if (!token_grid(c, r, 32, &units, &grid, &err)) return err;
+#define VBQ_CALL(G, DT) k_kv4_read<G, DT><<<grid, 256, 0, s>>>(c, r, k, v, units)
   VBQ_KV4_BY_TYPE(VBQ_CALL)
 #undef VBQ_CALL
   return hipGetLastError();
