@@ -301,7 +301,7 @@ vbq_status cell_drift_bound(const vbq_matrix* m, const uint16_t* x, int32_t B, f
  *
  * Quantiser, in binary32 without contraction:
  *   w' = w is NaN ? 0 : clamp(w, -61440, 61440); lo = min, hi = max of the group;
- *   scale16 = fp16(f32(hi - lo) / 15); offset16 = fp16(lo); s, o = those values;
+ *   scale16 = fp16(f32(hi - lo) * f32(1/15)); offset16 = fp16(lo); s, o = those values;
  *   q = s == 0 ? 0 : clamp(rint(f32(w' - o) / s), 0, 15)       (ties to even)
  * and the value held is f32(s*q) + o. With the clamp s <= 8192, so every value
  * held is a finite number that fp16 can round to: a cache written by kv4_append

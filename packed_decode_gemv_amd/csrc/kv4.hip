@@ -53,10 +53,7 @@ __device__ inline void load8(const void* base, int64_t elem, float (&x)[8]) {
   }
 }
 
-__device__ inline uint32_t bf16_bits(float v) {   // round to nearest even; v is finite
-  const uint32_t u = __builtin_bit_cast(uint32_t, v);
-  return (u + 0x7FFFu + ((u >> 16) & 1u)) >> 16;
-}
+typedef __bf16 bf2_t __attribute__((ext_vector_type(2)));
 
 template <int CTRL>
 __device__ inline uint32_t dpp(uint32_t v) {
@@ -197,18 +194,19 @@ __global__ __launch_bounds__(256) void k_kv4_append(KvCache c, KvRange r, const 
         }
       }
       spread_min_max(lo, hi);
-      const _Float16 s16 = (_Float16)__fdiv_rn(__fsub_rn(hi, lo), 15.f);
+      const _Float16 s16 = (_Float16)__fmul_rn(__fsub_rn(hi, lo), 1.f / 15.f);
       const _Float16 o16 = (_Float16)lo;
       const float s = (float)s16, of = (float)o16;
       const float r = s != 0.f ? __builtin_amdgcn_rcpf(s) : 0.f;
-      float q[8], off = 0.f;
+      float q[8];
+      uint32_t off = 0;   // largest |t - q| (of bits: they order like the numbers)
 #pragma unroll
       for (int i = 0; i < 8; ++i) {
         const float u = __builtin_amdgcn_fmed3f(__fmul_rn(__fsub_rn(w[i], of), r), 0.f, 15.f);
         q[i] = rintf(u);
-        off = fmaxf(off, fabsf(__fsub_rn(u, q[i])));
+        off = max(off, as_bits(__fsub_rn(u, q[i])) << 1);
       }
-      if (__any(off > 0.5f - 0x1p-16f)) {
+      if (__any(off > (as_bits(0.5f - 0x1p-16f) << 1))) {
 #pragma unroll
         for (int i = 0; i < 8; ++i)
           q[i] = s != 0.f ? __builtin_amdgcn_fmed3f(rintf(__fdiv_rn(__fsub_rn(w[i], of), s)), 0.f, 15.f) : 0.f;
@@ -248,7 +246,8 @@ __device__ inline void store_row(void* base, int64_t elem, const float (&x)[N]) 
         const half2_t h = {(_Float16)x[2 * i], (_Float16)x[2 * i + 1]};
         w[i] = __builtin_bit_cast(uint32_t, h);
       } else {
-        w[i] = bf16_bits(x[2 * i]) | (bf16_bits(x[2 * i + 1]) << 16);
+        const bf2_t h = {(__bf16)x[2 * i], (__bf16)x[2 * i + 1]};
+        w[i] = __builtin_bit_cast(uint32_t, h);
       }
     }
     uint16_t* const p = static_cast<uint16_t*>(base) + elem;

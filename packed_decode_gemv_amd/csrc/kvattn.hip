@@ -175,18 +175,18 @@ constexpr float kLn2 = 0.693147180559945309f;
 
 // Four neighbouring outputs, rounded once to the output type.
 __device__ inline void store4(const KvAttn& a, int64_t elem, const f32x4& v) {
-  uint32_t w[4];
-#pragma unroll
-  for (int i = 0; i < 4; ++i) {
-    const float f = v[i];
-    if (a.bf16) {
-      const uint32_t u = __builtin_bit_cast(uint32_t, f);
-      w[i] = f != f ? 0x7FC0u : (u + 0x7FFFu + ((u >> 16) & 1u)) >> 16;
-    } else {
-      w[i] = __builtin_bit_cast(uint16_t, (_Float16)f);
-    }
+  uint32_t lo, hi;
+  if (a.bf16) {
+    typedef __bf16 bf2_t __attribute__((ext_vector_type(2)));
+    const bf2_t x = {(__bf16)v[0], (__bf16)v[1]}, y = {(__bf16)v[2], (__bf16)v[3]};
+    lo = __builtin_bit_cast(uint32_t, x);
+    hi = __builtin_bit_cast(uint32_t, y);
+  } else {
+    const half2_t x = {(_Float16)v[0], (_Float16)v[1]}, y = {(_Float16)v[2], (_Float16)v[3]};
+    lo = __builtin_bit_cast(uint32_t, x);
+    hi = __builtin_bit_cast(uint32_t, y);
   }
-  *reinterpret_cast<u32x2*>(a.out + elem) = u32x2{w[0] | (w[1] << 16), w[2] | (w[3] << 16)};
+  *reinterpret_cast<u32x2*>(a.out + elem) = u32x2{lo, hi};
 }
 
 // Two numbers to and from other workgroups: device-scope accesses, past the
@@ -882,9 +882,9 @@ __device__ inline float half_sum(float v) {
   return __builtin_bit_cast(float, x) + __builtin_bit_cast(float, y);
 }
 
-template <int G, int NT>
-__global__ __launch_bounds__(256, G >= 3 || NT == 2 ? 1 : 2) void k_kv4_attn_tile(KvAttn a) {
-  constexpr int WAVES = 4, ROWS = 32 * NT * WAVES, D = 64 * G, BYTES = kKvGroupBytes * G, RAW = 4, TILES = D / 32;
+template <int G, bool FINE>
+__global__ __launch_bounds__(256, G >= 3 ? 1 : 2) void k_kv4_attn_tile(KvAttn a) {
+  constexpr int WAVES = 4, ROWS = 32 * WAVES, D = 64 * G, BYTES = kKvGroupBytes * G, RAW = 4, TILES = D / 32;
   constexpr int SHARE = BYTES / WAVES;   // a wavefront's part of a block's copy
   constexpr int COPIES = (SHARE + 1023) / 1024;
   constexpr int HELD = 32 * D * 2;   // a block's keys, or values
@@ -952,13 +952,12 @@ __global__ __launch_bounds__(256, G >= 3 || NT == 2 ? 1 : 2) void k_kv4_attn_til
   // Queries: B operands, channels of a chunk as pairs; what the lane's row sees.
   for (int i = 0; i < 2; ++i)
     if (i < blocks) start_copy(i);
-  half8_t qf[NT][D / 16], qsum[NT];
-  float to_log2[NT];
-  int hi[NT], lo[NT];
-  const int w_r0 = r0 + 32 * NT * wave;   // the wavefront's first row
-#pragma unroll
-  for (int nt = 0; nt < NT; ++nt) {
-    const int r = w_r0 + 32 * nt + (int)col, qi = r / a.ratio, hh = r - qi * a.ratio;
+  half8_t qf[D / 16], qsum;
+  float to_log2;
+  int hi, lo;
+  const int w_r0 = r0 + 32 * wave;   // the wavefront's first row
+  {
+    const int r = w_r0 + (int)col, qi = r / a.ratio, hh = r - qi * a.ratio;
     u32x4 x[D / 16];
 #pragma unroll
     for (int c = 0; c < D / 16; ++c) {
@@ -996,9 +995,9 @@ __global__ __launch_bounds__(256, G >= 3 || NT == 2 ? 1 : 2) void k_kv4_attn_til
     int ex = (int)(__builtin_bit_cast(uint32_t, top) >> 23) - 127;
     ex = top > 0.f ? max(ex, -100) : 13;
     const float up = ldexpf(1.f, 13 - ex);
-    to_log2[nt] = a.scale_log2 * ldexpf(1.f, ex - 13 + 24);
+    to_log2 = a.scale_log2 * ldexpf(1.f, ex - 13 + 24);
 #pragma unroll
-    for (int j = 0; j < 8; ++j) qsum[nt][j] = (_Float16)0.f;
+    for (int j = 0; j < 8; ++j) qsum[j] = (_Float16)0.f;
 #pragma unroll
     for (int g = 0; g < G; ++g) {
       float sum = 0.f;
@@ -1009,21 +1008,21 @@ __global__ __launch_bounds__(256, G >= 3 || NT == 2 ? 1 : 2) void k_kv4_attn_til
           const _Float16 v0 = (_Float16)(y[c][i] * up), v1 = (_Float16)(y[c][i + 4] * up);
           sum += (float)v0 + (float)v1;
           const _Float16 f = (i & 1) ? (_Float16)0.0625f : (_Float16)1.f;
-          qf[nt][c][2 * i] = v0 * f;
-          qf[nt][c][2 * i + 1] = v1 * f;
+          qf[c][2 * i] = v0 * f;
+          qf[c][2 * i + 1] = v1 * f;
         }
       // the sum as two fp16 numbers, the second times 2^11 (and its offsets by 2^-11)
       sum = half_sum(sum) * 0x1p-24f;
       const _Float16 big = (_Float16)sum;
-      qsum[nt][2 * g] = big;
-      qsum[nt][2 * g + 1] = (_Float16)((sum - (float)big) * 0x1p11f);
+      qsum[2 * g] = big;
+      qsum[2 * g + 1] = (_Float16)((sum - (float)big) * 0x1p11f);
     }
     const int p = a.causal ? first + qi : len - 1;
-    hi[nt] = r < rows ? min(p, len - 1) : -1;
-    lo[nt] = a.window ? p - a.window + 1 : INT32_MIN;
+    hi = r < rows ? min(p, len - 1) : -1;
+    lo = a.window ? p - a.window + 1 : INT32_MIN;
   }
   // this wavefront's first and last positions
-  const int w_r1 = min(rows, w_r0 + 32 * NT);
+  const int w_r1 = min(rows, w_r0 + 32);
   const int w_min = min(a.causal ? first + w_r0 / a.ratio : len - 1, len - 1);
   const int w_max = w_r0 >= rows ? -1 : a.causal ? first + (w_r1 - 1) / a.ratio : len - 1;
 
@@ -1062,7 +1061,7 @@ __global__ __launch_bounds__(256, G >= 3 || NT == 2 ? 1 : 2) void k_kv4_attn_til
   f32x16 none;
 #pragma unroll
   for (int j = 0; j < 16; ++j) none[j] = 0.f;
-  auto scores = [&](int i, f32x16(&x)[NT]) {
+  auto scores = [&](int i, f32x16& x) {
     const uint8_t* const k = keys + (i & 1) * HELD;
     const uint8_t* const so = raw + (i % RAW) * BYTES + kv_key_so(G);
     half8_t off;
@@ -1074,60 +1073,51 @@ __global__ __launch_bounds__(256, G >= 3 || NT == 2 ? 1 : 2) void k_kv4_attn_til
       off[2 * g] = half ? (_Float16)0.f : o;
       off[2 * g + 1] = half ? (_Float16)0.f : o * (_Float16)0x1p-11f;
     }
-#pragma unroll
-    for (int nt = 0; nt < NT; ++nt) x[nt] = __builtin_amdgcn_mfma_f32_32x32x16_f16(off, qsum[nt], none, 0, 0, 0);
+    x = __builtin_amdgcn_mfma_f32_32x32x16_f16(off, qsum, none, 0, 0, 0);
 #pragma unroll
     for (int g = 0; g < G; ++g) {
-      f32x16 d[NT];
+      f32x16 d;
 #pragma unroll
       for (int c = 0; c < 4; ++c) {
         const half8_t kc = __builtin_bit_cast(half8_t, lds16(k + 1024 * (4 * g + c) + 16 * lane));
-#pragma unroll
-        for (int nt = 0; nt < NT; ++nt)
-          d[nt] = __builtin_amdgcn_mfma_f32_32x32x16_f16(kc, qf[nt][4 * g + c], c ? d[nt] : none, 0, 0, 0);
+          d = __builtin_amdgcn_mfma_f32_32x32x16_f16(kc, qf[4 * g + c], c ? d : none, 0, 0, 0);
       }
 #pragma unroll
       for (int A = 0; A < 2; ++A) {
         const Halves<8> s(so + 128 * g + 16 * (2 * A + half));
 #pragma unroll
-        for (int nt = 0; nt < NT; ++nt)
-#pragma unroll
-          for (int j = 0; j < 8; ++j) x[nt][8 * A + j] = __builtin_fmaf(s[j], d[nt][8 * A + j], x[nt][8 * A + j]);
+          for (int j = 0; j < 8; ++j) x[8 * A + j] = __builtin_fmaf(s[j], d[8 * A + j], x[8 * A + j]);
       }
     }
   };
 
-  float m[NT], l[NT], mx[NT];
-  f32x16 acc[NT][TILES];
+  float m, l, mx;
+  f32x16 acc[TILES];
+  {
+    m = kNoMax;
+    l = 0.f;
 #pragma unroll
-  for (int nt = 0; nt < NT; ++nt) {
-    m[nt] = kNoMax;
-    l[nt] = 0.f;
-#pragma unroll
-    for (int t = 0; t < TILES; ++t) acc[nt][t] = none;
+    for (int t = 0; t < TILES; ++t) acc[t] = none;
   }
   // Masks scores of block i; their rows' maxima, and whether one passes its
   // running maximum by more than the slack.
-  auto settle = [&](int i, bool hidden, f32x16(&sc)[NT]) {
+  auto settle = [&](int i, bool hidden, f32x16& sc) {
     const int t0 = block_of(i) * kKvBlock;
     if (hidden || t0 + kKvBlock - 1 > w_min || (a.window && t0 <= w_max - a.window && t0 + kKvBlock > a.sinks)) {
 #pragma unroll
-      for (int nt = 0; nt < NT; ++nt)
-#pragma unroll
         for (int j = 0; j < 16; ++j) {
           const int t = t0 + 8 * (2 * (j >> 3) + (int)half) + (j & 7);
-          const bool see = !hidden && t <= hi[nt] && (t >= lo[nt] || t < a.sinks);
-          sc[nt][j] = see ? sc[nt][j] : -__builtin_inff();
+          const bool see = !hidden && t <= hi && (t >= lo || t < a.sinks);
+          sc[j] = see ? sc[j] : -__builtin_inff();
         }
     }
     bool pass = false;
+    {
+      float top = sc[0];
 #pragma unroll
-    for (int nt = 0; nt < NT; ++nt) {
-      float top = sc[nt][0];
-#pragma unroll
-      for (int j = 1; j < 16; ++j) top = fmaxf(top, sc[nt][j]);
-      mx[nt] = half_max(top) * to_log2[nt];
-      pass |= mx[nt] > m[nt] + kTileSlack;
+      for (int j = 1; j < 16; ++j) top = fmaxf(top, sc[j]);
+      mx = half_max(top) * to_log2;
+      pass |= mx > m + kTileSlack;
     }
     return (bool)__any(pass);
   };
@@ -1155,43 +1145,47 @@ __global__ __launch_bounds__(256, G >= 3 || NT == 2 ? 1 : 2) void k_kv4_attn_til
     arrive(1);
     bool hide = is_gone(0, min(2, blocks - 1));
     if (blocks > 1) spread(1);
-    f32x16 sc[NT];
+    f32x16 sc;
     scores(0, sc);
     settle(0, hide, sc);
     // The inner loop runs while no row's scores pass its running maximum by
     // more than the slack: it has no vector arithmetic on the sums, so they
     // stay in accumulation registers.
     for (int i = 0; i < blocks;) {
+      {
+        const float mt = fmaxf(m, mx), f = __builtin_amdgcn_exp2f(m - mt);
+        m = mt;
+        l *= f;
 #pragma unroll
-      for (int nt = 0; nt < NT; ++nt) {
-        const float mt = fmaxf(m[nt], mx[nt]), f = __builtin_amdgcn_exp2f(m[nt] - mt);
-        m[nt] = mt;
-        l[nt] *= f;
-#pragma unroll
-        for (int t = 0; t < TILES; ++t) acc[nt][t] *= f;
+        for (int t = 0; t < TILES; ++t) acc[t] *= f;
       }
       bool pass = false;
       do {
         arrive(i + 2);
         hide = i + 1 < blocks && is_gone(i + 1, min(i + 4, blocks - 1));
         // (the last turns spread and score what an older block left: unused)
-        f32x16 next[NT];
+        f32x16 next;
         scores(i + 1, next);
-        half8_t pf[NT][2];
+        half8_t pf[2], pl[2];   // probabilities, and what their rounding leaves
         const half2_t ones = {(_Float16)1.f, (_Float16)1.f};
-#pragma unroll
-        for (int nt = 0; nt < NT; ++nt) {
-          const float base = kTileShift - m[nt];
+        {
+          const float base = kTileShift - m;
 #pragma unroll
           for (int A = 0; A < 2; ++A)
 #pragma unroll
             for (int j = 0; j < 4; ++j) {
-              const half2_t pr = {
-                  (_Float16)__builtin_amdgcn_exp2f(__builtin_fmaf(sc[nt][8 * A + j], to_log2[nt], base)),
-                  (_Float16)__builtin_amdgcn_exp2f(__builtin_fmaf(sc[nt][8 * A + 4 + j], to_log2[nt], base))};
-              pf[nt][A][2 * j] = pr.x;
-              pf[nt][A][2 * j + 1] = pr.y;
-              l[nt] = __builtin_amdgcn_fdot2(pr, ones, l[nt], false);   // the sum of what is multiplied
+              const float p0 = __builtin_amdgcn_exp2f(__builtin_fmaf(sc[8 * A + j], to_log2, base));
+              const float p1 = __builtin_amdgcn_exp2f(__builtin_fmaf(sc[8 * A + 4 + j], to_log2, base));
+              const half2_t pr = {(_Float16)p0, (_Float16)p1};
+              pf[A][2 * j] = pr.x;
+              pf[A][2 * j + 1] = pr.y;
+              if constexpr (FINE) {
+                l += p0 + p1;
+                pl[A][2 * j] = (_Float16)(p0 - (float)pr.x);
+                pl[A][2 * j + 1] = (_Float16)(p1 - (float)pr.y);
+              } else {
+                l = __builtin_amdgcn_fdot2(pr, ones, l, false);   // the sum of what is multiplied
+              }
             }
         }
         const uint8_t* const v = vals + (i % 3) * HELD;
@@ -1200,24 +1194,24 @@ __global__ __launch_bounds__(256, G >= 3 || NT == 2 ? 1 : 2) void k_kv4_attn_til
 #pragma unroll
           for (int t = 0; t < TILES; ++t) {
             const half8_t vc = __builtin_bit_cast(half8_t, lds16(v + ((A * TILES + t) * 64 + lane) * 16));
-#pragma unroll
-            for (int nt = 0; nt < NT; ++nt)
-              acc[nt][t] = __builtin_amdgcn_mfma_f32_32x32x16_f16(vc, pf[nt][A], acc[nt][t], 0, 0, 0);
+            {
+              acc[t] = __builtin_amdgcn_mfma_f32_32x32x16_f16(vc, pf[A], acc[t], 0, 0, 0);
+              if constexpr (FINE)
+                acc[t] = __builtin_amdgcn_mfma_f32_32x32x16_f16(vc, pl[A], acc[t], 0, 0, 0);
+            }
           }
         spread(i + 2);
-#pragma unroll
-        for (int nt = 0; nt < NT; ++nt) sc[nt] = next[nt];
+        sc = next;
         ++i;
         if (i < blocks) pass = settle(i, hide, sc);
       } while (i < blocks && !pass);
     }
   }
 
-#pragma unroll
-  for (int nt = 0; nt < NT; ++nt) {
-    const float sum = half_sum(l[nt]);
-    const int r = w_r0 + 32 * nt + (int)col, qi = r / a.ratio, hh = r - qi * a.ratio;
-    if (r >= rows) continue;
+  {
+    const float sum = half_sum(l);
+    const int r = w_r0 + (int)col, qi = r / a.ratio, hh = r - qi * a.ratio;
+    if (r >= rows) return;
     const float inv = sum > 0.f ? 1.f / sum : sum == 0.f ? 0.f : sum;   // 0: nothing seen; NaN stays
     const int64_t o = (int64_t)(sq.c0 + qi) * a.n_heads + head * a.ratio + hh;
 #pragma unroll
@@ -1226,11 +1220,11 @@ __global__ __launch_bounds__(256, G >= 3 || NT == 2 ? 1 : 2) void k_kv4_attn_til
       for (int u = 0; u < 2; ++u)
 #pragma unroll
         for (int bb = 0; bb < 4; ++bb) {
-          const f32x4 v = {acc[nt][2 * g][4 * u + bb], acc[nt][2 * g][8 + 4 * u + bb], acc[nt][2 * g + 1][4 * u + bb],
-                           acc[nt][2 * g + 1][8 + 4 * u + bb]};
+          const f32x4 v = {acc[2 * g][4 * u + bb], acc[2 * g][8 + 4 * u + bb], acc[2 * g + 1][4 * u + bb],
+                           acc[2 * g + 1][8 + 4 * u + bb]};
           store4(a, o * D + 64 * g + 4 * (8 * u + 4 * (int)half + bb), v * inv);
         }
-    if (a.lse && half == 0) a.lse[o] = (__builtin_amdgcn_logf(sum) + m[nt] - kTileShift) * kLn2;
+    if (a.lse && half == 0) a.lse[o] = (__builtin_amdgcn_logf(sum) + m - kTileShift) * kLn2;
   }
 }
 
@@ -1281,15 +1275,15 @@ hipError_t launch_kv4_attention(const KvAttn& a, const KvAttnPlan& p, int batch,
   else if (p.rows == 8) VBQ_CALL(G, 8, FEW);                                            \
   else if (p.rows == 16) VBQ_CALL(G, 16, ST);                                           \
   else VBQ_CALL(G, 32, ST)
-#define VBQ_TILE(G, NT2)                                              \
-  if (p.rows > 128) k_kv4_attn_tile<G, NT2><<<grid, 256, 0, s>>>(a);  \
-  else k_kv4_attn_tile<G, 1><<<grid, 256, 0, s>>>(a)
+#define VBQ_TILE(G)                                              \
+  if (a.bf16) k_kv4_attn_tile<G, false><<<grid, 256, 0, s>>>(a); \
+  else k_kv4_attn_tile<G, true><<<grid, 256, 0, s>>>(a)
   if (p.rows > 32) {
     switch (a.cache.groups) {
-      case 1: VBQ_TILE(1, 2); break;
-      case 2: VBQ_TILE(2, 2); break;
-      case 3: VBQ_TILE(3, 1); break;
-      default: VBQ_TILE(4, 1); break;
+      case 1: VBQ_TILE(1); break;
+      case 2: VBQ_TILE(2); break;
+      case 3: VBQ_TILE(3); break;
+      default: VBQ_TILE(4); break;
     }
     return hipGetLastError();
   }

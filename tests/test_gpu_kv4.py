@@ -27,7 +27,7 @@ def quantise(x):
     x = np.asarray(x, np.float32)
     x = np.where(np.isnan(x), np.float32(0), np.clip(x, -CLAMP, CLAMP)).astype(np.float32)
     lo, hi = x.min(-1), x.max(-1)
-    s = ((hi - lo).astype(np.float32) / np.float32(15)).astype(np.float16)
+    s = ((hi - lo).astype(np.float32) * (np.float32(1) / np.float32(15))).astype(np.float16)
     o = lo.astype(np.float16)
     sf, of = s.astype(np.float32)[..., None], o.astype(np.float32)[..., None]
     with np.errstate(divide="ignore", invalid="ignore"):
