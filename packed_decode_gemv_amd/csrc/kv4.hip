@@ -1,8 +1,9 @@
 // The 4-bit key/value cache: quantising tokens as they are written, and
 // reading them back. The layout and the quantiser are stated in vbq.h.
 //
-// Writing. One wavefront takes eight consecutive tokens (an octet: the tokens
-// whose value codes share words) of one head. Lane l = token + 8 * e holds
+// Writing. A workgroup takes a block of 32 tokens of one head (so that the cache
+// of one die gathers the lines it writes), a wavefront eight of them (an octet:
+// the tokens whose value codes share words). Lane l = token + 8 * e holds
 // channels 8e .. 8e+7 of each group of one token: 16 bytes of fp16 per load, a
 // group's minimum and maximum over three exchanges (lanes 8, 16, 32 apart), and
 // one word of eight codes. For keys that word is a word of the cache; for values
@@ -91,76 +92,63 @@ __device__ inline void spread_min_max(float& lo, float& hi) {
   hi = fmaxf(as_float(q0), as_float(q1));
 }
 
-// One octet of one head of one sequence.
-struct Octet {
-  int32_t row0;      // tensor row of the octet's token 0 (may lie before the range)
-  uint32_t valid;    // bit t: token t is in the range
-  uint8_t* block;
-  uint32_t oct;      // octet in the block, 0..3
-};
-
 // Numbers of a sequence that fit the call.
 __device__ inline bool range_fits(const KvRange& r, int32_t c0, int64_t n, int32_t c1, int32_t s0) {
   return c0 >= 0 && n >= 0 && c1 <= r.total && n <= r.max_tokens && s0 >= 0 && s0 <= INT32_MAX - 64 - n;
 }
 
-__device__ inline bool find_octet(const KvCache& c, const KvRange& r, int G, int b, int64_t o, int head, bool report,
-                                  Octet& t) {
-  const int32_t c0 = r.cu[b], c1 = r.cu[b + 1], s0 = r.start[b];
-  const int64_t n = (int64_t)c1 - c0;
-  if (!range_fits(r, c0, n, c1, s0)) {
-    if (report) kv_flag(c, VBQ_KV4_FLAG_LENGTH);
-    return false;
-  }
-  const int64_t first = ((int64_t)(s0 >> 3) + o) * 8;   // the octet's first position
-  if (n == 0 || first >= (int64_t)s0 + n) return false;
-  const int lo = first < s0 ? (int)(s0 - first) : 0;
-  const int64_t left = (int64_t)s0 + n - first;
-  const int hi = left < 8 ? (int)left : 8;
-  t.valid = (uint32_t)((1u << hi) - (1u << lo)) & 0xFFu;
-  t.row0 = (int32_t)(c0 + (first - s0));
-  t.oct = (uint32_t)(first >> 3) & 3u;
-  const int64_t blk = first >> 5, entry = blk >> c.block_shift;
+// The page of a sequence's block, or -1.
+__device__ inline int32_t find_page(const KvCache& c, const KvRange& r, int b, int32_t blk, bool report) {
+  const int32_t entry = blk >> c.block_shift;
   if (entry >= r.width) {
     if (report) kv_flag(c, VBQ_KV4_FLAG_LENGTH);
-    return false;
+    return -1;
   }
   const int32_t page = r.table[(int64_t)b * r.width + entry];
-  if ((uint32_t)page >= (uint32_t)c.n_pages) {
-    if (report) kv_flag(c, VBQ_KV4_FLAG_PAGE);
-    return false;
-  }
-  t.block = kv_block(c, G, (uint32_t)page, head, (uint32_t)blk & ((1u << c.block_shift) - 1u));
-  return true;
+  if ((uint32_t)page < (uint32_t)c.n_pages) return page;
+  if (report) kv_flag(c, VBQ_KV4_FLAG_PAGE);
+  return -1;
 }
 
 template <int G, int DT>
 __global__ __launch_bounds__(256) void k_kv4_append(KvCache c, KvRange r, const void* k, const void* v, int64_t k_ts,
-                                                    int64_t k_hs, int64_t v_ts, int64_t v_hs, int64_t octets) {
+                                                    int64_t k_hs, int64_t v_ts, int64_t v_hs) {
   const uint32_t lane = threadIdx.x & 63u, tok = lane & 7u, e = lane >> 3;
-  const int64_t task = (int64_t)blockIdx.x * 4 + __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
-  const int64_t o = task / c.heads;
-  const int head = (int)(task - o * c.heads);
-  if (o >= octets) return;
-  Octet t;
-  if (!find_octet(c, r, G, blockIdx.y, o, head, lane == 0, t)) return;
-  const bool mine = (t.valid >> tok) & 1u;
+  const uint32_t oct = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+  const int head = (int)(blockIdx.x % (uint32_t)c.heads), b = (int)blockIdx.y;
+  const int32_t c0 = r.cu[b], c1 = r.cu[b + 1], s0 = r.start[b];
+  const int64_t n = (int64_t)c1 - c0;
+  if (!range_fits(r, c0, n, c1, s0)) {
+    if (threadIdx.x == 0) kv_flag(c, VBQ_KV4_FLAG_LENGTH);
+    return;
+  }
+  // the octet's first position, and its tokens that are in the range
+  const int64_t blk = (s0 >> 5) + (int64_t)(blockIdx.x / (uint32_t)c.heads), first = 32 * blk + 8 * oct;
+  const int64_t ahead = (int64_t)s0 + n - first;
+  if (ahead <= 0 || first + 8 <= s0) return;
+  const int from = first < s0 ? (int)(s0 - first) : 0, to = ahead < 8 ? (int)ahead : 8;
+  const uint32_t valid = (uint32_t)((1u << to) - (1u << from)) & 0xFFu;
+  const int64_t row0 = c0 + (first - s0);
+  const bool mine = (valid >> tok) & 1u;
   float x[2][G][8];
 #pragma unroll
   for (int kv = 0; kv < 2; ++kv)
 #pragma unroll
     for (int g = 0; g < G; ++g) {
-      const int64_t at = (int64_t)(t.row0 + (int)tok) * (kv ? v_ts : k_ts) + head * (kv ? v_hs : k_hs) + 64 * g + 8 * e;
+      const int64_t at = (row0 + tok) * (kv ? v_ts : k_ts) + head * (kv ? v_hs : k_hs) + 64 * g + 8 * e;
       if (mine) load8<DT>(kv ? v : k, at, x[kv][g]);
       else
 #pragma unroll
         for (int i = 0; i < 8; ++i) x[kv][g][i] = 0.f;
     }
+  const int32_t page = find_page(c, r, b, (int32_t)blk, lane == 0);
+  if (page < 0) return;
+  uint8_t* const block = kv_block(c, G, (uint32_t)page, head, (uint32_t)blk & ((1u << c.block_shift) - 1u));
   // Old words of a value octet that is written in part.
   uint32_t keep = 0;   // nibbles that stay
 #pragma unroll
-  for (int i = 0; i < 8; ++i) keep |= ((t.valid >> i) & 1u) ? 0u : 0xFu << (4 * i);
-  uint32_t* const vword = reinterpret_cast<uint32_t*>(t.block + kv_value_codes(G)) + 64 * t.oct + 8 * e + tok;
+  for (int i = 0; i < 8; ++i) keep |= ((valid >> i) & 1u) ? 0u : 0xFu << (4 * i);
+  uint32_t* const vword = reinterpret_cast<uint32_t*>(block + kv_value_codes(G)) + 64 * oct + 8 * e + tok;
   uint32_t old[G];
 #pragma unroll
   for (int g = 0; g < G; ++g) old[g] = keep ? vword[256 * g] : 0u;
@@ -215,15 +203,15 @@ __global__ __launch_bounds__(256) void k_kv4_append(KvCache c, KvRange r, const 
       const float h0 = __builtin_fmaf(q[3], 4096.f, __builtin_fmaf(q[2], 256.f, __builtin_fmaf(q[1], 16.f, q[0])));
       const float h1 = __builtin_fmaf(q[7], 4096.f, __builtin_fmaf(q[6], 256.f, __builtin_fmaf(q[5], 16.f, q[4])));
       const uint32_t word = (uint32_t)h0 | ((uint32_t)h1 << 16);
-      _Float16* so = reinterpret_cast<_Float16*>(t.block + (kv ? kv_value_so(G) : kv_key_so(G)) + 128 * g);
-      const uint32_t place = 8 * t.oct + (kv ? 2 * (tok & 3u) + (tok >> 2) : tok);
+      _Float16* so = reinterpret_cast<_Float16*>(block + (kv ? kv_value_so(G) : kv_key_so(G)) + 128 * g);
+      const uint32_t place = 8 * oct + (kv ? 2 * (tok & 3u) + (tok >> 2) : tok);
       if (mine && e == 0) {
         so[place] = s16;
         so[place + 32] = o16;
       }
       if (kv == 0) {
-        uint32_t* kw = reinterpret_cast<uint32_t*>(t.block) + 256 * g;
-        if (mine) kw[4 * (16 * (e & 3u) + 4 * t.oct + (tok & 3u)) + 2 * (tok >> 2) + (e >> 2)] = word;
+        uint32_t* kw = reinterpret_cast<uint32_t*>(block) + 256 * g;
+        if (mine) kw[4 * (16 * (e & 3u) + 4 * oct + (tok & 3u)) + 2 * (tok >> 2) + (e >> 2)] = word;
       } else {
         vword[256 * g] = (transpose8(word, tok) & ~keep) | (old[g] & keep);
       }
@@ -276,17 +264,7 @@ __global__ __launch_bounds__(256) void k_kv4_read(KvCache c, KvRange r, void* k,
   const int from = first < s0 ? (int)(s0 - first) : 0;
   const int to = (int)((int64_t)s0 + n - first < 32 ? (int64_t)s0 + n - first : 32);
   const int64_t row0 = c0 + (first - s0);
-  const int64_t entry = blk >> c.block_shift;
-  int32_t page = -1;
-  if (entry >= r.width) {
-    if (lane == 0) kv_flag(c, VBQ_KV4_FLAG_LENGTH);
-  } else {
-    page = r.table[(int64_t)b * r.width + entry];
-    if ((uint32_t)page >= (uint32_t)c.n_pages) {
-      if (lane == 0) kv_flag(c, VBQ_KV4_FLAG_PAGE);
-      page = -1;
-    }
-  }
+  const int32_t page = find_page(c, r, b, (int32_t)blk, lane == 0);
   const uint8_t* const p =
       kv_block(c, G, page < 0 ? 0u : (uint32_t)page, head, (uint32_t)blk & ((1u << c.block_shift) - 1u));
   u32x4 kw[G], vw[G], vs[G], vo[G];
@@ -342,19 +320,12 @@ __global__ __launch_bounds__(256) void k_kv4_read(KvCache c, KvRange r, void* k,
   }
 }
 
-// Units of `size` tokens that a sequence of max_tokens tokens can touch, and the
-// grid over (unit, head) and sequences; no launch when there is nothing to do.
-bool token_grid(const KvCache& c, const KvRange& r, int size, int64_t* units, dim3* grid, hipError_t* err) {
-  *err = hipSuccess;
-  if (r.max_tokens == 0 || r.total == 0) return false;
-  *units = ((int64_t)r.max_tokens + 2 * size - 2) / size;
-  const int64_t wgs = (*units * c.heads + 3) / 4;
-  if (wgs > INT32_MAX) {
-    *err = hipErrorNotSupported;
-    return false;
-  }
-  *grid = dim3((uint32_t)wgs, (uint32_t)r.batch);
-  return true;
+// Blocks that a sequence of max_tokens tokens can touch, times the heads; 0 when
+// there is nothing to do, -1 for more than a grid takes.
+int64_t block_tasks(const KvCache& c, const KvRange& r) {
+  if (r.max_tokens == 0 || r.total == 0) return 0;
+  const int64_t n = ((int64_t)r.max_tokens + 62) / 32 * c.heads;
+  return n > INT32_MAX ? -1 : n;
 }
 
 }  // namespace
@@ -373,22 +344,20 @@ bool token_grid(const KvCache& c, const KvRange& r, int size, int64_t* units, di
 
 hipError_t launch_kv4_append(const KvCache& c, const KvRange& r, const void* k, const void* v, int dtype,
                              int64_t k_ts, int64_t k_hs, int64_t v_ts, int64_t v_hs, hipStream_t s) {
-  int64_t units;
-  dim3 grid;
-  hipError_t err;
-  if (!token_grid(c, r, 8, &units, &grid, &err)) return err;
-#define VBQ_CALL(G, DT) k_kv4_append<G, DT><<<grid, 256, 0, s>>>(c, r, k, v, k_ts, k_hs, v_ts, v_hs, units)
+  const int64_t tasks = block_tasks(c, r);
+  if (tasks <= 0) return tasks < 0 ? hipErrorNotSupported : hipSuccess;
+  const dim3 grid((uint32_t)tasks, (uint32_t)r.batch);   // a workgroup a block: an octet a wavefront
+#define VBQ_CALL(G, DT) k_kv4_append<G, DT><<<grid, 256, 0, s>>>(c, r, k, v, k_ts, k_hs, v_ts, v_hs)
   VBQ_KV4_BY_TYPE(VBQ_CALL)
 #undef VBQ_CALL
   return hipGetLastError();
 }
 
 hipError_t launch_kv4_read(const KvCache& c, const KvRange& r, void* k, void* v, int dtype, hipStream_t s) {
-  int64_t units;
-  dim3 grid;
-  hipError_t err;
-  if (!token_grid(c, r, 32, &units, &grid, &err)) return err;
-#define VBQ_CALL(G, DT) k_kv4_read<G, DT><<<grid, 256, 0, s>>>(c, r, k, v, units)
+  const int64_t tasks = block_tasks(c, r);
+  if (tasks <= 0) return tasks < 0 ? hipErrorNotSupported : hipSuccess;
+  const dim3 grid((uint32_t)((tasks + 3) / 4), (uint32_t)r.batch);   // a wavefront a block
+#define VBQ_CALL(G, DT) k_kv4_read<G, DT><<<grid, 256, 0, s>>>(c, r, k, v, tasks / c.heads)
   VBQ_KV4_BY_TYPE(VBQ_CALL)
 #undef VBQ_CALL
   return hipGetLastError();
