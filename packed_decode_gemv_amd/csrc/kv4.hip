@@ -30,27 +30,42 @@ namespace {
 
 constexpr float kClamp = 61440.f;
 
+typedef uint16_t ushort2_t __attribute__((ext_vector_type(2)));
+
+// Eight numbers, and whether one is NaN or beyond the clamp (magnitudes order
+// like their bits).
 template <int DT>
-__device__ inline void load8(const void* base, int64_t elem, float (&x)[8]) {
+__device__ inline bool load8(const void* base, int64_t elem, float (&x)[8]) {
   if constexpr (DT == VBQ_F32) {
-    const float4* p = reinterpret_cast<const float4*>(static_cast<const float*>(base) + elem);
-    const float4 a = p[0], b = p[1];
-    x[0] = a.x; x[1] = a.y; x[2] = a.z; x[3] = a.w;
-    x[4] = b.x; x[5] = b.y; x[6] = b.z; x[7] = b.w;
-  } else {
-    const u32x4 w = *reinterpret_cast<const u32x4*>(static_cast<const uint16_t*>(base) + elem);
+    const u32x4* p = reinterpret_cast<const u32x4*>(static_cast<const float*>(base) + elem);
+    const u32x4 a = p[0], b = p[1];
+    uint32_t top = 0;
 #pragma unroll
     for (int i = 0; i < 4; ++i) {
+      const uint32_t u = a[i], w = b[i];
+      x[i] = __builtin_bit_cast(float, u);
+      x[4 + i] = __builtin_bit_cast(float, w);
+      top = max(max(top, u << 1), w << 1);
+    }
+    return top > (__builtin_bit_cast(uint32_t, kClamp) << 1);
+  } else {
+    const u32x4 w = *reinterpret_cast<const u32x4*>(static_cast<const uint16_t*>(base) + elem);
+    ushort2_t top = {0, 0};
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      const uint32_t u = w[i];
       if constexpr (DT == VBQ_F16) {
-        const uint32_t u = w[i];   // (bit casts take no vector elements)
         const half2_t h = __builtin_bit_cast(half2_t, u);
         x[2 * i] = (float)h.x;
         x[2 * i + 1] = (float)h.y;
       } else {
-        x[2 * i] = __builtin_bit_cast(float, w[i] << 16);
-        x[2 * i + 1] = __builtin_bit_cast(float, w[i] & 0xFFFF0000u);
+        x[2 * i] = __builtin_bit_cast(float, u << 16);
+        x[2 * i + 1] = __builtin_bit_cast(float, u & 0xFFFF0000u);
       }
+      top = __builtin_elementwise_max(top, __builtin_bit_cast(ushort2_t, u & 0x7FFF7FFFu));
     }
+    constexpr uint16_t most = DT == VBQ_F16 ? 0x7B80 : 0x4770;   // 61440
+    return top.x > most || top.y > most;
   }
 }
 
@@ -64,32 +79,36 @@ constexpr int kXor1 = 0xB1, kXor2 = 0x4E, kXor3 = 0x1B, kXor7 = 0x141, kXor8 = 0
 
 // Transposes the 8x8 nibbles that eight lanes (tok = 0..7) hold: nibble n of
 // lane t becomes nibble t of lane n.
+__device__ inline uint32_t swap_with(uint32_t w, uint32_t other, bool upper, uint32_t upper_mask, int bits) {
+  // the half of w that stays, and the other lane's half moved into its place
+  const uint32_t keep = upper ? upper_mask : ~upper_mask, turn = upper ? bits : 32 - bits;
+  return (w & keep) | (__builtin_amdgcn_alignbit(other, other, turn) & ~keep);
+}
 __device__ inline uint32_t transpose8(uint32_t w, uint32_t tok) {
-  const uint32_t p1 = dpp<kXor1>(w);
-  w = (tok & 1u) ? ((w & 0xF0F0F0F0u) | ((p1 >> 4) & 0x0F0F0F0Fu)) : ((w & 0x0F0F0F0Fu) | ((p1 << 4) & 0xF0F0F0F0u));
-  const uint32_t p2 = dpp<kXor2>(w);
-  w = (tok & 2u) ? ((w & 0xFF00FF00u) | ((p2 >> 8) & 0x00FF00FFu)) : ((w & 0x00FF00FFu) | ((p2 << 8) & 0xFF00FF00u));
-  const uint32_t p4 = dpp<kXor3>(dpp<kXor7>(w));
-  return (tok & 4u) ? ((w & 0xFFFF0000u) | (p4 >> 16)) : ((w & 0x0000FFFFu) | (p4 << 16));
+  w = swap_with(w, dpp<kXor1>(w), tok & 1u, 0xF0F0F0F0u, 4);
+  w = swap_with(w, dpp<kXor2>(w), tok & 2u, 0xFF00FF00u, 8);
+  return swap_with(w, dpp<kXor3>(dpp<kXor7>(w)), tok & 4u, 0xFFFF0000u, 16);
 }
 
 // Minimum and maximum over the lanes 8, 16 and 32 apart.
 __device__ inline float as_float(uint32_t u) { return __builtin_bit_cast(float, u); }
 __device__ inline uint32_t as_bits(float v) { return __builtin_bit_cast(uint32_t, v); }
-__device__ inline void spread_min_max(float& lo, float& hi) {
+__device__ inline float min2(float x, float y) { return __builtin_amdgcn_fmed3f(x, y, -__builtin_inff()); }
+__device__ inline float max2(float x, float y) { return __builtin_amdgcn_fmed3f(x, y, __builtin_inff()); }
+__device__ inline void spread_min_max(float& lo, float& hi) {   // (finite numbers)
   typedef uint32_t pair_t __attribute__((ext_vector_type(2)));
-  lo = fminf(lo, as_float(dpp<kXor8>(as_bits(lo))));
-  hi = fmaxf(hi, as_float(dpp<kXor8>(as_bits(hi))));
+  lo = min2(lo, as_float(dpp<kXor8>(as_bits(lo))));
+  hi = max2(hi, as_float(dpp<kXor8>(as_bits(hi))));
   pair_t p = __builtin_amdgcn_permlane16_swap(as_bits(lo), as_bits(lo), false, false);
   pair_t q = __builtin_amdgcn_permlane16_swap(as_bits(hi), as_bits(hi), false, false);
   uint32_t p0 = p.x, p1 = p.y, q0 = q.x, q1 = q.y;
-  lo = fminf(as_float(p0), as_float(p1));
-  hi = fmaxf(as_float(q0), as_float(q1));
+  lo = min2(as_float(p0), as_float(p1));
+  hi = max2(as_float(q0), as_float(q1));
   p = __builtin_amdgcn_permlane32_swap(as_bits(lo), as_bits(lo), false, false);
   q = __builtin_amdgcn_permlane32_swap(as_bits(hi), as_bits(hi), false, false);
   p0 = p.x, p1 = p.y, q0 = q.x, q1 = q.y;
-  lo = fminf(as_float(p0), as_float(p1));
-  hi = fmaxf(as_float(q0), as_float(q1));
+  lo = min2(as_float(p0), as_float(p1));
+  hi = max2(as_float(q0), as_float(q1));
 }
 
 // Numbers of a sequence that fit the call.
@@ -131,12 +150,13 @@ __global__ __launch_bounds__(256) void k_kv4_append(KvCache c, KvRange r, const 
   const int64_t row0 = c0 + (first - s0);
   const bool mine = (valid >> tok) & 1u;
   float x[2][G][8];
+  bool odd = false;   // a NaN, or a number beyond the clamp
 #pragma unroll
   for (int kv = 0; kv < 2; ++kv)
 #pragma unroll
     for (int g = 0; g < G; ++g) {
       const int64_t at = (row0 + tok) * (kv ? v_ts : k_ts) + head * (kv ? v_hs : k_hs) + 64 * g + 8 * e;
-      if (mine) load8<DT>(kv ? v : k, at, x[kv][g]);
+      if (mine) odd |= load8<DT>(kv ? v : k, at, x[kv][g]);
       else
 #pragma unroll
         for (int i = 0; i < 8; ++i) x[kv][g][i] = 0.f;
@@ -152,49 +172,45 @@ __global__ __launch_bounds__(256) void k_kv4_append(KvCache c, KvRange r, const 
   uint32_t old[G];
 #pragma unroll
   for (int g = 0; g < G; ++g) old[g] = keep ? vword[256 * g] : 0u;
-  bool nan = false;
+  if (__any(odd)) {
+    bool nan = false;
+#pragma unroll
+    for (int kv = 0; kv < 2; ++kv)
+#pragma unroll
+      for (int g = 0; g < G; ++g)
+#pragma unroll
+        for (int i = 0; i < 8; ++i) {
+          float& w = x[kv][g][i];
+          const bool bad = w != w;
+          nan |= bad;
+          w = bad ? 0.f : __builtin_amdgcn_fmed3f(w, -kClamp, kClamp);
+        }
+    if (__any(nan) && lane == 0) kv_flag(c, VBQ_KV4_FLAG_NAN);
+  }
 #pragma unroll
   for (int kv = 0; kv < 2; ++kv)
 #pragma unroll
     for (int g = 0; g < G; ++g) {
       float(&w)[8] = x[kv][g];
-      float lo = fminf(fminf(w[0], w[1]), w[2]), hi = fmaxf(fmaxf(w[0], w[1]), w[2]);
-      lo = fminf(fminf(lo, w[3]), w[4]);
-      hi = fmaxf(fmaxf(hi, w[3]), w[4]);
-      lo = fminf(fminf(lo, w[5]), w[6]);
-      hi = fmaxf(fmaxf(hi, w[5]), w[6]);
-      lo = fminf(lo, w[7]);
-      hi = fmaxf(hi, w[7]);
-      // NaN, or beyond the clamp: rare, so put right afterwards
-      const bool odd = __builtin_isunordered(w[0], w[1]) | __builtin_isunordered(w[2], w[3]) |
-                       __builtin_isunordered(w[4], w[5]) | __builtin_isunordered(w[6], w[7]) | (lo < -kClamp) |
-                       (hi > kClamp);
-      if (__any(odd)) {
-        lo = kClamp;
-        hi = -kClamp;
+      float lo = min2(w[0], w[1]), hi = max2(w[0], w[1]);
 #pragma unroll
-        for (int i = 0; i < 8; ++i) {
-          const bool bad = w[i] != w[i];
-          nan |= bad;
-          w[i] = bad ? 0.f : fminf(fmaxf(w[i], -kClamp), kClamp);
-          lo = fminf(lo, w[i]);
-          hi = fmaxf(hi, w[i]);
-        }
+      for (int i = 2; i < 8; ++i) {
+        lo = min2(lo, w[i]);
+        hi = max2(hi, w[i]);
       }
       spread_min_max(lo, hi);
       const _Float16 s16 = (_Float16)__fmul_rn(__fsub_rn(hi, lo), 1.f / 15.f);
       const _Float16 o16 = (_Float16)lo;
       const float s = (float)s16, of = (float)o16;
       const float r = s != 0.f ? __builtin_amdgcn_rcpf(s) : 0.f;
-      float q[8];
-      uint32_t off = 0;   // largest |t - q| (of bits: they order like the numbers)
+      float q[8], off = 0.f;
 #pragma unroll
       for (int i = 0; i < 8; ++i) {
         const float u = __builtin_amdgcn_fmed3f(__fmul_rn(__fsub_rn(w[i], of), r), 0.f, 15.f);
         q[i] = rintf(u);
-        off = max(off, as_bits(__fsub_rn(u, q[i])) << 1);
+        off = fmaxf(off, fabsf(__fsub_rn(u, q[i])));
       }
-      if (__any(off > (as_bits(0.5f - 0x1p-16f) << 1))) {
+      if (__any(off > 0.5f - 0x1p-16f)) {
 #pragma unroll
         for (int i = 0; i < 8; ++i)
           q[i] = s != 0.f ? __builtin_amdgcn_fmed3f(rintf(__fdiv_rn(__fsub_rn(w[i], of), s)), 0.f, 15.f) : 0.f;
@@ -216,7 +232,6 @@ __global__ __launch_bounds__(256) void k_kv4_append(KvCache c, KvRange r, const 
         vword[256 * g] = (transpose8(word, tok) & ~keep) | (old[g] & keep);
       }
     }
-  if (__ballot(nan && mine) && lane == 0) kv_flag(c, VBQ_KV4_FLAG_NAN);
 }
 
 // N neighbouring channels of a row, rounded once.
