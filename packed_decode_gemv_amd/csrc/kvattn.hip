@@ -140,6 +140,12 @@ struct Halves {
 // later blocks are on their way while one is worked on.
 template <int G>
 constexpr int kCopies = (kKvGroupBytes * G + 1023) / 1024;
+// The address that lane i holds.
+__device__ inline const uint8_t* lane_address(uint64_t v, int i) {
+  const uint32_t lo = __builtin_amdgcn_readlane((int)(uint32_t)v, i);
+  const uint32_t hi = __builtin_amdgcn_readlane((int)(uint32_t)(v >> 32), i);
+  return reinterpret_cast<const uint8_t*>((uint64_t)hi << 32 | lo);
+}
 template <int G>
 __device__ inline void copy_block(uint32_t lds, const uint8_t* p, uint32_t lane) {
   constexpr int BYTES = kKvGroupBytes * G;
@@ -377,29 +383,27 @@ __global__ __launch_bounds__(64 * kWaves, (kRoomy<G, ROWS>) ? 4 : G * ROWS > 64 
 
   // The wavefront's blocks: copies run STAGES - 1 ahead.
   const uint32_t in_page = (1u << a.cache.block_shift) - 1u;
-  int pages = -1;   // lane i: the page of the wavefront's block i (of 64 at a time)
+  uint64_t at = 0;   // lane i: where the wavefront's block i (of 64 at a time) lies
   uint64_t gone = 0, gone_before = 0;   // those that are not in the cache, and of the 64 before
   auto block_of = [&](int idx) { return idx < re.ns ? idx : idx - re.ns + re.w0; };
   auto start_copy = [&](int it) {
-    const int idx = i0 + wave + kWaves * it;
     if ((it & 63) == 0) {
-      const int next = idx + kWaves * (int)lane;
-      pages = 0;
+      const int next = i0 + wave + kWaves * (it + (int)lane), blk = block_of(next);
+      int page = 0;
       bool bad = false;
       if (next < i1) {
-        pages = a.table[(int64_t)b * a.width + (block_of(next) >> a.cache.block_shift)];
-        bad = (uint32_t)pages >= (uint32_t)a.cache.n_pages;
+        page = a.table[(int64_t)b * a.width + (blk >> a.cache.block_shift)];
+        bad = (uint32_t)page >= (uint32_t)a.cache.n_pages;
       }
       if (bad) {
-        pages = 0;   // copied, and left out of the sums
+        page = 0;   // copied, and left out of the sums
         kv_flag(a.cache, VBQ_KV4_FLAG_PAGE);
       }
+      at = (uint64_t)kv_block(a.cache, G, (uint32_t)page, head, (uint32_t)blk & in_page);
       gone_before = gone;
       gone = __ballot(bad);
     }
-    const int page = __builtin_amdgcn_readlane(pages, it & 63);
-    copy_block<G>(ring_lds + (uint32_t)(it % STAGES) * BYTES,
-                  kv_block(a.cache, G, (uint32_t)page, head, (uint32_t)block_of(idx) & in_page), lane);
+    copy_block<G>(ring_lds + (uint32_t)(it % STAGES) * BYTES, lane_address(at, it & 63), lane);
   };
   const int count = i0 + wave < i1 ? (i1 - i0 - wave + kWaves - 1) / kWaves : 0;
 #pragma unroll
@@ -490,7 +494,7 @@ __global__ __launch_bounds__(64 * kWaves, (kRoomy<G, ROWS>) ? 4 : G * ROWS > 64 
     const int ahead = it + STAGES - 1;
     if (ahead < count) start_copy(ahead);
     // (the pages of the 64 blocks after may have been looked up already)
-    if ((((it ^ min(ahead, count - 1)) >> 6 ? gone_before : gone) >> (it & 63)) & 1u) continue;
+    if ((gone | gone_before) && ((((it ^ min(ahead, count - 1)) >> 6 ? gone_before : gone) >> (it & 63)) & 1u)) continue;
     const int blk = block_of(i0 + wave + kWaves * it);
     const uint8_t* const k = own_ring + (it % STAGES) * BYTES;
 
@@ -918,35 +922,34 @@ __global__ __launch_bounds__(256, G >= 3 ? 1 : 2) void k_kv4_attn_tile(KvAttn a)
 
   // Copies: lane i keeps the page of block i of 64.
   const uint32_t in_page = (1u << a.cache.block_shift) - 1u;
-  int pages = -1;
+  uint64_t where = 0;   // lane i: where block i of 64 lies
   uint64_t gone = 0, gone_before = 0;   // blocks of the 64 (and of those before) whose page is not in the cache
   auto start_copy = [&](int i) {
     if ((i & 63) == 0) {
-      const int next = i + (int)lane;
-      pages = 0;
+      const int next = i + (int)lane, blk = block_of(next);
+      int page = 0;
       bool bad = false;
       if (next < blocks) {
-        pages = a.table[(int64_t)b * a.width + (block_of(next) >> a.cache.block_shift)];
-        bad = (uint32_t)pages >= (uint32_t)a.cache.n_pages;
+        page = a.table[(int64_t)b * a.width + (blk >> a.cache.block_shift)];
+        bad = (uint32_t)page >= (uint32_t)a.cache.n_pages;
       }
       if (bad) {
-        pages = 0;   // copied, and hidden
+        page = 0;   // copied, and hidden
         if (wave == 0) kv_flag(a.cache, VBQ_KV4_FLAG_PAGE);
       }
+      where = (uint64_t)kv_block(a.cache, G, (uint32_t)page, head, (uint32_t)blk & in_page) + wave * SHARE;
       gone_before = gone;
       gone = __ballot(bad);
     }
-    const int page = __builtin_amdgcn_readlane(pages, i & 63);
-    const uint8_t* const p =
-        kv_block(a.cache, G, (uint32_t)page, head, (uint32_t)block_of(i) & in_page) + wave * SHARE;
-    const u32x4 rsrc = make_rsrc(p, SHARE);
+    const u32x4 rsrc = make_rsrc(lane_address(where, i & 63), SHARE);
     const uint32_t to = raw_lds + (uint32_t)(i % RAW) * BYTES + (uint32_t)wave * SHARE;
 #pragma unroll
     for (int c = 0; c < SHARE / 1024; ++c) dma16(rsrc, to + 1024 * c, 1024 * c + 16 * lane);
     if (lane < (SHARE % 1024) / 16) dma16(rsrc, to + SHARE / 1024 * 1024, SHARE / 1024 * 1024 + 16 * lane);
   };
   auto is_gone = [&](int i, int newest) {   // newest: the last block whose copy was started
-    return (((i ^ newest) >> 6 ? gone_before : gone) >> (i & 63)) & 1u;
+    if (!(gone | gone_before)) return false;
+    return (bool)((((i ^ newest) >> 6 ? gone_before : gone) >> (i & 63)) & 1u);
   };
 
   // Queries: B operands, channels of a chunk as pairs; what the lane's row sees.
