@@ -326,8 +326,8 @@ __global__ __launch_bounds__(64 * kWaves, (kRoomy<G, ROWS>) ? 4 : G * ROWS > 64 
     for (int base = 0;; base += 64) {
       if (a.batch > 64) lanes_load(a, lane, base, false, ln);
       n = (int)((uint32_t)(ln.blocks + chunk - 1) / (uint32_t)chunk);
-      size = (int)((uint32_t)(ln.blocks + n - 1) / (uint32_t)max(n, 1));
-      n = (int)((uint32_t)(ln.blocks + size - 1) / (uint32_t)max(size, 1));
+      size = n > 0 ? (int)((uint32_t)(ln.blocks + n - 1) / (uint32_t)n) : 1;   // nothing to see: no part
+      n = (int)((uint32_t)(ln.blocks + size - 1) / (uint32_t)size);
       incl = before + wave_scan(n * a.cache.heads);
       past = __ballot(incl > (int)blockIdx.x);
       if (past) break;

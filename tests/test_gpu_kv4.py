@@ -371,6 +371,114 @@ def test_attention_in_pieces_and_whole(vbq):
     attend(vbq, rng, 1, 4, 256, 64, [1500], [9], window=900, sinks=5)
 
 
+@pytest.mark.parametrize("dim", [64, 128, 192, 256])
+@pytest.mark.parametrize("ratio,new", [(3, 1), (5, 1), (4, 3), (8, 4)])      # 4, 8, 16 and 32 rows a tile
+def test_attention_in_parts_for_every_tile(vbq, dim, ratio, new):
+    """Tiles cut into parts, for every head size and number of rows: lengths of one block and of many, and a
+    sequence that sees nothing beside them."""
+    rng = np.random.default_rng(dim + ratio)
+    attend(vbq, rng, 1, ratio, dim, 32, [1100, 0, 37], [new, 1, min(new, 2)], max_kv=1200)
+
+
+def test_attention_of_more_sequences_than_lanes(vbq):
+    """Parts of tiles are found by scanning the sequences 64 at a time."""
+    rng = np.random.default_rng(11)
+    lens = [int(n) for n in rng.integers(0, 90, 150)]
+    lens[3], lens[70], lens[149] = 1500, 0, 900
+    attend(vbq, rng, 1, 2, 64, 32, lens, [1] * 150)
+    lens[149] = 0
+    attend(vbq, rng, 1, 4, 64, 64, lens, [0 if n % 7 == 0 else 1 for n in range(150)], window=300, sinks=3)
+
+
+def test_attention_parts_where_pages_are_missing(vbq):
+    """A page that is not in the cache counts as tokens that nobody sees, wherever it lies."""
+    import torch
+    rng = np.random.default_rng(12)
+    for ratio, new in ((4, 1), (4, 40)):
+        page, dim, L = 32, 64, 2300            # more than 64 blocks: addresses are looked up 64 at a time
+        lens, news = [L], [new]
+        table, n_pages = table_for(rng, lens, page)
+        data = random_cache(rng, n_pages, page, 1, dim)
+        cache = vbq.Kv4Cache(n_pages, page, 1, dim, data=gpu(data))
+        q = torch.from_numpy(rng.normal(0, 1, (new, ratio, dim)).astype(np.float32)).half()
+        lost = [0, 1, 7, 62, 63, 64, 65, 70]
+        holed = table.copy()
+        holed[0, lost] = [-1, n_pages, 2 ** 31 - 1, -5, n_pages + 7, -1, -2 ** 31, n_pages]
+        args = (gpu(np.array(lens, np.int32)), gpu(cum(news)), new, L)
+        got = vbq.kv4_attention(cache, q.cuda(), gpu(holed), *args)
+        with pytest.raises(vbq.VbqError, match="block-table"):
+            cache.check()
+        lay = Layout(page, 1, dim)
+        hide = np.zeros(L, bool)
+        for e in lost:
+            hide[e * page:(e + 1) * page] = True
+        K = np.stack([lay.read(data, lay.block(int(table[0, t // page]), 0, t % page), t % 32, 0) for t in range(L)])
+        V = np.stack([lay.read(data, lay.block(int(table[0, t // page]), 0, t % page), t % 32, 1) for t in range(L)])
+        K, V = K.astype(np.float64), V.astype(np.float64)
+        want, mass, size = (np.zeros((new, ratio, n)) for n in (dim, dim, 1))
+        for i in range(new):
+            see = ~hide & (np.arange(L) <= L - new + i)
+            for r in range(ratio):
+                qv = q[i, r].double().numpy()
+                s = K[see] @ qv * dim ** -0.5
+                w = np.exp(s - s.max())
+                w /= w.sum()
+                want[i, r], mass[i, r] = w @ V[see], w @ np.abs(V[see])
+                size[i, r] = ((np.abs(K) + 2 * np.abs(K).max()) @ np.abs(qv)).max() * dim ** -0.5
+        check(got.double().cpu().numpy(), want, mass, size[..., 0], "float16", dim)
+
+
+def test_attention_of_more_tiles_than_counters(vbq):
+    """Beyond 2048 tiles none is cut; a workspace is not needed."""
+    import torch
+    rng = np.random.default_rng(13)
+    B = 300
+    table = torch.arange(B, dtype=torch.int32, device="cuda").view(B, 1)
+    data = random_cache(rng, B, 1024, 8, 64)
+    cache = vbq.Kv4Cache(B, 1024, 8, 64, data=gpu(data))
+    q = torch.randn(B, 8, 64, device="cuda").half()
+    lens = torch.full((B,), 1000, dtype=torch.int32, device="cuda")
+    cu = torch.arange(B + 1, dtype=torch.int32, device="cuda")
+    assert vbq.kv4_attention_workspace(cache, B, B, 8, 1, 1000).numel() == 0
+    out = vbq.kv4_attention(cache, q, table, lens, cu, 1, 1000)
+    few = vbq.kv4_attention(cache, q[7:9], table[7:9].contiguous(), lens[:2], cu[:3], 1, 1000)
+    err = (out[7:9].double() - few.double()).abs().max()
+    assert float(err) <= 2.0 ** -10 * float(few.abs().max())
+    assert cache.check() is False
+
+
+def test_attention_of_values_of_any_size(vbq):
+    """The product of probability and scale is held around the largest scale a row has met: scales from fp16's
+    smallest to the clamp's, growing and shrinking along the sequence."""
+    import torch
+    i32 = dict(dtype=torch.int32, device="cuda")
+    gen = torch.Generator(device="cuda").manual_seed(5)
+    L, dim = 700, 64
+    k = torch.randn(L, 1, dim, generator=gen, device="cuda")
+    table = torch.arange(32, device="cuda").int().view(1, 32)
+    cu, lens = torch.tensor([0, L], **i32), torch.tensor([L], **i32)
+    size = torch.linspace(-18, 15, L, device="cuda")
+    for exps in (size, size.flip(0), torch.full_like(size, -20.0), torch.full_like(size, 15.5)):
+        v = torch.randn(L, 1, dim, generator=gen, device="cuda") * torch.exp2(exps)[:, None, None]
+        cache = vbq.Kv4Cache(32, 32, 1, dim)
+        vbq.kv4_append(cache, k, v, table, torch.zeros(1, **i32), cu)
+        rk, rv = (x.double().cpu().numpy()[:, 0] for x in vbq.kv4_read(cache, table, torch.zeros(1, **i32), cu, L,
+                                                                       torch.float32))
+        for rows in (1, 50):
+            q = torch.randn(rows, 4, dim, generator=gen, device="cuda").half()
+            got = vbq.kv4_attention(cache, q, table, lens, torch.tensor([0, rows], **i32), rows, L)
+            for i in (0, rows - 1):
+                p = L - rows + i + 1
+                for r in range(4):
+                    s = rk[:p] @ q[i, r].double().cpu().numpy() * dim ** -0.5
+                    w = np.exp(s - s.max())
+                    w /= w.sum()
+                    want, mass = w @ rv[:p], w @ np.abs(rv[:p])
+                    # as in check(), with scores of up to 64 in magnitude, and fp16's subnormal outputs and values
+                    bound = (2 * (88 * 2.0 ** -24 * 64 + 2.0 ** -21) + 2.1 * 2.0 ** -11 + 2.0 ** -11) * mass + 2.0 ** -23
+                    assert (np.abs(got[i, r].double().cpu().numpy() - want) <= bound).all(), (i, r)
+
+
 def test_attention_of_peaked_and_flat_scores(vbq):
     rng = np.random.default_rng(6)
     attend(vbq, rng, 1, 4, 128, 64, [700], [1], gain=12.0)
