@@ -670,3 +670,18 @@ def test_the_binding_refuses_what_does_not_fit(vbq):
         vbq.kv4_attention(cache, q, table, lens, cu, 1, 3, scale=-1.0)
     with pytest.raises(ValueError, match="refused"):
         vbq.kv4_attention(cache, q, table, lens, cu, 1, -3)
+
+
+# ---- the layer that runs them together ------------------------------------------------
+@pytest.mark.parametrize("batch,prompt,steps,window", [(3, 70, 5, 0), (1, 200, 4, 60)])
+def test_the_decode_example(vbq, batch, prompt, steps, window):
+    import os
+    import sys
+    sys.path.insert(0, os.path.join(os.path.dirname(os.path.dirname(os.path.abspath(__file__))), "examples"))
+    import attention_decode as ex
+    layer = ex.AttentionLayer(hidden=256, heads=8, kv_heads=2, dim=64)
+    r = ex.run(batch, prompt, steps, window, layer=layer)
+    assert r["tokens"] == prompt + steps + 1
+    # probabilities, their product with a scale and the output are rounded to fp16 or better
+    assert r["rel_l2"] <= 3 * 2.0 ** -11
+    assert r["cache_bytes"] * 32 == r["bf16_bytes"] * 9
