@@ -68,7 +68,7 @@ hipError_t launch_kv4_read(const KvCache& c, const KvRange& r, void* k, void* v,
 // Sizes of an attention launch, from the call's sizes alone: rows of a tile,
 // parts (as above), tiles and workgroups.
 struct KvAttnPlan {
-  int32_t rows, row_tiles, parts;
+  int32_t rows, parts;
   int64_t tiles, grid;
 };
 KvAttnPlan kv4_attn_plan(int batch, int heads, int ratio, int groups, int max_q, int max_kv, int window, int sinks);

@@ -167,7 +167,7 @@ __device__ inline Reach reach(int len, int p_min, int p_max, int window, int sin
   r.ns = 0;
   r.w0 = 0;
   if (window) {
-    const int lo = p_min - window + 1;   // first token in any row's window
+    const int lo = max(p_min, 0) - window + 1;   // first token in the window of any row that sees one
     r.ns = min((min(sinks, end) + kKvBlock - 1) / kKvBlock, blocks);
     r.ns = max(r.ns, 0);
     r.w0 = lo > 0 ? lo / kKvBlock : 0;
@@ -457,7 +457,7 @@ __global__ __launch_bounds__(64 * kWaves, (kRoomy<G, ROWS>) ? 4 : G * ROWS > 64 
     }
     const int p = a.causal ? first + qi : len - 1;
     hi[nt] = in ? min(p, len - 1) : -1;
-    lo[nt] = a.window ? p - a.window + 1 : INT32_MIN;
+    lo[nt] = a.window ? max(p, 0) - a.window + 1 : INT32_MIN;   // (rows before position 0 see nothing)
   }
 
   // Running maximum m, and sums held times 2^base, base = S - m: of p, of p o,
@@ -1022,12 +1022,12 @@ __global__ __launch_bounds__(256, G >= 3 ? 1 : 2) void k_kv4_attn_tile(KvAttn a)
     }
     const int p = a.causal ? first + qi : len - 1;
     hi = r < rows ? min(p, len - 1) : -1;
-    lo = a.window ? p - a.window + 1 : INT32_MIN;
+    lo = a.window ? max(p, 0) - a.window + 1 : INT32_MIN;
   }
   // this wavefront's first and last positions
   const int w_r1 = min(rows, w_r0 + 32);
   const int w_min = min(a.causal ? first + w_r0 / a.ratio : len - 1, len - 1);
-  const int w_max = w_r0 >= rows ? -1 : a.causal ? first + (w_r1 - 1) / a.ratio : len - 1;
+  const int w_max = w_r0 >= rows ? -1 : a.causal ? max(first + (w_r1 - 1) / a.ratio, -1) : len - 1;
 
   // Operands of block i: a wavefront takes word `wave` of every lane's four.
   const uint32_t m16 = lane & 15u, kq = lane >> 4;
@@ -1083,46 +1083,39 @@ __global__ __launch_bounds__(256, G >= 3 ? 1 : 2) void k_kv4_attn_tile(KvAttn a)
 #pragma unroll
       for (int c = 0; c < 4; ++c) {
         const half8_t kc = __builtin_bit_cast(half8_t, lds16(k + 1024 * (4 * g + c) + 16 * lane));
-          d = __builtin_amdgcn_mfma_f32_32x32x16_f16(kc, qf[4 * g + c], c ? d : none, 0, 0, 0);
+        d = __builtin_amdgcn_mfma_f32_32x32x16_f16(kc, qf[4 * g + c], c ? d : none, 0, 0, 0);
       }
 #pragma unroll
       for (int A = 0; A < 2; ++A) {
         const Halves<8> s(so + 128 * g + 16 * (2 * A + half));
 #pragma unroll
-          for (int j = 0; j < 8; ++j) x[8 * A + j] = __builtin_fmaf(s[j], d[8 * A + j], x[8 * A + j]);
+        for (int j = 0; j < 8; ++j) x[8 * A + j] = __builtin_fmaf(s[j], d[8 * A + j], x[8 * A + j]);
       }
     }
   };
 
-  float m, l, mx;
+  // Running maximum, sum of p times 2^(kTileShift - m), sums of p v; mx: a block's maximum.
+  float m = kNoMax, l = 0.f, mx;
   f32x16 acc[TILES];
-  {
-    m = kNoMax;
-    l = 0.f;
 #pragma unroll
-    for (int t = 0; t < TILES; ++t) acc[t] = none;
-  }
+  for (int t = 0; t < TILES; ++t) acc[t] = none;
   // Masks scores of block i; their rows' maxima, and whether one passes its
   // running maximum by more than the slack.
   auto settle = [&](int i, bool hidden, f32x16& sc) {
     const int t0 = block_of(i) * kKvBlock;
     if (hidden || t0 + kKvBlock - 1 > w_min || (a.window && t0 <= w_max - a.window && t0 + kKvBlock > a.sinks)) {
 #pragma unroll
-        for (int j = 0; j < 16; ++j) {
-          const int t = t0 + 8 * (2 * (j >> 3) + (int)half) + (j & 7);
-          const bool see = !hidden && t <= hi && (t >= lo || t < a.sinks);
-          sc[j] = see ? sc[j] : -__builtin_inff();
-        }
+      for (int j = 0; j < 16; ++j) {
+        const int t = t0 + 8 * (2 * (j >> 3) + (int)half) + (j & 7);
+        const bool see = !hidden && t <= hi && (t >= lo || t < a.sinks);
+        sc[j] = see ? sc[j] : -__builtin_inff();
+      }
     }
-    bool pass = false;
-    {
-      float top = sc[0];
+    float top = sc[0];
 #pragma unroll
-      for (int j = 1; j < 16; ++j) top = fmaxf(top, sc[j]);
-      mx = half_max(top) * to_log2;
-      pass |= mx > m + kTileSlack;
-    }
-    return (bool)__any(pass);
+    for (int j = 1; j < 16; ++j) top = fmaxf(top, sc[j]);
+    mx = half_max(top) * to_log2;
+    return (bool)__any(mx > m + kTileSlack);
   };
   // Waits for the copy of block i (of which at most block i + 1's follow), for
   // every wavefront, and starts block i + 2's.
@@ -1155,13 +1148,11 @@ __global__ __launch_bounds__(256, G >= 3 ? 1 : 2) void k_kv4_attn_tile(KvAttn a)
     // more than the slack: it has no vector arithmetic on the sums, so they
     // stay in accumulation registers.
     for (int i = 0; i < blocks;) {
-      {
-        const float mt = fmaxf(m, mx), f = __builtin_amdgcn_exp2f(m - mt);
-        m = mt;
-        l *= f;
+      const float mt = fmaxf(m, mx), f = __builtin_amdgcn_exp2f(m - mt);
+      m = mt;
+      l *= f;
 #pragma unroll
-        for (int t = 0; t < TILES; ++t) acc[t] *= f;
-      }
+      for (int t = 0; t < TILES; ++t) acc[t] *= f;
       bool pass = false;
       do {
         arrive(i + 2);
@@ -1171,37 +1162,32 @@ __global__ __launch_bounds__(256, G >= 3 ? 1 : 2) void k_kv4_attn_tile(KvAttn a)
         scores(i + 1, next);
         half8_t pf[2], pl[2];   // probabilities, and what their rounding leaves
         const half2_t ones = {(_Float16)1.f, (_Float16)1.f};
-        {
-          const float base = kTileShift - m;
+        const float base = kTileShift - m;
 #pragma unroll
-          for (int A = 0; A < 2; ++A)
+        for (int A = 0; A < 2; ++A)
 #pragma unroll
-            for (int j = 0; j < 4; ++j) {
-              const float p0 = __builtin_amdgcn_exp2f(__builtin_fmaf(sc[8 * A + j], to_log2, base));
-              const float p1 = __builtin_amdgcn_exp2f(__builtin_fmaf(sc[8 * A + 4 + j], to_log2, base));
-              const half2_t pr = {(_Float16)p0, (_Float16)p1};
-              pf[A][2 * j] = pr.x;
-              pf[A][2 * j + 1] = pr.y;
-              if constexpr (FINE) {
-                l += p0 + p1;
-                pl[A][2 * j] = (_Float16)(p0 - (float)pr.x);
-                pl[A][2 * j + 1] = (_Float16)(p1 - (float)pr.y);
-              } else {
-                l = __builtin_amdgcn_fdot2(pr, ones, l, false);   // the sum of what is multiplied
-              }
+          for (int j = 0; j < 4; ++j) {
+            const float p0 = __builtin_amdgcn_exp2f(__builtin_fmaf(sc[8 * A + j], to_log2, base));
+            const float p1 = __builtin_amdgcn_exp2f(__builtin_fmaf(sc[8 * A + 4 + j], to_log2, base));
+            const half2_t pr = {(_Float16)p0, (_Float16)p1};
+            pf[A][2 * j] = pr.x;
+            pf[A][2 * j + 1] = pr.y;
+            if constexpr (FINE) {
+              l += p0 + p1;
+              pl[A][2 * j] = (_Float16)(p0 - (float)pr.x);
+              pl[A][2 * j + 1] = (_Float16)(p1 - (float)pr.y);
+            } else {
+              l = __builtin_amdgcn_fdot2(pr, ones, l, false);   // the sum of what is multiplied
             }
-        }
+          }
         const uint8_t* const v = vals + (i % 3) * HELD;
 #pragma unroll
         for (int A = 0; A < 2; ++A)
 #pragma unroll
           for (int t = 0; t < TILES; ++t) {
             const half8_t vc = __builtin_bit_cast(half8_t, lds16(v + ((A * TILES + t) * 64 + lane) * 16));
-            {
-              acc[t] = __builtin_amdgcn_mfma_f32_32x32x16_f16(vc, pf[A], acc[t], 0, 0, 0);
-              if constexpr (FINE)
-                acc[t] = __builtin_amdgcn_mfma_f32_32x32x16_f16(vc, pl[A], acc[t], 0, 0, 0);
-            }
+            acc[t] = __builtin_amdgcn_mfma_f32_32x32x16_f16(vc, pf[A], acc[t], 0, 0, 0);
+            if constexpr (FINE) acc[t] = __builtin_amdgcn_mfma_f32_32x32x16_f16(vc, pl[A], acc[t], 0, 0, 0);
           }
         spread(i + 2);
         sc = next;
@@ -1211,24 +1197,22 @@ __global__ __launch_bounds__(256, G >= 3 ? 1 : 2) void k_kv4_attn_tile(KvAttn a)
     }
   }
 
-  {
-    const float sum = half_sum(l);
-    const int r = w_r0 + (int)col, qi = r / a.ratio, hh = r - qi * a.ratio;
-    if (r >= rows) return;
-    const float inv = sum > 0.f ? 1.f / sum : sum == 0.f ? 0.f : sum;   // 0: nothing seen; NaN stays
-    const int64_t o = (int64_t)(sq.c0 + qi) * a.n_heads + head * a.ratio + hh;
+  const float sum = half_sum(l);
+  const int r = w_r0 + (int)col, qi = r / a.ratio, hh = r - qi * a.ratio;
+  if (r >= rows) return;
+  const float inv = sum > 0.f ? 1.f / sum : sum == 0.f ? 0.f : sum;   // 0: nothing seen; NaN stays
+  const int64_t o = (int64_t)(sq.c0 + qi) * a.n_heads + head * a.ratio + hh;
 #pragma unroll
-    for (int g = 0; g < G; ++g)
+  for (int g = 0; g < G; ++g)
 #pragma unroll
-      for (int u = 0; u < 2; ++u)
+    for (int u = 0; u < 2; ++u)
 #pragma unroll
-        for (int bb = 0; bb < 4; ++bb) {
-          const f32x4 v = {acc[2 * g][4 * u + bb], acc[2 * g][8 + 4 * u + bb], acc[2 * g + 1][4 * u + bb],
-                           acc[2 * g + 1][8 + 4 * u + bb]};
-          store4(a, o * D + 64 * g + 4 * (8 * u + 4 * (int)half + bb), v * inv);
-        }
-    if (a.lse && half == 0) a.lse[o] = (__builtin_amdgcn_logf(sum) + m - kTileShift) * kLn2;
-  }
+      for (int bb = 0; bb < 4; ++bb) {
+        const f32x4 v = {acc[2 * g][4 * u + bb], acc[2 * g][8 + 4 * u + bb], acc[2 * g + 1][4 * u + bb],
+                         acc[2 * g + 1][8 + 4 * u + bb]};
+        store4(a, o * D + 64 * g + 4 * (8 * u + 4 * (int)half + bb), v * inv);
+      }
+  if (a.lse && half == 0) a.lse[o] = (__builtin_amdgcn_logf(sum) + m - kTileShift) * kLn2;
 }
 
 }  // namespace
@@ -1244,14 +1228,12 @@ KvAttnPlan kv4_attn_plan(int batch, int heads, int ratio, int groups, int max_q,
   const int64_t rows = (int64_t)max_q * ratio;
   if (rows > 32) {   // many rows: the tile kernel
     p.rows = 128;
-    p.row_tiles = (int32_t)((rows + p.rows - 1) / p.rows);
-    p.tiles = (int64_t)batch * heads * p.row_tiles;
+    p.tiles = (int64_t)batch * heads * ((rows + p.rows - 1) / p.rows);
     p.parts = 0;
     p.grid = p.tiles;
     return p;
   }
   p.rows = rows <= 4 ? 4 : rows <= 8 ? 8 : rows <= 16 ? 16 : 32;
-  p.row_tiles = 1;
   p.tiles = (int64_t)batch * heads;
   int64_t blocks = ((int64_t)max_kv + kKvBlock - 1) / kKvBlock;
   if (window) {

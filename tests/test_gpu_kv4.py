@@ -363,6 +363,14 @@ def test_attention_under_a_window(vbq, window, sinks, lens, news):
     attend(vbq, rng, 1, 5, 128, 64, lens, news, "bfloat16", window=window, sinks=sinks)
 
 
+@pytest.mark.parametrize("window", [2 ** 31 - 1, 2 ** 31 - 40, 600])
+def test_attention_of_more_queries_than_tokens(vbq, window):
+    """Queries before position 0 see nothing, and do not disturb the others, whatever the window."""
+    rng = np.random.default_rng(8)
+    for ratio, lens, news in ((4, [3, 500, 0], [5, 8, 2]), (4, [50, 700], [60, 90])):
+        attend(vbq, rng, 1, ratio, 64, 32, lens, news, window=window, sinks=2)
+
+
 def test_attention_in_pieces_and_whole(vbq):
     """A long sequence is split over workgroups, beside short ones that are not."""
     rng = np.random.default_rng(5)
