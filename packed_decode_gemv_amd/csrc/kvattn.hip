@@ -43,7 +43,11 @@ typedef float f32x2 __attribute__((ext_vector_type(2)));
 constexpr int kWaves = 4;
 constexpr float kNoMax = -1e30f;     // running maximum before any token
 constexpr int kParts = 512;          // workgroups that a launch aims at, at most
-constexpr int kLeastPart = 8;        // blocks of a part: two a wavefront
+// Blocks of a part, at least: two a wavefront; with 32 rows, whose parts take
+// eight times the bytes of 4 rows to join, six (64 tiles of 20 rows of 80
+// blocks: parts of 11 blocks 29.3 us, of 16 29.8, of 24 26.2, of 32 28).
+template <int ROWS>
+constexpr int kLeastPart = ROWS > 16 ? 24 : 8;
 
 // Exchanges with the lanes 16 and 32 apart (the lane quarters of a column).
 typedef uint32_t pair_t __attribute__((ext_vector_type(2)));
@@ -320,7 +324,7 @@ __global__ __launch_bounds__(64 * kWaves, (kRoomy<G, ROWS>) ? 4 : G * ROWS > 64 
       }
     }
     const int chunk = max((int)(((uint32_t)total * (uint32_t)a.cache.heads + (uint32_t)a.parts - 1u) / (uint32_t)a.parts),
-                          kLeastPart);
+                          kLeastPart<ROWS>);
     int before = 0, incl, n, size;   // of each lane's sequence: parts up to its end, parts of a tile, blocks of a part
     uint64_t past;
     for (int base = 0;; base += 64) {
@@ -774,13 +778,21 @@ __global__ __launch_bounds__(64 * kWaves, (kRoomy<G, ROWS>) ? 4 : G * ROWS > 64 
     const int row = (int)tid / ROW_LANES, j = (int)tid % ROW_LANES;
     float low = -kNoMax, sum = 0.f;   // sum is held times 2^low
     if (row < rows) {
-#pragma unroll 8
-      for (int p = j; p < parts; p += ROW_LANES) {
-        const f32x2 v = get2(ml0 + (p * ROWS + row) * 2);
-        factor[row * kParts + p] = v.x;
-        const float to = fminf(low, v.x);
-        sum = __builtin_fmaf(sum, __builtin_amdgcn_exp2f(to - low), v.y * __builtin_amdgcn_exp2f(to - v.x));
-        low = to;
+      for (int p0 = j; p0 < parts; p0 += 8 * ROW_LANES) {
+        f32x2 v[8];
+#pragma unroll
+        for (int i = 0; i < 8; ++i)
+          if (i == 0 || p0 - j + i * ROW_LANES < parts)
+            v[i] = get2(ml0 + (min(p0 + i * ROW_LANES, parts - 1) * ROWS + row) * 2);
+#pragma unroll
+        for (int i = 0; i < 8; ++i) {
+          const int p = p0 + i * ROW_LANES;
+          if (p >= parts) break;
+          factor[row * kParts + p] = v[i].x;
+          const float to = fminf(low, v[i].x);
+          sum = __builtin_fmaf(sum, __builtin_amdgcn_exp2f(to - low), v[i].y * __builtin_amdgcn_exp2f(to - v[i].x));
+          low = to;
+        }
       }
     }
     const float own = low;
@@ -798,27 +810,53 @@ __global__ __launch_bounds__(64 * kWaves, (kRoomy<G, ROWS>) ? 4 : G * ROWS > 64 
     }
   }
   __syncthreads();
-  // Threads beyond the rows' outputs share the parts.
+  // Threads beyond the rows' outputs share the parts. A thread's loads go out
+  // together, 16 at a time (where a thread's part is past the last, the last is
+  // read and left out): one by one they took 6 of 28 us for 64 tiles of 20 rows
+  // in 4 parts.
+  constexpr int ROUNDS = ROWS * D / 4 > THREADS ? ROWS * D / 4 / THREADS : 1, BATCH = 16 / ROUNDS;
   const int ne = rows * (D / 4), shares = ne <= THREADS / 2 ? THREADS / ne : 1;
-  for (int e0 = 0; e0 < ne; e0 += THREADS) {
-    const int e = shares > 1 ? (int)tid % ne : e0 + (int)tid, share_no = shares > 1 ? (int)tid / ne : 0;
-    const int row = e / (D / 4), c = e % (D / 4);
-    f32x4 v = {0.f, 0.f, 0.f, 0.f};
-    if (e < ne && share_no < shares) {
-#pragma unroll 16
-      for (int p = share_no; p < parts; p += shares) {
-        const float* const q = acc0 + (p * ROWS + row) * D + 4 * c;
-        const f32x2 x = get2(q), y = get2(q + 2);
-        v += f32x4{x.x, x.y, y.x, y.y} * factor[row * kParts + p];
+  const int e0 = shares > 1 ? (int)tid % ne : (int)tid, share_no = shares > 1 ? (int)tid / ne : 0;
+  f32x4 v[ROUNDS];
+  const float* from[ROUNDS];
+#pragma unroll
+  for (int k = 0; k < ROUNDS; ++k) {
+    v[k] = f32x4{0.f, 0.f, 0.f, 0.f};
+    const int e = min(e0 + k * THREADS, ne - 1);
+    from[k] = acc0 + e / (D / 4) * D + 4 * (e % (D / 4));
+  }
+  if (share_no < shares)
+    for (int p0 = share_no; p0 < parts; p0 += BATCH * shares) {
+      f32x2 x[BATCH][ROUNDS], y[BATCH][ROUNDS];
+#pragma unroll
+      for (int i = 0; i < BATCH; ++i)
+#pragma unroll
+        for (int k = 0; k < ROUNDS; ++k) {
+          if (i && p0 - share_no + i * shares >= parts) continue;
+          const float* const q = from[k] + min(p0 + i * shares, parts - 1) * (ROWS * D);
+          x[i][k] = get2(q);
+          y[i][k] = get2(q + 2);
+        }
+#pragma unroll
+      for (int i = 0; i < BATCH; ++i) {
+        const int p = p0 + i * shares;
+        if (p >= parts) break;
+#pragma unroll
+        for (int k = 0; k < ROUNDS; ++k)
+          v[k] += f32x4{x[i][k].x, x[i][k].y, y[i][k].x, y[i][k].y} *
+                  factor[min(e0 + k * THREADS, ne - 1) / (D / 4) * kParts + p];
       }
     }
-    if (shares > 1) {
-      share[tid] = v;
-      __syncthreads();
-      if (share_no == 0)
-        for (int i = 1; i < shares; ++i) v += share[e + i * ne];
-    }
-    if (e < ne && share_no == 0) answer4<D>(a, c0, head, row, c, v, wml[0][row][1], wml[0][row][0]);
+  if (shares > 1) {   // (then a thread has one output at most: ne <= THREADS / 2)
+    share[tid] = v[0];
+    __syncthreads();
+    if (share_no == 0)
+      for (int i = 1; i < shares; ++i) v[0] += share[e0 + i * ne];
+  }
+#pragma unroll
+  for (int k = 0; k < ROUNDS; ++k) {
+    const int e = e0 + k * THREADS, row = e / (D / 4);
+    if (e < ne && share_no == 0) answer4<D>(a, c0, head, row, e % (D / 4), v[k], wml[0][row][1], wml[0][row][0]);
   }
 }
 
