@@ -21,8 +21,9 @@
  *   - Ownership: the caller allocates and frees every buffer it passes. The
  *     library allocates nothing, keeps no state between calls (apart from
  *     cached device attributes) and needs no workspace: partial sums stay
- *     on-chip inside a workgroup. The calls can therefore be captured into a
- *     HIP graph as they are. Buffers marked "device" live in GPU memory of
+ *     on-chip inside a workgroup. (vbq_gemv_batched_static keeps a scratch
+ *     array, kv4_attention takes a workspace from the caller.) The calls can
+ *     therefore be captured into a HIP graph as they are. Buffers marked "device" live in GPU memory of
  *     the current HIP device; "host" buffers are ordinary CPU memory.
  *   - Asynchrony: compute calls enqueue work on `stream` and return without
  *     waiting. Argument errors are found before anything is enqueued: the
@@ -391,11 +392,21 @@ vbq_status kv4_read(const vbq_kv4* cache, const vbq_kv4_range* r, void* k, void*
  * i of n is at p = kv_lens[b] - n + i. It sees j < kv_lens[b] with
  *   causal:  j <= p
  *   window:  j > p - window or j < sinks     (window > 0, causal only)
- * A row that sees nothing gives zeros (and lse = -infinity).
- * Scores are sums of products of q (fp16, or bf16) with the exact codes in
- * fp32, scaled and offset in fp32; the softmax is held in fp32; probabilities
- * and the values held are rounded to fp16 for the product with fp32 sums.
- * Results repeat bit for bit for the same sizes. */
+ * A row that sees nothing gives zeros (and lse = -infinity). A NaN or infinity
+ * in q reaches the outputs of its own row only.
+ * Scores are sums in fp32 of products of q with the exact codes; scale, offset
+ * and softmax are fp32. A row of q is scaled by a power of two that brings its
+ * largest number to [2^13, 2^14) and held in fp16: numbers down to 2^-23 (fp16)
+ * or 2^-26 (bf16) of that largest one keep every bit, smaller ones lose their
+ * low bits.
+ * The product with the values depends on the rows that share a head's tokens,
+ * max_q * n_heads / n_kv_heads:
+ *   up to 32: exact codes times p s (p the probability, s the token's scale in
+ *     the group), p s as the sum of two fp16 numbers, offsets in fp32;
+ *   more: values rounded once to fp16, p rounded to fp16; for fp16 outputs what
+ *     that rounding leaves of p is multiplied too.
+ * All sums are fp32. Results repeat bit for bit for the same sizes (max_q and
+ * max_kv among them: they decide how the work is cut). */
 typedef struct vbq_kv4_attn {
   int32_t batch;          /* 1 .. 65535 */
   int32_t table_width;

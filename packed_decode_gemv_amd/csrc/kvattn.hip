@@ -1,11 +1,14 @@
 // Attention over the 4-bit key/value cache (layout and meaning in vbq.h).
 //
 // Rows are the (query token, query head) pairs that share a key/value head:
-// row r of a sequence is query r / ratio, head r % ratio of the group. A
-// workgroup of four wavefronts takes one row tile and one piece of the token
-// axis; wavefront w takes every fourth block of 32 tokens and keeps its own
-// running maximum, sum and output in registers. The wavefronts are joined in
-// LDS, the pieces in the workspace by the last workgroup that finishes.
+// row r of a sequence is query r / ratio, head r % ratio of the group. Up to 32
+// rows a sequence and head take k_kv4_attn, more k_kv4_attn_tile (below).
+//
+// k_kv4_attn: a workgroup of four wavefronts takes a tile (all rows of one
+// sequence and head), or a part of its token axis; wavefront w takes every
+// fourth block of 32 tokens and keeps its own running maximum, sum and output in
+// registers. The wavefronts are joined in LDS, the parts in the workspace by
+// the last workgroup that finishes.
 //
 // Scores. S^T = K Q^T by 16x16x32 fp16 MFMAs: A is a block's key codes, 16
 // tokens by 32 channels of one group, B the queries. A code word holds eight
@@ -14,8 +17,8 @@
 // meet the latter are divided by 16). The group's scale and offset enter in
 // fp32: score = sum_g s_g (codes . q)_g + o_g sum_g(q).
 // Queries are scaled to a largest magnitude in [2^13, 2^14) per row (a power
-// of two, undone in the score), so fp16 holds bf16 queries exactly down to
-// 2^-28 of the row's largest.
+// of two, undone in the score), so that fp16 holds them exactly down to 2^-26
+// (bf16; 2^-23 fp16) of the row's largest, the odd pairs' 1/16 included.
 //
 // Output. O^T = V^T P^T by the same MFMA: A is the value codes, 16 channels by
 // 32 tokens, again as fp16 subnormals; B the probabilities as they come out of
@@ -31,6 +34,17 @@
 // queries, so every lane has every score of its row: lane part 0 .. 1 (0 .. 3)
 // takes the scores of a half (quarter) of its octet's tokens, and scale,
 // softmax and split are done once per score, not two (four) times.
+//
+// Bounds, heads of 128. 4 rows, 32 sequences of 167000 tokens in all, 8 heads:
+// 193 MB in 50 us (3.9 TB/s; a copy reaches 5.0). By clock stamps 4.5 us pass
+// until the first block is there (arguments, lengths, table, block: each waits
+// for the one before) and 2 and 3 us in the joins in LDS and in the workspace;
+// with the launch that leaves about 38 us, 5.1 TB/s, for the blocks. One
+// sequence of 131072 tokens: 151 MB in 42 us, 64 parts a tile to join.
+// 16 heads of 16 sequences under a window of 1024: 38 MB in 14 us, the chain of
+// dependent look-ups. 20 rows, 8 sequences of 20000 tokens in all, 8 heads: 24 MB
+// in 26 us; 1.8 us a block and wavefront (a wavefront a SIMD: vector
+// instructions and their latency), 4.6 us before the first, 7 us for the joins.
 #include "kv4.h"
 
 namespace vbq {
@@ -866,12 +880,27 @@ __global__ __launch_bounds__(64 * kWaves, (kRoomy<G, ROWS>) ? 4 : G * ROWS > 64 
 // wavefront), and multiplied by every wavefront with 32x32x16 MFMAs: S^T = K
 // Q^T, O^T = V^T P^T. One turn of the loop spreads block i + 2, forms the
 // scores of block i + 1 and the probabilities and output of block i, in one
-// straight piece of code, so that matrix and vector instructions overlap. Key operands are the exact codes
-// (fp16 subnormals), scores take scale in fp32 as above and offsets by one more
-// MFMA: A holds a token's offsets o_g, B the rows' sums of q over group g.
-// Rounding keys to fp16 instead would save the scaling, but a score's error is
-// multiplied into its probability: it doubled the output's error in fp16.
-// Values are s c + o rounded to fp16, as are probabilities.
+// straight piece of code, so that matrix and vector instructions overlap. Key
+// operands are the exact codes (fp16 subnormals), scores take scale in fp32 as
+// above and offsets by one more MFMA: A holds a token's offsets o_g, B the rows'
+// sums of q over group g. Rounding keys to fp16 instead would save the scaling,
+// but a score's error is multiplied into its probability: it doubled the
+// output's error in fp16. Values are s c + o rounded once to fp16, as are
+// probabilities; for fp16 outputs (FINE) what is left of a probability is
+// multiplied too: without it the outputs of 2500 rows under a window of 500
+// were off by 3.2e-4 (relative, whole tensor), with it by 2.8e-4, of which
+// 2.1e-4 are the rounding of the output itself; bf16 outputs are off by 1.7e-3
+// either way.
+//   Bounds. 2048 bf16 queries of 32 heads of 128 over 10240 tokens: 309 GFLOP in
+// 430 us, 0.72 PFLOP/s (a library product of 8192^3 reaches 1.37). A turn of
+// one wavefront is 17 MFMAs (544 cycles), about 150 vector instructions (850
+// cycles) and 28 KB of LDS reads (220 cycles of the CU, times 8 wavefronts),
+// and two wavefronts a SIMD overlap them in part. Heads of 256 have registers
+// for one wavefront a SIMD: 3 sequences under a window of 500, 36 GFLOP in 155 us;
+// 2.3 us a block, 7 us before the first and 2 us after the last, and 630
+// workgroups on 256 CUs end in a third round. (64 rows a wavefront: 536 against
+// 447 us. Reads of a group ahead of its products, held there by scheduling
+// barriers: no change.)
 // In LDS keys and values lie as the operands are read, 16 bytes a lane:
 //   keys:   chunk (channel / 8, row R), the 8 channels as pairs (n, n + 4);
 //           token 8 (2 A + h) + 4 u + b is row 8 (2 A + u) + 4 h + b, so the
