@@ -55,7 +55,18 @@ typedef float f32x4 __attribute__((ext_vector_type(4)));
 typedef float f32x2 __attribute__((ext_vector_type(2)));
 
 constexpr int kWaves = 4;
-constexpr float kNoMax = -1e30f;     // running maximum before any token
+constexpr float kNoMax = -3e38f;     // running maximum before any token
+// Probabilities are 2^(score * to_log2 - m) in one fma. m is a rounded product,
+// so beyond 2^22 the exact product may pass it by more than a quarter, and
+// beyond 2^31 by more than exp2 holds. Where a running maximum lies so far out,
+// products are rounded first and m subtracted from them.
+constexpr float kFar = 0x1p22f;
+__device__ inline bool is_far(float m) { return m != kNoMax && fabsf(m) > kFar; }
+__device__ inline float below(float score, float to_log2, float m) {
+  float t = score * to_log2;
+  asm("" : "+v"(t));   // (not one fma)
+  return t - m;
+}
 constexpr int kParts = 512;          // workgroups that a launch aims at, at most
 // Blocks of a part, at least: two a wavefront; with 32 rows, whose parts take
 // eight times the bytes of 4 rows to join, six (64 tiles of 20 rows of 80
@@ -482,6 +493,8 @@ __global__ __launch_bounds__(64 * kWaves, (kRoomy<G, ROWS>) ? 4 : G * ROWS > 64 
   // and (times 2^-24) of p s code.
   float m[NT], base[NT], l[NT][ODD], po[NT][G][ODD];
   f32x4 acc[NT][G][4];
+  float mul[NT], add[NT];   // of a score on its way to exp2
+  bool far = false;         // a row of the wavefront has its maximum far out
   float shift[NT];   // S of the lane's row
   int limit[NT];     // largest scale that S is fit for (bits of an fp16)
 #pragma unroll
@@ -490,6 +503,8 @@ __global__ __launch_bounds__(64 * kWaves, (kRoomy<G, ROWS>) ? 4 : G * ROWS > 64 
     limit[nt] = -1;
     m[nt] = kNoMax;
     base[nt] = -kNoMax;
+    mul[nt] = to_log2[nt];
+    add[nt] = base[nt];
 #pragma unroll
     for (int d = 0; d < ODD; ++d) l[nt][d] = 0.f;
 #pragma unroll
@@ -645,6 +660,23 @@ __global__ __launch_bounds__(64 * kWaves, (kRoomy<G, ROWS>) ? 4 : G * ROWS > 64 
           for (int w = 0; w < 4; ++w) acc[nt][g][w] *= f;
         }
       }
+      bool out = false;
+#pragma unroll
+      for (int nt = 0; nt < NT; ++nt) out |= is_far(m[nt]);
+      far = __any(out);
+#pragma unroll
+      for (int nt = 0; nt < NT; ++nt) {
+        mul[nt] = far ? 1.f : to_log2[nt];
+        add[nt] = far ? shift[nt] : base[nt];
+      }
+    }
+    if (far) {
+#pragma unroll
+      for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+        for (int j = 0; j < PAIRS; ++j)
+#pragma unroll
+          for (int h = 0; h < 2; ++h) sc[nt][j][h] = below(sc[nt][j][h], to_log2[nt], m[nt]);
     }
     // Probabilities times 2^S, those of odd pairs divided by 16.
     float p[NT][PAIRS][2];
@@ -652,9 +684,9 @@ __global__ __launch_bounds__(64 * kWaves, (kRoomy<G, ROWS>) ? 4 : G * ROWS > 64 
     for (int nt = 0; nt < NT; ++nt)
 #pragma unroll
       for (int j = 0; j < PAIRS; ++j) {
-        const float bs = base[nt] + (PARTS == 4 ? lane_odd : j & 1 ? -4.f : 0.f);
+        const float bs = add[nt] + (PARTS == 4 ? lane_odd : j & 1 ? -4.f : 0.f);
 #pragma unroll
-        for (int h = 0; h < 2; ++h) p[nt][j][h] = __builtin_amdgcn_exp2f(__builtin_fmaf(sc[nt][j][h], to_log2[nt], bs));
+        for (int h = 0; h < 2; ++h) p[nt][j][h] = __builtin_amdgcn_exp2f(__builtin_fmaf(sc[nt][j][h], mul[nt], bs));
         l[nt][j % ODD] += p[nt][j][0] + p[nt][j][1];
       }
 #pragma unroll
@@ -1163,6 +1195,7 @@ __global__ __launch_bounds__(256, G >= 3 ? 1 : 2) void k_kv4_attn_tile(KvAttn a)
 
   // Running maximum, sum of p times 2^(kTileShift - m), sums of p v; mx: a block's maximum.
   float m = kNoMax, l = 0.f, mx;
+  bool far = false;   // a row of the wavefront has its maximum far out
   f32x16 acc[TILES];
 #pragma unroll
   for (int t = 0; t < TILES; ++t) acc[t] = none;
@@ -1214,9 +1247,16 @@ __global__ __launch_bounds__(256, G >= 3 ? 1 : 2) void k_kv4_attn_tile(KvAttn a)
     // The inner loop runs while no row's scores pass its running maximum by
     // more than the slack: it has no vector arithmetic on the sums, so they
     // stay in accumulation registers.
+    auto settle_far = [&]() {
+#pragma unroll
+      for (int j = 0; j < 16; ++j) sc[j] = below(sc[j], to_log2, m);
+    };
     for (int i = 0; i < blocks;) {
       const float mt = fmaxf(m, mx), f = __builtin_amdgcn_exp2f(m - mt);
       m = mt;
+      far = __any(is_far(m));
+      if (far) settle_far();
+      const float mul = far ? 1.f : to_log2, base = far ? kTileShift : kTileShift - m;
       l *= f;
 #pragma unroll
       for (int t = 0; t < TILES; ++t) acc[t] *= f;
@@ -1229,13 +1269,12 @@ __global__ __launch_bounds__(256, G >= 3 ? 1 : 2) void k_kv4_attn_tile(KvAttn a)
         scores(i + 1, next);
         half8_t pf[2], pl[2];   // probabilities, and what their rounding leaves
         const half2_t ones = {(_Float16)1.f, (_Float16)1.f};
-        const float base = kTileShift - m;
 #pragma unroll
         for (int A = 0; A < 2; ++A)
 #pragma unroll
           for (int j = 0; j < 4; ++j) {
-            const float p0 = __builtin_amdgcn_exp2f(__builtin_fmaf(sc[8 * A + j], to_log2, base));
-            const float p1 = __builtin_amdgcn_exp2f(__builtin_fmaf(sc[8 * A + 4 + j], to_log2, base));
+            const float p0 = __builtin_amdgcn_exp2f(__builtin_fmaf(sc[8 * A + j], mul, base));
+            const float p1 = __builtin_amdgcn_exp2f(__builtin_fmaf(sc[8 * A + 4 + j], mul, base));
             const half2_t pr = {(_Float16)p0, (_Float16)p1};
             pf[A][2 * j] = pr.x;
             pf[A][2 * j + 1] = pr.y;
@@ -1260,6 +1299,7 @@ __global__ __launch_bounds__(256, G >= 3 ? 1 : 2) void k_kv4_attn_tile(KvAttn a)
         sc = next;
         ++i;
         if (i < blocks) pass = settle(i, hide, sc);
+        if (far && !pass) settle_far();   // (in the outer loop otherwise)
       } while (i < blocks && !pass);
     }
   }

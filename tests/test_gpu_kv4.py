@@ -494,6 +494,45 @@ def test_attention_of_peaked_and_flat_scores(vbq):
     attend(vbq, rng, 1, 4, 128, 64, [300], [20], gain=12.0)
 
 
+@pytest.mark.parametrize("dtype,gain", [("float16", 6e4), ("bfloat16", 1e5), ("bfloat16", 1e28)])
+@pytest.mark.parametrize("dim,ratio,new", [(64, 4, 1), (128, 7, 4), (64, 4, 30), (256, 2, 40)])
+def test_attention_of_scores_far_out(vbq, dtype, gain, dim, ratio, new):
+    """Queries and keys at the end of their ranges: the largest score takes the row, as long as fp32 holds it.
+    A score is off by (D + 16) u times the sum of its terms' magnitudes at most (u = 2^-24, one more rounding by
+    to_log2): rows whose two largest scores are nearer than 8 times that say nothing and are left out."""
+    import torch
+    gen = torch.Generator(device="cuda").manual_seed(dim + new)
+    i32 = dict(dtype=torch.int32, device="cuda")
+    L = 1500 if new < 10 else 200
+    k = ((torch.rand(L, 1, dim, generator=gen, device="cuda") - 0.5) * 122880).float()
+    v = torch.randn(L, 1, dim, generator=gen, device="cuda")
+    q = ((torch.rand(new, ratio, dim, generator=gen, device="cuda") - 0.5) * 2 * gain).to(getattr(torch, dtype))
+    cache = vbq.Kv4Cache(64, 32, 1, dim)
+    table, cu = torch.arange(64, **i32).view(1, 64), torch.tensor([0, L], **i32)
+    vbq.kv4_append(cache, k, v, table, torch.zeros(1, **i32), cu)
+    rk, rv = (x.double()[:, 0] for x in vbq.kv4_read(cache, table, torch.zeros(1, **i32), cu, L, torch.float32))
+    lse = torch.empty(new, ratio, device="cuda")
+    got = vbq.kv4_attention(cache, q, table, torch.tensor([L], **i32), torch.tensor([0, new], **i32), new, L, lse=lse)
+    assert torch.isfinite(got).all() and torch.isfinite(lse).all()
+    out_h = 2.0 ** -11 if dtype == "float16" else 2.0 ** -8
+    used = 0
+    for i in range(new):
+        for r in range(ratio):
+            p = L - new + i + 1
+            qd = q[i, r].double()
+            s = rk[:p] @ qd * dim ** -0.5
+            # keys are s c + o with |o| and |s c| up to twice the key's range
+            off = (dim + 17) * 2.0 ** -24 * float(qd.abs().sum() * 4 * rk.abs().max()) * dim ** -0.5
+            top = torch.topk(s, 2).values
+            assert abs(float(lse[i, r]) - float(top[0])) <= off + 2.0 ** -22 * abs(float(top[0]))
+            if float(top[0] - top[1]) < 8 * off + 40:
+                continue
+            used += 1
+            want = rv[int(s.argmax())]
+            assert ((got[i, r].double() - want).abs() <= (out_h + 2.1 * 2.0 ** -11) * want.abs() + 2.0 ** -24).all()
+    assert used * 2 >= new * ratio
+
+
 def test_attention_repeats_and_strided_queries_agree(vbq):
     import torch
     rng = np.random.default_rng(7)
