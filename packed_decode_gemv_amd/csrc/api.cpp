@@ -125,7 +125,7 @@ vbq_status check_attn(const vbq_kv4* cache, const vbq_kv4_attn* a, bool pointers
   if ((int64_t)a->max_q * ratio > INT32_MAX - 64) return VBQ_ERR_UNSUPPORTED;
   if (a->max_kv > INT32_MAX - 64) return VBQ_ERR_UNSUPPORTED;
   *p = kv4_attn_plan(a->batch, cache->n_kv_heads, ratio, c->groups, a->max_q, a->max_kv, a->window, a->sinks);
-  *bytes = p->parts ? VBQ_KV4_COUNTERS * 4 + p->grid * p->rows * (cache->head_dim + 2) * 4 : 0;
+  *bytes = p->places ? VBQ_KV4_COUNTERS * 4 + p->places * p->rows * (cache->head_dim + 2) * 4 : 0;
   return VBQ_OK;
 }
 
@@ -200,7 +200,7 @@ vbq_status kv4_attention(const vbq_kv4* cache, const vbq_kv4_attn* a, hipStream_
   k.lse = a->lse;
   k.counters = static_cast<uint32_t*>(a->workspace);
   k.acc = static_cast<float*>(a->workspace) + VBQ_KV4_COUNTERS;
-  k.ml = k.acc + p.grid * p.rows * cache->head_dim;
+  k.ml = k.acc + p.places * p.rows * cache->head_dim;
   k.width = a->table_width;
   k.total_q = a->total_q;
   k.max_q = a->max_q;

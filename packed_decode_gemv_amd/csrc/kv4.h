@@ -58,7 +58,8 @@ struct KvAttn {
   int32_t bf16, causal, window, sinks;
   int32_t ratio_inv;           // ceil(65536 / ratio)
   int32_t batch;
-  int32_t parts;               // that long tiles are cut into in all, about (0: no cuts, a workgroup a tile)
+  int32_t parts;               // up to 32 rows: that long tiles are cut into in all, about (0: no cuts, a
+                               // workgroup a tile); more rows: that each tile is cut into, at most
   float scale_log2;            // scale * log2(e)
 };
 
@@ -66,10 +67,10 @@ hipError_t launch_kv4_append(const KvCache& c, const KvRange& r, const void* k, 
                              int64_t k_ts, int64_t k_hs, int64_t v_ts, int64_t v_hs, hipStream_t s);
 hipError_t launch_kv4_read(const KvCache& c, const KvRange& r, void* k, void* v, int dtype, hipStream_t s);
 // Sizes of an attention launch, from the call's sizes alone: rows of a tile,
-// parts (as above), tiles and workgroups.
+// parts (as above), tiles, workgroups, and places for sums in the workspace.
 struct KvAttnPlan {
   int32_t rows, parts;
-  int64_t tiles, grid;
+  int64_t tiles, grid, places;
 };
 KvAttnPlan kv4_attn_plan(int batch, int heads, int ratio, int groups, int max_q, int max_kv, int window, int sinks);
 hipError_t launch_kv4_attention(const KvAttn& a, const KvAttnPlan& p, int batch, hipStream_t s);

@@ -985,9 +985,21 @@ __device__ inline float half_sum(float v) {
   return __builtin_bit_cast(float, x) + __builtin_bit_cast(float, y);
 }
 
+// Blocks that a tile's rows r0 .. look at, and how many of them a part takes.
+constexpr int kRowTile = 128;
+__device__ inline Reach tile_reach(const KvAttn& a, const Seq& sq, int rows, int r0) {
+  const int r1 = min(rows, r0 + kRowTile);
+  return reach(sq.len, a.causal ? sq.first + r0 / a.ratio : sq.len - 1,
+               a.causal ? sq.first + (r1 - 1) / a.ratio : sq.len - 1, a.window, a.sinks);
+}
+constexpr int kLeastTilePart = 8, kTileParts = 64;
+__device__ inline int part_blocks(const KvAttn& a, const Reach& re) {
+  return max((int)((uint32_t)(re.ns + re.nw + a.parts - 1) / (uint32_t)a.parts), kLeastTilePart);
+}
+
 template <int G, bool FINE>
 __global__ __launch_bounds__(256, G >= 3 ? 1 : 2) void k_kv4_attn_tile(KvAttn a) {
-  constexpr int WAVES = 4, ROWS = 32 * WAVES, D = 64 * G, BYTES = kKvGroupBytes * G, RAW = 4, TILES = D / 32;
+  constexpr int WAVES = 4, ROWS = kRowTile, D = 64 * G, BYTES = kKvGroupBytes * G, RAW = 4, TILES = D / 32;
   constexpr int SHARE = BYTES / WAVES;   // a wavefront's part of a block's copy
   constexpr int COPIES = (SHARE + 1023) / 1024;
   constexpr int HELD = 32 * D * 2;   // a block's keys, or values
@@ -1013,11 +1025,14 @@ __global__ __launch_bounds__(256, G >= 3 ? 1 : 2) void k_kv4_attn_tile(KvAttn a)
   const int rt = rts - 1 - (int)(blockIdx.x / bh_n);
   if (rt < 0) return;
   const int len = sq.len, first = sq.first;
-  const int r0 = rt * ROWS, r1 = min(rows, r0 + ROWS);
-  const Reach re = reach(len, a.causal ? first + r0 / a.ratio : len - 1,
-                         a.causal ? first + (r1 - 1) / a.ratio : len - 1, a.window, a.sinks);
-  const int blocks = re.ns + re.nw;
-  auto block_of = [&](int i) { return i < re.ns ? i : i - re.ns + re.w0; };
+  const int r0 = rt * ROWS;
+  const Reach re = tile_reach(a, sq, rows, r0);
+  // this workgroup's part: blocks i0 .. i0 + blocks - 1 of the tile
+  const int per = part_blocks(a, re), i0 = (int)blockIdx.y * per;
+  const int blocks = min(re.ns + re.nw - i0, per);
+  const bool whole = re.ns + re.nw <= per;
+  if (i0 && blocks <= 0) return;
+  auto block_of = [&](int i) { return i0 + i < re.ns ? i0 + i : i0 + i - re.ns + re.w0; };
 
   // Copies: lane i keeps the page of block i of 64.
   const uint32_t in_page = (1u << a.cache.block_shift) - 1u;
@@ -1307,6 +1322,21 @@ __global__ __launch_bounds__(256, G >= 3 ? 1 : 2) void k_kv4_attn_tile(KvAttn a)
   const float sum = half_sum(l);
   const int r = w_r0 + (int)col, qi = r / a.ratio, hh = r - qi * a.ratio;
   if (r >= rows) return;
+  if (!whole) {   // sums, and 2^base that they are held times
+    const int64_t place = ((int64_t)blockIdx.x * a.parts + blockIdx.y) * ROWS + (r - r0);
+    float* const to = a.acc + place * D;
+#pragma unroll
+    for (int g = 0; g < G; ++g)
+#pragma unroll
+      for (int u = 0; u < 2; ++u)
+#pragma unroll
+        for (int bb = 0; bb < 4; ++bb)
+          *reinterpret_cast<f32x4*>(to + 64 * g + 4 * (8 * u + 4 * (int)half + bb)) =
+              f32x4{acc[2 * g][4 * u + bb], acc[2 * g][8 + 4 * u + bb], acc[2 * g + 1][4 * u + bb],
+                    acc[2 * g + 1][8 + 4 * u + bb]};
+    if (half == 0) *reinterpret_cast<f32x2*>(a.ml + 2 * place) = f32x2{kTileShift - m, sum};
+    return;
+  }
   const float inv = sum > 0.f ? 1.f / sum : sum == 0.f ? 0.f : sum;   // 0: nothing seen; NaN stays
   const int64_t o = (int64_t)(sq.c0 + qi) * a.n_heads + head * a.ratio + hh;
 #pragma unroll
@@ -1322,6 +1352,49 @@ __global__ __launch_bounds__(256, G >= 3 ? 1 : 2) void k_kv4_attn_tile(KvAttn a)
   if (a.lse && half == 0) a.lse[o] = (__builtin_amdgcn_logf(sum) + m - kTileShift) * kLn2;
 }
 
+// Joins the parts of the tiles that were cut: blockIdx.x is the tile as above, a
+// thread takes four channels of a row. A launch of its own, since a tile's sums
+// are up to 128 rows times 64 parts: one workgroup a tile would read for longer
+// than the parts take.
+template <int G>
+__global__ __launch_bounds__(256) void k_kv4_attn_join(KvAttn a) {
+  constexpr int D = 64 * G;
+  const uint32_t bh_n = (uint32_t)(a.batch * a.cache.heads);
+  const uint32_t bh = blockIdx.x % bh_n;
+  const int b = (int)(bh / (uint32_t)a.cache.heads), head = (int)(bh % (uint32_t)a.cache.heads);
+  Seq sq;
+  if (!seq_from(a, a.cu[b], a.cu[b + 1], a.lens[b], sq)) return;
+  const int rows = sq.nq * a.ratio, rts = (rows + kRowTile - 1) / kRowTile;
+  const int rt = rts - 1 - (int)(blockIdx.x / bh_n);
+  if (rt < 0) return;
+  const int e = (int)(blockIdx.y * 256 + threadIdx.x), in_tile = e / (D / 4), c = e % (D / 4);
+  const int r = rt * kRowTile + in_tile;
+  if (r >= rows) return;
+  const Reach re = tile_reach(a, sq, rows, rt * kRowTile);
+  const int per = part_blocks(a, re), parts = (re.ns + re.nw + per - 1) / per;
+  if (parts <= 1) return;
+  const int64_t place = (int64_t)blockIdx.x * a.parts * kRowTile + in_tile;
+  const float* const ml = a.ml + 2 * place;
+  const float* const acc = a.acc + place * D + 4 * c;
+  float low = -kNoMax;
+#pragma unroll 4
+  for (int p = 0; p < parts; ++p) low = fminf(low, ml[p * (2 * kRowTile)]);
+  f32x4 v = {0.f, 0.f, 0.f, 0.f};
+  float sum = 0.f;
+#pragma unroll 4
+  for (int p = 0; p < parts; ++p) {
+    const f32x2 x = *reinterpret_cast<const f32x2*>(ml + p * (2 * kRowTile));
+    const float f = __builtin_amdgcn_exp2f(low - x.x);
+    sum = __builtin_fmaf(x.y, f, sum);
+    v += *reinterpret_cast<const f32x4*>(acc + (int64_t)p * (kRowTile * D)) * f;
+  }
+  const int qi = r / a.ratio, hh = r - qi * a.ratio;
+  const int64_t o = (int64_t)(sq.c0 + qi) * a.n_heads + head * a.ratio + hh;
+  const float inv = sum > 0.f ? 1.f / sum : sum == 0.f ? 0.f : sum;   // 0: nothing seen; NaN stays
+  store4(a, o * D + 4 * c, v * inv);
+  if (a.lse && c == 0) a.lse[o] = (__builtin_amdgcn_logf(sum) - low) * kLn2;
+}
+
 }  // namespace
 
 // Rows a tile takes: columns of one MFMA tile, or two tiles; above 32 the tile
@@ -1333,20 +1406,24 @@ __global__ __launch_bounds__(256, G >= 3 ? 1 : 2) void k_kv4_attn_tile(KvAttn a)
 KvAttnPlan kv4_attn_plan(int batch, int heads, int ratio, int groups, int max_q, int max_kv, int window, int sinks) {
   KvAttnPlan p;
   const int64_t rows = (int64_t)max_q * ratio;
+  int64_t blocks = ((int64_t)max_kv + kKvBlock - 1) / kKvBlock;
+  if (window) {   // (a tile's rows: at most 128 queries)
+    const int64_t most = ((int64_t)sinks + window + (max_q < kRowTile ? max_q : kRowTile)) / kKvBlock + 3;
+    blocks = blocks < most ? blocks : most;
+  }
   if (rows > 32) {   // many rows: the tile kernel
-    p.rows = 128;
+    p.rows = kRowTile;
     p.tiles = (int64_t)batch * heads * ((rows + p.rows - 1) / p.rows);
-    p.parts = 0;
+    // Where tiles leave places on the chip (two workgroups a CU, one with large heads), parts fill them.
+    const int64_t fill = (groups <= 2 ? 512 : 256) / (p.tiles ? p.tiles : 1), most = blocks / kLeastTilePart;
+    const int64_t parts = fill < most ? fill : most;
+    p.parts = (int32_t)(parts < 1 ? 1 : parts < kTileParts ? parts : kTileParts);
+    p.places = p.parts > 1 ? p.tiles * p.parts : 0;
     p.grid = p.tiles;
     return p;
   }
   p.rows = rows <= 4 ? 4 : rows <= 8 ? 8 : rows <= 16 ? 16 : 32;
   p.tiles = (int64_t)batch * heads;
-  int64_t blocks = ((int64_t)max_kv + kKvBlock - 1) / kKvBlock;
-  if (window) {
-    const int64_t most = ((int64_t)sinks + window + max_q) / kKvBlock + 3;
-    blocks = blocks < most ? blocks : most;
-  }
   // Tiles longer than total / parts are cut, so there are at most `parts` parts
   // beyond one a tile, and on average half a part a tile: the aim leaves room
   // for those where two workgroups fit a CU, so that all run at once.
@@ -1355,6 +1432,7 @@ KvAttnPlan kv4_attn_plan(int batch, int heads, int ratio, int groups, int max_q,
   const int spare = groups <= 2 && p.rows <= 8 ? 0 : (int)(p.tiles < kParts ? p.tiles : kParts) / 2;
   p.parts = cut ? kParts - spare : 0;
   p.grid = cut ? p.parts + p.tiles : p.tiles;
+  p.places = cut ? p.grid : 0;
   return p;
 }
 
@@ -1367,10 +1445,12 @@ hipError_t launch_kv4_attention(const KvAttn& a, const KvAttnPlan& p, int batch,
   else if (p.rows == 8) VBQ_CALL(G, 8, FEW);                                            \
   else if (p.rows == 16) VBQ_CALL(G, 16, ST);                                           \
   else VBQ_CALL(G, 32, ST)
-#define VBQ_TILE(G)                                              \
-  if (a.bf16) k_kv4_attn_tile<G, false><<<grid, 256, 0, s>>>(a); \
-  else k_kv4_attn_tile<G, true><<<grid, 256, 0, s>>>(a)
+#define VBQ_TILE(G)                                               \
+  if (a.bf16) k_kv4_attn_tile<G, false><<<tiles, 256, 0, s>>>(a); \
+  else k_kv4_attn_tile<G, true><<<tiles, 256, 0, s>>>(a);         \
+  if (a.parts > 1) k_kv4_attn_join<G><<<dim3((uint32_t)p.grid, kRowTile * G / 16), 256, 0, s>>>(a)
   if (p.rows > 32) {
+    const dim3 tiles((uint32_t)p.grid, (uint32_t)a.parts);
     switch (a.cache.groups) {
       case 1: VBQ_TILE(1); break;
       case 2: VBQ_TILE(2); break;

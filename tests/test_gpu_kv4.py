@@ -388,6 +388,28 @@ def test_attention_in_parts_for_every_tile(vbq, dim, ratio, new):
     attend(vbq, rng, 1, ratio, dim, 32, [1100, 0, 37], [new, 1, min(new, 2)], max_kv=1200)
 
 
+@pytest.mark.parametrize("dim", [64, 128, 192, 256])
+@pytest.mark.parametrize("dtype", ["float16", "bfloat16"])
+def test_attention_of_many_rows_in_parts(vbq, dim, dtype):
+    """More than 32 rows a head over caches long enough to be cut, and joined by a launch of its own: sequences that
+    are not cut, see nothing, or have no query beside one that is; windows; all tokens visible."""
+    rng = np.random.default_rng(dim)
+    attend(vbq, rng, 1, 4, dim, 32, [1500, 0, 90, 400], [12, 9, 0, 1], dtype)
+    attend(vbq, rng, 1, 40, dim, 64, [900], [1], dtype, causal=False)
+    attend(vbq, rng, 1, 3, dim, 64, [1100, 700], [90, 20], dtype, window=450, sinks=40)
+
+
+def test_attention_of_many_rows_in_parts_repeats(vbq):
+    import torch
+    rng = np.random.default_rng(3)
+    args, kw, out = attend(vbq, rng, 1, 8, 128, 64, [2000, 300], [8, 6], "bfloat16")
+    ws = vbq.kv4_attention_workspace(args[0], 2, 14, 8, 8, 2000)
+    assert ws.numel() > 0
+    ws[4 * vbq.KV4_COUNTERS:] = 255           # only the counters are zero before the first call
+    for _ in range(3):
+        assert torch.equal(vbq.kv4_attention(*args, workspace=ws, **kw), out)
+
+
 def test_attention_of_more_sequences_than_lanes(vbq):
     """Parts of tiles are found by scanning the sequences 64 at a time."""
     rng = np.random.default_rng(11)
