@@ -278,7 +278,11 @@ __device__ inline void answer4(const KvAttn& a, int c0, int head, int r, int c, 
 // Work is a tile (sequence, head) or a part of one: tiles longer than `chunk`
 // blocks are cut into equal parts, so that about kParts workgroups get work of
 // like size whatever the lengths are. The parts of all tiles, sequence by
-// sequence and head by head, are numbered by workgroup.
+// sequence and head by head, are numbered by workgroup. A tile of n blocks is
+// cut into sqrt(n) parts at most, since one workgroup joins them: the time of a
+// part falls with their number and that of the join grows (131072 tokens of one
+// head of 64 with 16 rows: 450 parts 72 us, 64 parts 30, 32 parts 38; 16384
+// tokens of 8 heads of 128 with 4 rows: 64 parts 22.6, 23 parts 17.3).
 struct Lanes {   // lane l: sequence base + l
   int32_t base, c0, nq, len, ns, w0, blocks;
 };
@@ -354,7 +358,8 @@ __global__ __launch_bounds__(64 * kWaves, (kRoomy<G, ROWS>) ? 4 : G * ROWS > 64 
     uint64_t past;
     for (int base = 0;; base += 64) {
       if (a.batch > 64) lanes_load(a, lane, base, false, ln);
-      n = (int)((uint32_t)(ln.blocks + chunk - 1) / (uint32_t)chunk);
+      const int most = max(chunk, (int)__builtin_amdgcn_sqrtf((float)ln.blocks));
+      n = (int)((uint32_t)(ln.blocks + most - 1) / (uint32_t)most);
       size = n > 0 ? (int)((uint32_t)(ln.blocks + n - 1) / (uint32_t)n) : 1;   // nothing to see: no part
       n = (int)((uint32_t)(ln.blocks + size - 1) / (uint32_t)size);
       incl = before + wave_scan(n * a.cache.heads);
@@ -1398,7 +1403,9 @@ __global__ __launch_bounds__(256) void k_kv4_attn_join(KvAttn a) {
 }  // namespace
 
 // Rows a tile takes: columns of one MFMA tile, or two tiles; above 32 the tile
-// kernel. Short tiles are not cut (a workgroup each, and no parts to work out
+// kernel, and above 16 for heads of 256, where two column tiles do not fit the
+// registers (8 sequences x 20 rows x 4 heads, 20206 tokens: 46 against 64 us; heads
+// of 192: 39 against 34). Short tiles are not cut (a workgroup each, and no parts to work out
 // and join): up to five blocks a wavefront, or twelve where the tiles alone fill
 // the chip. Uncut and cut, heads of 128, 4 rows: 8 tiles of 19 blocks 9.4 and
 // 10.0 us, of 29 blocks 12.0 and 10.1; 256 tiles of 38 blocks 16.4 and 18.0,
@@ -1411,7 +1418,7 @@ KvAttnPlan kv4_attn_plan(int batch, int heads, int ratio, int groups, int max_q,
     const int64_t most = ((int64_t)sinks + window + (max_q < kRowTile ? max_q : kRowTile)) / kKvBlock + 3;
     blocks = blocks < most ? blocks : most;
   }
-  if (rows > 32) {   // many rows: the tile kernel
+  if (rows > (groups == 4 ? 16 : 32)) {   // many rows: the tile kernel
     p.rows = kRowTile;
     p.tiles = (int64_t)batch * heads * ((rows + p.rows - 1) / p.rows);
     // Where tiles leave places on the chip (two workgroups a CU, one with large heads), parts fill them.
@@ -1440,16 +1447,18 @@ hipError_t launch_kv4_attention(const KvAttn& a, const KvAttnPlan& p, int batch,
   if (p.grid > INT32_MAX) return hipErrorNotSupported;
   const dim3 grid((uint32_t)p.grid);
 #define VBQ_CALL(G, ROWS, ST) k_kv4_attn<G, ROWS, ST><<<grid, 64 * kWaves, 0, s>>>(a)
-#define VBQ_CALL2(G, FEW, ST)                                                           \
-  if (p.rows == 4) VBQ_CALL(G, 4, FEW);                                                 \
-  else if (p.rows == 8) VBQ_CALL(G, 8, FEW);                                            \
-  else if (p.rows == 16) VBQ_CALL(G, 16, ST);                                           \
-  else VBQ_CALL(G, 32, ST)
+#define VBQ_CALL2(G, FEW, ST)                \
+  if (p.rows == 4) VBQ_CALL(G, 4, FEW);      \
+  else if (p.rows == 8) VBQ_CALL(G, 8, FEW); \
+  else VBQ_CALL(G, 16, ST)
+#define VBQ_CALL3(G, FEW, ST)                  \
+  if (p.rows == 32) VBQ_CALL(G, 32, ST);       \
+  else VBQ_CALL2(G, FEW, ST)
 #define VBQ_TILE(G)                                               \
   if (a.bf16) k_kv4_attn_tile<G, false><<<tiles, 256, 0, s>>>(a); \
   else k_kv4_attn_tile<G, true><<<tiles, 256, 0, s>>>(a);         \
   if (a.parts > 1) k_kv4_attn_join<G><<<dim3((uint32_t)p.grid, kRowTile * G / 16), 256, 0, s>>>(a)
-  if (p.rows > 32) {
+  if (p.rows == kRowTile) {
     const dim3 tiles((uint32_t)p.grid, (uint32_t)a.parts);
     switch (a.cache.groups) {
       case 1: VBQ_TILE(1); break;
@@ -1460,13 +1469,15 @@ hipError_t launch_kv4_attention(const KvAttn& a, const KvAttnPlan& p, int batch,
     return hipGetLastError();
   }
   switch (a.cache.groups) {
-    case 1: VBQ_CALL2(1, 4, 4); break;
-    case 2: VBQ_CALL2(2, 2, 4); break;
-    case 3: VBQ_CALL2(3, 2, 2); break;
+    case 1: VBQ_CALL3(1, 4, 4); break;
+    case 2: VBQ_CALL3(2, 2, 4); break;
+    case 3: VBQ_CALL3(3, 2, 2); break;
     default: VBQ_CALL2(4, 2, 2); break;
   }
+#undef VBQ_CALL3
 #undef VBQ_CALL2
 #undef VBQ_CALL
+#undef VBQ_TILE
   return hipGetLastError();
 }
 
