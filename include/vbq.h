@@ -401,7 +401,7 @@ vbq_status kv4_read(const vbq_kv4* cache, const vbq_kv4_range* r, void* k, void*
  * low bits.
  * The product with the values depends on the rows that share a head's tokens,
  * max_q * n_heads / n_kv_heads:
- *   up to 32: exact codes times p s (p the probability, s the token's scale in
+ *   up to 32 (16 for head_dim 256): exact codes times p s (p the probability, s the token's scale in
  *     the group), p s as the sum of two fp16 numbers, offsets in fp32;
  *   more: values rounded once to fp16, p rounded to fp16; for fp16 outputs what
  *     that rounding leaves of p is multiplied too.

@@ -2,7 +2,8 @@
 //
 // Rows are the (query token, query head) pairs that share a key/value head:
 // row r of a sequence is query r / ratio, head r % ratio of the group. Up to 32
-// rows a sequence and head take k_kv4_attn, more k_kv4_attn_tile (below).
+// rows a sequence and head (16 for heads of 256) take k_kv4_attn, more take
+// k_kv4_attn_tile (below).
 //
 // k_kv4_attn: a workgroup of four wavefronts takes a tile (all rows of one
 // sequence and head), or a part of its token axis; wavefront w takes every
