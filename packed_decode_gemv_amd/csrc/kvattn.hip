@@ -916,9 +916,10 @@ __global__ __launch_bounds__(64 * kWaves, (kRoomy<G, ROWS>) ? 4 : G * ROWS > 64 
 // Four wavefronts take 32 rows each of one head and walk the blocks together. A
 // block is copied raw to LDS, spread there into operands (a quarter by each
 // wavefront), and multiplied by every wavefront with 32x32x16 MFMAs: S^T = K
-// Q^T, O^T = V^T P^T. One turn of the loop spreads block i + 2, forms the
-// scores of block i + 1 and the probabilities and output of block i, in one
-// straight piece of code, so that matrix and vector instructions overlap. Key
+// Q^T, O^T = V^T P^T. One turn of the loop spreads the keys of block i + 2 and
+// the values of block i + 1, forms the scores of block i + 1 and the
+// probabilities and output of block i, in one straight piece of code, so that
+// matrix and vector instructions overlap. Key
 // operands are the exact codes (fp16 subnormals), scores take scale in fp32 as
 // above and offsets by one more MFMA: A holds a token's offsets o_g, B the rows'
 // sums of q over group g. Rounding keys to fp16 instead would save the scaling,
@@ -933,8 +934,10 @@ __global__ __launch_bounds__(64 * kWaves, (kRoomy<G, ROWS>) ? 4 : G * ROWS > 64 
 // 430 us, 0.72 PFLOP/s (a library product of 8192^3 reaches 1.37). A turn of
 // one wavefront is 17 MFMAs (544 cycles), about 150 vector instructions (850
 // cycles) and 28 KB of LDS reads (220 cycles of the CU, times 8 wavefronts),
-// and two wavefronts a SIMD overlap them in part. Heads of 256 have registers
-// for one wavefront a SIMD: 3 sequences under a window of 500, 36 GFLOP in 155 us;
+// and two wavefronts a SIMD overlap them in part. With values spread a block
+// later than keys two buffers do for both, and heads of 192 fit twice on a CU (17 x
+// 1193 queries, 16 heads: 462 -> 317 us). Heads of 256 have registers for one
+// wavefront a SIMD: 3 sequences under a window of 500, 36 GFLOP in 155 us;
 // 2.3 us a block, 7 us before the first and 2 us after the last, and 630
 // workgroups on 256 CUs end in a third round. (64 rows a wavefront: 536 against
 // 447 us. Reads of a group ahead of its products, held there by scheduling
@@ -1004,14 +1007,14 @@ __device__ inline int part_blocks(const KvAttn& a, const Reach& re) {
 }
 
 template <int G, bool FINE>
-__global__ __launch_bounds__(256, G >= 3 ? 1 : 2) void k_kv4_attn_tile(KvAttn a) {
+__global__ __launch_bounds__(256, G >= 4 ? 1 : 2) void k_kv4_attn_tile(KvAttn a) {
   constexpr int WAVES = 4, ROWS = kRowTile, D = 64 * G, BYTES = kKvGroupBytes * G, RAW = 4, TILES = D / 32;
   constexpr int SHARE = BYTES / WAVES;   // a wavefront's part of a block's copy
   constexpr int COPIES = (SHARE + 1023) / 1024;
   constexpr int HELD = 32 * D * 2;   // a block's keys, or values
   static_assert(SHARE % 16 == 0, "copies are 16 bytes a lane");
   __shared__ __attribute__((aligned(16))) uint8_t raw[RAW * BYTES];
-  __shared__ __attribute__((aligned(16))) uint8_t keys[2 * HELD], vals[3 * HELD];
+  __shared__ __attribute__((aligned(16))) uint8_t keys[2 * HELD], vals[2 * HELD];
   const uint32_t tid = threadIdx.x, lane = tid & 63u, col = lane & 31u, half = lane >> 5;
   const int wave = __builtin_amdgcn_readfirstlane(tid >> 6);
   const uint32_t raw_lds = lds_addr(raw);
@@ -1151,21 +1154,25 @@ __global__ __launch_bounds__(256, G >= 3 ? 1 : 2) void k_kv4_attn_tile(KvAttn a)
 
   // Operands of block i: a wavefront takes word `wave` of every lane's four.
   const uint32_t m16 = lane & 15u, kq = lane >> 4;
-  auto spread = [&](int i) {
-    const uint8_t* const from = raw + (i % RAW) * BYTES;
-    uint8_t* const tk = keys + (i & 1) * HELD + ((4 * (wave & 1) + kq) * 32 + 16 * (m16 >> 3) + 8 * (wave >> 1) +
+  auto spread_keys = [&](int i) {
+    const uint8_t* const from = raw + (i % RAW) * BYTES + 16 * lane + 4 * wave;
+    uint8_t* const to = keys + (i & 1) * HELD + ((4 * (wave & 1) + kq) * 32 + 16 * (m16 >> 3) + 8 * (wave >> 1) +
                                                  (m16 & 7u)) * 16;
-    uint8_t* const tv =
-        vals + (i % 3) * HELD + (((kq >> 1) * TILES + (wave >> 1)) * 64 + 32 * (kq & 1u) + 16 * (wave & 1) + m16) * 16;
+#pragma unroll
+    for (int g = 0; g < G; ++g)
+      *reinterpret_cast<half8_t*>(to + 8 * 32 * 16 * g) = codes_of(*reinterpret_cast<const uint32_t*>(from + 1024 * g));
+  };
+  auto spread_values = [&](int i) {
+    const uint8_t* const from = raw + (i % RAW) * BYTES;
+    uint8_t* const to =
+        vals + (i & 1) * HELD + (((kq >> 1) * TILES + (wave >> 1)) * 64 + 32 * (kq & 1u) + 16 * (wave & 1) + m16) * 16;
 #pragma unroll
     for (int g = 0; g < G; ++g) {
-      *reinterpret_cast<half8_t*>(tk + 8 * 32 * 16 * g) =
-          codes_of(*reinterpret_cast<const uint32_t*>(from + 1024 * g + 16 * lane + 4 * wave));
       const uint32_t w = *reinterpret_cast<const uint32_t*>(from + kv_value_codes(G) + 1024 * g + 16 * lane + 4 * wave);
       const Halves<8> s(from + kv_value_so(G) + 128 * g + 16 * kq), o(from + kv_value_so(G) + 128 * g + 64 + 16 * kq);
       const half2_t s2[4] = {pair_of(s.w[0]), pair_of(s.w[1]), pair_of(s.w[2]), pair_of(s.w[3])};
       const half2_t o2[4] = {pair_of(o.w[0]), pair_of(o.w[1]), pair_of(o.w[2]), pair_of(o.w[3])};
-      *reinterpret_cast<u32x4*>(tv + 2 * 64 * 16 * g) = values_of(dc, w, s2, o2);
+      *reinterpret_cast<u32x4*>(to + 2 * 64 * 16 * g) = values_of(dc, w, s2, o2);
     }
   };
   // Places of block i past the sequence's end (all of them if its page is not
@@ -1258,10 +1265,11 @@ __global__ __launch_bounds__(256, G >= 3 ? 1 : 2) void k_kv4_attn_tile(KvAttn a)
 
   if (blocks > 0) {
     arrive(0);
-    spread(0);
+    spread_keys(0);
+    spread_values(0);
     arrive(1);
     bool hide = is_gone(0, min(2, blocks - 1));
-    if (blocks > 1) spread(1);
+    if (blocks > 1) spread_keys(1);
     f32x16 sc;
     scores(0, sc);
     settle(0, hide, sc);
@@ -1307,7 +1315,7 @@ __global__ __launch_bounds__(256, G >= 3 ? 1 : 2) void k_kv4_attn_tile(KvAttn a)
               l = __builtin_amdgcn_fdot2(pr, ones, l, false);   // the sum of what is multiplied
             }
           }
-        const uint8_t* const v = vals + (i % 3) * HELD;
+        const uint8_t* const v = vals + (i & 1) * HELD;
 #pragma unroll
         for (int A = 0; A < 2; ++A)
 #pragma unroll
@@ -1316,7 +1324,8 @@ __global__ __launch_bounds__(256, G >= 3 ? 1 : 2) void k_kv4_attn_tile(KvAttn a)
             acc[t] = __builtin_amdgcn_mfma_f32_32x32x16_f16(vc, pf[A], acc[t], 0, 0, 0);
             if constexpr (FINE) acc[t] = __builtin_amdgcn_mfma_f32_32x32x16_f16(vc, pl[A], acc[t], 0, 0, 0);
           }
-        spread(i + 2);
+        spread_values(i + 1);
+        spread_keys(i + 2);
         sc = next;
         ++i;
         if (i < blocks) pass = settle(i, hide, sc);
@@ -1423,7 +1432,7 @@ KvAttnPlan kv4_attn_plan(int batch, int heads, int ratio, int groups, int max_q,
     p.rows = kRowTile;
     p.tiles = (int64_t)batch * heads * ((rows + p.rows - 1) / p.rows);
     // Where tiles leave places on the chip (two workgroups a CU, one with large heads), parts fill them.
-    const int64_t fill = (groups <= 2 ? 512 : 256) / (p.tiles ? p.tiles : 1), most = blocks / kLeastTilePart;
+    const int64_t fill = (groups <= 3 ? 512 : 256) / (p.tiles ? p.tiles : 1), most = blocks / kLeastTilePart;
     const int64_t parts = fill < most ? fill : most;
     p.parts = (int32_t)(parts < 1 ? 1 : parts < kTileParts ? parts : kTileParts);
     p.places = p.parts > 1 ? p.tiles * p.parts : 0;
