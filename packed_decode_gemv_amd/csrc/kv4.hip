@@ -202,7 +202,9 @@ __global__ __launch_bounds__(256) void k_kv4_append(KvCache c, KvRange r, const 
         hi = max2(hi, w[i]);
       }
       spread_min_max(lo, hi);
-      const _Float16 s16 = (_Float16)__fmul_rn(__fsub_rn(hi, lo), 1.f / 15.f);
+      float scale = __fmul_rn(__fsub_rn(hi, lo), 1.f / 15.f);
+      asm("" : "+v"(scale));   // or product and conversion become one instruction that rounds once
+      const _Float16 s16 = (_Float16)scale;
       const _Float16 o16 = (_Float16)lo;
       const float s = (float)s16, of = (float)o16;
       const float r = s != 0.f ? __builtin_amdgcn_rcpf(s) : 0.f;
@@ -249,7 +251,9 @@ __device__ inline void store_row(void* base, int64_t elem, const float (&x)[N]) 
 #pragma unroll
     for (int i = 0; i < N / 2; ++i) {
       if constexpr (DT == VBQ_F16) {
-        const half2_t h = {(_Float16)x[2 * i], (_Float16)x[2 * i + 1]};
+        float u = x[2 * i], v = x[2 * i + 1];
+        asm("" : "+v"(u), "+v"(v));   // the fp32 value is rounded, not the sum before it (see k_kv4_append)
+        const half2_t h = {(_Float16)u, (_Float16)v};
         w[i] = __builtin_bit_cast(uint32_t, h);
       } else {
         const bf2_t h = {(__bf16)x[2 * i], (__bf16)x[2 * i + 1]};

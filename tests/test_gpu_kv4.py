@@ -174,6 +174,29 @@ def test_append_writes_the_stated_bytes_and_no_others(vbq, case, strided):
     assert np.array_equal(got, want), np.flatnonzero(got != want)[:8]
 
 
+def test_the_scale_is_rounded_to_binary32_and_then_to_binary16(vbq):
+    """Ranges whose product with f32(1/15) is halfway between two fp16 numbers in binary32 though the exact product
+    is not: rounding once would give the neighbour."""
+    import torch
+    ranges = [float.fromhex(h) for h in ("0x1.5779fe0p+4", "0x1.4cb1fe0p+3", "0x1.a189fe0p+3",
+                                         "0x1.0da6000p+3", "0x1.60d9fe0p+3")]
+    x = np.zeros((len(ranges), 1, 64), np.float32)
+    x[:, 0, 17] = ranges
+    x[:, 0, 40] = np.float32(ranges) / 3
+    want = quantise(x.astype(np.float64))[1]
+    once = (np.float32(ranges).astype(np.float64) * np.float64(np.float32(1 / 15))).astype(np.float16)
+    assert (once != want.reshape(-1)).all()      # numpy rounds float64 to float16 once
+    cache = vbq.Kv4Cache(1, 32, 1, 64)
+    i32 = dict(dtype=torch.int32, device="cuda")
+    vbq.kv4_append(cache, gpu(x), gpu(x), torch.zeros(1, 1, **i32), torch.zeros(1, **i32),
+                   torch.tensor([0, len(ranges)], **i32))
+    data, lay = cache.data.cpu().numpy(), Layout(32, 1, 64)
+    for t in range(len(ranges)):
+        for kv in range(2):
+            a, _ = lay.places(lay.block(0, 0, t), t, kv)[0]
+            assert data[a:a + 2].view(np.float16)[0] == want.reshape(-1)[t]
+
+
 @pytest.mark.parametrize("dtype", ["float16", "bfloat16", "float32"])
 @pytest.mark.parametrize("heads,dim,page,seqs", [
     (1, 64, 32, [(0, 1)]),
