@@ -931,14 +931,14 @@ __global__ __launch_bounds__(64 * kWaves, (kRoomy<G, ROWS>) ? 4 : G * ROWS > 64 
 // 2.1e-4 are the rounding of the output itself; bf16 outputs are off by 1.7e-3
 // either way.
 //   Bounds. 2048 bf16 queries of 32 heads of 128 over 10240 tokens: 309 GFLOP in
-// 430 us, 0.72 PFLOP/s (a library product of 8192^3 reaches 1.37). A turn of
+// 427 us, 0.72 PFLOP/s (a library product of 8192^3 reaches 1.37). A turn of
 // one wavefront is 17 MFMAs (544 cycles), about 150 vector instructions (850
 // cycles) and 28 KB of LDS reads (220 cycles of the CU, times 8 wavefronts),
 // and two wavefronts a SIMD overlap them in part. With values spread a block
 // later than keys two buffers do for both, and heads of 192 fit twice on a CU (17 x
 // 1193 queries, 16 heads: 462 -> 317 us). Heads of 256 have registers for one
-// wavefront a SIMD: 3 sequences under a window of 500, 36 GFLOP in 155 us;
-// 2.3 us a block, 7 us before the first and 2 us after the last, and 630
+// wavefront a SIMD: 3 sequences under a window of 500, 36 GFLOP in 150 us;
+// 2.2 us a block, 7 us before the first and 2 us after the last, and 630
 // workgroups on 256 CUs end in a third round. (64 rows a wavefront: 536 against
 // 447 us. Reads of a group ahead of its products, held there by scheduling
 // barriers: no change.)
