@@ -5,11 +5,11 @@
 // rows a sequence and head (16 for heads of 256) take k_kv4_attn, more take
 // k_kv4_attn_tile (below).
 //
-// k_kv4_attn: a workgroup of four wavefronts takes a tile (all rows of one
-// sequence and head), or a part of its token axis; wavefront w takes every
-// fourth block of 32 tokens and keeps its own running maximum, sum and output in
-// registers. The wavefronts are joined in LDS, the parts in the workspace by
-// the last workgroup that finishes.
+// k_kv4_attn: a workgroup of four or eight wavefronts takes a tile (all rows of
+// one sequence and head), or a part of its token axis; wavefront w takes every
+// fourth (eighth) block of 32 tokens and keeps its own running maximum, sum and
+// output in registers. The wavefronts are joined in LDS, the parts in the
+// workspace by the last workgroup that finishes.
 //
 // Scores. S^T = K Q^T by 16x16x32 fp16 MFMAs: A is a block's key codes, 16
 // tokens by 32 channels of one group, B the queries. A code word holds eight
@@ -44,8 +44,9 @@
 // sequence of 131072 tokens: 151 MB in 42 us, 64 parts a tile to join.
 // 16 heads of 16 sequences under a window of 1024: 38 MB in 14 us, the chain of
 // dependent look-ups. 20 rows, 8 sequences of 20000 tokens in all, 8 heads: 24 MB
-// in 26 us; 1.8 us a block and wavefront (a wavefront a SIMD: vector
-// instructions and their latency), 4.6 us before the first, 7 us for the joins.
+// in 25 us; three blocks a wavefront, of about 1.8 us each where one has a SIMD to
+// itself (vector instructions and their latency), 4.6 us before the first, 7 us
+// for the joins.
 #include "kv4.h"
 
 namespace vbq {
@@ -55,7 +56,12 @@ typedef _Float16 half8_t __attribute__((ext_vector_type(8)));
 typedef float f32x4 __attribute__((ext_vector_type(4)));
 typedef float f32x2 __attribute__((ext_vector_type(2)));
 
-constexpr int kWaves = 4;
+// Wavefronts of a workgroup. Where registers allow two a SIMD but no more, eight
+// that share one join do better than two workgroups of four (8 heads of 128 over
+// 60000 tokens, 12 rows: 32 against 42 us; over 90000, 32 rows: 64 against 82; 64
+// tiles of 20 rows of 80 blocks: 25 against 26).
+template <int G, int ROWS>
+constexpr int kWaves = G <= 2 && ROWS >= 16 ? 8 : 4;
 constexpr float kNoMax = -3e38f;     // running maximum before any token
 // Probabilities are 2^(score * to_log2 - m) in one fma. m is a rounded product,
 // so beyond 2^22 the exact product may pass it by more than a quarter, and
@@ -69,9 +75,9 @@ __device__ inline float below(float score, float to_log2, float m) {
   return t - m;
 }
 constexpr int kParts = 512;          // workgroups that a launch aims at, at most
-// Blocks of a part, at least: two a wavefront; with 32 rows, whose parts take
-// eight times the bytes of 4 rows to join, six (64 tiles of 20 rows of 80
-// blocks: parts of 11 blocks 29.3 us, of 16 29.8, of 24 26.2, of 32 28).
+// Blocks of a part, at least; more with 32 rows, whose parts take eight times
+// the bytes of 4 rows to join (64 tiles of 20 rows of 80 blocks: parts of at
+// least 24 blocks 25 us, of 32 27; with four wavefronts of 11 blocks 29, of 24 26).
 template <int ROWS>
 constexpr int kLeastPart = ROWS > 16 ? 24 : 8;
 
@@ -309,22 +315,24 @@ __device__ inline void lanes_load(const KvAttn& a, uint32_t lane, int base, bool
 // registers allow four workgroups a CU (up to 8 rows, heads of up to 128), two
 // stages: with heads of 128 the same bytes are on their way as with two
 // workgroups of four stages, and the wavefronts hide each other's arithmetic
-// (32 sequences of up to 8192 tokens, 4 rows a tile: 50 against 60 us).
+// (32 sequences of up to 8192 tokens, 4 rows a tile: 50 against 60 us). Eight
+// wavefronts have two stages as well (8 x 4 queries of 4 heads a group, 20206
+// tokens in all: 18.1 us, with four stages 19.5).
 template <int G, int ROWS>
 constexpr bool kRoomy = G <= 2 && ROWS <= 8;
 typedef uint16_t ushort2_t __attribute__((ext_vector_type(2)));
 
 template <int G, int ROWS, int STAGES>
-__global__ __launch_bounds__(64 * kWaves, (kRoomy<G, ROWS>) ? 4 : G * ROWS > 64 ? 1 : 2) void k_kv4_attn(KvAttn a) {
-  constexpr int D = 64 * G, PITCH = D + 4, BYTES = kKvGroupBytes * G;
+__global__ __launch_bounds__((64 * kWaves<G, ROWS>), (kRoomy<G, ROWS>) ? 4 : G * ROWS > 64 ? 1 : 2) void k_kv4_attn(KvAttn a) {
+  constexpr int WAVES = kWaves<G, ROWS>, D = 64 * G, PITCH = D + 4, BYTES = kKvGroupBytes * G;
   constexpr int NT = ROWS > 16 ? 2 : 1, COLS = ROWS > 16 ? 16 : ROWS;   // column tiles, and columns used of each
   constexpr int PARTS = 16 / COLS, PAIRS = 4 / PARTS;   // lanes that share a row's octet, token pairs of each
   constexpr int ODD = PARTS == 4 ? 1 : 2;   // sums kept apart for pairs whose codes come times 16
-  constexpr int RING = kWaves * STAGES * BYTES, SUMS = kWaves * COLS * PITCH * 4;
-  constexpr int JOIN = ROWS * kParts * 4 + 64 * kWaves * 16, AFTER = SUMS > JOIN ? SUMS : JOIN;
+  constexpr int RING = WAVES * STAGES * BYTES, SUMS = WAVES * COLS * PITCH * 4;
+  constexpr int JOIN = ROWS * kParts * 4 + 64 * WAVES * 16, AFTER = SUMS > JOIN ? SUMS : JOIN;
   // blocks; afterwards the wavefronts' sums, or the parts' factors and shares
   __shared__ __attribute__((aligned(16))) uint8_t ring[RING > AFTER ? RING : AFTER];
-  __shared__ float wml[kWaves][ROWS][2];
+  __shared__ float wml[WAVES][ROWS][2];
   __shared__ uint32_t last;
   float* const buf = reinterpret_cast<float*>(ring);   // the wavefronts' sums, after a tile
   const uint32_t tid = threadIdx.x, lane = tid & 63u, col = lane & 15u, quarter = lane >> 4;
@@ -348,9 +356,9 @@ __global__ __launch_bounds__(64 * kWaves, (kRoomy<G, ROWS>) ? 4 : G * ROWS > 64 
         if ((uint32_t)(base + at) % gridDim.x != blockIdx.x) continue;
         const int n = __builtin_amdgcn_readlane(ln.nq, at) * a.n_heads;
         const int64_t from = (int64_t)__builtin_amdgcn_readlane(ln.c0, at) * a.n_heads;
-        for (int e = (int)tid; e < n * (D / 4); e += 64 * kWaves) store4(a, from * D + 4 * e, f32x4{0.f, 0.f, 0.f, 0.f});
+        for (int e = (int)tid; e < n * (D / 4); e += 64 * WAVES) store4(a, from * D + 4 * e, f32x4{0.f, 0.f, 0.f, 0.f});
         if (a.lse)
-          for (int e = (int)tid; e < n; e += 64 * kWaves) a.lse[from + e] = -__builtin_inff();
+          for (int e = (int)tid; e < n; e += 64 * WAVES) a.lse[from + e] = -__builtin_inff();
       }
     }
     const int chunk = max((int)(((uint32_t)total * (uint32_t)a.cache.heads + (uint32_t)a.parts - 1u) / (uint32_t)a.parts),
@@ -423,7 +431,7 @@ __global__ __launch_bounds__(64 * kWaves, (kRoomy<G, ROWS>) ? 4 : G * ROWS > 64 
   auto block_of = [&](int idx) { return idx < re.ns ? idx : idx - re.ns + re.w0; };
   auto start_copy = [&](int it) {
     if ((it & 63) == 0) {
-      const int next = i0 + wave + kWaves * (it + (int)lane), blk = block_of(next);
+      const int next = i0 + wave + WAVES * (it + (int)lane), blk = block_of(next);
       int page = 0;
       bool bad = false;
       if (next < i1) {
@@ -440,7 +448,7 @@ __global__ __launch_bounds__(64 * kWaves, (kRoomy<G, ROWS>) ? 4 : G * ROWS > 64 
     }
     copy_block<G>(ring_lds + (uint32_t)(it % STAGES) * BYTES, lane_address(at, it & 63), lane);
   };
-  const int count = i0 + wave < i1 ? (i1 - i0 - wave + kWaves - 1) / kWaves : 0;
+  const int count = i0 + wave < i1 ? (i1 - i0 - wave + WAVES - 1) / WAVES : 0;
 #pragma unroll
   for (int it = 0; it < STAGES - 1; ++it)
     if (it < count) start_copy(it);
@@ -534,7 +542,7 @@ __global__ __launch_bounds__(64 * kWaves, (kRoomy<G, ROWS>) ? 4 : G * ROWS > 64 
     if (ahead < count) start_copy(ahead);
     // (the pages of the 64 blocks after may have been looked up already)
     if ((gone | gone_before) && ((((it ^ min(ahead, count - 1)) >> 6 ? gone_before : gone) >> (it & 63)) & 1u)) continue;
-    const int blk = block_of(i0 + wave + kWaves * it);
+    const int blk = block_of(i0 + wave + WAVES * it);
     const uint8_t* const k = own_ring + (it % STAGES) * BYTES;
 
     // Scores of the lane's tokens 8 quarter + PAIRS part + j (+ 4).
@@ -767,7 +775,7 @@ __global__ __launch_bounds__(64 * kWaves, (kRoomy<G, ROWS>) ? 4 : G * ROWS > 64 
       const int rr = 16 * nt + (int)qcol;
       float low = wml[0][rr][0];
 #pragma unroll
-      for (int w = 1; w < kWaves; ++w) low = fminf(low, wml[w][rr][0]);
+      for (int w = 1; w < WAVES; ++w) low = fminf(low, wml[w][rr][0]);
       const float f = __builtin_amdgcn_exp2f(low - base[nt]), f24 = f * 0x1p24f;
       float* const to = buf + (wave * COLS + qcol) * PITCH + 16 * quarter;
 #pragma unroll
@@ -782,16 +790,16 @@ __global__ __launch_bounds__(64 * kWaves, (kRoomy<G, ROWS>) ? 4 : G * ROWS > 64 
       }
     }
     __syncthreads();
-    for (int e = (int)tid; e < COLS * (D / 4); e += 64 * kWaves) {
+    for (int e = (int)tid; e < COLS * (D / 4); e += 64 * WAVES) {
       const int row = e / (D / 4), c = e % (D / 4), rr = 16 * nt + row;
       if (rr >= rows) break;
       float low = wml[0][rr][0];
 #pragma unroll
-      for (int w = 1; w < kWaves; ++w) low = fminf(low, wml[w][rr][0]);
+      for (int w = 1; w < WAVES; ++w) low = fminf(low, wml[w][rr][0]);
       float sum = 0.f;
       f32x4 v = {0.f, 0.f, 0.f, 0.f};
 #pragma unroll
-      for (int w = 0; w < kWaves; ++w) {
+      for (int w = 0; w < WAVES; ++w) {
         sum += wml[w][rr][1] * __builtin_amdgcn_exp2f(low - wml[w][rr][0]);
         v += *reinterpret_cast<const f32x4*>(buf + (w * COLS + row) * PITCH + 4 * c);
       }
@@ -825,7 +833,7 @@ __global__ __launch_bounds__(64 * kWaves, (kRoomy<G, ROWS>) ? 4 : G * ROWS > 64 
   const float* const ml0 = slot_ml - (int64_t)part_no * ROWS * 2;
   float* const factor = buf;                                                 // [rows][kParts]
   f32x4* const share = reinterpret_cast<f32x4*>(ring + ROWS * kParts * 4);   // [threads]
-  constexpr int THREADS = 64 * kWaves, ROW_LANES = ROWS < 16 ? 16 : THREADS / ROWS;
+  constexpr int THREADS = 64 * WAVES, ROW_LANES = ROWS < 16 ? 16 : THREADS / ROWS;
   {   // some lanes a row: the smallest base, each part's factor, the sum
     const int row = (int)tid / ROW_LANES, j = (int)tid % ROW_LANES;
     float low = -kNoMax, sum = 0.f;   // sum is held times 2^low
@@ -1443,11 +1451,13 @@ KvAttnPlan kv4_attn_plan(int batch, int heads, int ratio, int groups, int max_q,
   p.tiles = (int64_t)batch * heads;
   // Tiles longer than total / parts are cut, so there are at most `parts` parts
   // beyond one a tile, and on average half a part a tile: the aim leaves room
-  // for those where two workgroups fit a CU, so that all run at once.
-  const bool cut = p.tiles <= VBQ_KV4_COUNTERS && blocks > (p.tiles < 256 ? 5 : 12) * kWaves &&
+  // for those where one workgroup of eight wavefronts or two of four fit a CU, so
+  // that all run at once (a second round: 34 against 23 us for 128 tiles of 16 rows).
+  const bool cut = p.tiles <= VBQ_KV4_COUNTERS && blocks > (p.tiles < 256 ? 5 : 12) * 4 &&
                    p.tiles * blocks < INT32_MAX - 65536;
-  const int spare = groups <= 2 && p.rows <= 8 ? 0 : (int)(p.tiles < kParts ? p.tiles : kParts) / 2;
-  p.parts = cut ? kParts - spare : 0;
+  const int fill = groups <= 2 && p.rows >= 16 ? kParts / 2 : kParts;   // (eight wavefronts each)
+  const int spare = groups <= 2 && p.rows <= 8 ? 0 : (int)(p.tiles < fill ? p.tiles : fill) / 2;
+  p.parts = cut ? fill - spare : 0;
   p.grid = cut ? p.parts + p.tiles : p.tiles;
   p.places = cut ? p.grid : 0;
   return p;
@@ -1456,7 +1466,7 @@ KvAttnPlan kv4_attn_plan(int batch, int heads, int ratio, int groups, int max_q,
 hipError_t launch_kv4_attention(const KvAttn& a, const KvAttnPlan& p, int batch, hipStream_t s) {
   if (p.grid > INT32_MAX) return hipErrorNotSupported;
   const dim3 grid((uint32_t)p.grid);
-#define VBQ_CALL(G, ROWS, ST) k_kv4_attn<G, ROWS, ST><<<grid, 64 * kWaves, 0, s>>>(a)
+#define VBQ_CALL(G, ROWS, ST) k_kv4_attn<G, ROWS, ST><<<grid, (64 * kWaves<G, ROWS>), 0, s>>>(a)
 #define VBQ_CALL2(G, FEW, ST)                \
   if (p.rows == 4) VBQ_CALL(G, 4, FEW);      \
   else if (p.rows == 8) VBQ_CALL(G, 8, FEW); \
@@ -1479,8 +1489,8 @@ hipError_t launch_kv4_attention(const KvAttn& a, const KvAttnPlan& p, int batch,
     return hipGetLastError();
   }
   switch (a.cache.groups) {
-    case 1: VBQ_CALL3(1, 4, 4); break;
-    case 2: VBQ_CALL3(2, 2, 4); break;
+    case 1: VBQ_CALL3(1, 4, 2); break;
+    case 2: VBQ_CALL3(2, 2, 2); break;
     case 3: VBQ_CALL3(3, 2, 2); break;
     default: VBQ_CALL2(4, 2, 2); break;
   }
