@@ -874,7 +874,8 @@ __global__ __launch_bounds__((64 * kWaves<G, ROWS>), (kRoomy<G, ROWS>) ? 4 : G *
   // together, 16 at a time (where a thread's part is past the last, the last is
   // read and left out): one by one they took 6 of 28 us for 64 tiles of 20 rows
   // in 4 parts.
-  constexpr int ROUNDS = ROWS * D / 4 > THREADS ? ROWS * D / 4 / THREADS : 1, BATCH = 16 / ROUNDS;
+  constexpr int ROUNDS = (ROWS * D / 4 + THREADS - 1) / THREADS, BATCH = 16 / ROUNDS;   // (the last one may be ragged)
+  static_assert(ROUNDS * THREADS >= ROWS * D / 4 && BATCH >= 1, "every output of a tile has a thread and a round");
   const int ne = rows * (D / 4), shares = ne <= THREADS / 2 ? THREADS / ne : 1;
   const int e0 = shares > 1 ? (int)tid % ne : (int)tid, share_no = shares > 1 ? (int)tid / ne : 0;
   f32x4 v[ROUNDS];

@@ -777,3 +777,21 @@ def test_the_decode_example(vbq, batch, prompt, steps, window):
     # probabilities, their product with a scale and the output are rounded to fp16 or better
     assert r["rel_l2"] <= 3 * 2.0 ** -11
     assert r["cache_bytes"] * 32 == r["bf16_bytes"] * 9
+
+
+# ---- every output is written -----------------------------------------------------------
+@pytest.mark.parametrize("dim", [64, 128, 192, 256])
+@pytest.mark.parametrize("ratio,new", [(4, 1), (5, 1), (2, 3), (7, 1), (2, 4), (8, 1), (3, 3), (16, 1), (5, 4), (8, 4)])
+def test_a_join_of_parts_writes_every_row(vbq, dim, ratio, new):
+    """Every row count at which a tile's outputs take another turn of the joining workgroup, up to the full 4, 8, 16 and
+    32 rows: what was in `out` and `lse` before the call is gone."""
+    import torch
+    rng = np.random.default_rng(100 * dim + 10 * ratio + new)
+    lens, news = [1100, 37], [new, 1]
+    args, kw, out = attend(vbq, rng, 1, ratio, dim, 32, lens, news, max_kv=1200)
+    assert dim == 256 and ratio * new > 16 or \
+        vbq.kv4_attention_workspace(args[0], 2, sum(news), ratio, new, 1200).numel() > 0     # (cut into parts)
+    filled = torch.full_like(out, float("nan"))
+    lse = torch.full(out.shape[:2], float("nan"), device="cuda")
+    vbq.kv4_attention(*args, out=filled, lse=lse, **kw)
+    assert torch.equal(filled, out) and torch.isfinite(lse).all()
