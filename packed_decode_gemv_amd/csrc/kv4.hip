@@ -144,6 +144,7 @@ __global__ __launch_bounds__(256) void k_kv4_append(KvCache c, KvRange r, const 
     if (threadIdx.x == 0) kv_flag(c, VBQ_KV4_FLAG_LENGTH);
     return;
   }
+  if (n == 0) return;   // (an idle sequence's row of the table may hold anything, another's page too)
   // the octet's first position, and its tokens that are in the range
   const int64_t blk = (s0 >> 5) + (int64_t)(blockIdx.x / (uint32_t)c.heads), first = 32 * blk + 8 * oct;
   const int64_t ahead = (int64_t)s0 + n - first;

@@ -795,3 +795,25 @@ def test_a_join_of_parts_writes_every_row(vbq, dim, ratio, new):
     lse = torch.full(out.shape[:2], float("nan"), device="cuda")
     vbq.kv4_attention(*args, out=filled, lse=lse, **kw)
     assert torch.equal(filled, out) and torch.isfinite(lse).all()
+
+
+# ---- sequences without new tokens --------------------------------------------------------
+@pytest.mark.parametrize("start", [0, 3, 35, 63, 4000])
+@pytest.mark.parametrize("dtype", ["float16", "float32"])
+def test_an_append_of_no_tokens_looks_at_nothing(vbq, start, dtype):
+    """A sequence that adds nothing neither needs pages nor rewrites them: its row of the table may be stale, -1, or name
+    a page that another sequence of the call writes."""
+    import torch
+    i32 = dict(dtype=torch.int32, device="cuda")
+    gen = torch.Generator(device="cuda").manual_seed(start)
+    k, v = torch.randn(2, 20, 2, 64, generator=gen, device="cuda").to(getattr(torch, dtype))
+    data = random_cache(np.random.default_rng(start), 4, 32, 2, 64)
+    alone, beside = (vbq.Kv4Cache(4, 32, 2, 64, data=gpu(data.copy())) for _ in range(2))
+    vbq.kv4_append(alone, k, v, torch.tensor([[1, 2]], **i32), torch.tensor([30], **i32), torch.tensor([0, 20], **i32))
+    for idle in ([-1, -1], [9, 9], [1, 2], [2, 1]):
+        beside.data.copy_(gpu(data))
+        vbq.kv4_append(beside, k, v, torch.tensor([idle, [1, 2], idle], **i32),
+                       torch.tensor([start, 30, start], **i32), torch.tensor([0, 0, 20, 20], **i32), max_tokens=20)
+        assert torch.equal(beside.data, alone.data)
+        assert beside.check() is False
+    assert alone.check() is False
