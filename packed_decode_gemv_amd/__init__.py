@@ -552,6 +552,8 @@ class Kv4Cache:
         self.n_pages, self.page_tokens = int(n_pages), int(page_tokens)
         self.n_kv_heads, self.head_dim = int(n_kv_heads), int(head_dim)
         if data is None:
+            if torch.device(device).type != "cuda":
+                raise ValueError(f"Kv4Cache: on {device}, expected a GPU")
             data = torch.zeros(self.nbytes, dtype=torch.uint8, device=device)
         else:
             _need(data, "data", torch.uint8, (self.nbytes,))

@@ -105,3 +105,14 @@ def test_workspace_is_bounded_and_grows_with_no_size_beyond_it(batch, heads, max
     n = vbq.lib.kv4_attention_workspace(C.byref(c), C.byref(_attn(vbq, batch=batch, n_heads=heads, max_q=max_q,
                                                                    max_kv=max_kv, window=window, sinks=sinks)))
     assert 0 <= n < 1 << 30
+
+
+@pytest.mark.parametrize("device", ["cpu", "meta"])
+def test_a_cache_is_on_a_gpu(device):
+    """A buffer elsewhere would reach the kernels as a device pointer."""
+    import torch
+    import packed_decode_gemv_amd as vbq
+    with pytest.raises(ValueError, match="expected a GPU"):
+        vbq.Kv4Cache(2, 32, 1, 64, device=device)
+    with pytest.raises(ValueError, match="expected a GPU"):
+        vbq.Kv4Cache(2, 32, 1, 64, data=torch.zeros(2 * 2304, dtype=torch.uint8, device=device))
