@@ -393,7 +393,9 @@ vbq_status kv4_read(const vbq_kv4* cache, const vbq_kv4_range* r, void* k, void*
  *   causal:  j <= p
  *   window:  j > p - window or j < sinks     (window > 0, causal only)
  * A row that sees nothing gives zeros (and lse = -infinity). A NaN or infinity
- * in q reaches the outputs of its own row only.
+ * in q reaches the outputs of its own row only, and so does a number so large
+ * that scale * log2(e) * |q| reaches 2^117. Scores have to be numbers that fp32
+ * holds.
  * Scores are sums in fp32 of products of q with the exact codes; scale, offset
  * and softmax are fp32. A row of q is scaled by a power of two that brings its
  * largest number to [2^13, 2^14) and held in fp16: numbers down to 2^-23 (fp16)
@@ -418,7 +420,7 @@ typedef struct vbq_kv4_attn {
   int32_t causal;         /* 0 or 1 */
   int32_t window;         /* 0: none */
   int32_t sinks;          /* first tokens that a window leaves visible */
-  float scale;            /* > 0 */
+  float scale;            /* > 0, and scale * log2(e) is a finite fp32 number */
   int32_t reserved;       /* 0 */
   const int32_t* table;   /* device, [batch][table_width] */
   const int32_t* kv_lens; /* device, [batch] */

@@ -5,6 +5,7 @@
 #include <string.h>
 
 #include <algorithm>
+#include <cfloat>
 #include <vector>
 
 #include "kv4.h"
@@ -73,6 +74,8 @@ uint64_t host_tile_bytes(const uint8_t* widths, int N, int G, int rt, int kt, bo
 }
 
 // ---- 4-bit key/value cache ----
+constexpr float kLog2e = 1.44269504088896341f;
+
 bool kv4_sizes_ok(int32_t page_tokens, int32_t heads, int32_t dim) {
   return page_tokens >= kKvBlock && page_tokens <= 65536 && (page_tokens & (page_tokens - 1)) == 0 && heads >= 1 &&
          heads <= 4096 && dim >= kGroup && dim % kGroup == 0 && dim / kGroup <= VBQ_KV4_MAX_GROUPS;
@@ -119,7 +122,7 @@ vbq_status check_attn(const vbq_kv4* cache, const vbq_kv4_attn* a, bool pointers
   if (a->dtype != VBQ_F16 && a->dtype != VBQ_BF16) return VBQ_ERR_INVALID_ARG;
   if ((a->causal != 0 && a->causal != 1) || a->window < 0 || a->sinks < 0) return VBQ_ERR_INVALID_ARG;
   if (a->window > 0 && !a->causal) return VBQ_ERR_INVALID_ARG;
-  if (!(a->scale > 0.f && a->scale <= 3.0e38f)) return VBQ_ERR_INVALID_ARG;
+  if (!(a->scale > 0.f && a->scale * kLog2e <= FLT_MAX)) return VBQ_ERR_INVALID_ARG;
   if (a->batch > 65535 || a->n_heads > 65536) return VBQ_ERR_UNSUPPORTED;
   const int ratio = a->n_heads / cache->n_kv_heads;
   if ((int64_t)a->max_q * ratio > INT32_MAX - 64) return VBQ_ERR_UNSUPPORTED;
@@ -214,7 +217,7 @@ vbq_status kv4_attention(const vbq_kv4* cache, const vbq_kv4_attn* a, hipStream_
   k.ratio_inv = (65536 + k.ratio - 1) / k.ratio;
   k.batch = a->batch;
   k.parts = p.parts;
-  k.scale_log2 = a->scale * 1.44269504088896341f;
+  k.scale_log2 = a->scale * kLog2e;
   hipError_t e = launch_kv4_attention(k, p, a->batch, stream);
   return e == hipErrorNotSupported ? VBQ_ERR_UNSUPPORTED : from_hip(e);
 }

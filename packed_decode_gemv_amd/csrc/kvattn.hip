@@ -482,7 +482,7 @@ __global__ __launch_bounds__((64 * kWaves<G, ROWS>), (kRoomy<G, ROWS>) ? 4 : G *
     int ex = (int)(__builtin_bit_cast(uint32_t, top) >> 23) - 127;
     ex = top > 0.f ? max(ex, -100) : 13;
     const float up = ldexpf(1.f, 13 - ex);
-    to_log2[nt] = a.scale_log2 * ldexpf(1.f, ex - 13 + 24);
+    to_log2[nt] = ldexpf(a.scale_log2, ex - 13 + 24);
 #pragma unroll
     for (int g = 0; g < G; ++g) {
       float sum = 0.f;
@@ -1130,7 +1130,7 @@ __global__ __launch_bounds__(256, G >= 4 ? 1 : 2) void k_kv4_attn_tile(KvAttn a)
     int ex = (int)(__builtin_bit_cast(uint32_t, top) >> 23) - 127;
     ex = top > 0.f ? max(ex, -100) : 13;
     const float up = ldexpf(1.f, 13 - ex);
-    to_log2 = a.scale_log2 * ldexpf(1.f, ex - 13 + 24);
+    to_log2 = ldexpf(a.scale_log2, ex - 13 + 24);
 #pragma unroll
     for (int j = 0; j < 8; ++j) qsum[j] = (_Float16)0.f;
 #pragma unroll

@@ -817,3 +817,37 @@ def test_an_append_of_no_tokens_looks_at_nothing(vbq, start, dtype):
         assert torch.equal(beside.data, alone.data)
         assert beside.check() is False
     assert alone.check() is False
+
+
+# ---- queries near the end of bfloat16's range ---------------------------------------------
+@pytest.mark.parametrize("dim,ratio,new", [(64, 4, 1), (128, 7, 4), (192, 2, 4), (64, 4, 30), (256, 2, 40)])
+def test_attention_of_the_largest_queries(vbq, dim, ratio, new):
+    """Queries of up to 2^119 on keys of ordinary size: scores are numbers that fp32 holds, and the largest takes its row.
+    Rows whose two largest scores are nearer than 8 times their rounding (see the scores far out) are left out."""
+    import torch
+    gen = torch.Generator(device="cuda").manual_seed(dim + new)
+    i32 = dict(dtype=torch.int32, device="cuda")
+    L = 300
+    k, v = torch.randn(2, L, 1, dim, generator=gen, device="cuda")
+    q = ((torch.rand(new, ratio, dim, generator=gen, device="cuda") - 0.5) * 2.0 ** 120).bfloat16()
+    cache = vbq.Kv4Cache(16, 32, 1, dim)
+    table, cu = torch.arange(16, **i32).view(1, 16), torch.tensor([0, L], **i32)
+    vbq.kv4_append(cache, k, v, table, torch.zeros(1, **i32), cu)
+    rk, rv = (x.double()[:, 0] for x in vbq.kv4_read(cache, table, torch.zeros(1, **i32), cu, L, torch.float32))
+    lse = torch.empty(new, ratio, device="cuda")
+    got = vbq.kv4_attention(cache, q, table, torch.tensor([L], **i32), torch.tensor([0, new], **i32), new, L, lse=lse)
+    assert torch.isfinite(got).all() and torch.isfinite(lse).all()
+    used = 0
+    for i in range(new):
+        for r in range(ratio):
+            qd = q[i, r].double()
+            s = rk[:L - new + i + 1] @ qd * dim ** -0.5
+            off = (dim + 17) * 2.0 ** -24 * float(qd.abs().sum() * 4 * rk.abs().max()) * dim ** -0.5
+            top = torch.topk(s, 2).values
+            assert abs(float(lse[i, r]) - float(top[0])) <= off + 2.0 ** -22 * abs(float(top[0]))
+            if float(top[0] - top[1]) < 8 * off + 40:
+                continue
+            used += 1
+            want = rv[int(s.argmax())]
+            assert ((got[i, r].double() - want).abs() <= (2.0 ** -8 + 2.1 * 2.0 ** -11) * want.abs() + 2.0 ** -24).all()
+    assert used * 2 >= new * ratio

@@ -116,3 +116,14 @@ def test_a_cache_is_on_a_gpu(device):
         vbq.Kv4Cache(2, 32, 1, 64, device=device)
     with pytest.raises(ValueError, match="expected a GPU"):
         vbq.Kv4Cache(2, 32, 1, 64, data=torch.zeros(2 * 2304, dtype=torch.uint8, device=device))
+
+
+def test_attention_refuses_a_scale_that_binary32_does_not_hold_in_base_two():
+    """Scores are formed in base two: scale * log2(e) has to be a number."""
+    import packed_decode_gemv_amd as vbq
+    c = _cache(vbq)
+    for scale, ok in ((2.3e38, True), (2.4e38, False), (2.9e38, False), (3.4e38, False), (1e-38, True)):
+        a = _attn(vbq, scale=scale)
+        assert (vbq.lib.kv4_attention_workspace(C.byref(c), C.byref(a)) >= 0) is ok, scale
+        if not ok:
+            assert vbq.lib.kv4_attention(C.byref(c), C.byref(a), None) == 1
