@@ -13,16 +13,25 @@
 //
 // Scores. S^T = K Q^T by 16x16x32 fp16 MFMAs: A is a block's key codes, 16
 // tokens by 32 channels of one group, B the queries. A code word holds eight
-// channels of a token; masked with 0x000F000F and 0x00F000F0 it is a pair of
-// fp16 subnormals c 2^-24 and 16 c 2^-24, exact operands (the queries that
-// meet the latter are divided by 16). The group's scale and offset enter in
+// channels of a token; a pair of codes masked out at bits 4-7 of each half is a
+// pair of fp16 numbers c 2^-20. The group's scale and offset enter in
 // fp32: score = sum_g s_g (codes . q)_g + o_g sum_g(q).
+//   Where a code lies in the number matters, exact as it is anywhere. The
+// matrix unit adds the eight products of a lane and cuts off what lies 24 bits
+// below the largest, counted from its exponent; a subnormal has the exponent of
+// 2^-14, so each zero in front of its bits costs one. At bits 4-7 it keeps a
+// product of a code and a query down to 2^-18 of the largest query, at bits 0-3
+// (c 2^-24, two shifts a word less) only to 2^-14: outputs of 32 sequences of
+// 167000 tokens were off by 2.42e-4 (relative, whole tensor) with those and are
+// off by 2.09e-4 with these, which is the rounding of the output itself. Normal
+// numbers (c 2^-10, a product a pair) change nothing more there and take 55 us
+// where these take 52 (and bits 0-3 took 51).
 // Queries are scaled to a largest magnitude in [2^13, 2^14) per row (a power
-// of two, undone in the score), so that fp16 holds them exactly down to 2^-26
-// (bf16; 2^-23 fp16) of the row's largest, the odd pairs' 1/16 included.
+// of two, undone in the score), so that fp16 holds them exactly down to 2^-30
+// (bf16; 2^-27 fp16) of the row's largest.
 //
 // Output. O^T = V^T P^T by the same MFMA: A is the value codes, 16 channels by
-// 32 tokens, again as fp16 subnormals; B the probabilities as they come out of
+// 32 tokens, again as c 2^-20; B the probabilities as they come out of
 // the score MFMA: its result holds tokens 4 q + i of a column (row of the
 // problem) in lane quarter q, and the cache orders a block's tokens so that
 // those of both 16-token halves are the octet 8 q .. 8 q + 7, a value word. B
@@ -138,17 +147,16 @@ __device__ inline int wave_scan(int v) {
   return v;
 }
 
-// Eight codes of a word as fp16 subnormals: pairs (n, n + 4), the odd pairs
-// times 16.
+// Eight codes of a word as fp16 numbers c 2^-kCodeExp (subnormal), pairs (n, n + 4).
 __device__ inline half8_t codes_of(uint32_t w) {
   u32x4 r;
-  r.x = w & 0x000F000Fu;
+  r.x = (w << 4) & 0x00F000F0u;
   r.y = w & 0x00F000F0u;
-  const uint32_t h = w >> 8;
-  r.z = h & 0x000F000Fu;
-  r.w = h & 0x00F000F0u;
+  r.z = (w >> 4) & 0x00F000F0u;
+  r.w = (w >> 8) & 0x00F000F0u;
   return __builtin_bit_cast(half8_t, r);
 }
+constexpr int kCodeExp = 20;
 
 __device__ inline half2_t pair_of(uint32_t w) { return __builtin_bit_cast(half2_t, w); }
 
@@ -327,7 +335,6 @@ __global__ __launch_bounds__((64 * kWaves<G, ROWS>), (kRoomy<G, ROWS>) ? 4 : G *
   constexpr int WAVES = kWaves<G, ROWS>, D = 64 * G, PITCH = D + 4, BYTES = kKvGroupBytes * G;
   constexpr int NT = ROWS > 16 ? 2 : 1, COLS = ROWS > 16 ? 16 : ROWS;   // column tiles, and columns used of each
   constexpr int PARTS = 16 / COLS, PAIRS = 4 / PARTS;   // lanes that share a row's octet, token pairs of each
-  constexpr int ODD = PARTS == 4 ? 1 : 2;   // sums kept apart for pairs whose codes come times 16
   constexpr int RING = WAVES * STAGES * BYTES, SUMS = WAVES * COLS * PITCH * 4;
   constexpr int JOIN = ROWS * kParts * 4 + 64 * WAVES * 16, AFTER = SUMS > JOIN ? SUMS : JOIN;
   // blocks; afterwards the wavefronts' sums, or the parts' factors and shares
@@ -482,7 +489,7 @@ __global__ __launch_bounds__((64 * kWaves<G, ROWS>), (kRoomy<G, ROWS>) ? 4 : G *
     int ex = (int)(__builtin_bit_cast(uint32_t, top) >> 23) - 127;
     ex = top > 0.f ? max(ex, -100) : 13;
     const float up = ldexpf(1.f, 13 - ex);
-    to_log2[nt] = ldexpf(a.scale_log2, ex - 13 + 24);
+    to_log2[nt] = ldexpf(a.scale_log2, ex - 13 + kCodeExp);
 #pragma unroll
     for (int g = 0; g < G; ++g) {
       float sum = 0.f;
@@ -492,11 +499,10 @@ __global__ __launch_bounds__((64 * kWaves<G, ROWS>), (kRoomy<G, ROWS>) ? 4 : G *
         for (int i = 0; i < 4; ++i) {
           const _Float16 v0 = (_Float16)(x[g][st][i] * up), v1 = (_Float16)(x[g][st][i + 4] * up);
           sum += (float)v0 + (float)v1;
-          const _Float16 f = (i & 1) ? (_Float16)0.0625f : (_Float16)1.f;
-          qf[nt][g][st][2 * i] = v0 * f;
-          qf[nt][g][st][2 * i + 1] = v1 * f;
+          qf[nt][g][st][2 * i] = v0;
+          qf[nt][g][st][2 * i + 1] = v1;
         }
-      qsum[nt][g] = rows_sum(sum) * 0x1p-24f;
+      qsum[nt][g] = ldexpf(rows_sum(sum), -kCodeExp);
     }
     const int p = a.causal ? first + qi : len - 1;
     hi[nt] = in ? min(p, len - 1) : -1;
@@ -504,8 +510,8 @@ __global__ __launch_bounds__((64 * kWaves<G, ROWS>), (kRoomy<G, ROWS>) ? 4 : G *
   }
 
   // Running maximum m, and sums held times 2^base, base = S - m: of p, of p o,
-  // and (times 2^-24) of p s code.
-  float m[NT], base[NT], l[NT][ODD], po[NT][G][ODD];
+  // and (times 2^-kCodeExp) of p s code.
+  float m[NT], base[NT], l[NT], po[NT][G];
   f32x4 acc[NT][G][4];
   float mul[NT], add[NT];   // of a score on its way to exp2
   bool far = false;         // a row of the wavefront has its maximum far out
@@ -519,17 +525,14 @@ __global__ __launch_bounds__((64 * kWaves<G, ROWS>), (kRoomy<G, ROWS>) ? 4 : G *
     base[nt] = -kNoMax;
     mul[nt] = to_log2[nt];
     add[nt] = base[nt];
-#pragma unroll
-    for (int d = 0; d < ODD; ++d) l[nt][d] = 0.f;
+    l[nt] = 0.f;
 #pragma unroll
     for (int g = 0; g < G; ++g) {
-#pragma unroll
-      for (int d = 0; d < ODD; ++d) po[nt][g][d] = 0.f;
+      po[nt][g] = 0.f;
 #pragma unroll
       for (int w = 0; w < 4; ++w) acc[nt][g][w] = f32x4{0.f, 0.f, 0.f, 0.f};
     }
   }
-  const float lane_odd = PARTS == 4 && (part & 1u) ? -4.f : 0.f;
 
   for (int it = 0; it < count; ++it) {
     // This block's copy has landed (later ones may be on their way), and the
@@ -664,12 +667,10 @@ __global__ __launch_bounds__((64 * kWaves<G, ROWS>), (kRoomy<G, ROWS>) ? 4 : G *
         m[nt] = mt[nt];
         const float now = shift[nt] - mt[nt], f = __builtin_amdgcn_exp2f(now - base[nt]);
         base[nt] = now;
-#pragma unroll
-        for (int d = 0; d < ODD; ++d) l[nt][d] *= f;
+        l[nt] *= f;
 #pragma unroll
         for (int g = 0; g < G; ++g) {
-#pragma unroll
-          for (int d = 0; d < ODD; ++d) po[nt][g][d] *= f;
+          po[nt][g] *= f;
 #pragma unroll
           for (int w = 0; w < 4; ++w) acc[nt][g][w] *= f;
         }
@@ -692,16 +693,15 @@ __global__ __launch_bounds__((64 * kWaves<G, ROWS>), (kRoomy<G, ROWS>) ? 4 : G *
 #pragma unroll
           for (int h = 0; h < 2; ++h) sc[nt][j][h] = below(sc[nt][j][h], to_log2[nt], m[nt]);
     }
-    // Probabilities times 2^S, those of odd pairs divided by 16.
+    // Probabilities times 2^S.
     float p[NT][PAIRS][2];
 #pragma unroll
     for (int nt = 0; nt < NT; ++nt)
 #pragma unroll
       for (int j = 0; j < PAIRS; ++j) {
-        const float bs = add[nt] + (PARTS == 4 ? lane_odd : j & 1 ? -4.f : 0.f);
 #pragma unroll
-        for (int h = 0; h < 2; ++h) p[nt][j][h] = __builtin_amdgcn_exp2f(__builtin_fmaf(sc[nt][j][h], mul[nt], bs));
-        l[nt][j % ODD] += p[nt][j][0] + p[nt][j][1];
+        for (int h = 0; h < 2; ++h) p[nt][j][h] = __builtin_amdgcn_exp2f(__builtin_fmaf(sc[nt][j][h], mul[nt], add[nt]));
+        l[nt] += p[nt][j][0] + p[nt][j][1];
       }
 #pragma unroll
     for (int g = 0; g < G; ++g) {
@@ -717,8 +717,7 @@ __global__ __launch_bounds__((64 * kWaves<G, ROWS>), (kRoomy<G, ROWS>) ? 4 : G *
           const half2_t r = {(_Float16)(u0 - (float)b.x), (_Float16)(u1 - (float)b.y)};
           x[j] = __builtin_bit_cast(uint32_t, b);
           y[j] = __builtin_bit_cast(uint32_t, r);
-          po[nt][g][j % ODD] =
-              __builtin_fmaf(p[nt][j][0], (float)o.x, __builtin_fmaf(p[nt][j][1], (float)o.y, po[nt][g][j % ODD]));
+          po[nt][g] = __builtin_fmaf(p[nt][j][0], (float)o.x, __builtin_fmaf(p[nt][j][1], (float)o.y, po[nt][g]));
         }
         // The octet's four pairs, from the lanes that hold them, in column `qcol`.
         u32x4 bx, by;
@@ -752,13 +751,9 @@ __global__ __launch_bounds__((64 * kWaves<G, ROWS>), (kRoomy<G, ROWS>) ? 4 : G *
   float sum_l[NT];
 #pragma unroll
   for (int nt = 0; nt < NT; ++nt) {
-    const float times = PARTS == 4 && (part & 1u) ? 16.f : 1.f;
-    auto whole_row = [&](const float(&v)[ODD]) {
-      return lanes_sum<PARTS>(ODD == 2 ? v[0] + 16.f * v[ODD - 1] : times * v[0]);
-    };
-    sum_l[nt] = whole_row(l[nt]);
+    sum_l[nt] = lanes_sum<PARTS>(l[nt]);
 #pragma unroll
-    for (int g = 0; g < G; ++g) po[nt][g][0] = whole_row(po[nt][g]);
+    for (int g = 0; g < G; ++g) po[nt][g] = lanes_sum<PARTS>(po[nt][g]);
     if (quarter == 0 && part == 0) {
       wml[wave][16 * nt + qcol][0] = base[nt];
       wml[wave][16 * nt + qcol][1] = sum_l[nt];
@@ -776,15 +771,15 @@ __global__ __launch_bounds__((64 * kWaves<G, ROWS>), (kRoomy<G, ROWS>) ? 4 : G *
       float low = wml[0][rr][0];
 #pragma unroll
       for (int w = 1; w < WAVES; ++w) low = fminf(low, wml[w][rr][0]);
-      const float f = __builtin_amdgcn_exp2f(low - base[nt]), f24 = f * 0x1p24f;
+      const float f = __builtin_amdgcn_exp2f(low - base[nt]), f_code = ldexpf(f, kCodeExp);
       float* const to = buf + (wave * COLS + qcol) * PITCH + 16 * quarter;
 #pragma unroll
       for (int g = 0; g < G; ++g) {
-        const float z = po[nt][g][0] * f;
+        const float z = po[nt][g] * f;
 #pragma unroll
         for (int i = 0; i < 4; ++i) {
-          const f32x4 v = {__builtin_fmaf(acc[nt][g][0][i], f24, z), __builtin_fmaf(acc[nt][g][1][i], f24, z),
-                           __builtin_fmaf(acc[nt][g][2][i], f24, z), __builtin_fmaf(acc[nt][g][3][i], f24, z)};
+          const f32x4 v = {__builtin_fmaf(acc[nt][g][0][i], f_code, z), __builtin_fmaf(acc[nt][g][1][i], f_code, z),
+                           __builtin_fmaf(acc[nt][g][2][i], f_code, z), __builtin_fmaf(acc[nt][g][3][i], f_code, z)};
           *reinterpret_cast<f32x4*>(to + 64 * g + 4 * i) = v;
         }
       }
@@ -929,8 +924,10 @@ __global__ __launch_bounds__((64 * kWaves<G, ROWS>), (kRoomy<G, ROWS>) ? 4 : G *
 // the values of block i + 1, forms the scores of block i + 1 and the
 // probabilities and output of block i, in one straight piece of code, so that
 // matrix and vector instructions overlap. Key
-// operands are the exact codes (fp16 subnormals), scores take scale in fp32 as
-// above and offsets by one more MFMA: A holds a token's offsets o_g, B the rows'
+// operands are the exact codes (normal fp16 numbers: a word is spread once for
+// 128 rows, and the matrix unit keeps all of their products, as explained above;
+// 2048 queries over 10240 tokens take 438 us so, 433 with subnormal c 2^-20),
+// scores take scale in fp32 as above and offsets by one more MFMA: A holds a token's offsets o_g, B the rows'
 // sums of q over group g. Rounding keys to fp16 instead would save the scaling,
 // but a score's error is multiplied into its probability: it doubled the
 // output's error in fp16. Values are s c + o rounded once to fp16, as are
@@ -962,6 +959,19 @@ typedef float f32x16 __attribute__((ext_vector_type(16)));
 
 constexpr float kTileShift = 7.f;   // probabilities are held times 2^7 ...
 constexpr float kTileSlack = 8.f;   // ... and the maximum may be passed by 2^8 before sums are scaled
+
+// Eight codes of a word as normal fp16 numbers c 2^-kTileCodeExp, pairs (n, n + 4).
+constexpr int kTileCodeExp = 10;
+__device__ inline half8_t normal_codes_of(uint32_t w) {
+  const half2_t up = {(_Float16)0x1p14f, (_Float16)0x1p14f}, up4 = {(_Float16)0x1p10f, (_Float16)0x1p10f};
+  const uint32_t h = w >> 8;
+  u32x4 r;
+  r.x = __builtin_bit_cast(uint32_t, pair_of(w & 0x000F000Fu) * up);
+  r.y = __builtin_bit_cast(uint32_t, pair_of(w & 0x00F000F0u) * up4);
+  r.z = __builtin_bit_cast(uint32_t, pair_of(h & 0x000F000Fu) * up);
+  r.w = __builtin_bit_cast(uint32_t, pair_of(h & 0x00F000F0u) * up4);
+  return __builtin_bit_cast(half8_t, r);
+}
 
 // Constants of the decode, opaque to the compiler: with the masks in scalar and
 // the exponent in a vector register (w & mask) | exponent is one instruction;
@@ -1130,7 +1140,7 @@ __global__ __launch_bounds__(256, G >= 4 ? 1 : 2) void k_kv4_attn_tile(KvAttn a)
     int ex = (int)(__builtin_bit_cast(uint32_t, top) >> 23) - 127;
     ex = top > 0.f ? max(ex, -100) : 13;
     const float up = ldexpf(1.f, 13 - ex);
-    to_log2 = ldexpf(a.scale_log2, ex - 13 + 24);
+    to_log2 = ldexpf(a.scale_log2, ex - 13 + kTileCodeExp);
 #pragma unroll
     for (int j = 0; j < 8; ++j) qsum[j] = (_Float16)0.f;
 #pragma unroll
@@ -1142,12 +1152,11 @@ __global__ __launch_bounds__(256, G >= 4 ? 1 : 2) void k_kv4_attn_tile(KvAttn a)
         for (int i = 0; i < 4; ++i) {
           const _Float16 v0 = (_Float16)(y[c][i] * up), v1 = (_Float16)(y[c][i + 4] * up);
           sum += (float)v0 + (float)v1;
-          const _Float16 f = (i & 1) ? (_Float16)0.0625f : (_Float16)1.f;
-          qf[c][2 * i] = v0 * f;
-          qf[c][2 * i + 1] = v1 * f;
+          qf[c][2 * i] = v0;
+          qf[c][2 * i + 1] = v1;
         }
       // the sum as two fp16 numbers, the second times 2^11 (and its offsets by 2^-11)
-      sum = half_sum(sum) * 0x1p-24f;
+      sum = ldexpf(half_sum(sum), -kTileCodeExp);
       const _Float16 big = (_Float16)sum;
       qsum[2 * g] = big;
       qsum[2 * g + 1] = (_Float16)((sum - (float)big) * 0x1p11f);
@@ -1169,7 +1178,8 @@ __global__ __launch_bounds__(256, G >= 4 ? 1 : 2) void k_kv4_attn_tile(KvAttn a)
                                                  (m16 & 7u)) * 16;
 #pragma unroll
     for (int g = 0; g < G; ++g)
-      *reinterpret_cast<half8_t*>(to + 8 * 32 * 16 * g) = codes_of(*reinterpret_cast<const uint32_t*>(from + 1024 * g));
+      *reinterpret_cast<half8_t*>(to + 8 * 32 * 16 * g) =
+          normal_codes_of(*reinterpret_cast<const uint32_t*>(from + 1024 * g));
   };
   auto spread_values = [&](int i) {
     const uint8_t* const from = raw + (i % RAW) * BYTES;

@@ -851,3 +851,103 @@ def test_attention_of_the_largest_queries(vbq, dim, ratio, new):
             want = rv[int(s.argmax())]
             assert ((got[i, r].double() - want).abs() <= (2.0 ** -8 + 2.1 * 2.0 ** -11) * want.abs() + 2.0 ** -24).all()
     assert used * 2 >= new * ratio
+
+
+# ---- products of codes lose nothing that binary32 holds -------------------------------------
+def blank_cache(n_pages, heads, dim):
+    return np.zeros(n_pages * heads * 2304 * (dim // 64), np.uint8), Layout(32, heads, dim)
+
+
+@pytest.mark.parametrize("dtype", ["float16", "bfloat16"])
+@pytest.mark.parametrize("dim", [64, 128, 192, 256])
+@pytest.mark.parametrize("ratio,new", [(4, 1), (8, 1), (8, 2), (8, 4), (8, 5)])      # every tile
+def test_scores_that_binary32_holds_are_exact(vbq, dtype, dim, ratio, new):
+    """Sequences of one token, so lse is the score. One channel of the query is 2^8 times the others, scales are 1 and
+    offsets -8: every sum of products is a whole multiple of 2^-18 below 2^5 in magnitude, in any order, which
+    binary32 holds exactly. What is left are roundings of the score on its way to lse, u = 2^-24: scale * log2(e), two
+    products and a difference, one u each of the score, and exponential and logarithm of a number of magnitude up
+    to 16, a last place each, and its own rounding: below 8 u |score| + 2^-18."""
+    import torch
+    rng = np.random.default_rng(dim + new + ratio)
+    B, G = 6, dim // 64
+    data, lay = blank_cache(B, 1, dim)
+    codes = rng.integers(0, 16, (B, G, 64)).astype(np.uint32)
+    one, off, zero = np.ones(G, np.float16), np.full(G, -8, np.float16), np.zeros(G, np.float16)
+    for b in range(B):
+        lay.write(data, lay.block(b, 0, 0), 0, 0, codes[b], one, off)
+        lay.write(data, lay.block(b, 0, 0), 0, 1, codes[b], one, zero)
+    T, steps = B * new, 1024 if dtype == "float16" else 128
+    q = (1 + rng.integers(0, steps, (T, ratio, dim)) / steps) * rng.choice([-1, 1], (T, ratio, dim)) * 2.0 ** -8
+    big = rng.integers(0, 64, (T, ratio))
+    np.put_along_axis(q, big[..., None], np.take_along_axis(q, big[..., None], -1) * 2.0 ** 8, -1)
+    qt = torch.from_numpy(q).to(getattr(torch, dtype))
+    assert np.array_equal(qt.double().numpy(), q)
+    cache = vbq.Kv4Cache(B, 32, 1, dim, data=gpu(data))
+    lse = torch.full((T, ratio), float("nan"), device="cuda")
+    vbq.kv4_attention(cache, qt.cuda(), torch.arange(B, dtype=torch.int32, device="cuda").view(B, 1),
+                      gpu(np.ones(B, np.int32)), gpu(cum([new] * B)), new, 1, scale=8.0, causal=False, lse=lse)
+    K = codes.reshape(B, dim).astype(np.float64) - 8
+    want = 8 * np.einsum("trd,td->tr", q, np.repeat(K, new, 0))
+    err = np.abs(lse.cpu().numpy().astype(np.float64) - want)
+    bound = 8 * 2.0 ** -24 * np.abs(want) + 2.0 ** -18
+    assert (err <= bound).all(), float((err / bound).max())
+
+
+@pytest.mark.parametrize("dim,ratio,new", [(d, r, n) for d in (64, 128, 192, 256)      # every tile of the few-row kernel
+                                           for r, n in ((4, 1), (8, 1), (8, 2), (8, 4)) if d < 256 or r * n <= 16])
+def test_sums_of_values_that_binary32_holds_are_exact(vbq, dim, ratio, new):
+    """Sixteen tokens of equal probability (queries of 0), two with scales 2^8 times the others', offsets about -7.5
+    scales: sums of s c are whole multiples of 2^-18 below 2^6 and those of offsets too, in any order, so binary32 holds
+    them and their difference, and the output is the exact mean, rounded once."""
+    import torch
+    rng = np.random.default_rng(dim + new + ratio)
+    G, n = dim // 64, 16
+    data, lay = blank_cache(1, 1, dim)
+    want = np.zeros(dim)
+    for t in range(n):
+        codes = rng.integers(0, 16, (G, 64)).astype(np.uint32)
+        s = ((1 + rng.integers(0, 1024, G) / 1024) * (1.0 if t in (5, 8) else 2.0 ** -8)).astype(np.float16)
+        o = (-7.5 * s.astype(np.float64)).astype(np.float16)
+        lay.write(data, lay.block(0, 0, t), t, 0, codes, s, o)
+        lay.write(data, lay.block(0, 0, t), t, 1, codes, s, o)
+        want += (codes * s.astype(np.float64)[:, None] + o.astype(np.float64)[:, None]).reshape(-1)
+    cache = vbq.Kv4Cache(1, 32, 1, dim, data=gpu(data))
+    i32 = dict(dtype=torch.int32, device="cuda")
+    got = vbq.kv4_attention(cache, torch.zeros(new, ratio, dim, device="cuda").half(), torch.zeros(1, 1, **i32),
+                            torch.tensor([n], **i32), torch.tensor([0, new], **i32), new, n, causal=False)
+    want = (want / n).astype(np.float16)
+    assert (got.cpu().numpy() == want).all()
+
+
+@pytest.mark.parametrize("batch,heads,ratio,dim,kv", [(8, 4, 4, 128, 1500), (6, 4, 1, 64, 5000), (4, 4, 2, 192, 1700),
+                                                      (6, 2, 6, 128, 2500), (5, 2, 20, 64, 1500), (4, 2, 8, 256, 1500)])
+def test_few_rows_are_as_near_as_the_output_type_allows(vbq, batch, heads, ratio, dim, kv):
+    """Keys with strong channels over many tokens, fp16 outputs: the root mean square error exceeds that of the exact
+    outputs' own rounding by what binary32 scores leave. A score's terms have magnitudes that add up to
+    S = scale sum |q| (|s c| + |o|), up to 250 here; its sums take four roundings of such a size (two products a
+    group, scale, offset): 4 u S = 6e-5 of a probability."""
+    import torch
+    gen = torch.Generator(device="cuda").manual_seed(dim + kv)
+    i32 = dict(dtype=torch.int32, device="cuda")
+    pages = -(-kv // 256)
+    cache = vbq.Kv4Cache(batch * pages, 256, heads, dim)
+    table = torch.randperm(batch * pages, generator=gen, device="cuda").int().view(batch, pages)
+    gain = torch.ones(dim, device="cuda")
+    gain[::17] = 4.0
+    k, v = torch.randn(2, batch * kv, heads, dim, generator=gen, device="cuda")
+    k = k * gain + torch.randn(heads, dim, generator=gen, device="cuda")
+    start, cu = torch.zeros(batch, **i32), torch.arange(0, batch * kv + 1, kv, **i32)
+    vbq.kv4_append(cache, k, v, table, start, cu, max_tokens=kv)
+    k, v = (x.double().view(batch, kv, heads, dim) for x in
+            vbq.kv4_read(cache, table, start, cu, batch * kv, torch.float32, max_tokens=kv))
+    q = (torch.randn(batch, heads * ratio, dim, generator=gen, device="cuda") * 1.5).half()
+    got = vbq.kv4_attention(cache, q, table, torch.full((batch,), kv, **i32), torch.arange(batch + 1, **i32), 1, kv)
+    want = torch.empty(batch, heads * ratio, dim, dtype=torch.float64, device="cuda")
+    for b in range(batch):
+        for h in range(heads):
+            rows = slice(h * ratio, (h + 1) * ratio)
+            p = torch.softmax(q[b, rows].double() @ k[b, :, h].T.contiguous() * dim ** -0.5, -1)
+            want[b, rows] = p @ v[b, :, h].contiguous()
+    rms = lambda x: float(x.square().mean().sqrt())
+    more = rms(got.double() - want) ** 2 - rms(want.half().double() - want) ** 2
+    assert max(more, 0.0) ** 0.5 <= 6e-5 * rms(want), (max(more, 0.0) ** 0.5 / rms(want))
