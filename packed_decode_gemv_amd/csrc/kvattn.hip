@@ -1155,11 +1155,11 @@ __global__ __launch_bounds__(256, G >= 4 ? 1 : 2) void k_kv4_attn_tile(KvAttn a)
           qf[c][2 * i] = v0;
           qf[c][2 * i + 1] = v1;
         }
-      // the sum as two fp16 numbers, the second times 2^11 (and its offsets by 2^-11)
+      // the sum as two fp16 numbers, which leave 2^-25 at most of it (the row's largest |q| is 2^3 or more here)
       sum = ldexpf(half_sum(sum), -kTileCodeExp);
       const _Float16 big = (_Float16)sum;
       qsum[2 * g] = big;
-      qsum[2 * g + 1] = (_Float16)((sum - (float)big) * 0x1p11f);
+      qsum[2 * g + 1] = (_Float16)(sum - (float)big);
     }
     const int p = a.causal ? first + qi : len - 1;
     hi = r < rows ? min(p, len - 1) : -1;
@@ -1219,8 +1219,7 @@ __global__ __launch_bounds__(256, G >= 4 ? 1 : 2) void k_kv4_attn_tile(KvAttn a)
 #pragma unroll
     for (int g = 0; g < G; ++g) {
       const _Float16 o = *reinterpret_cast<const _Float16*>(so + 128 * g + 64 + 2 * tok);
-      off[2 * g] = half ? (_Float16)0.f : o;
-      off[2 * g + 1] = half ? (_Float16)0.f : o * (_Float16)0x1p-11f;
+      off[2 * g] = off[2 * g + 1] = half ? (_Float16)0.f : o;
     }
     x = __builtin_amdgcn_mfma_f32_32x32x16_f16(off, qsum, none, 0, 0, 0);
 #pragma unroll

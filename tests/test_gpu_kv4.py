@@ -951,3 +951,36 @@ def test_few_rows_are_as_near_as_the_output_type_allows(vbq, batch, heads, ratio
     rms = lambda x: float(x.square().mean().sqrt())
     more = rms(got.double() - want) ** 2 - rms(want.half().double() - want) ** 2
     assert max(more, 0.0) ** 0.5 <= 6e-5 * rms(want), (max(more, 0.0) ** 0.5 / rms(want))
+
+
+@pytest.mark.parametrize("dim", [64, 128, 192, 256])
+@pytest.mark.parametrize("ratio,new", [(4, 1), (8, 2), (8, 4), (8, 5), (2, 40)])
+@pytest.mark.parametrize("exp", [-14, -12, -9, -4, 0, 15])
+def test_key_offsets_of_any_size_enter_scores_in_binary32(vbq, dim, ratio, new, exp):
+    """Sequences of one token whose keys are constant groups (scale 0, offset o of about 2^exp), so lse is scale * sum of
+    o sum(q). Queries of one binade: their sums are exact in binary32. Products with offsets and their sum over groups,
+    all of one sign, take below 8 u; with the roundings of test_scores_that_binary32_holds_are_exact below
+    16 u |score| + 2^-18."""
+    import torch
+    rng = np.random.default_rng(dim + new + ratio + 50 + exp)
+    B, G = 4, dim // 64
+    data, lay = blank_cache(B, 1, dim)
+    off = ((1 + rng.integers(0, 1024, (B, G)) / 1024) * 2.0 ** exp).astype(np.float16)
+    off = np.minimum(off, np.float16(61440))
+    for b in range(B):
+        zero = np.zeros(G, np.float16)
+        lay.write(data, lay.block(b, 0, 0), 0, 0, rng.integers(0, 16, (G, 64)).astype(np.uint32), zero, off[b])
+        lay.write(data, lay.block(b, 0, 0), 0, 1, np.zeros((G, 64), np.uint32), zero, zero)
+    T = B * new
+    q = 1 + rng.integers(0, 1024, (T, ratio, dim)) / 1024
+    scale = 2.0 ** (-2 - exp)
+    cache = vbq.Kv4Cache(B, 32, 1, dim, data=gpu(data))
+    lse = torch.full((T, ratio), float("nan"), device="cuda")
+    vbq.kv4_attention(cache, torch.from_numpy(q).half().cuda(),
+                      torch.arange(B, dtype=torch.int32, device="cuda").view(B, 1), gpu(np.ones(B, np.int32)),
+                      gpu(cum([new] * B)), new, 1, scale=scale, causal=False, lse=lse)
+    sums = q.reshape(T, ratio, G, 64).sum(-1)
+    want = scale * np.einsum("trg,tg->tr", sums, np.repeat(off.astype(np.float64), new, 0))
+    err = np.abs(lse.cpu().numpy().astype(np.float64) - want)
+    bound = 16 * 2.0 ** -24 * np.abs(want) + 2.0 ** -18
+    assert (err <= bound).all(), float((err / bound).max())
