@@ -575,11 +575,15 @@ class Kv4Cache:
         return self.n_pages * self.page_bytes
 
     def check(self):
-        """Waits for the device and raises VbqError if a call so far met a page
-        outside the cache or lengths that do not fit; returns True if a NaN was
-        stored as 0, else False. The flags are cleared."""
+        """Waits for the device, all streams of it, and raises VbqError if a call
+        so far met a page outside the cache or lengths that do not fit; returns
+        True if a NaN was stored as 0, else False. The flags are cleared."""
+        import torch
+        torch.cuda.synchronize(self.device)
         f = int(self.flags.item())
-        self.flags.zero_()
+        if f:
+            self.flags.zero_()
+            torch.cuda.current_stream(self.device).synchronize()   # or a later call's flag could be cleared with them
         if f & (KV4_FLAG_PAGE | KV4_FLAG_LENGTH):
             raise VbqError(6, "Kv4Cache: " + " and ".join(
                 n for b, n in ((KV4_FLAG_PAGE, "a block-table entry outside the cache"),

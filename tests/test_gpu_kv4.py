@@ -984,3 +984,19 @@ def test_key_offsets_of_any_size_enter_scores_in_binary32(vbq, dim, ratio, new, 
     err = np.abs(lse.cpu().numpy().astype(np.float64) - want)
     bound = 16 * 2.0 ** -24 * np.abs(want) + 2.0 ** -18
     assert (err <= bound).all(), float((err / bound).max())
+
+
+def test_check_waits_for_calls_on_other_streams(vbq):
+    import torch
+    i32 = dict(dtype=torch.int32, device="cuda")
+    cache = vbq.Kv4Cache(2, 32, 1, 64)
+    k = torch.zeros(1, 1, 64, device="cuda")
+    args = (torch.tensor([[7]], **i32), torch.zeros(1, **i32), torch.tensor([0, 1], **i32))      # page 7 of 2
+    side = torch.cuda.Stream()
+    torch.cuda.synchronize()
+    with torch.cuda.stream(side):
+        torch.cuda._sleep(20_000_000)        # work ahead of the call on its stream
+    vbq.kv4_append(cache, k, k, *args, stream=side)
+    with pytest.raises(vbq.VbqError, match="block-table"):
+        cache.check()
+    assert cache.check() is False
