@@ -124,7 +124,7 @@ def _load():
     lib.kv4_read.restype = C.c_int
     lib.kv4_read.argtypes = [C.POINTER(vbq_kv4), P, P, P, I32, P]
     lib.kv4_attention_workspace.restype = I64
-    lib.kv4_attention_workspace.argtypes = [C.POINTER(vbq_kv4), C.POINTER(vbq_kv4_attn)]
+    lib.kv4_attention_workspace.argtypes = [C.POINTER(vbq_kv4), P]
     lib.kv4_attention.restype = C.c_int
     lib.kv4_attention.argtypes = [C.POINTER(vbq_kv4), P, P]
     return lib
@@ -545,7 +545,8 @@ class Kv4Cache:
 
     def __init__(self, n_pages: int, page_tokens: int, n_kv_heads: int, head_dim: int, device="cuda", data=None):
         import torch
-        self.page_bytes = lib.kv4_page_bytes(page_tokens, n_kv_heads, head_dim)
+        ints = max(page_tokens, n_kv_heads, head_dim) < 2 ** 31 and min(page_tokens, n_kv_heads, head_dim) > 0
+        self.page_bytes = lib.kv4_page_bytes(page_tokens, n_kv_heads, head_dim) if ints else 0
         if self.page_bytes == 0 or not 1 <= n_pages < 2 ** 31:
             raise ValueError(f"Kv4Cache: {n_pages} pages of {page_tokens} tokens, {n_kv_heads} heads of {head_dim}: "
                              "pages take a power of two of tokens (32..65536), heads 64, 128, 192 or 256 channels")
@@ -620,8 +621,11 @@ def kv4_append(cache: Kv4Cache, k, v, block_table, start, cu_tokens, max_tokens=
     dt = _kv4_dtype(k.dtype, "k")
     if v.dtype is not k.dtype or Tv != T:
         raise ValueError(f"v: {v.dtype} {tuple(v.shape)}, expected k's {k.dtype} {tuple(k.shape)}")
-    r = _KV4_RANGE.pack(B, W, T, T if max_tokens is None else max_tokens, block_table.data_ptr(), start.data_ptr(),
-                        cu_tokens.data_ptr())
+    try:
+        r = _KV4_RANGE.pack(B, W, T, T if max_tokens is None else max_tokens, block_table.data_ptr(), start.data_ptr(),
+                            cu_tokens.data_ptr())
+    except struct.error as e:
+        raise ValueError(f"kv4_append: max_tokens {max_tokens}, {T} tokens: {e}") from None
     st = lib.kv4_append(cache._ref, r, k.data_ptr(), v.data_ptr(), dt, kts, khs, vts, vhs, _kv4_stream(cache, stream))
     if st:
         _check(st, "kv4_append")
@@ -642,8 +646,11 @@ def kv4_read(cache: Kv4Cache, block_table, start, cu_tokens, total_tokens, dtype
         k, v = out
         _need(k, "out k", dtype, shape, cache.device)
         _need(v, "out v", dtype, shape, cache.device)
-    r = _KV4_RANGE.pack(B, W, total_tokens, total_tokens if max_tokens is None else max_tokens,
-                        block_table.data_ptr(), start.data_ptr(), cu_tokens.data_ptr())
+    try:
+        r = _KV4_RANGE.pack(B, W, total_tokens, total_tokens if max_tokens is None else max_tokens,
+                            block_table.data_ptr(), start.data_ptr(), cu_tokens.data_ptr())
+    except struct.error as e:
+        raise ValueError(f"kv4_read: max_tokens {max_tokens}, {total_tokens} tokens: {e}") from None
     st = lib.kv4_read(cache._ref, r, k.data_ptr(), v.data_ptr(), dt, _kv4_stream(cache, stream))
     if st:
         _check(st, "kv4_read")
@@ -655,9 +662,12 @@ def kv4_attention_workspace(cache: Kv4Cache, batch: int, total_q: int, n_heads: 
     """A workspace for kv4_attention calls of these sizes (or any that need no
     more) that do not overlap in time."""
     import torch
-    a = vbq_kv4_attn(batch=batch, table_width=1, total_q=total_q, max_q=max_q, max_kv=max_kv, n_heads=n_heads,
-                     dtype=0, causal=1, window=window, sinks=sinks, scale=1.0)
-    n = lib.kv4_attention_workspace(cache._ref, C.byref(a))
+    try:
+        a = _KV4_ATTN.pack(batch, 1, total_q, max_q, max_kv, n_heads, 0, 1, window, sinks, 1.0, 0, 0, 0, 0, 0, 0, 0, 0,
+                           0, 0, 0)
+        n = lib.kv4_attention_workspace(cache._ref, a)
+    except struct.error:
+        n = -1
     if n < 0:
         raise ValueError(f"kv4_attention: sizes refused (batch {batch}, {total_q} queries, {n_heads} heads over "
                          f"{cache.n_kv_heads}, max_q {max_q}, max_kv {max_kv}, window {window}, sinks {sinks})")
@@ -702,10 +712,13 @@ def kv4_attention(cache: Kv4Cache, q, block_table, kv_lens, cu_q, max_q: int, ma
     elif workspace.dtype is not cache.data.dtype or workspace.get_device() != cache.index or \
             not workspace.is_contiguous():
         raise ValueError("workspace: expected a contiguous uint8 tensor on the cache's device")
-    a = _KV4_ATTN.pack(B, W, T, max_q, max_kv, H, dt, 1 if causal else 0, window, sinks,
-                       D ** -0.5 if scale is None else scale, 0, block_table.data_ptr(), kv_lens.data_ptr(),
-                       cu_q.data_ptr(), q.data_ptr(), ts, hs, out.data_ptr(), 0 if lse is None else lse.data_ptr(),
-                       workspace.data_ptr(), workspace.numel())
+    try:
+        a = _KV4_ATTN.pack(B, W, T, max_q, max_kv, H, dt, 1 if causal else 0, window, sinks,
+                           D ** -0.5 if scale is None else scale, 0, block_table.data_ptr(), kv_lens.data_ptr(),
+                           cu_q.data_ptr(), q.data_ptr(), ts, hs, out.data_ptr(), 0 if lse is None else lse.data_ptr(),
+                           workspace.data_ptr(), workspace.numel())
+    except struct.error as e:
+        raise ValueError(f"kv4_attention: max_q {max_q}, max_kv {max_kv}, window {window}, sinks {sinks}: {e}") from None
     st = lib.kv4_attention(cache._ref, a, _kv4_stream(cache, stream))
     if st:
         _check(st, "kv4_attention")

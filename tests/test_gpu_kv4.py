@@ -1000,3 +1000,29 @@ def test_check_waits_for_calls_on_other_streams(vbq):
     with pytest.raises(vbq.VbqError, match="block-table"):
         cache.check()
     assert cache.check() is False
+
+
+@pytest.mark.parametrize("big", [2 ** 31, 2 ** 32 + 1, 2 ** 40, -2 ** 31 - 1])
+def test_the_binding_refuses_numbers_beyond_an_int(vbq, big):
+    """As a ValueError, whichever argument it is; a workspace is not sized for what is left of such a number."""
+    import torch
+    i32 = dict(dtype=torch.int32, device="cuda")
+    cache = vbq.Kv4Cache(2, 32, 2, 64)
+    table, lens, cu = torch.zeros(1, 2, **i32), torch.tensor([3], **i32), torch.tensor([0, 1], **i32)
+    q = torch.zeros(1, 4, 64, device="cuda").half()
+    k = torch.zeros(1, 2, 64, device="cuda").half()
+    ws = vbq.kv4_attention_workspace(cache, 1, 1, 4, 1, 4096)
+    for kw in (dict(max_q=big), dict(max_kv=big), dict(window=big), dict(sinks=big, window=4)):
+        args = dict(dict(max_q=1, max_kv=3), **kw)
+        with pytest.raises(ValueError, match="kv4_attention"):
+            vbq.kv4_attention(cache, q, table, lens, cu, workspace=ws, **args)
+        with pytest.raises(ValueError, match="kv4_attention"):
+            vbq.kv4_attention(cache, q, table, lens, cu, **args)
+    for sizes in ((big, 1, 4, 1, 9), (1, big, 4, 1, 9), (1, 1, 2 * big, 1, 9), (1, 1, 4, big, 9), (1, 1, 4, 1, big)):
+        with pytest.raises(ValueError, match="kv4_attention"):
+            vbq.kv4_attention_workspace(cache, *sizes)
+    with pytest.raises(ValueError, match="kv4_append"):
+        vbq.kv4_append(cache, k, k, table, lens, cu, max_tokens=big)
+    with pytest.raises(ValueError, match="kv4_read"):
+        vbq.kv4_read(cache, table, lens, cu, 1, torch.float16, max_tokens=big)
+    assert cache.check() is False

@@ -127,3 +127,12 @@ def test_attention_refuses_a_scale_that_binary32_does_not_hold_in_base_two():
         assert (vbq.lib.kv4_attention_workspace(C.byref(c), C.byref(a)) >= 0) is ok, scale
         if not ok:
             assert vbq.lib.kv4_attention(C.byref(c), C.byref(a), None) == 1
+
+
+@pytest.mark.parametrize("sizes", [(4, 2 ** 32 + 32, 1, 64), (4, 32, 2 ** 32 + 1, 64), (4, 32, 1, 2 ** 32 + 64),
+                                   (4, 32 - 2 ** 32, 1, 64), (2 ** 32 + 4, 32, 1, 64), (0, 32, 1, 64), (4, 33, 1, 64)])
+def test_a_cache_refuses_sizes_beyond_an_int(sizes):
+    """They would be cut to 32 bits on their way into the library."""
+    import packed_decode_gemv_amd as vbq
+    with pytest.raises(ValueError, match="pages take"):
+        vbq.Kv4Cache(*sizes, device="cpu")      # (nothing is allocated)
