@@ -125,7 +125,7 @@ vbq_status check_attn(const vbq_kv4* cache, const vbq_kv4_attn* a, bool pointers
   if (!(a->scale > 0.f && a->scale * kLog2e <= FLT_MAX)) return VBQ_ERR_INVALID_ARG;
   if (a->batch > 65535 || a->n_heads > 65536) return VBQ_ERR_UNSUPPORTED;
   const int ratio = a->n_heads / cache->n_kv_heads;
-  if ((int64_t)a->max_q * ratio > INT32_MAX - 64) return VBQ_ERR_UNSUPPORTED;
+  if ((int64_t)a->max_q * ratio > INT32_MAX - 128) return VBQ_ERR_UNSUPPORTED;   // (a tile beyond the last row is counted)
   if (a->max_kv > INT32_MAX - 64) return VBQ_ERR_UNSUPPORTED;
   *p = kv4_attn_plan(a->batch, cache->n_kv_heads, ratio, c->groups, a->max_q, a->max_kv, a->window, a->sinks);
   *bytes = p->places ? VBQ_KV4_COUNTERS * 4 + p->places * p->rows * (cache->head_dim + 2) * 4 : 0;

@@ -136,3 +136,11 @@ def test_a_cache_refuses_sizes_beyond_an_int(sizes):
     import packed_decode_gemv_amd as vbq
     with pytest.raises(ValueError, match="pages take"):
         vbq.Kv4Cache(*sizes, device="cpu")      # (nothing is allocated)
+
+
+def test_rows_that_an_int_does_not_hold_with_a_tile_more_are_refused():
+    import packed_decode_gemv_amd as vbq
+    c = _cache(vbq, n_kv_heads=1)
+    for rows, ok in ((2 ** 31 - 1 - 128, True), (2 ** 31 - 1 - 127, False), (2 ** 31 - 1 - 64, False)):
+        a = _attn(vbq, batch=1, n_heads=1, max_q=rows, total_q=9)
+        assert (vbq.lib.kv4_attention_workspace(C.byref(c), C.byref(a)) >= 0) is ok
