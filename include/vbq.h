@@ -360,7 +360,8 @@ typedef struct vbq_kv4_range {
   int32_t batch;          /* 1 .. 65535 */
   int32_t table_width;    /* entries per row of the block table, >= 1 */
   int32_t total_tokens;   /* rows of the tensors, >= 0 */
-  int32_t max_tokens;     /* no sequence has more rows than this; >= 0 */
+  int32_t max_tokens;     /* no sequence has more rows than this; >= 0. With m the lesser of this and
+                             total_tokens, (m + 62) / 32 * n_kv_heads is below 2^24 (a read: 2^26) */
   const int32_t* table;   /* device, [batch][table_width] */
   const int32_t* start;   /* device, [batch], first position */
   const int32_t* cu;      /* device, [batch + 1], cumulative row counts from 0 */
@@ -416,7 +417,8 @@ typedef struct vbq_kv4_attn {
   int32_t batch;          /* 1 .. 65535 */
   int32_t table_width;
   int32_t total_q;        /* rows of q, >= 0 */
-  int32_t max_q;          /* no sequence has more queries than this */
+  int32_t max_q;          /* no sequence has more queries than this. batch * n_kv_heads, times the tiles of 128
+                             that the rows of a head take (see above), is below 2^24 (2^23 with 9 .. 32 rows) */
   int32_t max_kv;         /* no sequence holds more tokens than this */
   int32_t n_heads;        /* a multiple of the cache's n_kv_heads */
   int32_t dtype;          /* VBQ_F16 or VBQ_BF16: q and out */

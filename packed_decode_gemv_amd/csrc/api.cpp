@@ -127,7 +127,9 @@ vbq_status check_attn(const vbq_kv4* cache, const vbq_kv4_attn* a, bool pointers
   const int ratio = a->n_heads / cache->n_kv_heads;
   if ((int64_t)a->max_q * ratio > INT32_MAX - 128) return VBQ_ERR_UNSUPPORTED;   // (a tile beyond the last row is counted)
   if (a->max_kv > INT32_MAX - 64) return VBQ_ERR_UNSUPPORTED;
-  *p = kv4_attn_plan(a->batch, cache->n_kv_heads, ratio, c->groups, a->max_q, a->max_kv, a->window, a->sinks);
+  *p = kv4_attn_plan(a->batch, cache->n_kv_heads, ratio, c->groups, a->total_q, a->max_q, a->max_kv, a->window,
+                     a->sinks);
+  if (!kv_grid_fits(p->grid, p->threads)) return VBQ_ERR_UNSUPPORTED;
   *bytes = p->places ? VBQ_KV4_COUNTERS * 4 + p->places * p->rows * (cache->head_dim + 2) * 4 : 0;
   return VBQ_OK;
 }
@@ -218,8 +220,7 @@ vbq_status kv4_attention(const vbq_kv4* cache, const vbq_kv4_attn* a, hipStream_
   k.batch = a->batch;
   k.parts = p.parts;
   k.scale_log2 = a->scale * kLog2e;
-  hipError_t e = launch_kv4_attention(k, p, a->batch, stream);
-  return e == hipErrorNotSupported ? VBQ_ERR_UNSUPPORTED : from_hip(e);
+  return from_hip(launch_kv4_attention(k, p, stream));
 }
 
 int vbq_abi_version(void) { return VBQ_ABI_VERSION; }

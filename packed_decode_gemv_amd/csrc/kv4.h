@@ -63,16 +63,21 @@ struct KvAttn {
   float scale_log2;            // scale * log2(e)
 };
 
+// A launch's first dimension holds 2^32 - 1 threads, and more are cut off without an error.
+constexpr bool kv_grid_fits(int64_t groups, int64_t threads) { return groups * threads <= (int64_t)UINT32_MAX; }
+
 hipError_t launch_kv4_append(const KvCache& c, const KvRange& r, const void* k, const void* v, int dtype,
                              int64_t k_ts, int64_t k_hs, int64_t v_ts, int64_t v_hs, hipStream_t s);
 hipError_t launch_kv4_read(const KvCache& c, const KvRange& r, void* k, void* v, int dtype, hipStream_t s);
 // Sizes of an attention launch, from the call's sizes alone: rows of a tile,
-// parts (as above), tiles, workgroups, and places for sums in the workspace.
+// parts (as above), tiles, workgroups and their threads, and places for sums in
+// the workspace.
 struct KvAttnPlan {
-  int32_t rows, parts;
+  int32_t rows, parts, threads;
   int64_t tiles, grid, places;
 };
-KvAttnPlan kv4_attn_plan(int batch, int heads, int ratio, int groups, int max_q, int max_kv, int window, int sinks);
-hipError_t launch_kv4_attention(const KvAttn& a, const KvAttnPlan& p, int batch, hipStream_t s);
+KvAttnPlan kv4_attn_plan(int batch, int heads, int ratio, int groups, int total_q, int max_q, int max_kv, int window,
+                         int sinks);
+hipError_t launch_kv4_attention(const KvAttn& a, const KvAttnPlan& p, hipStream_t s);
 
 }  // namespace vbq

@@ -343,12 +343,11 @@ __global__ __launch_bounds__(256) void k_kv4_read(KvCache c, KvRange r, void* k,
   }
 }
 
-// Blocks that a sequence of max_tokens tokens can touch, times the heads; 0 when
-// there is nothing to do, -1 for more than a grid takes.
+// Blocks that a sequence can touch, times the heads; 0 when there is nothing to
+// do. No sequence has more tokens than the call.
 int64_t block_tasks(const KvCache& c, const KvRange& r) {
   if (r.max_tokens == 0 || r.total == 0) return 0;
-  const int64_t n = ((int64_t)r.max_tokens + 62) / 32 * c.heads;
-  return n > INT32_MAX ? -1 : n;
+  return ((int64_t)(r.max_tokens < r.total ? r.max_tokens : r.total) + 62) / 32 * c.heads;
 }
 
 }  // namespace
@@ -367,9 +366,10 @@ int64_t block_tasks(const KvCache& c, const KvRange& r) {
 
 hipError_t launch_kv4_append(const KvCache& c, const KvRange& r, const void* k, const void* v, int dtype,
                              int64_t k_ts, int64_t k_hs, int64_t v_ts, int64_t v_hs, hipStream_t s) {
-  const int64_t tasks = block_tasks(c, r);
-  if (tasks <= 0) return tasks < 0 ? hipErrorNotSupported : hipSuccess;
-  const dim3 grid((uint32_t)tasks, (uint32_t)r.batch);   // a workgroup a block: an octet a wavefront
+  const int64_t tasks = block_tasks(c, r);   // a workgroup a block: an octet a wavefront
+  if (tasks == 0) return hipSuccess;
+  if (!kv_grid_fits(tasks, 256)) return hipErrorNotSupported;
+  const dim3 grid((uint32_t)tasks, (uint32_t)r.batch);
 #define VBQ_CALL(G, DT) k_kv4_append<G, DT><<<grid, 256, 0, s>>>(c, r, k, v, k_ts, k_hs, v_ts, v_hs)
   VBQ_KV4_BY_TYPE(VBQ_CALL)
 #undef VBQ_CALL
@@ -377,9 +377,10 @@ hipError_t launch_kv4_append(const KvCache& c, const KvRange& r, const void* k, 
 }
 
 hipError_t launch_kv4_read(const KvCache& c, const KvRange& r, void* k, void* v, int dtype, hipStream_t s) {
-  const int64_t tasks = block_tasks(c, r);
-  if (tasks <= 0) return tasks < 0 ? hipErrorNotSupported : hipSuccess;
-  const dim3 grid((uint32_t)((tasks + 3) / 4), (uint32_t)r.batch);   // a wavefront a block
+  const int64_t tasks = block_tasks(c, r), groups = (tasks + 3) / 4;   // a wavefront a block
+  if (tasks == 0) return hipSuccess;
+  if (!kv_grid_fits(groups, 256)) return hipErrorNotSupported;
+  const dim3 grid((uint32_t)groups, (uint32_t)r.batch);
 #define VBQ_CALL(G, DT) k_kv4_read<G, DT><<<grid, 256, 0, s>>>(c, r, k, v, tasks / c.heads)
   VBQ_KV4_BY_TYPE(VBQ_CALL)
 #undef VBQ_CALL

@@ -69,8 +69,9 @@ typedef float f32x2 __attribute__((ext_vector_type(2)));
 // that share one join do better than two workgroups of four (8 heads of 128 over
 // 60000 tokens, 12 rows: 32 against 42 us; over 90000, 32 rows: 64 against 82; 64
 // tiles of 20 rows of 80 blocks: 25 against 26).
+constexpr int few_row_waves(int groups, int rows) { return groups <= 2 && rows >= 16 ? 8 : 4; }
 template <int G, int ROWS>
-constexpr int kWaves = G <= 2 && ROWS >= 16 ? 8 : 4;
+constexpr int kWaves = few_row_waves(G, ROWS);
 constexpr float kNoMax = -3e38f;     // running maximum before any token
 // Probabilities are 2^(score * to_log2 - m) in one fma. m is a rounded product,
 // so beyond 2^22 the exact product may pass it by more than a quarter, and
@@ -1438,8 +1439,10 @@ __global__ __launch_bounds__(256) void k_kv4_attn_join(KvAttn a) {
 // the chip. Uncut and cut, heads of 128, 4 rows: 8 tiles of 19 blocks 9.4 and
 // 10.0 us, of 29 blocks 12.0 and 10.1; 256 tiles of 38 blocks 16.4 and 18.0,
 // of 63 blocks 21.8 and 22.2.
-KvAttnPlan kv4_attn_plan(int batch, int heads, int ratio, int groups, int max_q, int max_kv, int window, int sinks) {
+KvAttnPlan kv4_attn_plan(int batch, int heads, int ratio, int groups, int total_q, int max_q, int max_kv, int window,
+                         int sinks) {
   KvAttnPlan p;
+  p.threads = 256;
   const int64_t rows = (int64_t)max_q * ratio;
   int64_t blocks = ((int64_t)max_kv + kKvBlock - 1) / kKvBlock;
   if (window) {   // (a tile's rows: at most 128 queries)
@@ -1454,7 +1457,9 @@ KvAttnPlan kv4_attn_plan(int batch, int heads, int ratio, int groups, int max_q,
     const int64_t parts = fill < most ? fill : most;
     p.parts = (int32_t)(parts < 1 ? 1 : parts < kTileParts ? parts : kTileParts);
     p.places = p.parts > 1 ? p.tiles * p.parts : 0;
-    p.grid = p.tiles;
+    // (no sequence has more queries than the call: a workgroup beyond them would find no tile)
+    const int64_t most_rows = (int64_t)(max_q < total_q ? max_q : total_q) * ratio;
+    p.grid = (int64_t)batch * heads * ((most_rows + p.rows - 1) / p.rows);
     return p;
   }
   p.rows = rows <= 4 ? 4 : rows <= 8 ? 8 : rows <= 16 ? 16 : 32;
@@ -1470,11 +1475,11 @@ KvAttnPlan kv4_attn_plan(int batch, int heads, int ratio, int groups, int max_q,
   p.parts = cut ? fill - spare : 0;
   p.grid = cut ? p.parts + p.tiles : p.tiles;
   p.places = cut ? p.grid : 0;
+  p.threads = 64 * few_row_waves(groups, p.rows);
   return p;
 }
 
-hipError_t launch_kv4_attention(const KvAttn& a, const KvAttnPlan& p, int batch, hipStream_t s) {
-  if (p.grid > INT32_MAX) return hipErrorNotSupported;
+hipError_t launch_kv4_attention(const KvAttn& a, const KvAttnPlan& p, hipStream_t s) {
   const dim3 grid((uint32_t)p.grid);
 #define VBQ_CALL(G, ROWS, ST) k_kv4_attn<G, ROWS, ST><<<grid, (64 * kWaves<G, ROWS>), 0, s>>>(a)
 #define VBQ_CALL2(G, FEW, ST)                \

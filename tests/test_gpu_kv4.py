@@ -1026,3 +1026,34 @@ def test_the_binding_refuses_numbers_beyond_an_int(vbq, big):
     with pytest.raises(ValueError, match="kv4_read"):
         vbq.kv4_read(cache, table, lens, cu, 1, torch.float16, max_tokens=big)
     assert cache.check() is False
+
+
+# ---- maxima that say nothing -----------------------------------------------------------------
+@pytest.mark.parametrize("most", [2 ** 24, 2 ** 29 + 500, 2 ** 30, 2 ** 31 - 1])
+@pytest.mark.parametrize("heads", [1, 8])
+def test_a_maximum_far_beyond_the_lengths_changes_nothing(vbq, most, heads):
+    """max_tokens and max_q may be any number that no sequence passes."""
+    import torch
+    i32 = dict(dtype=torch.int32, device="cuda")
+    gen = torch.Generator(device="cuda").manual_seed(heads)
+    k, v = torch.randn(2, 700, heads, 64, generator=gen, device="cuda").half()
+    table, start = torch.arange(8, **i32).view(2, 4), torch.tensor([5, 100], **i32)
+    cu = torch.tensor([0, 300, 700], **i32)
+    a, b = (vbq.Kv4Cache(8, 128, heads, 64) for _ in range(2))
+    vbq.kv4_append(a, k, v, table, start, cu, max_tokens=400)
+    vbq.kv4_append(b, k, v, table, start, cu, max_tokens=most)
+    assert torch.equal(a.data, b.data) and a.data.any()
+    out = torch.full((2, 700, heads, 64), 9.0, device="cuda").half()
+    vbq.kv4_read(a, table, start, cu, 700, torch.float16, max_tokens=most, out=(out[0], out[1]))
+    for x, y in zip(out, vbq.kv4_read(a, table, start, cu, 700, torch.float16, max_tokens=400)):
+        assert torch.equal(x, y)
+    most = min(most, 2 ** 31 - 1 - 128)
+    q = torch.randn(700, heads, 64, generator=gen, device="cuda").half()
+    args = (a, q, table, start + torch.tensor([300, 400], **i32), cu)
+    ws = vbq.kv4_attention_workspace(a, 2, 700, heads, most, 128)      # too short to be cut, whatever max_q
+    want = vbq.kv4_attention(*args, 400, 512)
+    got = torch.full_like(want, float("nan"))
+    vbq.kv4_attention(*args, most, 512, out=got)
+    # the same kernel; with the smaller maximum it may have cut the tiles, which sums in another order
+    assert float((got.double() - want.double()).abs().max()) <= 2.0 ** -9 * float(want.abs().max())
+    assert ws.numel() == 0 and a.check() is False and b.check() is False

@@ -138,6 +138,22 @@ def test_a_cache_refuses_sizes_beyond_an_int(sizes):
         vbq.Kv4Cache(*sizes, device="cpu")      # (nothing is allocated)
 
 
+def test_more_workgroups_than_a_launch_takes_are_refused():
+    """A launch's first dimension holds 2^32 - 1 threads; what is beyond would be left undone."""
+    import packed_decode_gemv_amd as vbq
+    L, p = vbq.lib, C.c_void_p(BASE)
+    c = _cache(vbq, n_kv_heads=2)
+    r = _range(vbq, total_tokens=2 ** 30, max_tokens=2 ** 30)
+    assert L.kv4_append(C.byref(c), C.byref(r), p, p, 0, 256, 128, 256, 128, None) == 5
+    r = _range(vbq, total_tokens=2 ** 31 - 1, max_tokens=2 ** 31 - 1)
+    assert L.kv4_read(C.byref(c), C.byref(r), p, p, 0, None) == 5
+    many = _cache(vbq, n_kv_heads=512, head_dim=64)
+    for ratio in (1, 16):
+        a = _attn(vbq, batch=65535, total_q=65535, max_q=1, n_heads=512 * ratio)
+        assert L.kv4_attention(C.byref(many), C.byref(a), None) == 5
+        assert L.kv4_attention_workspace(C.byref(many), C.byref(a)) == -1
+
+
 def test_rows_that_an_int_does_not_hold_with_a_tile_more_are_refused():
     import packed_decode_gemv_amd as vbq
     c = _cache(vbq, n_kv_heads=1)
