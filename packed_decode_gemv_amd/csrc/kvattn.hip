@@ -85,11 +85,15 @@ __device__ inline float below(float score, float to_log2, float m) {
   return t - m;
 }
 constexpr int kParts = 512;          // workgroups that a launch aims at, at most
-// Blocks of a part, at least; more with 32 rows, whose parts take eight times
-// the bytes of 4 rows to join (64 tiles of 20 rows of 80 blocks: parts of at
-// least 24 blocks 25 us, of 32 27; with four wavefronts of 11 blocks 29, of 24 26).
-template <int ROWS>
-constexpr int kLeastPart = ROWS > 16 ? 24 : 8;
+// Blocks of a part, at least. With 32 rows a part's sums are eight times those of
+// 4 rows to join, and longer parts do no better even so (us with at least 8, 16,
+// 24 and 32 blocks; heads of 128 but for the last): 64 tiles of 20 rows over 32
+// blocks 19.5, 20.5, 20.5, 22.9; over 80 blocks 25.3, 25.3, 25.3, 27.8; over 125
+// blocks 29.4, 29.2, 29.6, 29.1; 32 tiles of 24 rows over 94 blocks 21.4, 22.4, 24.1,
+// 26.8; 16 tiles of 32 rows over 188 blocks 27.3, 25.8, 26.4, 28.0; 8 tiles over 625
+// blocks 34.9, 34.8, 34.9, 34.4; 6 tiles of heads of 192 over 282 blocks 37.0, 37.1,
+// 39.3, 43.5.
+constexpr int kLeastPart = 8;
 
 // Exchanges with the lanes 16 and 32 apart (the lane quarters of a column).
 typedef uint32_t pair_t __attribute__((ext_vector_type(2)));
@@ -370,7 +374,7 @@ __global__ __launch_bounds__((64 * kWaves<G, ROWS>), (kRoomy<G, ROWS>) ? 4 : G *
       }
     }
     const int chunk = max((int)(((uint32_t)total * (uint32_t)a.cache.heads + (uint32_t)a.parts - 1u) / (uint32_t)a.parts),
-                          kLeastPart<ROWS>);
+                          kLeastPart);
     int before = 0, incl, n, size;   // of each lane's sequence: parts up to its end, parts of a tile, blocks of a part
     uint64_t past;
     for (int base = 0;; base += 64) {
