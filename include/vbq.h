@@ -381,7 +381,8 @@ vbq_status kv4_append(const vbq_kv4* cache, const vbq_kv4_range* r, const void* 
 
 /* Reads tokens back: f32(s*q) + o rounded once to `dtype`. k, v: device,
  * [total_tokens][n_kv_heads][head_dim], contiguous, 16-byte aligned; either
- * may be NULL. Rows of tokens whose page is not in the cache are zeroed. */
+ * may be NULL. Rows of tokens whose page is not in the cache are zeroed; rows of
+ * a sequence that is left out, and of none, keep what they held. */
 vbq_status kv4_read(const vbq_kv4* cache, const vbq_kv4_range* r, void* k, void* v, int32_t dtype,
                     hipStream_t stream);
 
@@ -393,7 +394,8 @@ vbq_status kv4_read(const vbq_kv4* cache, const vbq_kv4_range* r, void* k, void*
  * i of n is at p = kv_lens[b] - n + i. It sees j < kv_lens[b] with
  *   causal:  j <= p
  *   window:  j > p - window or j < sinks     (window > 0, causal only)
- * A row that sees nothing gives zeros (and lse = -infinity). A NaN or infinity
+ * A row that sees nothing gives zeros (and lse = -infinity); rows of a sequence
+ * that is left out, and of none, keep what they held. A NaN or infinity
  * in q reaches the outputs of its own row only, and so does a number so large
  * that scale * log2(e) * |q| reaches 2^121. Scores have to be numbers that fp32
  * holds.

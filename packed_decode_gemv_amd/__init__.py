@@ -614,7 +614,8 @@ def kv4_append(cache: Kv4Cache, k, v, block_table, start, cu_tokens, max_tokens=
     token and head rows may be strided) into the cache: sequence b's rows
     cu_tokens[b] .. cu_tokens[b+1] become its tokens start[b], start[b] + 1, ...
     block_table int32 [B][W], start int32 [B], cu_tokens int32 [B+1], all on
-    the GPU. max_tokens: no sequence has more rows (default: all of them)."""
+    the GPU. max_tokens: no sequence has more rows (default: all of them; the
+    launch is sized for it, so a near bound saves time)."""
     B, W = _kv4_index(cache, block_table, start, cu_tokens)
     T, kts, khs = _kv4_rows(k, "k", cache.n_kv_heads, cache)
     Tv, vts, vhs = _kv4_rows(v, "v", cache.n_kv_heads, cache)
@@ -635,7 +636,8 @@ def kv4_read(cache: Kv4Cache, block_table, start, cu_tokens, total_tokens, dtype
              stream=None):
     """Reads tokens back as k, v [total_tokens][n_kv_heads][head_dim] of
     `dtype` (fp16, bf16 or fp32), rows as in kv4_append. out: (k, v) tensors
-    to fill."""
+    to fill. Rows of no sequence, and of one whose lengths do not fit (see
+    Kv4Cache.check), are not written."""
     B, W = _kv4_index(cache, block_table, start, cu_tokens)
     dt = _kv4_dtype(dtype, "dtype")
     shape = (total_tokens, cache.n_kv_heads, cache.head_dim)
@@ -688,8 +690,9 @@ def kv4_attention(cache: Kv4Cache, q, block_table, kv_lens, cu_q, max_q: int, ma
     `window` of them and the first `sinks` of the sequence. n_heads is a
     multiple of the cache's heads. max_q, max_kv: no sequence has more queries
     or tokens. scale: 1/sqrt(head_dim) by default. Returns out, of q's type;
-    lse: float32 [queries][n_heads] to fill, or None. workspace: from
-    kv4_attention_workspace, for calls that allocate nothing."""
+    lse: float32 [queries][n_heads] to fill, or None. Rows of no sequence, and of
+    one whose lengths do not fit (see Kv4Cache.check), are not written. workspace:
+    from kv4_attention_workspace, for calls that allocate nothing."""
     B, W = _kv4_index(cache, block_table, kv_lens, cu_q)
     H = q.shape[1] if getattr(q, "ndim", 0) == 3 else 0
     if H < 1 or H % cache.n_kv_heads:

@@ -13,8 +13,8 @@
 // keep the other tokens' nibbles (one wavefront owns an octet, so the read and
 // the write do not race).
 //   25800 bf16 tokens of 8 heads of 128 take 44 us, 135 MB at 3.1 TB/s. The
-// arithmetic bounds it (about 34 us of vector issue; a copy of as many bytes
-// takes 27): a correctly rounded quotient a value made it 56 us. Codes are
+// arithmetic bounds it (about 34 us of vector issue; a plain copy of as many bytes
+// takes 22): a correctly rounded quotient a value made it 56 us. Codes are
 // decided by t = (w - o) * rcp(s): rcp is within 2^-23 and the product within
 // 2^-24, so t is within 16 * 2^-22 = 2^-18 of the correctly rounded quotient
 // where a code hangs on it (t < 16), and only a t within 2^-16 of a tie takes
@@ -25,7 +25,7 @@
 // between lanes: a key word is eight channels of a token, the four value words
 // of a lane four channels of eight tokens. HBM writes bound it: 65000 bf16
 // tokens of 8 heads of 128 take 81 us, 334 MB at 4.1 TB/s, where a copy that
-// reads as much as it writes reaches 5.0.
+// reads as much as it writes reaches 6.2.
 #include "kv4.h"
 
 namespace vbq {

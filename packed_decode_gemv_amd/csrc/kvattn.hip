@@ -46,12 +46,12 @@
 // softmax and split are done once per score, not two (four) times.
 //
 // Bounds, heads of 128. 4 rows, 32 sequences of 167000 tokens in all, 8 heads:
-// 193 MB in 50 us (3.9 TB/s; a copy reaches 5.0). By clock stamps 4.5 us pass
+// 193 MB in 51 us (3.8 TB/s; a plain read reaches 6.4). By clock stamps 4.5 us pass
 // until the first block is there (arguments, lengths, table, block: each waits
 // for the one before) and 2 and 3 us in the joins in LDS and in the workspace;
-// with the launch that leaves about 38 us, 5.1 TB/s, for the blocks. One
+// with the launch that leaves about 39 us, 5.0 TB/s, for the blocks. One
 // sequence of 131072 tokens: 151 MB in 42 us, 64 parts a tile to join.
-// 16 heads of 16 sequences under a window of 1024: 38 MB in 14 us, the chain of
+// 16 heads of 16 sequences under a window of 1024: 38 MB in 15 us, the chain of
 // dependent look-ups. 20 rows, 8 sequences of 20000 tokens in all, 8 heads: 24 MB
 // in 25 us; three blocks a wavefront, of about 1.8 us each where one has a SIMD to
 // itself (vector instructions and their latency), 4.6 us before the first, 7 us
@@ -928,11 +928,11 @@ __global__ __launch_bounds__((64 * kWaves<G, ROWS>), (kRoomy<G, ROWS>) ? 4 : G *
 // Q^T, O^T = V^T P^T. One turn of the loop spreads the keys of block i + 2 and
 // the values of block i + 1, forms the scores of block i + 1 and the
 // probabilities and output of block i, in one straight piece of code, so that
-// matrix and vector instructions overlap. Key
-// operands are the exact codes (normal fp16 numbers: a word is spread once for
-// 128 rows, and the matrix unit keeps all of their products, as explained above;
-// 2048 queries over 10240 tokens take 438 us so, 433 with subnormal c 2^-20),
-// scores take scale in fp32 as above and offsets by one more MFMA: A holds a token's offsets o_g, B the rows'
+// matrix and vector instructions overlap. Key operands are the exact codes as
+// normal fp16 numbers, of whose products the matrix unit loses nothing that fp32
+// holds (see above): a word is spread once for 128 rows, and 2048 queries over
+// 10240 tokens take 1% longer so than with c 2^-20. Scores take scale in fp32 as
+// above and offsets by one more MFMA: A holds a token's offsets o_g, B the rows'
 // sums of q over group g. Rounding keys to fp16 instead would save the scaling,
 // but a score's error is multiplied into its probability: it doubled the
 // output's error in fp16. Values are s c + o rounded once to fp16, as are
@@ -942,8 +942,8 @@ __global__ __launch_bounds__((64 * kWaves<G, ROWS>), (kRoomy<G, ROWS>) ? 4 : G *
 // 2.1e-4 are the rounding of the output itself; bf16 outputs are off by 1.7e-3
 // either way.
 //   Bounds. 2048 bf16 queries of 32 heads of 128 over 10240 tokens: 309 GFLOP in
-// 427 us, 0.72 PFLOP/s (a library product of 8192^3 reaches 1.37). A turn of
-// one wavefront is 17 MFMAs (544 cycles), about 150 vector instructions (850
+// 426 us, 0.73 PFLOP/s (a library product of 8192^3 reaches 1.24 to 1.37; some
+// cards run the same code in 480 us). A turn of one wavefront is 17 MFMAs (544 cycles), about 150 vector instructions (850
 // cycles) and 28 KB of LDS reads (220 cycles of the CU, times 8 wavefronts),
 // and two wavefronts a SIMD overlap them in part. With values spread a block
 // later than keys two buffers do for both, and heads of 192 fit twice on a CU (17 x
