@@ -165,6 +165,10 @@ constexpr int kCodeExp = 20;
 
 __device__ inline half2_t pair_of(uint32_t w) { return __builtin_bit_cast(half2_t, w); }
 
+// What brings a row's products, held times 2^-exp, to base two. Not 0, with which
+// a hidden token's minus infinity would be NaN: at 2^-126 scores are below 2^-90.
+__device__ inline float row_scale(const KvAttn& a, int exp) { return fmaxf(ldexpf(a.scale_log2, exp), 0x1p-126f); }
+
 // N fp16 numbers from LDS.
 template <int N>
 struct Halves {
@@ -494,7 +498,7 @@ __global__ __launch_bounds__((64 * kWaves<G, ROWS>), (kRoomy<G, ROWS>) ? 4 : G *
     int ex = (int)(__builtin_bit_cast(uint32_t, top) >> 23) - 127;
     ex = top > 0.f ? max(ex, -100) : 13;
     const float up = ldexpf(1.f, 13 - ex);
-    to_log2[nt] = ldexpf(a.scale_log2, ex - 13 + kCodeExp);
+    to_log2[nt] = row_scale(a, ex - 13 + kCodeExp);
 #pragma unroll
     for (int g = 0; g < G; ++g) {
       float sum = 0.f;
@@ -935,7 +939,9 @@ __global__ __launch_bounds__((64 * kWaves<G, ROWS>), (kRoomy<G, ROWS>) ? 4 : G *
 // above and offsets by one more MFMA: A holds a token's offsets o_g, B the rows'
 // sums of q over group g. Rounding keys to fp16 instead would save the scaling,
 // but a score's error is multiplied into its probability: it doubled the
-// output's error in fp16. Values are s c + o rounded once to fp16, as are
+// output's error in fp16. Values are s c + o rounded once to fp16 (as codes they
+// would need p s of every group and what its rounding leaves, 2 G conversions a
+// probability instead of one, where vector instructions bound the kernel), as are
 // probabilities; for fp16 outputs (FINE) what is left of a probability is
 // multiplied too: without it the outputs of 2500 rows under a window of 500
 // were off by 3.2e-4 (relative, whole tensor), with it by 2.8e-4, of which
@@ -1145,7 +1151,7 @@ __global__ __launch_bounds__(256, G >= 4 ? 1 : 2) void k_kv4_attn_tile(KvAttn a)
     int ex = (int)(__builtin_bit_cast(uint32_t, top) >> 23) - 127;
     ex = top > 0.f ? max(ex, -100) : 13;
     const float up = ldexpf(1.f, 13 - ex);
-    to_log2 = ldexpf(a.scale_log2, ex - 13 + kTileCodeExp);
+    to_log2 = row_scale(a, ex - 13 + kTileCodeExp);
 #pragma unroll
     for (int j = 0; j < 8; ++j) qsum[j] = (_Float16)0.f;
 #pragma unroll

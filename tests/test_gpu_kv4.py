@@ -1057,3 +1057,31 @@ def test_a_maximum_far_beyond_the_lengths_changes_nothing(vbq, most, heads):
     # the same kernel; with the smaller maximum it may have cut the tiles, which sums in another order
     assert float((got.double() - want.double()).abs().max()) <= 2.0 ** -9 * float(want.abs().max())
     assert ws.numel() == 0 and a.check() is False and b.check() is False
+
+
+@pytest.mark.parametrize("dtype,size", [("float16", 2.0 ** -12), ("bfloat16", 2.0 ** -12), ("bfloat16", 2.0 ** -120)])
+@pytest.mark.parametrize("scale", [1e-45, 1e-41, 1e-30, 1e-3])
+@pytest.mark.parametrize("dim,ratio,new", [(64, 4, 1), (128, 4, 3), (64, 4, 30), (256, 2, 40)])
+def test_attention_of_vanishing_scores(vbq, dtype, size, scale, dim, ratio, new):
+    """However small scale and queries are, tokens that are seen weigh the same and hidden ones nothing: scores are below
+    2^-8 in magnitude, so probabilities are off by 2^-7 of themselves at most, and the rest is as in check()."""
+    import torch
+    gen = torch.Generator(device="cuda").manual_seed(dim + new)
+    i32 = dict(dtype=torch.int32, device="cuda")
+    L = 70
+    k, v = torch.randn(2, L, 1, dim, generator=gen, device="cuda")
+    q = ((torch.rand(new, ratio, dim, generator=gen, device="cuda") - 0.5) * 2 * size).to(getattr(torch, dtype))
+    cache = vbq.Kv4Cache(4, 32, 1, dim)
+    table, cu = torch.arange(4, **i32).view(1, 4), torch.tensor([0, L], **i32)
+    vbq.kv4_append(cache, k, v, table, torch.zeros(1, **i32), cu)
+    rv = vbq.kv4_read(cache, table, torch.zeros(1, **i32), cu, L, torch.float32)[1].double()[:, 0]
+    lse = torch.empty(new, ratio, device="cuda")
+    got = vbq.kv4_attention(cache, q, table, torch.tensor([L], **i32), torch.tensor([0, new], **i32), new, L,
+                            scale=scale, window=40, sinks=2, lse=lse)
+    for i in range(new):
+        p = L - new + i
+        see = [j for j in range(p + 1) if j > p - 40 or j < 2]
+        want, mass = rv[see].mean(0), rv[see].abs().mean(0)
+        bound = (2.0 ** -7 + 2.1 * 2.0 ** -11) * mass + 2.0 ** -8 * want.abs() + 2.0 ** -24
+        assert ((got[i].double() - want).abs() <= bound).all()
+        assert ((lse[i].double() - math.log(len(see))).abs() <= 2.0 ** -7).all()
