@@ -949,9 +949,10 @@ __global__ __launch_bounds__((64 * kWaves<G, ROWS>), (kRoomy<G, ROWS>) ? 4 : G *
 // either way.
 //   Bounds. 2048 bf16 queries of 32 heads of 128 over 10240 tokens: 309 GFLOP in
 // 426 us, 0.73 PFLOP/s (a library product of 8192^3 reaches 1.24 to 1.37; some
-// cards run the same code in 480 us). A turn of one wavefront is 17 MFMAs (544 cycles), about 150 vector instructions (850
-// cycles) and 28 KB of LDS reads (220 cycles of the CU, times 8 wavefronts),
-// and two wavefronts a SIMD overlap them in part. With values spread a block
+// cards run the same code in 480 us). A turn of one wavefront is 17 MFMAs (544
+// cycles), about 150 vector instructions (850 cycles) and 28 KB of LDS reads (220
+// cycles of the CU, times 8 wavefronts), and two wavefronts a SIMD overlap them
+// in part. With values spread a block
 // later than keys two buffers do for both, and heads of 192 fit twice on a CU (17 x
 // 1193 queries, 16 heads: 462 -> 317 us). Heads of 256 have registers for one
 // wavefront a SIMD: 3 sequences under a window of 500, 36 GFLOP in 150 us;
