@@ -339,6 +339,7 @@ vbq_status cell_drift_bound(const vbq_matrix* m, const uint16_t* x, int32_t B, f
 #define VBQ_KV4_FLAG_PAGE 1u      /* a block-table entry outside the cache */
 #define VBQ_KV4_FLAG_LENGTH 2u    /* lengths or starts that are negative, beyond the table or the stated maxima */
 #define VBQ_KV4_FLAG_NAN 4u       /* kv4_append stored a NaN as 0 */
+#define VBQ_KV4_FLAG_FULL 8u      /* kv4_fork found fewer free pages than it needed */
 
 typedef enum vbq_dtype { VBQ_F16 = 0, VBQ_BF16 = 1, VBQ_F32 = 2 } vbq_dtype;
 
@@ -449,6 +450,128 @@ typedef struct vbq_kv4_attn {
  * not looked at), or -1 if the sizes are refused. Host only. */
 int64_t kv4_attention_workspace(const vbq_kv4* cache, const vbq_kv4_attn* a);
 vbq_status kv4_attention(const vbq_kv4* cache, const vbq_kv4_attn* a, hipStream_t stream);
+
+/* ---- several continuations of one prompt ---------------------------------------------
+ *
+ * Parallel sampling, beam search and the scoring of candidates decode sequences
+ * that begin alike. kv4_fork makes sequences of a cache go on from others,
+ * kv4_attention_shared reads what a group of them has in common once for all,
+ * head_norm_rotary makes the queries and keys that enter, and token_logprobs says how
+ * likely the next tokens are.
+ *
+ * Queries and keys: norms for each head, and the rotation by position, in one pass.
+ * With x a head's D channels of one token and R = rotary_dim <= D:
+ *   n = x * w / sqrt(mean(x^2) + eps)          (n = x where the tensor has no weight)
+ *   pair i < R/2 is channels (i, i + R/2), or (2i, 2i + 1) where `interleaved`;
+ *   a' = a cos(phi_i) - b sin(phi_i), b' = b cos(phi_i) + a sin(phi_i) for a pair (a, b),
+ *   phi_i = positions[axis[i]][token] * inv_freq[i] radians; channels from R on stay n.
+ * Sums and products are fp32, angles binary64; one rounding to the output's type. The
+ * sum of x^2 has to be a number that fp32 holds. Several axes (time, height and width of
+ * an image's patches) are pairs that go by different rows of the positions. */
+typedef struct vbq_head_rotary {
+  int32_t head_dim;       /* D: 64, 128, 192 or 256 */
+  int32_t rotary_dim;     /* R: a multiple of 16, 0 .. D */
+  int32_t axes;           /* rows of the positions, 1 .. 255 */
+  int32_t interleaved;    /* 0 or 1 */
+  float eps;              /* >= 0, finite */
+  int32_t reserved;       /* 0 */
+  const float* inv_freq;  /* device, [R/2] */
+  const uint8_t* axis;    /* device, [R/2], each below `axes` (larger ones count as the last), or NULL: row 0 for all */
+  const float* q_weight;  /* device, [D], 16-byte aligned, or NULL: queries are not normed */
+  const float* k_weight;  /* the same for keys */
+} vbq_head_rotary;
+
+/* Rows [token][head][channel] of a vbq_dtype; strides in elements. Channels are
+ * contiguous; base pointers and strides are multiples of 16 bytes. An output may be its
+ * own input (same pointer, type and strides) and overlaps nothing else. */
+typedef struct vbq_head_rows {
+  const void* in;
+  void* out;
+  int64_t in_token_stride, in_head_stride, out_token_stride, out_head_stride;
+  int32_t heads;          /* 0 .. 65536; 0: no such tensor, nothing else is looked at */
+  int32_t in_dtype;       /* the same for queries and keys */
+  int32_t out_dtype;
+  int32_t reserved;       /* 0 */
+} vbq_head_rows;
+
+/* positions: device, int32, row a of axis a is at positions + a * position_stride
+ * (NULL if R is 0); any number, negative ones too. */
+vbq_status head_norm_rotary(const vbq_head_rotary* plan, const vbq_head_rows* q, const vbq_head_rows* k,
+                            const int32_t* positions, int64_t position_stride, int32_t n_tokens, hipStream_t stream);
+
+/* Sequences become continuations of others. refs[page] counts the entries of block
+ * tables that name a page, 0 for a free one (counts of entries in other tables, or of
+ * anything else that holds a page, stay in it). Entries of a row that name no page are
+ * -1. With P = page_tokens, new sequence b goes on from old sequence p = parents[b]
+ * (-1: from none, it is empty), L = lens_in[p]:
+ *   lens_out[b] = L;
+ *   entries j < L / P (whole pages): those of p, shared;
+ *   entries from there on, j < ceil((L + reserve[b]) / P): the first b with this parent
+ *     keeps those of p that name a page with refs_in 1; every other entry is a free page,
+ *     and the L % P tokens of a part page are copied into it (whole blocks of 32);
+ *   the other entries: -1.
+ * refs_out: refs_in less the entries of table_in, plus those of table_out. So an old
+ * sequence that nothing goes on from is dropped, and its pages are free. The i-th page
+ * taken, in the order of b, then j, is the i-th lowest with refs_in 0; pages that this
+ * call frees are not taken by it. Outputs overlap no input. Entries outside 0 ..
+ * n_pages-1 are left out (not -1: FLAG_PAGE; also -1 below ceil(L / P)); a parent outside
+ * -1 .. batch_in-1 or with a length that does not fit counts as none, entries beyond the
+ * table and negative reserves as 0 (FLAG_LENGTH); where free pages run out, entries are
+ * -1 and nothing is copied (FLAG_FULL).
+ * kv4_fork_workspace: bytes for calls of these sizes (or less), -1 if they are refused.
+ * Calls that overlap in time need workspaces of their own; nothing in it has to be set. */
+typedef struct vbq_kv4_fork {
+  int32_t batch_in, batch_out;  /* 1 .. 65535 */
+  int32_t table_width;          /* 1 .. 2^20 */
+  int32_t reserved;             /* 0 */
+  const int32_t* table_in;      /* device, [batch_in][table_width] */
+  const int32_t* lens_in;       /* device, [batch_in] */
+  const int32_t* refs_in;       /* device, [n_pages], 16-byte aligned */
+  const int32_t* parents;       /* device, [batch_out] */
+  const int32_t* reserve;       /* device, [batch_out] tokens, or NULL: 0 */
+  int32_t* table_out;           /* device, [batch_out][table_width] */
+  int32_t* lens_out;            /* device, [batch_out] */
+  int32_t* refs_out;            /* device, [n_pages], 16-byte aligned */
+  void* workspace;              /* device, 16-byte aligned */
+  int64_t workspace_bytes;
+} vbq_kv4_fork;
+int64_t kv4_fork_workspace(const vbq_kv4* cache, int32_t batch_in, int32_t batch_out, int32_t table_width);
+vbq_status kv4_fork(const vbq_kv4* cache, const vbq_kv4_fork* f, hipStream_t stream);
+
+/* Log probabilities of rows of logits x[0 .. vocab-1] (those of an LM head, say), in one
+ * pass over them; sums are fp32:
+ *   lse = log sum_i exp(x_i); logprob_i = x_i - lse; entropy = -sum_i exp(logprob_i) logprob_i
+ * Tokens stand in the order of their logits, largest first, equal ones by their number:
+ * rank is the given token's place in it, from 0, and the `top` first are listed. Logits may
+ * be -infinity (masked). A row of nothing else has lse and log probabilities -infinity and
+ * entropy 0. A row that holds a NaN or +infinity gives NaN, and -1 for rank and numbers. A
+ * given token outside 0 .. vocab-1 gives NaN and -1.
+ * Results repeat bit for bit for the same sizes and alignment of the rows. */
+#define VBQ_LOGPROBS_MAX_TOP 32
+#define VBQ_LOGPROBS_COUNTERS 512
+typedef struct vbq_logprobs {
+  int32_t rows;           /* >= 0; times the workgroups of a row (up to 32), below 2^24 */
+  int32_t vocab;          /* 1 .. 2^30 */
+  int32_t dtype;          /* a vbq_dtype */
+  int32_t top;            /* 0 .. VBQ_LOGPROBS_MAX_TOP, at most vocab */
+  int64_t row_stride;     /* in elements */
+  const void* logits;     /* device, aligned to its type */
+  const void* tokens;     /* device, [rows], int32 or int64, or NULL: none */
+  int32_t token_bytes;    /* 4 or 8 */
+  int32_t reserved;       /* 0 */
+  float* logprob;         /* device, [rows] (with tokens) */
+  int32_t* rank;          /* device, [rows] (with tokens) */
+  float* entropy;         /* device, [rows], or NULL */
+  float* lse;             /* device, [rows], or NULL */
+  float* top_logprob;     /* device, [rows][top] (with top > 0) */
+  int32_t* top_index;     /* device, [rows][top] (with top > 0) */
+  void* workspace;        /* device, 16-byte aligned (NULL if 0 bytes). Its first 4 * VBQ_LOGPROBS_COUNTERS
+                             bytes are zero before the first call that uses it; every call leaves them zero. Calls that overlap in time
+                             need workspaces of their own. */
+  int64_t workspace_bytes;
+} vbq_logprobs;
+int64_t token_logprobs_workspace(int32_t rows, int32_t vocab, int32_t top);
+vbq_status token_logprobs(const vbq_logprobs* a, hipStream_t stream);
 
 #ifdef __cplusplus
 }

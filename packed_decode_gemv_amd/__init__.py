@@ -14,12 +14,15 @@ Function names follow the C ABI: ``vbq_pack``, ``vbq_gemv``,
 ``vbq_gemv_cell8``, ``vbq_gemm``, ``cell_requant_verify``, ``cell_drift_bound``,
 ``cell8_encode``, ``cell8_decode``, ``vbq_residual_error``, and for the 4-bit
 key/value cache (``Kv4Cache``) ``kv4_append``, ``kv4_read``, ``kv4_attention``.
+For several continuations of one prompt: ``kv4_fork``, ``kv4_attention_shared``,
+``head_norm_rotary`` (with a ``HeadRotary``) and ``token_logprobs``.
 """
 from __future__ import annotations
 
 import ctypes as C
 import os
 import struct
+import typing
 
 import numpy as np
 
@@ -55,7 +58,8 @@ class vbq_layout_sizes(C.Structure):
 EXPORTS = ("vbq_abi_version", "vbq_status_string", "vbq_pack_query", "vbq_pack", "vbq_matrix_check",
            "vbq_gemv", "vbq_gemv_batched", "vbq_gemv_batched_static", "vbq_gemv_levels", "vbq_gemm",
            "cell_requant_verify", "cell_drift_bound", "vbq_residual_error", "vbq_gemv_cell8", "cell8_encode",
-           "cell8_decode", "kv4_page_bytes", "kv4_append", "kv4_read", "kv4_attention_workspace", "kv4_attention")
+           "cell8_decode", "kv4_page_bytes", "kv4_append", "kv4_read", "kv4_attention_workspace", "kv4_attention",
+           "head_norm_rotary", "kv4_fork_workspace", "kv4_fork", "token_logprobs_workspace", "token_logprobs")
 
 
 class vbq_kv4(C.Structure):
@@ -75,6 +79,31 @@ class vbq_kv4_attn(C.Structure):
                [(n, C.c_void_p) for n in ("table", "kv_lens", "cu_q", "q")] + \
                [("q_token_stride", C.c_int64), ("q_head_stride", C.c_int64)] + \
                [(n, C.c_void_p) for n in ("out", "lse", "workspace")] + [("workspace_bytes", C.c_int64)]
+
+
+class vbq_head_rotary(C.Structure):
+    _fields_ = [(n, C.c_int32) for n in ("head_dim", "rotary_dim", "axes", "interleaved")] + \
+               [("eps", C.c_float), ("reserved", C.c_int32)] + \
+               [(n, C.c_void_p) for n in ("inv_freq", "axis", "q_weight", "k_weight")]
+
+
+class vbq_head_rows(C.Structure):
+    _fields_ = [("in_", C.c_void_p), ("out", C.c_void_p)] + \
+               [(n, C.c_int64) for n in ("in_token_stride", "in_head_stride", "out_token_stride", "out_head_stride")] + \
+               [(n, C.c_int32) for n in ("heads", "in_dtype", "out_dtype", "reserved")]
+
+
+class vbq_kv4_fork(C.Structure):
+    _fields_ = [(n, C.c_int32) for n in ("batch_in", "batch_out", "table_width", "reserved")] + \
+               [(n, C.c_void_p) for n in ("table_in", "lens_in", "refs_in", "parents", "reserve", "table_out",
+                                          "lens_out", "refs_out", "workspace")] + [("workspace_bytes", C.c_int64)]
+
+
+class vbq_logprobs(C.Structure):
+    _fields_ = [(n, C.c_int32) for n in ("rows", "vocab", "dtype", "top")] + [("row_stride", C.c_int64)] + \
+               [("logits", C.c_void_p), ("tokens", C.c_void_p), ("token_bytes", C.c_int32), ("reserved", C.c_int32)] + \
+               [(n, C.c_void_p) for n in ("logprob", "rank", "entropy", "lse", "top_logprob", "top_index",
+                                          "workspace")] + [("workspace_bytes", C.c_int64)]
 
 
 def _load():
@@ -127,6 +156,16 @@ def _load():
     lib.kv4_attention_workspace.argtypes = [C.POINTER(vbq_kv4), P]
     lib.kv4_attention.restype = C.c_int
     lib.kv4_attention.argtypes = [C.POINTER(vbq_kv4), P, P]
+    lib.head_norm_rotary.restype = C.c_int
+    lib.head_norm_rotary.argtypes = [C.POINTER(vbq_head_rotary), P, P, P, I64, I32, P]
+    lib.kv4_fork_workspace.restype = I64
+    lib.kv4_fork_workspace.argtypes = [C.POINTER(vbq_kv4), I32, I32, I32]
+    lib.kv4_fork.restype = C.c_int
+    lib.kv4_fork.argtypes = [C.POINTER(vbq_kv4), P, P]
+    lib.token_logprobs_workspace.restype = I64
+    lib.token_logprobs_workspace.argtypes = [I32, I32, I32]
+    lib.token_logprobs.restype = C.c_int
+    lib.token_logprobs.argtypes = [P, P]
     return lib
 
 
@@ -480,7 +519,7 @@ def vbq_gemv_levels(pms, x, out=None, stream=None):
 
 
 # ---- 4-bit key/value cache ---------------------------------------------------------
-KV4_FLAG_PAGE, KV4_FLAG_LENGTH, KV4_FLAG_NAN = 1, 2, 4
+KV4_FLAG_PAGE, KV4_FLAG_LENGTH, KV4_FLAG_NAN, KV4_FLAG_FULL = 1, 2, 4, 8
 KV4_COUNTERS = 2048
 
 
@@ -577,7 +616,7 @@ class Kv4Cache:
 
     def check(self):
         """Waits for the device, all streams of it, and raises VbqError if a call
-        so far met a page outside the cache or lengths that do not fit; returns
+        so far met a page outside the cache, lengths that do not fit or too few free pages; returns
         True if a NaN was stored as 0, else False. The flags are cleared."""
         import torch
         torch.cuda.synchronize(self.device)
@@ -585,10 +624,11 @@ class Kv4Cache:
         if f:
             self.flags.zero_()
             torch.cuda.current_stream(self.device).synchronize()   # or a later call's flag could be cleared with them
-        if f & (KV4_FLAG_PAGE | KV4_FLAG_LENGTH):
+        if f & (KV4_FLAG_PAGE | KV4_FLAG_LENGTH | KV4_FLAG_FULL):
             raise VbqError(6, "Kv4Cache: " + " and ".join(
                 n for b, n in ((KV4_FLAG_PAGE, "a block-table entry outside the cache"),
-                               (KV4_FLAG_LENGTH, "lengths outside the table or the stated maxima")) if f & b))
+                               (KV4_FLAG_LENGTH, "lengths outside the table or the stated maxima"),
+                               (KV4_FLAG_FULL, "fewer free pages than a fork needed")) if f & b))
         return bool(f & KV4_FLAG_NAN)
 
 
@@ -725,4 +765,261 @@ def kv4_attention(cache: Kv4Cache, q, block_table, kv_lens, cu_q, max_q: int, ma
     st = lib.kv4_attention(cache._ref, a, _kv4_stream(cache, stream))
     if st:
         _check(st, "kv4_attention")
+    return out
+
+
+# ---- several continuations of one prompt ---------------------------------------------
+_HEAD_ROWS = struct.Struct("@2P4q4i")                   # vbq_head_rows
+_KV4_FORK = struct.Struct("@4i9Pq")                     # vbq_kv4_fork
+_LOGPROBS = struct.Struct("@4iq2P2i7Pq")                # vbq_logprobs
+assert _HEAD_ROWS.size == C.sizeof(vbq_head_rows) and _KV4_FORK.size == C.sizeof(vbq_kv4_fork) and \
+    _LOGPROBS.size == C.sizeof(vbq_logprobs)
+LOGPROBS_MAX_TOP, LOGPROBS_COUNTERS = 32, 512
+
+
+class HeadRotary:
+    """What head_norm_rotary needs beside its tensors: inv_freq float32
+    [rotary_dim / 2] (radians a position), axis uint8 [rotary_dim / 2] (the row of
+    the positions that a pair goes by; None: the only one), interleaved (pairs
+    are neighbouring channels, else channel i and i + rotary_dim / 2), and the
+    weights float32 [head_dim] of the norms of queries and keys (None: not
+    normed). Tensors are kept, not copied; rotary_dim is a multiple of 16."""
+
+    def __init__(self, head_dim: int, inv_freq=None, axis=None, axes: int = 1, interleaved: bool = False, q_weight=None,
+                 k_weight=None, eps: float = 1e-6):
+        import torch
+        if head_dim not in (64, 128, 192, 256):
+            raise ValueError(f"HeadRotary: head_dim {head_dim}, expected 64, 128, 192 or 256")
+        given = [t for t in (inv_freq, q_weight, k_weight) if t is not None]
+        if not given:
+            raise ValueError("HeadRotary: neither inv_freq nor weights")
+        half = 0 if inv_freq is None else inv_freq.numel()
+        if half % 8 or 2 * half > head_dim:
+            raise ValueError(f"inv_freq: {half} pairs, expected a multiple of 8, at most {head_dim // 2}")
+        if not 1 <= axes <= 255 or (axis is None and axes > 1):
+            raise ValueError(f"HeadRotary: {axes} axes{' and no axis of the pairs' if axis is None else ''}")
+        if not 0.0 <= eps <= 3e38:
+            raise ValueError(f"HeadRotary: eps {eps}")
+        self.device = given[0].device
+        if inv_freq is not None:
+            _need(inv_freq, "inv_freq", torch.float32, (half,), self.device)
+        for t, what in ((q_weight, "q_weight"), (k_weight, "k_weight")):
+            if t is not None:
+                _need(t, what, torch.float32, (head_dim,), self.device)
+                if t.data_ptr() % 16:
+                    raise ValueError(f"{what}: not 16-byte aligned")
+        if axis is not None:
+            _need(axis, "axis", torch.uint8, (half,), self.device)
+            if half and int(axis.max()) >= axes:
+                raise ValueError(f"axis: a row of the positions beyond the {axes}")
+        if self.device.type != "cuda":
+            raise ValueError(f"HeadRotary: on {self.device}, expected GPU tensors")
+        self.head_dim, self.rotary_dim, self.axes = int(head_dim), 2 * half, int(axes)
+        self.interleaved, self.eps = bool(interleaved), float(eps)
+        self._keep = (inv_freq, axis, q_weight, k_weight)
+        self.desc = vbq_head_rotary(self.head_dim, self.rotary_dim, self.axes, int(self.interleaved), self.eps, 0,
+                                    *(None if t is None else t.data_ptr() for t in self._keep))
+        self._ref = C.byref(self.desc)
+        self.index = given[0].get_device()
+        self._i32 = torch.int32
+        self._raw_stream = torch._C._cuda_getCurrentRawStream
+
+
+def _on_device(index: int, call, *args) -> int:
+    """call(*args) with the tensors' device as the current one."""
+    import torch
+    if torch._C._cuda_getDevice() == index:
+        return call(*args)
+    with torch.cuda.device(index):
+        return call(*args)
+
+
+def _new(t, shape, dtype, stream):
+    """A tensor beside t that belongs to the stream that will fill it."""
+    if stream is None:
+        return t.new_empty(shape, dtype=dtype)
+    import torch
+    with torch.cuda.stream(stream):
+        return t.new_empty(shape, dtype=dtype)
+
+
+def _head_rows(plan, x, what: str, out, dtype, stream):
+    """The output for x, its tokens, its type and its vbq_head_rows."""
+    dt = _kv4_dtype(getattr(x, "dtype", None), what)
+    H = x.shape[1] if x.ndim == 3 else 0
+    T, ts, hs = _kv4_rows(x, what, H, plan)
+    if out is None:
+        out = _new(x, (T, H, plan.head_dim), x.dtype if dtype is None else dtype, stream)
+        To, ots, ohs = T, H * plan.head_dim, plan.head_dim
+    else:
+        if dtype is not None and out.dtype is not dtype:
+            raise ValueError(f"{what}_out: {out.dtype}, expected {dtype}")
+        To, ots, ohs = _kv4_rows(out, what + "_out", H, plan)
+    odt = _kv4_dtype(out.dtype, what + "_out")
+    if To != T:
+        raise ValueError(f"{what}_out: {To} tokens, expected {T}")
+    return out, T, dt, _HEAD_ROWS.pack(x.data_ptr(), out.data_ptr(), ts, hs, ots, ohs, H, dt, odt, 0)
+
+
+def head_norm_rotary(plan: HeadRotary, q, k, positions, q_out=None, k_out=None, q_dtype=None, k_dtype=None,
+                     stream=None):
+    """Norms every head of q and k [tokens][heads][head_dim] (fp16, bf16 or fp32;
+    token and head rows may be strided; either may be None) and rotates it by its
+    token's positions, int32 [tokens] or [axes][tokens], in one pass. Returns the
+    results, of q_dtype and k_dtype (the inputs' type by default). q_out and k_out:
+    tensors to fill, the inputs themselves for example; other overlaps are
+    refused nowhere and give anything."""
+    if q is None and k is None:
+        raise ValueError("head_norm_rotary: neither q nor k")
+    empty = _HEAD_ROWS.pack(0, 0, 0, 0, 0, 0, 0, 0, 0, 0)
+    rows_q = rows_k = empty
+    T = types = None
+    if q is not None:
+        q_out, T, types, rows_q = _head_rows(plan, q, "q", q_out, q_dtype, stream)
+    if k is not None:
+        k_out, Tk, dt, rows_k = _head_rows(plan, k, "k", k_out, k_dtype, stream)
+        if T is not None and (Tk != T or dt != types):
+            raise ValueError(f"k: {k.dtype} with {Tk} tokens, expected q's {q.dtype} with {T}")
+        T = Tk
+    step = 0
+    if plan.rotary_dim:
+        shape = (T,) if plan.axes == 1 and positions.ndim == 1 else (plan.axes, T)
+        if positions.dtype is not plan._i32 or positions.shape != shape or not positions.is_contiguous() or \
+                positions.get_device() != plan.index:
+            _need(positions, "positions", plan._i32, shape, plan.device)
+        step = T
+    st = _on_device(plan.index, lib.head_norm_rotary, plan._ref, rows_q, rows_k,
+                    positions.data_ptr() if plan.rotary_dim else None, step, T, _kv4_stream(plan, stream))
+    if st:
+        _check(st, "head_norm_rotary")
+    return q_out if q is not None else None, k_out if k is not None else None
+
+
+def kv4_fork_workspace(cache: Kv4Cache, batch: int, table_width: int, batch_before=None, stream=None):
+    """A workspace for kv4_fork calls to `batch` sequences from `batch_before` (default:
+    as many) with tables of this width, or less of each, that do not overlap in time."""
+    try:
+        n = lib.kv4_fork_workspace(cache._ref, batch if batch_before is None else batch_before, batch, table_width)
+    except C.ArgumentError:
+        n = -1
+    if n < 0:
+        raise ValueError(f"kv4_fork: sizes refused ({batch_before} to {batch} sequences, tables of {table_width} entries)")
+    return _kv4_new(cache, (n,), cache.data.dtype, stream)
+
+
+def kv4_fork(cache: Kv4Cache, refs, block_table, lens, parents, reserve=None, out=None, workspace=None, stream=None):
+    """Makes sequences go on from others. block_table int32 [B][W] (-1: no page) and
+    lens int32 [B] are the sequences before, refs int32 [n_pages] how many entries
+    name each page (0: free); parents int32 [B'] says which of them each new
+    sequence goes on from (-1: none, it is empty), reserve int32 [B'] (or None) for
+    how many further tokens it gets pages. Whole pages are shared, part pages
+    copied for all but the first continuation, pages of sequences that nothing
+    goes on from are free afterwards. Returns the new block_table [B'][W], lens and
+    refs; out: tensors to fill (not the inputs). Kv4Cache.check raises where pages ran
+    out. workspace: from kv4_fork_workspace, for calls that allocate nothing."""
+    i32, dev = cache._i32, cache.index
+    if getattr(block_table, "ndim", 0) != 2 or getattr(parents, "ndim", 0) != 1:
+        raise ValueError("block_table, parents: expected a 2-D and a 1-D torch tensor")
+    B, W = block_table.shape
+    N = parents.shape[0]
+    for t, what, shape in ((block_table, "block_table", (B, W)), (lens, "lens", (B,)), (refs, "refs", (cache.n_pages,)),
+                           (parents, "parents", (N,)), (reserve, "reserve", (N,))):
+        if t is None and what == "reserve":
+            continue
+        if t.dtype is not i32 or t.get_device() != dev or t.shape != shape or not t.is_contiguous():
+            _need(t, what, i32, shape, cache.device)
+    if min(B, W, N) < 1:
+        raise ValueError(f"block_table: shape {(B, W)}, {N} parents")
+    if out is None:
+        out = tuple(_kv4_new(cache, shape, i32, stream) for shape in ((N, W), (N,), (cache.n_pages,)))
+    else:
+        for t, what, shape in zip(out, ("out block_table", "out lens", "out refs"), ((N, W), (N,), (cache.n_pages,))):
+            _need(t, what, i32, shape, cache.device)
+    table_out, lens_out, refs_out = out
+    if workspace is None:
+        workspace = kv4_fork_workspace(cache, N, W, B, stream)
+    elif workspace.dtype is not cache.data.dtype or workspace.get_device() != dev or not workspace.is_contiguous():
+        raise ValueError("workspace: expected a contiguous uint8 tensor on the cache's device")
+    f = _KV4_FORK.pack(B, N, W, 0, block_table.data_ptr(), lens.data_ptr(), refs.data_ptr(), parents.data_ptr(),
+                       0 if reserve is None else reserve.data_ptr(), table_out.data_ptr(), lens_out.data_ptr(),
+                       refs_out.data_ptr(), workspace.data_ptr(), workspace.numel())
+    st = _on_device(dev, lib.kv4_fork, cache._ref, f, _kv4_stream(cache, stream))
+    if st:
+        _check(st, "kv4_fork")
+    return table_out, lens_out, refs_out
+
+
+class TokenLogprobs(typing.NamedTuple):
+    """What token_logprobs returns; None for what was not asked for."""
+    logprob: object        # float32 [rows], of the given tokens
+    rank: object           # int32 [rows], their places in the order of the logits, from 0
+    entropy: object        # float32 [rows]
+    lse: object            # float32 [rows], log of the sum of exponentials
+    top_logprob: object    # float32 [rows][top], of the most likely tokens
+    top_index: object      # int32 [rows][top], their numbers
+
+
+def token_logprobs_workspace(rows: int, vocab: int, top: int = 0, device="cuda", stream=None):
+    """A workspace for token_logprobs calls of these sizes (or any that need no
+    more) that do not overlap in time."""
+    import torch
+    try:
+        n = lib.token_logprobs_workspace(rows, vocab, top)
+    except C.ArgumentError:
+        n = -1
+    if n < 0:
+        raise ValueError(f"token_logprobs: sizes refused ({rows} rows of {vocab} logits, top {top})")
+    with torch.cuda.stream(stream):
+        w = torch.empty(n, dtype=torch.uint8, device=device)
+        w[:4 * LOGPROBS_COUNTERS].zero_()
+    return w
+
+
+def token_logprobs(logits, tokens=None, top: int = 0, out=None, workspace=None, stream=None) -> TokenLogprobs:
+    """Log probabilities of rows of logits [rows][vocab] (fp16, bf16 or fp32; rows may be
+    strided): those of `tokens` (int32 or int64 [rows]) with their ranks, the rows'
+    entropies and log-sum-exps, and the `top` most likely tokens (at most 32, ties go
+    to the lower number). Logits may be -infinity; rows with a NaN or +infinity give
+    NaN and -1. out: a TokenLogprobs of tensors to fill. workspace: from
+    token_logprobs_workspace, for calls that allocate nothing."""
+    import torch
+    if getattr(logits, "ndim", 0) != 2:
+        raise ValueError("logits: expected a 2-D torch tensor")
+    M, V = logits.shape
+    dt = _kv4_dtype(logits.dtype, "logits")
+    if logits.device.type != "cuda":
+        raise ValueError(f"logits: on {logits.device}, expected a GPU tensor")
+    if V > 1 and logits.stride(1) != 1:
+        raise ValueError("logits: a row is not contiguous")
+    dev = logits.get_device()
+    size = 0
+    if tokens is not None:
+        if tokens.dtype is not torch.int64 and tokens.dtype is not torch.int32:
+            raise ValueError(f"tokens: dtype {tokens.dtype}, expected int32 or int64")
+        if tokens.shape != (M,) or not tokens.is_contiguous() or tokens.get_device() != dev:
+            _need(tokens, "tokens", tokens.dtype, (M,), logits.device)
+        size = tokens.itemsize
+    if not 0 <= top <= min(LOGPROBS_MAX_TOP, V):
+        raise ValueError(f"top: {top}, expected 0..{min(LOGPROBS_MAX_TOP, V)}")
+    kinds = ((torch.float32, (M,), size), (torch.int32, (M,), size), (torch.float32, (M,), 1), (torch.float32, (M,), 1),
+             (torch.float32, (M, top), top), (torch.int32, (M, top), top))
+    if out is None:
+        out = TokenLogprobs(*(_new(logits, shape, dtype, stream) if want else None for dtype, shape, want in kinds))
+    else:
+        out = TokenLogprobs(*out)
+        for t, what, (dtype, shape, want) in zip(out, TokenLogprobs._fields, kinds):
+            if want and (t is not None or what not in ("entropy", "lse")):
+                _need(t, "out " + what, dtype, shape, logits.device)
+    if workspace is None:
+        workspace = token_logprobs_workspace(M, V, top, logits.device, stream)
+    elif workspace.dtype is not torch.uint8 or workspace.get_device() != dev or not workspace.is_contiguous():
+        raise ValueError("workspace: expected a contiguous uint8 tensor on the logits' device")
+    a = _LOGPROBS.pack(M, V, dt, top, logits.stride(0) if M > 1 else V, logits.data_ptr(),
+                       tokens.data_ptr() if size else 0, size, 0,
+                       *(t.data_ptr() if t is not None and want else 0 for t, (_, _, want) in zip(out, kinds)),
+                       workspace.data_ptr(), workspace.numel())
+    st = _on_device(dev, lib.token_logprobs, a,
+                    torch._C._cuda_getCurrentRawStream(dev) if stream is None else stream.cuda_stream)
+    if st:
+        _check(st, "token_logprobs")
     return out

@@ -8,7 +8,9 @@
 #include <cfloat>
 #include <vector>
 
+#include "heads.h"
 #include "kv4.h"
+#include "logprobs.h"
 
 using namespace vbq;
 
@@ -221,6 +223,199 @@ vbq_status kv4_attention(const vbq_kv4* cache, const vbq_kv4_attn* a, hipStream_
   k.parts = p.parts;
   k.scale_log2 = a->scale * kLog2e;
   return from_hip(launch_kv4_attention(k, p, stream));
+}
+
+static vbq_status check_rows(const vbq_head_rows* r, const float* weight, HeadRows* out) {
+  *out = HeadRows{};
+  if (!r) return VBQ_ERR_INVALID_ARG;
+  if (r->reserved != 0) return VBQ_ERR_INVALID_ARG;
+  if (r->heads < 0) return VBQ_ERR_SHAPE;
+  if (r->heads > 65536) return VBQ_ERR_UNSUPPORTED;
+  if (r->heads == 0) return VBQ_OK;
+  if (r->in_dtype < VBQ_F16 || r->in_dtype > VBQ_F32 || r->out_dtype < VBQ_F16 || r->out_dtype > VBQ_F32)
+    return VBQ_ERR_INVALID_ARG;
+  const int64_t in16 = r->in_dtype == VBQ_F32 ? 4 : 8, out16 = r->out_dtype == VBQ_F32 ? 4 : 8;
+  if (!aligned(r->in, 16) || !aligned(r->out, 16) || !aligned(weight, 16) || r->in_token_stride % in16 ||
+      r->in_head_stride % in16 || r->out_token_stride % out16 || r->out_head_stride % out16)
+    return VBQ_ERR_ALIGNMENT;
+  *out = HeadRows{r->in, r->out, weight, r->in_token_stride, r->in_head_stride, r->out_token_stride,
+                  r->out_head_stride, r->heads, r->out_dtype};
+  return VBQ_OK;
+}
+
+vbq_status head_norm_rotary(const vbq_head_rotary* plan, const vbq_head_rows* q, const vbq_head_rows* k,
+                            const int32_t* positions, int64_t position_stride, int32_t n_tokens, hipStream_t stream) {
+  if (!plan || plan->reserved != 0) return VBQ_ERR_INVALID_ARG;
+  const int32_t D = plan->head_dim, R = plan->rotary_dim;
+  if (D < kGroup || D % kGroup || D / kGroup > VBQ_KV4_MAX_GROUPS || R < 0 || R > D || R % 16 || n_tokens < 0)
+    return VBQ_ERR_SHAPE;
+  if (plan->axes < 1 || plan->axes > 255 || (plan->interleaved != 0 && plan->interleaved != 1) ||
+      !(plan->eps >= 0.f && plan->eps <= FLT_MAX))
+    return VBQ_ERR_INVALID_ARG;
+  HeadRotary a;
+  vbq_status st = check_rows(q, plan->q_weight, &a.q);
+  if (st == VBQ_OK) st = check_rows(k, plan->k_weight, &a.k);
+  if (st != VBQ_OK) return st;
+  if (a.q.heads && a.k.heads && q->in_dtype != k->in_dtype) return VBQ_ERR_INVALID_ARG;
+  if (n_tokens == 0 || (a.q.heads == 0 && a.k.heads == 0)) return VBQ_OK;
+  if (R && (!plan->inv_freq || !positions)) return VBQ_ERR_INVALID_ARG;
+  if ((a.q.heads && (!a.q.in || !a.q.out)) || (a.k.heads && (!a.k.in || !a.k.out))) return VBQ_ERR_INVALID_ARG;
+  if (!aligned(plan->inv_freq, 4) || !aligned(positions, 4)) return VBQ_ERR_ALIGNMENT;
+  a.positions = positions;
+  a.inv_freq = plan->inv_freq;
+  a.axis = plan->axis;
+  a.position_stride = position_stride;
+  a.tokens = n_tokens;
+  a.head_dim = D;
+  a.rotary_dim = R;
+  a.axes = plan->axes;
+  a.interleaved = plan->interleaved;
+  a.eps = plan->eps;
+  const hipError_t e = launch_head_norm_rotary(a, a.q.heads ? q->in_dtype : k->in_dtype, stream);
+  return e == hipErrorNotSupported ? VBQ_ERR_UNSUPPORTED : from_hip(e);
+}
+
+// Places in a fork's workspace, in bytes from its start; the last is its size.
+struct ForkPlaces {
+  int64_t offset, kids, first, free, end;
+};
+static ForkPlaces fork_places(int64_t n_pages, int64_t in, int64_t out, int64_t width) {
+  ForkPlaces p;
+  const auto up = [](int64_t v) { return (v + 15) & ~(int64_t)15; };
+  p.offset = 16;
+  p.kids = up(p.offset + 4 * out);
+  p.first = up(p.kids + 4 * in);
+  p.free = up(p.first + 4 * in);
+  p.end = up(p.free + 4 * std::min(n_pages, out * width));
+  return p;
+}
+static vbq_status check_fork_sizes(int32_t in, int32_t out, int32_t width) {
+  if (in < 1 || out < 1 || width < 1) return VBQ_ERR_SHAPE;
+  if (in > 65535 || out > 65535 || width > (1 << 20)) return VBQ_ERR_UNSUPPORTED;
+  return VBQ_OK;
+}
+
+int64_t kv4_fork_workspace(const vbq_kv4* cache, int32_t batch_in, int32_t batch_out, int32_t table_width) {
+  KvCache c;
+  if (check_cache(cache, false, &c) != VBQ_OK || check_fork_sizes(batch_in, batch_out, table_width) != VBQ_OK) return -1;
+  return fork_places(c.n_pages, batch_in, batch_out, table_width).end;
+}
+
+vbq_status kv4_fork(const vbq_kv4* cache, const vbq_kv4_fork* a, hipStream_t stream) {
+  KvFork f;
+  vbq_status st = check_cache(cache, true, &f.cache);
+  if (st != VBQ_OK) return st;
+  if (!a || a->reserved != 0) return VBQ_ERR_INVALID_ARG;
+  st = check_fork_sizes(a->batch_in, a->batch_out, a->table_width);
+  if (st != VBQ_OK) return st;
+  if (!a->table_in || !a->lens_in || !a->refs_in || !a->parents || !a->table_out || !a->lens_out || !a->refs_out ||
+      !a->workspace)
+    return VBQ_ERR_INVALID_ARG;
+  if (!aligned(a->table_in, 4) || !aligned(a->lens_in, 4) || !aligned(a->parents, 4) || !aligned(a->reserve, 4) ||
+      !aligned(a->table_out, 4) || !aligned(a->lens_out, 4) || !aligned(a->refs_in, 16) || !aligned(a->refs_out, 16) ||
+      !aligned(a->workspace, 16))
+    return VBQ_ERR_ALIGNMENT;
+  const ForkPlaces p = fork_places(f.cache.n_pages, a->batch_in, a->batch_out, a->table_width);
+  if (a->workspace_bytes < p.end) return VBQ_ERR_CAPACITY;
+  // no output overlaps an input or another output
+  struct Span {
+    const void* at;
+    int64_t bytes;
+  };
+  const int64_t rows_in = 4ll * a->batch_in, rows_out = 4ll * a->batch_out, counts = 4ll * f.cache.n_pages;
+  const Span in[] = {{a->table_in, rows_in * a->table_width}, {a->lens_in, rows_in}, {a->refs_in, counts},
+                     {a->parents, rows_out}, {a->reserve, a->reserve ? rows_out : 0}};
+  const Span out[] = {{a->table_out, rows_out * a->table_width}, {a->lens_out, rows_out}, {a->refs_out, counts},
+                      {a->workspace, p.end}};
+  const auto meet = [](const Span& u, const Span& v) {
+    const uintptr_t x = reinterpret_cast<uintptr_t>(u.at), y = reinterpret_cast<uintptr_t>(v.at);
+    return x < y + (uintptr_t)v.bytes && y < x + (uintptr_t)u.bytes;
+  };
+  for (int i = 0; i < 4; ++i) {
+    for (const Span& v : in)
+      if (meet(out[i], v)) return VBQ_ERR_INVALID_ARG;
+    for (int j = 0; j < i; ++j)
+      if (meet(out[i], out[j])) return VBQ_ERR_INVALID_ARG;
+  }
+  uint8_t* const w = static_cast<uint8_t*>(a->workspace);
+  f.table_in = a->table_in;
+  f.lens_in = a->lens_in;
+  f.refs_in = a->refs_in;
+  f.parents = a->parents;
+  f.reserve = a->reserve;
+  f.table_out = a->table_out;
+  f.lens_out = a->lens_out;
+  f.refs_out = a->refs_out;
+  f.batch_in = a->batch_in;
+  f.batch_out = a->batch_out;
+  f.width = a->table_width;
+  f.head = reinterpret_cast<int32_t*>(w);
+  f.offset = reinterpret_cast<int32_t*>(w + p.offset);
+  f.kids = reinterpret_cast<int32_t*>(w + p.kids);
+  f.first = reinterpret_cast<int32_t*>(w + p.first);
+  f.free = reinterpret_cast<int32_t*>(w + p.free);
+  return from_hip(launch_kv4_fork(f, stream));
+}
+
+// Bytes of a workspace, -1 for sizes that are refused: counters, keys, sums.
+struct LogprobPlaces {
+  int64_t keys, parts, end;
+  int splits;
+};
+static vbq_status logprob_places(int32_t rows, int32_t vocab, int32_t top, LogprobPlaces* p) {
+  if (rows < 0 || vocab < 1 || top < 0 || top > vocab) return VBQ_ERR_SHAPE;
+  if (vocab > (1 << 30) || top > VBQ_LOGPROBS_MAX_TOP) return VBQ_ERR_UNSUPPORTED;
+  p->splits = rows ? logprob_splits(rows, vocab) : 1;
+  const int64_t n = (int64_t)rows * p->splits;
+  if (n >= (1 << 24)) return VBQ_ERR_UNSUPPORTED;
+  p->keys = 4 * VBQ_LOGPROBS_COUNTERS;   // (more rows are not shared out)
+  p->parts = (p->keys + 8 * n * top + 15) & ~15ll;
+  p->end = p->splits > 1 ? p->parts + (int64_t)sizeof(LogprobPart) * n : 0;
+  return VBQ_OK;
+}
+
+int64_t token_logprobs_workspace(int32_t rows, int32_t vocab, int32_t top) {
+  LogprobPlaces p;
+  return logprob_places(rows, vocab, top, &p) == VBQ_OK ? p.end : -1;
+}
+
+vbq_status token_logprobs(const vbq_logprobs* a, hipStream_t stream) {
+  if (!a || a->reserved != 0) return VBQ_ERR_INVALID_ARG;
+  if (a->dtype < VBQ_F16 || a->dtype > VBQ_F32) return VBQ_ERR_INVALID_ARG;
+  LogprobPlaces p;
+  vbq_status st = logprob_places(a->rows, a->vocab, a->top, &p);
+  if (st != VBQ_OK) return st;
+  if (a->tokens && a->token_bytes != 4 && a->token_bytes != 8) return VBQ_ERR_INVALID_ARG;
+  if (a->rows == 0) return VBQ_OK;
+  if (!a->logits || (a->tokens && (!a->logprob || !a->rank)) || (a->top && (!a->top_logprob || !a->top_index)) ||
+      (p.end && !a->workspace))
+    return VBQ_ERR_INVALID_ARG;
+  if (!aligned(a->logits, a->dtype == VBQ_F32 ? 4 : 2) || (a->tokens && !aligned(a->tokens, a->token_bytes)) ||
+      !aligned(a->logprob, 4) || !aligned(a->rank, 4) || !aligned(a->entropy, 4) || !aligned(a->lse, 4) ||
+      !aligned(a->top_logprob, 4) || !aligned(a->top_index, 4) || !aligned(a->workspace, 16))
+    return VBQ_ERR_ALIGNMENT;
+  if (a->workspace_bytes < p.end) return VBQ_ERR_CAPACITY;
+  uint8_t* const w = static_cast<uint8_t*>(a->workspace);
+  Logprobs k;
+  k.logits = a->logits;
+  k.tokens = a->tokens;
+  k.row_stride = a->row_stride;
+  k.logprob = a->logprob;
+  k.rank = a->rank;
+  k.entropy = a->entropy;
+  k.lse = a->lse;
+  k.top_logprob = a->top_logprob;
+  k.top_index = a->top_index;
+  k.counters = reinterpret_cast<uint32_t*>(w);
+  k.keys = reinterpret_cast<uint64_t*>(w + p.keys);
+  k.parts = reinterpret_cast<LogprobPart*>(w + p.parts);
+  k.rows = a->rows;
+  k.vocab = a->vocab;
+  k.top = a->top;
+  k.long_tokens = a->tokens && a->token_bytes == 8;
+  k.splits = p.splits;
+  const hipError_t e = launch_token_logprobs(k, a->dtype, stream);
+  return e == hipErrorNotSupported ? VBQ_ERR_UNSUPPORTED : from_hip(e);
 }
 
 int vbq_abi_version(void) { return VBQ_ABI_VERSION; }

@@ -63,6 +63,26 @@ struct KvAttn {
   float scale_log2;            // scale * log2(e)
 };
 
+// A fork (see kvfork.hip): the call's arguments, and places in its workspace.
+struct KvFork {
+  KvCache cache;
+  const int32_t* table_in;
+  const int32_t* lens_in;
+  const int32_t* refs_in;
+  const int32_t* parents;
+  const int32_t* reserve;   // NULL: none
+  int32_t* table_out;
+  int32_t* lens_out;
+  int32_t* refs_out;
+  int32_t batch_in, batch_out, width;
+  int32_t* head;     // pages that were found
+  int32_t* offset;   // [batch_out] pages taken by the sequences before, sign bit: a first continuation
+  int32_t* kids;     // [batch_in] continuations
+  int32_t* first;    // [batch_in] (used where they do not fit LDS)
+  int32_t* free;     // the pages to take
+};
+hipError_t launch_kv4_fork(const KvFork& f, hipStream_t s);
+
 // A launch's first dimension holds 2^32 - 1 threads, and more are cut off without an error.
 constexpr bool kv_grid_fits(int64_t groups, int64_t threads) { return groups * threads <= (int64_t)UINT32_MAX; }
 

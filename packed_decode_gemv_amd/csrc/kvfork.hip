@@ -1,0 +1,272 @@
+// Forks of cached sequences (meaning in vbq.h): two launches.
+//
+// k_kv4_fork_plan: its first workgroup counts each old sequence's continuations and
+// finds the first of them, counts the pages that every new sequence needs, and lists
+// the lowest free pages, as many as are needed; the others copy the reference counts.
+// Which page a sequence gets follows from the numbers alone: the i-th page needed, in
+// the order of sequences and their entries, is the i-th free one.
+//
+// k_kv4_fork: for every new sequence its row of the table, its length, its pages'
+// counts, and (by several workgroups) the copy of its part page; for every old one
+// what its row's pages lose or gain. Counts are sums of whole numbers by atomics, the
+// same in any order. Pages that are free before the call alone are given out, so no
+// page that is read is written.
+#include "kv4.h"
+
+namespace vbq {
+namespace {
+
+constexpr int kPlan = 1024;                  // threads of the planning workgroup
+constexpr int kPlanKids = 4096;              // old sequences that it counts in LDS
+constexpr int kScan = 16;                    // counts that a thread looks at, at a time
+
+// Of a new sequence: what it goes on from.
+struct Parent {
+  int p;             // -1: nothing
+  int32_t len, whole, have;   // tokens, whole pages, pages
+  int64_t need;      // pages with those reserved
+  bool bad_len;      // something does not fit
+};
+__device__ inline Parent parent_of(const KvFork& f, int b) {
+  Parent r;
+  r.p = f.parents[b];
+  r.len = r.whole = r.have = 0;
+  r.bad_len = false;
+  int64_t more = f.reserve ? f.reserve[b] : 0;
+  if (more < 0) {
+    r.bad_len = true;
+    more = 0;
+  }
+  if (r.p >= f.batch_in) r.bad_len = true;
+  if (r.p < 0 || r.p >= f.batch_in) r.p = -1;
+  const int shift = f.cache.block_shift + 5;
+  if (r.p >= 0) {
+    const int32_t len = f.lens_in[r.p];
+    if (len < 0 || (int64_t)len > ((int64_t)f.width << shift)) {
+      r.bad_len = true;
+      r.p = -1;
+    } else {
+      r.len = len;
+      r.whole = len >> shift;
+      r.have = (int)(((int64_t)len + (1 << shift) - 1) >> shift);
+    }
+  }
+  r.need = (r.len + more + (1 << shift) - 1) >> shift;
+  if (r.need > f.width) {
+    r.bad_len = true;
+    r.need = f.width;
+  }
+  return r;
+}
+// Whether the first continuation keeps entry j (from the part page on) of its parent's row.
+__device__ inline bool keeps(const KvFork& f, int p, int j, int32_t& page) {
+  page = f.table_in[(int64_t)p * f.width + j];
+  return (uint32_t)page < (uint32_t)f.cache.n_pages && f.refs_in[page] == 1;
+}
+
+// Inclusive sum over the workgroup; total to every thread. sums: a place a wavefront.
+template <int WAVES>
+__device__ inline int group_scan(int v, int* sums, int& total) {
+  const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
+#pragma unroll
+  for (int d = 1; d < 64; d <<= 1) {
+    const int u = __shfl_up(v, d, 64);
+    if (lane >= d) v += u;
+  }
+  if (lane == 63) sums[wave] = v;
+  __syncthreads();
+  int before = 0;
+  total = 0;
+#pragma unroll
+  for (int w = 0; w < WAVES; ++w) {
+    const int s = sums[w];
+    before += w < wave ? s : 0;
+    total += s;
+  }
+  __syncthreads();
+  return v + before;
+}
+
+template <bool IN_LDS>
+__global__ __launch_bounds__(kPlan) void k_kv4_fork_plan(KvFork f) {
+  const int tid = (int)threadIdx.x;
+  if (blockIdx.x) {   // the counts as they were
+    const int64_t n = f.cache.n_pages;
+    for (int64_t i = ((int64_t)(blockIdx.x - 1) * kPlan + tid) * 4; i < n; i += (int64_t)(gridDim.x - 1) * kPlan * 4) {
+      if (i + 4 <= n) *reinterpret_cast<u32x4*>(f.refs_out + i) = *reinterpret_cast<const u32x4*>(f.refs_in + i);
+      else
+        for (int64_t e = i; e < n; ++e) f.refs_out[e] = f.refs_in[e];
+    }
+    return;
+  }
+  __shared__ int lds_first[IN_LDS ? kPlanKids : 1], lds_kids[IN_LDS ? kPlanKids : 1];
+  __shared__ int sums[kPlan / 64];
+  int* const first = IN_LDS ? lds_first : f.first;
+  int* const kids = IN_LDS ? lds_kids : f.kids;
+  auto get = [](int* p) { return IN_LDS ? *p : __hip_atomic_load(p, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT); };
+  auto put = [](int* p, int v) {
+    if (IN_LDS) *p = v;
+    else __hip_atomic_store(p, v, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
+  };
+  for (int p = tid; p < f.batch_in; p += kPlan) {
+    put(first + p, INT32_MAX);
+    put(kids + p, 0);
+  }
+  __builtin_amdgcn_s_waitcnt(VBQ_VMCNT_IMM(0));   // (device-scope stores are where the atomics see them)
+  __syncthreads();
+  for (int b = tid; b < f.batch_out; b += kPlan) {
+    const Parent r = parent_of(f, b);
+    if (r.bad_len) kv_flag(f.cache, VBQ_KV4_FLAG_LENGTH);
+    if (r.p < 0) continue;
+    __hip_atomic_fetch_min(first + r.p, b, __ATOMIC_RELAXED, IN_LDS ? __HIP_MEMORY_SCOPE_WORKGROUP : __HIP_MEMORY_SCOPE_AGENT);
+    __hip_atomic_fetch_add(kids + r.p, 1, __ATOMIC_RELAXED, IN_LDS ? __HIP_MEMORY_SCOPE_WORKGROUP : __HIP_MEMORY_SCOPE_AGENT);
+  }
+  __builtin_amdgcn_s_waitcnt(VBQ_VMCNT_IMM(0));
+  __syncthreads();
+  // Pages that each new sequence needs, and how many those before it do.
+  int64_t wanted = 0;
+  for (int b0 = 0; b0 < f.batch_out; b0 += kPlan) {
+    const int b = b0 + tid;
+    int n = 0;
+    bool is_first = false;
+    if (b < f.batch_out) {
+      const Parent r = parent_of(f, b);
+      is_first = r.p >= 0 && get(first + r.p) == b;
+      n = (int)r.need - r.whole;
+      if (n < 0) n = 0;
+      if (is_first)
+        for (int j = r.whole, e = (int)r.need, page; j < e; ++j) n -= keeps(f, r.p, j, page);
+    }
+    int total;
+    const int upto = group_scan<kPlan / 64>(n, sums, total);
+    // (more than there are pages is cut off: those beyond find none)
+    if (b < f.batch_out) {
+      const int64_t before = wanted + (upto - n);
+      f.offset[b] = (int)(before < f.cache.n_pages ? before : f.cache.n_pages) | (is_first ? INT32_MIN : 0);
+    }
+    wanted += total;
+  }
+  if (IN_LDS)
+    for (int p = tid; p < f.batch_in; p += kPlan) f.kids[p] = lds_kids[p];
+  // The lowest free pages.
+  int found = 0;
+  const int want = (int)(wanted < f.cache.n_pages ? wanted : f.cache.n_pages);
+  for (int64_t base = 0; base < f.cache.n_pages && found < want; base += kPlan * kScan) {
+    const int64_t at = base + (int64_t)tid * kScan;
+    uint32_t free = 0;
+#pragma unroll
+    for (int i = 0; i < kScan; i += 4) {
+      if (at + i + 4 <= f.cache.n_pages) {
+        const u32x4 v = *reinterpret_cast<const u32x4*>(f.refs_in + at + i);
+#pragma unroll
+        for (int c = 0; c < 4; ++c) free |= (v[c] == 0 ? 1u : 0u) << (i + c);
+      } else {
+        for (int c = 0; c < 4; ++c)
+          if (at + i + c < f.cache.n_pages) free |= (f.refs_in[at + i + c] == 0 ? 1u : 0u) << (i + c);
+      }
+    }
+    int total;
+    int place = found + group_scan<kPlan / 64>(__builtin_popcount(free), sums, total) - __builtin_popcount(free);
+    for (; free; free &= free - 1, ++place)
+      if (place < want) f.free[place] = (int)(at + __builtin_ctz(free));
+    found += total;
+  }
+  if (tid == 0) {
+    f.head[0] = found < want ? found : want;
+    if (found < wanted) kv_flag(f.cache, VBQ_KV4_FLAG_FULL);
+  }
+}
+
+constexpr int kForkThreads = 256;
+
+__global__ __launch_bounds__(kForkThreads) void k_kv4_fork(KvFork f) {
+  __shared__ int sums[kForkThreads / 64];
+  const int tid = (int)threadIdx.x;
+  const int32_t n_pages = f.cache.n_pages;
+  if (blockIdx.x >= (uint32_t)f.batch_out) {   // an old sequence: its row is gone, its whole pages go to its continuations
+    if (blockIdx.y) return;
+    const int p = (int)(blockIdx.x - (uint32_t)f.batch_out), kids = f.kids[p];
+    const int32_t whole = kids ? f.lens_in[p] >> (f.cache.block_shift + 5) : 0;
+    for (int j = tid; j < f.width; j += kForkThreads) {
+      const int32_t page = f.table_in[(int64_t)p * f.width + j];
+      const int d = (j < whole ? kids : 0) - 1;
+      if ((uint32_t)page < (uint32_t)n_pages) {
+        if (d) __hip_atomic_fetch_add(f.refs_out + page, d, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
+      } else if (page != -1) {
+        kv_flag(f.cache, VBQ_KV4_FLAG_PAGE);
+      }
+    }
+    return;
+  }
+  const int b = (int)blockIdx.x;
+  const Parent r = parent_of(f, b);
+  const int off = f.offset[b], found = f.head[0];
+  const bool first = off < 0;
+  int at = off & INT32_MAX;   // the next page taken
+  const int32_t* const from = f.table_in + (int64_t)(r.p < 0 ? 0 : r.p) * f.width;
+
+  // The part page: copied unless it is kept.
+  const int32_t part = r.have > r.whole ? from[r.whole] : -1;
+  int32_t page;
+  if ((uint32_t)part < (uint32_t)n_pages && at < found && !(first && keeps(f, r.p, r.whole, page))) {
+    const int G = f.cache.groups;
+    const int rest = r.len & ((32 << f.cache.block_shift) - 1);
+    const int run = (rest + kKvBlock - 1) / kKvBlock * (kKvGroupBytes * G / 16);   // of one head, in 16 bytes
+    const int stride = (kKvGroupBytes * G / 16) << f.cache.block_shift;            // between heads
+    const u32x4* const src = reinterpret_cast<const u32x4*>(kv_block(f.cache, G, (uint32_t)part, 0, 0));
+    u32x4* const dst = reinterpret_cast<u32x4*>(kv_block(f.cache, G, (uint32_t)f.free[at], 0, 0));
+    const int all = run * f.cache.heads;
+    for (int i = (int)blockIdx.y * kForkThreads + tid; i < all; i += (int)gridDim.y * kForkThreads) {
+      const int h = i / run, o = h * (stride - run) + i;
+      dst[o] = src[o];
+    }
+  }
+  if (blockIdx.y) return;
+
+  if (tid == 0) f.lens_out[b] = r.len;
+  int32_t* const to = f.table_out + (int64_t)b * f.width;
+  for (int j = tid; j < r.whole; j += kForkThreads) {
+    const int32_t e = from[j];
+    const bool ok = (uint32_t)e < (uint32_t)n_pages;
+    if (!ok) kv_flag(f.cache, VBQ_KV4_FLAG_PAGE);
+    to[j] = ok ? e : -1;
+  }
+  for (int j0 = r.whole; j0 < (int)r.need; j0 += kForkThreads) {
+    const int j = j0 + tid;
+    bool keep = false, fresh = false;
+    int32_t e = -1;
+    if (j < (int)r.need) {
+      if (j < r.have && (uint32_t)from[j] >= (uint32_t)n_pages) kv_flag(f.cache, VBQ_KV4_FLAG_PAGE);
+      keep = first && keeps(f, r.p, j, e);
+      fresh = !keep;
+    }
+    int total;
+    const int place = at + group_scan<kForkThreads / 64>(fresh ? 1 : 0, sums, total) - 1;
+    if (fresh) e = place < found ? f.free[place] : -1;
+    if (j < (int)r.need) {
+      to[j] = e;
+      if (e >= 0) __hip_atomic_fetch_add(f.refs_out + e, 1, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
+    }
+    at += total;
+  }
+  for (int j = (int)(r.need > r.whole ? r.need : r.whole) + tid; j < f.width; j += kForkThreads) to[j] = -1;
+}
+
+}  // namespace
+
+hipError_t launch_kv4_fork(const KvFork& f, hipStream_t s) {
+  const int64_t page = (int64_t)f.cache.heads * f.cache.groups * kKvGroupBytes << f.cache.block_shift;
+  const int64_t copies = (f.cache.n_pages + kPlan * 4 - 1) / (kPlan * 4);
+  const dim3 plan((uint32_t)(1 + (copies < 64 ? copies : 64)));
+  if (f.batch_in <= kPlanKids) k_kv4_fork_plan<true><<<plan, kPlan, 0, s>>>(f);
+  else k_kv4_fork_plan<false><<<plan, kPlan, 0, s>>>(f);
+  hipError_t e = hipGetLastError();
+  if (e != hipSuccess) return e;
+  int64_t slices = page / (kForkThreads * 16 * 4);
+  slices = slices < 1 ? 1 : slices < 32 ? slices : 32;
+  const dim3 grid((uint32_t)(f.batch_out + f.batch_in), (uint32_t)slices);
+  k_kv4_fork<<<grid, kForkThreads, 0, s>>>(f);
+  return hipGetLastError();
+}
+
+}  // namespace vbq
