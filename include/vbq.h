@@ -538,6 +538,31 @@ typedef struct vbq_kv4_fork {
 int64_t kv4_fork_workspace(const vbq_kv4* cache, int32_t batch_in, int32_t batch_out, int32_t table_width);
 vbq_status kv4_fork(const vbq_kv4* cache, const vbq_kv4_fork* f, hipStream_t stream);
 
+/* Attention of sequences that have their first tokens in common: kv4_attention's results,
+ * with what a group of sequences shares read once for the rows of all of them.
+ * Group g is sequences cu_groups[g] .. cu_groups[g+1] - 1; its first shared[g] tokens lie
+ * in the pages that the table's row of its first sequence names (the other rows' entries
+ * of whole blocks of 32 among them are not read). Sequences of no group have nothing in
+ * common. Queries stand behind the shared tokens: kv_lens[b] less the sequence's queries
+ * is shared[g] at least. Windows are not offered (window and sinks are 0). max_kv is not
+ * looked at; max_own is: no sequence holds more tokens beyond its group's shared ones.
+ * A sequence for whose group or itself numbers do not fit is left out (FLAG_LENGTH).
+ * The arithmetic is kv4_attention's, with the rows of a group together in place of a
+ * sequence's for the shared tokens; sums of both kinds are joined in fp32.
+ * workspace: as for kv4_attention, of kv4_attention_shared_workspace() bytes. */
+typedef struct vbq_kv4_groups {
+  int32_t n_groups;       /* 1 .. 65535 */
+  int32_t max_shared;     /* no group shares more tokens than this */
+  int32_t max_own;
+  int32_t max_group_q;    /* no group's sequences have more queries in all */
+  const int32_t* cu_groups; /* device, [n_groups + 1], not falling, at most batch */
+  const int32_t* shared;  /* device, [n_groups] */
+  int64_t reserved;       /* 0 */
+} vbq_kv4_groups;
+int64_t kv4_attention_shared_workspace(const vbq_kv4* cache, const vbq_kv4_attn* a, const vbq_kv4_groups* g);
+vbq_status kv4_attention_shared(const vbq_kv4* cache, const vbq_kv4_attn* a, const vbq_kv4_groups* g,
+                                hipStream_t stream);
+
 /* Log probabilities of rows of logits x[0 .. vocab-1] (those of an LM head, say), in one
  * pass over them; sums are fp32:
  *   lse = log sum_i exp(x_i); logprob_i = x_i - lse; entropy = -sum_i exp(logprob_i) logprob_i

@@ -59,7 +59,8 @@ EXPORTS = ("vbq_abi_version", "vbq_status_string", "vbq_pack_query", "vbq_pack",
            "vbq_gemv", "vbq_gemv_batched", "vbq_gemv_batched_static", "vbq_gemv_levels", "vbq_gemm",
            "cell_requant_verify", "cell_drift_bound", "vbq_residual_error", "vbq_gemv_cell8", "cell8_encode",
            "cell8_decode", "kv4_page_bytes", "kv4_append", "kv4_read", "kv4_attention_workspace", "kv4_attention",
-           "head_norm_rotary", "kv4_fork_workspace", "kv4_fork", "token_logprobs_workspace", "token_logprobs")
+           "head_norm_rotary", "kv4_fork_workspace", "kv4_fork",
+           "kv4_attention_shared_workspace", "kv4_attention_shared", "token_logprobs_workspace", "token_logprobs")
 
 
 class vbq_kv4(C.Structure):
@@ -97,6 +98,11 @@ class vbq_kv4_fork(C.Structure):
     _fields_ = [(n, C.c_int32) for n in ("batch_in", "batch_out", "table_width", "reserved")] + \
                [(n, C.c_void_p) for n in ("table_in", "lens_in", "refs_in", "parents", "reserve", "table_out",
                                           "lens_out", "refs_out", "workspace")] + [("workspace_bytes", C.c_int64)]
+
+
+class vbq_kv4_groups(C.Structure):
+    _fields_ = [(n, C.c_int32) for n in ("n_groups", "max_shared", "max_own", "max_group_q")] + \
+               [("cu_groups", C.c_void_p), ("shared", C.c_void_p), ("reserved", C.c_int64)]
 
 
 class vbq_logprobs(C.Structure):
@@ -162,6 +168,10 @@ def _load():
     lib.kv4_fork_workspace.argtypes = [C.POINTER(vbq_kv4), I32, I32, I32]
     lib.kv4_fork.restype = C.c_int
     lib.kv4_fork.argtypes = [C.POINTER(vbq_kv4), P, P]
+    lib.kv4_attention_shared_workspace.restype = I64
+    lib.kv4_attention_shared_workspace.argtypes = [C.POINTER(vbq_kv4), P, P]
+    lib.kv4_attention_shared.restype = C.c_int
+    lib.kv4_attention_shared.argtypes = [C.POINTER(vbq_kv4), P, P, P]
     lib.token_logprobs_workspace.restype = I64
     lib.token_logprobs_workspace.argtypes = [I32, I32, I32]
     lib.token_logprobs.restype = C.c_int
@@ -771,9 +781,10 @@ def kv4_attention(cache: Kv4Cache, q, block_table, kv_lens, cu_q, max_q: int, ma
 # ---- several continuations of one prompt ---------------------------------------------
 _HEAD_ROWS = struct.Struct("@2P4q4i")                   # vbq_head_rows
 _KV4_FORK = struct.Struct("@4i9Pq")                     # vbq_kv4_fork
+_KV4_GROUPS = struct.Struct("@4i2Pq")                   # vbq_kv4_groups
 _LOGPROBS = struct.Struct("@4iq2P2i7Pq")                # vbq_logprobs
 assert _HEAD_ROWS.size == C.sizeof(vbq_head_rows) and _KV4_FORK.size == C.sizeof(vbq_kv4_fork) and \
-    _LOGPROBS.size == C.sizeof(vbq_logprobs)
+    _KV4_GROUPS.size == C.sizeof(vbq_kv4_groups) and _LOGPROBS.size == C.sizeof(vbq_logprobs)
 LOGPROBS_MAX_TOP, LOGPROBS_COUNTERS = 32, 512
 
 
@@ -823,6 +834,11 @@ class HeadRotary:
         self.index = given[0].get_device()
         self._i32 = torch.int32
         self._raw_stream = torch._C._cuda_getCurrentRawStream
+
+
+def _int32(*numbers) -> bool:
+    """Whether all are numbers that an int32 holds (ctypes would cut off the rest)."""
+    return all(-2 ** 31 <= n < 2 ** 31 for n in numbers)
 
 
 def _on_device(index: int, call, *args) -> int:
@@ -881,6 +897,8 @@ def head_norm_rotary(plan: HeadRotary, q, k, positions, q_out=None, k_out=None, 
         if T is not None and (Tk != T or dt != types):
             raise ValueError(f"k: {k.dtype} with {Tk} tokens, expected q's {q.dtype} with {T}")
         T = Tk
+    if not _int32(T):
+        raise ValueError(f"head_norm_rotary: {T} tokens")
     step = 0
     if plan.rotary_dim:
         shape = (T,) if plan.axes == 1 and positions.ndim == 1 else (plan.axes, T)
@@ -898,10 +916,9 @@ def head_norm_rotary(plan: HeadRotary, q, k, positions, q_out=None, k_out=None, 
 def kv4_fork_workspace(cache: Kv4Cache, batch: int, table_width: int, batch_before=None, stream=None):
     """A workspace for kv4_fork calls to `batch` sequences from `batch_before` (default:
     as many) with tables of this width, or less of each, that do not overlap in time."""
-    try:
-        n = lib.kv4_fork_workspace(cache._ref, batch if batch_before is None else batch_before, batch, table_width)
-    except C.ArgumentError:
-        n = -1
+    if batch_before is None:
+        batch_before = batch
+    n = lib.kv4_fork_workspace(cache._ref, batch_before, batch, table_width) if _int32(batch_before, batch, table_width) else -1
     if n < 0:
         raise ValueError(f"kv4_fork: sizes refused ({batch_before} to {batch} sequences, tables of {table_width} entries)")
     return _kv4_new(cache, (n,), cache.data.dtype, stream)
@@ -928,7 +945,7 @@ def kv4_fork(cache: Kv4Cache, refs, block_table, lens, parents, reserve=None, ou
             continue
         if t.dtype is not i32 or t.get_device() != dev or t.shape != shape or not t.is_contiguous():
             _need(t, what, i32, shape, cache.device)
-    if min(B, W, N) < 1:
+    if min(B, W, N) < 1 or not _int32(B, W, N):
         raise ValueError(f"block_table: shape {(B, W)}, {N} parents")
     if out is None:
         out = tuple(_kv4_new(cache, shape, i32, stream) for shape in ((N, W), (N,), (cache.n_pages,)))
@@ -949,6 +966,82 @@ def kv4_fork(cache: Kv4Cache, refs, block_table, lens, parents, reserve=None, ou
     return table_out, lens_out, refs_out
 
 
+def kv4_attention_shared_workspace(cache: Kv4Cache, batch: int, groups: int, total_q: int, n_heads: int, max_q: int,
+                                   max_shared: int, max_own: int, max_group_q=None, stream=None):
+    """A workspace for kv4_attention_shared calls of these sizes (or any that need no
+    more) that do not overlap in time."""
+    import torch
+    try:
+        a = _KV4_ATTN.pack(batch, 1, total_q, max_q, 0, n_heads, 0, 1, 0, 0, 1.0, 0, 0, 0, 0, 0, 0, 0, 0, 0, 0, 0)
+        g = _KV4_GROUPS.pack(groups, max_shared, max_own, total_q if max_group_q is None else max_group_q, 0, 0, 0)
+        n = lib.kv4_attention_shared_workspace(cache._ref, a, g)
+    except struct.error:
+        n = -1
+    if n < 0:
+        raise ValueError(f"kv4_attention_shared: sizes refused (batch {batch} in {groups} groups, {total_q} queries, "
+                         f"{n_heads} heads over {cache.n_kv_heads}, max_q {max_q}, max_shared {max_shared}, max_own "
+                         f"{max_own}, max_group_q {max_group_q})")
+    w = _kv4_new(cache, (n,), cache.data.dtype, stream)
+    with torch.cuda.stream(stream):
+        w[:4 * KV4_COUNTERS].zero_()
+    return w
+
+
+def kv4_attention_shared(cache: Kv4Cache, q, block_table, kv_lens, cu_q, cu_groups, shared, max_q: int, max_shared: int,
+                         max_own: int, max_group_q=None, scale=None, causal: bool = True, out=None, lse=None,
+                         workspace=None, stream=None):
+    """kv4_attention for sequences that have their first tokens in common: group g is
+    sequences cu_groups[g] .. cu_groups[g+1] (int32 [groups + 1]), and its first shared[g]
+    tokens (int32 [groups]) are read once for all of them, from the pages that the
+    block table's row of its first sequence names. Queries stand behind the shared
+    tokens. max_shared: no group shares more tokens; max_own: no sequence holds more
+    beyond them; max_group_q: no group has more queries in all (default: any number).
+    The rest is as for kv4_attention, without windows; workspace: from
+    kv4_attention_shared_workspace."""
+    B, W = _kv4_index(cache, block_table, kv_lens, cu_q)
+    if getattr(shared, "ndim", 0) != 1 or shared.shape[0] < 1:
+        raise ValueError("shared: expected a 1-D torch tensor, a number for each group")
+    n = shared.shape[0]
+    i32, dev = cache._i32, cache.index
+    if not (shared.dtype is i32 and cu_groups.dtype is i32 and shared.get_device() == dev and
+            cu_groups.get_device() == dev and shared.is_contiguous() and cu_groups.is_contiguous() and
+            cu_groups.shape == (n + 1,)):
+        _need(shared, "shared", i32, (n,), cache.device)
+        _need(cu_groups, "cu_groups", i32, (n + 1,), cache.device)
+    H = q.shape[1] if getattr(q, "ndim", 0) == 3 else 0
+    if H < 1 or H % cache.n_kv_heads:
+        raise ValueError(f"q: shape {tuple(getattr(q, 'shape', ()))}, expected (queries, a multiple of "
+                         f"{cache.n_kv_heads}, {cache.head_dim})")
+    T, ts, hs = _kv4_rows(q, "q", H, cache)
+    D, dtype = cache.head_dim, q.dtype
+    dt = _kv4_dtype(dtype, "q", 1)
+    if out is None:
+        out = _kv4_new(cache, (T, H, D), dtype, stream)
+    else:
+        _need(out, "out", dtype, (T, H, D), cache.device)
+    if lse is not None:
+        import torch
+        _need(lse, "lse", torch.float32, (T, H), cache.device)
+    if workspace is None:
+        workspace = kv4_attention_shared_workspace(cache, B, n, T, H, max_q, max_shared, max_own, max_group_q, stream)
+    elif workspace.dtype is not cache.data.dtype or workspace.get_device() != dev or not workspace.is_contiguous():
+        raise ValueError("workspace: expected a contiguous uint8 tensor on the cache's device")
+    try:
+        a = _KV4_ATTN.pack(B, W, T, max_q, 0, H, dt, 1 if causal else 0, 0, 0, D ** -0.5 if scale is None else scale, 0,
+                           block_table.data_ptr(), kv_lens.data_ptr(), cu_q.data_ptr(), q.data_ptr(), ts, hs,
+                           out.data_ptr(), 0 if lse is None else lse.data_ptr(), workspace.data_ptr(),
+                           workspace.numel())
+        g = _KV4_GROUPS.pack(n, max_shared, max_own, T if max_group_q is None else max_group_q, cu_groups.data_ptr(),
+                             shared.data_ptr(), 0)
+    except struct.error as e:
+        raise ValueError(f"kv4_attention_shared: max_q {max_q}, max_shared {max_shared}, max_own {max_own}, "
+                         f"max_group_q {max_group_q}: {e}") from None
+    st = _on_device(dev, lib.kv4_attention_shared, cache._ref, a, g, _kv4_stream(cache, stream))
+    if st:
+        _check(st, "kv4_attention_shared")
+    return out
+
+
 class TokenLogprobs(typing.NamedTuple):
     """What token_logprobs returns; None for what was not asked for."""
     logprob: object        # float32 [rows], of the given tokens
@@ -963,10 +1056,7 @@ def token_logprobs_workspace(rows: int, vocab: int, top: int = 0, device="cuda",
     """A workspace for token_logprobs calls of these sizes (or any that need no
     more) that do not overlap in time."""
     import torch
-    try:
-        n = lib.token_logprobs_workspace(rows, vocab, top)
-    except C.ArgumentError:
-        n = -1
+    n = lib.token_logprobs_workspace(rows, vocab, top) if _int32(rows, vocab, top) else -1
     if n < 0:
         raise ValueError(f"token_logprobs: sizes refused ({rows} rows of {vocab} logits, top {top})")
     with torch.cuda.stream(stream):
@@ -999,6 +1089,8 @@ def token_logprobs(logits, tokens=None, top: int = 0, out=None, workspace=None, 
         if tokens.shape != (M,) or not tokens.is_contiguous() or tokens.get_device() != dev:
             _need(tokens, "tokens", tokens.dtype, (M,), logits.device)
         size = tokens.itemsize
+    if not _int32(M, V):
+        raise ValueError(f"logits: shape {(M, V)}")
     if not 0 <= top <= min(LOGPROBS_MAX_TOP, V):
         raise ValueError(f"top: {top}, expected 0..{min(LOGPROBS_MAX_TOP, V)}")
     kinds = ((torch.float32, (M,), size), (torch.int32, (M,), size), (torch.float32, (M,), 1), (torch.float32, (M,), 1),

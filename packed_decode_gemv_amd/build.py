@@ -33,7 +33,7 @@ COMMON = [
 # Sources whose arithmetic decides integers are built without FMA contraction.
 EXACT = {"pack.hip", "verify.hip", "kv4.hip"}
 SOURCES = ["api.cpp", "pack.hip", "gemv.hip", "verify.hip", "gemm.hip", "kv4.hip", "kvattn.hip",
-           "kvfork.hip", "heads.hip", "logprobs.hip"]
+           "kvshared.hip", "kvfork.hip", "heads.hip", "logprobs.hip"]
 
 
 def _compile(src: str) -> str:

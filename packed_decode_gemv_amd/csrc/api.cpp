@@ -183,46 +183,133 @@ int64_t kv4_attention_workspace(const vbq_kv4* cache, const vbq_kv4_attn* a) {
   return check_attn(cache, a, false, &c, &p, &bytes) == VBQ_OK ? bytes : -1;
 }
 
-vbq_status kv4_attention(const vbq_kv4* cache, const vbq_kv4_attn* a, hipStream_t stream) {
-  KvAttn k;
-  KvAttnPlan p;
-  int64_t bytes = 0;
-  vbq_status st = check_attn(cache, a, true, &k.cache, &p, &bytes);
-  if (st != VBQ_OK) return st;
+// What a launch takes from the call's arguments alone.
+static void fill_attn(const vbq_kv4* cache, const vbq_kv4_attn* a, KvAttn* k) {
+  *k = KvAttn{k->cache};
+  k->table = a->table;
+  k->lens = a->kv_lens;
+  k->cu = a->cu_q;
+  k->q = static_cast<const uint16_t*>(a->q);
+  k->q_ts = a->q_token_stride;
+  k->q_hs = a->q_head_stride;
+  k->out = static_cast<uint16_t*>(a->out);
+  k->lse = a->lse;
+  k->counters = static_cast<uint32_t*>(a->workspace);
+  k->acc = static_cast<float*>(a->workspace) + VBQ_KV4_COUNTERS;
+  k->width = a->table_width;
+  k->total_q = a->total_q;
+  k->max_q = a->max_q;
+  k->max_kv = a->max_kv;
+  k->n_heads = a->n_heads;
+  k->ratio = a->n_heads / cache->n_kv_heads;
+  k->bf16 = a->dtype == VBQ_BF16;
+  k->causal = a->causal;
+  k->window = a->window;
+  k->sinks = a->window ? a->sinks : 0;
+  k->ratio_inv = (65536 + k->ratio - 1) / k->ratio;
+  k->batch = a->batch;
+  k->scale_log2 = a->scale * kLog2e;
+}
+static vbq_status check_attn_buffers(const vbq_kv4_attn* a, int64_t bytes) {
   if (!a->table || !a->kv_lens || !a->cu_q || (bytes > 0 && !a->workspace)) return VBQ_ERR_INVALID_ARG;
   if (!aligned(a->table, 4) || !aligned(a->kv_lens, 4) || !aligned(a->cu_q, 4) || !aligned(a->workspace, 16) ||
       !aligned(a->lse, 4) || !aligned(a->q, 16) || !aligned(a->out, 16) || a->q_token_stride % 8 ||
       a->q_head_stride % 8)
     return VBQ_ERR_ALIGNMENT;
-  if (a->workspace_bytes < bytes) return VBQ_ERR_CAPACITY;
+  return a->workspace_bytes < bytes ? VBQ_ERR_CAPACITY : VBQ_OK;
+}
+
+vbq_status kv4_attention(const vbq_kv4* cache, const vbq_kv4_attn* a, hipStream_t stream) {
+  KvAttn k;
+  KvAttnPlan p;
+  int64_t bytes = 0;
+  vbq_status st = check_attn(cache, a, true, &k.cache, &p, &bytes);
+  if (st == VBQ_OK) st = check_attn_buffers(a, bytes);
+  if (st != VBQ_OK) return st;
   if (a->total_q == 0 || a->max_q == 0) return VBQ_OK;
   if (!a->q || !a->out) return VBQ_ERR_INVALID_ARG;
-  k.table = a->table;
-  k.lens = a->kv_lens;
-  k.cu = a->cu_q;
-  k.q = static_cast<const uint16_t*>(a->q);
-  k.q_ts = a->q_token_stride;
-  k.q_hs = a->q_head_stride;
-  k.out = static_cast<uint16_t*>(a->out);
-  k.lse = a->lse;
-  k.counters = static_cast<uint32_t*>(a->workspace);
-  k.acc = static_cast<float*>(a->workspace) + VBQ_KV4_COUNTERS;
+  fill_attn(cache, a, &k);
   k.ml = k.acc + p.places * p.rows * cache->head_dim;
-  k.width = a->table_width;
-  k.total_q = a->total_q;
-  k.max_q = a->max_q;
-  k.max_kv = a->max_kv;
-  k.n_heads = a->n_heads;
-  k.ratio = a->n_heads / cache->n_kv_heads;
-  k.bf16 = a->dtype == VBQ_BF16;
-  k.causal = a->causal;
-  k.window = a->window;
-  k.sinks = a->window ? a->sinks : 0;
-  k.ratio_inv = (65536 + k.ratio - 1) / k.ratio;
-  k.batch = a->batch;
   k.parts = p.parts;
-  k.scale_log2 = a->scale * kLog2e;
   return from_hip(launch_kv4_attention(k, p, stream));
+}
+
+// Plans of the two launches of attention with shared tokens, and its workspace: counters,
+// the sums of shared tokens, then what either launch needs for its parts.
+struct SharedPlan {
+  KvAttnPlan shared, own;
+  int64_t pre, pre_ml, acc, bytes;   // (in floats from the workspace's start; bytes in all)
+  int32_t max_shared, max_own;       // whole blocks, and what rounding leaves to the sequences
+};
+static vbq_status check_shared(const vbq_kv4* cache, const vbq_kv4_attn* a, const vbq_kv4_groups* g, bool pointers,
+                               KvCache* c, SharedPlan* p) {
+  if (!a || !g || g->reserved != 0) return VBQ_ERR_INVALID_ARG;
+  if (g->n_groups < 1 || g->max_shared < 0 || g->max_own < 0 || g->max_group_q < 0) return VBQ_ERR_SHAPE;
+  if (g->n_groups > 65535) return VBQ_ERR_UNSUPPORTED;
+  if (a->window != 0 || a->sinks != 0) return VBQ_ERR_INVALID_ARG;
+  if (g->max_own > INT32_MAX - 64 - kKvBlock || g->max_shared > INT32_MAX - 64) return VBQ_ERR_UNSUPPORTED;
+  p->max_shared = g->max_shared / kKvBlock * kKvBlock;
+  p->max_own = g->max_own + (g->max_shared ? kKvBlock - 1 : 0);
+  vbq_kv4_attn part = *a;
+  part.max_kv = p->max_own;
+  int64_t bytes = 0;
+  vbq_status st = check_attn(cache, &part, pointers, c, &p->own, &bytes);
+  if (st != VBQ_OK) return st;
+  part.batch = g->n_groups;
+  part.max_q = std::min(g->max_group_q, a->total_q);
+  part.max_kv = p->max_shared;
+  part.causal = 0;
+  st = check_attn(cache, &part, pointers, c, &p->shared, &bytes);
+  if (st != VBQ_OK) return st;
+  const int64_t rows = p->max_shared ? (int64_t)a->total_q * a->n_heads : 0;
+  const auto floats = [&](const KvAttnPlan& q) { return q.places * q.rows * (cache->head_dim + 2); };
+  p->pre = VBQ_KV4_COUNTERS;
+  p->pre_ml = p->pre + rows * cache->head_dim;
+  p->acc = (p->pre_ml + 2 * rows + 3) & ~(int64_t)3;
+  p->bytes = 4 * (p->acc + std::max(floats(p->own), floats(p->shared)));
+  return VBQ_OK;
+}
+
+int64_t kv4_attention_shared_workspace(const vbq_kv4* cache, const vbq_kv4_attn* a, const vbq_kv4_groups* g) {
+  KvCache c;
+  SharedPlan p;
+  return check_shared(cache, a, g, false, &c, &p) == VBQ_OK ? p.bytes : -1;
+}
+
+vbq_status kv4_attention_shared(const vbq_kv4* cache, const vbq_kv4_attn* a, const vbq_kv4_groups* g,
+                                hipStream_t stream) {
+  KvAttn own;
+  SharedPlan p;
+  vbq_status st = check_shared(cache, a, g, true, &own.cache, &p);
+  if (st != VBQ_OK) return st;
+  if (!g->cu_groups || !g->shared) return VBQ_ERR_INVALID_ARG;
+  if (!aligned(g->cu_groups, 4) || !aligned(g->shared, 4)) return VBQ_ERR_ALIGNMENT;
+  st = check_attn_buffers(a, p.bytes);
+  if (st != VBQ_OK) return st;
+  if (a->total_q == 0 || a->max_q == 0) return VBQ_OK;
+  if (!a->q || !a->out) return VBQ_ERR_INVALID_ARG;
+  fill_attn(cache, a, &own);
+  float* const w = static_cast<float*>(a->workspace);
+  own.groups = g->cu_groups;
+  own.shared = g->shared;
+  own.n_groups = g->n_groups;
+  own.sequences = a->batch;
+  own.max_shared = g->max_shared;
+  own.max_group_q = g->max_group_q;
+  own.pre = w + p.pre;
+  own.pre_ml = w + p.pre_ml;
+  own.acc = w + p.acc;
+  KvAttn shared = own;
+  own.max_kv = p.max_own;
+  own.parts = p.own.parts;
+  own.ml = own.acc + p.own.places * p.own.rows * cache->head_dim;
+  shared.batch = g->n_groups;
+  shared.max_q = std::min(g->max_group_q, a->total_q);
+  shared.max_kv = p.max_shared;
+  shared.causal = 0;
+  shared.parts = p.shared.parts;
+  shared.ml = shared.acc + p.shared.places * p.shared.rows * cache->head_dim;
+  return from_hip(launch_kv4_attention_shared(shared, p.shared, own, p.own, stream));
 }
 
 static vbq_status check_rows(const vbq_head_rows* r, const float* weight, HeadRows* out) {

@@ -61,6 +61,13 @@ struct KvAttn {
   int32_t parts;               // up to 32 rows: that long tiles are cut into in all, about (0: no cuts, a
                                // workgroup a tile); more rows: that each tile is cut into, at most
   float scale_log2;            // scale * log2(e)
+  // With shared tokens (see Part in kvattn_kernels.h); batch, max_q and max_kv are then those
+  // of a launch: groups with their rows and shared tokens, or sequences with their own.
+  const int32_t* groups;       // [n_groups + 1] sequences before each
+  const int32_t* shared;       // [n_groups] tokens
+  float* pre;                  // sums over shared tokens: [total_q][n_heads][head_dim]
+  float* pre_ml;               // their bases and sums of p
+  int32_t n_groups, sequences, max_shared, max_group_q;
 };
 
 // A fork (see kvfork.hip): the call's arguments, and places in its workspace.
@@ -99,5 +106,7 @@ struct KvAttnPlan {
 KvAttnPlan kv4_attn_plan(int batch, int heads, int ratio, int groups, int total_q, int max_q, int max_kv, int window,
                          int sinks);
 hipError_t launch_kv4_attention(const KvAttn& a, const KvAttnPlan& p, hipStream_t s);
+hipError_t launch_kv4_attention_shared(const KvAttn& shared, const KvAttnPlan& sp, const KvAttn& own,
+                                       const KvAttnPlan& op, hipStream_t s);
 
 }  // namespace vbq
