@@ -5,13 +5,12 @@
 
 namespace vbq {
 
-constexpr int kLogprobSteps = 4;     // (see k_token_logprobs) wavefronts of a workgroup
-constexpr int kLogprobStep = 2048;   // logits of one step of a wavefront
+constexpr int kLogprobStep = 1024;   // logits of one step of a wavefront
 constexpr int kLogprobSplits = 32;   // workgroups that share a row, at most
 
 // What a workgroup leaves of its part of a row, beside its best keys.
 struct LogprobPart {
-  float m, s, t;     // maximum, sum of e = exp(x - m), sum of e (x - m)
+  float m, s, t;     // maximum, sum of e = exp(x - m), sum of e log2(e)
   int32_t before;    // logits that stand before the given token's
 };
 
