@@ -549,7 +549,8 @@ vbq_status kv4_fork(const vbq_kv4* cache, const vbq_kv4_fork* f, hipStream_t str
  * A sequence for whose group or itself numbers do not fit is left out (FLAG_LENGTH).
  * The arithmetic is kv4_attention's, with the rows of a group together in place of a
  * sequence's for the shared tokens; sums of both kinds are joined in fp32.
- * workspace: as for kv4_attention, of kv4_attention_shared_workspace() bytes. */
+ * workspace: as for kv4_attention, of kv4_attention_shared_workspace() bytes, the first
+ * 8 * VBQ_KV4_COUNTERS of them zero before the first call that uses it. */
 typedef struct vbq_kv4_groups {
   int32_t n_groups;       /* 1 .. 65535 */
   int32_t max_shared;     /* no group shares more tokens than this */

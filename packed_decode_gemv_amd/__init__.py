@@ -983,7 +983,7 @@ def kv4_attention_shared_workspace(cache: Kv4Cache, batch: int, groups: int, tot
                          f"{max_own}, max_group_q {max_group_q})")
     w = _kv4_new(cache, (n,), cache.data.dtype, stream)
     with torch.cuda.stream(stream):
-        w[:4 * KV4_COUNTERS].zero_()
+        w[:8 * KV4_COUNTERS].zero_()
     return w
 
 

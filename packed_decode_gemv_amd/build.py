@@ -32,8 +32,8 @@ COMMON = [
 ]
 # Sources whose arithmetic decides integers are built without FMA contraction.
 EXACT = {"pack.hip", "verify.hip", "kv4.hip"}
-SOURCES = ["api.cpp", "pack.hip", "gemv.hip", "verify.hip", "gemm.hip", "kv4.hip", "kvattn.hip",
-           "kvshared.hip", "kvfork.hip", "heads.hip", "logprobs.hip"]
+SOURCES = ["api.cpp", "pack.hip", "gemv.hip", "verify.hip", "gemm.hip", "kv4.hip", "kvattn.hip", "kvfork.hip",
+           "heads.hip", "logprobs.hip", "kvshared_g1.hip", "kvshared_g2.hip", "kvshared_g3.hip", "kvshared_g4.hip"]
 
 
 def _compile(src: str) -> str:

@@ -234,11 +234,12 @@ vbq_status kv4_attention(const vbq_kv4* cache, const vbq_kv4_attn* a, hipStream_
   return from_hip(launch_kv4_attention(k, p, stream));
 }
 
-// Plans of the two launches of attention with shared tokens, and its workspace: counters,
-// the sums of shared tokens, then what either launch needs for its parts.
+// Plans of the workgroups over shared and own tokens, and places in the workspace (in
+// floats from its start): two sets of counters, a row's sums of own tokens, and of
+// shared ones where few rows share them, then what either kind needs for its parts.
 struct SharedPlan {
   KvAttnPlan shared, own;
-  int64_t pre, pre_ml, acc, bytes;   // (in floats from the workspace's start; bytes in all)
+  int64_t own_sums, own_ml, sums, ml, own_acc, own_acc_ml, acc, acc_ml, bytes;
   int32_t max_shared, max_own;       // whole blocks, and what rounding leaves to the sequences
 };
 static vbq_status check_shared(const vbq_kv4* cache, const vbq_kv4_attn* a, const vbq_kv4_groups* g, bool pointers,
@@ -261,12 +262,26 @@ static vbq_status check_shared(const vbq_kv4* cache, const vbq_kv4_attn* a, cons
   part.causal = 0;
   st = check_attn(cache, &part, pointers, c, &p->shared, &bytes);
   if (st != VBQ_OK) return st;
-  const int64_t rows = p->max_shared ? (int64_t)a->total_q * a->n_heads : 0;
-  const auto floats = [&](const KvAttnPlan& q) { return q.places * q.rows * (cache->head_dim + 2); };
-  p->pre = VBQ_KV4_COUNTERS;
-  p->pre_ml = p->pre + rows * cache->head_dim;
-  p->acc = (p->pre_ml + 2 * rows + 3) & ~(int64_t)3;
-  p->bytes = 4 * (p->acc + std::max(floats(p->own), floats(p->shared)));
+  if (!kv_grid_fits(p->shared.grid * std::max(p->shared.parts, 1) + p->own.grid, 256)) return VBQ_ERR_UNSUPPORTED;
+  const bool tile = p->shared.rows == 128;
+  if (p->shared.rows < 8) p->shared.rows = 8;   // (tiles of 4 rows have no kernel of their own here)
+  if (tile) p->shared.places = p->max_shared ? p->shared.grid * p->shared.parts : 0;   // (one part too)
+  const int64_t rows = p->max_shared ? (int64_t)a->total_q * a->n_heads : 0, D = cache->head_dim;
+  int64_t at = 2 * VBQ_KV4_COUNTERS;
+  const auto take = [&](int64_t n) {
+    const int64_t from = at;
+    at = (at + n + 3) & ~(int64_t)3;
+    return from;
+  };
+  p->own_sums = take(rows * D);
+  p->own_ml = take(rows * 2);
+  p->sums = take(tile ? 0 : rows * D);
+  p->ml = take(tile ? 0 : rows * 2);
+  p->own_acc = take(p->own.places * p->own.rows * D);
+  p->own_acc_ml = take(p->own.places * p->own.rows * 2);
+  p->acc = take(p->shared.places * p->shared.rows * D);
+  p->acc_ml = take(p->shared.places * p->shared.rows * 2);
+  p->bytes = 4 * at;
   return VBQ_OK;
 }
 
@@ -296,20 +311,29 @@ vbq_status kv4_attention_shared(const vbq_kv4* cache, const vbq_kv4_attn* a, con
   own.sequences = a->batch;
   own.max_shared = g->max_shared;
   own.max_group_q = g->max_group_q;
-  own.pre = w + p.pre;
-  own.pre_ml = w + p.pre_ml;
-  own.acc = w + p.acc;
   KvAttn shared = own;
   own.max_kv = p.max_own;
   own.parts = p.own.parts;
-  own.ml = own.acc + p.own.places * p.own.rows * cache->head_dim;
+  own.sums = w + p.own_sums;
+  own.sums_ml = w + p.own_ml;
+  own.acc = w + p.own_acc;
+  own.ml = w + p.own_acc_ml;
+  shared.counters = own.counters + VBQ_KV4_COUNTERS;
   shared.batch = g->n_groups;
   shared.max_q = std::min(g->max_group_q, a->total_q);
   shared.max_kv = p.max_shared;
   shared.causal = 0;
   shared.parts = p.shared.parts;
-  shared.ml = shared.acc + p.shared.places * p.shared.rows * cache->head_dim;
-  return from_hip(launch_kv4_attention_shared(shared, p.shared, own, p.own, stream));
+  shared.sums = w + p.sums;
+  shared.sums_ml = w + p.ml;
+  shared.acc = w + p.acc;
+  shared.ml = w + p.acc_ml;
+  switch (own.cache.groups) {
+    case 1: return from_hip(launch_kv4_attention_shared_g1(shared, p.shared, own, p.own, stream));
+    case 2: return from_hip(launch_kv4_attention_shared_g2(shared, p.shared, own, p.own, stream));
+    case 3: return from_hip(launch_kv4_attention_shared_g3(shared, p.shared, own, p.own, stream));
+    default: return from_hip(launch_kv4_attention_shared_g4(shared, p.shared, own, p.own, stream));
+  }
 }
 
 static vbq_status check_rows(const vbq_head_rows* r, const float* weight, HeadRows* out) {

@@ -65,8 +65,8 @@ struct KvAttn {
   // of a launch: groups with their rows and shared tokens, or sequences with their own.
   const int32_t* groups;       // [n_groups + 1] sequences before each
   const int32_t* shared;       // [n_groups] tokens
-  float* pre;                  // sums over shared tokens: [total_q][n_heads][head_dim]
-  float* pre_ml;               // their bases and sums of p
+  float* sums;                 // of a launch's rows: [total_q][n_heads][head_dim]
+  float* sums_ml;              // their bases and sums of p
   int32_t n_groups, sequences, max_shared, max_group_q;
 };
 
@@ -106,7 +106,14 @@ struct KvAttnPlan {
 KvAttnPlan kv4_attn_plan(int batch, int heads, int ratio, int groups, int total_q, int max_q, int max_kv, int window,
                          int sinks);
 hipError_t launch_kv4_attention(const KvAttn& a, const KvAttnPlan& p, hipStream_t s);
-hipError_t launch_kv4_attention_shared(const KvAttn& shared, const KvAttnPlan& sp, const KvAttn& own,
-                                       const KvAttnPlan& op, hipStream_t s);
+// (see kvshared.h) for heads of 64, 128, 192 and 256 channels.
+hipError_t launch_kv4_attention_shared_g1(const KvAttn& shared, const KvAttnPlan& sp, const KvAttn& own,
+                                          const KvAttnPlan& op, hipStream_t s);
+hipError_t launch_kv4_attention_shared_g2(const KvAttn& shared, const KvAttnPlan& sp, const KvAttn& own,
+                                          const KvAttnPlan& op, hipStream_t s);
+hipError_t launch_kv4_attention_shared_g3(const KvAttn& shared, const KvAttnPlan& sp, const KvAttn& own,
+                                          const KvAttnPlan& op, hipStream_t s);
+hipError_t launch_kv4_attention_shared_g4(const KvAttn& shared, const KvAttnPlan& sp, const KvAttn& own,
+                                          const KvAttnPlan& op, hipStream_t s);
 
 }  // namespace vbq

@@ -265,8 +265,8 @@ __device__ inline f32x2 get2(const float* p) {
 
 // Whose tokens a launch takes: kAll, a sequence's; for attention with shared tokens
 // kShared, those that a group of sequences has in common (whole blocks), for the rows
-// of all of them, whose sums stay in the workspace; kOwn, a sequence's others, joined
-// with those sums.
+// of all of them; kOwn, a sequence's others. The sums of both stay in the workspace and
+// are joined afterwards (see kvshared.h).
 enum Part { kAll, kShared, kOwn };
 
 // A sequence of the call as the kernels see it (kShared: a group).
@@ -309,6 +309,16 @@ __device__ inline bool group_from(const KvAttn& a, int g, Group& r) {
   r.c1 = a.cu[r.g1];
   return r.c0 >= 0 && r.c1 >= r.c0 && r.c1 <= a.total_q && r.c1 - r.c0 <= a.max_group_q;
 }
+// The last group that begins at or before sequence b, or the first.
+__device__ inline int group_of(const KvAttn& a, int b) {
+  int lo = 0, hi = a.n_groups;
+  while (hi - lo > 1) {
+    const int mid = (lo + hi) >> 1;
+    if (a.groups[mid] <= b) lo = mid;
+    else hi = mid;
+  }
+  return lo;
+}
 // A sequence (a group) by its number; false, and nothing to do, for numbers that do
 // not fit.
 template <Part PART>
@@ -333,13 +343,7 @@ __device__ inline bool seq_at(const KvAttn& a, int b, Seq& s) {
       return true;
     } else {
       const int32_t c0 = a.cu[b], c1 = a.cu[b + 1], len = a.lens[b];
-      int lo = 0, hi = a.n_groups;   // the last group that begins at or before b
-      while (hi - lo > 1) {
-        const int mid = (lo + hi) >> 1;
-        if (a.groups[mid] <= b) lo = mid;
-        else hi = mid;
-      }
-      const bool fits = group_from(a, lo, g), in = b >= g.g0 && b < g.g1;   // (or of no group)
+      const bool fits = group_from(a, group_of(a, b), g), in = b >= g.g0 && b < g.g1;   // (or of no group)
       if (in && !fits) return false;
       const int32_t shared = in ? g.shared : 0, from = shared & ~(kKvBlock - 1);
       const int64_t nq = (int64_t)c1 - c0;
@@ -363,34 +367,41 @@ __device__ inline bool seq_at(const KvAttn& a, int b, Seq& s) {
 // Query of row r < 32 (up to 32 heads share a key/value head in the few-row kernel).
 __device__ inline int query_of(const KvAttn& a, int r) { return (r * a.ratio_inv) >> 16; }
 
+// Rows of a sequence that seq_at<kOwn> refuses, where they are a group's with shared
+// tokens: r0 .. r1 - 1 (sums of shared tokens wait for them).
+__device__ inline bool left_out(const KvAttn& a, int b, int& r0, int& r1) {
+  Group g;
+  const int at = group_of(a, b);
+  if (!group_from(a, at, g) || b < g.g0 || b >= g.g1 || g.shared < kKvBlock) return false;
+  r0 = max(a.cu[b], g.c0);
+  r1 = min(a.cu[b + 1], g.c1);
+  return r0 < r1;
+}
+constexpr float kLeftOut = -1.f;   // in place of a row's sum of p: it is not written
+
 // Four channels of output row o (sums v and of p, held times 2^base) and, once a
-// row, the log of the sum of exponentials. kShared: the sums themselves, for the
-// launch that comes after; kOwn: joined with those (where `more`).
-template <int D, Part PART>
-__device__ inline void answer_row(const KvAttn& a, int64_t o, int c, f32x4 v, float sum, float base, bool more) {
-  if constexpr (PART == kShared) {
-    *reinterpret_cast<f32x4*>(a.pre + o * D + 4 * c) = v;
-    if (c == 0) *reinterpret_cast<f32x2*>(a.pre_ml + 2 * o) = f32x2{base, sum};
-    return;
-  }
-  if constexpr (PART == kOwn) {
-    if (more) {
-      const f32x2 x = *reinterpret_cast<const f32x2*>(a.pre_ml + 2 * o);
-      const float low = fminf(base, x.x), f = __builtin_amdgcn_exp2f(low - base), g = __builtin_amdgcn_exp2f(low - x.x);
-      v = v * f + *reinterpret_cast<const f32x4*>(a.pre + o * D + 4 * c) * g;
-      sum = __builtin_fmaf(sum, f, x.y * g);
-      base = low;
-    }
-  }
+// row, the log of the sum of exponentials. kShared, and kOwn where a group has shared
+// tokens (`more`): the sums themselves.
+template <int D>
+__device__ inline void answer_row(const KvAttn& a, int64_t o, int c, const f32x4& v, float sum, float base) {
   const float inv = sum > 0.f ? 1.f / sum : sum == 0.f ? 0.f : sum;   // 0: nothing seen; NaN stays
   store4(a, o * D + 4 * c, v * inv);
   if (a.lse && c == 0) a.lse[o] = (__builtin_amdgcn_logf(sum) - base) * kLn2;
 }
 template <int D, Part PART>
+__device__ inline void answer_part(const KvAttn& a, int64_t o, int c, const f32x4& v, float sum, float base, bool more) {
+  if (PART == kShared || (PART == kOwn && more)) {
+    *reinterpret_cast<f32x4*>(a.sums + o * D + 4 * c) = v;
+    if (c == 0) *reinterpret_cast<f32x2*>(a.sums_ml + 2 * o) = f32x2{base, sum};
+  } else {
+    answer_row<D>(a, o, c, v, sum, base);
+  }
+}
+template <int D, Part PART>
 __device__ inline void answer4(const KvAttn& a, int c0, int head, int r, int c, const f32x4& v, float sum, float base,
                                bool more) {
   const int qi = query_of(a, r), hh = r - qi * a.ratio;
-  answer_row<D, PART>(a, (int64_t)(c0 + qi) * a.n_heads + head * a.ratio + hh, c, v, sum, base, more);
+  answer_part<D, PART>(a, (int64_t)(c0 + qi) * a.n_heads + head * a.ratio + hh, c, v, sum, base, more);
 }
 
 // Work is a tile (sequence, head) or a part of one: tiles longer than `chunk`
@@ -411,7 +422,8 @@ __device__ inline void lanes_load(const KvAttn& a, uint32_t lane, int base, bool
   s.c0 = s.nq = s.len = s.blocks = s.row = 0;
   s.re = Reach{0, 0, 0};
   if (b < a.batch && !seq_at<PART>(a, b, s)) {
-    s.nq = 0;
+    s.nq = PART == kOwn ? -1 : 0;
+    s.blocks = 0;
     if (report) kv_flag(a.cache, VBQ_KV4_FLAG_LENGTH);
   }
   l.base = base;
@@ -435,17 +447,21 @@ template <int G, int ROWS>
 constexpr bool kRoomy = G <= 2 && ROWS <= 8;
 typedef uint16_t ushort2_t __attribute__((ext_vector_type(2)));
 
-template <int G, int ROWS, int STAGES, Part PART = kAll>
-__global__ __launch_bounds__((64 * kWaves<G, ROWS>), (kRoomy<G, ROWS>) ? 4 : G * ROWS > 64 ? 1 : 2) void k_kv4_attn(KvAttn a) {
-  constexpr int WAVES = kWaves<G, ROWS>, D = 64 * G, PITCH = D + 4, BYTES = kKvGroupBytes * G;
+// LDS of a workgroup: blocks; afterwards the wavefronts' sums, or the parts' factors and shares.
+template <int G, int ROWS, int STAGES, int WAVES>
+constexpr int few_rows_lds() {
+  constexpr int COLS = ROWS > 16 ? 16 : ROWS;
+  constexpr int RING = WAVES * STAGES * kKvGroupBytes * G, SUMS = WAVES * COLS * (64 * G + 4) * 4;
+  constexpr int JOIN = ROWS * kParts * 4 + 64 * WAVES * 16, AFTER = SUMS > JOIN ? SUMS : JOIN;
+  return RING > AFTER ? RING : AFTER;
+}
+// block: of `grid` in the launch.
+template <int G, int ROWS, int STAGES, Part PART, int WAVES>
+__device__ __forceinline__ void few_rows(const KvAttn& a, uint8_t* const ring, float (*const wml)[ROWS][2],
+                                         uint32_t* const last, const uint32_t block, const uint32_t grid) {
+  constexpr int D = 64 * G, PITCH = D + 4, BYTES = kKvGroupBytes * G;
   constexpr int NT = ROWS > 16 ? 2 : 1, COLS = ROWS > 16 ? 16 : ROWS;   // column tiles, and columns used of each
   constexpr int PARTS = 16 / COLS, PAIRS = 4 / PARTS;   // lanes that share a row's octet, token pairs of each
-  constexpr int RING = WAVES * STAGES * BYTES, SUMS = WAVES * COLS * PITCH * 4;
-  constexpr int JOIN = ROWS * kParts * 4 + 64 * WAVES * 16, AFTER = SUMS > JOIN ? SUMS : JOIN;
-  // blocks; afterwards the wavefronts' sums, or the parts' factors and shares
-  __shared__ __attribute__((aligned(16))) uint8_t ring[RING > AFTER ? RING : AFTER];
-  __shared__ float wml[WAVES][ROWS][2];
-  __shared__ uint32_t last;
   float* const buf = reinterpret_cast<float*>(ring);   // the wavefronts' sums, after a tile
   const uint32_t tid = threadIdx.x, lane = tid & 63u, col = lane & 15u, quarter = lane >> 4;
   const uint32_t qcol = col % COLS, part = col / COLS;
@@ -460,18 +476,27 @@ __global__ __launch_bounds__((64 * kWaves<G, ROWS>), (kRoomy<G, ROWS>) ? 4 : G *
     Lanes ln;
     int total = 0;
     for (int base = 0; base < a.batch; base += 64) {
-      lanes_load<PART>(a, lane, base, blockIdx.x == 0 && wave == 0, ln);
+      lanes_load<PART>(a, lane, base, block == 0 && wave == 0, ln);
       total += __builtin_amdgcn_readlane(wave_scan(ln.blocks), 63);
       // sequences that see nothing have no parts: their rows are answered here
       // (with shared tokens there are none: a query sees itself)
       for (uint64_t none = PART == kAll ? __ballot(ln.nq > 0 && ln.blocks == 0) : 0; none; none &= none - 1) {
         const int at = __builtin_ctzll(none);
-        if ((uint32_t)(base + at) % gridDim.x != blockIdx.x) continue;
+        if ((uint32_t)(base + at) % grid != block) continue;
         const int n = __builtin_amdgcn_readlane(ln.nq, at) * a.n_heads;
         const int64_t from = (int64_t)__builtin_amdgcn_readlane(ln.c0, at) * a.n_heads;
         for (int e = (int)tid; e < n * (D / 4); e += 64 * WAVES) store4(a, from * D + 4 * e, f32x4{0.f, 0.f, 0.f, 0.f});
         if (a.lse)
           for (int e = (int)tid; e < n; e += 64 * WAVES) a.lse[from + e] = -__builtin_inff();
+      }
+      if constexpr (PART == kOwn) {
+        for (uint64_t out = __ballot(ln.nq < 0); out; out &= out - 1) {
+          const int b = base + __builtin_ctzll(out);
+          int r0, r1;
+          if ((uint32_t)b % grid != block || !left_out(a, b, r0, r1)) continue;
+          for (int64_t e = (int64_t)r0 * a.n_heads + tid; e < (int64_t)r1 * a.n_heads; e += 64 * WAVES)
+            a.sums_ml[2 * e + 1] = kLeftOut;
+        }
       }
     }
     const int chunk = max((int)(((uint32_t)total * (uint32_t)a.cache.heads + (uint32_t)a.parts - 1u) / (uint32_t)a.parts),
@@ -485,7 +510,7 @@ __global__ __launch_bounds__((64 * kWaves<G, ROWS>), (kRoomy<G, ROWS>) ? 4 : G *
       size = n > 0 ? (int)((uint32_t)(ln.blocks + n - 1) / (uint32_t)n) : 1;   // nothing to see: no part
       n = (int)((uint32_t)(ln.blocks + size - 1) / (uint32_t)size);
       incl = before + wave_scan(n * a.cache.heads);
-      past = __ballot(incl > (int)blockIdx.x);
+      past = __ballot(incl > (int)block);
       if (past) break;
       if (base + 64 >= a.batch) return;
       before = __builtin_amdgcn_readlane(incl, 63);
@@ -500,17 +525,23 @@ __global__ __launch_bounds__((64 * kWaves<G, ROWS>), (kRoomy<G, ROWS>) ? 4 : G *
     re.ns = __builtin_amdgcn_readlane(ln.ns, at);
     re.w0 = __builtin_amdgcn_readlane(ln.w0, at);
     parts = __builtin_amdgcn_readlane(n, at);
-    const int rel = (int)blockIdx.x - (__builtin_amdgcn_readlane(incl, at) - parts * a.cache.heads);
+    const int rel = (int)block - (__builtin_amdgcn_readlane(incl, at) - parts * a.cache.heads);
     head = (int)((uint32_t)rel / (uint32_t)parts);
     part_no = rel - head * parts;
     i0 = part_no * __builtin_amdgcn_readlane(size, at);
     i1 = min(blocks, i0 + __builtin_amdgcn_readlane(size, at));
   } else {
-    b = (int)(blockIdx.x / (uint32_t)a.cache.heads);
-    head = (int)(blockIdx.x % (uint32_t)a.cache.heads);
+    b = (int)(block / (uint32_t)a.cache.heads);
+    head = (int)(block % (uint32_t)a.cache.heads);
     Seq sq;
     if (!seq_at<PART>(a, b, sq)) {
       if (tid == 0) kv_flag(a.cache, VBQ_KV4_FLAG_LENGTH);
+      if constexpr (PART == kOwn) {
+        int r0, r1;
+        if (left_out(a, b, r0, r1))
+          for (int64_t e = tid; e < (int64_t)(r1 - r0) * a.ratio; e += 64 * WAVES)
+            a.sums_ml[2 * ((r0 + e / a.ratio) * a.n_heads + head * a.ratio + e % a.ratio) + 1] = kLeftOut;
+      }
       return;
     }
     c0 = sq.c0, nq = sq.nq, len = sq.len, re = sq.re, blocks = sq.blocks, row = sq.row;
@@ -867,8 +898,8 @@ __global__ __launch_bounds__((64 * kWaves<G, ROWS>), (kRoomy<G, ROWS>) ? 4 : G *
     }
   }
   __syncthreads();
-  float* const slot = a.acc + (int64_t)blockIdx.x * ROWS * D;   // a part's sums, and their bases and sums of p
-  float* const slot_ml = a.ml + (int64_t)blockIdx.x * ROWS * 2;
+  float* const slot = a.acc + (int64_t)block * ROWS * D;   // a part's sums, and their bases and sums of p
+  float* const slot_ml = a.ml + (int64_t)block * ROWS * 2;
 #pragma unroll
   for (int nt = 0; nt < NT; ++nt) {
     if (16 * nt >= rows) break;
@@ -926,11 +957,11 @@ __global__ __launch_bounds__((64 * kWaves<G, ROWS>), (kRoomy<G, ROWS>) ? 4 : G *
   __builtin_amdgcn_s_waitcnt(VBQ_VMCNT_IMM(0));
   __syncthreads();
   if (tid == 0) {
-    last = __hip_atomic_fetch_add(counter, 1u, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT) == (uint32_t)(parts - 1);
-    if (last) __hip_atomic_store(counter, 0u, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
+    *last = __hip_atomic_fetch_add(counter, 1u, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT) == (uint32_t)(parts - 1);
+    if (*last) __hip_atomic_store(counter, 0u, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
   }
   __syncthreads();
-  if (!last) return;
+  if (!*last) return;
   const float* const acc0 = slot - (int64_t)part_no * ROWS * D;
   const float* const ml0 = slot_ml - (int64_t)part_no * ROWS * 2;
   float* const factor = buf;                                                 // [rows][kParts]
@@ -1021,6 +1052,15 @@ __global__ __launch_bounds__((64 * kWaves<G, ROWS>), (kRoomy<G, ROWS>) ? 4 : G *
     const int e = e0 + k * THREADS, row = e / (D / 4);
     if (e < ne && share_no == 0) answer4<D, PART>(a, c0, head, row, e % (D / 4), v[k], wml[0][row][1], wml[0][row][0], re.w0 > 0);
   }
+}
+
+template <int G, int ROWS, int STAGES, Part PART = kAll>
+__global__ __launch_bounds__((64 * kWaves<G, ROWS>), (kRoomy<G, ROWS>) ? 4 : G * ROWS > 64 ? 1 : 2) void k_kv4_attn(KvAttn a) {
+  constexpr int WAVES = kWaves<G, ROWS>;
+  __shared__ __attribute__((aligned(16))) uint8_t ring[few_rows_lds<G, ROWS, STAGES, WAVES>()];
+  __shared__ float wml[WAVES][ROWS][2];
+  __shared__ uint32_t last;
+  few_rows<G, ROWS, STAGES, PART, WAVES>(a, ring, wml, &last, blockIdx.x, gridDim.x);
 }
 
 // ---- many rows ---------------------------------------------------------------------
@@ -1142,15 +1182,21 @@ __device__ inline int part_blocks(const KvAttn& a, const Reach& re) {
   return max((int)((uint32_t)(re.ns + re.nw + a.parts - 1) / (uint32_t)a.parts), kLeastTilePart);
 }
 
-template <int G, bool FINE, Part PART = kAll>
-__global__ __launch_bounds__(256, G >= 4 ? 1 : 2) void k_kv4_attn_tile(KvAttn a) {
-  constexpr int WAVES = 4, ROWS = kRowTile, D = 64 * G, BYTES = kKvGroupBytes * G, RAW = 4, TILES = D / 32;
+// LDS of a workgroup: raw blocks, keys and values as operands.
+template <int G>
+struct TileLds {
+  static constexpr int RAW = 4, HELD = 32 * 64 * G * 2;   // blocks as copied; a block's keys, or values
+  static constexpr int kRaw = RAW * kKvGroupBytes * G, kKeys = 2 * HELD, kVals = 2 * HELD;
+};
+// Workgroup (bx, by) of the launch.
+template <int G, bool FINE, Part PART>
+__device__ __forceinline__ void tile_rows(const KvAttn& a, uint8_t* const raw, uint8_t* const keys, uint8_t* const vals,
+                                          const uint32_t bx, const uint32_t by) {
+  constexpr int WAVES = 4, ROWS = kRowTile, D = 64 * G, BYTES = kKvGroupBytes * G, RAW = TileLds<G>::RAW, TILES = D / 32;
   constexpr int SHARE = BYTES / WAVES;   // a wavefront's part of a block's copy
   constexpr int COPIES = (SHARE + 1023) / 1024;
-  constexpr int HELD = 32 * D * 2;   // a block's keys, or values
+  constexpr int HELD = TileLds<G>::HELD;   // a block's keys, or values
   static_assert(SHARE % 16 == 0, "copies are 16 bytes a lane");
-  __shared__ __attribute__((aligned(16))) uint8_t raw[RAW * BYTES];
-  __shared__ __attribute__((aligned(16))) uint8_t keys[2 * HELD], vals[2 * HELD];
   const uint32_t tid = threadIdx.x, lane = tid & 63u, col = lane & 31u, half = lane >> 5;
   const int wave = __builtin_amdgcn_readfirstlane(tid >> 6);
   const uint32_t raw_lds = lds_addr(raw);
@@ -1159,21 +1205,27 @@ __global__ __launch_bounds__(256, G >= 4 ? 1 : 2) void k_kv4_attn_tile(KvAttn a)
   // The tiles of a (sequence, head) lie a multiple of the heads apart (one L2
   // where that is a multiple of 8); the last rows, which see most, go first.
   const uint32_t bh_n = (uint32_t)(a.batch * a.cache.heads);
-  const uint32_t bh = blockIdx.x % bh_n;
+  const uint32_t bh = bx % bh_n;
   const int b = (int)(bh / (uint32_t)a.cache.heads), head = (int)(bh % (uint32_t)a.cache.heads);
   Seq sq;
   if (!seq_at<PART>(a, b, sq)) {
     if (tid == 0) kv_flag(a.cache, VBQ_KV4_FLAG_LENGTH);
+    if constexpr (PART == kOwn) {
+      int r0, r1;
+      if (bx < bh_n && by == 0 && left_out(a, b, r0, r1))
+        for (int64_t e = tid; e < (int64_t)(r1 - r0) * a.ratio; e += 256)
+          a.sums_ml[2 * ((r0 + e / a.ratio) * a.n_heads + head * a.ratio + e % a.ratio) + 1] = kLeftOut;
+    }
     return;
   }
   const int rows = sq.nq * a.ratio, rts = (rows + ROWS - 1) / ROWS;
-  const int rt = rts - 1 - (int)(blockIdx.x / bh_n);
+  const int rt = rts - 1 - (int)(bx / bh_n);
   if (rt < 0) return;
   const int len = sq.len, first = sq.first;
   const int r0 = rt * ROWS;
   const Reach re = tile_reach<PART>(a, sq, rows, r0);
   // this workgroup's part: blocks i0 .. i0 + blocks - 1 of the tile
-  const int per = part_blocks(a, re), i0 = (int)blockIdx.y * per;
+  const int per = part_blocks(a, re), i0 = (int)by * per;
   const int blocks = min(re.ns + re.nw - i0, per);
   const bool whole = re.ns + re.nw <= per;
   if (i0 && blocks <= 0) return;
@@ -1472,8 +1524,8 @@ __global__ __launch_bounds__(256, G >= 4 ? 1 : 2) void k_kv4_attn_tile(KvAttn a)
   const float sum = half_sum(l);
   const int r = w_r0 + (int)col, qi = r / a.ratio, hh = r - qi * a.ratio;
   if (r >= rows) return;
-  if (!whole) {   // sums, and 2^base that they are held times
-    const int64_t place = ((int64_t)blockIdx.x * a.parts + blockIdx.y) * ROWS + (r - r0);
+  if (PART == kShared || !whole) {   // sums, and 2^base that they are held times
+    const int64_t place = ((int64_t)bx * a.parts + by) * ROWS + (r - r0);
     float* const to = a.acc + place * D;
 #pragma unroll
     for (int g = 0; g < G; ++g)
@@ -1488,17 +1540,17 @@ __global__ __launch_bounds__(256, G >= 4 ? 1 : 2) void k_kv4_attn_tile(KvAttn a)
     return;
   }
   const int64_t o = (int64_t)(sq.c0 + qi) * a.n_heads + head * a.ratio + hh;
-  if constexpr (PART != kAll) {
+  if constexpr (PART == kOwn) {
 #pragma unroll
     for (int g = 0; g < G; ++g)
 #pragma unroll
       for (int u = 0; u < 2; ++u)
 #pragma unroll
         for (int bb = 0; bb < 4; ++bb)   // (channel 0 is the lane's of half 0)
-          answer_row<D, PART>(a, o, 16 * g + 8 * u + 4 * (int)half + bb,
-                              f32x4{acc[2 * g][4 * u + bb], acc[2 * g][8 + 4 * u + bb], acc[2 * g + 1][4 * u + bb],
-                                    acc[2 * g + 1][8 + 4 * u + bb]},
-                              sum, kTileShift - m, re.w0 > 0);
+          answer_part<D, PART>(a, o, 16 * g + 8 * u + 4 * (int)half + bb,
+                               f32x4{acc[2 * g][4 * u + bb], acc[2 * g][8 + 4 * u + bb], acc[2 * g + 1][4 * u + bb],
+                                     acc[2 * g + 1][8 + 4 * u + bb]},
+                               sum, kTileShift - m, re.w0 > 0);
     return;
   }
   const float inv = sum > 0.f ? 1.f / sum : sum == 0.f ? 0.f : sum;   // 0: nothing seen; NaN stays
@@ -1513,6 +1565,13 @@ __global__ __launch_bounds__(256, G >= 4 ? 1 : 2) void k_kv4_attn_tile(KvAttn a)
         store4(a, o * D + 64 * g + 4 * (8 * u + 4 * (int)half + bb), v * inv);
       }
   if (a.lse && half == 0) a.lse[o] = (__builtin_amdgcn_logf(sum) + m - kTileShift) * kLn2;
+}
+
+template <int G, bool FINE, Part PART = kAll>
+__global__ __launch_bounds__(256, G >= 4 ? 1 : 2) void k_kv4_attn_tile(KvAttn a) {
+  __shared__ __attribute__((aligned(16))) uint8_t raw[TileLds<G>::kRaw];
+  __shared__ __attribute__((aligned(16))) uint8_t keys[TileLds<G>::kKeys], vals[TileLds<G>::kVals];
+  tile_rows<G, FINE, PART>(a, raw, keys, vals, blockIdx.x, blockIdx.y);
 }
 
 // Joins the parts of the tiles that were cut: blockIdx.x is the tile as above, a
@@ -1552,7 +1611,7 @@ __global__ __launch_bounds__(256) void k_kv4_attn_join(KvAttn a) {
     v += *reinterpret_cast<const f32x4*>(acc + (int64_t)p * (kRowTile * D)) * f;
   }
   const int qi = r / a.ratio, hh = r - qi * a.ratio;
-  answer_row<D, PART>(a, (int64_t)(sq.c0 + qi) * a.n_heads + head * a.ratio + hh, c, v, sum, low, re.w0 > 0);
+  answer_part<D, PART>(a, (int64_t)(sq.c0 + qi) * a.n_heads + head * a.ratio + hh, c, v, sum, low, re.w0 > 0);
 }
 
 }  // namespace

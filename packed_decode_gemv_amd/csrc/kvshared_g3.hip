@@ -1,0 +1,9 @@
+// Attention with shared tokens, heads of 192 channels.
+#include "kvshared.h"
+
+namespace vbq {
+hipError_t launch_kv4_attention_shared_g3(const KvAttn& shared, const KvAttnPlan& sp, const KvAttn& own,
+                                          const KvAttnPlan& op, hipStream_t s) {
+  return launch_shared<3>(shared, sp, own, op, s);
+}
+}  // namespace vbq

@@ -100,7 +100,7 @@ def test_shared_attention_refuses_bad_arguments():
         x, y = pair(dict(a), dict(g))
         return vbq.lib.kv4_attention_shared_workspace(C.byref(c), C.byref(x), C.byref(y))
 
-    assert size() >= 4 * 4 * 8 * 130 + 4 * 2048
+    assert size() >= 4 * 4 * 8 * 130 + 8 * 2048
     assert size(g=dict(max_shared=0)) < size()
     for bad, st in ((dict(window=5), 1), (dict(sinks=1), 1), (dict(batch=0), 2), (dict(n_heads=7), 2), (dict(max_q=-1), 2),
                     (dict(batch=65536), 5), (dict(dtype=2), 1), (dict(causal=2), 1), (dict(scale=0.0), 1)):

@@ -159,7 +159,7 @@ def test_results_repeat_and_strides_and_workspaces_change_nothing(vbq):
         n = len(case.lens)
         ws = vbq.kv4_attention_shared_workspace(args["cache"], n, len(groups), len(case.q), 8, args["max_q"],
                                                 args["max_shared"], args["max_own"], args["max_group_q"])
-        ws[4 * vbq.KV4_COUNTERS:] = 255
+        ws[8 * vbq.KV4_COUNTERS:] = 255
         wide = torch.zeros(len(case.q), 11, 128, dtype=torch.float16, device="cuda")
         wide[:, 2:10] = args["q"]
         args["q"] = wide[:, 2:10]
