@@ -388,12 +388,13 @@ vbq_status head_norm_rotary(const vbq_head_rotary* plan, const vbq_head_rows* q,
 
 // Places in a fork's workspace, in bytes from its start; the last is its size.
 struct ForkPlaces {
-  int64_t offset, kids, first, free, end;
+  int64_t copies, offset, kids, first, free, end;
 };
 static ForkPlaces fork_places(int64_t n_pages, int64_t in, int64_t out, int64_t width) {
   ForkPlaces p;
   const auto up = [](int64_t v) { return (v + 15) & ~(int64_t)15; };
-  p.offset = 16;
+  p.copies = 16;
+  p.offset = p.copies + 16 * out;
   p.kids = up(p.offset + 4 * out);
   p.first = up(p.kids + 4 * in);
   p.free = up(p.first + 4 * in);
@@ -461,6 +462,7 @@ vbq_status kv4_fork(const vbq_kv4* cache, const vbq_kv4_fork* a, hipStream_t str
   f.batch_out = a->batch_out;
   f.width = a->table_width;
   f.head = reinterpret_cast<int32_t*>(w);
+  f.copies = reinterpret_cast<int4*>(w + p.copies);
   f.offset = reinterpret_cast<int32_t*>(w + p.offset);
   f.kids = reinterpret_cast<int32_t*>(w + p.kids);
   f.first = reinterpret_cast<int32_t*>(w + p.first);

@@ -82,11 +82,13 @@ struct KvFork {
   int32_t* lens_out;
   int32_t* refs_out;
   int32_t batch_in, batch_out, width;
-  int32_t* head;     // pages that were found
+  int32_t* head;     // pages that were found; copies
+  int4* copies;      // [batch_out] page, which of the pages to take, blocks
   int32_t* offset;   // [batch_out] pages taken by the sequences before, sign bit: a first continuation
   int32_t* kids;     // [batch_in] continuations
   int32_t* first;    // [batch_in] (used where they do not fit LDS)
   int32_t* free;     // the pages to take
+  uint32_t copiers;  // workgroups that copy (set by the launch)
 };
 hipError_t launch_kv4_fork(const KvFork& f, hipStream_t s);
 

@@ -1,16 +1,16 @@
 // Forks of cached sequences (meaning in vbq.h): two launches.
 //
 // k_kv4_fork_plan: its first workgroup counts each old sequence's continuations and
-// finds the first of them, counts the pages that every new sequence needs, and lists
-// the lowest free pages, as many as are needed; the others copy the reference counts.
-// Which page a sequence gets follows from the numbers alone: the i-th page needed, in
-// the order of sequences and their entries, is the i-th free one.
+// finds the first of them, counts the pages that every new sequence needs, lists the
+// part pages to copy and the lowest free pages, as many as are needed; the others copy
+// the reference counts. Which page a sequence gets follows from the numbers alone: the
+// i-th page needed, in the order of sequences and their entries, is the i-th free one.
 //
-// k_kv4_fork: for every new sequence its row of the table, its length, its pages'
-// counts, and (by several workgroups) the copy of its part page; for every old one
-// what its row's pages lose or gain. Counts are sums of whole numbers by atomics, the
-// same in any order. Pages that are free before the call alone are given out, so no
-// page that is read is written.
+// k_kv4_fork: for every new sequence its row of the table, its length and its pages'
+// counts, for every old one what its row's pages lose or gain, and by workgroups of
+// their own the listed copies. Counts are sums of whole numbers by atomics, the same in
+// any order. Pages that are free before the call alone are given out, so no page that is
+// read is written.
 #include "kv4.h"
 
 namespace vbq {
@@ -101,6 +101,8 @@ __global__ __launch_bounds__(kPlan) void k_kv4_fork_plan(KvFork f) {
   }
   __shared__ int lds_first[IN_LDS ? kPlanKids : 1], lds_kids[IN_LDS ? kPlanKids : 1];
   __shared__ int sums[kPlan / 64];
+  __shared__ int copies;
+  if (tid == 0) copies = 0;
   int* const first = IN_LDS ? lds_first : f.first;
   int* const kids = IN_LDS ? lds_kids : f.kids;
   auto get = [](int* p) { return IN_LDS ? *p : __hip_atomic_load(p, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT); };
@@ -127,22 +129,33 @@ __global__ __launch_bounds__(kPlan) void k_kv4_fork_plan(KvFork f) {
   int64_t wanted = 0;
   for (int b0 = 0; b0 < f.batch_out; b0 += kPlan) {
     const int b = b0 + tid;
-    int n = 0;
+    int n = 0, blocks = 0, part = -1;
     bool is_first = false;
     if (b < f.batch_out) {
       const Parent r = parent_of(f, b);
       is_first = r.p >= 0 && get(first + r.p) == b;
       n = (int)r.need - r.whole;
       if (n < 0) n = 0;
+      if (r.have > r.whole) {   // a part page: copied unless it is kept
+        part = f.table_in[(int64_t)r.p * f.width + r.whole];
+        if ((uint32_t)part < (uint32_t)f.cache.n_pages)
+          blocks = ((r.len & ((kKvBlock << f.cache.block_shift) - 1)) + kKvBlock - 1) / kKvBlock;
+      }
       if (is_first)
-        for (int j = r.whole, e = (int)r.need, page; j < e; ++j) n -= keeps(f, r.p, j, page);
+        for (int j = r.whole, e = (int)r.need, page; j < e; ++j)
+          if (keeps(f, r.p, j, page)) {
+            n -= 1;
+            if (j == r.whole) blocks = 0;
+          }
     }
     int total;
     const int upto = group_scan<kPlan / 64>(n, sums, total);
     // (more than there are pages is cut off: those beyond find none)
     if (b < f.batch_out) {
       const int64_t before = wanted + (upto - n);
-      f.offset[b] = (int)(before < f.cache.n_pages ? before : f.cache.n_pages) | (is_first ? INT32_MIN : 0);
+      const int at = (int)(before < f.cache.n_pages ? before : f.cache.n_pages);
+      f.offset[b] = at | (is_first ? INT32_MIN : 0);
+      if (blocks) f.copies[__hip_atomic_fetch_add(&copies, 1, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_WORKGROUP)] = int4{part, at, blocks, 0};
     }
     wanted += total;
   }
@@ -171,21 +184,49 @@ __global__ __launch_bounds__(kPlan) void k_kv4_fork_plan(KvFork f) {
       if (place < want) f.free[place] = (int)(at + __builtin_ctz(free));
     found += total;
   }
+  __syncthreads();
   if (tid == 0) {
     f.head[0] = found < want ? found : want;
+    f.head[1] = copies;
     if (found < wanted) kv_flag(f.cache, VBQ_KV4_FLAG_FULL);
   }
 }
 
-constexpr int kForkThreads = 256;
+constexpr int kForkThreads = 256, kCopyAtOnce = 4;
 
 __global__ __launch_bounds__(kForkThreads) void k_kv4_fork(KvFork f) {
   __shared__ int sums[kForkThreads / 64];
   const int tid = (int)threadIdx.x;
   const int32_t n_pages = f.cache.n_pages;
-  if (blockIdx.x >= (uint32_t)f.batch_out) {   // an old sequence: its row is gone, its whole pages go to its continuations
-    if (blockIdx.y) return;
-    const int p = (int)(blockIdx.x - (uint32_t)f.batch_out), kids = f.kids[p];
+  if (blockIdx.x < f.copiers) {   // pieces of the copies, kCopyAtOnce loads of a thread at a time
+    const int found = f.head[0], heads = f.cache.heads, unit = kKvGroupBytes * f.cache.groups / 16;   // (of 16 bytes)
+    const int stride = unit << f.cache.block_shift;   // between heads
+    constexpr int PIECE = kForkThreads * kCopyAtOnce;
+    const int pieces = (stride * heads + PIECE - 1) / PIECE;   // of a whole page
+    const int64_t all = (int64_t)f.head[1] * pieces;
+    for (int64_t w = blockIdx.x; w < all; w += f.copiers) {
+      const int4 copy = f.copies[w / pieces];
+      const int run = copy.z * unit, end = run * heads, i0 = (int)(w % pieces) * PIECE + tid;
+      if (copy.y >= found || i0 - tid >= end) continue;
+      const u32x4* const src = reinterpret_cast<const u32x4*>(kv_block(f.cache, f.cache.groups, (uint32_t)copy.x, 0, 0));
+      u32x4* const dst = reinterpret_cast<u32x4*>(kv_block(f.cache, f.cache.groups, (uint32_t)f.free[copy.y], 0, 0));
+      u32x4 v[kCopyAtOnce];
+      int o[kCopyAtOnce];
+#pragma unroll
+      for (int c = 0; c < kCopyAtOnce; ++c) {
+        const int i = i0 + c * kForkThreads;
+        o[c] = i < end ? i / run * (stride - run) + i : -1;
+        if (o[c] >= 0) v[c] = src[o[c]];
+      }
+#pragma unroll
+      for (int c = 0; c < kCopyAtOnce; ++c)
+        if (o[c] >= 0) dst[o[c]] = v[c];
+    }
+    return;
+  }
+  const uint32_t block = blockIdx.x - f.copiers;
+  if (block >= (uint32_t)f.batch_out) {   // an old sequence: its row is gone, its whole pages go to its continuations
+    const int p = (int)(block - (uint32_t)f.batch_out), kids = f.kids[p];
     const int32_t whole = kids ? f.lens_in[p] >> (f.cache.block_shift + 5) : 0;
     for (int j = tid; j < f.width; j += kForkThreads) {
       const int32_t page = f.table_in[(int64_t)p * f.width + j];
@@ -198,30 +239,12 @@ __global__ __launch_bounds__(kForkThreads) void k_kv4_fork(KvFork f) {
     }
     return;
   }
-  const int b = (int)blockIdx.x;
+  const int b = (int)block;
   const Parent r = parent_of(f, b);
   const int off = f.offset[b], found = f.head[0];
   const bool first = off < 0;
   int at = off & INT32_MAX;   // the next page taken
   const int32_t* const from = f.table_in + (int64_t)(r.p < 0 ? 0 : r.p) * f.width;
-
-  // The part page: copied unless it is kept.
-  const int32_t part = r.have > r.whole ? from[r.whole] : -1;
-  int32_t page;
-  if ((uint32_t)part < (uint32_t)n_pages && at < found && !(first && keeps(f, r.p, r.whole, page))) {
-    const int G = f.cache.groups;
-    const int rest = r.len & ((32 << f.cache.block_shift) - 1);
-    const int run = (rest + kKvBlock - 1) / kKvBlock * (kKvGroupBytes * G / 16);   // of one head, in 16 bytes
-    const int stride = (kKvGroupBytes * G / 16) << f.cache.block_shift;            // between heads
-    const u32x4* const src = reinterpret_cast<const u32x4*>(kv_block(f.cache, G, (uint32_t)part, 0, 0));
-    u32x4* const dst = reinterpret_cast<u32x4*>(kv_block(f.cache, G, (uint32_t)f.free[at], 0, 0));
-    const int all = run * f.cache.heads;
-    for (int i = (int)blockIdx.y * kForkThreads + tid; i < all; i += (int)gridDim.y * kForkThreads) {
-      const int h = i / run, o = h * (stride - run) + i;
-      dst[o] = src[o];
-    }
-  }
-  if (blockIdx.y) return;
 
   if (tid == 0) f.lens_out[b] = r.len;
   int32_t* const to = f.table_out + (int64_t)b * f.width;
@@ -262,10 +285,12 @@ hipError_t launch_kv4_fork(const KvFork& f, hipStream_t s) {
   else k_kv4_fork_plan<false><<<plan, kPlan, 0, s>>>(f);
   hipError_t e = hipGetLastError();
   if (e != hipSuccess) return e;
-  int64_t slices = page / (kForkThreads * 16 * 4);
-  slices = slices < 1 ? 1 : slices < 32 ? slices : 32;
-  const dim3 grid((uint32_t)(f.batch_out + f.batch_in), (uint32_t)slices);
-  k_kv4_fork<<<grid, kForkThreads, 0, s>>>(f);
+  // (a page is copied for every new sequence, at most; more workgroups than fill the chip take turns)
+  const int64_t pieces = f.batch_out * ((page + kForkThreads * kCopyAtOnce * 16 - 1) / (kForkThreads * kCopyAtOnce * 16));
+  KvFork k = f;
+  k.copiers = (uint32_t)(pieces < 2048 ? pieces : 2048);
+  const dim3 grid(k.copiers + (uint32_t)(f.batch_out + f.batch_in));
+  k_kv4_fork<<<grid, kForkThreads, 0, s>>>(k);
   return hipGetLastError();
 }
 
