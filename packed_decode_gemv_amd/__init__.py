@@ -19,6 +19,7 @@ For several continuations of one prompt: ``kv4_fork``, ``kv4_attention_shared``,
 """
 from __future__ import annotations
 
+import contextlib
 import ctypes as C
 import os
 import struct
@@ -786,6 +787,7 @@ _LOGPROBS = struct.Struct("@4iq2P2i7Pq")                # vbq_logprobs
 assert _HEAD_ROWS.size == C.sizeof(vbq_head_rows) and _KV4_FORK.size == C.sizeof(vbq_kv4_fork) and \
     _KV4_GROUPS.size == C.sizeof(vbq_kv4_groups) and _LOGPROBS.size == C.sizeof(vbq_logprobs)
 LOGPROBS_MAX_TOP, LOGPROBS_COUNTERS = 32, 512
+_NO_STREAM = contextlib.nullcontext()
 
 
 class HeadRotary:
@@ -841,11 +843,18 @@ def _int32(*numbers) -> bool:
     return all(-2 ** 31 <= n < 2 ** 31 for n in numbers)
 
 
+def _current_device() -> int:
+    global _current_device
+    import torch
+    _current_device = torch._C._cuda_getDevice    # (this function the first time only)
+    return _current_device()
+
+
 def _on_device(index: int, call, *args) -> int:
     """call(*args) with the tensors' device as the current one."""
-    import torch
-    if torch._C._cuda_getDevice() == index:
+    if _current_device() == index:
         return call(*args)
+    import torch
     with torch.cuda.device(index):
         return call(*args)
 
@@ -859,21 +868,28 @@ def _new(t, shape, dtype, stream):
         return t.new_empty(shape, dtype=dtype)
 
 
+_NO_ROWS = _HEAD_ROWS.pack(0, 0, 0, 0, 0, 0, 0, 0, 0, 0)
+
+
 def _head_rows(plan, x, what: str, out, dtype, stream):
     """The output for x, its tokens, its type and its vbq_head_rows."""
     dt = _kv4_dtype(getattr(x, "dtype", None), what)
     H = x.shape[1] if x.ndim == 3 else 0
     T, ts, hs = _kv4_rows(x, what, H, plan)
     if out is None:
-        out = _new(x, (T, H, plan.head_dim), x.dtype if dtype is None else dtype, stream)
-        To, ots, ohs = T, H * plan.head_dim, plan.head_dim
+        D = plan.head_dim
+        if dtype is None:
+            dtype = x.dtype
+        odt = _kv4_dtype(dtype, what + "_out")
+        out = x.new_empty((T, H, D), dtype=dtype) if stream is None else _new(x, (T, H, D), dtype, stream)
+        ots, ohs = H * D, D
     else:
         if dtype is not None and out.dtype is not dtype:
             raise ValueError(f"{what}_out: {out.dtype}, expected {dtype}")
+        odt = _kv4_dtype(out.dtype, what + "_out")
         To, ots, ohs = _kv4_rows(out, what + "_out", H, plan)
-    odt = _kv4_dtype(out.dtype, what + "_out")
-    if To != T:
-        raise ValueError(f"{what}_out: {To} tokens, expected {T}")
+        if To != T:
+            raise ValueError(f"{what}_out: {To} tokens, expected {T}")
     return out, T, dt, _HEAD_ROWS.pack(x.data_ptr(), out.data_ptr(), ts, hs, ots, ohs, H, dt, odt, 0)
 
 
@@ -883,34 +899,36 @@ def head_norm_rotary(plan: HeadRotary, q, k, positions, q_out=None, k_out=None, 
     token and head rows may be strided; either may be None) and rotates it by its
     token's positions, int32 [tokens] or [axes][tokens], in one pass. Returns the
     results, of q_dtype and k_dtype (the inputs' type by default). q_out and k_out:
-    tensors to fill, the inputs themselves for example; other overlaps are
-    refused nowhere and give anything."""
-    if q is None and k is None:
-        raise ValueError("head_norm_rotary: neither q nor k")
-    empty = _HEAD_ROWS.pack(0, 0, 0, 0, 0, 0, 0, 0, 0, 0)
-    rows_q = rows_k = empty
+    tensors to fill, the inputs themselves for example; what overlaps otherwise is
+    not looked for, and must not."""
+    rows_q = rows_k = _NO_ROWS
     T = types = None
     if q is not None:
         q_out, T, types, rows_q = _head_rows(plan, q, "q", q_out, q_dtype, stream)
+    else:
+        q_out = None
     if k is not None:
         k_out, Tk, dt, rows_k = _head_rows(plan, k, "k", k_out, k_dtype, stream)
         if T is not None and (Tk != T or dt != types):
             raise ValueError(f"k: {k.dtype} with {Tk} tokens, expected q's {q.dtype} with {T}")
         T = Tk
-    if not _int32(T):
+    else:
+        k_out = None
+        if T is None:
+            raise ValueError("head_norm_rotary: neither q nor k")
+    if T >= 2 ** 31:
         raise ValueError(f"head_norm_rotary: {T} tokens")
-    step = 0
+    at = None
     if plan.rotary_dim:
         shape = (T,) if plan.axes == 1 and positions.ndim == 1 else (plan.axes, T)
         if positions.dtype is not plan._i32 or positions.shape != shape or not positions.is_contiguous() or \
                 positions.get_device() != plan.index:
             _need(positions, "positions", plan._i32, shape, plan.device)
-        step = T
-    st = _on_device(plan.index, lib.head_norm_rotary, plan._ref, rows_q, rows_k,
-                    positions.data_ptr() if plan.rotary_dim else None, step, T, _kv4_stream(plan, stream))
+        at = positions.data_ptr()
+    st = _on_device(plan.index, lib.head_norm_rotary, plan._ref, rows_q, rows_k, at, T, T, _kv4_stream(plan, stream))
     if st:
         _check(st, "head_norm_rotary")
-    return q_out if q is not None else None, k_out if k is not None else None
+    return q_out, k_out
 
 
 def kv4_fork_workspace(cache: Kv4Cache, batch: int, table_width: int, batch_before=None, stream=None):
@@ -939,16 +957,24 @@ def kv4_fork(cache: Kv4Cache, refs, block_table, lens, parents, reserve=None, ou
         raise ValueError("block_table, parents: expected a 2-D and a 1-D torch tensor")
     B, W = block_table.shape
     N = parents.shape[0]
-    for t, what, shape in ((block_table, "block_table", (B, W)), (lens, "lens", (B,)), (refs, "refs", (cache.n_pages,)),
-                           (parents, "parents", (N,)), (reserve, "reserve", (N,))):
-        if t is None and what == "reserve":
-            continue
-        if t.dtype is not i32 or t.get_device() != dev or t.shape != shape or not t.is_contiguous():
-            _need(t, what, i32, shape, cache.device)
+    n = cache.n_pages
+    if not (block_table.dtype is i32 and lens.dtype is i32 and refs.dtype is i32 and parents.dtype is i32 and
+            block_table.get_device() == dev and lens.get_device() == dev and refs.get_device() == dev and
+            parents.get_device() == dev and block_table.is_contiguous() and lens.is_contiguous() and
+            refs.is_contiguous() and parents.is_contiguous() and lens.shape == (B,) and refs.shape == (n,) and
+            (reserve is None or (reserve.dtype is i32 and reserve.get_device() == dev and reserve.is_contiguous() and
+                                 reserve.shape == (N,)))):
+        for t, what, shape in ((block_table, "block_table", (B, W)), (lens, "lens", (B,)), (refs, "refs", (n,)),
+                               (parents, "parents", (N,)), (reserve, "reserve", (N,))):
+            if t is not None or what != "reserve":
+                _need(t, what, i32, shape, cache.device)
     if min(B, W, N) < 1 or not _int32(B, W, N):
         raise ValueError(f"block_table: shape {(B, W)}, {N} parents")
     if out is None:
-        out = tuple(_kv4_new(cache, shape, i32, stream) for shape in ((N, W), (N,), (cache.n_pages,)))
+        if stream is None:
+            out = (refs.new_empty((N, W)), refs.new_empty((N,)), refs.new_empty((n,)))
+        else:
+            out = tuple(_new(refs, shape, i32, stream) for shape in ((N, W), (N,), (n,)))
     else:
         for t, what, shape in zip(out, ("out block_table", "out lens", "out refs"), ((N, W), (N,), (cache.n_pages,))):
             _need(t, what, i32, shape, cache.device)
@@ -1042,6 +1068,17 @@ def kv4_attention_shared(cache: Kv4Cache, q, block_table, kv_lens, cu_q, cu_grou
     return out
 
 
+_TOKEN_BYTES = {"torch.int32": 4, "torch.int64": 8}
+
+
+def _on_stream(stream):
+    """The stream as the current one, for what is allocated for it."""
+    if stream is None:
+        return _NO_STREAM
+    import torch
+    return torch.cuda.stream(stream)
+
+
 class TokenLogprobs(typing.NamedTuple):
     """What token_logprobs returns; None for what was not asked for."""
     logprob: object        # float32 [rows], of the given tokens
@@ -1072,43 +1109,57 @@ def token_logprobs(logits, tokens=None, top: int = 0, out=None, workspace=None, 
     to the lower number). Logits may be -infinity; rows with a NaN or +infinity give
     NaN and -1. out: a TokenLogprobs of tensors to fill. workspace: from
     token_logprobs_workspace, for calls that allocate nothing."""
-    import torch
     if getattr(logits, "ndim", 0) != 2:
         raise ValueError("logits: expected a 2-D torch tensor")
     M, V = logits.shape
     dt = _kv4_dtype(logits.dtype, "logits")
-    if logits.device.type != "cuda":
-        raise ValueError(f"logits: on {logits.device}, expected a GPU tensor")
-    if V > 1 and logits.stride(1) != 1:
-        raise ValueError("logits: a row is not contiguous")
     dev = logits.get_device()
+    if dev < 0:
+        raise ValueError(f"logits: on {logits.device}, expected a GPU tensor")
+    row, step = logits.stride()
+    if V > 1 and step != 1:
+        raise ValueError("logits: a row is not contiguous")
+    if not _int32(M, V):
+        raise ValueError(f"logits: shape {(M, V)}")
     size = 0
     if tokens is not None:
-        if tokens.dtype is not torch.int64 and tokens.dtype is not torch.int32:
+        size = _TOKEN_BYTES.get(str(tokens.dtype), 0)
+        if not size:
             raise ValueError(f"tokens: dtype {tokens.dtype}, expected int32 or int64")
         if tokens.shape != (M,) or not tokens.is_contiguous() or tokens.get_device() != dev:
             _need(tokens, "tokens", tokens.dtype, (M,), logits.device)
-        size = tokens.itemsize
-    if not _int32(M, V):
-        raise ValueError(f"logits: shape {(M, V)}")
     if not 0 <= top <= min(LOGPROBS_MAX_TOP, V):
         raise ValueError(f"top: {top}, expected 0..{min(LOGPROBS_MAX_TOP, V)}")
-    kinds = ((torch.float32, (M,), size), (torch.int32, (M,), size), (torch.float32, (M,), 1), (torch.float32, (M,), 1),
-             (torch.float32, (M, top), top), (torch.int32, (M, top), top))
+    import torch
+    f32, i32 = torch.float32, torch.int32
     if out is None:
-        out = TokenLogprobs(*(_new(logits, shape, dtype, stream) if want else None for dtype, shape, want in kinds))
+        with _on_stream(stream):
+            new = logits.new_empty
+            # (one tensor for the three)
+            entropy, lse, logprob = new((3, M), dtype=f32).unbind(0)
+            rank = new((M,), dtype=i32) if size else None
+            top_logprob, top_index = (new((M, top), dtype=f32), new((M, top), dtype=i32)) if top else (None, None)
+        if not size:
+            logprob = None
+        out = TokenLogprobs(logprob, rank, entropy, lse, top_logprob, top_index)
     else:
         out = TokenLogprobs(*out)
-        for t, what, (dtype, shape, want) in zip(out, TokenLogprobs._fields, kinds):
-            if want and (t is not None or what not in ("entropy", "lse")):
+        logprob, rank, entropy, lse, top_logprob, top_index = out
+        for t, what, dtype, shape, want in ((logprob, "logprob", f32, (M,), size), (rank, "rank", i32, (M,), size),
+                                            (entropy, "entropy", f32, (M,), entropy is not None),
+                                            (lse, "lse", f32, (M,), lse is not None),
+                                            (top_logprob, "top_logprob", f32, (M, top), top),
+                                            (top_index, "top_index", i32, (M, top), top)):
+            if want:
                 _need(t, "out " + what, dtype, shape, logits.device)
     if workspace is None:
         workspace = token_logprobs_workspace(M, V, top, logits.device, stream)
     elif workspace.dtype is not torch.uint8 or workspace.get_device() != dev or not workspace.is_contiguous():
         raise ValueError("workspace: expected a contiguous uint8 tensor on the logits' device")
-    a = _LOGPROBS.pack(M, V, dt, top, logits.stride(0) if M > 1 else V, logits.data_ptr(),
-                       tokens.data_ptr() if size else 0, size, 0,
-                       *(t.data_ptr() if t is not None and want else 0 for t, (_, _, want) in zip(out, kinds)),
+    a = _LOGPROBS.pack(M, V, dt, top, row if M > 1 else V, logits.data_ptr(), tokens.data_ptr() if size else 0, size, 0,
+                       logprob.data_ptr() if size else 0, rank.data_ptr() if size else 0,
+                       0 if entropy is None else entropy.data_ptr(), 0 if lse is None else lse.data_ptr(),
+                       top_logprob.data_ptr() if top else 0, top_index.data_ptr() if top else 0,
                        workspace.data_ptr(), workspace.numel())
     st = _on_device(dev, lib.token_logprobs, a,
                     torch._C._cuda_getCurrentRawStream(dev) if stream is None else stream.cuda_stream)

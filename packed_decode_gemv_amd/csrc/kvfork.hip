@@ -26,6 +26,8 @@ struct Parent {
   int32_t len, whole, have;   // tokens, whole pages, pages
   int64_t need;      // pages with those reserved
   bool bad_len;      // something does not fit
+  int32_t part;      // the entry behind the whole pages (of the table's row), -1: no page
+  bool part_mine;    // that nothing else names
 };
 __device__ inline Parent parent_of(const KvFork& f, int b) {
   Parent r;
@@ -56,6 +58,10 @@ __device__ inline Parent parent_of(const KvFork& f, int b) {
     r.bad_len = true;
     r.need = f.width;
   }
+  r.part = -1;
+  if (r.p >= 0 && r.whole < r.need) r.part = f.table_in[(int64_t)r.p * f.width + r.whole];
+  if ((uint32_t)r.part >= (uint32_t)f.cache.n_pages) r.part = -1;
+  r.part_mine = r.part >= 0 && f.refs_in[r.part] == 1;
   return r;
 }
 // Whether the first continuation keeps entry j (from the part page on) of its parent's row.
@@ -68,11 +74,12 @@ __device__ inline bool keeps(const KvFork& f, int p, int j, int32_t& page) {
 template <int WAVES>
 __device__ inline int group_scan(int v, int* sums, int& total) {
   const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
-#pragma unroll
-  for (int d = 1; d < 64; d <<= 1) {
-    const int u = __shfl_up(v, d, 64);
-    if (lane >= d) v += u;
-  }
+  v += __builtin_amdgcn_update_dpp(0, v, 0x111, 0xF, 0xF, true);   // row_shr:1
+  v += __builtin_amdgcn_update_dpp(0, v, 0x112, 0xF, 0xF, true);   // row_shr:2
+  v += __builtin_amdgcn_update_dpp(0, v, 0x114, 0xF, 0xF, true);   // row_shr:4
+  v += __builtin_amdgcn_update_dpp(0, v, 0x118, 0xF, 0xF, true);   // row_shr:8
+  v += __builtin_amdgcn_update_dpp(0, v, 0x142, 0xA, 0xF, false);  // row_bcast:15 into rows 1 and 3
+  v += __builtin_amdgcn_update_dpp(0, v, 0x143, 0xC, 0xF, false);  // row_bcast:31 into rows 2 and 3
   if (lane == 63) sums[wave] = v;
   __syncthreads();
   int before = 0;
@@ -114,10 +121,29 @@ __global__ __launch_bounds__(kPlan) void k_kv4_fork_plan(KvFork f) {
     put(first + p, INT32_MAX);
     put(kids + p, 0);
   }
+  // Free pages among the thread's first counts, on their way with the rest.
+  auto free_at = [&](int64_t at) {
+    uint32_t free = 0;
+#pragma unroll
+    for (int i = 0; i < kScan; i += 4) {
+      if (at + i + 4 <= f.cache.n_pages) {
+        const u32x4 v = *reinterpret_cast<const u32x4*>(f.refs_in + at + i);
+#pragma unroll
+        for (int c = 0; c < 4; ++c) free |= (v[c] == 0 ? 1u : 0u) << (i + c);
+      } else {
+        for (int c = 0; c < 4; ++c)
+          if (at + i + c < f.cache.n_pages) free |= (f.refs_in[at + i + c] == 0 ? 1u : 0u) << (i + c);
+      }
+    }
+    return free;
+  };
+  Parent mine;
+  if (tid < f.batch_out) mine = parent_of(f, tid);
+  const uint32_t first_free = free_at((int64_t)tid * kScan);
   __builtin_amdgcn_s_waitcnt(VBQ_VMCNT_IMM(0));   // (device-scope stores are where the atomics see them)
   __syncthreads();
   for (int b = tid; b < f.batch_out; b += kPlan) {
-    const Parent r = parent_of(f, b);
+    const Parent r = b < kPlan ? mine : parent_of(f, b);
     if (r.bad_len) kv_flag(f.cache, VBQ_KV4_FLAG_LENGTH);
     if (r.p < 0) continue;
     __hip_atomic_fetch_min(first + r.p, b, __ATOMIC_RELAXED, IN_LDS ? __HIP_MEMORY_SCOPE_WORKGROUP : __HIP_MEMORY_SCOPE_AGENT);
@@ -132,21 +158,21 @@ __global__ __launch_bounds__(kPlan) void k_kv4_fork_plan(KvFork f) {
     int n = 0, blocks = 0, part = -1;
     bool is_first = false;
     if (b < f.batch_out) {
-      const Parent r = parent_of(f, b);
+      const Parent r = b < kPlan ? mine : parent_of(f, b);
       is_first = r.p >= 0 && get(first + r.p) == b;
       n = (int)r.need - r.whole;
       if (n < 0) n = 0;
       if (r.have > r.whole) {   // a part page: copied unless it is kept
-        part = f.table_in[(int64_t)r.p * f.width + r.whole];
-        if ((uint32_t)part < (uint32_t)f.cache.n_pages)
-          blocks = ((r.len & ((kKvBlock << f.cache.block_shift) - 1)) + kKvBlock - 1) / kKvBlock;
+        part = r.part;
+        if (part >= 0) blocks = ((r.len & ((kKvBlock << f.cache.block_shift) - 1)) + kKvBlock - 1) / kKvBlock;
       }
-      if (is_first)
-        for (int j = r.whole, e = (int)r.need, page; j < e; ++j)
-          if (keeps(f, r.p, j, page)) {
-            n -= 1;
-            if (j == r.whole) blocks = 0;
-          }
+      if (is_first) {
+        if (r.part_mine) {
+          n -= 1;
+          blocks = 0;
+        }
+        for (int j = r.whole + 1, e = (int)r.need, page; j < e; ++j) n -= keeps(f, r.p, j, page);
+      }
     }
     int total;
     const int upto = group_scan<kPlan / 64>(n, sums, total);
@@ -166,18 +192,7 @@ __global__ __launch_bounds__(kPlan) void k_kv4_fork_plan(KvFork f) {
   const int want = (int)(wanted < f.cache.n_pages ? wanted : f.cache.n_pages);
   for (int64_t base = 0; base < f.cache.n_pages && found < want; base += kPlan * kScan) {
     const int64_t at = base + (int64_t)tid * kScan;
-    uint32_t free = 0;
-#pragma unroll
-    for (int i = 0; i < kScan; i += 4) {
-      if (at + i + 4 <= f.cache.n_pages) {
-        const u32x4 v = *reinterpret_cast<const u32x4*>(f.refs_in + at + i);
-#pragma unroll
-        for (int c = 0; c < 4; ++c) free |= (v[c] == 0 ? 1u : 0u) << (i + c);
-      } else {
-        for (int c = 0; c < 4; ++c)
-          if (at + i + c < f.cache.n_pages) free |= (f.refs_in[at + i + c] == 0 ? 1u : 0u) << (i + c);
-      }
-    }
+    uint32_t free = base ? free_at(at) : first_free;
     int total;
     int place = found + group_scan<kPlan / 64>(__builtin_popcount(free), sums, total) - __builtin_popcount(free);
     for (; free; free &= free - 1, ++place)
