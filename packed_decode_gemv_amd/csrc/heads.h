@@ -23,7 +23,7 @@ struct HeadRotary {
   int64_t tokens;
   int32_t head_dim, rotary_dim, axes, interleaved;
   float eps;
-  int32_t splits, passes;  // wavefronts that share a token, and what each takes (set by the launch)
+  int32_t passes;          // wavefronts that share a token (set by the launch)
 };
 
 hipError_t launch_head_norm_rotary(HeadRotary a, int dtype, hipStream_t s);

@@ -5,8 +5,13 @@
 // chunks of eight that hold whole pairs, so no channel moves between lanes. With
 // halves paired, lane e < R / 16 holds channels 8e .. 8e+7 and R/2 + 8e ..; lanes
 // beyond, and all lanes where neighbours are paired, hold 16e .. 16e+15. A
-// wavefront takes one token and 64 / 4G heads at a time; the token's cosines and
-// sines are worked out once, a pair a lane, and read back from LDS.
+// wavefront takes 64 / 4G heads of one token; the token's cosines and sines are worked
+// out a pair a lane and read back from LDS. (Two such passes a wavefront save half of
+// that, but leave less on its way: 25763 bf16 tokens of 32 + 8 heads of 128 take 98 us by
+// one and 96 by two, 7001 fp32 tokens of 16 + 4 heads of 256 43 and 45; five take 105
+// and 52.)
+//   Memory bounds it: those move 528 and 215 MB, at 5.4 and 5.0 TB/s; a large copy
+// reaches 5.1 to 6.2 from card to card.
 //
 // Angles. position * inv_freq in turns, in binary64: 2^31 positions leave 8e-8 of a
 // turn, and what is left of whole turns is rounded to binary32 only then.
@@ -91,9 +96,9 @@ __global__ __launch_bounds__(64 * kHeadWaves) void k_head_norm_rotary(HeadRotary
   const uint32_t lane = threadIdx.x & 63u;
   const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
   const int64_t task = (int64_t)blockIdx.x * kHeadWaves + wave;
-  const int64_t token = task / a.splits;
+  const int64_t token = task / a.passes;
   if (token >= a.tokens) return;
-  const int split = (int)(task - token * a.splits);
+  const int pass = (int)(task - token * a.passes);
   const int e = (int)(lane % LANES), slot = (int)(lane / LANES);
 
   // The token's turns, a pair a lane.
@@ -128,55 +133,47 @@ __global__ __launch_bounds__(64 * kHeadWaves) void k_head_norm_rotary(HeadRotary
     sn[i] = t.y;
   }
 
-  const int q_passes = (a.q.heads + HEADS - 1) / HEADS, passes = q_passes + (a.k.heads + HEADS - 1) / HEADS;
-  const int from = split * a.passes, to = min(passes, from + a.passes);
-  float w0[8], w1[8];
-  bool held = false, held_k = false;
-  for (int p = from; p < to; ++p) {
-    const bool is_k = p >= q_passes;
-    const HeadRows& t = is_k ? a.k : a.q;
-    const int head = (p - (is_k ? q_passes : 0)) * HEADS + slot;
-    const bool in = head < t.heads && (G != 3 || slot < HEADS);
-    float x0[8], x1[8];
+  const int q_passes = (a.q.heads + HEADS - 1) / HEADS;
+  const bool is_k = pass >= q_passes;
+  const HeadRows& t = is_k ? a.k : a.q;
+  const int head = (is_k ? pass - q_passes : pass) * HEADS + slot;
+  const bool in = head < t.heads && slot < HEADS;
+  float x0[8], x1[8];
 #pragma unroll
-    for (int i = 0; i < 8; ++i) x0[i] = x1[i] = 0.f;
-    if (in) {
-      const int64_t at = token * t.in_ts + head * t.in_hs;
-      load8<DT>(t.in, at + ch0, x0);
-      load8<DT>(t.in, at + ch1, x1);
-    }
-    if (t.weight) {
-      if (!held || is_k != held_k) {
-        load8<VBQ_F32>(t.weight, ch0, w0);
-        load8<VBQ_F32>(t.weight, ch1, w1);
-        held = true;
-        held_k = is_k;
-      }
-      float sum = 0.f;
+  for (int i = 0; i < 8; ++i) x0[i] = x1[i] = 0.f;
+  if (in) {
+    const int64_t at = token * t.in_ts + head * t.in_hs;
+    load8<DT>(t.in, at + ch0, x0);
+    load8<DT>(t.in, at + ch1, x1);
+  }
+  if (t.weight) {
+    float w0[8], w1[8];
+    load8<VBQ_F32>(t.weight, ch0, w0);
+    load8<VBQ_F32>(t.weight, ch1, w1);
+    float sum = 0.f;
 #pragma unroll
-      for (int i = 0; i < 8; ++i) sum = __builtin_fmaf(x0[i], x0[i], __builtin_fmaf(x1[i], x1[i], sum));
-      const float r = rsqrtf(__builtin_fmaf(head_sum<G>(sum, lane), 1.f / D, a.eps));
+    for (int i = 0; i < 8; ++i) sum = __builtin_fmaf(x0[i], x0[i], __builtin_fmaf(x1[i], x1[i], sum));
+    const float r = rsqrtf(__builtin_fmaf(head_sum<G>(sum, lane), 1.f / D, a.eps));
 #pragma unroll
-      for (int i = 0; i < 8; ++i) {
-        x0[i] *= r * w0[i];
-        x1[i] *= r * w1[i];
-      }
+    for (int i = 0; i < 8; ++i) {
+      x0[i] *= r * w0[i];
+      x1[i] *= r * w1[i];
     }
-    if (turned) {
+  }
+  if (turned) {
 #pragma unroll
-      for (int i = 0; i < 8; ++i) {
-        float& u = NEIGHBOURS ? (i < 4 ? x0[2 * i] : x1[2 * i - 8]) : x0[i];
-        float& v = NEIGHBOURS ? (i < 4 ? x0[2 * i + 1] : x1[2 * i - 7]) : x1[i];
-        const float y = __builtin_fmaf(u, cs[i], -v * sn[i]);
-        v = __builtin_fmaf(v, cs[i], u * sn[i]);
-        u = y;
-      }
+    for (int i = 0; i < 8; ++i) {
+      float& u = NEIGHBOURS ? (i < 4 ? x0[2 * i] : x1[2 * i - 8]) : x0[i];
+      float& v = NEIGHBOURS ? (i < 4 ? x0[2 * i + 1] : x1[2 * i - 7]) : x1[i];
+      const float y = __builtin_fmaf(u, cs[i], -v * sn[i]);
+      v = __builtin_fmaf(v, cs[i], u * sn[i]);
+      u = y;
     }
-    if (in) {
-      const int64_t at = token * t.out_ts + head * t.out_hs;
-      store8(t.out, at + ch0, t.out_dtype, x0);
-      store8(t.out, at + ch1, t.out_dtype, x1);
-    }
+  }
+  if (in) {
+    const int64_t at = token * t.out_ts + head * t.out_hs;
+    store8(t.out, at + ch0, t.out_dtype, x0);
+    store8(t.out, at + ch1, t.out_dtype, x1);
   }
 }
 
@@ -186,9 +183,8 @@ hipError_t launch_head_norm_rotary(HeadRotary a, int dtype, hipStream_t s) {
   const int groups = a.head_dim / 64, heads = 64 / (4 * groups);
   const int64_t passes = (a.q.heads + heads - 1) / heads + (a.k.heads + heads - 1) / heads;
   if (a.tokens == 0 || passes == 0) return hipSuccess;
-  a.splits = (int32_t)passes;
-  a.passes = 1;
-  const int64_t groups_n = (a.tokens * a.splits + kHeadWaves - 1) / kHeadWaves;
+  a.passes = (int32_t)passes;
+  const int64_t groups_n = (a.tokens * passes + kHeadWaves - 1) / kHeadWaves;
   if (groups_n * (64 * kHeadWaves) > (int64_t)UINT32_MAX) return hipErrorNotSupported;
   const dim3 grid((uint32_t)groups_n);
 #define VBQ_ONE(G, DT)                                                                               \
