@@ -23,7 +23,7 @@ namespace {
 constexpr int kWaves = 4;                     // of a workgroup
 constexpr int kPer = kLogprobStep / 64;       // logits of a lane and step
 constexpr int kTop = VBQ_LOGPROBS_MAX_TOP;
-constexpr int kKeep = 64;                     // a list longer than this is cut back
+constexpr int kKeep = 64, kSpare = 16;        // a list is cut back when it passes `top` by so many, or 64
 constexpr int kList = kKeep + 64;             // places: a wavefront appends 64 keys at a time
 constexpr float kLog2e = 1.44269504088896341f, kLn2 = 0.693147180559945309f;
 
@@ -95,7 +95,7 @@ __device__ inline void wave_sync() {
 struct Best {
   uint64_t* list;
   uint64_t least;   // keys up to it are not wanted
-  int n, top;
+  int n, top, limit;   // cut back when there are more than `limit`
   uint32_t lane;
   int sorted;       // keys in order at the list's head
 
@@ -139,7 +139,7 @@ struct Best {
     if (!who) return;
     if (want) list[n + lanes_below(who)] = key;
     n += __builtin_popcountll(who);
-    if (n > kKeep) cut();
+    if (n > limit) cut();
   }
 };
 
@@ -279,11 +279,14 @@ __global__ __launch_bounds__(64 * kWaves) void k_token_logprobs(Logprobs a) {
   const int steps = (vecs + 64 * VECS - 1) / (64 * VECS), stride = a.splits * ROW_WAVES;
   u32x4 raw[VECS];
   auto load = [&](int j) {
-    const int v0 = j * (64 * VECS);
+    const u32x4* const at = body + (int64_t)j * (64 * VECS) + lane;
+    const int left = vecs - j * (64 * VECS) - (int)lane;
+    if ((j + 1) * (64 * VECS) <= vecs) {
 #pragma unroll
-    for (int i = 0; i < VECS; ++i) {
-      raw[i] = u32x4{0, 0, 0, 0};
-      if (v0 + 64 * VECS <= vecs || v0 + 64 * i + (int)lane < vecs) raw[i] = body[v0 + 64 * i + lane];
+      for (int i = 0; i < VECS; ++i) raw[i] = at[64 * i];
+    } else {
+#pragma unroll
+      for (int i = 0; i < VECS; ++i) raw[i] = 64 * i < left ? at[64 * i] : u32x4{0, 0, 0, 0};
     }
   };
   int j = split * ROW_WAVES + (ROW_WAVES == 1 ? 0 : wave);
@@ -295,7 +298,7 @@ __global__ __launch_bounds__(64 * kWaves) void k_token_logprobs(Logprobs a) {
   w.add = -w.m;
   w.s = w.t = 0.f;
   w.before = 0;
-  w.best = Best{lists[wave], 0, 0, a.top, lane, 0};
+  w.best = Best{lists[wave], 0, 0, a.top, min(a.top + kSpare, kKeep), lane, 0};
   w.count = token >= 0 && token < a.vocab;
   w.token = w.count ? (uint32_t)token : 0u;
   w.given = w.count ? value_at<DT>(x, token) : 0.f;
