@@ -22,8 +22,8 @@
  *     library allocates nothing, keeps no state between calls (apart from
  *     cached device attributes) and needs no workspace: partial sums stay
  *     on-chip inside a workgroup. (vbq_gemv_batched_static keeps a scratch
- *     array, kv4_attention takes a workspace from the caller.) The calls can
- *     therefore be captured into a HIP graph as they are. Buffers marked "device" live in GPU memory of
+ *     array; kv4_attention, kv4_attention_shared, kv4_fork and token_logprobs
+ *     take a workspace from the caller.) The calls can therefore be captured into a HIP graph as they are. Buffers marked "device" live in GPU memory of
  *     the current HIP device; "host" buffers are ordinary CPU memory.
  *   - Asynchrony: compute calls enqueue work on `stream` and return without
  *     waiting. Argument errors are found before anything is enqueued: the
@@ -518,6 +518,7 @@ vbq_status head_norm_rotary(const vbq_head_rotary* plan, const vbq_head_rows* q,
  * -1 .. batch_in-1 or with a length that does not fit counts as none, entries beyond the
  * table and negative reserves as 0 (FLAG_LENGTH); where free pages run out, entries are
  * -1 and nothing is copied (FLAG_FULL).
+ * Pages are 16 GiB at most.
  * kv4_fork_workspace: bytes for calls of these sizes (or less), -1 if they are refused.
  * Calls that overlap in time need workspaces of their own; nothing in it has to be set. */
 typedef struct vbq_kv4_fork {

@@ -349,6 +349,9 @@ static vbq_status check_rows(const vbq_head_rows* r, const float* weight, HeadRo
   if (!aligned(r->in, 16) || !aligned(r->out, 16) || !aligned(weight, 16) || r->in_token_stride % in16 ||
       r->in_head_stride % in16 || r->out_token_stride % out16 || r->out_head_stride % out16)
     return VBQ_ERR_ALIGNMENT;
+  if (r->in && r->in == r->out && (r->in_dtype != r->out_dtype || r->in_token_stride != r->out_token_stride ||
+                          r->in_head_stride != r->out_head_stride))
+    return VBQ_ERR_INVALID_ARG;   // (in place: number for number)
   *out = HeadRows{r->in, r->out, weight, r->in_token_stride, r->in_head_stride, r->out_token_stride,
                   r->out_head_stride, r->heads, r->out_dtype};
   return VBQ_OK;
@@ -386,6 +389,7 @@ vbq_status head_norm_rotary(const vbq_head_rotary* plan, const vbq_head_rows* q,
   return e == hipErrorNotSupported ? VBQ_ERR_UNSUPPORTED : from_hip(e);
 }
 
+constexpr int64_t kMaxForkPage = (int64_t)1 << 34;   // (pieces of a page are counted in 16 bytes, in 32 bits)
 // Places in a fork's workspace, in bytes from its start; the last is its size.
 struct ForkPlaces {
   int64_t copies, offset, kids, first, free, end;
@@ -419,6 +423,8 @@ vbq_status kv4_fork(const vbq_kv4* cache, const vbq_kv4_fork* a, hipStream_t str
   if (st != VBQ_OK) return st;
   if (!a || a->reserved != 0) return VBQ_ERR_INVALID_ARG;
   st = check_fork_sizes(a->batch_in, a->batch_out, a->table_width);
+  if (st == VBQ_OK && kv4_page_bytes(cache->page_tokens, cache->n_kv_heads, cache->head_dim) > kMaxForkPage)
+    st = VBQ_ERR_UNSUPPORTED;
   if (st != VBQ_OK) return st;
   if (!a->table_in || !a->lens_in || !a->refs_in || !a->parents || !a->table_out || !a->lens_out || !a->refs_out ||
       !a->workspace)

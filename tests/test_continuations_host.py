@@ -43,6 +43,8 @@ def test_rotary_refuses_bad_arguments():
         assert run(q=bad) == st, bad
         assert run(k=bad) == st, bad
     assert run(q=dict(in_dtype=1)) == 1                  # queries and keys of two types
+    for bad in (dict(out_dtype=1), dict(out_token_stride=1024), dict(out_head_stride=256)):
+        assert run(q=bad) == 1 and run(k=bad) == 1, bad  # in place, but not number for number
     assert run(positions=None) == 1 and run(positions=BASE + 2) == 4
 
 
@@ -66,6 +68,7 @@ def test_fork_sizes_and_refusals():
         return vbq.lib.kv4_fork(cache and C.byref(cache), C.byref(vbq.vbq_kv4_fork(**d)), None)
 
     assert run(cache=None) == 1 and run(reserved=1) == 1
+    assert run(cache=_cache(vbq, page_tokens=65536, n_kv_heads=4096, head_dim=256)) == 5      # pages of 77 GB
     for bad, st in ((dict(batch_in=0), 2), (dict(batch_out=65536), 5), (dict(table_width=0), 2),
                     (dict(table_width=(1 << 20) + 1), 5), (dict(workspace_bytes=15), 6)):
         assert run(**bad) == st, bad

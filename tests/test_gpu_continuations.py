@@ -616,3 +616,22 @@ def test_fork_refusals(vbq):
             vbq.kv4_fork(cache, refs, table, lens, torch.zeros(2, **i32), out=out)
     with pytest.raises(vbq.VbqError):        # a workspace that is too small
         vbq.kv4_fork(cache, refs, table, lens, parents, workspace=torch.zeros(16, dtype=torch.uint8, device="cuda"))
+
+
+# ---- together ------------------------------------------------------------------------
+@pytest.mark.parametrize("beams,prompt,steps", [(1, 5, 3), (4, 70, 6), (8, 200, 5), (3, 64, 9)])
+def test_the_beam_search_example(vbq, beams, prompt, steps):
+    """All operators as they are used together: scores of beams that share a prompt's pages are those of every
+    sequence decoded by itself. A log probability differs by the rounding of fp16 activations that two kernels leave
+    apart (2^-11 of the logits' size, logits of standard deviation 4 and 4 sigma, a few times a step)."""
+    import os
+    import sys
+    sys.path.insert(0, os.path.join(os.path.dirname(os.path.dirname(os.path.abspath(__file__))), "examples"))
+    import continuations
+    model = continuations.Model(hidden=256, heads=8, kv_heads=2, dim=64, vocab=997)
+    r = continuations.run(beams, prompt, steps, model=model)
+    assert all(a >= b for a, b in zip(r["scores"], r["scores"][1:]))
+    assert all(np.isfinite(r["scores"]))
+    for a, b in zip(r["scores"], r["alone"]):
+        assert abs(a - b) <= steps * 8 * 2.0 ** -11 * 16
+    assert r["pages"] <= r["apart"]

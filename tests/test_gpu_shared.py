@@ -304,3 +304,67 @@ def test_refusals(vbq):
             vbq.kv4_attention_shared(**{**args, **bad})
     empty = dict(args, q=args["q"][:0], cu_q=torch.zeros_like(args["cu_q"]))
     assert vbq.kv4_attention_shared(**empty).shape == (0, 2, 64)
+
+
+def test_rows_behind_the_last_sequence_stay(vbq):
+    import torch
+    rng = np.random.default_rng(12)
+    for count in (5, 40):
+        case = Case(rng, 1, 4, 64, 32, [(100, [(9, 1)] * count)])
+        args = case.args(vbq)
+        want = vbq.kv4_attention_shared(**args)
+        args["q"] = torch.cat([args["q"], torch.full_like(args["q"][:3], float("nan"))])
+        out = torch.full((count + 3, 4, 64), 7.0, dtype=torch.float16, device="cuda")
+        vbq.kv4_attention_shared(**args, out=out)
+        assert torch.equal(out[:count], want) and (out[count:] == 7.0).all()
+        assert args["cache"].check() is False
+
+
+def test_calls_on_two_streams_at_once(vbq):
+    """Each with a workspace of its own; a captured graph replays beside eager calls of another size."""
+    import torch
+    rng = np.random.default_rng(13)
+    case = Case(rng, 2, 4, 128, 64, [(1500, [(60, 1)] * 6)])
+    big = Case(rng, 1, 4, 64, 32, [(900, [(30, 2)] * 40)])
+    a, b = case.args(vbq), big.args(vbq)
+    want = [vbq.kv4_attention_shared(**a), vbq.kv4_attention_shared(**b)]
+    torch.cuda.synchronize()
+    streams = [torch.cuda.Stream() for _ in range(2)]
+    got = [[], []]
+    for _ in range(20):
+        for i, (args, s) in enumerate(zip((a, b), streams)):
+            got[i].append(vbq.kv4_attention_shared(**args, stream=s))
+    torch.cuda.synchronize()
+    for outs, w in zip(got, want):
+        assert all(torch.equal(o, w) for o in outs)
+
+
+def test_far_pages_of_a_large_cache(vbq):
+    """Pages beyond 4 GiB: attention reads them, a fork copies them."""
+    import torch
+    heads, dim, page = 1, 64, 1024
+    n_pages = (5 << 30) // (1024 * 72)
+    cache = vbq.Kv4Cache(n_pages, page, heads, dim)
+    rng = np.random.default_rng(14)
+    case = Case(rng, heads, 2, dim, page, [(1500, [(40, 1)] * 3)])
+    args = case.args(vbq)
+    want = vbq.kv4_attention_shared(**args)
+    far = n_pages - case.n_pages
+    cache.data[far * cache.page_bytes:] = args["cache"].data
+    args["cache"] = cache
+    args["block_table"] = torch.where(args["block_table"] >= 0, args["block_table"] + far, args["block_table"])
+    assert torch.equal(vbq.kv4_attention_shared(**args), want)
+    # a fork of the first sequence, where only the last pages are free
+    i32 = dict(dtype=torch.int32, device="cuda")
+    refs = torch.ones(n_pages, **i32)
+    src = int(args["block_table"][0, 1])
+    dst = far + case.n_pages - 1 if src != far + case.n_pages - 1 else far + case.n_pages - 2
+    refs[dst] = 0
+    table, lens, counts = vbq.kv4_fork(cache, refs, args["block_table"][:1].contiguous(), args["kv_lens"][:1].contiguous(),
+                                       torch.zeros(2, **i32))
+    assert table[1, 1] == dst and table[0, 1] == src and table[1, 0] == table[0, 0]
+    assert counts[dst] == 1 and counts[int(table[0, 0])] == 2
+    blocks = -(-(1540 - 1024) // 32) * 2304
+    pages = cache.data.view(n_pages, -1)
+    assert torch.equal(pages[dst, :blocks], pages[src, :blocks])
+    assert cache.check() is False
