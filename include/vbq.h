@@ -549,7 +549,8 @@ vbq_status kv4_fork(const vbq_kv4* cache, const vbq_kv4_fork* f, hipStream_t str
  * looked at; max_own is: no sequence holds more tokens beyond its group's shared ones.
  * A sequence for whose group or itself numbers do not fit is left out (FLAG_LENGTH).
  * The arithmetic is kv4_attention's, with the rows of a group together in place of a
- * sequence's for the shared tokens; sums of both kinds are joined in fp32.
+ * sequence's for the shared tokens; sums of both kinds are joined in fp32. Where the
+ * stated sizes are so small that it takes less time, sequences read the shared tokens one by one.
  * workspace: as for kv4_attention, of kv4_attention_shared_workspace() bytes, the first
  * 8 * VBQ_KV4_COUNTERS of them zero before the first call that uses it. */
 typedef struct vbq_kv4_groups {

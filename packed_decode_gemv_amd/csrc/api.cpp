@@ -241,7 +241,19 @@ struct SharedPlan {
   KvAttnPlan shared, own;
   int64_t own_sums, own_ml, sums, ml, own_acc, own_acc_ml, acc, acc_ml, bytes;
   int32_t max_shared, max_own;       // whole blocks, and what rounding leaves to the sequences
+  bool each;                         // sequence by sequence
 };
+// Up to so many blocks in all (a block of 32 tokens for each sequence and head that reads
+// it), and with up to 32 rows a sequence and head, each sequence reads the shared tokens
+// for itself: they come from the caches, and one launch without sums in between takes
+// less than the tiles' start and join. Both ways, us (first: each for itself), 100 own tokens:
+// 1 x 8 sequences x 8 heads of 128 with 4 rows, 512 shared tokens 10.9 and 16.6, 8192
+// (16640 blocks) 20.7 and 28.0; 1 x 32, 2048 (17000) 20.6 and 22.1, 4096 (33500) 29.3 and
+// 23.5; 1 x 64, 2048 (34000) 26.5 and 23.8; 8 x 8, 1024 (18000) 17.1 and 23.7, 2048
+// (34000) 26.9 and 24.6; 64 x 12 heads of 64, 1 row, 1024 (27000) 15.0 and 15.8, 2048
+// (51000) 23.4 and 16.7; 8 x 12 heads of 64, 2048 (6500) 12.4 and 12.7, 4096 (12600) 15.5 and 14.2;
+// 16 x 4 heads of 256, 8192 (16600) 30.8 and 31.7.
+constexpr int64_t kEachBlocks = 20000;
 static vbq_status check_shared(const vbq_kv4* cache, const vbq_kv4_attn* a, const vbq_kv4_groups* g, bool pointers,
                                KvCache* c, SharedPlan* p) {
   if (!a || !g || g->reserved != 0) return VBQ_ERR_INVALID_ARG;
@@ -256,6 +268,19 @@ static vbq_status check_shared(const vbq_kv4* cache, const vbq_kv4_attn* a, cons
   int64_t bytes = 0;
   vbq_status st = check_attn(cache, &part, pointers, c, &p->own, &bytes);
   if (st != VBQ_OK) return st;
+  p->each = false;
+  const int64_t blocks = ((int64_t)p->max_shared + p->max_own + kKvBlock - 1) / kKvBlock;
+  if (p->own.rows <= 32 && blocks * a->batch * cache->n_kv_heads <= kEachBlocks) {
+    part.max_kv = p->max_shared + p->max_own;
+    st = check_attn(cache, &part, pointers, c, &p->own, &bytes);
+    if (st != VBQ_OK) return st;
+    p->each = true;
+    p->own_sums = p->own_ml = p->sums = p->ml = p->acc = p->acc_ml = 0;
+    p->own_acc = 2 * VBQ_KV4_COUNTERS;   // (where a call of the other kind has its own)
+    p->own_acc_ml = p->own_acc + p->own.places * p->own.rows * cache->head_dim;
+    p->bytes = 4 * (p->own_acc_ml + p->own.places * p->own.rows * 2);
+    return VBQ_OK;
+  }
   part.batch = g->n_groups;
   part.max_q = std::min(g->max_group_q, a->total_q);
   part.max_kv = p->max_shared;
@@ -329,10 +354,10 @@ vbq_status kv4_attention_shared(const vbq_kv4* cache, const vbq_kv4_attn* a, con
   shared.acc = w + p.acc;
   shared.ml = w + p.acc_ml;
   switch (own.cache.groups) {
-    case 1: return from_hip(launch_kv4_attention_shared_g1(shared, p.shared, own, p.own, stream));
-    case 2: return from_hip(launch_kv4_attention_shared_g2(shared, p.shared, own, p.own, stream));
-    case 3: return from_hip(launch_kv4_attention_shared_g3(shared, p.shared, own, p.own, stream));
-    default: return from_hip(launch_kv4_attention_shared_g4(shared, p.shared, own, p.own, stream));
+    case 1: return from_hip(launch_kv4_attention_shared_g1(shared, p.shared, own, p.own, p.each, stream));
+    case 2: return from_hip(launch_kv4_attention_shared_g2(shared, p.shared, own, p.own, p.each, stream));
+    case 3: return from_hip(launch_kv4_attention_shared_g3(shared, p.shared, own, p.own, p.each, stream));
+    default: return from_hip(launch_kv4_attention_shared_g4(shared, p.shared, own, p.own, p.each, stream));
   }
 }
 

@@ -108,14 +108,14 @@ struct KvAttnPlan {
 KvAttnPlan kv4_attn_plan(int batch, int heads, int ratio, int groups, int total_q, int max_q, int max_kv, int window,
                          int sinks);
 hipError_t launch_kv4_attention(const KvAttn& a, const KvAttnPlan& p, hipStream_t s);
-// (see kvshared.h) for heads of 64, 128, 192 and 256 channels.
+// (see kvshared.h) for heads of 64, 128, 192 and 256 channels. each: one launch, `own` over all tokens.
 hipError_t launch_kv4_attention_shared_g1(const KvAttn& shared, const KvAttnPlan& sp, const KvAttn& own,
-                                          const KvAttnPlan& op, hipStream_t s);
+                                          const KvAttnPlan& op, bool each, hipStream_t s);
 hipError_t launch_kv4_attention_shared_g2(const KvAttn& shared, const KvAttnPlan& sp, const KvAttn& own,
-                                          const KvAttnPlan& op, hipStream_t s);
+                                          const KvAttnPlan& op, bool each, hipStream_t s);
 hipError_t launch_kv4_attention_shared_g3(const KvAttn& shared, const KvAttnPlan& sp, const KvAttn& own,
-                                          const KvAttnPlan& op, hipStream_t s);
+                                          const KvAttnPlan& op, bool each, hipStream_t s);
 hipError_t launch_kv4_attention_shared_g4(const KvAttn& shared, const KvAttnPlan& sp, const KvAttn& own,
-                                          const KvAttnPlan& op, hipStream_t s);
+                                          const KvAttnPlan& op, bool each, hipStream_t s);
 
 }  // namespace vbq

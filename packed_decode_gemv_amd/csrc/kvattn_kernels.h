@@ -266,8 +266,9 @@ __device__ inline f32x2 get2(const float* p) {
 // Whose tokens a launch takes: kAll, a sequence's; for attention with shared tokens
 // kShared, those that a group of sequences has in common (whole blocks), for the rows
 // of all of them; kOwn, a sequence's others. The sums of both stay in the workspace and
-// are joined afterwards (see kvshared.h).
-enum Part { kAll, kShared, kOwn };
+// are joined afterwards (see kvshared.h). kEach: a sequence's tokens, shared ones too, for
+// its own rows alone.
+enum Part { kAll, kShared, kOwn, kEach };
 
 // A sequence of the call as the kernels see it (kShared: a group).
 struct Seq {
@@ -275,6 +276,7 @@ struct Seq {
   Reach re;
   int32_t blocks;               // that any of its rows sees
   int32_t row;                  // of the table
+  int32_t shared, shared_row;   // kEach: first blocks that are another row's
 };
 // False (and nothing to do) for numbers that do not fit.
 __device__ inline bool seq_from(const KvAttn& a, int c0, int c1, int len, Seq& s) {
@@ -357,8 +359,10 @@ __device__ inline bool seq_at(const KvAttn& a, int b, Seq& s) {
       s.nq = (int32_t)nq;
       s.len = len;
       s.first = len - s.nq;
-      s.re.w0 = from / kKvBlock;
+      s.re.w0 = PART == kEach ? 0 : from / kKvBlock;
       s.re.nw = s.blocks = (len + kKvBlock - 1) / kKvBlock - s.re.w0;
+      s.shared = from / kKvBlock;
+      s.shared_row = g.g0;
       return true;
     }
   }
@@ -413,13 +417,13 @@ __device__ inline void answer4(const KvAttn& a, int c0, int head, int r, int c, 
 // head of 64 with 16 rows: 450 parts 72 us, 64 parts 30, 32 parts 38; 16384
 // tokens of 8 heads of 128 with 4 rows: 64 parts 22.6, 23 parts 17.3).
 struct Lanes {   // lane l: sequence base + l
-  int32_t base, c0, nq, len, ns, w0, blocks, row;
+  int32_t base, c0, nq, len, ns, w0, blocks, row, shared, shared_row;
 };
 template <Part PART>
 __device__ inline void lanes_load(const KvAttn& a, uint32_t lane, int base, bool report, Lanes& l) {
   const int b = base + (int)lane;
   Seq s;
-  s.c0 = s.nq = s.len = s.blocks = s.row = 0;
+  s.c0 = s.nq = s.len = s.blocks = s.row = s.shared = s.shared_row = 0;
   s.re = Reach{0, 0, 0};
   if (b < a.batch && !seq_at<PART>(a, b, s)) {
     s.nq = PART == kOwn ? -1 : 0;
@@ -434,6 +438,8 @@ __device__ inline void lanes_load(const KvAttn& a, uint32_t lane, int base, bool
   l.w0 = s.re.w0;
   l.blocks = s.blocks;
   l.row = s.row;
+  l.shared = s.shared;
+  l.shared_row = s.shared_row;
 }
 
 // STAGES blocks a wavefront in LDS, STAGES - 1 of them on their way. Where
@@ -470,7 +476,7 @@ __device__ __forceinline__ void few_rows(const KvAttn& a, uint8_t* const ring, f
   const uint32_t ring_lds = lds_addr(own_ring);
 
   // This workgroup's part: blocks i0 .. i1 - 1 of a tile.
-  int b, head, i0 = 0, i1, blocks, c0, nq, len, row, part_no = 0, parts = 1;
+  int b, head, i0 = 0, i1, blocks, c0, nq, len, row, shared = 0, shared_row = 0, part_no = 0, parts = 1;
   Reach re;
   if (a.parts) {
     Lanes ln;
@@ -522,6 +528,10 @@ __device__ __forceinline__ void few_rows(const KvAttn& a, uint8_t* const ring, f
     nq = __builtin_amdgcn_readlane(ln.nq, at);
     len = __builtin_amdgcn_readlane(ln.len, at);
     row = PART == kShared ? __builtin_amdgcn_readlane(ln.row, at) : b;
+    if constexpr (PART == kEach) {
+      shared = __builtin_amdgcn_readlane(ln.shared, at);
+      shared_row = __builtin_amdgcn_readlane(ln.shared_row, at);
+    }
     re.ns = __builtin_amdgcn_readlane(ln.ns, at);
     re.w0 = __builtin_amdgcn_readlane(ln.w0, at);
     parts = __builtin_amdgcn_readlane(n, at);
@@ -545,6 +555,7 @@ __device__ __forceinline__ void few_rows(const KvAttn& a, uint8_t* const ring, f
       return;
     }
     c0 = sq.c0, nq = sq.nq, len = sq.len, re = sq.re, blocks = sq.blocks, row = sq.row;
+    if constexpr (PART == kEach) shared = sq.shared, shared_row = sq.shared_row;
     if (nq == 0) return;
     i1 = blocks;
   }
@@ -580,7 +591,8 @@ __device__ __forceinline__ void few_rows(const KvAttn& a, uint8_t* const ring, f
       int page = 0;
       bool bad = false;
       if (next < i1) {
-        page = a.table[(int64_t)row * a.width + (blk >> a.cache.block_shift)];
+        page = a.table[(int64_t)(PART == kEach && blk < shared ? shared_row : row) * a.width +
+                       (blk >> a.cache.block_shift)];
         bad = (uint32_t)page >= (uint32_t)a.cache.n_pages;
       }
       if (bad) {

@@ -7,6 +7,7 @@
 // tokens, one or two a CU), the second short, and fill the places that are left. All
 // sums go to the workspace, and a second launch joins a row's and answers it. Where a
 // sequence's own rows need the kernel for many rows, the two kinds take a launch each.
+// Small calls are one launch of the kernel for few rows, sequence by sequence.
 #pragma once
 
 #include "kvattn_kernels.h"
@@ -146,8 +147,12 @@ void launch_both(const KvAttn& sh, const KvAttnPlan& sp, const KvAttn& own, cons
 }
 
 template <int G>
-hipError_t launch_shared(const KvAttn& sh, const KvAttnPlan& sp, const KvAttn& own, const KvAttnPlan& op,
+hipError_t launch_shared(const KvAttn& sh, const KvAttnPlan& sp, const KvAttn& own, const KvAttnPlan& op, bool each,
                          hipStream_t s) {
+  if (each) {
+    launch_few<kEach, G>(own, op, s);
+    return hipGetLastError();
+  }
   const bool tile = sp.rows == kRowTile, any = sp.grid > 0 && sh.max_kv > 0;
   if (any && op.rows <= 16 && (tile || sp.rows >= op.rows)) {
     if (op.rows == 4) launch_both<G, 4>(sh, sp, own, op, s);

@@ -103,8 +103,10 @@ def test_shared_attention_refuses_bad_arguments():
         x, y = pair(dict(a), dict(g))
         return vbq.lib.kv4_attention_shared_workspace(C.byref(c), C.byref(x), C.byref(y))
 
-    assert size() >= 4 * 4 * 8 * 130 + 8 * 2048
-    assert size(g=dict(max_shared=0)) < size()
+    far = dict(max_shared=1 << 22)                    # too many tokens for each sequence to read them for itself
+    assert size(g=far) >= 4 * 4 * 8 * 130 + 8 * 2048
+    assert 8 * 2048 <= size(g=dict(max_shared=0)) <= size() < size(g=far)
+    assert size(a=dict(n_heads=2 * 33)) > 8 * 2048    # more rows than the kernel for few takes
     for bad, st in ((dict(window=5), 1), (dict(sinks=1), 1), (dict(batch=0), 2), (dict(n_heads=7), 2), (dict(max_q=-1), 2),
                     (dict(batch=65536), 5), (dict(dtype=2), 1), (dict(causal=2), 1), (dict(scale=0.0), 1)):
         assert run(a=bad) == st and size(a=bad) == -1, bad

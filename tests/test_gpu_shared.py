@@ -73,28 +73,30 @@ class Case:
         self.q = torch.from_numpy(rng.normal(0, gain, (T, heads * ratio, dim)).astype(np.float32)).to(getattr(torch, dtype))
         self.group_q = max([0] + [sum(n for _, n in m) for _, m in groups])
 
-    def args(self, vbq):
+    def args(self, vbq, far=False):
+        """far: a bound on the shared tokens that makes the rows of a group take them together."""
         cache = vbq.Kv4Cache(self.n_pages, self.page, self.heads, self.dim, data=gpu(self.cache_data))
         return dict(cache=cache, q=self.q.cuda(), block_table=gpu(self.table), kv_lens=gpu(np.array(self.lens, np.int32)),
                     cu_q=gpu(cum(self.news)), cu_groups=gpu(self.cu_groups), shared=gpu(np.array(self.shared, np.int32)),
-                    max_q=max(self.news), max_shared=max(self.shared), max_own=self.own, max_group_q=self.group_q)
+                    max_q=max(self.news), max_shared=1 << 22 if far else max(self.shared), max_own=self.own, max_group_q=self.group_q)
 
     def want(self, scale=None, causal=True):
         return reference(Layout(self.page, self.heads, self.dim), self.data, self.full, self.lens, self.news,
                          self.q.double().numpy(), self.dim ** -0.5 if scale is None else scale, causal, 0, 0)
 
 
-def attend(vbq, case, scale=None, causal=True, **kw):
+def attend(vbq, case, scale=None, causal=True):
+    """Both ways to take the shared tokens, against the reference."""
     import torch
-    args = case.args(vbq)
-    args.update(kw)
-    lse = torch.full(case.q.shape[:2], float("nan"), device="cuda")
-    out = vbq.kv4_attention_shared(**args, scale=scale, causal=causal, lse=lse)
-    assert args["cache"].check() is False
     want = case.want(scale, causal)
-    check(out.double().cpu().numpy(), want[0], want[2], want[3], case.dtype, case.dim)
-    tol = (case.dim + 40) * 2.0 ** -24 * (want[3] + np.abs(want[1]) + 30)
-    assert (np.abs(lse.cpu().numpy() - want[1]) <= tol).all()
+    for far in (False, True):
+        args = case.args(vbq, far)
+        lse = torch.full(case.q.shape[:2], float("nan"), device="cuda")
+        out = vbq.kv4_attention_shared(**args, scale=scale, causal=causal, lse=lse)
+        assert args["cache"].check() is False
+        check(out.double().cpu().numpy(), want[0], want[2], want[3], case.dtype, case.dim)
+        tol = (case.dim + 40) * 2.0 ** -24 * (want[3] + np.abs(want[1]) + 30)
+        assert (np.abs(lse.cpu().numpy() - want[1]) <= tol).all()
     return args, out, lse
 
 
@@ -155,7 +157,8 @@ def test_results_repeat_and_strides_and_workspaces_change_nothing(vbq):
     rng = np.random.default_rng(5)
     for groups in ([(1500, [(40, 1)] * 6)], [(900, [(40, 5)] * 10), (64, [(33, 2)])]):
         case = Case(rng, 2, 4, 128, 64, groups)
-        args, out, lse = attend(vbq, case)
+        _, out, lse = attend(vbq, case)
+        args = case.args(vbq, True)
         n = len(case.lens)
         ws = vbq.kv4_attention_shared_workspace(args["cache"], n, len(groups), len(case.q), 8, args["max_q"],
                                                 args["max_shared"], args["max_own"], args["max_group_q"])
@@ -163,8 +166,11 @@ def test_results_repeat_and_strides_and_workspaces_change_nothing(vbq):
         wide = torch.zeros(len(case.q), 11, 128, dtype=torch.float16, device="cuda")
         wide[:, 2:10] = args["q"]
         args["q"] = wide[:, 2:10]
+        near = dict(args, max_shared=max(case.shared))        # the other way, with the same workspace
+        alone = vbq.kv4_attention_shared(**near)
         for _ in range(3):
             assert torch.equal(vbq.kv4_attention_shared(**args, workspace=ws), out)
+            assert torch.equal(vbq.kv4_attention_shared(**near, workspace=ws), alone)
 
 
 def test_scores_far_out_and_special_queries(vbq):
@@ -173,22 +179,23 @@ def test_scores_far_out_and_special_queries(vbq):
     for count in (4, 40):
         case = Case(rng, 1, 4, 64, 32, [(200, [(9, 1)] * count)], "bfloat16", gain=20.0)
         attend(vbq, case)
-        args = case.args(vbq)
-        clean = vbq.kv4_attention_shared(**args)
-        args["q"][1, 2] = float("nan")
-        args["q"][3, 0, 5] = float("inf")
-        got = vbq.kv4_attention_shared(**args)
-        hurt = torch.zeros(got.shape[:2], dtype=torch.bool, device="cuda")
-        hurt[1, 2] = hurt[3, 0] = True
-        assert not got[hurt].isfinite().any() and torch.equal(got[~hurt], clean[~hurt])
+        for far in (False, True):
+            args = case.args(vbq, far)
+            clean = vbq.kv4_attention_shared(**args)
+            args["q"][1, 2] = float("nan")
+            args["q"][3, 0, 5] = float("inf")
+            got = vbq.kv4_attention_shared(**args)
+            hurt = torch.zeros(got.shape[:2], dtype=torch.bool, device="cuda")
+            hurt[1, 2] = hurt[3, 0] = True
+            assert not got[hurt].isfinite().any() and torch.equal(got[~hurt], clean[~hurt])
 
 
 def test_shared_pages_that_are_missing_count_as_hidden(vbq):
     import torch
     rng = np.random.default_rng(7)
-    for count in (3, 40):
+    for count, far in ((3, False), (3, True), (40, True), (40, False)):
         case = Case(rng, 1, 4, 64, 32, [(2300, [(5, 1)] * count)])
-        args = case.args(vbq)
+        args = case.args(vbq, far)
         holed = case.table.copy()
         lost = [0, 1, 7, 62, 63, 64, 65, 70]
         holed[0, lost] = [-1, case.n_pages, 2 ** 31 - 1, -5, case.n_pages + 7, -1, -2 ** 31, case.n_pages]
@@ -198,7 +205,7 @@ def test_shared_pages_that_are_missing_count_as_hidden(vbq):
             args["cache"].check()
         # the same tokens by a table without the holes
         keep = [j for j in range(2300 // 32) if j not in lost]
-        args = case.args(vbq)
+        args = case.args(vbq, far)
         tight = np.full_like(case.table, -1)
         moved = len(lost)
         tight[0, :len(keep)] = case.table[0, keep]
@@ -215,16 +222,17 @@ def test_shared_pages_that_are_missing_count_as_hidden(vbq):
 def test_what_does_not_fit_is_left_out(vbq):
     import torch
     rng = np.random.default_rng(8)
-    for page, ratio in ((32, 2), (64, 16)):
+    for page, ratio, far in ((32, 2, False), (32, 2, True), (64, 16, True), (64, 16, False), (64, 40, True)):
         case = Case(rng, 1, ratio, 64, page, [(100, [(9, 1), (12, 2), (5, 1)]), (40, [(20, 1)] * 3), (64, [(5, 1)])],
                     alone=([(9, 1)], []))
-        clean = vbq.kv4_attention_shared(**case.args(vbq))
+        clean = vbq.kv4_attention_shared(**case.args(vbq, far))
         rows = cum(case.news)
-        for key, at, value, gone in (("shared", 0, 101, (1, 2, 3)), ("shared", 0, -1, (1, 2, 3)), ("shared", 1, 61, (4, 5, 6)),
+        for key, at, value, gone in (("shared", 0, 105 if far else 101, (3,) if far else (1, 2, 3)),
+                                     ("shared", 0, -1, (1, 2, 3)), ("shared", 1, 61, (4, 5, 6)),
                                      ("kv_lens", 2, 101, (2,)), ("kv_lens", 2, -1, (2,)), ("kv_lens", 4, 10 ** 6, (4,)),
                                      ("kv_lens", 7, 64 + 60, (7,)), ("cu_groups", 3, 9, (7,)),
                                      ("cu_groups", 2, -3, (4, 5, 6, 7)), ("cu_groups", 0, -1, (1, 2, 3, 0))):
-            args = case.args(vbq)
+            args = case.args(vbq, far)
             args[key][at] = value
             out = torch.full_like(clean, 7.0)
             vbq.kv4_attention_shared(**args, out=out)
@@ -234,9 +242,9 @@ def test_what_does_not_fit_is_left_out(vbq):
                 mine = slice(int(rows[b]), int(rows[b + 1]))
                 if b in gone:
                     assert (out[mine] == 7.0).all(), (key, at, value, b)
-                elif key != "cu_groups":
+                elif key != "cu_groups" and not (key == "shared" and far and b in (1, 2)):
                     assert torch.equal(out[mine], clean[mine]), (key, at, value, b)
-        args = case.args(vbq)
+        args = case.args(vbq, far)
         args["max_group_q"] = 3                # the first group has 4
         out = vbq.kv4_attention_shared(**args, out=torch.full_like(clean, 7.0))
         assert (out[1:5] == 7.0).all() and int(args["cache"].flags.item()) == 2
@@ -246,10 +254,10 @@ def test_what_does_not_fit_is_left_out(vbq):
 def test_in_a_graph_while_sequences_grow(vbq):
     import torch
     rng = np.random.default_rng(9)
-    for count, heads, dim in ((6, 2, 128), (40, 1, 64)):
+    for count, heads, dim, far in ((6, 2, 128, False), (6, 2, 128, True), (40, 1, 64, True)):
         case = Case(rng, heads, 4, dim, 64, [(700, [(120, 1)] * count)])
-        args = case.args(vbq)
-        ws = vbq.kv4_attention_shared_workspace(args["cache"], count, 1, count, 4 * heads, 1, 700, 120, count)
+        args = case.args(vbq, far)
+        ws = vbq.kv4_attention_shared_workspace(args["cache"], count, 1, count, 4 * heads, 1, args["max_shared"], 120, count)
         out = torch.zeros_like(args["q"])
         lens = args["kv_lens"]
         lens -= 100
@@ -279,7 +287,7 @@ def test_agrees_with_attention_of_every_sequence_by_itself(vbq):
     for heads, ratio, dim, shared, count, new in ((8, 4, 128, 9000, 33, 1), (4, 1, 64, 20000, 5, 2), (2, 2, 256, 4000, 30, 1)):
         page = 64
         case = Case(rng, heads, ratio, dim, page, [(shared // page * page, [(int(n), new) for n in rng.integers(new, 500, count)])])
-        args = case.args(vbq)
+        args = case.args(vbq, True)
         got = vbq.kv4_attention_shared(**args)
         want = vbq.kv4_attention(args["cache"], args["q"], gpu(case.full), args["kv_lens"], args["cu_q"], new,
                                  max(case.lens))
@@ -309,9 +317,9 @@ def test_refusals(vbq):
 def test_rows_behind_the_last_sequence_stay(vbq):
     import torch
     rng = np.random.default_rng(12)
-    for count in (5, 40):
+    for count, far in ((5, False), (5, True), (40, True)):
         case = Case(rng, 1, 4, 64, 32, [(100, [(9, 1)] * count)])
-        args = case.args(vbq)
+        args = case.args(vbq, far)
         want = vbq.kv4_attention_shared(**args)
         args["q"] = torch.cat([args["q"], torch.full_like(args["q"][:3], float("nan"))])
         out = torch.full((count + 3, 4, 64), 7.0, dtype=torch.float16, device="cuda")
@@ -326,7 +334,7 @@ def test_calls_on_two_streams_at_once(vbq):
     rng = np.random.default_rng(13)
     case = Case(rng, 2, 4, 128, 64, [(1500, [(60, 1)] * 6)])
     big = Case(rng, 1, 4, 64, 32, [(900, [(30, 2)] * 40)])
-    a, b = case.args(vbq), big.args(vbq)
+    a, b = case.args(vbq, True), big.args(vbq, True)
     want = [vbq.kv4_attention_shared(**a), vbq.kv4_attention_shared(**b)]
     torch.cuda.synchronize()
     streams = [torch.cuda.Stream() for _ in range(2)]
@@ -347,13 +355,15 @@ def test_far_pages_of_a_large_cache(vbq):
     cache = vbq.Kv4Cache(n_pages, page, heads, dim)
     rng = np.random.default_rng(14)
     case = Case(rng, heads, 2, dim, page, [(1500, [(40, 1)] * 3)])
-    args = case.args(vbq)
-    want = vbq.kv4_attention_shared(**args)
+    args = case.args(vbq, True)
+    near = dict(args, max_shared=1500)
+    want, want_near = vbq.kv4_attention_shared(**args), vbq.kv4_attention_shared(**near)
     far = n_pages - case.n_pages
     cache.data[far * cache.page_bytes:] = args["cache"].data
     args["cache"] = cache
     args["block_table"] = torch.where(args["block_table"] >= 0, args["block_table"] + far, args["block_table"])
     assert torch.equal(vbq.kv4_attention_shared(**args), want)
+    assert torch.equal(vbq.kv4_attention_shared(**dict(args, max_shared=1500)), want_near)
     # a fork of the first sequence, where only the last pages are free
     i32 = dict(dtype=torch.int32, device="cuda")
     refs = torch.ones(n_pages, **i32)
