@@ -4,7 +4,9 @@
 // One launch takes both kinds of tokens: workgroups over the groups' shared tokens,
 // where the rows of all of a group's sequences make the tiles, then workgroups over the
 // sequences' own. The first are few and long (a tile is cut into parts along the
-// tokens, one or two a CU), the second short, and fill the places that are left. All
+// tokens, one or two a CU), the second short, and fill the places that are left (own
+// tokens first: 32 sequences over 8192 shared tokens 30.4 against 28.7 us, 6 groups of 16
+// with 3 queries 67.9 against 60.7). All
 // sums go to the workspace, and a second launch joins a row's and answers it. Where a
 // sequence's own rows need the kernel for many rows, the two kinds take a launch each.
 // Small calls are one launch of the kernel for few rows, sequence by sequence.
