@@ -11,6 +11,10 @@
 // their own the listed copies. Counts are sums of whole numbers by atomics, the same in
 // any order. Pages that are free before the call alone are given out, so no page that is
 // read is written.
+//
+// 512 sequences of 4001 tokens, 8 heads of 128 (26 MB of part pages, read and written):
+// the plan 6.4 us, a chain of dependent look-ups and scans by one workgroup, the rest 11.0,
+// copies at 4.8 TB/s. One sequence to eight: 5.0 and 3.6 us, look-ups alone.
 #include "kv4.h"
 
 namespace vbq {

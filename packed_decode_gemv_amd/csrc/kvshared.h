@@ -8,8 +8,19 @@
 // tokens first: 32 sequences over 8192 shared tokens 30.4 against 28.7 us, 6 groups of 16
 // with 3 queries 67.9 against 60.7). All
 // sums go to the workspace, and a second launch joins a row's and answers it. Where a
-// sequence's own rows need the kernel for many rows, the two kinds take a launch each.
+// sequence's own rows need the kernel for many rows, the two kinds take a launch each;
+// so they do where one workgroup of heads of 256 takes a CU and the own tokens' are more
+// than the CUs, as several of those fit a CU by themselves. Together and apart, us, groups of 32
+// sequences, 100 own tokens: 4 heads of 256, 2 groups of 8192 shared 56.4 and 57.3, 4 of 8192
+// 78.9 and 75.0, 16 of 4096 160 and 133; 8 heads of 128 with 4 rows, 6 of 8192 76.8 and 84.6,
+// 16 of 4096 120 and 116, 24 of 2048 130 and 131; of 192 with 2, 8 of 4096 87.4 and 93.9;
+// groups of 64, 12 heads of 64, 1 of 8192 20.9 and 27.0, 24 of 2048 169 and 196.
 // Small calls are one launch of the kernel for few rows, sequence by sequence.
+//
+// Measured, 32 heads of 128 on 8: 64 sequences over 65000 shared tokens (bf16) 117 us,
+// 0.58 PFLOP/s of products, bound by the loop over blocks (matrix units 30% busy, vector
+// instructions 51%); 32 over 8192 (fp16) 28.7 us, bound by a part's start (5 us), its eight
+// blocks (11), the store of its sums (3.5) and the join (6).
 #pragma once
 
 #include "kvattn_kernels.h"
@@ -51,7 +62,10 @@ __global__ __launch_bounds__(256, (kBothRoom<G, SHARED_ROWS>)) void k_kv4_attn_b
 // Joins a row's sums: of the parts of its group's shared tokens (TILE: as the kernel for
 // many rows leaves them; else one part), and of its sequence's own. Where there are many
 // parts, slices of a row's threads take every SLICESth, eight loads on their way at a
-// time. blockIdx.x is the tile as in the kernel for many rows.
+// time. blockIdx.x is the tile as in the kernel for many rows. Bound by reading the sums:
+// 34 MB of 32 parts 8.4 us, 17 MB 6.0. Whole calls by one and by four slices, us: 32 parts of
+// 8 tiles of heads of 128 31.5 and 28.6, 16 of 16 44.7 and 43.7, 10 of 48 76.5 and 76.8, 8 of 64
+// 95.1 and 96.8, 4 of 128 119.6 and 125.8; 32 of heads of 64 24.2 and 20.8, of 256 59.7 and 55.2.
 template <int G, bool TILE, int SLICES>
 __global__ __launch_bounds__(256) void k_kv4_attn_meet(KvAttn a, const float* own, const float* own_ml) {
   constexpr int D = 64 * G, LANES = D / 4, ROWS = 256 / (LANES * SLICES), AT_ONCE = TILE ? 8 : 1;
@@ -123,7 +137,7 @@ template <Part PART, int G>
 void launch_few(const KvAttn& a, const KvAttnPlan& p, hipStream_t s) {
   const dim3 grid((uint32_t)p.grid);
 #define VBQ_CALL(ROWS) k_kv4_attn<G, ROWS, kStages<G, ROWS>, PART><<<grid, (64 * kWaves<G, ROWS>), 0, s>>>(a)
-  if (p.rows == 4) VBQ_CALL(4);
+  if (PART != kShared && p.rows == 4) { if constexpr (PART != kShared) VBQ_CALL(4); }   // (shared: 8 at least)
   else if (p.rows == 8) VBQ_CALL(8);
   else if (G == 4 || p.rows == 16) VBQ_CALL(16);
   else if constexpr (G < 4) VBQ_CALL(32);
@@ -156,7 +170,8 @@ hipError_t launch_shared(const KvAttn& sh, const KvAttnPlan& sp, const KvAttn& o
     return hipGetLastError();
   }
   const bool tile = sp.rows == kRowTile, any = sp.grid > 0 && sh.max_kv > 0;
-  if (any && op.rows <= 16 && (tile || sp.rows >= op.rows)) {
+  const bool together = !(G == 4 && tile && op.grid > 256);   // (both sides measured above)
+  if (any && together && op.rows <= 16 && (tile || sp.rows >= op.rows)) {
     if (op.rows == 4) launch_both<G, 4>(sh, sp, own, op, s);
     else if (op.rows == 8) launch_both<G, 8>(sh, sp, own, op, s);
     else launch_both<G, 16>(sh, sp, own, op, s);

@@ -15,6 +15,11 @@
 // the first step the top-th largest of the lanes' own best is a bound that few pass.
 //   The wavefronts of a workgroup are joined in LDS, the workgroups of a row by the
 // last of them that finishes.
+//   Many rows are bound by memory: 2047 rows of 128256 fp32 logits (1.05 GB), top 5, take
+// 189 us, 5.6 TB/s, with vector instructions 60% of that time beside it (a bound
+// shared by a row's wavefronts 188 us, but 64 rows of 32001 18.7 for 17.7; registers for
+// six and eight wavefronts a SIMD 206 and 205). Few rows are a chain of one step and two
+// joins: one row of 128256, top 20, 13.3 us, of which the first step 3.5, the joins 2 each.
 #include "logprobs.h"
 
 namespace vbq {

@@ -143,6 +143,14 @@ def test_long_shared_and_own_tokens_are_cut(vbq, dim, count, ratio):
     attend(vbq, Case(rng, 1, ratio, dim, 32, [(1500, [(1100, 1)] + [(7, 1)] * (count - 1)), (900, [(30, 1)])]))
 
 
+@pytest.mark.parametrize("dim,new", [(256, 1), (256, 4), (128, 1)])
+def test_more_tiles_of_own_tokens_than_units(vbq, dim, new):
+    """Many tiles of own tokens, short and long, behind tiles of many rows over shared ones."""
+    rng = np.random.default_rng(dim + new)
+    groups = [(70, [(5, new)] * 30), (320, [(int(rng.integers(new, 90)), new) for _ in range(37)])]
+    attend(vbq, Case(rng, 4, 4, dim, 32, groups, "bfloat16"))
+
+
 def test_more_sequences_and_groups_than_lanes(vbq):
     rng = np.random.default_rng(4)
     groups = [(int(rng.integers(0, 90)), [(int(rng.integers(1, 50)), 1) for _ in range(int(rng.integers(0, 4)))])
