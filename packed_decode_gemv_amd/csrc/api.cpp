@@ -430,15 +430,18 @@ static ForkPlaces fork_places(int64_t n_pages, int64_t in, int64_t out, int64_t 
   p.end = up(p.free + 4 * std::min(n_pages, out * width));
   return p;
 }
-static vbq_status check_fork_sizes(int32_t in, int32_t out, int32_t width) {
+static vbq_status check_fork_sizes(const vbq_kv4* cache, int32_t in, int32_t out, int32_t width) {
   if (in < 1 || out < 1 || width < 1) return VBQ_ERR_SHAPE;
-  if (in > 65535 || out > 65535 || width > (1 << 20)) return VBQ_ERR_UNSUPPORTED;
+  if (in > 65535 || out > 65535 || width > (1 << 20) ||
+      kv4_page_bytes(cache->page_tokens, cache->n_kv_heads, cache->head_dim) > kMaxForkPage)
+    return VBQ_ERR_UNSUPPORTED;
   return VBQ_OK;
 }
 
 int64_t kv4_fork_workspace(const vbq_kv4* cache, int32_t batch_in, int32_t batch_out, int32_t table_width) {
   KvCache c;
-  if (check_cache(cache, false, &c) != VBQ_OK || check_fork_sizes(batch_in, batch_out, table_width) != VBQ_OK) return -1;
+  if (check_cache(cache, false, &c) != VBQ_OK || check_fork_sizes(cache, batch_in, batch_out, table_width) != VBQ_OK)
+    return -1;
   return fork_places(c.n_pages, batch_in, batch_out, table_width).end;
 }
 
@@ -447,9 +450,7 @@ vbq_status kv4_fork(const vbq_kv4* cache, const vbq_kv4_fork* a, hipStream_t str
   vbq_status st = check_cache(cache, true, &f.cache);
   if (st != VBQ_OK) return st;
   if (!a || a->reserved != 0) return VBQ_ERR_INVALID_ARG;
-  st = check_fork_sizes(a->batch_in, a->batch_out, a->table_width);
-  if (st == VBQ_OK && kv4_page_bytes(cache->page_tokens, cache->n_kv_heads, cache->head_dim) > kMaxForkPage)
-    st = VBQ_ERR_UNSUPPORTED;
+  st = check_fork_sizes(cache, a->batch_in, a->batch_out, a->table_width);
   if (st != VBQ_OK) return st;
   if (!a->table_in || !a->lens_in || !a->refs_in || !a->parents || !a->table_out || !a->lens_out || !a->refs_out ||
       !a->workspace)

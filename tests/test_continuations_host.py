@@ -68,7 +68,8 @@ def test_fork_sizes_and_refusals():
         return vbq.lib.kv4_fork(cache and C.byref(cache), C.byref(vbq.vbq_kv4_fork(**d)), None)
 
     assert run(cache=None) == 1 and run(reserved=1) == 1
-    assert run(cache=_cache(vbq, page_tokens=65536, n_kv_heads=4096, head_dim=256)) == 5      # pages of 77 GB
+    large = _cache(vbq, page_tokens=65536, n_kv_heads=4096, head_dim=256)      # pages of 77 GB
+    assert run(cache=large) == 5 and size(C.byref(large), 2, 3, 4) == -1
     for bad, st in ((dict(batch_in=0), 2), (dict(batch_out=65536), 5), (dict(table_width=0), 2),
                     (dict(table_width=(1 << 20) + 1), 5), (dict(workspace_bytes=15), 6)):
         assert run(**bad) == st, bad

@@ -151,6 +151,22 @@ def test_more_tiles_of_own_tokens_than_units(vbq, dim, new):
     attend(vbq, Case(rng, 4, 4, dim, 32, groups, "bfloat16"))
 
 
+@pytest.mark.parametrize("dim,new", [(64, 1), (128, 3), (192, 1), (256, 9)])
+def test_less_than_a_block_in_common_and_far_bounds_of_own_tokens(vbq, dim, new):
+    """Nothing is taken together, and the sequences' bound is too large to take them as small."""
+    import torch
+    rng = np.random.default_rng(dim + new)
+    case = Case(rng, 2, 4, dim, 32, [(31, [(new, new), (700, new)]), (0, [(50, new)]), (1, [(32, new)] * 3)], "bfloat16")
+    want = case.want()
+    args = {**case.args(vbq), "max_own": 1 << 22}
+    lse = torch.full(case.q.shape[:2], float("nan"), device="cuda")
+    out = vbq.kv4_attention_shared(**args, lse=lse)
+    assert args["max_shared"] == 31 and args["cache"].check() is False
+    check(out.double().cpu().numpy(), want[0], want[2], want[3], case.dtype, case.dim)
+    tol = (case.dim + 40) * 2.0 ** -24 * (want[3] + np.abs(want[1]) + 30)
+    assert (np.abs(lse.cpu().numpy() - want[1]) <= tol).all()
+
+
 def test_more_sequences_and_groups_than_lanes(vbq):
     rng = np.random.default_rng(4)
     groups = [(int(rng.integers(0, 90)), [(int(rng.integers(1, 50)), 1) for _ in range(int(rng.integers(0, 4)))])
