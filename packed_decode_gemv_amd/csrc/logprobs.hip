@@ -16,9 +16,10 @@
 //   The wavefronts of a workgroup are joined in LDS, the workgroups of a row by the
 // last of them that finishes.
 //   Many rows are bound by memory: 2047 rows of 128256 fp32 logits (1.05 GB), top 5, take
-// 189 us, 5.6 TB/s, with vector instructions 60% of that time beside it (a bound
-// shared by a row's wavefronts 188 us, but 64 rows of 32001 18.7 for 17.7; registers for
-// six and eight wavefronts a SIMD 206 and 205). Few rows are a chain of one step and two
+// 185 us, 5.7 TB/s, with vector instructions 60% of that time beside it (189 with a row's
+// first and last logits loaded in the step that takes them; then a bound shared by a row's
+// wavefronts 188, but 64 rows of 32001 18.7 and 19.2 for 17.7; registers for six and eight
+// wavefronts a SIMD 206 and 205). Few rows are a chain of one step and two
 // joins: one row of 128256, top 20, 13.3 us, of which the first step 3.5, the joins 2 each.
 #include "logprobs.h"
 
@@ -311,6 +312,9 @@ __global__ __launch_bounds__(64 * kWaves) void k_token_logprobs(Logprobs a) {
   // Steps of this wavefront, those of whole loads first; the row's first and last logits,
   // one a lane, are the step after the last of them.
   bool edges = (head || tail) && steps % stride == split * ROW_WAVES + (ROW_WAVES == 1 ? 0 : wave);
+  float edge_value = -__builtin_inff();
+  const uint32_t edge_at = (int)lane < head ? lane : (uint32_t)(a.vocab - (head + tail)) + lane;
+  if (edges && (int)lane < head + tail) edge_value = value_at<DT>(x, edge_at);
   while (j < steps || edges) {
     float v[kPer];
     uint32_t at, first;        // the lane's first logit, the step's
@@ -320,11 +324,11 @@ __global__ __launch_bounds__(64 * kWaves) void k_token_logprobs(Logprobs a) {
     if (edge) {
       left = head + tail;
       first = 0;
-      at = (int)lane < head ? lane : (uint32_t)(a.vocab - left) + lane;
+      at = edge_at;
       values = 1;
 #pragma unroll
-      for (int i = 0; i < kPer; ++i) v[i] = -__builtin_inff();
-      if ((int)lane < left) v[0] = value_at<DT>(x, at);
+      for (int i = 1; i < kPer; ++i) v[i] = -__builtin_inff();
+      v[0] = edge_value;
       edges = false;
     } else {
       const int v0 = j * (64 * VECS);
