@@ -1,4 +1,4 @@
-// Forks of cached sequences (meaning in vbq.h): two launches.
+// Forks of cached sequences (meaning in vbq.h): two launches, or one for small calls.
 //
 // k_kv4_fork_plan: its first workgroup counts each old sequence's continuations and
 // finds the first of them, counts the pages that every new sequence needs, lists the
@@ -15,6 +15,14 @@
 // 512 sequences of 4001 tokens, 8 heads of 128 (26 MB of part pages, read and written):
 // the plan 6.4 us, a chain of dependent look-ups and scans by one workgroup, the rest 11.0,
 // copies at 4.8 TB/s. One sequence to eight: 5.0 and 3.6 us, look-ups alone.
+//
+// k_kv4_fork_small: where the plan is short every workgroup makes it by itself, so that
+// none waits for another's and one launch does. Counts are then summed in LDS, a slice of
+// the pages a workgroup. In one and in two launches (us, in a graph; from Python 10.5 and
+// 13.1): 1 sequence of 577 tokens to 8, 12 heads of 64, 200 pages 6.6 and 8.1, 60000 pages
+// 7.3 and 8.3; 8 of 2000 to 8, 8 heads of 128 4.8 and 6.3; 16 of 1000 to 64 8.7 and 9.0; 64 to
+// 64 of 1000 6.0 and 6.7, of 4000 (4032 entries) 7.0 and 6.8; 128 of 2000 7.5 and 6.8; 1 of 250
+// to 128 11.3 and 10.1.
 #include "kv4.h"
 
 namespace vbq {
@@ -23,6 +31,8 @@ namespace {
 constexpr int kPlan = 1024;                  // threads of the planning workgroup
 constexpr int kPlanKids = 4096;              // old sequences that it counts in LDS
 constexpr int kScan = 16;                    // counts that a thread looks at, at a time
+// Of small calls: sequences, entries of their rows, pages; of a workgroup's counts; workgroups that copy.
+constexpr int kSmallBatch = 64, kSmallRows = 4096, kSmallPages = 65536, kSmallCounts = 4096, kSmallCopiers = 192;
 
 // Of a new sequence: what it goes on from.
 struct Parent {
@@ -75,6 +85,7 @@ __device__ inline bool keeps(const KvFork& f, int p, int j, int32_t& page) {
 }
 
 // Inclusive sum over the workgroup; total to every thread. sums: a place a wavefront.
+// (WAVES 1: over a wavefront by itself.)
 template <int WAVES>
 __device__ inline int group_scan(int v, int* sums, int& total) {
   const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
@@ -84,6 +95,10 @@ __device__ inline int group_scan(int v, int* sums, int& total) {
   v += __builtin_amdgcn_update_dpp(0, v, 0x118, 0xF, 0xF, true);   // row_shr:8
   v += __builtin_amdgcn_update_dpp(0, v, 0x142, 0xA, 0xF, false);  // row_bcast:15 into rows 1 and 3
   v += __builtin_amdgcn_update_dpp(0, v, 0x143, 0xC, 0xF, false);  // row_bcast:31 into rows 2 and 3
+  if constexpr (WAVES == 1) {
+    total = __builtin_amdgcn_readlane(v, 63);
+    return v;
+  }
   if (lane == 63) sums[wave] = v;
   __syncthreads();
   int before = 0;
@@ -98,24 +113,20 @@ __device__ inline int group_scan(int v, int* sums, int& total) {
   return v + before;
 }
 
+// Places for what the planning workgroup finds (see KvFork), its counts in LDS or not.
+struct Plan {
+  int *first, *kids, *sums, *copied;
+  int4* copies;
+  int32_t *offset, *free;
+};
+// Continuations, pages, copies and free pages; the first `found` of the pages `wanted`
+// are there. Flags are set where `tells`.
 template <bool IN_LDS>
-__global__ __launch_bounds__(kPlan) void k_kv4_fork_plan(KvFork f) {
+__device__ inline void plan(const KvFork& f, const Plan& at, bool tells, int& found, int64_t& wanted) {
   const int tid = (int)threadIdx.x;
-  if (blockIdx.x) {   // the counts as they were
-    const int64_t n = f.cache.n_pages;
-    for (int64_t i = ((int64_t)(blockIdx.x - 1) * kPlan + tid) * 4; i < n; i += (int64_t)(gridDim.x - 1) * kPlan * 4) {
-      if (i + 4 <= n) *reinterpret_cast<u32x4*>(f.refs_out + i) = *reinterpret_cast<const u32x4*>(f.refs_in + i);
-      else
-        for (int64_t e = i; e < n; ++e) f.refs_out[e] = f.refs_in[e];
-    }
-    return;
-  }
-  __shared__ int lds_first[IN_LDS ? kPlanKids : 1], lds_kids[IN_LDS ? kPlanKids : 1];
-  __shared__ int sums[kPlan / 64];
-  __shared__ int copies;
-  if (tid == 0) copies = 0;
-  int* const first = IN_LDS ? lds_first : f.first;
-  int* const kids = IN_LDS ? lds_kids : f.kids;
+  if (tid == 0) *at.copied = 0;
+  int* const first = at.first;
+  int* const kids = at.kids;
   auto get = [](int* p) { return IN_LDS ? *p : __hip_atomic_load(p, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT); };
   auto put = [](int* p, int v) {
     if (IN_LDS) *p = v;
@@ -148,7 +159,7 @@ __global__ __launch_bounds__(kPlan) void k_kv4_fork_plan(KvFork f) {
   __syncthreads();
   for (int b = tid; b < f.batch_out; b += kPlan) {
     const Parent r = b < kPlan ? mine : parent_of(f, b);
-    if (r.bad_len) kv_flag(f.cache, VBQ_KV4_FLAG_LENGTH);
+    if (r.bad_len && tells) kv_flag(f.cache, VBQ_KV4_FLAG_LENGTH);
     if (r.p < 0) continue;
     __hip_atomic_fetch_min(first + r.p, b, __ATOMIC_RELAXED, IN_LDS ? __HIP_MEMORY_SCOPE_WORKGROUP : __HIP_MEMORY_SCOPE_AGENT);
     __hip_atomic_fetch_add(kids + r.p, 1, __ATOMIC_RELAXED, IN_LDS ? __HIP_MEMORY_SCOPE_WORKGROUP : __HIP_MEMORY_SCOPE_AGENT);
@@ -156,7 +167,7 @@ __global__ __launch_bounds__(kPlan) void k_kv4_fork_plan(KvFork f) {
   __builtin_amdgcn_s_waitcnt(VBQ_VMCNT_IMM(0));
   __syncthreads();
   // Pages that each new sequence needs, and how many those before it do.
-  int64_t wanted = 0;
+  wanted = 0;
   for (int b0 = 0; b0 < f.batch_out; b0 += kPlan) {
     const int b = b0 + tid;
     int n = 0, blocks = 0, part = -1;
@@ -179,101 +190,91 @@ __global__ __launch_bounds__(kPlan) void k_kv4_fork_plan(KvFork f) {
       }
     }
     int total;
-    const int upto = group_scan<kPlan / 64>(n, sums, total);
+    const int upto = group_scan<kPlan / 64>(n, at.sums, total);
     // (more than there are pages is cut off: those beyond find none)
     if (b < f.batch_out) {
       const int64_t before = wanted + (upto - n);
-      const int at = (int)(before < f.cache.n_pages ? before : f.cache.n_pages);
-      f.offset[b] = at | (is_first ? INT32_MIN : 0);
-      if (blocks) f.copies[__hip_atomic_fetch_add(&copies, 1, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_WORKGROUP)] = int4{part, at, blocks, 0};
+      const int from = (int)(before < f.cache.n_pages ? before : f.cache.n_pages);
+      at.offset[b] = from | (is_first ? INT32_MIN : 0);
+      if (blocks) at.copies[__hip_atomic_fetch_add(at.copied, 1, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_WORKGROUP)] = int4{part, from, blocks, 0};
     }
     wanted += total;
   }
-  if (IN_LDS)
-    for (int p = tid; p < f.batch_in; p += kPlan) f.kids[p] = lds_kids[p];
   // The lowest free pages.
-  int found = 0;
+  found = 0;
   const int want = (int)(wanted < f.cache.n_pages ? wanted : f.cache.n_pages);
   for (int64_t base = 0; base < f.cache.n_pages && found < want; base += kPlan * kScan) {
-    const int64_t at = base + (int64_t)tid * kScan;
-    uint32_t free = base ? free_at(at) : first_free;
+    const int64_t page = base + (int64_t)tid * kScan;
+    uint32_t free = base ? free_at(page) : first_free;
     int total;
-    int place = found + group_scan<kPlan / 64>(__builtin_popcount(free), sums, total) - __builtin_popcount(free);
+    int place = found + group_scan<kPlan / 64>(__builtin_popcount(free), at.sums, total) - __builtin_popcount(free);
     for (; free; free &= free - 1, ++place)
-      if (place < want) f.free[place] = (int)(at + __builtin_ctz(free));
+      if (place < want) at.free[place] = (int)(page + __builtin_ctz(free));
     found += total;
   }
+  found = found < want ? found : want;
   __syncthreads();
-  if (tid == 0) {
-    f.head[0] = found < want ? found : want;
-    f.head[1] = copies;
-    if (found < wanted) kv_flag(f.cache, VBQ_KV4_FLAG_FULL);
+  if (tells && tid == 0 && found < wanted) kv_flag(f.cache, VBQ_KV4_FLAG_FULL);
+}
+
+// The counts as they were, by workgroup `group` of `groups`.
+__device__ inline void keep_counts(const KvFork& f, int64_t group, int64_t groups) {
+  const int64_t n = f.cache.n_pages;
+  for (int64_t i = (group * kPlan + threadIdx.x) * 4; i < n; i += groups * kPlan * 4) {
+    if (i + 4 <= n) *reinterpret_cast<u32x4*>(f.refs_out + i) = *reinterpret_cast<const u32x4*>(f.refs_in + i);
+    else
+      for (int64_t e = i; e < n; ++e) f.refs_out[e] = f.refs_in[e];
   }
 }
 
-constexpr int kForkThreads = 256, kCopyAtOnce = 4;
+constexpr int kCopyAtOnce = 4;   // loads of a thread
 
-__global__ __launch_bounds__(kForkThreads) void k_kv4_fork(KvFork f) {
-  __shared__ int sums[kForkThreads / 64];
-  const int tid = (int)threadIdx.x;
+// Pieces of the copies, by workgroup `group` of `groups`.
+template <int THREADS>
+__device__ inline void copy_parts(const KvFork& f, const int4* copies, int n, const int32_t* free, int found, uint32_t group,
+                                  uint32_t groups) {
+  const int heads = f.cache.heads, unit = kKvGroupBytes * f.cache.groups / 16;   // (of 16 bytes)
+  const int stride = unit << f.cache.block_shift;   // between heads
+  constexpr int PIECE = THREADS * kCopyAtOnce;
+  const int pieces = (stride * heads + PIECE - 1) / PIECE;   // of a whole page
+  const int64_t all = (int64_t)n * pieces;
+  for (int64_t w = group; w < all; w += groups) {
+    const int4 copy = copies[w / pieces];
+    const int run = copy.z * unit, end = run * heads, i0 = (int)(w % pieces) * PIECE + (int)threadIdx.x;
+    if (copy.y >= found || i0 - (int)threadIdx.x >= end) continue;
+    const u32x4* const src = reinterpret_cast<const u32x4*>(kv_block(f.cache, f.cache.groups, (uint32_t)copy.x, 0, 0));
+    u32x4* const dst = reinterpret_cast<u32x4*>(kv_block(f.cache, f.cache.groups, (uint32_t)free[copy.y], 0, 0));
+    u32x4 v[kCopyAtOnce];
+    int o[kCopyAtOnce];
+#pragma unroll
+    for (int c = 0; c < kCopyAtOnce; ++c) {
+      const int i = i0 + c * THREADS;
+      o[c] = i < end ? i / run * (stride - run) + i : -1;
+      if (o[c] >= 0) v[c] = src[o[c]];
+    }
+#pragma unroll
+    for (int c = 0; c < kCopyAtOnce; ++c)
+      if (o[c] >= 0) dst[o[c]] = v[c];
+  }
+}
+
+// New sequence b: its row, its length, and (COUNTS) what its pages' counts gain.
+template <int THREADS, bool COUNTS>
+__device__ inline void new_row(const KvFork& f, int b, int off, const int32_t* free, int found, int* sums, int tid) {
   const int32_t n_pages = f.cache.n_pages;
-  if (blockIdx.x < f.copiers) {   // pieces of the copies, kCopyAtOnce loads of a thread at a time
-    const int found = f.head[0], heads = f.cache.heads, unit = kKvGroupBytes * f.cache.groups / 16;   // (of 16 bytes)
-    const int stride = unit << f.cache.block_shift;   // between heads
-    constexpr int PIECE = kForkThreads * kCopyAtOnce;
-    const int pieces = (stride * heads + PIECE - 1) / PIECE;   // of a whole page
-    const int64_t all = (int64_t)f.head[1] * pieces;
-    for (int64_t w = blockIdx.x; w < all; w += f.copiers) {
-      const int4 copy = f.copies[w / pieces];
-      const int run = copy.z * unit, end = run * heads, i0 = (int)(w % pieces) * PIECE + tid;
-      if (copy.y >= found || i0 - tid >= end) continue;
-      const u32x4* const src = reinterpret_cast<const u32x4*>(kv_block(f.cache, f.cache.groups, (uint32_t)copy.x, 0, 0));
-      u32x4* const dst = reinterpret_cast<u32x4*>(kv_block(f.cache, f.cache.groups, (uint32_t)f.free[copy.y], 0, 0));
-      u32x4 v[kCopyAtOnce];
-      int o[kCopyAtOnce];
-#pragma unroll
-      for (int c = 0; c < kCopyAtOnce; ++c) {
-        const int i = i0 + c * kForkThreads;
-        o[c] = i < end ? i / run * (stride - run) + i : -1;
-        if (o[c] >= 0) v[c] = src[o[c]];
-      }
-#pragma unroll
-      for (int c = 0; c < kCopyAtOnce; ++c)
-        if (o[c] >= 0) dst[o[c]] = v[c];
-    }
-    return;
-  }
-  const uint32_t block = blockIdx.x - f.copiers;
-  if (block >= (uint32_t)f.batch_out) {   // an old sequence: its row is gone, its whole pages go to its continuations
-    const int p = (int)(block - (uint32_t)f.batch_out), kids = f.kids[p];
-    const int32_t whole = kids ? f.lens_in[p] >> (f.cache.block_shift + 5) : 0;
-    for (int j = tid; j < f.width; j += kForkThreads) {
-      const int32_t page = f.table_in[(int64_t)p * f.width + j];
-      const int d = (j < whole ? kids : 0) - 1;
-      if ((uint32_t)page < (uint32_t)n_pages) {
-        if (d) __hip_atomic_fetch_add(f.refs_out + page, d, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
-      } else if (page != -1) {
-        kv_flag(f.cache, VBQ_KV4_FLAG_PAGE);
-      }
-    }
-    return;
-  }
-  const int b = (int)block;
   const Parent r = parent_of(f, b);
-  const int off = f.offset[b], found = f.head[0];
   const bool first = off < 0;
   int at = off & INT32_MAX;   // the next page taken
   const int32_t* const from = f.table_in + (int64_t)(r.p < 0 ? 0 : r.p) * f.width;
-
   if (tid == 0) f.lens_out[b] = r.len;
   int32_t* const to = f.table_out + (int64_t)b * f.width;
-  for (int j = tid; j < r.whole; j += kForkThreads) {
+  for (int j = tid; j < r.whole; j += THREADS) {
     const int32_t e = from[j];
     const bool ok = (uint32_t)e < (uint32_t)n_pages;
     if (!ok) kv_flag(f.cache, VBQ_KV4_FLAG_PAGE);
     to[j] = ok ? e : -1;
   }
-  for (int j0 = r.whole; j0 < (int)r.need; j0 += kForkThreads) {
+  for (int j0 = r.whole; j0 < (int)r.need; j0 += THREADS) {
     const int j = j0 + tid;
     bool keep = false, fresh = false;
     int32_t e = -1;
@@ -283,25 +284,135 @@ __global__ __launch_bounds__(kForkThreads) void k_kv4_fork(KvFork f) {
       fresh = !keep;
     }
     int total;
-    const int place = at + group_scan<kForkThreads / 64>(fresh ? 1 : 0, sums, total) - 1;
-    if (fresh) e = place < found ? f.free[place] : -1;
+    const int place = at + group_scan<THREADS / 64>(fresh ? 1 : 0, sums, total) - 1;
+    if (fresh) e = place < found ? free[place] : -1;
     if (j < (int)r.need) {
       to[j] = e;
-      if (e >= 0) __hip_atomic_fetch_add(f.refs_out + e, 1, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
+      if (COUNTS && e >= 0) __hip_atomic_fetch_add(f.refs_out + e, 1, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
     }
     at += total;
   }
-  for (int j = (int)(r.need > r.whole ? r.need : r.whole) + tid; j < f.width; j += kForkThreads) to[j] = -1;
+  for (int j = (int)(r.need > r.whole ? r.need : r.whole) + tid; j < f.width; j += THREADS) to[j] = -1;
+}
+
+template <bool IN_LDS>
+__global__ __launch_bounds__(kPlan) void k_kv4_fork_plan(KvFork f) {
+  const int tid = (int)threadIdx.x;
+  if (blockIdx.x) {
+    keep_counts(f, blockIdx.x - 1, gridDim.x - 1);
+    return;
+  }
+  __shared__ int lds_first[IN_LDS ? kPlanKids : 1], lds_kids[IN_LDS ? kPlanKids : 1];
+  __shared__ int sums[kPlan / 64];
+  __shared__ int copied;
+  int found;
+  int64_t wanted;
+  plan<IN_LDS>(f, Plan{IN_LDS ? lds_first : f.first, IN_LDS ? lds_kids : f.kids, sums, &copied, f.copies, f.offset, f.free},
+               true, found, wanted);
+  if (IN_LDS)
+    for (int p = tid; p < f.batch_in; p += kPlan) f.kids[p] = lds_kids[p];
+  if (tid == 0) {
+    f.head[0] = found;
+    f.head[1] = copied;
+  }
+}
+
+constexpr int kForkThreads = 256;
+
+__global__ __launch_bounds__(kForkThreads) void k_kv4_fork(KvFork f) {
+  __shared__ int sums[kForkThreads / 64];
+  const int tid = (int)threadIdx.x;
+  if (blockIdx.x < f.copiers) {
+    copy_parts<kForkThreads>(f, f.copies, f.head[1], f.free, f.head[0], blockIdx.x, f.copiers);
+    return;
+  }
+  const uint32_t block = blockIdx.x - f.copiers;
+  if (block >= (uint32_t)f.batch_out) {
+    // an old sequence: its row is gone, its whole pages go to its continuations
+    const int p = (int)(block - (uint32_t)f.batch_out), kids = f.kids[p];
+    const int32_t whole = kids ? f.lens_in[p] >> (f.cache.block_shift + 5) : 0;
+    for (int j = tid; j < f.width; j += kForkThreads) {
+      const int32_t page = f.table_in[(int64_t)p * f.width + j];
+      const int d = (j < whole ? kids : 0) - 1;
+      if ((uint32_t)page < (uint32_t)f.cache.n_pages) {
+        if (d) __hip_atomic_fetch_add(f.refs_out + page, d, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
+      } else if (page != -1) {
+        kv_flag(f.cache, VBQ_KV4_FLAG_PAGE);
+      }
+    }
+  } else {
+    new_row<kForkThreads, true>(f, (int)block, f.offset[block], f.free, f.head[0], sums, tid);
+  }
+}
+
+// Small calls: every workgroup plans by itself, then takes a share of the counts, of the
+// rows, or of the copies.
+__global__ __launch_bounds__(kPlan) void k_kv4_fork_small(KvFork f) {
+  __shared__ int first[kSmallBatch], kids[kSmallBatch], sums[kPlan / 64], copied;
+  __shared__ int4 copies[kSmallBatch];
+  __shared__ int32_t offset[kSmallBatch], free[kSmallRows], counts[kSmallCounts];
+  __shared__ int2 old[kSmallBatch];   // of an old sequence with continuations: whole pages, pages that the first has
+  const int tid = (int)threadIdx.x, lane = tid & 63, wave = __builtin_amdgcn_readfirstlane(tid >> 6);
+  const int counters = (f.cache.n_pages + kSmallCounts - 1) / kSmallCounts, block = (int)blockIdx.x;
+  const int rows = (f.batch_out + kPlan / 64 - 1) / (kPlan / 64);
+  const bool counts_here = block < counters;
+  const int page0 = counts_here ? block * kSmallCounts : 0, pages = min(f.cache.n_pages - page0, kSmallCounts);
+  if (counts_here)
+    for (int i = tid; i < pages; i += kPlan) counts[i] = f.refs_in[page0 + i];
+  int found;
+  int64_t wanted;
+  plan<true>(f, Plan{first, kids, sums, &copied, copies, offset, free}, block == 0, found, wanted);
+  if (block >= counters + rows) {
+    copy_parts<kPlan>(f, copies, copied, free, found, (uint32_t)(block - counters - rows), gridDim.x - (uint32_t)(counters + rows));
+    return;
+  }
+  if (!counts_here) {   // a sequence a wavefront
+    const int b = (block - counters) * (kPlan / 64) + wave;
+    if (b < f.batch_out) new_row<64, false>(f, b, offset[b], free, found, sums, lane);
+    return;
+  }
+  // What the old rows' entries lose and gain (those that the first continuation keeps stay), and the pages taken.
+  if (tid < f.batch_in) {
+    const int b = first[tid];
+    const Parent r = parent_of(f, b == INT32_MAX ? 0 : b);
+    old[tid] = b == INT32_MAX ? int2{0, 0} : int2{r.whole, (int)r.need};
+  }
+  __syncthreads();
+  for (int i = tid; i < f.batch_in * f.width; i += kPlan) {
+    const int p = i / f.width, j = i - p * f.width;
+    const int32_t page = f.table_in[i];
+    if ((uint32_t)page >= (uint32_t)f.cache.n_pages) {
+      if (page != -1 && block == 0) kv_flag(f.cache, VBQ_KV4_FLAG_PAGE);
+      continue;
+    }
+    if ((uint32_t)(page - page0) >= (uint32_t)pages) continue;
+    const int d = (j < old[p].x ? kids[p] : j < old[p].y && f.refs_in[page] == 1 ? 1 : 0) - 1;
+    if (d) __hip_atomic_fetch_add(counts + (page - page0), d, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_WORKGROUP);
+  }
+  for (int i = tid; i < found; i += kPlan) {
+    const int page = free[i] - page0;
+    if ((uint32_t)page < (uint32_t)pages)
+      __hip_atomic_fetch_add(counts + page, 1, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_WORKGROUP);
+  }
+  __syncthreads();
+  for (int i = tid; i < pages; i += kPlan) f.refs_out[page0 + i] = counts[i];
 }
 
 }  // namespace
 
 hipError_t launch_kv4_fork(const KvFork& f, hipStream_t s) {
   const int64_t page = (int64_t)f.cache.heads * f.cache.groups * kKvGroupBytes << f.cache.block_shift;
+  if (f.batch_in <= kSmallBatch && f.batch_out <= kSmallBatch && (int64_t)f.batch_out * f.width <= kSmallRows &&
+      (int64_t)f.batch_in * f.width <= kSmallRows && f.cache.n_pages <= kSmallPages) {
+    const int64_t pieces = f.batch_out * ((page + kPlan * kCopyAtOnce * 16 - 1) / (kPlan * kCopyAtOnce * 16));
+    const int64_t others = (f.cache.n_pages + kSmallCounts - 1) / kSmallCounts + (f.batch_out + kPlan / 64 - 1) / (kPlan / 64);
+    k_kv4_fork_small<<<dim3((uint32_t)(others + (pieces < kSmallCopiers ? pieces : kSmallCopiers))), kPlan, 0, s>>>(f);
+    return hipGetLastError();
+  }
   const int64_t copies = (f.cache.n_pages + kPlan * 4 - 1) / (kPlan * 4);
-  const dim3 plan((uint32_t)(1 + (copies < 64 ? copies : 64)));
-  if (f.batch_in <= kPlanKids) k_kv4_fork_plan<true><<<plan, kPlan, 0, s>>>(f);
-  else k_kv4_fork_plan<false><<<plan, kPlan, 0, s>>>(f);
+  const dim3 plan_grid((uint32_t)(1 + (copies < 64 ? copies : 64)));
+  if (f.batch_in <= kPlanKids) k_kv4_fork_plan<true><<<plan_grid, kPlan, 0, s>>>(f);
+  else k_kv4_fork_plan<false><<<plan_grid, kPlan, 0, s>>>(f);
   hipError_t e = hipGetLastError();
   if (e != hipSuccess) return e;
   // (a page is copied for every new sequence, at most; more workgroups than fill the chip take turns)

@@ -514,6 +514,10 @@ FORK = [
     (30, 30, 9, 128, 300, 1, 192, 1), (3, 5, 3, 256, 20, 2, 256, 300), (100, 700, 6, 32, 5000, 1, 64, 33),
     (1500, 1300, 4, 32, 20000, 1, 64, 5), (5000, 4200, 3, 32, 30000, 1, 64, 1), (2, 3, 300, 32, 700, 1, 64, 9000),
     (2, 2, 3, 2048, 9, 2, 64, 10), (7, 40, 4, 64, 3, 2, 64, 70),
+    # many pages beside few sequences, and the sizes at which calls stop being small
+    (5, 9, 6, 32, 4090, 1, 64, 40), (64, 64, 64, 32, 20000, 1, 64, 70), (64, 65, 8, 32, 900, 1, 64, 33),
+    (65, 3, 8, 32, 900, 1, 64, 33), (64, 64, 65, 32, 5000, 1, 64, 70), (3, 4, 5, 32, 65520, 1, 64, 40),
+    (3, 4, 5, 32, 65560, 1, 64, 40), (64, 20, 3, 512, 40, 3, 256, 600), (9, 64, 4, 1024, 200, 2, 128, 5),
 ]
 
 
