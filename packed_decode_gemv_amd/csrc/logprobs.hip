@@ -50,12 +50,18 @@ __device__ inline uint64_t key_of(float x, uint32_t index) {
 __device__ inline float key_value(uint64_t k) { return value_of((uint32_t)(k >> 32)); }
 __device__ inline uint32_t key_index(uint64_t k) { return 0xFFFFFFFFu - (uint32_t)k; }
 
-// A maximum in base two. Beyond 2^100 numbers that are not equal are further apart than
-// any exponential reaches, whatever the base, and products with log2(e) might overflow.
-__device__ inline bool is_far(float m) { return !(fabsf(m) < 0x1p100f); }
+// A maximum in base two, b. What rounding leaves of m log2(e) is in every exponent of its
+// sums: up to 2^30 64 at most, so that sums of 2^30 terms, and these times it, stay within
+// 2^101. From 2^30 on (far) b is m itself: there numbers that are not equal are 64 apart at
+// least, further than 2^y or exp reach beside 1 (2^30 terms of 2^-64).
+__device__ inline bool is_far(float m) { return !(fabsf(m) < 0x1p30f); }
 __device__ inline float to_base(float m) { return is_far(m) ? m : m * kLog2e; }
-// (of two parts: not below 2^-1000, so that nothing times it is no number)
-__device__ inline float down(float from, float to) { return fmaxf(to_base(from) - to_base(to), -1000.f); }
+// log2 of what sums on one maximum are worth on another, as large or larger: not below
+// -1000, so that nothing times its power is no number. Of two kinds they are 64 apart too.
+__device__ inline float down(float from, float to) {
+  const float d = is_far(from) == is_far(to) ? to_base(from) - to_base(to) : -1000.f;
+  return fmaxf(d, -1000.f);
+}
 
 // Over the wavefront, the result in every lane: within rows of 16 lanes, then rows.
 template <class Op>
@@ -477,7 +483,8 @@ __global__ __launch_bounds__(64 * kWaves) void k_token_logprobs(Logprobs a) {
   const float log_s = log2f(part.s);
   auto logprob = [&](float v) {
     if (none) return -__builtin_inff();
-    return is_far(part.m) || is_far(v) ? (v - part.m) - log_s * kLn2 : (__builtin_fmaf(v, kLog2e, -to_base(part.m)) - log_s) * kLn2;
+    const bool whole = is_far(part.m) || !(fabsf(v) < 0x1p100f);   // (beyond, what log s holds of b's rounding is nothing)
+    return whole ? (v - part.m) - log_s * kLn2 : (__builtin_fmaf(v, kLog2e, -to_base(part.m)) - log_s) * kLn2;
   };
   if (me == 0) {
     const float nan = __builtin_nanf("");
