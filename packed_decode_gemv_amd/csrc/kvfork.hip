@@ -196,7 +196,15 @@ __device__ inline void plan(const KvFork& f, const Plan& at, bool tells, int& fo
       const int64_t before = wanted + (upto - n);
       const int from = (int)(before < f.cache.n_pages ? before : f.cache.n_pages);
       at.offset[b] = from | (is_first ? INT32_MIN : 0);
-      if (blocks) at.copies[__hip_atomic_fetch_add(at.copied, 1, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_WORKGROUP)] = int4{part, from, blocks, 0};
+      // A wavefront's copies are listed in the order of its lanes. That of the wavefronts is
+      // open, so lists that several workgroups make, each its own, are of one wavefront's.
+      const uint64_t who = __ballot(blocks != 0);
+      if (blocks) {
+        const int lead = __builtin_ctzll(who), n_before = lanes_below(who);
+        int place = 0;
+        if (n_before == 0) place = __hip_atomic_fetch_add(at.copied, __builtin_popcountll(who), __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_WORKGROUP);
+        at.copies[__builtin_amdgcn_readlane(place, lead) + n_before] = int4{part, from, blocks, 0};
+      }
     }
     wanted += total;
   }
@@ -348,6 +356,7 @@ __global__ __launch_bounds__(kForkThreads) void k_kv4_fork(KvFork f) {
 // Small calls: every workgroup plans by itself, then takes a share of the counts, of the
 // rows, or of the copies.
 __global__ __launch_bounds__(kPlan) void k_kv4_fork_small(KvFork f) {
+  static_assert(kSmallBatch <= 64, "the copies are listed by one wavefront, the same in every workgroup");
   __shared__ int first[kSmallBatch], kids[kSmallBatch], sums[kPlan / 64], copied;
   __shared__ int4 copies[kSmallBatch];
   __shared__ int32_t offset[kSmallBatch], free[kSmallRows], counts[kSmallCounts];

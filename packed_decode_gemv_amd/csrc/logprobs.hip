@@ -93,9 +93,6 @@ __device__ inline uint64_t lane_key(uint64_t v, int i) {
   const uint32_t hi = __builtin_amdgcn_readlane((int)(uint32_t)(v >> 32), i);
   return (uint64_t)hi << 32 | lo;
 }
-__device__ inline int lanes_below(uint64_t who) {
-  return (int)__builtin_amdgcn_mbcnt_hi((uint32_t)(who >> 32), __builtin_amdgcn_mbcnt_lo((uint32_t)who, 0));
-}
 // What a wavefront wrote to LDS is read by its other lanes afterwards.
 __device__ inline void wave_sync() {
   __builtin_amdgcn_fence(__ATOMIC_RELEASE, "wavefront");

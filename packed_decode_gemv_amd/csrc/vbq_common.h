@@ -97,6 +97,11 @@ __device__ inline uint32_t wave_total(uint32_t v) {
   return v;
 }
 
+// How many of `who` (a ballot) are lanes below this one.
+__device__ inline int lanes_below(uint64_t who) {
+  return (int)__builtin_amdgcn_mbcnt_hi((uint32_t)(who >> 32), __builtin_amdgcn_mbcnt_lo((uint32_t)who, 0));
+}
+
 // s_waitcnt immediate that waits until at most n vector-memory operations of
 // the wavefront are outstanding (and for nothing else).
 #define VBQ_VMCNT_IMM(n) (((n) & 15) | (((n) >> 4) << 14) | (7 << 4) | (15 << 8))
