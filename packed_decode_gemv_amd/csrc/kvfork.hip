@@ -113,6 +113,50 @@ __device__ inline int group_scan(int v, int* sums, int& total) {
   return v + before;
 }
 
+// How many of `n` entries of old row p, from j0 on, a first continuation keeps (n 0: none).
+// The wavefront's lanes each take their own, a look-up after the other (0.17 us an entry),
+// or, where the longest are many more than the lanes' share of all, take them in turn (entry
+// i of the lanes' one after the other), 512 a step of about 2.5 us. 1 sequence to 8 with pages
+// kept for 8, 40, 128 and 1000 entries, each lane its own and shared out, us: 8.5 14.0 28.5 176
+// and - 10.0 10.1 20.4; 64 to 64 with 40 each 16.4 and 24.6, 512 to 512 with 64 each 36.3 and 39.4.
+constexpr int kFewEntries = 8;
+__device__ inline int kept_behind(const KvFork& f, int p, int j0, int n) {
+  int kept = 0, total = 0, upto = 0;
+  bool share = __any(n > kFewEntries);
+  if (share) {
+    upto = group_scan<1>(n, nullptr, total);
+    share = __any(n > kFewEntries + total / 32);
+  }
+  if (!share) {
+    for (int i = 0, page; i < n; ++i) kept += keeps(f, p, j0 + i, page);
+    return kept;
+  }
+  constexpr int AT_ONCE = 8;
+  const int lane = threadIdx.x & 63, before = upto - n;
+  for (int i0 = 0; i0 < total; i0 += 64 * AT_ONCE) {
+    int32_t page[AT_ONCE];
+#pragma unroll
+    for (int c = 0; c < AT_ONCE; ++c) {
+      const int i = i0 + 64 * c + lane;
+      int whose = 0;   // lanes whose entries end at i or before
+#pragma unroll
+      for (int d = 32; d; d >>= 1) whose += __shfl(upto, whose + d - 1, 64) <= i ? d : 0;
+      const int row = __shfl(p, whose, 64), j = __shfl(j0 - before, whose, 64) + i;
+      page[c] = i < total ? f.table_in[(int64_t)row * f.width + j] : -1;
+    }
+    bool keep[AT_ONCE];
+#pragma unroll
+    for (int c = 0; c < AT_ONCE; ++c) keep[c] = (uint32_t)page[c] < (uint32_t)f.cache.n_pages && f.refs_in[page[c]] == 1;
+#pragma unroll
+    for (int c = 0; c < AT_ONCE; ++c) {
+      const uint64_t who = __ballot(keep[c]);
+      const int from = max(before - (i0 + 64 * c), 0), to = min(upto - (i0 + 64 * c), 64);   // the lane's of these 64
+      if (from < to) kept += __builtin_popcountll((who >> from) & (~0ull >> (64 - (to - from))));
+    }
+  }
+  return kept;
+}
+
 // Places for what the planning workgroup finds (see KvFork), its counts in LDS or not.
 struct Plan {
   int *first, *kids, *sums, *copied;
@@ -170,7 +214,7 @@ __device__ inline void plan(const KvFork& f, const Plan& at, bool tells, int& fo
   wanted = 0;
   for (int b0 = 0; b0 < f.batch_out; b0 += kPlan) {
     const int b = b0 + tid;
-    int n = 0, blocks = 0, part = -1;
+    int n = 0, blocks = 0, part = -1, p = 0, behind = 0, rest = 0;
     bool is_first = false;
     if (b < f.batch_out) {
       const Parent r = b < kPlan ? mine : parent_of(f, b);
@@ -186,9 +230,12 @@ __device__ inline void plan(const KvFork& f, const Plan& at, bool tells, int& fo
           n -= 1;
           blocks = 0;
         }
-        for (int j = r.whole + 1, e = (int)r.need, page; j < e; ++j) n -= keeps(f, r.p, j, page);
+        p = r.p;
+        behind = r.whole + 1;
+        rest = max((int)r.need - behind, 0);
       }
     }
+    n -= kept_behind(f, p, behind, rest);
     int total;
     const int upto = group_scan<kPlan / 64>(n, at.sums, total);
     // (more than there are pages is cut off: those beyond find none)

@@ -30,3 +30,45 @@ def test_part_pages_of_many_pieces(vbq, olds, news):  # noqa: F811
     for _ in range(3):
         run = fork_run(vbq, page, heads, dim, n_pages, table, lens, refs, parents, reserve)
         fork_check(*run, want, page, heads, dim)
+
+
+LONG = [
+    # old sequences, new ones, width, most entries in reserve, pages to spare
+    (1, 8, 64, 50, 400), (2, 3, 1200, 1100, 3500), (64, 64, 64, 60, 5000), (20, 64, 60, 40, 40), (63, 64, 63, 9, 300),
+    (64, 300, 130, 120, 40000), (700, 900, 40, 30, 30000), (1100, 2100, 20, 18, 30000), (5, 70, 3000, 2900, 250000),
+    (4200, 3000, 12, 10, 30000),
+]
+
+
+@pytest.mark.parametrize("case", range(len(LONG)))
+def test_many_entries_in_reserve(vbq, case):  # noqa: F811
+    """Rows of the table that name pages far beyond their tokens, with gaps, pages that another row names too and numbers
+    outside the cache among them: the first continuation keeps those that are its own, others are taken."""
+    olds, news, W, most, spare = LONG[case]
+    page = 32
+    rng = np.random.default_rng(case)
+    table = np.full((olds, W), -1, np.int32)
+    lens = rng.integers(0, (W - most) * page + 1, olds).astype(np.int32)
+    used = 0
+    for b in range(olds):
+        n = -(-int(lens[b]) // page) + int(rng.choice([0, 1, 5, 8, 9, most], p=[0.1, 0.1, 0.1, 0.1, 0.1, 0.5]))
+        n = min(n, W)
+        table[b, :n] = np.arange(used, used + n)
+        used += n
+    n_pages = used + spare
+    number = rng.permutation(n_pages).astype(np.int32)
+    table = np.where(table >= 0, number[np.maximum(table, 0)], -1).astype(np.int32)
+    held = np.arange(W)[None] >= -(-lens[:, None] // page)
+    gaps = held & (rng.random((olds, W)) < 0.1)
+    table[gaps] = -1
+    again = held & (table >= 0) & (rng.random((olds, W)) < 0.05)       # named by another row too
+    table[again] = rng.choice(table[table >= 0], int(again.sum())) if again.any() else table[again]
+    if case % 3 == 1:
+        table[held & (rng.random((olds, W)) < 0.02)] = n_pages + 7
+    there = (table >= 0) & (table < n_pages)
+    refs = np.bincount(table[there], minlength=n_pages).astype(np.int32)
+    parents = rng.integers(-1, olds, news).astype(np.int32)
+    reserve = np.minimum(rng.choice([0, 1, 9 * page, most * page, (most + 3) * page], news), W * page).astype(np.int32)
+    want = fork_reference(page, n_pages, table, lens, refs, parents, reserve)
+    run = fork_run(vbq, page, 1, 64, n_pages, table, lens, refs, parents, reserve)
+    fork_check(*run, want, page, 1, 64)
