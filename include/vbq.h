@@ -495,7 +495,8 @@ typedef struct vbq_head_rows {
 } vbq_head_rows;
 
 /* positions: device, int32, row a of axis a is at positions + a * position_stride
- * (NULL if R is 0); any number, negative ones too. */
+ * (NULL if R is 0); any number, negative ones too. n_tokens >= 0; times the heads of q and k
+ * together, up to 2^40 are taken. */
 vbq_status head_norm_rotary(const vbq_head_rotary* plan, const vbq_head_rows* q, const vbq_head_rows* k,
                             const int32_t* positions, int64_t position_stride, int32_t n_tokens, hipStream_t stream);
 

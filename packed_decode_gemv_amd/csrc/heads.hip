@@ -95,7 +95,7 @@ __global__ __launch_bounds__(64 * kHeadWaves) void k_head_norm_rotary(HeadRotary
   __shared__ __attribute__((aligned(16))) float2 turn[kHeadWaves][D / 2];
   const uint32_t lane = threadIdx.x & 63u;
   const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
-  const int64_t task = (int64_t)blockIdx.x * kHeadWaves + wave;
+  const int64_t task = ((int64_t)blockIdx.y * gridDim.x + blockIdx.x) * kHeadWaves + wave;
   const int64_t token = task / a.passes;
   if (token >= a.tokens) return;
   const int pass = (int)(task - token * a.passes);
@@ -185,8 +185,11 @@ hipError_t launch_head_norm_rotary(HeadRotary a, int dtype, hipStream_t s) {
   if (a.tokens == 0 || passes == 0) return hipSuccess;
   a.passes = (int32_t)passes;
   const int64_t groups_n = (a.tokens * passes + kHeadWaves - 1) / kHeadWaves;
-  if (groups_n * (64 * kHeadWaves) > (int64_t)UINT32_MAX) return hipErrorNotSupported;
-  const dim3 grid((uint32_t)groups_n);
+  // (a dimension holds fewer than 2^32 threads; workgroups past the last token have nothing to do)
+  constexpr int64_t ROW = 1 << 23;
+  const int64_t across = groups_n < ROW ? groups_n : ROW, down = (groups_n + across - 1) / across;
+  if (down > 65535) return hipErrorNotSupported;
+  const dim3 grid((uint32_t)across, (uint32_t)down);
 #define VBQ_ONE(G, DT)                                                                               \
   if (a.interleaved) k_head_norm_rotary<G, DT, true><<<grid, 64 * kHeadWaves, 0, s>>>(a);            \
   else k_head_norm_rotary<G, DT, false><<<grid, 64 * kHeadWaves, 0, s>>>(a)

@@ -167,3 +167,12 @@ def test_the_binding_refuses_before_the_library_is_reached():
     for args in ((1, 2 ** 40, 0), (2 ** 33, 10, 0), (1, 10, 11), (-1, 10, 0)):
         with pytest.raises(ValueError, match="refused"):
             vbq.token_logprobs_workspace(*args)
+
+
+def test_rotary_refuses_more_than_a_launch_holds():
+    import packed_decode_gemv_amd as vbq
+    p = vbq.vbq_head_rotary(head_dim=64, rotary_dim=0, axes=1, interleaved=0, eps=0.0, reserved=0, inv_freq=None, axis=None,
+                            q_weight=None, k_weight=None)
+    rows = vbq.vbq_head_rows(in_=BASE, out=BASE, in_token_stride=64, in_head_stride=64, out_token_stride=64,
+                             out_head_stride=64, heads=65536, in_dtype=0, out_dtype=0, reserved=0)
+    assert vbq.lib.head_norm_rotary(C.byref(p), C.byref(rows), C.byref(rows), None, 0, 2 ** 31 - 1, None) == 5
