@@ -649,9 +649,13 @@ def _kv4_index(cache: Kv4Cache, block_table, vec, cu):
         raise ValueError("block_table: expected a 2-D torch tensor")
     B, W = block_table.shape
     i32, dev = cache._i32, cache.index
-    if not (block_table.dtype is i32 and vec.dtype is i32 and cu.dtype is i32 and block_table.get_device() == dev and
-            vec.get_device() == dev and cu.get_device() == dev and block_table.is_contiguous() and
-            vec.is_contiguous() and cu.is_contiguous() and vec.shape == (B,) and cu.shape == (B + 1,)):
+    try:
+        fine = (block_table.dtype is i32 and vec.dtype is i32 and cu.dtype is i32 and block_table.get_device() == dev and
+                vec.get_device() == dev and cu.get_device() == dev and block_table.is_contiguous() and
+                vec.is_contiguous() and cu.is_contiguous() and vec.shape == (B,) and cu.shape == (B + 1,))
+    except AttributeError:   # not a tensor
+        fine = False
+    if not fine:
         _need(block_table, "block_table", i32, (B, W), cache.device)
         _need(vec, "lengths", i32, (B,), cache.device)
         _need(cu, "cumulative lengths", i32, (B + 1,), cache.device)
@@ -763,7 +767,7 @@ def kv4_attention(cache: Kv4Cache, q, block_table, kv_lens, cu_q, max_q: int, ma
         _need(lse, "lse", torch.float32, (T, H), cache.device)
     if workspace is None:
         workspace = kv4_attention_workspace(cache, B, T, H, max_q, max_kv, window, sinks, stream)
-    elif workspace.dtype is not cache.data.dtype or workspace.get_device() != cache.index or \
+    elif getattr(workspace, "dtype", None) is not cache.data.dtype or workspace.get_device() != cache.index or \
             not workspace.is_contiguous():
         raise ValueError("workspace: expected a contiguous uint8 tensor on the cache's device")
     try:
@@ -874,7 +878,7 @@ _NO_ROWS = _HEAD_ROWS.pack(0, 0, 0, 0, 0, 0, 0, 0, 0, 0)
 def _head_rows(plan, x, what: str, out, dtype, stream):
     """The output for x, its tokens, its type and its vbq_head_rows."""
     dt = _kv4_dtype(getattr(x, "dtype", None), what)
-    H = x.shape[1] if x.ndim == 3 else 0
+    H = x.shape[1] if getattr(x, "ndim", 0) == 3 else 0
     T, ts, hs = _kv4_rows(x, what, H, plan)
     if out is None:
         D = plan.head_dim
@@ -884,9 +888,9 @@ def _head_rows(plan, x, what: str, out, dtype, stream):
         out = x.new_empty((T, H, D), dtype=dtype) if stream is None else _new(x, (T, H, D), dtype, stream)
         ots, ohs = H * D, D
     else:
+        odt = _kv4_dtype(getattr(out, "dtype", None), what + "_out")
         if dtype is not None and out.dtype is not dtype:
             raise ValueError(f"{what}_out: {out.dtype}, expected {dtype}")
-        odt = _kv4_dtype(out.dtype, what + "_out")
         To, ots, ohs = _kv4_rows(out, what + "_out", H, plan)
         if To != T:
             raise ValueError(f"{what}_out: {To} tokens, expected {T}")
@@ -920,9 +924,9 @@ def head_norm_rotary(plan: HeadRotary, q, k, positions, q_out=None, k_out=None, 
         raise ValueError(f"head_norm_rotary: {T} tokens")
     at = None
     if plan.rotary_dim:
-        shape = (T,) if plan.axes == 1 and positions.ndim == 1 else (plan.axes, T)
-        if positions.dtype is not plan._i32 or positions.shape != shape or not positions.is_contiguous() or \
-                positions.get_device() != plan.index:
+        shape = (T,) if plan.axes == 1 and getattr(positions, "ndim", 1) == 1 else (plan.axes, T)
+        if getattr(positions, "dtype", None) is not plan._i32 or positions.shape != shape or \
+                not positions.is_contiguous() or positions.get_device() != plan.index:
             _need(positions, "positions", plan._i32, shape, plan.device)
         at = positions.data_ptr()
     st = _on_device(plan.index, lib.head_norm_rotary, plan._ref, rows_q, rows_k, at, T, T, _kv4_stream(plan, stream))
@@ -958,12 +962,16 @@ def kv4_fork(cache: Kv4Cache, refs, block_table, lens, parents, reserve=None, ou
     B, W = block_table.shape
     N = parents.shape[0]
     n = cache.n_pages
-    if not (block_table.dtype is i32 and lens.dtype is i32 and refs.dtype is i32 and parents.dtype is i32 and
-            block_table.get_device() == dev and lens.get_device() == dev and refs.get_device() == dev and
-            parents.get_device() == dev and block_table.is_contiguous() and lens.is_contiguous() and
-            refs.is_contiguous() and parents.is_contiguous() and lens.shape == (B,) and refs.shape == (n,) and
-            (reserve is None or (reserve.dtype is i32 and reserve.get_device() == dev and reserve.is_contiguous() and
-                                 reserve.shape == (N,)))):
+    try:
+        fine = (block_table.dtype is i32 and lens.dtype is i32 and refs.dtype is i32 and parents.dtype is i32 and
+                block_table.get_device() == dev and lens.get_device() == dev and refs.get_device() == dev and
+                parents.get_device() == dev and block_table.is_contiguous() and lens.is_contiguous() and
+                refs.is_contiguous() and parents.is_contiguous() and lens.shape == (B,) and refs.shape == (n,) and
+                (reserve is None or (reserve.dtype is i32 and reserve.get_device() == dev and reserve.is_contiguous() and
+                                     reserve.shape == (N,))))
+    except AttributeError:   # not a tensor
+        fine = False
+    if not fine:
         for t, what, shape in ((block_table, "block_table", (B, W)), (lens, "lens", (B,)), (refs, "refs", (n,)),
                                (parents, "parents", (N,)), (reserve, "reserve", (N,))):
             if t is not None or what != "reserve":
@@ -981,7 +989,8 @@ def kv4_fork(cache: Kv4Cache, refs, block_table, lens, parents, reserve=None, ou
     table_out, lens_out, refs_out = out
     if workspace is None:
         workspace = kv4_fork_workspace(cache, N, W, B, stream)
-    elif workspace.dtype is not cache.data.dtype or workspace.get_device() != dev or not workspace.is_contiguous():
+    elif getattr(workspace, "dtype", None) is not cache.data.dtype or workspace.get_device() != dev or \
+            not workspace.is_contiguous():
         raise ValueError("workspace: expected a contiguous uint8 tensor on the cache's device")
     f = _KV4_FORK.pack(B, N, W, 0, block_table.data_ptr(), lens.data_ptr(), refs.data_ptr(), parents.data_ptr(),
                        0 if reserve is None else reserve.data_ptr(), table_out.data_ptr(), lens_out.data_ptr(),
@@ -1029,18 +1038,22 @@ def kv4_attention_shared(cache: Kv4Cache, q, block_table, kv_lens, cu_q, cu_grou
         raise ValueError("shared: expected a 1-D torch tensor, a number for each group")
     n = shared.shape[0]
     i32, dev = cache._i32, cache.index
-    if not (shared.dtype is i32 and cu_groups.dtype is i32 and shared.get_device() == dev and
-            cu_groups.get_device() == dev and shared.is_contiguous() and cu_groups.is_contiguous() and
-            cu_groups.shape == (n + 1,)):
+    try:
+        fine = (shared.dtype is i32 and cu_groups.dtype is i32 and shared.get_device() == dev and
+                cu_groups.get_device() == dev and shared.is_contiguous() and cu_groups.is_contiguous() and
+                cu_groups.shape == (n + 1,))
+    except AttributeError:   # not a tensor
+        fine = False
+    if not fine:
         _need(shared, "shared", i32, (n,), cache.device)
         _need(cu_groups, "cu_groups", i32, (n + 1,), cache.device)
     H = q.shape[1] if getattr(q, "ndim", 0) == 3 else 0
     if H < 1 or H % cache.n_kv_heads:
         raise ValueError(f"q: shape {tuple(getattr(q, 'shape', ()))}, expected (queries, a multiple of "
                          f"{cache.n_kv_heads}, {cache.head_dim})")
-    T, ts, hs = _kv4_rows(q, "q", H, cache)
-    D, dtype = cache.head_dim, q.dtype
+    D, dtype = cache.head_dim, getattr(q, "dtype", None)
     dt = _kv4_dtype(dtype, "q", 1)
+    T, ts, hs = _kv4_rows(q, "q", H, cache)
     if out is None:
         out = _kv4_new(cache, (T, H, D), dtype, stream)
     else:
@@ -1050,7 +1063,8 @@ def kv4_attention_shared(cache: Kv4Cache, q, block_table, kv_lens, cu_q, cu_grou
         _need(lse, "lse", torch.float32, (T, H), cache.device)
     if workspace is None:
         workspace = kv4_attention_shared_workspace(cache, B, n, T, H, max_q, max_shared, max_own, max_group_q, stream)
-    elif workspace.dtype is not cache.data.dtype or workspace.get_device() != dev or not workspace.is_contiguous():
+    elif getattr(workspace, "dtype", None) is not cache.data.dtype or workspace.get_device() != dev or \
+            not workspace.is_contiguous():
         raise ValueError("workspace: expected a contiguous uint8 tensor on the cache's device")
     try:
         a = _KV4_ATTN.pack(B, W, T, max_q, 0, H, dt, 1 if causal else 0, 0, 0, D ** -0.5 if scale is None else scale, 0,
@@ -1123,9 +1137,9 @@ def token_logprobs(logits, tokens=None, top: int = 0, out=None, workspace=None, 
         raise ValueError(f"logits: shape {(M, V)}")
     size = 0
     if tokens is not None:
-        size = _TOKEN_BYTES.get(str(tokens.dtype), 0)
+        size = _TOKEN_BYTES.get(str(getattr(tokens, "dtype", None)), 0)
         if not size:
-            raise ValueError(f"tokens: dtype {tokens.dtype}, expected int32 or int64")
+            raise ValueError(f"tokens: {getattr(tokens, 'dtype', type(tokens).__name__)}, expected int32 or int64")
         if tokens.shape != (M,) or not tokens.is_contiguous() or tokens.get_device() != dev:
             _need(tokens, "tokens", tokens.dtype, (M,), logits.device)
     if not 0 <= top <= min(LOGPROBS_MAX_TOP, V):
@@ -1154,7 +1168,8 @@ def token_logprobs(logits, tokens=None, top: int = 0, out=None, workspace=None, 
                 _need(t, "out " + what, dtype, shape, logits.device)
     if workspace is None:
         workspace = token_logprobs_workspace(M, V, top, logits.device, stream)
-    elif workspace.dtype is not torch.uint8 or workspace.get_device() != dev or not workspace.is_contiguous():
+    elif getattr(workspace, "dtype", None) is not torch.uint8 or workspace.get_device() != dev or \
+            not workspace.is_contiguous():
         raise ValueError("workspace: expected a contiguous uint8 tensor on the logits' device")
     a = _LOGPROBS.pack(M, V, dt, top, row if M > 1 else V, logits.data_ptr(), tokens.data_ptr() if size else 0, size, 0,
                        logprob.data_ptr() if size else 0, rank.data_ptr() if size else 0,

@@ -176,3 +176,48 @@ def test_rotary_refuses_more_than_a_launch_holds():
     rows = vbq.vbq_head_rows(in_=BASE, out=BASE, in_token_stride=64, in_head_stride=64, out_token_stride=64,
                              out_head_stride=64, heads=65536, in_dtype=0, out_dtype=0, reserved=0)
     assert vbq.lib.head_norm_rotary(C.byref(p), C.byref(rows), C.byref(rows), None, 0, 2 ** 31 - 1, None) == 5
+
+
+def test_the_binding_refuses_what_is_no_tensor():
+    """On CPU tensors with a stand-in for the plan and the cache: refusals come before the library is called."""
+    from types import SimpleNamespace
+
+    import numpy as np
+    import torch
+
+    import packed_decode_gemv_amd as vbq
+    i32 = torch.int32
+    plan = SimpleNamespace(rotary_dim=64, axes=1, head_dim=64, index=-1, _i32=i32, device=torch.device("cpu"))
+    q = torch.zeros(3, 2, 64)
+    for bad in (None, [0, 1, 2], 7, np.zeros(3, np.int32)):
+        with pytest.raises(ValueError, match="positions"):
+            vbq.head_norm_rotary(plan, q, None, bad)
+    for bad in ([0], np.zeros((3, 2, 64), np.float32), 5):
+        for args in ((bad, None), (None, bad)):
+            with pytest.raises(ValueError):
+                vbq.head_norm_rotary(plan, *args, torch.zeros(3, dtype=i32))
+        for kw in (dict(q_out=bad), dict(q_out=bad, q_dtype=torch.float32)):
+            with pytest.raises(ValueError):
+                vbq.head_norm_rotary(plan, q, None, torch.zeros(3, dtype=i32), **kw)
+
+    cache = SimpleNamespace(n_pages=10, page_tokens=32, n_kv_heads=1, head_dim=64, index=-1, _i32=i32,
+                            device=torch.device("cpu"), data=torch.zeros(1, dtype=torch.uint8))
+    good = dict(refs=torch.zeros(10, dtype=i32), block_table=torch.zeros(2, 3, dtype=i32), lens=torch.zeros(2, dtype=i32),
+                parents=torch.zeros(4, dtype=i32), reserve=torch.zeros(4, dtype=i32), workspace=None)
+    for name in good:
+        for bad in ([1, 2], 3, np.zeros(2, np.int32)) + (() if name in ("reserve", "workspace") else (None,)):
+            with pytest.raises(ValueError):
+                vbq.kv4_fork(cache, **{**good, "out": (torch.zeros(4, 3, dtype=i32), torch.zeros(4, dtype=i32),
+                                                       torch.zeros(10, dtype=i32)), name: bad})
+    with pytest.raises(ValueError):
+        vbq.kv4_fork(cache, **good, out=(None, None, None))
+
+    good = dict(q=torch.zeros(2, 1, 64, dtype=torch.float16), block_table=torch.zeros(2, 3, dtype=i32),
+                kv_lens=torch.zeros(2, dtype=i32), cu_q=torch.zeros(3, dtype=i32), cu_groups=torch.zeros(2, dtype=i32),
+                shared=torch.zeros(1, dtype=i32), out=torch.zeros(2, 1, 64, dtype=torch.float16), workspace=None)
+    for name in good:
+        for bad in ([1, 2], 3, np.zeros((2, 1, 64), np.float16)) + (() if name in ("out", "workspace") else (None,)):
+            with pytest.raises(ValueError):
+                vbq.kv4_attention_shared(cache, **{**good, name: bad}, max_q=1, max_shared=1, max_own=1)
+    with pytest.raises(ValueError):
+        vbq.kv4_attention_shared(cache, **good, lse=[1], max_q=1, max_shared=1, max_own=1)
