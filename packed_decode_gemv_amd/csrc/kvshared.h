@@ -84,7 +84,11 @@ __global__ __launch_bounds__(256) void k_kv4_attn_meet(KvAttn a, const float* ow
   const bool mine = slot < SLICES * ROWS && r < rows && in_tile < kRowTile;
   const int qi = r / a.ratio, hh = r - qi * a.ratio;
   const int64_t o = (int64_t)(sq.c0 + qi) * a.n_heads + head * a.ratio + hh;
-  const int per = part_blocks(a, sq.re), parts = TILE ? (sq.re.nw + per - 1) / per : 1;
+  int parts = 1;
+  if constexpr (TILE) {
+    const int per = part_blocks(a, sq.re);
+    parts = (sq.re.nw + per - 1) / per;
+  }
   const int64_t place = TILE ? (int64_t)blockIdx.x * a.parts * kRowTile + in_tile : o;
   const float* const sums = (TILE ? a.acc : a.sums) + place * D + 4 * c;
   const float* const ml = (TILE ? a.ml : a.sums_ml) + 2 * place;
