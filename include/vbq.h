@@ -553,7 +553,8 @@ vbq_status kv4_fork(const vbq_kv4* cache, const vbq_kv4_fork* f, hipStream_t str
  * sequence's for the shared tokens; sums of both kinds are joined in fp32. Where the
  * stated sizes are so small that it takes less time, sequences read the shared tokens one by one.
  * workspace: as for kv4_attention, of kv4_attention_shared_workspace() bytes, the first
- * 8 * VBQ_KV4_COUNTERS of them zero before the first call that uses it. */
+ * 8 * VBQ_KV4_COUNTERS of them zero before the first call that uses it; every call, and every
+ * kv4_attention on the same workspace, leaves them zero. */
 typedef struct vbq_kv4_groups {
   int32_t n_groups;       /* 1 .. 65535 */
   int32_t max_shared;     /* no group shares more tokens than this */

@@ -717,7 +717,7 @@ def kv4_read(cache: Kv4Cache, block_table, start, cu_tokens, total_tokens, dtype
 def kv4_attention_workspace(cache: Kv4Cache, batch: int, total_q: int, n_heads: int, max_q: int, max_kv: int,
                             window: int = 0, sinks: int = 0, stream=None):
     """A workspace for kv4_attention calls of these sizes (or any that need no
-    more) that do not overlap in time."""
+    more, of kv4_attention_shared too) that do not overlap in time."""
     import torch
     try:
         a = _KV4_ATTN.pack(batch, 1, total_q, max_q, max_kv, n_heads, 0, 1, window, sinks, 1.0, 0, 0, 0, 0, 0, 0, 0, 0,
@@ -731,7 +731,7 @@ def kv4_attention_workspace(cache: Kv4Cache, batch: int, total_q: int, n_heads: 
     w = _kv4_new(cache, (n,), cache.data.dtype, stream)
     if n:
         with torch.cuda.stream(stream):
-            w[:4 * KV4_COUNTERS].zero_()
+            w[:8 * KV4_COUNTERS].zero_()
     return w
 
 
@@ -1004,7 +1004,7 @@ def kv4_fork(cache: Kv4Cache, refs, block_table, lens, parents, reserve=None, ou
 def kv4_attention_shared_workspace(cache: Kv4Cache, batch: int, groups: int, total_q: int, n_heads: int, max_q: int,
                                    max_shared: int, max_own: int, max_group_q=None, stream=None):
     """A workspace for kv4_attention_shared calls of these sizes (or any that need no
-    more) that do not overlap in time."""
+    more, of kv4_attention too) that do not overlap in time."""
     import torch
     try:
         a = _KV4_ATTN.pack(batch, 1, total_q, max_q, 0, n_heads, 0, 1, 0, 0, 1.0, 0, 0, 0, 0, 0, 0, 0, 0, 0, 0, 0)

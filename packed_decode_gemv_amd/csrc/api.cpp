@@ -132,7 +132,7 @@ vbq_status check_attn(const vbq_kv4* cache, const vbq_kv4_attn* a, bool pointers
   *p = kv4_attn_plan(a->batch, cache->n_kv_heads, ratio, c->groups, a->total_q, a->max_q, a->max_kv, a->window,
                      a->sinks);
   if (!kv_grid_fits(p->grid, p->threads)) return VBQ_ERR_UNSUPPORTED;
-  *bytes = p->places ? VBQ_KV4_COUNTERS * 4 + p->places * p->rows * (cache->head_dim + 2) * 4 : 0;
+  *bytes = p->places ? 2 * VBQ_KV4_COUNTERS * 4 + p->places * p->rows * (cache->head_dim + 2) * 4 : 0;
   return VBQ_OK;
 }
 
@@ -195,7 +195,7 @@ static void fill_attn(const vbq_kv4* cache, const vbq_kv4_attn* a, KvAttn* k) {
   k->out = static_cast<uint16_t*>(a->out);
   k->lse = a->lse;
   k->counters = static_cast<uint32_t*>(a->workspace);
-  k->acc = static_cast<float*>(a->workspace) + VBQ_KV4_COUNTERS;
+  k->acc = static_cast<float*>(a->workspace) + 2 * VBQ_KV4_COUNTERS;   // (behind all counters of shared attention)
   k->width = a->table_width;
   k->total_q = a->total_q;
   k->max_q = a->max_q;
@@ -276,7 +276,7 @@ static vbq_status check_shared(const vbq_kv4* cache, const vbq_kv4_attn* a, cons
     if (st != VBQ_OK) return st;
     p->each = true;
     p->own_sums = p->own_ml = p->sums = p->ml = p->acc = p->acc_ml = 0;
-    p->own_acc = 2 * VBQ_KV4_COUNTERS;   // (where a call of the other kind has its own)
+    p->own_acc = 2 * VBQ_KV4_COUNTERS;   // (where calls of the other kinds have theirs)
     p->own_acc_ml = p->own_acc + p->own.places * p->own.rows * cache->head_dim;
     p->bytes = 4 * (p->own_acc_ml + p->own.places * p->own.rows * 2);
     return VBQ_OK;
