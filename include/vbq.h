@@ -520,6 +520,9 @@ vbq_status head_norm_rotary(const vbq_head_rotary* plan, const vbq_head_rows* q,
  * table and negative reserves as 0 (FLAG_LENGTH); where free pages run out, entries are
  * -1 and nothing is copied (FLAG_FULL).
  * Pages are 16 GiB at most.
+ * Layers of a model that share one table each have a cache of their own, of as many pages of
+ * as many tokens: a call for each, with the same inputs, copies its pages and writes the same
+ * tables, lengths and counts, on one stream into the same outputs.
  * kv4_fork_workspace: bytes for calls of these sizes (or less), -1 if they are refused.
  * Calls that overlap in time need workspaces of their own; nothing in it has to be set. */
 typedef struct vbq_kv4_fork {
@@ -550,8 +553,14 @@ vbq_status kv4_fork(const vbq_kv4* cache, const vbq_kv4_fork* f, hipStream_t str
  * looked at; max_own is: no sequence holds more tokens beyond its group's shared ones.
  * A sequence for whose group or itself numbers do not fit is left out (FLAG_LENGTH).
  * The arithmetic is kv4_attention's, with the rows of a group together in place of a
- * sequence's for the shared tokens; sums of both kinds are joined in fp32. Where the
- * stated sizes are so small that it takes less time, sequences read the shared tokens one by one.
+ * sequence's for the shared tokens: max_group_q * n_heads / n_kv_heads decides how their values
+ * are multiplied (above 32, or 16 for head_dim 256: rounded once to fp16), max_q * n_heads /
+ * n_kv_heads for the own ones. Sums of both kinds are joined in fp32. Where the stated sizes are so
+ * small that it takes less time (by max_shared, max_own, batch and heads at most 20000 blocks of 32
+ * tokens in all, and at most 32 rows of a sequence, or 16), sequences read the shared tokens one
+ * by one, with the products of their own rows: a wider bound can change the last bits.
+ * Where a sequence has 128 rows of a key/value head or more by itself, kv4_attention over a
+ * table whose rows all name the shared pages takes as long or less.
  * workspace: as for kv4_attention, of kv4_attention_shared_workspace() bytes, the first
  * 8 * VBQ_KV4_COUNTERS of them zero before the first call that uses it; every call, and every
  * kv4_attention on the same workspace, leaves them zero. */

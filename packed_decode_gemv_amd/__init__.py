@@ -955,7 +955,8 @@ def kv4_fork(cache: Kv4Cache, refs, block_table, lens, parents, reserve=None, ou
     copied for all but the first continuation, pages of sequences that nothing
     goes on from are free afterwards. Returns the new block_table [B'][W], lens and
     refs; out: tensors to fill (not the inputs). Kv4Cache.check raises where pages ran
-    out. workspace: from kv4_fork_workspace, for calls that allocate nothing."""
+    out. Layers that share one table: a call for each layer's cache with the same
+    inputs, out the first one's results. workspace: from kv4_fork_workspace, for calls that allocate nothing."""
     i32, dev = cache._i32, cache.index
     if getattr(block_table, "ndim", 0) != 2 or getattr(parents, "ndim", 0) != 1:
         raise ValueError("block_table, parents: expected a 2-D and a 1-D torch tensor")
@@ -1031,6 +1032,8 @@ def kv4_attention_shared(cache: Kv4Cache, q, block_table, kv_lens, cu_q, cu_grou
     block table's row of its first sequence names. Queries stand behind the shared
     tokens. max_shared: no group shares more tokens; max_own: no sequence holds more
     beyond them; max_group_q: no group has more queries in all (default: any number).
+    For steps of few queries: where a sequence has 128 rows (queries times query heads of a
+    key/value head) or more, kv4_attention takes as long or less.
     The rest is as for kv4_attention, without windows; workspace: from
     kv4_attention_shared_workspace."""
     B, W = _kv4_index(cache, block_table, kv_lens, cu_q)

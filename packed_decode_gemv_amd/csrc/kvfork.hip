@@ -14,7 +14,8 @@
 //
 // 512 sequences of 4001 tokens, 8 heads of 128 (26 MB of part pages, read and written):
 // the plan 6.4 us, a chain of dependent look-ups and scans by one workgroup, the rest 11.0,
-// copies at 4.8 TB/s. One sequence to eight: 5.0 and 3.6 us, look-ups alone.
+// copies at 4.8 TB/s. One sequence to eight: 5.0 and 3.6 us, look-ups alone. (Few pages in
+// reserve each; for many see kept_behind.)
 //
 // k_kv4_fork_small: where the plan is short every workgroup makes it by itself, so that
 // none waits for another's and one launch does. Counts are then summed in LDS, a slice of
@@ -249,7 +250,8 @@ __device__ inline void plan(const KvFork& f, const Plan& at, bool tells, int& fo
       if (blocks) {
         const int lead = __builtin_ctzll(who), n_before = lanes_below(who);
         int place = 0;
-        if (n_before == 0) place = __hip_atomic_fetch_add(at.copied, __builtin_popcountll(who), __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_WORKGROUP);
+        if (n_before == 0)
+          place = __hip_atomic_fetch_add(at.copied, __builtin_popcountll(who), __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_WORKGROUP);
         at.copies[__builtin_amdgcn_readlane(place, lead) + n_before] = int4{part, from, blocks, 0};
       }
     }

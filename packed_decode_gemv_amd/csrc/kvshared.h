@@ -16,6 +16,12 @@
 // 16 of 4096 120 and 116, 24 of 2048 130 and 131; of 192 with 2, 8 of 4096 87.4 and 93.9;
 // groups of 64, 12 heads of 64, 1 of 8192 20.9 and 27.0, 24 of 2048 169 and 196.
 // Small calls are one launch of the kernel for few rows, sequence by sequence.
+// Own rows that fill tiles of 128 by themselves make enough of a block, and sums of both kinds
+// cost more than the shared blocks again: this and kv4_attention over a table that names the
+// shared pages in every row, us, bf16, 32 heads of 128 on 8 (4 rows a query): 64 sequences of 257
+// queries behind 512 shared tokens 581 and 327, behind 2048 1097 and 884, behind 8192 3293 and
+// 3174; 16 of 64 behind 65536 1453 and 1448; 32 of 40 behind 8192 376 and 359, of 20 152 and 193;
+// 64 of 9 148 and 356.
 //
 // Measured, 32 heads of 128 on 8: 64 sequences over 65000 shared tokens (bf16) 117 us,
 // 0.58 PFLOP/s of products, bound by the loop over blocks (matrix units 30% busy, vector

@@ -5,7 +5,8 @@
 // one is worked on. In base two, with b = m log2(e) for the wavefront's maximum m, it
 // keeps s = sum of e and t = sum of e y with e = 2^y, y = x log2(e) - b (one fma: the
 // rounding of b is the same for all, and leaves the logarithms again), from which
-// lse = m + ln2 log2 s, logprob = ln2 (y - log2 s) and entropy = ln2 (log2 s - t / s).
+// lse = m + ln2 log2 s (here it stays, 2^-24 m at most), logprob = ln2 (y - log2 s) and
+// entropy = ln2 (log2 s - t / s).
 //   For the most likely tokens it keeps a list in LDS of 64-bit keys (the value's
 // order, then the lowest index), and `least`, the top-th largest key of those met.
 // Indexes rise from step to step, so a value is wanted only if it is larger than
@@ -15,12 +16,13 @@
 // the first step the top-th largest of the lanes' own best is a bound that few pass.
 //   The wavefronts of a workgroup are joined in LDS, the workgroups of a row by the
 // last of them that finishes.
-//   Many rows are bound by memory: 2047 rows of 128256 fp32 logits (1.05 GB), top 5, take
-// 185 us, 5.7 TB/s, with vector instructions 60% of that time beside it (189 with a row's
-// first and last logits loaded in the step that takes them; then a bound shared by a row's
-// wavefronts 188, but 64 rows of 32001 18.7 and 19.2 for 17.7; registers for six and eight
-// wavefronts a SIMD 206 and 205). Few rows are a chain of one step and two
-// joins: one row of 128256, top 20, 13.3 us, of which the first step 3.5, the joins 2 each.
+//   Many fp32 rows are bound by memory: 2047 of 128256 (1.05 GB), top 5, take 185 us,
+// 5.7 TB/s, with vector instructions 60 to 70% of that time beside it; in 16 bits they bind, 91%
+// busy: 117 us (4.5 TB/s; 104 without a list). What did not help the first: a row's first and
+// last logits loaded in the step that takes them 189; then a bound shared by a row's wavefronts
+// 188, but 64 rows of 32001 18.7 and 19.2 for 17.7; registers for six and eight wavefronts a SIMD
+// 206 and 205. Few rows are a chain of one step and two joins: one row of 128256, top 20,
+// 13.3 us, of which the first step 3.5, the joins 2 each.
 #include "logprobs.h"
 
 namespace vbq {

@@ -72,3 +72,29 @@ def test_many_entries_in_reserve(vbq, case):  # noqa: F811
     want = fork_reference(page, n_pages, table, lens, refs, parents, reserve)
     run = fork_run(vbq, page, 1, 64, n_pages, table, lens, refs, parents, reserve)
     fork_check(*run, want, page, 1, 64)
+
+
+@pytest.mark.parametrize("olds,news", [(5, 30), (90, 200)])
+def test_a_stack_of_layers(vbq, olds, news):  # noqa: F811
+    """A cache a layer, one table: a call for each with the same inputs gives the same numbers, into the same outputs."""
+    import torch
+
+    from test_gpu_continuations import fork_case
+    page, W = 64, 6
+    rng = np.random.default_rng(olds)
+    n_pages, table, lens, refs, parents, more = fork_case(rng, olds, news, W, page, 2000, reserve=90)
+    want = fork_reference(page, n_pages, table, lens, refs, parents, more)
+    shapes = [(2, 64), (1, 128), (3, 64)]
+    caches = [vbq.Kv4Cache(n_pages, page, heads, dim) for heads, dim in shapes]
+    before = []
+    for c in caches:
+        c.data.copy_(torch.randint(0, 256, (c.nbytes,), dtype=torch.uint8))
+        before.append(c.data.clone())
+    t = [torch.from_numpy(np.ascontiguousarray(a)).cuda() for a in (refs, table, lens, parents)]
+    more = torch.from_numpy(more).cuda()
+    out, ws = None, vbq.kv4_fork_workspace(caches[0], news, W, olds)
+    for c in caches:
+        out = vbq.kv4_fork(c, *t, reserve=more, out=out, workspace=ws)
+    torch.cuda.synchronize()
+    for c, b, (heads, dim) in zip(caches, before, shapes):
+        fork_check(c, b, [o.cpu().numpy() for o in out], want, page, heads, dim)
